@@ -351,6 +351,7 @@ def _adamw_one(case, st, t, index, scale):
     if scale is not None:
         g = g * scale
     small = case["bits"] == 8
+    noise = _noise(g.numel(), index, step) if case["stochastic"] else None
     m = _unpack(t["m"], t["m_scale"], True) if small else t["m"]
     v = _unpack(t["v"], t["v_scale"], False) if small else t["v"]
     m = m * h["beta1"] + g * (1.0 - h["beta1"])
@@ -360,7 +361,6 @@ def _adamw_one(case, st, t, index, scale):
     p = p * (1.0 - h["lr"] * t["decay"]) - (h["lr"] / (1.0 - h["beta1"] ** step)) * (m / denom)
     if small:
         half = torch.tensor(0x8000, device="cuda")
-        noise = _noise(g.numel(), index, step) if case["stochastic"] else None
         t["m"], t["m_scale"] = _pack(m, M_TOP, half if noise is None else noise & 0xFFFF, True)
         t["v"], t["v_scale"] = _pack(v, V_TOP, half if noise is None else noise >> 16, False)
         m, v = _unpack(t["m"], t["m_scale"], True), _unpack(t["v"], t["v_scale"], False)
@@ -369,6 +369,8 @@ def _adamw_one(case, st, t, index, scale):
     out = {"m": m, "v": v}
     if "master" in t:
         t["master"] = out["master"] = p
+    elif noise is not None and t["param"].dtype == torch.bfloat16:  # no master copy: the parameter rounds by the noise too
+        p = (((p.view(torch.int32).to(torch.int64) + (((noise * 0x9E3779B1) & 0xFFFFFFFF) >> 16)) >> 16) << 16).to(torch.int32).view(torch.float32)
     t["param"] = out["param"] = p.to(t["param"].dtype)
     return out
 
