@@ -15,7 +15,9 @@ from . import _build
 c_void_p = ctypes.c_void_p
 c_int32 = ctypes.c_int32
 c_size_t = ctypes.c_size_t
+c_int64 = ctypes.c_int64
 c_float = ctypes.c_float
+c_double = ctypes.c_double
 
 ZB_OK = 0
 STATUS_NAMES = {
@@ -49,6 +51,24 @@ class zb_kernel_stats(ctypes.Structure):
                 ("bytes", ctypes.c_double)]
 
 
+class zb_rotary_config(ctypes.Structure):
+    _fields_ = [("scaling", c_int32), ("rotary_dim", c_int32), ("base", c_double), ("factor", c_double),
+                ("context", c_double), ("low", c_double), ("high", c_double)]
+
+
+class zb_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", c_void_p), ("master", c_void_p), ("grad", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_scale", c_void_p), ("v_scale", c_void_p), ("count", c_int64), ("weight_decay", c_float),
+                ("param_dtype", c_int32), ("grad_dtype", c_int32), ("reserved", c_int32)]
+
+
+class zb_adamw_config(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("state_bits", c_int32), ("stochastic", c_int32), ("seed", ctypes.c_uint32), ("reserved", c_int32)]
+
+
+ROTARY_PAIRS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 KERNEL_CLASSES = ["gemm_forward", "gemm_backward_input", "gemm_backward_weight", "row_backward_input",
                   "row_backward_weight", "row_forward", "attn_forward", "attn_backward", "stash_copy"]
 ATTENTION_KINDS = {"standin": 0, "causal": 1}
@@ -95,6 +115,19 @@ _SIGS = {
     "zb_op_attention_stat_stride": (c_int32, [c_int32]),
     "zb_op_attention_causal_forward": (c_int32, [c_void_p, c_void_p, c_void_p] + [c_int32] * 5 + [c_void_p]),
     "zb_op_attention_causal_backward": (c_int32, [c_void_p] * 6 + [c_int32] * 5 + [c_void_p]),
+    "zb_rotary_frequencies": (c_int32, [ctypes.POINTER(zb_rotary_config), ctypes.POINTER(ctypes.c_uint64),
+                                        ctypes.POINTER(c_float)]),
+    "zb_op_rotary_forward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_float] + [c_int32] * 5
+                             + [c_void_p]),
+    "zb_op_rotary_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_float] + [c_int32] * 5
+                              + [c_void_p]),
+    "zb_op_adamw_step": (c_int32, [ctypes.POINTER(zb_adamw_tensor), c_int32, ctypes.POINTER(zb_adamw_config), c_int64,
+                                   c_void_p, c_void_p, c_void_p, c_void_p]),
+    "zb_op_adamw_unpack": (c_int32, [ctypes.POINTER(zb_adamw_tensor), c_int32, ctypes.POINTER(c_void_p),
+                                     ctypes.POINTER(c_void_p), c_void_p]),
+    "zb_op_grad_norm_scratch_bytes": (c_size_t, [ctypes.POINTER(zb_adamw_tensor), c_int32]),
+    "zb_op_grad_norm": (c_int32, [ctypes.POINTER(zb_adamw_tensor), c_int32, c_float, c_void_p, c_void_p, c_size_t,
+                                  c_void_p]),
     "zb_device_status": (c_int32, [c_void_p, c_int32, ctypes.POINTER(c_int32)]),
     "zb_selftest_wait_timeout": (c_int32, [c_int32, c_void_p]),
     "zb_stage_workspace_bytes": (c_size_t, [ctypes.POINTER(zb_stage_config)]),
@@ -308,6 +341,98 @@ def zb_op_attention_causal_backward(qkv, a, da, lse, dvec, dqkv, tokens, n_heads
     _check(lib().zb_op_attention_causal_backward(_ptr(qkv), _ptr(a), _ptr(da), _ptr(lse), _ptr(dvec), _ptr(dqkv),
                                                  tokens, n_heads, n_kv_heads, head_dim, seq_len, _stream(stream)),
            "zb_op_attention_causal_backward")
+
+
+# ---------------------------------------------------------------- rotary positions
+
+
+def zb_rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0, high=None):
+    """(turns, magnitude): the list of 64-bit fractions of a turn per position, and the factor on rotated values.
+    `high` defaults to 32 turns (yarn) or 4 (banded)."""
+    if high is None:
+        high = 4.0 if scaling == "banded" else 32.0
+    cfg = zb_rotary_config(ROTARY_SCALINGS[scaling], rotary_dim, base, factor, context, low, high)
+    turns = (ctypes.c_uint64 * max(1, rotary_dim // 2))()
+    mag = c_float(0)
+    _check(lib().zb_rotary_frequencies(ctypes.byref(cfg), turns, ctypes.byref(mag)), "zb_rotary_frequencies")
+    return list(turns), mag.value
+
+
+def zb_op_rotary_forward(x, y, positions, turns, magnitude, tokens, n_heads, head_dim, rotary_dim, pairs="half", ld_x=None,
+                         ld_y=None, stream=None):
+    """Strides default to dense rows of n_heads heads."""
+    dense = n_heads * head_dim
+    _check(lib().zb_op_rotary_forward(_ptr(x), dense if ld_x is None else ld_x, _ptr(y), dense if ld_y is None else ld_y,
+                                      _ptr(positions), _ptr(turns), magnitude, tokens, n_heads, head_dim, rotary_dim,
+                                      ROTARY_PAIRS[pairs], _stream(stream)), "zb_op_rotary_forward")
+
+
+def zb_op_rotary_backward(dy, dx, positions, turns, magnitude, tokens, n_heads, head_dim, rotary_dim, pairs="half",
+                          ld_x=None, ld_y=None, stream=None):
+    """`ld_x` is the stride of dy, the input, and `ld_y` that of dx."""
+    dense = n_heads * head_dim
+    _check(lib().zb_op_rotary_backward(_ptr(dy), dense if ld_x is None else ld_x, _ptr(dx), dense if ld_y is None else ld_y,
+                                       _ptr(positions), _ptr(turns), magnitude, tokens, n_heads, head_dim, rotary_dim,
+                                       ROTARY_PAIRS[pairs], _stream(stream)), "zb_op_rotary_backward")
+
+
+# ---------------------------------------------------------------- AdamW
+
+
+def adamw_table(tensors):
+    """The C array of a list of dicts: param, grad, m, v, and where they apply master, m_scale, v_scale, weight_decay
+    (tensors, whose dtypes and sizes it takes).  The table holds addresses: keep the tensors alive."""
+    import torch
+
+    codes = {torch.bfloat16: 0, torch.float32: 1}
+    arr = (zb_adamw_tensor * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        param, grad = t["param"], t["grad"]
+        if param.dtype not in codes or grad.dtype not in codes:
+            raise ZBError(-1, "adamw_table (param and grad are bf16 or float32)")
+        n = param.numel()
+        sizes = {"master": (torch.float32, n), "grad": (grad.dtype, n)}
+        if t["m"].dtype == torch.uint8:
+            blocks = (n + 255) // 256
+            sizes.update(m=(torch.uint8, n), v=(torch.uint8, n), m_scale=(torch.float32, blocks),
+                         v_scale=(torch.float32, blocks))
+        else:
+            sizes.update(m=(torch.float32, n), v=(torch.float32, n))
+        for name, (dtype, count) in sizes.items():
+            x = t.get(name)
+            if x is None and name == "master":
+                continue
+            if x is None or x.dtype != dtype or x.numel() != count or not x.is_contiguous():
+                raise ZBError(-1, f"adamw_table ({name}: {count} contiguous values of {dtype})")
+        if not param.is_contiguous():
+            raise ZBError(-1, "adamw_table (param must be contiguous)")
+        arr[i] = zb_adamw_tensor(_ptr(param), _ptr(t.get("master")), _ptr(grad), _ptr(t["m"]), _ptr(t["v"]),
+                                 _ptr(t.get("m_scale")), _ptr(t.get("v_scale")), n, t.get("weight_decay", 0.0),
+                                 codes[param.dtype], codes[grad.dtype], 0)
+    return arr
+
+
+def make_adamw_config(lr, beta1=0.9, beta2=0.95, eps=1e-8, state_bits=32, stochastic=False, seed=0):
+    return zb_adamw_config(lr, beta1, beta2, eps, state_bits, 1 if stochastic else 0, seed & 0xFFFFFFFF, 0)
+
+
+def zb_op_adamw_step(table, n, cfg, step, grad_scale=None, lr_device=None, step_device=None, stream=None):
+    _check(lib().zb_op_adamw_step(table, n, ctypes.byref(cfg), step, _ptr(grad_scale), _ptr(lr_device), _ptr(step_device),
+                                  _stream(stream)), "zb_op_adamw_step")
+
+
+def zb_op_adamw_unpack(table, n, ms, vs, stream=None):
+    ptrs = lambda ts: (c_void_p * max(1, n))(*[_ptr(t) for t in ts])  # noqa: E731
+    _check(lib().zb_op_adamw_unpack(table, n, ptrs(ms), ptrs(vs), _stream(stream)), "zb_op_adamw_unpack")
+
+
+def zb_op_grad_norm_scratch_bytes(table, n):
+    return lib().zb_op_grad_norm_scratch_bytes(table, n)
+
+
+def zb_op_grad_norm(table, n, max_norm, out, scratch, scratch_bytes, stream=None):
+    _check(lib().zb_op_grad_norm(table, n, max_norm, _ptr(out), _ptr(scratch), scratch_bytes, _stream(stream)),
+           "zb_op_grad_norm")
 
 
 def zb_device_status(stream=None, reset=False):

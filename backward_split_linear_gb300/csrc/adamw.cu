@@ -1,0 +1,545 @@
+// AdamW over many tensors in one launch, with moments in 32 or 8 bits, and the
+// global gradient norm that clips it.
+//
+// For every element, with g the gradient times *grad_scale:
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps).
+// The kernels stream every tensor once and are bound by HBM: 30 bytes an
+// element with float32 moments and master weights, 18 with 8-bit moments.
+//
+// 8-bit moments.  256 consecutive elements share a float32 scale per moment.
+// A code's value is scale times an integer of the grid (8 + f) 2^(e - 1) (f for
+// e = 0), e the code's upper bits and f its lower three: three significant
+// bits over 2^18 (m: a sign and 7 bits) or 2^34 (v: 8 bits).  The scale is the
+// block's largest value over the largest code's.  An exponential moving average
+// moves by a fraction 1 - b of the difference per step, far less than a code's
+// step for v (1 - b2 of 0.05 to 0.001 against 1/8): rounding to the nearest
+// code would stand still, so the rounding can be stochastic, from a hash of
+// (seed, step, tensor, element).  v rounds no nonzero value to zero: a
+// vanished v would make the next update as large as m / eps.  m and v are
+// formed with separately rounded products and sums, so that the codes are
+// reproducible by any IEEE implementation of the formulas.
+#include <algorithm>
+#include <cmath>
+
+#include "checks.h"
+#include "device_common.cuh"
+
+namespace zbk {
+
+namespace {
+
+constexpr int kAdamThreads = 256;
+constexpr int kPerThread = 8;
+constexpr int kChunk = kAdamThreads * kPerThread;  // elements per block
+constexpr int kStateBlock = 256;                   // elements per 8-bit scale: one warp's
+constexpr float kMTop = 245760.f;                  // 15 * 2^14, the value of m's largest code
+constexpr float kVTop = 16106127360.f;             // 15 * 2^30, the value of v's largest code
+constexpr int kMaxAdamTensors = 64;                // per launch
+
+// The tensors of one launch, and the first chunk of each (first[n]: all chunks).
+struct AdamTable {
+    zb_adamw_tensor t[kMaxAdamTensors];
+    int64_t first[kMaxAdamTensors + 1];
+    int n;
+    int index0;  // number of t[0] in the caller's list (for the hash)
+};
+
+// Where adamw_unpack_kernel writes the moments of each tensor of a table.
+struct AdamUnpack {
+    float* m[kMaxAdamTensors];
+    float* v[kMaxAdamTensors];
+};
+
+struct AdamArgs {
+    float beta1, beta2, one_minus_beta1, one_minus_beta2, eps;
+    float lr, bias1, rsqrt_bias2;          // bias1 = 1 - b1^t, rsqrt_bias2 = (1 - b2^t)^(-1/2)
+    float log_beta1, log_beta2;            // for a step number on the device
+    uint32_t seed, step;
+    int stochastic;
+    const float* grad_scale;
+    const float* lr_dev;
+    const int64_t* step_dev;
+};
+
+// The tensor that chunk c belongs to: the last one that starts at or before it.
+__device__ __forceinline__ int find_tensor(const AdamTable& tab, int64_t c) {
+    int lo = 0, hi = tab.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Eight consecutive values from e on, zero past the end.
+__device__ __forceinline__ void load8f(const float* p, int64_t e, int64_t n, float (&v)[8]) {
+    if (e + 8 <= n) {
+        const float4 a = *reinterpret_cast<const float4*>(p + e), b = *reinterpret_cast<const float4*>(p + e + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = e + k < n ? p[e + k] : 0.f;
+    }
+}
+__device__ __forceinline__ void store8f(float* p, int64_t e, int64_t n, const float (&v)[8]) {
+    if (e + 8 <= n) {
+        *reinterpret_cast<float4*>(p + e) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + e + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e + k < n) p[e + k] = v[k];
+    }
+}
+__device__ __forceinline__ void load8h(const uint16_t* p, int64_t e, int64_t n, float (&v)[8]) {
+    if (e + 8 <= n) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p + e);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = bf16_lo(w[k]);
+            v[2 * k + 1] = bf16_hi(w[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = e + k < n ? __uint_as_float(static_cast<uint32_t>(p[e + k]) << 16) : 0.f;
+    }
+}
+__device__ __forceinline__ void store8h(uint16_t* p, int64_t e, int64_t n, const uint32_t (&w)[4]) {
+    if (e + 8 <= n) {
+        *reinterpret_cast<uint4*>(p + e) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e + k < n) p[e + k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    }
+}
+__device__ __forceinline__ uint2 load8b(const uint8_t* p, int64_t e, int64_t n) {
+    if (e + 8 <= n) return *reinterpret_cast<const uint2*>(p + e);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (e + k < n) w[k >> 2] |= static_cast<uint32_t>(p[e + k]) << (8 * (k & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store8b(uint8_t* p, int64_t e, int64_t n, uint2 q) {
+    if (e + 8 <= n) {
+        *reinterpret_cast<uint2*>(p + e) = q;
+    } else {
+        const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e + k < n) p[e + k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
+    }
+}
+
+// The xorshift-multiply mixing of a 32-bit word.
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+    x = (x ^ (x >> 16)) * 0x7FEB352Du;
+    x = (x ^ (x >> 15)) * 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+// The grid's value of a code without its sign, and its code from a scaled value
+// z >= 0; `noise` (16 bits, 0x8000: to the nearest) is the rounding's threshold.
+__device__ __forceinline__ float code_value(uint32_t c) {
+    return c < 8u ? static_cast<float>(c) : __uint_as_float((c + 1032u) << 20);
+}
+__device__ __forceinline__ uint32_t code_of(float z, uint32_t noise) {
+    const bool small = z < 8.f;
+    const uint32_t bits = __float_as_uint(small ? __fadd_rn(z, 8.f) : z);
+    return ((bits + (noise << 4)) >> 20) - (small ? 1040u : 1032u);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kState8>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable tab, const AdamArgs a) {
+    // A scale that is not finite (an overflowed or NaN gradient norm) skips the step.
+    float gs = 1.f;
+    if (a.grad_scale) {
+        gs = *a.grad_scale;
+        if (!(fabsf(gs) <= 3.402823466e38f)) return;
+    }
+    const int64_t chunk = blockIdx.x;
+    const int ti = find_tensor(tab, chunk);
+    const zb_adamw_tensor& t = tab.t[ti];
+    const int64_t n = t.count;
+    const int64_t e = (chunk - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
+    const float lr = a.lr_dev ? *a.lr_dev : a.lr;
+    float bias1 = a.bias1, rbias2 = a.rsqrt_bias2;
+    uint32_t step = a.step;
+    if (a.step_dev) {
+        const int64_t s = *a.step_dev;
+        step = static_cast<uint32_t>(s);
+        bias1 = -expm1f(static_cast<float>(s) * a.log_beta1);
+        rbias2 = rsqrtf(-expm1f(static_cast<float>(s) * a.log_beta2));
+    }
+    // Whole warps run on (the 8-bit scales are reduced across a warp); elements
+    // past the end hold zeros and are not stored.
+    float g[8], m[8], v[8], p[8];
+    if (t.grad_dtype == ZB_F32)
+        load8f(static_cast<const float*>(t.grad), e, n, g);
+    else
+        load8h(static_cast<const uint16_t*>(t.grad), e, n, g);
+    const float* p32 = t.master ? t.master : static_cast<const float*>(t.param);
+    if (t.master || t.param_dtype == ZB_F32)
+        load8f(p32, e, n, p);
+    else
+        load8h(static_cast<const uint16_t*>(t.param), e, n, p);
+    const int64_t block = e / kStateBlock;
+    const bool in = e - (threadIdx.x & 31) * kPerThread < n;  // this warp's block exists
+    if constexpr (kState8) {
+        const uint2 cm = load8b(static_cast<const uint8_t*>(t.m), e, n), cv = load8b(static_cast<const uint8_t*>(t.v), e, n);
+        const float sm = in ? t.m_scale[block] : 0.f, sv = in ? t.v_scale[block] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t c = ((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u;
+            const float x = __fmul_rn(code_value(c & 127u), sm);
+            m[k] = c > 127u ? -x : x;
+            v[k] = __fmul_rn(code_value(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u), sv);
+        }
+    } else {
+        load8f(static_cast<const float*>(t.m), e, n, m);
+        load8f(static_cast<const float*>(t.v), e, n, v);
+    }
+    const float decay = 1.f - lr * t.weight_decay, rate = lr / bias1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float gk = a.grad_scale ? __fmul_rn(g[k], gs) : g[k];
+        m[k] = __fadd_rn(__fmul_rn(m[k], a.beta1), __fmul_rn(gk, a.one_minus_beta1));
+        v[k] = __fadd_rn(__fmul_rn(v[k], a.beta2), __fmul_rn(__fmul_rn(gk, gk), a.one_minus_beta2));
+        p[k] = p[k] * decay - rate * __fdividef(m[k], fmaf(sqrt_approx(v[k]), rbias2, a.eps));
+    }
+    uint32_t noise[8];
+    if (a.stochastic) {
+        const uint32_t key = mix32(mix32(a.seed ^ (step * 0x9E3779B1u)) + static_cast<uint32_t>(tab.index0 + ti) * 0x85EBCA77u);
+        // elements past 2^32 start another stream
+        const uint32_t k2 = key + static_cast<uint32_t>(static_cast<uint64_t>(e) >> 32) * 0x632BE5ABu;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) noise[k] = mix32(static_cast<uint32_t>(e + k) ^ k2);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) noise[k] = 0x80008000u;
+    }
+    if constexpr (kState8) {
+        float mm = 0.f, mv = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (e + k < n) {
+                mm = fmaxf(mm, fabsf(m[k]));
+                mv = fmaxf(mv, v[k]);
+            }
+        mm = warp_max(mm);
+        mv = warp_max(mv);
+        const float tiny = 1.17549435e-38f;
+        const float sm = fmaxf(__fmul_rn(mm, 1.f / kMTop), tiny), sv = fmaxf(__fmul_rn(mv, 1.f / kVTop), tiny);
+        const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
+        uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t c = code_of(fminf(__fmul_rn(fabsf(m[k]), im), kMTop), noise[k] & 0xFFFFu);
+            c |= (__float_as_uint(m[k]) >> 24) & 128u;
+            cm[k >> 2] |= c << (8 * (k & 3));
+            const float z = fminf(__fmul_rn(v[k], iv), kVTop);
+            c = max(code_of(z, noise[k] >> 16), z > 0.f ? 1u : 0u);
+            cv[k >> 2] |= c << (8 * (k & 3));
+        }
+        store8b(static_cast<uint8_t*>(t.m), e, n, make_uint2(cm[0], cm[1]));
+        store8b(static_cast<uint8_t*>(t.v), e, n, make_uint2(cv[0], cv[1]));
+        if (in && (threadIdx.x & 31) == 0) {
+            t.m_scale[block] = sm;
+            t.v_scale[block] = sv;
+        }
+    } else {
+        store8f(static_cast<float*>(t.m), e, n, m);
+        store8f(static_cast<float*>(t.v), e, n, v);
+    }
+    if (t.master) store8f(t.master, e, n, p);
+    if (t.param_dtype == ZB_F32) {
+        store8f(static_cast<float*>(t.param), e, n, p);
+        return;
+    }
+    uint32_t w[4];
+    if (a.stochastic && !t.master) {
+        // without a master copy the parameter itself rounds stochastically: an
+        // update below half a bf16 step would otherwise be lost every time
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t u[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = p[2 * k + i];
+                const uint32_t b = __float_as_uint(x);
+                u[i] = fabsf(x) <= 3.3895314e38f ? (b + ((noise[2 * k + i] * 0x9E3779B1u) >> 16)) >> 16 : pack_bf16x2(x, 0.f) & 0xFFFFu;
+            }
+            w[k] = u[0] | (u[1] << 16);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
+    }
+    store8h(static_cast<uint16_t*>(t.param), e, n, w);
+}
+
+// The 8-bit moments as float32 values.
+__global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid_constant__ AdamTable tab,
+                                                                    const __grid_constant__ AdamUnpack out) {
+    const int64_t chunk = blockIdx.x;
+    const int ti = find_tensor(tab, chunk);
+    const zb_adamw_tensor& t = tab.t[ti];
+    const int64_t n = t.count;
+    const int64_t e = (chunk - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
+    if (e >= n) return;
+    const uint2 cm = load8b(static_cast<const uint8_t*>(t.m), e, n), cv = load8b(static_cast<const uint8_t*>(t.v), e, n);
+    const float sm = t.m_scale[e / kStateBlock], sv = t.v_scale[e / kStateBlock];
+    float m[8], v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t c = ((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u;
+        const float x = __fmul_rn(code_value(c & 127u), sm);
+        m[k] = c > 127u ? -x : x;
+        v[k] = __fmul_rn(code_value(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u), sv);
+    }
+    store8f(out.m[ti], e, n, m);
+    store8f(out.v[ti], e, n, v);
+}
+
+// Sum of squares of every chunk of kNormChunks x kChunk elements, one float64
+// per block: a fixed partition and order, so the norm is the same bits every
+// time.  Squares are summed in float32 over a thread's 64 elements, then in
+// float64.
+constexpr int kNormChunks = 8;
+
+__global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid_constant__ AdamTable tab, double* part) {
+    __shared__ double red[kAdamThreads / 32];
+    const int64_t chunk = blockIdx.x;
+    const int ti = find_tensor(tab, chunk);
+    const zb_adamw_tensor& t = tab.t[ti];
+    const int64_t n = t.count;
+    const int64_t e0 = (chunk - tab.first[ti]) * kNormChunks * kChunk + threadIdx.x * kPerThread;
+    float g[kNormChunks][8];
+#pragma unroll
+    for (int c = 0; c < kNormChunks; ++c) {
+        const int64_t e = e0 + c * kChunk;
+        if (t.grad_dtype == ZB_F32)
+            load8f(static_cast<const float*>(t.grad), e, n, g[c]);
+        else
+            load8h(static_cast<const uint16_t*>(t.grad), e, n, g[c]);
+    }
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < kNormChunks; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] = fmaf(g[c][k], g[c][k], s[k]);
+    double sum = 0.0;
+    float total32 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        total32 += s[k];
+        sum += static_cast<double>(s[k]);
+    }
+    // squares outside float32's range: this thread's sum again in float64
+    if (!(total32 <= 3.4e38f) || total32 < 1e-30f) {
+        sum = 0.0;
+#pragma unroll
+        for (int c = 0; c < kNormChunks; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += static_cast<double>(g[c][k]) * static_cast<double>(g[c][k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int w = 0; w < kAdamThreads / 32; ++w) total += red[w];
+        part[chunk] = total;
+    }
+}
+
+// out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)).
+__global__ void __launch_bounds__(1024) norm_final_kernel(const double* part, int64_t n, float max_norm, float* out) {
+    __shared__ double red[32];
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) sum += part[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int w = 0; w < 32; ++w) total += red[w];
+        const double norm = sqrt(total);
+        out[0] = static_cast<float>(norm);
+        // a NaN or infinite norm gives a NaN coefficient, which skips the step
+        out[1] = isfinite(norm) ? static_cast<float>(fmin(1.0, max_norm / (norm + 1e-6))) : __int_as_float(0x7FC00000);
+    }
+}
+
+int64_t chunks_of(int64_t count, int64_t per) { return (count + per - 1) / per; }
+
+// Calls fn(table, chunks) for every group of up to kMaxAdamTensors tensors;
+// empty tensors take no chunk.
+template <typename Fn>
+cudaError_t for_tables(const zb_adamw_tensor* ts, int n, int64_t per, Fn&& fn) {
+    for (int i0 = 0; i0 < n; i0 += kMaxAdamTensors) {
+        AdamTable tab{};
+        tab.n = std::min(kMaxAdamTensors, n - i0);
+        tab.index0 = i0;
+        int64_t c = 0;
+        for (int i = 0; i < tab.n; ++i) {
+            tab.t[i] = ts[i0 + i];
+            tab.first[i] = c;
+            c += chunks_of(ts[i0 + i].count, per);
+        }
+        tab.first[tab.n] = c;
+        if (c == 0) continue;
+        if (c > 0x7fffffff) return cudaErrorInvalidValue;
+        const cudaError_t e = fn(tab, c, i0);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+constexpr int64_t kMaxCount = int64_t(1) << 40;
+
+zb_status tensors_ok(const zb_adamw_tensor* ts, int32_t n) {
+    if (n < 0 || (n > 0 && !ts)) return ZB_ERR_ARG;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        if (ts[i].count < 0 || ts[i].count > kMaxCount) return ZB_ERR_SHAPE;
+        total += ts[i].count;
+        if (total > kMaxCount) return ZB_ERR_SHAPE;
+        if ((ts[i].grad_dtype != ZB_BF16 && ts[i].grad_dtype != ZB_F32) ||
+            (ts[i].param_dtype != ZB_BF16 && ts[i].param_dtype != ZB_F32))
+            return ZB_ERR_ARG;
+    }
+    return ZB_OK;
+}
+
+zb_status moments_ok(const zb_adamw_tensor& t, bool state8) {
+    if (t.count == 0) return ZB_OK;
+    if (!fixed_ok(t.m) || !fixed_ok(t.v)) return ZB_ERR_ARG;
+    if (state8 && (!fixed_ok(t.m_scale) || !fixed_ok(t.v_scale))) return ZB_ERR_ARG;
+    return ZB_OK;
+}
+
+}  // namespace
+
+}  // namespace zbk
+
+using namespace zbk;
+
+extern "C" zb_status zb_op_adamw_step(const zb_adamw_tensor* tensors, int32_t n, const zb_adamw_config* cfg, int64_t step,
+                                      const float* grad_scale, const float* lr_device, const int64_t* step_device,
+                                      void* stream) {
+    if (!cfg) return ZB_ERR_ARG;
+    ZB_TRY(tensors_ok(tensors, n));
+    if (cfg->state_bits != 32 && cfg->state_bits != 8) return ZB_ERR_ARG;
+    if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps > 0.0) ||
+        !std::isfinite(cfg->eps) || !std::isfinite(cfg->lr) || (!step_device && step < 1))
+        return ZB_ERR_ARG;
+    auto word_ok = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
+    if (!word_ok(grad_scale, 4) || !word_ok(lr_device, 4) || !word_ok(step_device, 8)) return ZB_ERR_ARG;
+    const bool state8 = cfg->state_bits == 8;
+    for (int i = 0; i < n; ++i) {
+        const zb_adamw_tensor& t = tensors[i];
+        if (!std::isfinite(t.weight_decay)) return ZB_ERR_ARG;
+        if (t.count == 0) continue;
+        if (!fixed_ok(t.param) || !fixed_ok(t.grad) || (t.master && !aligned16(t.master))) return ZB_ERR_ARG;
+        if (t.master && t.param_dtype == ZB_F32) return ZB_ERR_ARG;  // a float32 parameter is its own master
+        ZB_TRY(moments_ok(t, state8));
+    }
+    ZB_TRY(device_ok());
+    AdamArgs a{};
+    a.beta1 = static_cast<float>(cfg->beta1);
+    a.beta2 = static_cast<float>(cfg->beta2);
+    a.one_minus_beta1 = static_cast<float>(1.0 - cfg->beta1);
+    a.one_minus_beta2 = static_cast<float>(1.0 - cfg->beta2);
+    a.eps = static_cast<float>(cfg->eps);
+    a.lr = static_cast<float>(cfg->lr);
+    if (!step_device) {
+        a.bias1 = static_cast<float>(1.0 - std::pow(cfg->beta1, static_cast<double>(step)));
+        a.rsqrt_bias2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(cfg->beta2, static_cast<double>(step))));
+        a.step = static_cast<uint32_t>(step);
+    }
+    a.log_beta1 = static_cast<float>(std::log(cfg->beta1));
+    a.log_beta2 = static_cast<float>(std::log(cfg->beta2));
+    a.seed = cfg->seed;
+    a.stochastic = cfg->stochastic != 0;
+    a.grad_scale = grad_scale;
+    a.lr_dev = lr_device;
+    a.step_dev = step_device;
+    cudaStream_t s = as_stream(stream);
+    return cuda_status(for_tables(tensors, n, kChunk, [&](const AdamTable& tab, int64_t c, int) {
+        if (state8)
+            adamw_kernel<true><<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, a);
+        else
+            adamw_kernel<false><<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, a);
+        return cudaGetLastError();
+    }));
+}
+
+extern "C" zb_status zb_op_adamw_unpack(const zb_adamw_tensor* tensors, int32_t n, float* const* m, float* const* v,
+                                        void* stream) {
+    ZB_TRY(tensors_ok(tensors, n));
+    if (n > 0 && (!m || !v)) return ZB_ERR_ARG;
+    for (int i = 0; i < n; ++i) {
+        ZB_TRY(moments_ok(tensors[i], true));
+        if (tensors[i].count > 0 && (!fixed_ok(m[i]) || !fixed_ok(v[i]))) return ZB_ERR_ARG;
+    }
+    ZB_TRY(device_ok());
+    cudaStream_t s = as_stream(stream);
+    return cuda_status(for_tables(tensors, n, kChunk, [&](const AdamTable& tab, int64_t c, int i0) {
+        AdamUnpack out{};
+        for (int i = 0; i < tab.n; ++i) {
+            out.m[i] = m[i0 + i];
+            out.v[i] = v[i0 + i];
+        }
+        adamw_unpack_kernel<<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, out);
+        return cudaGetLastError();
+    }));
+}
+
+extern "C" size_t zb_op_grad_norm_scratch_bytes(const zb_adamw_tensor* tensors, int32_t n) {
+    if (tensors_ok(tensors, n) != ZB_OK) return 0;
+    int64_t c = 0;
+    for (int i = 0; i < n; ++i) c += chunks_of(tensors[i].count, int64_t(kNormChunks) * kChunk);
+    return static_cast<size_t>(std::max<int64_t>(c, 1)) * sizeof(double);
+}
+
+extern "C" zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, float max_norm, float* out, void* scratch,
+                                     size_t scratch_bytes, void* stream) {
+    ZB_TRY(tensors_ok(tensors, n));
+    if (!(max_norm > 0.f) || !fixed_ok(out)) return ZB_ERR_ARG;
+    for (int i = 0; i < n; ++i)
+        if (tensors[i].count > 0 && !fixed_ok(tensors[i].grad)) return ZB_ERR_ARG;
+    if (!scratch || !aligned16(scratch) || scratch_bytes < zb_op_grad_norm_scratch_bytes(tensors, n)) return ZB_ERR_WORKSPACE;
+    ZB_TRY(device_ok());
+    cudaStream_t s = as_stream(stream);
+    double* part = static_cast<double*>(scratch);
+    int64_t done = 0;
+    const cudaError_t e = for_tables(tensors, n, int64_t(kNormChunks) * kChunk, [&](const AdamTable& tab, int64_t c, int) {
+        norm_partial_kernel<<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, part + done);
+        done += c;
+        return cudaGetLastError();
+    });
+    if (e != cudaSuccess) return ZB_ERR_CUDA;
+    norm_final_kernel<<<1, 1024, 0, s>>>(part, done, max_norm, out);
+    return cuda_status(cudaGetLastError());
+}

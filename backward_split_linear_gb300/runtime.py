@@ -120,3 +120,78 @@ class Stage:
             self.close()
         except Exception:
             pass
+
+
+class AdamW:
+    """AdamW over a list of tensors, or over a stage's parameters and accumulators (`for_stage`).
+
+    Each entry of `tensors` is a dict with param, grad, m and v, and where they apply master, m_scale, v_scale and
+    weight_decay (see `binding.adamw_table`).  The object keeps the tensors, the step number and the norm's scratch; it
+    allocates nothing after it is made, so `grad_norm` and `step` can be captured into a graph (then with `step_device`,
+    the device's step number, which the graph itself advances).
+    """
+
+    def __init__(self, tensors, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, state_bits=32, stochastic=False, seed=0, step=0,
+                 step_device=None, lr_device=None):
+        self.tensors = list(tensors)
+        self.table = zb.adamw_table(self.tensors)
+        self.cfg = zb.make_adamw_config(lr, beta1, beta2, eps, state_bits, stochastic, seed)
+        self.steps = step
+        self.step_device, self.lr_device = step_device, lr_device
+        for name, t, dtype in (("step_device", step_device, torch.int64), ("lr_device", lr_device, torch.float32)):
+            if t is not None and t.dtype != dtype:
+                raise zb.ZBError(-1, f"AdamW ({name} is {dtype})")
+        want = torch.uint8 if state_bits == 8 else torch.float32
+        if any(t["m"].dtype != want or t["v"].dtype != want for t in self.tensors):
+            raise zb.ZBError(-1, f"AdamW (moments of {state_bits} bits are {want})")
+        device = self.tensors[0]["param"].device if self.tensors else "cuda"
+        nbytes = zb.zb_op_grad_norm_scratch_bytes(self.table, len(self.tensors))
+        self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.norm = torch.zeros(4, dtype=torch.float32, device=device)  # norm, clip coefficient
+        self.stage = None
+        self._states = None
+
+    @staticmethod
+    def for_stage(stage, lr=1e-3, weight_decay=0.1, state_bits=32, master=True, **kw):
+        """Over every parameter of a `Stage`, with fresh moments: weights decay, RMSNorm gammas do not.  `master`: float32
+        copies of the bf16 weights."""
+        tensors = []
+        for prm, grads in zip(stage.params, stage.grads):
+            for name, p in prm.items():
+                n, dev = p.numel(), p.device
+                t = {"param": p, "grad": grads[name], "weight_decay": weight_decay if p.dtype == torch.bfloat16 else 0.0}
+                if master and p.dtype == torch.bfloat16:
+                    t["master"] = p.float()
+                for s in ("m", "v"):
+                    t[s] = torch.zeros(n, dtype=torch.uint8 if state_bits == 8 else torch.float32, device=dev)
+                    if state_bits == 8:
+                        t[s + "_scale"] = torch.zeros((n + 255) // 256, dtype=torch.float32, device=dev)
+                tensors.append(t)
+        opt = AdamW(tensors, lr=lr, state_bits=state_bits, **kw)
+        opt.stage = stage
+        return opt
+
+    def grad_norm(self, max_norm=1.0, stream=None):
+        """(norm, clip coefficient) of all the gradients: float32 scalars on the device, rewritten by the next call."""
+        zb.zb_op_grad_norm(self.table, len(self.tensors), max_norm, self.norm, self.scratch, self.scratch.numel(), stream)
+        return self.norm[0], self.norm[1]
+
+    def step(self, grad_scale=None, stream=None):
+        """One update.  A stage's weights must not change between F and W of a microbatch: its microbatches must all have
+        run their W."""
+        if self.stage is not None and self.stage.stats()[0] != 0:
+            raise zb.ZBError(-3, "AdamW.step (microbatches of the stage still wait for their W)")
+        zb.zb_op_adamw_step(self.table, len(self.tensors), self.cfg, self.steps + 1, grad_scale, self.lr_device,
+                            self.step_device, stream)
+        self.steps += 1
+
+    def unpack_states(self, stream=None):
+        """[(m, v)] as float32 values; 8-bit states are written into buffers that the next call rewrites."""
+        if self.cfg.state_bits != 8:
+            return [(t["m"], t["v"]) for t in self.tensors]
+        if self._states is None:
+            self._states = [tuple(torch.empty(t["m"].numel(), dtype=torch.float32, device=t["m"].device) for _ in range(2))
+                            for t in self.tensors]
+        zb.zb_op_adamw_unpack(self.table, len(self.tensors), [m for m, _ in self._states], [v for _, v in self._states],
+                              stream)
+        return self._states

@@ -293,6 +293,135 @@ zb_status zb_op_attention_causal_backward(const void* qkv, const void* a, const 
                                           int32_t tokens, int32_t n_heads, int32_t n_kv_heads,
                                           int32_t head_dim, int32_t seq_len, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions.  Beside the attention core, whose scores carry no position
+ * of their own.  Pair i (0 <= i < rotary_dim / 2) of a head at position p
+ * turns by the angle p f_i:
+ *   y_a = g (x_a cos - x_b sin),  y_b = g (x_b cos + x_a sin);
+ * the backward turns by the opposite angle: dx_a = g (dy_a cos + dy_b sin),
+ * dx_b = g (dy_b cos - dy_a sin).  Elements behind rotary_dim pass unchanged.
+ *  - x: n_heads heads of head_dim bf16 elements per token, tokens ld_x elements
+ *    apart; y likewise, ld_y apart.  Strides may be larger than
+ *    n_heads * head_dim, so the query and key heads at the front of a qkv
+ *    tensor rotate in place: n_heads = nh + nkv, ld = (nh + 2 nkv) head_dim.
+ *    y may be x (with the same stride); otherwise they must not overlap.
+ *    Elements between n_heads * head_dim and a stride are left as they are.
+ *  - pairs: a = i, b = i + rotary_dim / 2 (HALF), or a = 2 i, b = 2 i + 1
+ *    (INTERLEAVED).
+ *  - rotary_dim is a multiple of 16, at most head_dim and 1024; strides and
+ *    head_dim are multiples of 8, n_heads * head_dim one of 64
+ *    (ZB_ERR_SHAPE).
+ *  - positions: int32 [tokens] on the device (any value; negative ones turn
+ *    backwards), or NULL for the row number.
+ *  - turns: uint64 [rotary_dim / 2] on the device: f_i / (2 pi) as a 64-bit
+ *    binary fraction of a turn (a copy of what zb_rotary_frequencies wrote).
+ *    Angles are exact modulo a turn to p 2^-65 turns at any position.
+ *  - magnitude is g. */
+typedef enum { ZB_ROTARY_HALF = 0, ZB_ROTARY_INTERLEAVED = 1 } zb_rotary_pairs;
+
+typedef enum {
+    ZB_ROTARY_SCALE_NONE = 0,   /* f_i = base^(-2 i / rotary_dim) */
+    ZB_ROTARY_SCALE_LINEAR = 1, /* f_i / factor: positions interpolated */
+    ZB_ROTARY_SCALE_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+    ZB_ROTARY_SCALE_YARN = 3,   /* f_i / factor for pairs below `low` turns over the original
+                                   context, f_i above `high`, a ramp over the pair number in
+                                   between; g = 0.1 ln(factor) + 1 */
+    ZB_ROTARY_SCALE_BANDED = 4  /* the same with a ramp over the turns, and g = 1 */
+} zb_rotary_scaling;
+
+typedef struct {
+    int32_t scaling;     /* zb_rotary_scaling */
+    int32_t rotary_dim;
+    double base;         /* > 1 */
+    double factor;       /* >= 1: how much longer the context is (all but NONE) */
+    double context;      /* the original context length (YARN, BANDED) */
+    double low, high;    /* turns, 0 < low < high (YARN: usually 1 and 32; BANDED: 1 and 4) */
+} zb_rotary_config;
+
+/* Writes rotary_dim / 2 turns (host memory) and g.  CPU only. */
+zb_status zb_rotary_frequencies(const zb_rotary_config* cfg, uint64_t* turns, float* magnitude);
+
+zb_status zb_op_rotary_forward(const void* x, int64_t ld_x, void* y, int64_t ld_y,
+                               const int32_t* positions, const uint64_t* turns, float magnitude,
+                               int32_t tokens, int32_t n_heads, int32_t head_dim,
+                               int32_t rotary_dim, int32_t pairs, void* stream);
+zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx,
+                                const int32_t* positions, const uint64_t* turns, float magnitude,
+                                int32_t tokens, int32_t n_heads, int32_t head_dim,
+                                int32_t rotary_dim, int32_t pairs, void* stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW: the optimizer step that the weight gradients of a flush wait for
+ * ([G3]: accumulators are complete after the last W; [G1]: only the optimizer
+ * step needs W).  One call updates any number of tensors:
+ *   g = grad * *grad_scale
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *  - param: bf16 or float32, updated in place.  master: float32 copy of a bf16
+ *    param, updated in place and rounded to it; NULL: the param itself is read
+ *    and rounded.  grad: bf16 or float32, read only.
+ *  - m, v: float32 (state_bits 32), or 8-bit codes with float32 scales
+ *    (state_bits 8): m_scale, v_scale hold ceil(count / 256) floats, one per
+ *    256 consecutive elements.  A code's value is its scale times c for
+ *    c < 8, else (8 + c % 8) 2^(c / 8 - 1); for m bit 7 is the sign and c the
+ *    other seven bits.  A step sets each scale to the block's largest value
+ *    times 1 / 245760 (m) or 1 / (15 2^30) (v), the largest codes' values, and
+ *    never below the smallest normal float; a nonzero v never gets the code 0.
+ *    New states are all-zero bytes, scales included.
+ *  - stochastic != 0: 8-bit codes, and bf16 params without a master copy,
+ *    round up with the probability of their remainder, by a hash of (seed, t,
+ *    the tensor's place in the list, the element); 0: to the nearest.  Same
+ *    call, same bits.
+ *  - t is `step` (from 1), or *step_device when not NULL; lr is cfg->lr, or
+ *    *lr_device when not NULL; grad_scale NULL means 1.  The device forms let
+ *    a captured graph advance.  When *grad_scale is not finite the call writes
+ *    nothing: a skipped step.
+ *  - Tensors are 16-byte aligned and must not overlap; count may be 0.  The
+ *    array is read during the call and not kept. */
+typedef enum { ZB_BF16 = 0, ZB_F32 = 1 } zb_dtype;
+
+typedef struct {
+    void* param;
+    float* master;       /* NULL, or the float32 master copy of a bf16 param */
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;      /* state_bits 8 only */
+    float* v_scale;
+    int64_t count;
+    float weight_decay;
+    int32_t param_dtype; /* zb_dtype */
+    int32_t grad_dtype;  /* zb_dtype */
+    int32_t reserved;
+} zb_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps > 0 */
+    int32_t state_bits;           /* 32 or 8 */
+    int32_t stochastic;
+    uint32_t seed;
+    int32_t reserved;
+} zb_adamw_config;
+
+zb_status zb_op_adamw_step(const zb_adamw_tensor* tensors, int32_t n, const zb_adamw_config* cfg,
+                           int64_t step, const float* grad_scale, const float* lr_device,
+                           const int64_t* step_device, void* stream);
+
+/* The 8-bit moments as float32 values: m[i], v[i] (host arrays of device
+ * pointers) receive count floats of tensor i.  For checkpoints and diagnostics. */
+zb_status zb_op_adamw_unpack(const zb_adamw_tensor* tensors, int32_t n, float* const* m,
+                             float* const* v, void* stream);
+
+/* The L2 norm of all the tensors' gradients (only grad, grad_dtype and count
+ * are read): out[0] = norm, out[1] = min(1, max_norm / (norm + 1e-6)), the
+ * grad_scale of a clipped step; NaN when the norm is not finite.  out is two
+ * floats on the device, 16-byte aligned.  A fixed partition and order: the same
+ * bits every time.  scratch: device memory of at least
+ * zb_op_grad_norm_scratch_bytes(tensors, n) bytes, contents ignored. */
+size_t zb_op_grad_norm_scratch_bytes(const zb_adamw_tensor* tensors, int32_t n);
+zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, float max_norm, float* out,
+                          void* scratch, size_t scratch_bytes, void* stream);
+
 /* Device status word shared by all kernels of the library on the current
  * device: 0 = fine, else the code of the first wait that ran out:
  *   1  GEMM TMA producer waiting for a free shared-memory stage

@@ -1,0 +1,151 @@
+"""The training operators without a GPU: refusals, the frequency tables, and the oracle's own identities."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from backward_split_linear_gb300 import binding as zb
+from oracle import train_ops as O
+
+FAKE = 1 << 20  # never dereferenced: the calls below fail their checks before any device call
+
+
+def refused(name, fn, *args, **kw):
+    with pytest.raises(zb.ZBError) as e:
+        fn(*args, **kw)
+    assert e.value.name == name
+
+
+# ---------------------------------------------------------------- rotary
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="linear", factor=4.0), dict(scaling="ntk", factor=8.0),
+                                dict(scaling="yarn", factor=8.0, context=8192.0),
+                                dict(scaling="banded", factor=8.0, context=8192.0, low=1.0, high=4.0)])
+@pytest.mark.parametrize("rot,base", [(16, 10000.0), (64, 500000.0), (128, 10000.0), (1024, 10.0)])
+def test_frequencies_equal_the_definitions(zblib, rot, base, kw):
+    turns, g = zb.zb_rotary_frequencies(rot, base, **kw)
+    f, g_ref = O.rotary_frequencies(rot, base, **kw)
+    # a handful of float64 roundings (pow, the ramp) on either side, and half a unit of the 64-bit fraction
+    np.testing.assert_allclose(np.array([t / 2.0 ** 64 for t in turns]), f / (2.0 * np.pi), rtol=64 * 2.0 ** -53,
+                               atol=2.0 ** -65)
+    assert abs(g - g_ref) <= 2.0 ** -24 * g_ref
+
+
+def test_frequency_refusals(zblib):
+    refused("ZB_ERR_SHAPE", zb.zb_rotary_frequencies, 24)
+    refused("ZB_ERR_SHAPE", zb.zb_rotary_frequencies, 0)
+    refused("ZB_ERR_SHAPE", zb.zb_rotary_frequencies, 1040)
+    refused("ZB_ERR_ARG", zb.zb_rotary_frequencies, 64, 1.0)
+    refused("ZB_ERR_ARG", zb.zb_rotary_frequencies, 64, float("nan"))
+    refused("ZB_ERR_ARG", zb.zb_rotary_frequencies, 64, scaling="linear", factor=0.5)
+    refused("ZB_ERR_ARG", zb.zb_rotary_frequencies, 64, scaling="yarn", factor=2.0)               # no context
+    refused("ZB_ERR_ARG", zb.zb_rotary_frequencies, 64, scaling="banded", factor=2.0, context=8.0, low=4.0, high=4.0)
+    bad = zb.zb_rotary_config(9, 64, 10000.0, 1.0, 0.0, 1.0, 4.0)
+    out, mag = (ctypes.c_uint64 * 32)(), ctypes.c_float()
+    assert zblib.zb_rotary_frequencies(ctypes.byref(bad), out, ctypes.byref(mag)) == -1
+
+
+@pytest.mark.parametrize("op", ["zb_op_rotary_forward", "zb_op_rotary_backward"])
+def test_rotary_refusals(zblib, op):
+    ok = dict(x=FAKE, ld=128, y=2 * FAKE, ldy=128, pos=FAKE, turns=FAKE, mag=1.0, t=8, n=2, d=64, rot=64, pairs=0)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return getattr(zblib, op)(a["x"], a["ld"], a["y"], a["ldy"], a["pos"], a["turns"], a["mag"], a["t"], a["n"], a["d"],
+                                  a["rot"], a["pairs"], None)
+
+    for kw in (dict(rot=8), dict(rot=24), dict(rot=80), dict(t=-1), dict(t=(1 << 24) + 1), dict(n=0), dict(d=60), dict(n=3, d=8),
+               dict(ld=120), dict(ldy=132), dict(ld=64), dict(n=1 << 30), dict(n=1, d=2048, rot=2048, ld=2048, ldy=2048)):
+        assert call(**kw) == -2, kw
+    for kw in (dict(x=None), dict(y=None), dict(x=FAKE + 2), dict(pos=FAKE + 2), dict(turns=None), dict(pairs=2),
+               dict(mag=float("nan")), dict(mag=float("inf")), dict(y=FAKE, ldy=192)):
+        assert call(**kw) == -1, kw
+
+
+def test_oracle_rotary_is_a_rotation():
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((9, 2, 32))
+    f, g = O.rotary_frequencies(16)
+    for pairs in ("half", "interleaved"):
+        y = O.rotary(x, np.arange(9) + 100, f, g, pairs)
+        np.testing.assert_allclose((y ** 2).sum(-1), (x ** 2).sum(-1), rtol=1e-12)
+        np.testing.assert_allclose(O.rotary(y, np.arange(9) + 100, f, g, pairs, backward=True), x, atol=1e-12)
+        # scores depend on the difference of positions alone
+        z = O.rotary(x, np.arange(9) + 7, f, g, pairs)
+        np.testing.assert_allclose(y[3, 0] @ y[8, 1], z[3, 0] @ z[8, 1], atol=1e-10)
+
+
+# ---------------------------------------------------------------- AdamW
+
+
+def tensors(n=300, bits=32, **kw):
+    t = {"param": torch.zeros(n, dtype=torch.bfloat16), "grad": torch.zeros(n), "master": torch.zeros(n)}
+    kind = torch.uint8 if bits == 8 else torch.float32
+    t.update(m=torch.zeros(n, dtype=kind), v=torch.zeros(n, dtype=kind))
+    if bits == 8:
+        t.update(m_scale=torch.zeros((n + 255) // 256), v_scale=torch.zeros((n + 255) // 256))
+    t.update(kw)
+    return t
+
+
+def test_adamw_table_refusals(zblib):
+    zb.adamw_table([tensors(), tensors(bits=8)])
+    for kw in (dict(grad=torch.zeros(299)), dict(param=torch.zeros(300, dtype=torch.float16)), dict(m=torch.zeros(10)),
+               dict(master=torch.zeros(300, dtype=torch.bfloat16)), dict(grad=torch.zeros(600)[::2]), dict(v=None)):
+        refused("ZB_ERR_ARG", zb.adamw_table, [tensors(**kw)])
+    refused("ZB_ERR_ARG", zb.adamw_table, [tensors(bits=8, m_scale=torch.zeros(1))])
+
+
+def test_adamw_refusals(zblib):
+    def entry(**kw):
+        a = dict(param=FAKE, master=FAKE, grad=FAKE, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, count=100, weight_decay=0.1,
+                 param_dtype=0, grad_dtype=1, reserved=0)
+        a.update(kw)
+        return (zb.zb_adamw_tensor * 1)(zb.zb_adamw_tensor(*[a[k] for k, _ in zb.zb_adamw_tensor._fields_]))
+
+    def step(table, cfg=None, step=1, n=1, **kw):
+        cfg = cfg or zb.make_adamw_config(1e-3)
+        zb.zb_op_adamw_step(table, n, cfg, step, stream=0, **kw)
+
+    for kw in (dict(param=None), dict(grad=FAKE + 4), dict(m=None), dict(master=FAKE + 8), dict(param_dtype=2), dict(grad_dtype=5),
+               dict(param_dtype=1), dict(weight_decay=float("nan"))):
+        refused("ZB_ERR_ARG", step, entry(**kw))
+    for kw in (dict(count=-1), dict(count=(1 << 40) + 1)):
+        refused("ZB_ERR_SHAPE", step, entry(**kw))
+    eight = zb.make_adamw_config(1e-3, state_bits=8)
+    refused("ZB_ERR_ARG", step, entry(v_scale=None), eight)
+    for kw in (dict(beta1=1.0), dict(beta2=-0.1), dict(eps=0.0), dict(lr=float("inf")), dict(state_bits=16)):
+        refused("ZB_ERR_ARG", step, entry(), zb.make_adamw_config(**{"lr": 1e-3, **kw}))
+    refused("ZB_ERR_ARG", step, entry(), step=0)
+    refused("ZB_ERR_ARG", step, entry(), n=-1)
+    refused("ZB_ERR_ARG", step, entry(), grad_scale=FAKE + 2)
+    refused("ZB_ERR_ARG", step, entry(), step_device=FAKE + 4)
+    nbytes = zb.zb_op_grad_norm_scratch_bytes(entry(), 1)
+    assert nbytes >= 8 and zb.zb_op_grad_norm_scratch_bytes(entry(count=-1), 1) == 0
+    refused("ZB_ERR_ARG", zb.zb_op_grad_norm, entry(), 1, 0.0, FAKE, FAKE, nbytes, stream=0)
+    refused("ZB_ERR_ARG", zb.zb_op_grad_norm, entry(grad=None), 1, 1.0, FAKE, FAKE, nbytes, stream=0)
+    refused("ZB_ERR_WORKSPACE", zb.zb_op_grad_norm, entry(), 1, 1.0, FAKE, FAKE, nbytes - 1, stream=0)
+    refused("ZB_ERR_ARG", zb.zb_op_adamw_unpack, entry(m_scale=None), 1, [FAKE], [FAKE], stream=0)
+    refused("ZB_ERR_ARG", zb.zb_op_adamw_unpack, entry(), 1, [None], [FAKE], stream=0)
+
+
+@pytest.mark.parametrize("signed", [True, False])
+def test_oracle_codes(signed):
+    """Every code's value packs to itself, nearest rounding takes the nearer neighbour, and the noise decides the rest."""
+    values = O.code_values(False)[: 128 if signed else 256]
+    assert values[-1] == (O.M_TOP if signed else O.V_TOP) and np.all(np.diff(values) > 0)
+    codes, scales = O.pack(values.astype(np.float32), signed, 0x8000)
+    # the largest value's block scale is exactly 1
+    assert np.array_equal(codes, np.arange(values.size)) and scales[0] == 1.0
+    rng = np.random.default_rng(1)
+    x = (np.exp(rng.uniform(-6, np.log(float(values[-1])), 255))).astype(np.float32)
+    x = np.append(x, np.float32(values[-1]))
+    got = O.unpack(*O.pack(x, signed, 0x8000), signed)
+    near = values[np.abs(values[None, :] - x[:, None].astype(np.float64)).argmin(1)]
+    if not signed:
+        near = np.maximum(near, 1.0)
+    assert np.array_equal(got, near.astype(np.float32))
+    down, up = O.unpack(*O.pack(x, signed, 0), signed), O.unpack(*O.pack(x, signed, 0xFFFF), signed)
+    assert np.all(down <= np.maximum(x, 0.0 if signed else 1.0)) and np.all(up >= x * (1 - 2.0 ** -16))
