@@ -115,6 +115,12 @@ _SIGS = {
     "zb_op_attention_stat_stride": (c_int32, [c_int32]),
     "zb_op_attention_causal_forward": (c_int32, [c_void_p, c_void_p, c_void_p] + [c_int32] * 5 + [c_void_p]),
     "zb_op_attention_causal_backward": (c_int32, [c_void_p] * 6 + [c_int32] * 5 + [c_void_p]),
+    "zb_op_attention_document_plan_bytes": (c_size_t, [c_int32]),
+    "zb_op_attention_document_plan": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "zb_op_attention_document_scratch_bytes": (c_size_t, [c_int32, c_int32]),
+    "zb_op_attention_document_forward": (c_int32, [c_void_p] * 5 + [c_float] + [c_int32] * 4 + [c_void_p]),
+    "zb_op_attention_document_backward": (c_int32, [c_void_p] * 7 + [c_float] + [c_int32] * 4
+                                          + [c_void_p, c_size_t, c_void_p]),
     "zb_rotary_frequencies": (c_int32, [ctypes.POINTER(zb_rotary_config), ctypes.POINTER(ctypes.c_uint64),
                                         ctypes.POINTER(c_float)]),
     "zb_op_rotary_forward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_float] + [c_int32] * 5
@@ -341,6 +347,35 @@ def zb_op_attention_causal_backward(qkv, a, da, lse, dvec, dqkv, tokens, n_heads
     _check(lib().zb_op_attention_causal_backward(_ptr(qkv), _ptr(a), _ptr(da), _ptr(lse), _ptr(dvec), _ptr(dqkv),
                                                  tokens, n_heads, n_kv_heads, head_dim, seq_len, _stream(stream)),
            "zb_op_attention_causal_backward")
+
+
+# ---------------------------------------------------------------- attention inside packed documents
+
+
+def zb_op_attention_document_plan_bytes(tokens):
+    return lib().zb_op_attention_document_plan_bytes(tokens)
+
+
+def zb_op_attention_document_plan(doc_offsets, prefix_len, n_docs, tokens, plan, plan_bytes, positions=None, stream=None):
+    _check(lib().zb_op_attention_document_plan(_ptr(doc_offsets), _ptr(prefix_len), n_docs, tokens, _ptr(plan), plan_bytes,
+                                               _ptr(positions), _stream(stream)), "zb_op_attention_document_plan")
+
+
+def zb_op_attention_document_scratch_bytes(tokens, n_heads):
+    return lib().zb_op_attention_document_scratch_bytes(tokens, n_heads)
+
+
+def zb_op_attention_document_forward(qkv, a, lse, plan, slopes, cap, tokens, n_heads, n_kv_heads, head_dim, stream=None):
+    _check(lib().zb_op_attention_document_forward(_ptr(qkv), _ptr(a), _ptr(lse), _ptr(plan), _ptr(slopes), cap, tokens,
+                                                  n_heads, n_kv_heads, head_dim, _stream(stream)),
+           "zb_op_attention_document_forward")
+
+
+def zb_op_attention_document_backward(qkv, a, da, lse, dqkv, plan, slopes, cap, tokens, n_heads, n_kv_heads, head_dim,
+                                      scratch, scratch_bytes, stream=None):
+    _check(lib().zb_op_attention_document_backward(_ptr(qkv), _ptr(a), _ptr(da), _ptr(lse), _ptr(dqkv), _ptr(plan),
+                                                   _ptr(slopes), cap, tokens, n_heads, n_kv_heads, head_dim, _ptr(scratch),
+                                                   scratch_bytes, _stream(stream)), "zb_op_attention_document_backward")
 
 
 # ---------------------------------------------------------------- rotary positions

@@ -29,8 +29,10 @@ using zbk::cuda_status;
 using zbk::device_ok;
 using zbk::feature_ok;
 using zbk::fixed_ok;
+using zbk::heads_ok;
 using zbk::kMaxTokens;
 using zbk::rows_ok;
+using zbk::stat_stride;
 using zbk::tokens_ok;
 
 namespace {
@@ -213,19 +215,10 @@ zb_status run_backward_weight(const void* dy, const void* x, float* dw, int t, i
     return cuda_status(zbk::launch_gemm(g, s));
 }
 
-bool heads_ok(int32_t nh, int32_t nkv, int32_t hd) {
-    if (nh <= 0 || nkv <= 0 || hd <= 0 || hd % 8 != 0 || nh % nkv != 0) return false;
-    if (!feature_ok(nh * hd) || !feature_ok((nh + 2 * nkv) * hd)) return false;
-    return true;
-}
-
 // Causal attention: head_dim 64 or 128, sequences of a multiple of 128 tokens (or one sequence).
 bool causal_ok(int32_t nh, int32_t nkv, int32_t hd, int32_t seq_len) {
     return heads_ok(nh, nkv, hd) && (hd == 64 || hd == 128) && seq_len >= 0 && seq_len % 128 == 0;
 }
-
-// Floats per head row of the attention statistics (lse, rowsum): whole 128-row blocks.
-int32_t stat_stride(int32_t tokens) { return std::max<int32_t>(128, (tokens + 127) / 128 * 128); }
 
 zbk::AttnShape attn_shape(int t, int nh, int nkv, int hd, int seq_len, int ld_stat) {
     zbk::AttnShape a;

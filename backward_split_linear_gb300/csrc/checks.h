@@ -1,6 +1,7 @@
 // Argument checks that every C entry point shares (see the conventions in zb.h).
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -26,6 +27,15 @@ inline bool fixed_ok(const void* p) { return p && aligned16(p); }
 inline bool feature_ok(int32_t f) { return f > 0 && f <= kMaxFeature && f % 64 == 0; }
 
 inline bool tokens_ok(int32_t t) { return t >= 0 && t <= kMaxTokens; }
+
+inline bool heads_ok(int32_t nh, int32_t nkv, int32_t hd) {
+    if (nh <= 0 || nkv <= 0 || hd <= 0 || hd % 8 != 0 || nh % nkv != 0) return false;
+    if (!feature_ok(nh * hd) || !feature_ok((nh + 2 * nkv) * hd)) return false;
+    return true;
+}
+
+// Floats per head row of the attention statistics (lse, rowsum): whole 128-row blocks.
+inline int32_t stat_stride(int32_t tokens) { return std::max<int32_t>(128, (tokens + 127) / 128 * 128); }
 
 inline zb_status device_ok() {
     const int arch = device_arch();

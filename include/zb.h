@@ -293,6 +293,57 @@ zb_status zb_op_attention_causal_backward(const void* qkv, const void* a, const 
                                           int32_t tokens, int32_t n_heads, int32_t n_kv_heads,
                                           int32_t head_dim, int32_t seq_len, void* stream);
 
+/* Softmax attention inside packed documents, with the same tensors, heads and
+ * grouped K/V as the causal core.  The rows of a microbatch are documents one
+ * behind another; for query i and key j of one document and head h
+ *   s = q_i k_j^T / sqrt(hd);  cap > 0: s = cap tanh(s / cap);
+ *   slopes given: s = s - slopes[h] |i - j|;
+ *   a_i = softmax over the visible j of s, times v_j.
+ * Key j is visible to query i when j <= i, or when j is among the document's
+ * first prefix_len rows (a prompt that all of its document sees).
+ *
+ * The plan turns a batch's offsets into what the kernels read; one plan serves
+ * every layer's forward and backward of that batch.
+ *  - doc_offsets: int32 [n_docs + 1] on the device, not decreasing: document d is
+ *    the rows [doc_offsets[d], doc_offsets[d + 1]) (it may be empty).  NULL with
+ *    n_docs = 1: all rows are one document.  Offsets are data and are not
+ *    checked: values that decrease give an unspecified mask, but no access
+ *    outside the tensors.
+ *  - prefix_len: int32 [n_docs] on the device, or NULL for none; values are
+ *    clamped to [0, the document's length].
+ *  - Rows before the first or behind the last document are padding: they see
+ *    nothing and nothing sees them, whatever they hold (NaN and infinity
+ *    included).  Their a and dqkv are zeros and their lse is -infinity.  The
+ *    same holds across documents: a value that is not finite in one document
+ *    reaches no row of another, and a key's reaches no query that does not see
+ *    it.
+ *  - positions: int32 [tokens], receives each row's place in its document (0
+ *    for padding), for the rotary positions; may be NULL.
+ *  - plan: zb_op_attention_document_plan_bytes(tokens) bytes of device memory.
+ *    The attention calls must get a plan made for the same `tokens`.
+ *
+ * slopes: float32 [n_heads] on the device, finite, or NULL; a constant, which
+ * gets no gradient.  cap: 0 (none) or up to 1e30.  lse as in the causal core.
+ * scratch: device memory of at least
+ * zb_op_attention_document_scratch_bytes(tokens, n_heads) bytes, contents
+ * ignored; calls that share it must not overlap on the GPU.  hd is 64 or 128.
+ * Every row of a and dqkv is written, rows at and behind `tokens` are left as
+ * they are, and results are bitwise reproducible. */
+size_t zb_op_attention_document_plan_bytes(int32_t tokens);
+zb_status zb_op_attention_document_plan(const int32_t* doc_offsets, const int32_t* prefix_len,
+                                        int32_t n_docs, int32_t tokens, void* plan,
+                                        size_t plan_bytes, int32_t* positions, void* stream);
+size_t zb_op_attention_document_scratch_bytes(int32_t tokens, int32_t n_heads);
+zb_status zb_op_attention_document_forward(const void* qkv, void* a, float* lse, const void* plan,
+                                           const float* slopes, float cap, int32_t tokens,
+                                           int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                           void* stream);
+zb_status zb_op_attention_document_backward(const void* qkv, const void* a, const void* da,
+                                            const float* lse, void* dqkv, const void* plan,
+                                            const float* slopes, float cap, int32_t tokens,
+                                            int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                            void* scratch, size_t scratch_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Rotary positions.  Beside the attention core, whose scores carry no position
  * of their own.  Pair i (0 <= i < rotary_dim / 2) of a head at position p

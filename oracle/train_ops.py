@@ -62,6 +62,72 @@ def rotary(x, positions, f, magnitude, pairs, backward=False):
     return y
 
 
+# ---------------------------------------------------------------- attention inside packed documents
+
+
+def document_visible(t, offsets, prefix=None):
+    """[t, t] truth values: row i sees key j."""
+    see = np.zeros((t, t), dtype=bool)
+    for d in range(len(offsets) - 1):
+        s, e = offsets[d], offsets[d + 1]
+        see[s:e, s:e] = np.tril(np.ones((e - s, e - s), dtype=bool))
+        if prefix is not None:
+            see[s:e, s:min(e, s + max(0, prefix[d]))] = True
+    return see
+
+
+def _document_scores(q, k, see, cap, slope):
+    """(scores with -inf where hidden, the cap's derivative)."""
+    s = np.where(see, (q @ k.T) / np.sqrt(q.shape[1]), 0.0)
+    deriv = np.ones_like(s)
+    if cap:
+        r = np.tanh(s / cap)
+        deriv, s = 1.0 - r * r, cap * r
+    i = np.arange(q.shape[0])
+    return np.where(see, s - slope * np.abs(i[:, None] - i[None, :]), -np.inf), deriv
+
+
+def document_attention(qkv, nh, nkv, d, see, cap=0.0, slopes=None):
+    """(a [t, nh d], lse [nh, t] in base 2); rows that see nothing get zeros and -inf.  Values of hidden keys are never
+    used: they may be NaN."""
+    t = qkv.shape[0]
+    x = qkv.reshape(t, nh + 2 * nkv, d)
+    a, lse = np.zeros((t, nh, d)), np.full((nh, t), -np.inf)
+    live = see.any(axis=1)
+    for h in range(nh):
+        j = nh + h // (nh // nkv)
+        with np.errstate(invalid="ignore"):
+            s, _ = _document_scores(x[:, h], x[:, j], see, cap, 0.0 if slopes is None else slopes[h])
+        for i in np.nonzero(live)[0]:
+            keys = np.nonzero(see[i])[0]
+            z = s[i, keys]
+            top = z.max()
+            p = np.exp(z - top)
+            lse[h, i] = (top + np.log(p.sum())) / np.log(2.0)
+            a[i, h] = (p / p.sum()) @ x[keys, j + nkv]
+    return a.reshape(t, nh * d), lse
+
+
+def document_attention_grad(da, qkv, nh, nkv, d, see, cap=0.0, slopes=None):
+    """Gradient of document_attention with respect to qkv (finite inputs)."""
+    t = qkv.shape[0]
+    x, dy = qkv.reshape(t, nh + 2 * nkv, d), da.reshape(t, nh, d)
+    out = np.zeros_like(x)
+    for h in range(nh):
+        j = nh + h // (nh // nkv)
+        s, deriv = _document_scores(x[:, h], x[:, j], see, cap, 0.0 if slopes is None else slopes[h])
+        top = np.where(see.any(axis=1), s.max(axis=1, initial=-np.inf), 0.0)
+        p = np.exp(s - top[:, None])
+        total = p.sum(axis=1, keepdims=True)
+        p = np.divide(p, total, out=np.zeros_like(p), where=total > 0)
+        out[:, j + nkv] += p.T @ dy[:, h]
+        dp = dy[:, h] @ x[:, j + nkv].T
+        ds = p * (dp - np.sum(p * dp, axis=1, keepdims=True)) * deriv / np.sqrt(d)
+        out[:, h] = ds @ x[:, j]
+        out[:, j] += ds.T @ x[:, h]
+    return out.reshape(t, -1)
+
+
 # ---------------------------------------------------------------- AdamW
 
 F32 = np.float32

@@ -149,3 +149,69 @@ def test_oracle_codes(signed):
     assert np.array_equal(got, near.astype(np.float32))
     down, up = O.unpack(*O.pack(x, signed, 0), signed), O.unpack(*O.pack(x, signed, 0xFFFF), signed)
     assert np.all(down <= np.maximum(x, 0.0 if signed else 1.0)) and np.all(up >= x * (1 - 2.0 ** -16))
+
+
+# ---------------------------------------------------------------- document attention
+
+
+def test_document_refusals(zblib):
+    nbytes = zb.zb_op_attention_document_plan_bytes(300)
+    assert nbytes == 3 * (2 * 128 + 2) * 8 and zb.zb_op_attention_document_plan_bytes(0) == 0
+    assert zb.zb_op_attention_document_plan_bytes(-1) == 0
+    scratch = zb.zb_op_attention_document_scratch_bytes(300, 4)
+    assert scratch >= 4 * 384 * 4 and zb.zb_op_attention_document_scratch_bytes(300, 0) == 0
+
+    def plan(off=FAKE, pre=FAKE, n=2, t=300, p=FAKE, size=nbytes, pos=FAKE):
+        zb.zb_op_attention_document_plan(off, pre, n, t, p, size, pos, stream=0)
+
+    refused("ZB_ERR_SHAPE", plan, t=-1)
+    refused("ZB_ERR_ARG", plan, n=0)
+    refused("ZB_ERR_ARG", plan, off=None)            # no offsets: one document
+    refused("ZB_ERR_ARG", plan, off=FAKE + 2)
+    refused("ZB_ERR_ARG", plan, pos=FAKE + 1)
+    refused("ZB_ERR_WORKSPACE", plan, size=nbytes - 1)
+    refused("ZB_ERR_WORKSPACE", plan, p=None)
+    refused("ZB_ERR_WORKSPACE", plan, p=FAKE + 8)
+
+    def fwd(qkv=FAKE, a=FAKE, lse=FAKE, p=FAKE, slopes=None, cap=0.0, t=300, nh=4, nkv=2, d=64):
+        zb.zb_op_attention_document_forward(qkv, a, lse, p, slopes, cap, t, nh, nkv, d, stream=0)
+
+    def bwd(qkv=FAKE, a=FAKE, da=FAKE, lse=FAKE, dqkv=FAKE, p=FAKE, slopes=None, cap=0.0, t=300, nh=4, nkv=2, d=64, s=FAKE,
+            size=scratch):
+        zb.zb_op_attention_document_backward(qkv, a, da, lse, dqkv, p, slopes, cap, t, nh, nkv, d, s, size, stream=0)
+
+    for call in (fwd, bwd):
+        for kw in (dict(d=96), dict(d=32), dict(nkv=3), dict(nkv=0), dict(t=-1), dict(t=(1 << 24) + 1)):
+            refused("ZB_ERR_SHAPE", call, **kw)
+        for kw in (dict(qkv=None), dict(a=FAKE + 2), dict(lse=None), dict(p=None), dict(p=FAKE + 8), dict(slopes=FAKE + 2),
+                   dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf"))):
+            refused("ZB_ERR_ARG", call, **kw)
+    refused("ZB_ERR_ARG", bwd, da=None)
+    refused("ZB_ERR_ARG", bwd, dqkv=FAKE + 4)
+    refused("ZB_ERR_WORKSPACE", bwd, size=scratch - 1)
+    refused("ZB_ERR_WORKSPACE", bwd, s=None)
+
+
+@pytest.mark.parametrize("cap,slopes", [(0.0, None), (1.5, None), (0.0, [0.3, 0.02, 0.1, 0.0]), (2.0, [0.3, 0.02, 0.1, 0.0])])
+def test_oracle_document_gradient_against_differences(cap, slopes):
+    t, nh, nkv, d = 23, 4, 2, 8
+    rng = np.random.default_rng(2)
+    x, dy, u = (rng.standard_normal((t, w * d)) for w in (nh + 2 * nkv, nh, nh + 2 * nkv))
+    see = O.document_visible(t, [1, 9, 9, 20], [3, 0, 20])
+    f = lambda z: np.sum(O.document_attention(z, nh, nkv, d, see, cap, slopes)[0] * dy)  # noqa: E731
+    h = 1e-5
+    got = np.sum(O.document_attention_grad(dy, x, nh, nkv, d, see, cap, slopes) * u)
+    # central differences: h^2 of truncation, 2^-53 / h of rounding, on sums of some hundreds of terms
+    assert abs((f(x + h * u) - f(x - h * u)) / (2 * h) - got) < 1e-7 * max(1.0, abs(got))
+
+
+def test_oracle_documents_are_independent_and_causal():
+    from oracle import stage as S
+
+    t, nh, nkv, d = 12, 2, 1, 8
+    x = np.random.default_rng(3).standard_normal((t, 4 * d))
+    see = O.document_visible(t, [0, 4, 8, 12])
+    np.testing.assert_allclose(O.document_attention(x, nh, nkv, d, see)[0], S.attention_causal(x, nh, nkv, d, 4), atol=1e-12)
+    dy = np.random.default_rng(4).standard_normal((t, 2 * d))
+    np.testing.assert_allclose(O.document_attention_grad(dy, x, nh, nkv, d, see),
+                               S.attention_causal_grad(dy, x, nh, nkv, d, 4), atol=1e-12)
