@@ -1,12 +1,34 @@
-// Softmax attention inside packed documents: the plan of a batch, and the
-// kernels row by row.
+// Softmax attention inside packed documents, on tcgen05 (sm_103a).
 //
 // Score of query i and key j of one document, h the head:
 //   s = q_i . k_j / sqrt(d);  s = cap tanh(s / cap) with a cap;  s -= slope_h |i - j|.
 // Key j is visible to query i when both are in the same document and j <= i or
 // j is among the document's first `prefix` rows.
-#include "checks.h"
+//
+// A plan of intervals (attention_document.h) tells every tile of 128 rows which
+// 128-row blocks it shares a visible pair with, and every row which columns:
+// the work is that of the visible blocks, however the batch is packed.  The
+// kernels are those of the causal core (attention.cu) with that in place of the
+// diagonal, and differ where short documents ask for it: the forward is
+// persistent, and the backward's two kernels are one launch.
+//
+//   document_fwd_kernel  two tiles a CTA (two heads of a group, or two
+//                        consecutive query blocks of a head when the group is
+//                        odd): S = Q K^T -> online softmax -> O += P V.
+//   document_bwd_kernel  CTAs of two kinds: (kv head, key block) forms dK and dV
+//                        over the group's heads and the query blocks that see
+//                        the keys; the others take (head, query block) tiles
+//                        from a counter and form dQ.
+//
+// Values that are not finite.  The tensor cores multiply every row of a tile
+// with every other, and 0 times NaN is NaN: a hidden key's value, or a query of
+// another document, would reach rows that do not see it.  Scores are selected,
+// not multiplied, where they are hidden; and a result row that is not finite is
+// formed again from its visible pairs alone, by the row-by-row code below.  In
+// a finite batch that code never runs.
+#include "attention_common.cuh"
 #include "attention_document.h"
+#include "checks.h"
 
 namespace zbk {
 
@@ -75,21 +97,33 @@ __global__ void __launch_bounds__(kDocBlock) document_plan_kernel(const int32_t*
     }
 }
 
-// ------------------------------------------------------------------------ row by row
+// ------------------------------------------------------------------------ arguments
 
 struct DocArgs {
     const uint16_t* qkv;
-    const uint16_t* a;
     const uint16_t* da;
-    uint16_t* out;
-    const float* lse;
-    float* lse_out;
-    const float* dvec;
+    uint16_t* out;         // forward: a [T, n_heads d]; backward: dqkv
+    const float* lse;      // [n_heads][ld_stat], backward
+    float* lse_out;        // the same, forward
+    const float* dvec;     // [n_heads][ld_stat]: rowsum(da * a)
+    int* counter;          // backward: the next dQ tile
     DocPlan plan;
-    const float* slopes;
+    const float* slopes;   // [n_heads] or null
     float cap, scale;
-    int tokens, n_heads, n_kv_heads, ld_stat;
+    float scale_log2;      // log2(e) / sqrt(d)
+    float cap_log2;        // cap log2(e)
+    float cap_rate;        // 1 / (cap sqrt(d))
+    float cap_exp;         // 2 log2(e) / (cap sqrt(d)): the exponent of e^(2 s / cap) per unit of q . k
+    int tokens, n_heads, n_kv_heads, ld_stat, n_blocks;
+    int* status;
 };
+
+// How scores are modified: not at all, by the distance, or by the cap (and the
+// distance).  Every kernel exists once for each, so that a plain batch pays for
+// neither.
+enum DocMode : int { kDocPlain = 0, kDocBias = 1, kDocCap = 2 };
+
+// ------------------------------------------------------------------------ row by row
 
 template <int D>
 __device__ __forceinline__ void load_row(const uint16_t* p, int lane, float (&v)[D / 32]) {
@@ -101,10 +135,10 @@ __device__ __forceinline__ void load_row(const uint16_t* p, int lane, float (&v)
     }
 }
 template <int D>
-__device__ __forceinline__ void store_row(uint16_t* p, int lane, const float (&v)[D / 32], float f) {
+__device__ __forceinline__ void store_row(uint16_t* p, int lane, const float (&v)[D / 32], float f, int c0, int c1) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-        *reinterpret_cast<uint32_t*>(p + 64 * c + 2 * lane) = pack_bf16x2(v[2 * c] * f, v[2 * c + 1] * f);
+        if (64 * c + 2 * lane >= c0 && 64 * c + 2 * lane < c1) *reinterpret_cast<uint32_t*>(p + 64 * c + 2 * lane) = pack_bf16x2(v[2 * c] * f, v[2 * c + 1] * f);
 }
 template <int N>
 __device__ __forceinline__ float dot_rows(const float (&a)[N], const float (&b)[N]) {
@@ -128,13 +162,9 @@ __device__ __forceinline__ float score2(const DocArgs& p, float dot, float slope
     return (s - slope * static_cast<float>(dist)) * kLog2e;
 }
 
-// One warp per query row and head.
+// One query row and head by a whole warp: a and lse.
 template <int D>
-__global__ void __launch_bounds__(128) document_forward_rows(const DocArgs p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int i = static_cast<int>(w / p.n_heads), h = static_cast<int>(w % p.n_heads);
-    if (i >= p.tokens) return;
+__device__ __noinline__ void document_forward_row(const DocArgs& p, int i, int h, int lane) {
     const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
     const int g = h / (p.n_heads / p.n_kv_heads);
     const uint16_t* k = p.qkv + (p.n_heads + g) * D;
@@ -155,30 +185,13 @@ __global__ void __launch_bounds__(128) document_forward_rows(const DocArgs p) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) acc[c] = acc[c] * f + e * x[c];
     }
-    store_row<D>(p.out + (static_cast<int64_t>(i) * p.n_heads + h) * D, lane, acc, see.y > see.x ? 1.f / l : 0.f);
-    if (lane == 0) p.lse_out[static_cast<int64_t>(h) * p.ld_stat + i] = see.y > see.x ? m + log2f(l) : -INFINITY;
+    store_row<D>(p.out + (static_cast<int64_t>(i) * p.n_heads + h) * D, lane, acc, 1.f / l, 0, D);
+    if (lane == 0) p.lse_out[static_cast<int64_t>(h) * p.ld_stat + i] = m + log2f(l);
 }
 
-// D = rowsum(da * a) of one row and head per warp.
+// Columns [c0, c1) of dq of one query row and head.
 template <int D>
-__global__ void __launch_bounds__(128) document_rowsum(const DocArgs p, float* dvec) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (w >= static_cast<int64_t>(p.tokens) * p.n_heads) return;
-    float x[D / 32], y[D / 32];
-    load_row<D>(p.da + w * D, lane, x);
-    load_row<D>(p.a + w * D, lane, y);
-    const float s = dot_rows(x, y);
-    if (lane == 0) dvec[(w % p.n_heads) * p.ld_stat + w / p.n_heads] = s;
-}
-
-// dq: one warp per query row and head.
-template <int D>
-__global__ void __launch_bounds__(128) document_dq_rows(const DocArgs p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int i = static_cast<int>(w / p.n_heads), h = static_cast<int>(w % p.n_heads);
-    if (i >= p.tokens) return;
+__device__ __noinline__ void document_dq_row(const DocArgs& p, int i, int h, int lane, int c0, int c1) {
     const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
     const int g = h / (p.n_heads / p.n_kv_heads);
     const uint16_t* k = p.qkv + (p.n_heads + g) * D;
@@ -198,20 +211,16 @@ __global__ void __launch_bounds__(128) document_dq_rows(const DocArgs p) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) acc[c] += ds * x[c];
     }
-    store_row<D>(p.out + i * width + h * D, lane, acc, p.scale);
+    store_row<D>(p.out + i * width + h * D, lane, acc, p.scale, c0, c1);
 }
 
-// dk and dv: one warp per key row and kv head.
+// dk (or dv, with `value`) of one key row and kv head.
 template <int D>
-__global__ void __launch_bounds__(128) document_dkv_rows(const DocArgs p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int j = static_cast<int>(w / p.n_kv_heads), g = static_cast<int>(w % p.n_kv_heads);
-    if (j >= p.tokens) return;
+__device__ __noinline__ void document_dkv_row(const DocArgs& p, int j, int g, int lane, bool value) {
     const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
     const int group = p.n_heads / p.n_kv_heads;
     const int64_t kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
-    float k[D / 32], v[D / 32], dk[D / 32] = {}, dv[D / 32] = {};
+    float k[D / 32], v[D / 32], acc[D / 32] = {};
     load_row<D>(p.qkv + j * width + kcol, lane, k);
     load_row<D>(p.qkv + j * width + vcol, lane, v);
     const int2 see = p.plan.cols[j];
@@ -223,19 +232,1297 @@ __global__ void __launch_bounds__(128) document_dkv_rows(const DocArgs p) {
             load_row<D>(p.da + (static_cast<int64_t>(i) * p.n_heads + h) * D, lane, y);
             const float lse = p.lse[static_cast<int64_t>(h) * p.ld_stat + i], dsum = p.dvec[static_cast<int64_t>(h) * p.ld_stat + i];
             const float e = exp2f(score2(p, dot_rows(k, x), slope, abs(i - j), f) - lse);
-            const float ds = e * (dot_rows(v, y) - dsum) * f;
+            const float w = value ? e : e * (dot_rows(v, y) - dsum) * f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                dv[c] += e * y[c];
-                dk[c] += ds * x[c];
+            for (int c = 0; c < D / 32; ++c) acc[c] += w * (value ? y[c] : x[c]);
+        }
+    }
+    store_row<D>(p.out + j * width + (value ? vcol : kcol), lane, acc, value ? 1.f : p.scale, 0, D);
+}
+
+// ------------------------------------------------------------------------ scores on the tensor-core path
+
+// s <- tanh(s / (cap sqrt(d))) for N columns of a row.  Where all of a warp's
+// arguments lie in [-1, 1] (scores below the cap, the usual case), an odd
+// polynomial of degree 13 on the FMA pipe, relative error below 2^-22 (its
+// coefficients: a weighted least-squares fit of tanh(x) / x in x^2, reweighted to
+// equal ripple).  Else 1 - 2 / (1 + e^(2x)): two more special-function operations
+// an element beside the softmax's one, and off by 2^-22 of the cap, which there is
+// below the largest score.
+template <int N>
+__device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], fabsf(s[c]));
+    if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.cap_rate <= 1.f)) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const float x = s[c] * p.cap_rate, u = x * x;
+            float r = fmaf(0.00104102242f, u, -0.00620337895f);
+            r = fmaf(r, u, 0.0202899809f);
+            r = fmaf(r, u, -0.0534570303f);
+            r = fmaf(r, u, 0.133252041f);
+            r = fmaf(r, u, -0.333328392f);
+            r = fmaf(r, u, 0.99999995f);
+            s[c] = x * r;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] = 1.f - __fdividef(2.f, 1.f + ex2(s[c] * p.cap_exp));
+    }
+}
+
+// -inf outside the columns [lo, hi) of a row, by selects.  A warp whose rows all
+// see every column skips it, and one side's test when only the other cuts.
+template <int N>
+__device__ __forceinline__ void hide_scores(float (&s)[N], int lo, int hi) {
+    if (!__all_sync(0xffffffffu, hi >= N)) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const uint32_t mk = 0u - static_cast<uint32_t>(c < hi);
+            s[c] = __uint_as_float((__float_as_uint(s[c]) & mk) | (0xff800000u & ~mk));
+        }
+    }
+    if (!__all_sync(0xffffffffu, lo <= 0)) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const uint32_t mk = 0u - static_cast<uint32_t>(c >= lo);
+            s[c] = __uint_as_float((__float_as_uint(s[c]) & mk) | (0xff800000u & ~mk));
+        }
+    }
+}
+
+// Zeros outside [lo, hi): the gradients' form, for N columns from `first` on.
+template <int N>
+__device__ __forceinline__ void hide_grads(float* s, int first, int lo, int hi) {
+    if (!__all_sync(0xffffffffu, lo <= first && hi >= first + N)) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] = keep_if(s[c], (first + c >= lo) & (first + c < hi));
+    }
+}
+
+// The blocks that a tile of the plan walks, whatever the plan's memory holds.
+__device__ __forceinline__ int2 block_range(const int2* blocks, int b, int n_blocks) {
+    if (b >= n_blocks) return make_int2(0, 0);
+    const int2 r = blocks[b];
+    const int first = min(max(r.x, 0), n_blocks);
+    return make_int2(first, min(max(r.y, first), n_blocks));
+}
+
+__device__ __forceinline__ bool finite32(const float (&v)[32]) {
+    float m = 0.f;  // 0 v is NaN for a v that is not finite
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m = fmaf(v[e], 0.f, m);
+    return m == 0.f;
+}
+
+__device__ __forceinline__ void store32(uint16_t* dst, const float (&v)[32], float f) {
+    uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        d4[k] = make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                           pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f), pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+}
+__device__ __forceinline__ void store32_zero(uint16_t* dst) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(dst)[k] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+__device__ __forceinline__ void load_tmem32(uint32_t t, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_load_32(t, r);
+    tmem_wait_load();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+}
+
+// ------------------------------------------------------------------------ forward
+
+// Cancels the launch of the next CTA of the grid that has not started and
+// writes its place to `slot` (16 bytes), completing on `bar`: the CTA takes that
+// one's work.  Tiles go to whichever CTA is free, with no counter in memory that
+// two calls or two graphs could share.
+__device__ __forceinline__ void next_cta_request(uint32_t slot, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(slot),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer: the CTA's number, or -1 when none is left (after which no request
+// may follow).
+__device__ __forceinline__ int next_cta_answer(uint32_t slot) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(slot)
+        : "memory");
+    return got ? static_cast<int>(x) : -1;
+}
+
+// The two tiles of forward tile t: the same kv group and one K / V stream.
+struct FwdTile {
+    int h[2], q0[2];
+    int g, first, nk;
+};
+
+__host__ __device__ inline int fwd_tiles(const DocArgs& p) {
+    return (p.n_heads / p.n_kv_heads) % 2 == 0 ? p.n_blocks * (p.n_heads / 2) : (p.n_blocks + 1) / 2 * p.n_heads;
+}
+
+__device__ __forceinline__ FwdTile fwd_tile(const DocArgs& p, int t) {
+    FwdTile f;
+    const int group = p.n_heads / p.n_kv_heads;
+    if (group % 2 == 0) {
+        const int pairs = p.n_heads / 2;
+        const int qb = p.n_blocks - 1 - t / pairs;  // in one long document, the longest rows first
+        f.h[0] = 2 * (t % pairs);
+        f.h[1] = f.h[0] + 1;
+        f.q0[0] = f.q0[1] = qb * kRows;
+        const int2 r = block_range(p.plan.q_blocks, qb, p.n_blocks);
+        f.first = r.x;
+        f.nk = r.y - r.x;
+    } else {
+        const int b = (p.n_blocks + 1) / 2 - 1 - t / p.n_heads;
+        f.h[0] = f.h[1] = t % p.n_heads;
+        f.q0[0] = 2 * b * kRows;
+        f.q0[1] = f.q0[0] + kRows;
+        const int2 x = block_range(p.plan.q_blocks, 2 * b, p.n_blocks), y = block_range(p.plan.q_blocks, 2 * b + 1, p.n_blocks);
+        const bool ex = x.x == x.y, ey = y.x == y.y;
+        f.first = ex ? y.x : ey ? x.x : min(x.x, y.x);
+        f.nk = (ex ? y.y : ey ? x.y : max(x.y, y.y)) - f.first;
+    }
+    f.g = f.h[0] / group;
+    return f;
+}
+
+template <int D>
+struct DocFwdSmem {
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr uint32_t kTile = D * 256;
+    static constexpr uint32_t kQ = 0;           // Q of tile A, then Q of tile B
+    static constexpr uint32_t kKV = 2 * kTile;  // stage s: K at kKV + 2 s kTile, V after it
+    static constexpr uint32_t kAnswer = kKV + 2 * kStages * kTile;  // 16 bytes
+    static constexpr uint32_t kBars = kAnswer + 16;
+    // Q full / empty, the K / V ring, S, P and done of both tiles, tile slots full / empty, answer, drain
+    static constexpr int kNumBars = 2 + 2 * kStages + 6 + 4 + 2;
+    static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
+    static constexpr uint32_t kTileSlot = kTmemSlot + 8;
+    static constexpr size_t kUsed = kTileSlot + 8;
+    static constexpr size_t kBytes = kUsed > kMinSmem ? kUsed : kMinSmem;
+};
+
+// The two-head forward of the causal core over the steps of many tiles: the
+// K / V ring, the score buffers and the barriers' phases run on from one tile to
+// the next, and the next tile's Q loads as soon as the last scores of the
+// current one are formed, while its softmax, last product and stores run.  A
+// tile that sees nothing (padding) has no steps.
+template <int D, int M>
+__global__ void __launch_bounds__(kAttnBwdThreads, 1)
+    document_fwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ DocArgs p) {
+    using L = DocFwdSmem<D>;
+    constexpr int NS = L::kStages;
+    constexpr uint32_t kTile = L::kTile;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = smem_addr(smem_raw);
+    if (base & 1023u) {  // the tiles' 128-byte swizzle needs a 1 KiB-aligned start
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, kSiteAttn);
+        return;
+    }
+    const uint32_t s_q = base + L::kQ, s_kv = base + L::kKV, s_answer = base + L::kAnswer;
+    const uint32_t bars = base + L::kBars;
+    const uint32_t q_full = bars, q_empty = bars + 8u;
+    auto kv_full = [&](uint32_t s) { return bars + 8u * (2 + s); };
+    auto kv_empty = [&](uint32_t s) { return bars + 8u * (2 + NS + s); };
+    constexpr int kB = 2 + 2 * NS;
+    auto s_full = [&](int x) { return bars + 8u * (kB + x); };
+    auto p_full = [&](int x) { return bars + 8u * (kB + 2 + x); };
+    auto done = [&](int x) { return bars + 8u * (kB + 4 + x); };
+    auto tile_full = [&](uint32_t s) { return bars + 8u * (kB + 6 + s); };
+    auto tile_empty = [&](uint32_t s) { return bars + 8u * (kB + 8 + s); };
+    const uint32_t answer_full = bars + 8u * (kB + 10), drain = bars + 8u * (kB + 11);
+    const uint32_t tmem_slot = base + L::kTmemSlot;
+    volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + L::kTmemSlot);
+    volatile int* tile_slot = reinterpret_cast<volatile int*>(smem_raw + L::kTileSlot);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(kv_full(s), 1);
+            mbar_init(kv_empty(s), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full(x), 1);
+            mbar_init(p_full(x), 4);
+            mbar_init(done(x), 1);
+            mbar_init(tile_full(x), 1);
+            mbar_init(tile_empty(x), 9);  // the MMA warp and the eight row warps
+        }
+        mbar_init(answer_full, 1);
+        mbar_init(drain, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&map_qkv);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    // columns: S_A 0-127, S_B 128-255 (P packed into the first 64 columns of its
+    // buffer once read), O_A 256.., O_B 384..
+    auto t_s = [&](int x) { return tmem_base + 128u * static_cast<uint32_t>(x); };
+    auto t_o = [&](int x) { return tmem_base + 256u + 128u * static_cast<uint32_t>(x); };
+    // A consumer warp's view of tile slot n & 1 (-1: none left), after which the
+    // warp releases the slot.
+    auto take_tile = [&](uint32_t n, int& t) {
+        if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
+        t = tile_slot[n & 1u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tile_empty(n & 1u));
+        return true;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t nq = 0, nkv = 0;  // Q loads and K / V steps issued
+            int t = static_cast<int>(blockIdx.x);
+            for (uint32_t n = 0;; ++n) {
+                if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                tile_slot[n & 1u] = t;
+                mbar_arrive(tile_full(n & 1u));
+                if (t < 0) break;
+                const FwdTile f = fwd_tile(p, t);
+                if (f.nk > 0) {
+                    // Q once the previous tile's scores are formed
+                    if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(q_full, 2 * kTile);
+                    load_tile<D>(s_q, &map_qkv, q_full, f.h[0] * D, f.q0[0]);
+                    load_tile<D>(s_q + kTile, &map_qkv, q_full, f.h[1] * D, f.q0[1]);
+                    ++nq;
+                }
+                const int kcol = (p.n_heads + f.g) * D, vcol = (p.n_heads + p.n_kv_heads + f.g) * D;
+                bool ok = true;
+                for (int j = 0; j < f.nk; ++j) {
+                    const uint32_t st = nkv % NS;
+                    if (!mbar_wait_fast(kv_empty(st), ((nkv / NS) & 1u) ^ 1u, p.status, kSiteAttn)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(kv_full(st), 2 * kTile);
+                    const int k0 = (f.first + j) * kRows;
+                    load_tile<D>(s_kv + 2 * st * kTile, &map_qkv, kv_full(st), kcol, k0);
+                    load_tile<D>(s_kv + (2 * st + 1) * kTile, &map_qkv, kv_full(st), vcol, k0);
+                    ++nkv;
+                }
+                if (!ok) break;
+                // the next tile's number after this tile's last load, a ring's depth before its end
+                mbar_arrive_expect_tx(answer_full, 16);
+                next_cta_request(s_answer, answer_full);
+                if (!mbar_wait_fast(answer_full, n & 1u, p.status, kSiteAttn)) break;
+                t = next_cta_answer(s_answer);
+                fence_proxy_async_smem();  // the answer is read before another one is written over it
+                if (t >= 0) {
+                    const FwdTile nx = fwd_tile(p, t);
+                    prefetch_tile<D>(&map_qkv, nx.h[0] * D, nx.q0[0]);
+                    if (nx.q0[1] < p.tokens) prefetch_tile<D>(&map_qkv, nx.h[1] * D, nx.q0[1]);
+                }
+            }
+            // no copy may land after the CTA has gone
+            if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t u = ring_uses(nkv, NS, s);
+                if (u > 0) mbar_wait_fast(kv_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+            }
+        }
+    } else if (warp == 1) {
+        // the whole warp runs the issue loop; its elected lane carries each instruction
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idesc_o = mma_idesc_bf16(128, D, false, true);
+        auto issue_s = [&](int x, uint32_t g) {
+            const uint64_t a_desc = kdesc_base(s_q + static_cast<uint32_t>(x) * kTile),
+                           b_desc = kdesc_base(s_kv + 2 * (g % NS) * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_s(x), kdesc_at(a_desc, kk), kdesc_at(b_desc, kk), idesc_s, kk > 0);
+            umma_commit_elected(leader, s_full(x));
+        };
+        auto issue_pv = [&](int x, uint32_t g, bool first) {
+            if (!warp_wait(p_full(x), g & 1u, p.status)) return false;
+            tc_fence_after();
+            const uint64_t v_desc = mndesc_base(s_kv + (2 * (g % NS) + 1) * kTile);
+#pragma unroll
+            for (int kk = 0; kk < kRows / 16; ++kk)
+                umma_bf16_ts_elected(leader, t_o(x), t_s(x) + 8 * kk, mndesc_at(v_desc, kk), idesc_o,
+                                     (!first || kk > 0) ? 1u : 0u);
+            return true;
+        };
+        auto kv_ready = [&](uint32_t g) {
+            if (!warp_wait(kv_full(g % NS), (g / NS) & 1u, p.status)) return false;
+            tc_fence_after();
+            return true;
+        };
+        uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const int nk = fwd_tile(p, t).nk;
+            if (nk == 0) continue;
+            if (!warp_wait(q_full, nq & 1u, p.status) || !kv_ready(g)) break;
+            ++nq;
+            issue_s(0, g);
+            issue_s(1, g);
+            if (nk == 1) umma_commit_elected(leader, q_empty);
+            for (int j = 0; j < nk; ++j, ++g) {
+                const bool more = j + 1 < nk;
+                if (!issue_pv(0, g, j == 0) || (more && !kv_ready(g + 1))) {
+                    ok = false;
+                    break;
+                }
+                if (more)
+                    issue_s(0, g + 1);
+                else
+                    umma_commit_elected(leader, done(0));
+                if (!issue_pv(1, g, j == 0)) {
+                    ok = false;
+                    break;
+                }
+                umma_commit_elected(leader, kv_empty(g % NS));
+                if (more)
+                    issue_s(1, g + 1);
+                else
+                    umma_commit_elected(leader, done(1));
+                // Q is free for the next tile once its last scores are formed
+                if (j + 2 == nk) umma_commit_elected(leader, q_empty);
+            }
+        }
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    } else {
+        // ---------------- softmax rows: warps 2-5 tile A, warps 6-9 tile B
+        const int x = (warp - 2) >> 2;
+        const int qw = warp & 3;
+        const int row = qw * 32 + lane;
+        const uint32_t t_row = static_cast<uint32_t>(qw * 32) << 16;
+        const uint32_t ts = t_s(x), to = t_o(x);
+        uint32_t g = 0, nd = 0;  // steps and tiles with steps so far
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const FwdTile f = fwd_tile(p, t);
+            const int h = x ? f.h[1] : f.h[0];
+            const int q = (x ? f.q0[1] : f.q0[0]) + row;
+            const bool valid = q < p.tokens;
+            const int2 see = valid ? p.plan.rows[q] : make_int2(0, 0);
+            const bool empty = see.y <= see.x;
+            const float slope2 = M != kDocPlain && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+            // -1e30, not -infinity: a row that has seen no key yet keeps finite differences
+            float m = -1e30f, l = 0.f;
+            for (int j = 0; j < f.nk; ++j, ++g) {
+                if (!warp_wait(s_full(x), g & 1u, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float s[128];
+                {
+                    uint32_t r[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tmem_load_32(ts + t_row + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * c));
+                    tmem_wait_load();
+#pragma unroll
+                    for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(r[e]);
+                }
+                const int k0 = (f.first + j) * kRows;
+                // unmodified (and capped, undistanced) scores are scaled below and in the exponent's FMA
+                float sc = 1.f;
+                if constexpr (M == kDocPlain) sc = p.scale_log2;
+                if constexpr (M == kDocCap) {
+                    cap_tanh<128>(p, s);
+                    sc = p.cap_log2;
+                }
+                if (M == kDocBias || (M == kDocCap && p.slopes)) {
+                    const float mul = M == kDocBias ? p.scale_log2 : p.cap_log2, at = static_cast<float>(q - k0);
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], mul, -slope2 * fabsf(static_cast<float>(c) - at));
+                    sc = 1.f;
+                }
+                hide_scores(s, see.x - k0, see.y - k0);
+                // eight running maxima and sums, not one chain of 128 dependent operations
+                float mx8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 128; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], s[c]);
+                float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+                mx *= sc;
+                if (j == 0) {
+                    m = fmaxf(m, mx);
+                } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                    // A row's maximum rose far above its reference: the warp rescales
+                    // O and l of all its rows to their new maxima (warp-wide
+                    // tensor-memory loads and stores; rescaling to any larger
+                    // reference is exact).  PV_X[j-1] completed before S_X[j].
+                    const float m_new = fmaxf(m, mx);
+                    const float alpha = ex2(m - m_new);
+                    l *= alpha;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_load_32(to + t_row + 32 * c, r);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                        tmem_store_32(to + t_row + 32 * c, r);
+                    }
+                    m = m_new;
+                }
+                float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = ex2(fmaf(s[32 * c + 2 * e], sc, -m));
+                        const float b = ex2(fmaf(s[32 * c + 2 * e + 1], sc, -m));
+                        sum8[e & 7] += a + b;
+                        w[e] = pack_bf16x2(a, b);  // P to bf16: the tensor cores' operand; l sums it unrounded
+                    }
+                    tmem_store_16(ts + t_row + 16 * c, w);
+                }
+                l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(p_full(x), lane);
+            }
+            if (!ok) break;
+            uint16_t* dst = p.out + (static_cast<int64_t>(q) * p.n_heads + h) * D;
+            bool again = false;  // not finite: formed again below
+            if (f.nk > 0) {
+                if (!warp_wait(done(x), nd & 1u, p.status)) break;
+                ++nd;
+                tc_fence_after();
+                const float inv = 1.f / l;
+                again = !(fabsf(inv) <= 3e38f);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    load_tmem32(to + t_row + 32 * c, o);
+                    again |= !finite32(o);
+                    if (valid && !empty) store32(dst + 32 * c, o, inv);
+                }
+                tc_fence_before();
+            }
+            if (valid) {
+                if (empty)
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) store32_zero(dst + 32 * c);
+                p.lse_out[static_cast<int64_t>(h) * p.ld_stat + q] = empty ? -INFINITY : m + lg2(l);
+            }
+            uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
+            while (redo) {
+                const int src = __ffs(redo) - 1;
+                redo &= redo - 1;
+                __syncwarp();  // the row's first results are written before they are written over
+                document_forward_row<D>(p, q - lane + src, h, lane);
             }
         }
     }
-    store_row<D>(p.out + j * width + kcol, lane, dk, p.scale);
-    store_row<D>(p.out + j * width + vcol, lane, dv, 1.f);
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
 }
 
-unsigned warps4(int64_t n) { return static_cast<unsigned>((n + 3) / 4); }
+// ------------------------------------------------------------------------ backward: dq
+
+// The causal core's dQ tiles and pipeline (attention.cu): S and dP by warp 1, dQ
+// by warp 10, two groups of row warps with 64 key columns each.
+template <int D>
+struct DocDqSmem {
+    static constexpr int kKStages = 3, kVStages = 2;
+    static constexpr uint32_t kTile = D * 256;
+    static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile;
+    static constexpr uint32_t kV = kK + kKStages * kTile;
+    static constexpr uint32_t kBars = kV + kVStages * kTile;
+    // q full / empty, the K ring (full, empty), the V ring (empty), S (2), dP,
+    // dS (2), done, drain, the two tile slots (full, empty), dQ issued (2), dP issued (2)
+    static constexpr int kNumBars = 2 + 2 * kKStages + kVStages + 2 + 5 + 4 + 4;
+    static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
+    static constexpr uint32_t kTileSlot = kTmemSlot + 8;  // the tile number held by each slot (two ints)
+    static constexpr size_t kUsed = kTileSlot + 8;
+};
+
+struct DqTile {
+    int h, q0, kb0, nk;
+};
+__device__ __forceinline__ DqTile dq_tile(const DocArgs& p, int t) {
+    DqTile d;
+    const int qb = p.n_blocks - 1 - t / p.n_heads;
+    d.h = t % p.n_heads;
+    d.q0 = qb * kRows;
+    const int2 r = block_range(p.plan.q_blocks, qb, p.n_blocks);
+    d.kb0 = r.x;
+    d.nk = r.y - r.x;
+    return d;
+}
+
+template <int D, int M>
+__device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CUtensorMap& map_do, const DocArgs& p,
+                                            uint8_t* smem_raw) {
+    using L = DocDqSmem<D>;
+    constexpr int NK = L::kKStages, NV = L::kVStages;
+    constexpr uint32_t kTile = L::kTile;
+    const uint32_t base = smem_addr(smem_raw);
+    const uint32_t s_q = base + L::kQ, s_do = base + L::kDO, s_k = base + L::kK, s_v = base + L::kV;
+    const uint32_t bars = base + L::kBars;
+    const uint32_t q_full = bars, q_empty = bars + 8u;
+    auto k_full = [&](uint32_t s) { return bars + 8u * (2 + s); };
+    auto k_empty = [&](uint32_t s) { return bars + 8u * (2 + NK + s); };
+    auto v_empty = [&](uint32_t s) { return bars + 8u * (2 + 2 * NK + s); };
+    constexpr int kB = 2 + 2 * NK + NV;
+    auto s_full = [&](uint32_t b) { return bars + 8u * (kB + b); };
+    const uint32_t dp_full = bars + 8u * (kB + 2), done = bars + 8u * (kB + 3), drain = bars + 8u * (kB + 4);
+    auto ds_full = [&](uint32_t g) { return bars + 8u * (kB + 5 + (g & 1u)); };
+    auto tile_full = [&](uint32_t s) { return bars + 8u * (kB + 7 + s); };
+    auto tile_empty = [&](uint32_t s) { return bars + 8u * (kB + 9 + s); };
+    auto dq_issued = [&](uint32_t g) { return bars + 8u * (kB + 11 + (g & 1u)); };
+    auto dp_issued = [&](uint32_t g) { return bars + 8u * (kB + 13 + (g & 1u)); };
+    const uint32_t tmem_slot = base + L::kTmemSlot;
+    volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + L::kTmemSlot);
+    volatile int* tile_slot = reinterpret_cast<volatile int*>(smem_raw + L::kTileSlot);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_tiles = p.n_blocks * p.n_heads;
+    const int group = p.n_heads / p.n_kv_heads;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+        }
+        for (int s = 0; s < NV; ++s) mbar_init(v_empty(s), 1);
+        mbar_init(s_full(0), 1);
+        mbar_init(s_full(1), 1);
+        mbar_init(dp_full, 1);
+        mbar_init(done, 1);
+        mbar_init(drain, 2);  // both MMA warps
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(ds_full(s), 8);
+            mbar_init(tile_full(s), 1);
+            mbar_init(tile_empty(s), 10);  // the two MMA warps and the eight row warps
+            mbar_init(dq_issued(s), 1);
+            mbar_init(dp_issued(s), 1);
+        }
+        mbar_fence_init();
+        tma_prefetch_map(&map_qkv);
+        tma_prefetch_map(&map_do);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    // columns: S buffers 0-127 and 128-255 (dS packed into columns 0-31 and
+    // 64-95 of a buffer once read), dP 256-383, dQ 384..
+    const uint32_t t_dp = tmem_base + 256, t_dq = tmem_base + 384;
+    auto t_s = [&](uint32_t g) { return tmem_base + 128u * (g & 1u); };
+    auto take_tile = [&](uint32_t n, int& t) {
+        if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
+        t = tile_slot[n & 1u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tile_empty(n & 1u));
+        return true;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto fetch = [&](uint32_t n) {
+                if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) return -2;
+                int t = atomicAdd(p.counter, 1);
+                if (t >= n_tiles) t = -1;
+                tile_slot[n & 1u] = t;
+                mbar_arrive(tile_full(n & 1u));
+                return t;
+            };
+            uint32_t nq = 0, nkf = 0;  // Q / dO loads and K / V steps issued
+            int t = fetch(0);
+            for (uint32_t n = 0; t >= 0; ++n) {
+                const DqTile tl = dq_tile(p, t);
+                if (tl.nk > 0) {
+                    // Q and dO once the previous tile's S and dP products are done
+                    if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(q_full, 2 * kTile);
+                    load_tile<D>(s_q, &map_qkv, q_full, tl.h * D, tl.q0);
+                    load_tile<D>(s_do, &map_do, q_full, tl.h * D, tl.q0);
+                    ++nq;
+                }
+                const int g = tl.h / group;
+                const int kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
+                int t_next = tl.nk > 0 ? -2 : fetch(n + 1);
+                for (int j = 0; j < tl.nk; ++j) {
+                    const uint32_t u = nkf;
+                    // K[j] and V[j] land on one barrier: one wait per step for the MMA warp
+                    if (!mbar_wait_fast(k_empty(u % NK), ((u / NK) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(k_full(u % NK), 2 * kTile);
+                    load_tile<D>(s_k + (u % NK) * kTile, &map_qkv, k_full(u % NK), kcol, (tl.kb0 + j) * kRows);
+                    load_tile<D>(s_v + (u % NV) * kTile, &map_qkv, k_full(u % NK), vcol, (tl.kb0 + j) * kRows);
+                    ++nkf;
+                    // the next tile's number at this tile's last load, and its Q and dO into L2
+                    if (j == tl.nk - 1) {
+                        t_next = fetch(n + 1);
+                        if (t_next >= 0) {
+                            const DqTile nx = dq_tile(p, t_next);
+                            prefetch_tile<D>(&map_qkv, nx.h * D, nx.q0);
+                            prefetch_tile<D>(&map_do, nx.h * D, nx.q0);
+                        }
+                    }
+                }
+                t = t_next;  // -2 after a failed wait ends the loop
+            }
+            // no copy may land after the CTA has gone
+            if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
+            for (int s = 0; s < NK; ++s) {
+                const uint32_t u = ring_uses(nkf, NK, s);
+                if (u > 0) mbar_wait_fast(k_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- S and dP products
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
+        const uint64_t q_desc = kdesc_base(s_q), do_desc = kdesc_base(s_do);
+        auto issue_s = [&](uint32_t g) {
+            const uint32_t st = g % NK;
+            if (!warp_wait(k_full(st), (g / NK) & 1u, p.status)) return false;
+            tc_fence_after();
+            const uint64_t k_desc = kdesc_base(s_k + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_s(g), kdesc_at(q_desc, kk), kdesc_at(k_desc, kk), idesc_s, kk > 0);
+            umma_commit_elected(leader, s_full(g & 1u));
+            return true;
+        };
+        auto issue_dp = [&](uint32_t g) {
+            const uint32_t st = g % NV;  // V[g] landed with K[g] (issue_s(g) waited for both)
+            const uint64_t v_desc = kdesc_base(s_v + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_dp, kdesc_at(do_desc, kk), kdesc_at(v_desc, kk), idesc_s, kk > 0);
+            umma_commit_elected(leader, dp_full);
+            umma_commit_elected(leader, v_empty(st));
+        };
+        // S[g] overwrites the S buffer of step g - 2 once the dQ warp has issued
+        // dQ[g - 2], which reads dS[g - 2] from it; dP[g] overwrites dP[g - 1]
+        // once the row warps are done with it.
+        auto may_issue_s = [&](uint32_t g) {
+            if (g < 2) return true;
+            if (!warp_wait(dq_issued(g - 2), ((g - 2) >> 1) & 1u, p.status)) return false;
+            tc_fence_after();
+            return true;
+        };
+        auto may_issue_dp = [&](uint32_t g) {
+            if (g < 1) return true;
+            if (!warp_wait(ds_full(g - 1), ((g - 1) >> 1) & 1u, p.status)) return false;
+            tc_fence_after();
+            return true;
+        };
+        uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const int nk = dq_tile(p, t).nk;
+            if (nk == 0) continue;
+            if (!warp_wait(q_full, nq & 1u, p.status)) break;
+            ++nq;
+            tc_fence_after();
+            // the MMA order per step is S[g+1], dP[g+1] (here) beside dQ[g] (the dQ warp)
+            for (int j = 0; j < nk; ++j, ++g) {
+                if (!may_issue_s(g) || !issue_s(g) || !may_issue_dp(g)) {
+                    ok = false;
+                    break;
+                }
+                issue_dp(g);
+                tc_fence_before();
+                if (leader) mbar_arrive(dp_issued(g));
+                // Q and dO are free for the next tile once its last S and dP are done
+                if (j + 1 == nk) umma_commit_elected(leader, q_empty);
+            }
+        }
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    } else if (warp == kDqWarp) {
+        // ---------------- dQ products
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_q = mma_idesc_bf16(128, D, false, true);
+        uint32_t g = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const int nk = dq_tile(p, t).nk;
+            if (nk == 0) continue;
+            for (int j = 0; j < nk; ++j, ++g) {
+                if (!warp_wait(ds_full(g), (g >> 1) & 1u, p.status) ||
+                    (j + 1 < nk && !warp_wait(dp_issued(g + 1), ((g + 1) >> 1) & 1u, p.status))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t k_mn = mndesc_base(s_k + (g % NK) * kTile);
+#pragma unroll
+                for (int kk = 0; kk < kRows / 16; ++kk)
+                    umma_bf16_ts_elected(leader, t_dq, t_s(g) + packed_col(kk), mndesc_at(k_mn, kk), idesc_q,
+                                         (j > 0 || kk > 0) ? 1u : 0u);
+                umma_commit_elected(leader, k_empty(g % NK));
+                tc_fence_before();
+                if (leader) mbar_arrive(dq_issued(g));
+            }
+            if (ok) umma_commit_elected(leader, done);
+        }
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    } else {
+        // ---------------- row warps: group gi takes key columns 64 gi .. 64 gi + 63 of every step
+        const int gi = (warp - 2) >> 2;
+        const int qw = warp & 3;
+        const int row = qw * 32 + lane;
+        const uint32_t t_row = (static_cast<uint32_t>(qw * 32) << 16) + 64u * gi;
+        uint32_t g = 0, nd = 0;  // steps and tiles with steps so far
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const DqTile tl = dq_tile(p, t);
+            const int q = tl.q0 + row;
+            const bool valid = q < p.tokens;
+            const int2 see = valid ? p.plan.rows[q] : make_int2(0, 0);
+            const bool empty = see.y <= see.x;
+            const float lse = empty ? 0.f : p.lse[static_cast<int64_t>(tl.h) * p.ld_stat + q];
+            const float dv = empty ? 0.f : p.dvec[static_cast<int64_t>(tl.h) * p.ld_stat + q];
+            const float slope2 = M != kDocPlain && p.slopes ? p.slopes[tl.h] * kLog2e : 0.f;
+            for (int j = 0; j < tl.nk; ++j, ++g) {
+                const int c0 = (tl.kb0 + j) * kRows + 64 * gi;
+                if (!warp_wait(s_full(g & 1u), (g >> 1) & 1u, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float pr[64];  // P, times the cap's derivative
+                {
+                    uint32_t rs[64];
+                    tmem_load_32(t_s(g) + t_row, *reinterpret_cast<uint32_t(*)[32]>(rs));
+                    tmem_load_32(t_s(g) + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rs + 32));
+                    tmem_wait_load();
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) pr[i] = __uint_as_float(rs[i]);
+                }
+                const float x = static_cast<float>(q - c0);
+                if constexpr (M == kDocPlain) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) pr[i] = ex2(fmaf(pr[i], p.scale_log2, -lse));
+                } else if constexpr (M == kDocBias) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        pr[i] = ex2(fmaf(pr[i], p.scale_log2, fmaf(-slope2, fabsf(static_cast<float>(i) - x), -lse)));
+                } else {
+                    cap_tanh<64>(p, pr);
+                    if (p.slopes) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            pr[i] = ex2(fmaf(pr[i], p.cap_log2, fmaf(-slope2, fabsf(static_cast<float>(i) - x), -lse))) *
+                                    fmaf(-pr[i], pr[i], 1.f);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) pr[i] = ex2(fmaf(pr[i], p.cap_log2, -lse)) * fmaf(-pr[i], pr[i], 1.f);
+                    }
+                }
+                if (!warp_wait(dp_full, g & 1u, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t rp[64];
+                tmem_load_32(t_dp + t_row, *reinterpret_cast<uint32_t(*)[32]>(rp));
+                tmem_load_32(t_dp + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rp + 32));
+                tmem_wait_load();
+#pragma unroll
+                for (int i = 0; i < 64; ++i) pr[i] *= __uint_as_float(rp[i]) - dv;
+                // hidden pairs last: their P or dP may be anything
+                hide_grads<64>(pr, 0, see.x - c0, see.y - c0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
+                    // packed columns 16 c .. 16 c + 15 of the group's S columns, all read above
+                    tmem_store_16(t_s(g) + t_row + 16 * c, w);
+                }
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(ds_full(g), lane);
+            }
+            if (!ok) break;
+            // group gi stores dQ columns [D/2 gi, D/2 (gi + 1)); the tile's next
+            // dQ product waits for this group's next dS arrival, after these loads
+            constexpr int kChunks = D / 64;  // 32-column chunks of this group's half
+            uint16_t* dst = p.out + static_cast<int64_t>(q) * ((p.n_heads + 2 * p.n_kv_heads) * D) + tl.h * D;
+            bool again = false;
+            if (tl.nk > 0) {
+                if (!warp_wait(done, nd & 1u, p.status)) break;
+                ++nd;
+                tc_fence_after();
+                const uint32_t t_q = t_dq + (static_cast<uint32_t>(qw * 32) << 16) + 32u * (gi * kChunks);
+                float r[kChunks][32];
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) load_tmem32(t_q + 32 * c, r[c]);
+                tc_fence_before();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    again |= !finite32(r[c]);
+                    if (valid && !empty) store32(dst + 32 * (gi * kChunks + c), r[c], p.scale);
+                }
+            }
+            if (valid && empty)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) store32_zero(dst + 32 * (gi * kChunks + c));
+            uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
+            while (redo) {
+                const int src = __ffs(redo) - 1;
+                redo &= redo - 1;
+                __syncwarp();
+                document_dq_row<D>(p, q - lane + src, tl.h, lane, gi * (D / 2), (gi + 1) * (D / 2));
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// ------------------------------------------------------------------------ backward: dk, dv
+
+// The causal core's dK / dV pipeline (attention.cu).  lse enters the score
+// product as an extra K step where scores are linear in q . k; a cap applies to
+// the product alone, so there the row warps read lse themselves (broadcast reads
+// that the L1 serves).
+template <int D>
+struct DocDkvSmem {
+    static constexpr int kQStages = 2, kDoStages = 2, kStatStages = 2, kAugStages = 2;
+    static constexpr uint32_t kTile = D * 256;
+    static constexpr uint32_t kAugTile = 128 * 16 * 2;  // 128 rows x one K step of 16 bf16, no swizzle
+    static constexpr uint32_t kK = 0, kV = kTile, kQ = 2 * kTile;
+    static constexpr uint32_t kDO = kQ + kQStages * kTile;
+    static constexpr uint32_t kOnes = kDO + kDoStages * kTile;  // two constant A operands: lse, D selectors
+    static constexpr uint32_t kAug = kOnes + 2 * kAugTile;      // stage s: the B operand of step s
+    static constexpr uint32_t kStat = kAug + kAugStages * kAugTile;  // stage s: lse (512 bytes) then D (512 bytes)
+    static constexpr uint32_t kBars = kStat + 1024 * kStatStages;
+    static constexpr int kNumBars = 1 + 2 * (kQStages + kStatStages) + kAugStages + 8;
+    static constexpr size_t kUsed = kBars + 8 * kNumBars + 16;
+};
+
+template <int D>
+constexpr size_t doc_bwd_smem() {
+    return std::max({DocDqSmem<D>::kUsed, DocDkvSmem<D>::kUsed, kMinSmem});
+}
+
+template <int D, int M>
+__device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const CUtensorMap& map_do, const DocArgs& p,
+                                             uint8_t* smem_raw) {
+    using L = DocDkvSmem<D>;
+    constexpr int NQ = L::kQStages, ND = L::kDoStages, NT = L::kStatStages, NA = L::kAugStages;
+    constexpr uint32_t kTile = L::kTile;
+    constexpr int kThreads = kAttnDqThreads, kStats = kDqWarp;  // warp 10: statistics
+    const uint32_t base = smem_addr(smem_raw);
+    const uint32_t s_k = base + L::kK, s_v = base + L::kV, s_q = base + L::kQ, s_do = base + L::kDO,
+                   s_ones = base + L::kOnes, s_aug = base + L::kAug, s_stat = base + L::kStat;
+    const uint32_t bars = base + L::kBars;
+    const uint32_t kv_full = bars;
+    auto q_full = [&](int s) { return bars + 8u * (1 + s); };
+    // q_empty(s) releases Q, dO (same ring position, ND == NQ) and nothing else
+    auto q_empty = [&](int s) { return bars + 8u * (1 + NQ + s); };
+    auto st_full = [&](int s) { return bars + 8u * (1 + 2 * NQ + s); };
+    auto st_empty = [&](int s) { return bars + 8u * (1 + 2 * NQ + NT + s); };
+    auto aug_empty = [&](int s) { return bars + 8u * (1 + 2 * NQ + 2 * NT + s); };
+    constexpr int kB = 1 + 2 * (NQ + NT) + NA;
+    static_assert(NQ == ND, "Q and dO share their ring position and release");
+    // p_full(c) / ds_full(c): chunk c (32 query columns of each group) of P^T / dS^T is packed
+    auto p_full = [&](int c) { return bars + 8u * (kB + 2 + c); };
+    auto ds_full = [&](int c) { return bars + 8u * (kB + 4 + c); };
+    const uint32_t s_full = bars + 8u * kB, dp_full = bars + 8u * (kB + 1), done = bars + 8u * (kB + 6),
+                   drain = bars + 8u * (kB + 7);
+    const uint32_t tmem_slot = bars + 8u * L::kNumBars;
+    volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - base));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = p.n_heads / p.n_kv_heads;
+    const int kb = static_cast<int>(blockIdx.x) / p.n_kv_heads;  // in one long document, the most work first
+    const int g = static_cast<int>(blockIdx.x) % p.n_kv_heads;
+    const int k0 = kb * kRows;
+    const int2 range = block_range(p.plan.k_blocks, kb, p.n_blocks);
+    const int n_steps = group * (range.y - range.x);  // (query block, head of the group) pairs
+    const int kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
+    const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
+    if (n_steps == 0) {  // keys that nothing sees
+        for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
+            const int r = e / (D / 4), c = e % (D / 4);  // 16-byte pieces: D / 8 of dk, then D / 8 of dv
+            if (k0 + r < p.tokens)
+                *reinterpret_cast<uint4*>(p.out + (k0 + r) * width + (c < D / 8 ? kcol + 8 * c : vcol + 8 * (c - D / 8))) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+
+    // The constant A operands of the statistics step (ones in bf16 columns 0-2
+    // for lse, 8-10 for D) and zeros in the B operands' unused columns; the
+    // statistics warp rewrites only columns 0-2 and 8-10 of a B operand.
+    {
+        uint4* z = reinterpret_cast<uint4*>(smem_raw + L::kOnes);
+        constexpr int n16 = (2 + NA) * L::kAugTile / 16;
+        for (int e = threadIdx.x; e < n16; e += kThreads) {
+            const int tile = e / (L::kAugTile / 16);
+            const int kc = (e >> 3) & 1;  // 16-byte rows: 8 rows per chunk, chunks alternate every 128 bytes
+            const bool ones = tile < 2 && kc == tile;
+            z[e] = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(kv_full, 1);
+        for (int s = 0; s < NQ; ++s) {
+            mbar_init(q_full(s), 2);  // the Q and dO tiles' TMA and the statistics warp's B operand
+            mbar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < NT; ++s) {
+            mbar_init(st_full(s), 1);
+            mbar_init(st_empty(s), 1);
+        }
+        for (int s = 0; s < NA; ++s) mbar_init(aug_empty(s), 1);
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        for (int c = 0; c < 2; ++c) {
+            mbar_init(p_full(c), 8);
+            mbar_init(ds_full(c), 8);
+        }
+        mbar_init(done, 1);
+        mbar_init(drain, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&map_qkv);
+        tma_prefetch_map(&map_do);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    // columns: S^T 0-127 (P^T packed into 0-31 and 64-95 once read), dP^T
+    // 128-255 (dS^T likewise), dV 256.., dK 256 + D..
+    const uint32_t t_s = tmem_base, t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 256 + D;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(kv_full, 2 * kTile);
+            load_tile<D>(s_k, &map_qkv, kv_full, kcol, k0);
+            load_tile<D>(s_v, &map_qkv, kv_full, vcol, k0);
+            uint32_t nq = 0, nt = 0;
+            for (int i = 0; i < n_steps; ++i) {
+                const int h = g * group + i % group;
+                const int r0 = (range.x + i / group) * kRows;
+                if (!mbar_wait_fast(st_empty(i % NT), ((i / NT) & 1) ^ 1u, p.status, kSiteAttn)) break;
+                const uint32_t stat = s_stat + 1024u * (i % NT);
+                mbar_arrive_expect_tx(st_full(i % NT), 1024);
+                bulk_load_1d(stat, p.lse + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
+                bulk_load_1d(stat + 512, p.dvec + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
+                ++nt;
+                // Q[i] and dO[i] land on one barrier (with the statistics operand); one
+                // release covers both stages (dK[i - 2], after dV[i - 2], read the last of them)
+                if (!mbar_wait_fast(q_empty(i % NQ), ((i / NQ) & 1) ^ 1u, p.status, kSiteAttn)) break;
+                mbar_arrive_expect_tx(q_full(i % NQ), 2 * kTile);
+                load_tile<D>(s_q + (i % NQ) * kTile, &map_qkv, q_full(i % NQ), h * D, r0);
+                load_tile<D>(s_do + (i % ND) * kTile, &map_do, q_full(i % NQ), h * D, r0);
+                ++nq;
+            }
+            mbar_wait_fast(kv_full, 0, p.status, kSiteDrain);
+            for (int s = 0; s < NQ; ++s) {
+                const uint32_t u = ring_uses(nq, NQ, s);
+                if (u > 0) mbar_wait_fast(q_full(s), (u - 1) & 1, p.status, kSiteDrain);
+            }
+            for (int s = 0; s < NT; ++s) {
+                const uint32_t u = ring_uses(nt, NT, s);
+                if (u > 0) mbar_wait_fast(st_full(s), (u - 1) & 1, p.status, kSiteDrain);
+            }
+        }
+    } else if (warp == 1) {
+        // the whole warp runs the issue loop; its elected lane carries each instruction
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idesc_g = mma_idesc_bf16(128, D, false, true);
+        const uint64_t k_desc = kdesc_base(s_k), v_desc = kdesc_base(s_v);
+        const uint64_t ones_lse = aug_desc(s_ones), ones_d = aug_desc(s_ones + L::kAugTile);
+        auto issue_s = [&](int i) {
+            const int st = i % NQ;
+            // Q tile i and statistics operand i % NA (NA = NQ) complete one phase together
+            if (!warp_wait(q_full(st), (i / NQ) & 1, p.status)) return false;
+            tc_fence_after();
+            const uint64_t q_desc = kdesc_base(s_q + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_s, kdesc_at(k_desc, kk), kdesc_at(q_desc, kk), idesc_s, kk > 0);
+            if constexpr (M != kDocCap)
+                umma_bf16_elected(leader, t_s, ones_lse, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
+            umma_commit_elected(leader, s_full);
+            return true;
+        };
+        auto issue_dp = [&](int i) {  // after issue_s(i), which waited for dO[i] and the statistics too
+            const int st = i % ND;
+            const uint64_t do_desc = kdesc_base(s_do + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_dp, kdesc_at(v_desc, kk), kdesc_at(do_desc, kk), idesc_s, kk > 0);
+            umma_bf16_elected(leader, t_dp, ones_d, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
+            umma_commit_elected(leader, dp_full);
+            umma_commit_elected(leader, aug_empty(i % NA));
+            return true;
+        };
+        bool ok = warp_wait(kv_full, 0, p.status) && issue_s(0) && issue_dp(0);
+        // K steps of dV / dK in the order their P^T / dS^T chunks are packed:
+        // chunk c of group g holds the K steps 4 g + 2 c and 4 g + 2 c + 1
+        constexpr int kOrder[8] = {0, 1, 4, 5, 2, 3, 6, 7};
+        for (int i = 0; ok && i < n_steps; ++i) {
+            const uint64_t do_mn = mndesc_base(s_do + (i % ND) * kTile);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (!warp_wait(p_full(c), i & 1, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = kOrder[4 * c + e];
+                    umma_bf16_ts_elected(leader, t_dv, t_s + packed_col(kk), mndesc_at(do_mn, kk), idesc_g,
+                                         (i > 0 || kk > 0) ? 1u : 0u);
+                }
+            }
+            if (!ok) break;
+            // S^T[i+1] overwrites the S^T buffer after dV[i] has read P^T[i] from it
+            if (i + 1 < n_steps && !issue_s(i + 1)) break;
+            const uint64_t q_mn = mndesc_base(s_q + (i % NQ) * kTile);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (!warp_wait(ds_full(c), i & 1, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = kOrder[4 * c + e];
+                    umma_bf16_ts_elected(leader, t_dk, t_dp + packed_col(kk), mndesc_at(q_mn, kk), idesc_g,
+                                         (i > 0 || kk > 0) ? 1u : 0u);
+                }
+            }
+            if (!ok) break;
+            // Q[i] and dO[i]: dK[i] is the last product that reads either
+            umma_commit_elected(leader, q_empty(i % NQ));
+            if (i + 1 < n_steps && !issue_dp(i + 1)) break;
+        }
+        umma_commit_elected(leader, done);
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    } else if (warp == kStats) {
+        // ---------------- statistics warp: step i's lse and D into B operand i % NA
+        const float inv_c = 1.f / p.scale_log2;
+        for (int i = 0; i < n_steps; ++i) {
+            if (!warp_wait(st_full(i % NT), (i / NT) & 1, p.status) ||
+                !warp_wait(aug_empty(i % NA), ((i / NA) & 1) ^ 1u, p.status))
+                break;
+            const float* stat = reinterpret_cast<const float*>(smem_raw + L::kStat + 1024u * (i % NT));
+            uint8_t* aug = smem_raw + L::kAug + (i % NA) * L::kAugTile;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int r = lane + 32 * u;
+                // statistics of rows that see nothing, or behind the last row, reach
+                // hidden columns only, whatever they hold
+                if constexpr (M != kDocCap)
+                    *reinterpret_cast<uint2*>(aug + aug_offset(r, 0)) = split3_bf16(-stat[r] * inv_c);
+                *reinterpret_cast<uint2*>(aug + aug_offset(r, 1)) = split3_bf16(-stat[128 + r]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(q_full(i % NQ));
+                mbar_arrive(st_empty(i % NT));
+            }
+        }
+    } else {
+        // ---------------- two groups of four warps, one key row per thread in each:
+        // group gi takes query columns 64 gi .. 64 gi + 63 of every step
+        const int gi = (warp - 2) >> 2;
+        const int qw = warp & 3;
+        const int row = qw * 32 + lane;
+        const int k = k0 + row;
+        const bool valid = k < p.tokens;
+        const int2 see = valid ? p.plan.cols[k] : make_int2(0, 0);
+        const bool empty = see.y <= see.x;
+        const uint32_t t_row = (static_cast<uint32_t>(qw * 32) << 16) + 64u * gi;
+        bool ok = true;
+        for (int i = 0; i < n_steps; ++i) {
+            const int qc0 = (range.x + i / group) * kRows + 64 * gi;  // query of this group's first column
+            const int h = g * group + i % group;
+            const float slope2 = M != kDocPlain && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+            const float x = static_cast<float>(k - qc0);  // the column at distance 0
+            const int lo = see.x - qc0, hi = see.y - qc0;  // this key's queries
+            if (!warp_wait(s_full, i & 1, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float pr[64];  // P; after the first pass, times the cap's derivative
+            {
+                uint32_t rs[64];
+                tmem_load_32(t_s + t_row, *reinterpret_cast<uint32_t(*)[32]>(rs));
+                tmem_load_32(t_s + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rs + 32));
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 64; ++j) pr[j] = __uint_as_float(rs[j]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float th[32];
+                if constexpr (M == kDocPlain) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) pr[32 * c + j] = ex2(pr[32 * c + j] * p.scale_log2);
+                } else if constexpr (M == kDocBias) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        pr[32 * c + j] = ex2(fmaf(pr[32 * c + j], p.scale_log2, -slope2 * fabsf(static_cast<float>(32 * c + j) - x)));
+                } else {
+                    const float4* lse4 = reinterpret_cast<const float4*>(p.lse + static_cast<int64_t>(h) * p.ld_stat + qc0 + 32 * c);
+                    cap_tanh<32>(p, pr + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 v = lse4[e];
+                        const float lse[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int j = 4 * e + u;
+                            th[j] = pr[32 * c + j];
+                            const float dist = p.slopes ? slope2 * fabsf(static_cast<float>(32 * c + j) - x) : 0.f;
+                            pr[32 * c + j] = ex2(fmaf(th[j], p.cap_log2, -lse[u] - dist));
+                        }
+                    }
+                }
+                hide_grads<32>(pr + 32 * c, 32 * c, lo, hi);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
+                // packed columns 16 c .. 16 c + 15 of the group's columns, all read above
+                tmem_store_16(t_s + t_row + 16 * c, w);
+                if constexpr (M == kDocCap) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) pr[32 * c + j] *= fmaf(-th[j], th[j], 1.f);
+                }
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(p_full(c), lane);
+            }
+            if (!warp_wait(dp_full, i & 1, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t rp[64];
+            tmem_load_32(t_dp + t_row, *reinterpret_cast<uint32_t(*)[32]>(rp));
+            tmem_load_32(t_dp + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rp + 32));
+            tmem_wait_load();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float ds[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) ds[j] = pr[32 * c + j] * __uint_as_float(rp[32 * c + j]);
+                hide_grads<32>(ds, 32 * c, lo, hi);  // a hidden column's dP may be anything
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(ds[2 * e], ds[2 * e + 1]);
+                tmem_store_16(t_dp + t_row + 16 * c, w);
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(ds_full(c), lane);
+            }
+        }
+        // group 0 stores dK, group 1 dV
+        if (ok && warp_wait(done, 0, p.status)) {
+            tc_fence_after();
+            const uint32_t t_acc = (gi == 0 ? t_dk : t_dv) + (static_cast<uint32_t>(qw * 32) << 16);
+            uint16_t* dst = p.out + k * width + (gi == 0 ? kcol : vcol);
+            const float sc = gi == 0 ? p.scale : 1.f;
+            bool again = false;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float r[32];
+                load_tmem32(t_acc + 32 * c, r);
+                again |= !finite32(r);
+                if (valid && !empty) store32(dst + 32 * c, r, sc);
+                if (valid && empty) store32_zero(dst + 32 * c);
+            }
+            uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
+            while (redo) {
+                const int src = __ffs(redo) - 1;
+                redo &= redo - 1;
+                __syncwarp();
+                document_dkv_row<D>(p, k - lane + src, g, lane, gi == 1);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// One launch for both halves of the backward: the first n_blocks * n_kv_heads
+// CTAs form dK and dV, the rest, one per SM at most, take dQ tiles as SMs come
+// free.  (The causal core runs them on two streams, which costs a small call a
+// fork and a join, and makes one stream and counter the whole device's.)
+template <int D, int M>
+__global__ void __launch_bounds__(kAttnDqThreads, 1)
+    document_bwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ CUtensorMap map_do,
+                        const __grid_constant__ DocArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if (smem_addr(smem_raw) & 1023u) {  // the tiles' 128-byte swizzle needs a 1 KiB-aligned start
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, kSiteAttn);
+        return;
+    }
+    if (static_cast<int>(blockIdx.x) < p.n_blocks * p.n_kv_heads)
+        document_dkv<D, M>(map_qkv, map_do, p, smem_raw);
+    else
+        document_dq<D, M>(map_qkv, map_do, p, smem_raw);
+}
 
 DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const float* slopes, float cap) {
     DocArgs p{};
@@ -244,27 +1531,77 @@ DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const flo
     p.slopes = slopes;
     p.cap = cap;
     p.scale = 1.f / sqrtf(static_cast<float>(s.head_dim));
+    p.scale_log2 = kLog2e * p.scale;
+    p.cap_log2 = cap * kLog2e;
+    p.cap_rate = cap > 0.f ? fminf(p.scale / cap, 1e37f) : 0.f;
+    p.cap_exp = 2.f * kLog2e * p.cap_rate;
     p.tokens = s.tokens;
     p.n_heads = s.n_heads;
     p.n_kv_heads = s.n_kv_heads;
     p.ld_stat = s.ld_stat;
+    p.n_blocks = static_cast<int>(doc_blocks(s.tokens));
+    p.status = status_word();
     return p;
 }
 
-template <int D>
+DocMode mode_of(const DocArgs& p) { return p.cap > 0.f ? kDocCap : p.slopes ? kDocBias : kDocPlain; }
+
+template <int D, int M>
 cudaError_t forward(const DocArgs& p, cudaStream_t stream) {
-    document_forward_rows<D><<<warps4(static_cast<int64_t>(p.tokens) * p.n_heads), 128, 0, stream>>>(p);
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] { err = set_smem(document_fwd_kernel<D, M>, DocFwdSmem<D>::kBytes); });
+    if (err != cudaSuccess) return err;
+    const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
+    CUtensorMap map;
+    if (!attn_map(&map, p.qkv, p.tokens, width, width)) return cudaErrorInvalidValue;
+    const int64_t tiles = static_cast<int64_t>(fwd_tiles(p));
+    document_fwd_kernel<D, M><<<static_cast<unsigned>(tiles), kAttnBwdThreads, DocFwdSmem<D>::kBytes, stream>>>(map, p);
+    return cudaGetLastError();
+}
+
+template <int D, int M>
+cudaError_t backward(const DocArgs& p, const uint16_t* a, float* dvec, bool d_ready, cudaStream_t stream) {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] { err = set_smem(document_bwd_kernel<D, M>, doc_bwd_smem<D>()); });
+    if (err != cudaSuccess) return err;
+    const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
+    CUtensorMap mq, md;
+    if (!attn_map(&mq, p.qkv, p.tokens, width, width) || !attn_map(&md, p.da, p.tokens, p.n_heads * D, p.n_heads * D))
+        return cudaErrorInvalidValue;
+    if (d_ready) {
+        const cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream);
+        if (e != cudaSuccess) return e;
+    } else {
+        const int64_t warps = (static_cast<int64_t>(p.tokens) * p.n_heads + 7) / 8;  // 8 rows per warp
+        attn_causal_rowsum_kernel<D><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(
+            p.da, a, dvec, p.tokens, p.n_heads, p.ld_stat, p.counter);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t dkv = static_cast<int64_t>(p.n_blocks) * p.n_kv_heads;
+    const int64_t dq = std::min<int64_t>(static_cast<int64_t>(p.n_blocks) * p.n_heads, sm_count());
+    document_bwd_kernel<D, M><<<static_cast<unsigned>(dkv + dq), kAttnDqThreads, doc_bwd_smem<D>(), stream>>>(mq, md, p);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t backward(DocArgs p, float* dvec, bool d_ready, cudaStream_t stream) {
-    const unsigned rows = warps4(static_cast<int64_t>(p.tokens) * p.n_heads);
-    p.dvec = dvec;
-    if (!d_ready) document_rowsum<D><<<rows, 128, 0, stream>>>(p, dvec);
-    document_dkv_rows<D><<<warps4(static_cast<int64_t>(p.tokens) * p.n_kv_heads), 128, 0, stream>>>(p);
-    document_dq_rows<D><<<rows, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t forward_mode(const DocArgs& p, cudaStream_t stream) {
+    switch (mode_of(p)) {
+        case kDocPlain: return forward<D, kDocPlain>(p, stream);
+        case kDocBias: return forward<D, kDocBias>(p, stream);
+        default: return forward<D, kDocCap>(p, stream);
+    }
+}
+
+template <int D>
+cudaError_t backward_mode(const DocArgs& p, const uint16_t* a, float* dvec, bool d_ready, cudaStream_t stream) {
+    switch (mode_of(p)) {
+        case kDocPlain: return backward<D, kDocPlain>(p, a, dvec, d_ready, stream);
+        case kDocBias: return backward<D, kDocBias>(p, a, dvec, d_ready, stream);
+        default: return backward<D, kDocCap>(p, a, dvec, d_ready, stream);
+    }
 }
 
 }  // namespace
@@ -283,9 +1620,10 @@ cudaError_t launch_document_forward(const DocShape& s, const void* qkv, void* a,
                                     const float* slopes, float cap, cudaStream_t stream) {
     if (s.tokens <= 0) return cudaSuccess;
     DocArgs p = doc_args(s, qkv, plan, slopes, cap);
+    if (!p.status) return cudaErrorInvalidDevice;
     p.out = static_cast<uint16_t*>(a);
     p.lse_out = lse;
-    return s.head_dim == 128 ? forward<128>(p, stream) : forward<64>(p, stream);
+    return s.head_dim == 128 ? forward_mode<128>(p, stream) : forward_mode<64>(p, stream);
 }
 
 cudaError_t launch_document_backward(const DocShape& s, const void* qkv, const void* a, const void* da, const float* lse,
@@ -293,12 +1631,16 @@ cudaError_t launch_document_backward(const DocShape& s, const void* qkv, const v
                                      cudaStream_t stream, bool d_ready) {
     if (s.tokens <= 0) return cudaSuccess;
     DocArgs p = doc_args(s, qkv, plan, slopes, cap);
-    p.a = static_cast<const uint16_t*>(a);
+    if (!p.status) return cudaErrorInvalidDevice;
+    float* dvec = static_cast<float*>(scratch);
     p.da = static_cast<const uint16_t*>(da);
     p.out = static_cast<uint16_t*>(dqkv);
     p.lse = lse;
-    float* dvec = static_cast<float*>(scratch);
-    return s.head_dim == 128 ? backward<128>(p, dvec, d_ready, stream) : backward<64>(p, dvec, d_ready, stream);
+    p.dvec = dvec;
+    p.counter = reinterpret_cast<int*>(dvec + static_cast<int64_t>(s.n_heads) * s.ld_stat);
+    const uint16_t* av = static_cast<const uint16_t*>(a);
+    return s.head_dim == 128 ? backward_mode<128>(p, av, dvec, d_ready, stream)
+                             : backward_mode<64>(p, av, dvec, d_ready, stream);
 }
 
 namespace {

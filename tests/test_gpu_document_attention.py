@@ -97,13 +97,21 @@ def reference(qkv, nh, nkv, d, see, cap=0.0, slopes=None, da=None):
     return a, lse, out.transpose(0, 1).reshape(t, (nh + 2 * nkv) * d)
 
 
-def assert_near(got, ref, what):
+def cancelled(qkv, a, da, nh, d):
+    """What is left of dq and dk where the formula gives zero (a row that sees one key: P = 1 and dP = D).  dP and D are
+    float32 sums of the same d products in two orders: each is off by at most d 2^-24 of the sum of their sizes, and the
+    difference meets a query or key, and the scale."""
+    sums = (da.double() * a.double()).abs().view(da.shape[0], nh, d).sum(2).max()
+    return float(2 * d * 2.0 ** -24 * sums * qkv.double().abs().max() / math.sqrt(d))
+
+
+def assert_near(got, ref, what, floor=0.0):
     got = got.double()
     assert torch.isfinite(got).all(), f"{what}: not finite"
     norm, top = float(ref.norm()), float(ref.abs().max()) if ref.numel() else 0.0
     d = got - ref
     if norm == 0.0:
-        assert float(d.abs().sum()) == 0.0, what
+        assert not d.numel() or float(d.abs().max()) <= floor, what
         return
     assert float(d.norm()) <= FRO_TOL * norm and float(d.abs().max()) <= MAX_TOL * top, \
         f"{what}: {float(d.norm()) / norm:.2e}, {float(d.abs().max()) / top:.2e}"
@@ -142,8 +150,9 @@ def both_ways(seed, t, nh, nkv, d, offsets, prefix=None, cap=0.0, bias=False):
     assert_lse(lse, rl, t)
     dqkv = backward(qkv, a, da, lse, t, nh, nkv, d, plan, cap, slopes)
     w, kw = nh * d, nkv * d
-    assert_near(dqkv[:, :w], rd[:, :w], "dq")
-    assert_near(dqkv[:, w:w + kw], rd[:, w:w + kw], "dk")
+    floor = cancelled(qkv, a, da, nh, d)
+    assert_near(dqkv[:, :w], rd[:, :w], "dq", floor)
+    assert_near(dqkv[:, w:w + kw], rd[:, w:w + kw], "dk", floor)
     assert_near(dqkv[:, w + kw:], rd[:, w + kw:], "dv")
     dead = ~see.any(1)
     assert torch.all(a[dead] == 0) and torch.all(dqkv[dead] == 0)
