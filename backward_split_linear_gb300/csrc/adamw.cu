@@ -144,15 +144,21 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// The grid's value of a code without its sign, and its code from a scaled value
-// z >= 0; `noise` (16 bits, 0x8000: to the nearest) is the rounding's threshold.
+// The grid's value of a code without its sign.  The float whose upper bits are
+// the code plus 1040 is twice the value, or the value plus 8 for the codes below
+// 8, and the smaller of the two readings is the right one on both sides.
 __device__ __forceinline__ float code_value(uint32_t c) {
-    return c < 8u ? static_cast<float>(c) : __uint_as_float((c + 1032u) << 20);
+    const float x = __uint_as_float((c + 1040u) << 20);
+    return fminf(0.5f * x, x - 8.f);
 }
-__device__ __forceinline__ uint32_t code_of(float z, uint32_t noise) {
-    const bool small = z < 8.f;
-    const uint32_t bits = __float_as_uint(small ? __fadd_rn(z, 8.f) : z);
-    return ((bits + (noise << 4)) >> 20) - (small ? 1040u : 1032u);
+// The code of a scaled value z >= 0, in bits 20 to 27: the inverse, rounded up when
+// the remainder's 20 bits and `noise` << 4 carry (16 bits; 0x8000: to the nearest).
+__device__ __forceinline__ uint32_t code_bits(float z, uint32_t noise4) {
+    return __float_as_uint(fmaxf(z + z, __fadd_rn(z, 8.f))) + noise4 - (1040u << 20);
+}
+// Bits 20 to 27 of four words as four bytes.
+__device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a >> 20, b >> 20, 0x0040), __byte_perm(c >> 20, d >> 20, 0x0040), 0x5410);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -238,29 +244,39 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     }
     if constexpr (kState8) {
         float mm = 0.f, mv = 0.f;
+        if (e + 8 <= n) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (e + k < n) {
+            for (int k = 0; k < 8; ++k) {
                 mm = fmaxf(mm, fabsf(m[k]));
                 mv = fmaxf(mv, v[k]);
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (e + k < n) {
+                    mm = fmaxf(mm, fabsf(m[k]));
+                    mv = fmaxf(mv, v[k]);
+                }
+        }
         mm = warp_max(mm);
         mv = warp_max(mv);
         const float tiny = 1.17549435e-38f;
         const float sm = fmaxf(__fmul_rn(mm, 1.f / kMTop), tiny), sv = fmaxf(__fmul_rn(mv, 1.f / kVTop), tiny);
         const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
-        uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
+        uint32_t cm[8], cv[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            uint32_t c = code_of(fminf(__fmul_rn(fabsf(m[k]), im), kMTop), noise[k] & 0xFFFFu);
-            c |= (__float_as_uint(m[k]) >> 24) & 128u;
-            cm[k >> 2] |= c << (8 * (k & 3));
+            cm[k] = code_bits(fminf(__fmul_rn(fabsf(m[k]), im), kMTop), (noise[k] << 4) & 0xFFFF0u);
+            // the sign above the code's seven bits (27 is m's bit 31 four places down)
+            cm[k] = (cm[k] & 0x07FFFFFFu) | ((__float_as_uint(m[k]) >> 4) & 0x08000000u);
             const float z = fminf(__fmul_rn(v[k], iv), kVTop);
-            c = max(code_of(z, noise[k] >> 16), z > 0.f ? 1u : 0u);
-            cv[k >> 2] |= c << (8 * (k & 3));
+            cv[k] = code_bits(z, (noise[k] >> 12) & 0xFFFF0u);
+            if (z > 0.f) cv[k] = max(cv[k], 1u << 20);
         }
-        store8b(static_cast<uint8_t*>(t.m), e, n, make_uint2(cm[0], cm[1]));
-        store8b(static_cast<uint8_t*>(t.v), e, n, make_uint2(cv[0], cv[1]));
+        store8b(static_cast<uint8_t*>(t.m), e, n,
+                make_uint2(pack_codes(cm[0], cm[1], cm[2], cm[3]), pack_codes(cm[4], cm[5], cm[6], cm[7])));
+        store8b(static_cast<uint8_t*>(t.v), e, n,
+                make_uint2(pack_codes(cv[0], cv[1], cv[2], cv[3]), pack_codes(cv[4], cv[5], cv[6], cv[7])));
         if (in && (threadIdx.x & 31) == 0) {
             t.m_scale[block] = sm;
             t.v_scale[block] = sv;
@@ -319,56 +335,65 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid
     store8f(out.v[ti], e, n, v);
 }
 
-// Sum of squares of every chunk of kNormChunks x kChunk elements, one float64
-// per block: a fixed partition and order, so the norm is the same bits every
-// time.  Squares are summed in float32 over a thread's 64 elements, then in
-// float64.
-constexpr int kNormChunks = 8;
+// Sums of squares.  The chunks of a launch go round-robin to a fixed number of
+// blocks, whatever the device, and each block writes one float64: a fixed
+// partition and order, so the norm is the same bits every time.  Squares are summed
+// in float32, eight sums a thread: FP64 units are scarce, and positive terms'
+// rounding errors average out (about 1e-7 of the norm measured).
+constexpr int kNormChunks = 4;       // chunks of a block in flight
+constexpr int kNormBlocks = 1216;    // eight blocks on each of 152 SMs
 
-__global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid_constant__ AdamTable tab, double* part) {
+// Sum of squares of thread `threadIdx.x`'s elements of chunks blockIdx.x + i gridDim.x.
+template <typename T>
+__device__ __forceinline__ T thread_squares(const AdamTable& tab, int64_t chunks) {
+    T s[8] = {};
+    for (int64_t c0 = blockIdx.x; c0 < chunks; c0 += static_cast<int64_t>(kNormChunks) * gridDim.x) {
+        float g[kNormChunks][8];
+#pragma unroll
+        for (int i = 0; i < kNormChunks; ++i) {
+            const int64_t c = c0 + static_cast<int64_t>(i) * gridDim.x;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[i][k] = 0.f;
+            if (c < chunks) {
+                const int ti = find_tensor(tab, c);
+                const zb_adamw_tensor& t = tab.t[ti];
+                const int64_t e = (c - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
+                if (t.grad_dtype == ZB_F32)
+                    load8f(static_cast<const float*>(t.grad), e, t.count, g[i]);
+                else
+                    load8h(static_cast<const uint16_t*>(t.grad), e, t.count, g[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kNormChunks; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[k] += static_cast<T>(g[i][k]) * static_cast<T>(g[i][k]);
+    }
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+__global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid_constant__ AdamTable tab, int64_t chunks,
+                                                                    double* part) {
     __shared__ double red[kAdamThreads / 32];
-    const int64_t chunk = blockIdx.x;
-    const int ti = find_tensor(tab, chunk);
-    const zb_adamw_tensor& t = tab.t[ti];
-    const int64_t n = t.count;
-    const int64_t e0 = (chunk - tab.first[ti]) * kNormChunks * kChunk + threadIdx.x * kPerThread;
-    float g[kNormChunks][8];
+    float sum = thread_squares<float>(tab, chunks);
+    // squares that leave float32's range (or all but leave it) are summed again in float64, by the whole warp
+    const bool ok = sum <= 1e30f && sum >= 1e-25f;
+    double total;
+    if (__all_sync(0xffffffffu, ok)) {
 #pragma unroll
-    for (int c = 0; c < kNormChunks; ++c) {
-        const int64_t e = e0 + c * kChunk;
-        if (t.grad_dtype == ZB_F32)
-            load8f(static_cast<const float*>(t.grad), e, n, g[c]);
-        else
-            load8h(static_cast<const uint16_t*>(t.grad), e, n, g[c]);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        total = sum;
+    } else {
+        total = thread_squares<double>(tab, chunks);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < kNormChunks; ++c)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[k] = fmaf(g[c][k], g[c][k], s[k]);
-    double sum = 0.0;
-    float total32 = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        total32 += s[k];
-        sum += static_cast<double>(s[k]);
-    }
-    // squares outside float32's range: this thread's sum again in float64
-    if (!(total32 <= 3.4e38f) || total32 < 1e-30f) {
-        sum = 0.0;
-#pragma unroll
-        for (int c = 0; c < kNormChunks; ++c)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += static_cast<double>(g[c][k]) * static_cast<double>(g[c][k]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double total = 0.0;
-        for (int w = 0; w < kAdamThreads / 32; ++w) total += red[w];
-        part[chunk] = total;
+        double t = 0.0;
+        for (int w = 0; w < kAdamThreads / 32; ++w) t += red[w];
+        part[blockIdx.x] = t;
     }
 }
 
@@ -518,9 +543,8 @@ extern "C" zb_status zb_op_adamw_unpack(const zb_adamw_tensor* tensors, int32_t 
 
 extern "C" size_t zb_op_grad_norm_scratch_bytes(const zb_adamw_tensor* tensors, int32_t n) {
     if (tensors_ok(tensors, n) != ZB_OK) return 0;
-    int64_t c = 0;
-    for (int i = 0; i < n; ++i) c += chunks_of(tensors[i].count, int64_t(kNormChunks) * kChunk);
-    return static_cast<size_t>(std::max<int64_t>(c, 1)) * sizeof(double);
+    const int64_t launches = (n + kMaxAdamTensors - 1) / kMaxAdamTensors;
+    return static_cast<size_t>(std::max<int64_t>(launches, 1)) * kNormBlocks * sizeof(double);
 }
 
 extern "C" zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, float max_norm, float* out, void* scratch,
@@ -534,9 +558,10 @@ extern "C" zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, 
     cudaStream_t s = as_stream(stream);
     double* part = static_cast<double*>(scratch);
     int64_t done = 0;
-    const cudaError_t e = for_tables(tensors, n, int64_t(kNormChunks) * kChunk, [&](const AdamTable& tab, int64_t c, int) {
-        norm_partial_kernel<<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, part + done);
-        done += c;
+    const cudaError_t e = for_tables(tensors, n, kChunk, [&](const AdamTable& tab, int64_t c, int) {
+        const int64_t blocks = std::min<int64_t>(c, kNormBlocks);
+        norm_partial_kernel<<<static_cast<unsigned>(blocks), kAdamThreads, 0, s>>>(tab, c, part + done);
+        done += blocks;
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return ZB_ERR_CUDA;

@@ -21,10 +21,10 @@ namespace zbk {
 
 namespace {
 
-constexpr int kRotThreads = 256;
-// A block computes the sines of kRotPairs (token, pair) entries into shared
-// memory, then applies them to every head of those tokens.
-constexpr int kRotPairs = 512;
+constexpr int kRotThreads = 128;
+constexpr int kRotMaxPairs = 512;
+constexpr int kRotUnroll = 4;  // heads whose loads a thread issues together
+constexpr int kRotHeads = 8;   // heads a thread takes, about
 
 struct RotaryArgs {
     const uint16_t* x;
@@ -34,7 +34,8 @@ struct RotaryArgs {
     const uint64_t* turns;
     float magnitude;
     int tokens, n_heads, head_dim, rot;
-    int tokens_per_block;
+    int columns, groups;  // 16-element columns of a head; threads that share a column's heads
+    int64_t threads;
     float sign;  // +1 forward, -1 backward
 };
 
@@ -50,57 +51,73 @@ __device__ __forceinline__ uint32_t rotate1(uint32_t w, float2 cs) {
     return pack_bf16x2(a * cs.x - b * cs.y, b * cs.x + a * cs.y);
 }
 
-// One item is 16 elements of one head of one token: 8 from each half of the
-// rotated part (kHalf), or 16 consecutive ones.
+// One thread takes one 16-element column of one token (8 elements from each half
+// of the rotated part with kHalf, or 16 consecutive ones; behind the rotated part
+// a column is copied) and every groups-th head.  It issues the loads of its first
+// heads, forms the column's 8 cosines and sines while they fly, and keeps those in
+// registers.  Neighbouring threads take neighbouring columns, then neighbouring
+// heads: a warp's accesses cover whole heads.  Every head is read and written once;
+// the kernel is bound by HBM.
 template <bool kHalf>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p) {
-    __shared__ float2 table[kRotPairs];
-    const int pairs = p.rot >> 1;
-    const int t0 = blockIdx.x * p.tokens_per_block;
-    const int nt = min(p.tokens_per_block, p.tokens - t0);
-    for (int e = threadIdx.x; e < nt * pairs; e += kRotThreads) {
-        const int t = e / pairs, i = e - t * pairs;
-        const int64_t pos = p.positions ? p.positions[t0 + t] : t0 + t;
-        const uint64_t frac = static_cast<uint64_t>(pos) * p.turns[i];
-        // the upper 32 bits as a signed number of half turns in [-1, 1)
-        float s, c;
-        sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &s, &c);
-        table[e] = make_float2(c * p.magnitude, s * p.magnitude * p.sign);
-    }
-    __syncthreads();
-    const int per_head = p.rot >> 4;
-    const int per_token = p.n_heads * per_head;
-    for (int e = threadIdx.x; e < nt * per_token; e += kRotThreads) {
-        const int t = e / per_token, r = e - t * per_token;
-        const int h = r / per_head, c = r - h * per_head;
-        const int64_t at = static_cast<int64_t>(h) * p.head_dim + (kHalf ? 8 * c : 16 * c);
-        const uint16_t* src = p.x + (t0 + t) * p.ld_x + at;
-        uint16_t* dst = p.y + (t0 + t) * p.ld_y + at;
-        const int second = kHalf ? pairs : 8;
-        uint4 u = *reinterpret_cast<const uint4*>(src), v = *reinterpret_cast<const uint4*>(src + second);
-        const float2* cs = table + t * pairs + 8 * c;
-        if (kHalf) {
-            rotate2(u.x, v.x, cs[0], cs[1]);
-            rotate2(u.y, v.y, cs[2], cs[3]);
-            rotate2(u.z, v.z, cs[4], cs[5]);
-            rotate2(u.w, v.w, cs[6], cs[7]);
-        } else {
-            u = make_uint4(rotate1(u.x, cs[0]), rotate1(u.y, cs[1]), rotate1(u.z, cs[2]), rotate1(u.w, cs[3]));
-            v = make_uint4(rotate1(v.x, cs[4]), rotate1(v.y, cs[5]), rotate1(v.z, cs[6]), rotate1(v.w, cs[7]));
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kRotThreads + threadIdx.x;
+    if (id >= p.threads) return;
+    const int per_token = p.columns * p.groups;
+    const int t = static_cast<int>(id / per_token);
+    const int r = static_cast<int>(id - static_cast<int64_t>(t) * per_token);
+    const int group = r / p.columns, c = r - group * p.columns;
+    const bool turned = 16 * c < p.rot;
+    const int at = kHalf && turned ? 8 * c : 16 * c;
+    const int second = kHalf && turned ? p.rot >> 1 : 8;
+    const bool both = turned || at + second < p.head_dim;  // the last copied column may be 8 elements
+    const uint16_t* src = p.x + t * p.ld_x + at;
+    uint16_t* dst = p.y + t * p.ld_y + at;
+    uint4 u[kRotUnroll], v[kRotUnroll];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < kRotUnroll; ++i) {
+            const int h = h0 + i * p.groups;
+            if (h < p.n_heads) {
+                u[i] = *reinterpret_cast<const uint4*>(src + h * p.head_dim);
+                if (both) v[i] = *reinterpret_cast<const uint4*>(src + h * p.head_dim + second);
+            }
         }
-        *reinterpret_cast<uint4*>(dst) = u;
-        *reinterpret_cast<uint4*>(dst + second) = v;
+    };
+    load(group);
+    float2 cs[8];
+    if (turned) {
+        const int64_t pos = p.positions ? p.positions[t] : t;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint64_t frac = static_cast<uint64_t>(pos) * p.turns[8 * c + k];
+            // the upper 32 bits as a signed number of half turns in [-1, 1)
+            float sn, cn;
+            sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &sn, &cn);
+            cs[k] = make_float2(cn * p.magnitude, sn * p.magnitude * p.sign);
+        }
     }
-    // the part of a head behind the rotated one, when y is not x
-    const int tail = (p.head_dim - p.rot) >> 3;
-    if (tail == 0 || p.x == p.y) return;
-    const int tail_token = p.n_heads * tail;
-    for (int e = threadIdx.x; e < nt * tail_token; e += kRotThreads) {
-        const int t = e / tail_token, r = e - t * tail_token;
-        const int h = r / tail, c = r - h * tail;
-        const int64_t at = static_cast<int64_t>(h) * p.head_dim + p.rot + 8 * c;
-        *reinterpret_cast<uint4*>(p.y + (t0 + t) * p.ld_y + at) =
-            *reinterpret_cast<const uint4*>(p.x + (t0 + t) * p.ld_x + at);
+    for (int h0 = group;;) {
+#pragma unroll
+        for (int i = 0; i < kRotUnroll; ++i) {
+            const int h = h0 + i * p.groups;
+            if (h >= p.n_heads) break;
+            if (turned) {
+                if (kHalf) {
+                    rotate2(u[i].x, v[i].x, cs[0], cs[1]);
+                    rotate2(u[i].y, v[i].y, cs[2], cs[3]);
+                    rotate2(u[i].z, v[i].z, cs[4], cs[5]);
+                    rotate2(u[i].w, v[i].w, cs[6], cs[7]);
+                } else {
+                    u[i] = make_uint4(rotate1(u[i].x, cs[0]), rotate1(u[i].y, cs[1]), rotate1(u[i].z, cs[2]), rotate1(u[i].w, cs[3]));
+                    v[i] = make_uint4(rotate1(v[i].x, cs[4]), rotate1(v[i].y, cs[5]), rotate1(v[i].z, cs[6]), rotate1(v[i].w, cs[7]));
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + h * p.head_dim) = u[i];
+            if (both) *reinterpret_cast<uint4*>(dst + h * p.head_dim + second) = v[i];
+        }
+        h0 += kRotUnroll * p.groups;
+        if (h0 >= p.n_heads) break;
+        load(h0);
     }
 }
 
@@ -110,7 +127,7 @@ zb_status rotary(const void* x, int64_t ld_x, void* y, int64_t ld_y, const int32
     if (pairs != ZB_ROTARY_HALF && pairs != ZB_ROTARY_INTERLEAVED) return ZB_ERR_ARG;
     if (!tokens_ok(tokens) || n_heads <= 0 || head_dim <= 0 || head_dim % 8 != 0 || n_heads > kMaxFeature / head_dim ||
         !feature_ok(n_heads * head_dim) || rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0 ||
-        rotary_dim / 2 > kRotPairs)
+        rotary_dim / 2 > kRotMaxPairs)
         return ZB_ERR_SHAPE;
     if (ld_x < n_heads * head_dim || ld_y < n_heads * head_dim || ld_x % 8 != 0 || ld_y % 8 != 0) return ZB_ERR_SHAPE;
     if (!rows_ok(x, tokens) || !rows_ok(y, tokens) || (positions && (reinterpret_cast<uintptr_t>(positions) & 3u)) ||
@@ -141,8 +158,11 @@ cudaError_t launch_rotary(const void* x, int64_t ld_x, void* y, int64_t ld_y, co
     p.head_dim = head_dim;
     p.rot = rotary_dim;
     p.sign = sign;
-    p.tokens_per_block = std::max(1, kRotPairs / (rotary_dim / 2));
-    const unsigned grid = static_cast<unsigned>((tokens + p.tokens_per_block - 1) / p.tokens_per_block);
+    // in place, what lies behind the rotated part stays as it is
+    p.columns = (rotary_dim >> 4) + (x == y ? 0 : (head_dim - rotary_dim + 15) >> 4);
+    p.groups = (n_heads + kRotHeads - 1) / kRotHeads;
+    p.threads = static_cast<int64_t>(tokens) * p.columns * p.groups;
+    const unsigned grid = static_cast<unsigned>((p.threads + kRotThreads - 1) / kRotThreads);
     if (half)
         rotary_kernel<true><<<grid, kRotThreads, 0, stream>>>(p);
     else
@@ -169,7 +189,7 @@ extern "C" zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* 
 extern "C" zb_status zb_rotary_frequencies(const zb_rotary_config* cfg, uint64_t* turns, float* magnitude) {
     if (!cfg || !turns || !magnitude) return ZB_ERR_ARG;
     const int rot = cfg->rotary_dim;
-    if (rot < 16 || rot % 16 != 0 || rot / 2 > zbk::kRotPairs) return ZB_ERR_SHAPE;
+    if (rot < 16 || rot % 16 != 0 || rot / 2 > zbk::kRotMaxPairs) return ZB_ERR_SHAPE;
     const double two_pi = 6.283185307179586476925286766559;
     double base = cfg->base;
     const double factor = cfg->factor, context = cfg->context;
