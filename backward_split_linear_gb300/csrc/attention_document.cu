@@ -113,6 +113,7 @@ struct DocArgs {
     float scale_log2;      // log2(e) / sqrt(d)
     float cap_log2;        // cap log2(e)
     float cap_rate;        // 1 / (cap sqrt(d))
+    float cap_poly[5];     // tanh(s cap_rate) / s as a polynomial in s^2
     float cap_exp;         // 2 log2(e) / (cap sqrt(d)): the exponent of e^(2 s / cap) per unit of q . k
     int tokens, n_heads, n_kv_heads, ld_stat, n_blocks;
     int* status;
@@ -242,29 +243,34 @@ __device__ __noinline__ void document_dkv_row(const DocArgs& p, int j, int g, in
 
 // ------------------------------------------------------------------------ scores on the tensor-core path
 
-// s <- tanh(s / (cap sqrt(d))) for N columns of a row.  Where all of a warp's
-// arguments lie in [-1, 1] (scores below the cap, the usual case), an odd
-// polynomial of degree 13 on the FMA pipe, relative error below 2^-22 (its
-// coefficients: a weighted least-squares fit of tanh(x) / x in x^2, reweighted to
-// equal ripple).  Else 1 - 2 / (1 + e^(2x)): two more special-function operations
-// an element beside the softmax's one, and off by 2^-22 of the cap, which there is
-// below the largest score.
+// The largest of three, one instruction (NaN operands give way, as in fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// s <- tanh(x), x = s / (cap sqrt(d)), for N columns of a row.  Where all of a
+// warp's |x| are at most 3/4 (scores below 3/4 of the cap, the usual case), an odd
+// polynomial of degree 9 on the FMA pipe, relative error below 6e-7: x P(x^2), P a
+// weighted least-squares fit of tanh(x) / x reweighted to equal ripple, with the
+// factor between s and x in its coefficients.  Else 1 - 2 / (1 + e^(2x)): two more
+// special-function operations an element beside the softmax's one, and off by
+// 2^-22 of the cap, which there is not far above the largest score.
 template <int N>
 __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], fabsf(s[c]));
-    if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.cap_rate <= 1.f)) {
+    if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.cap_rate <= 0.75f)) {
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-            const float x = s[c] * p.cap_rate, u = x * x;
-            float r = fmaf(0.00104102242f, u, -0.00620337895f);
-            r = fmaf(r, u, 0.0202899809f);
-            r = fmaf(r, u, -0.0534570303f);
-            r = fmaf(r, u, 0.133252041f);
-            r = fmaf(r, u, -0.333328392f);
-            r = fmaf(r, u, 0.99999995f);
-            s[c] = x * r;
+            const float u = s[c] * s[c];
+            float r = fmaf(p.cap_poly[4], u, p.cap_poly[3]);
+            r = fmaf(r, u, p.cap_poly[2]);
+            r = fmaf(r, u, p.cap_poly[1]);
+            r = fmaf(r, u, p.cap_poly[0]);
+            s[c] *= r;
         }
     } else {
 #pragma unroll
@@ -316,16 +322,26 @@ __device__ __forceinline__ bool finite32(const float (&v)[32]) {
     return m == 0.f;
 }
 
+// 32 bytes of one row in one instruction: the lanes of a warp store to 32 rows, and
+// each row costs the store unit a pass, however few of its bytes are written.
+__device__ __forceinline__ void store_bytes32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 __device__ __forceinline__ void store32(uint16_t* dst, const float (&v)[32], float f) {
-    uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        d4[k] = make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
-                           pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f), pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+    for (int k = 0; k < 2; ++k) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(v[16 * k + 2 * e] * f, v[16 * k + 2 * e + 1] * f);
+        store_bytes32(dst + 16 * k, w);
+    }
 }
 __device__ __forceinline__ void store32_zero(uint16_t* dst) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(dst)[k] = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    store_bytes32(dst, zero);
+    store_bytes32(dst + 16, zero);
 }
 
 __device__ __forceinline__ void load_tmem32(uint32_t t, float (&v)[32]) {
@@ -374,8 +390,9 @@ __host__ __device__ inline int fwd_tiles(const DocArgs& p) {
     return (p.n_heads / p.n_kv_heads) % 2 == 0 ? p.n_blocks * (p.n_heads / 2) : (p.n_blocks + 1) / 2 * p.n_heads;
 }
 
-__device__ __forceinline__ FwdTile fwd_tile(const DocArgs& p, int t) {
-    FwdTile f;
+// Where tile t lies: heads, query rows, kv head.
+__device__ __forceinline__ FwdTile fwd_place(const DocArgs& p, int t) {
+    FwdTile f{};
     const int group = p.n_heads / p.n_kv_heads;
     if (group % 2 == 0) {
         const int pairs = p.n_heads / 2;
@@ -383,20 +400,23 @@ __device__ __forceinline__ FwdTile fwd_tile(const DocArgs& p, int t) {
         f.h[0] = 2 * (t % pairs);
         f.h[1] = f.h[0] + 1;
         f.q0[0] = f.q0[1] = qb * kRows;
-        const int2 r = block_range(p.plan.q_blocks, qb, p.n_blocks);
-        f.first = r.x;
-        f.nk = r.y - r.x;
     } else {
         const int b = (p.n_blocks + 1) / 2 - 1 - t / p.n_heads;
         f.h[0] = f.h[1] = t % p.n_heads;
         f.q0[0] = 2 * b * kRows;
         f.q0[1] = f.q0[0] + kRows;
-        const int2 x = block_range(p.plan.q_blocks, 2 * b, p.n_blocks), y = block_range(p.plan.q_blocks, 2 * b + 1, p.n_blocks);
-        const bool ex = x.x == x.y, ey = y.x == y.y;
-        f.first = ex ? y.x : ey ? x.x : min(x.x, y.x);
-        f.nk = (ex ? y.y : ey ? x.y : max(x.y, y.y)) - f.first;
     }
     f.g = f.h[0] / group;
+    return f;
+}
+
+// The same with its key blocks: those that a row of either tile sees.
+__device__ __forceinline__ FwdTile fwd_tile(const DocArgs& p, int t) {
+    FwdTile f = fwd_place(p, t);
+    const int2 x = block_range(p.plan.q_blocks, f.q0[0] / kRows, p.n_blocks), y = block_range(p.plan.q_blocks, f.q0[1] / kRows, p.n_blocks);
+    const bool ex = x.x == x.y, ey = y.x == y.y;
+    f.first = ex ? y.x : ey ? x.x : min(x.x, y.x);
+    f.nk = (ex ? y.y : ey ? x.y : max(x.y, y.y)) - f.first;
     return f;
 }
 
@@ -411,8 +431,9 @@ struct DocFwdSmem {
     // Q full / empty, the K / V ring, S, P and done of both tiles, tile slots full / empty, answer, drain
     static constexpr int kNumBars = 2 + 2 * kStages + 6 + 4 + 2;
     static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
-    static constexpr uint32_t kTileSlot = kTmemSlot + 8;
-    static constexpr size_t kUsed = kTileSlot + 8;
+    static constexpr uint32_t kTileSlot = kTmemSlot + 16;  // two slots of a tile's number, first key block and steps
+    static constexpr uint32_t kRowSlot = kTileSlot + 2 * 16;  // and of its rows' intervals, 1 KiB a tile
+    static constexpr size_t kUsed = kRowSlot + 2 * 2 * 1024;
     static constexpr size_t kBytes = kUsed > kMinSmem ? kUsed : kMinSmem;
 };
 
@@ -447,7 +468,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const uint32_t answer_full = bars + 8u * (kB + 10), drain = bars + 8u * (kB + 11);
     const uint32_t tmem_slot = base + L::kTmemSlot;
     volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + L::kTmemSlot);
-    volatile int* tile_slot = reinterpret_cast<volatile int*>(smem_raw + L::kTileSlot);
+    const int4* tile_slot = reinterpret_cast<const int4*>(smem_raw + L::kTileSlot);
+    const int2* row_slot = reinterpret_cast<const int2*>(smem_raw + L::kRowSlot);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -479,25 +501,39 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     auto t_s = [&](int x) { return tmem_base + 128u * static_cast<uint32_t>(x); };
     auto t_o = [&](int x) { return tmem_base + 256u + 128u * static_cast<uint32_t>(x); };
     // A consumer warp's view of tile slot n & 1 (-1: none left), after which the
-    // warp releases the slot.
-    auto take_tile = [&](uint32_t n, int& t) {
+    // warp releases the slot; `see`: its row of tile x's intervals.
+    auto take_tile = [&](uint32_t n, FwdTile& f, int x, int row, int2& see) {
         if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
-        t = tile_slot[n & 1u];
+        const int4 slot = tile_slot[n & 1u];
+        see = row_slot[((n & 1u) * 2 + x) * kRows + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(tile_empty(n & 1u));
+        if (slot.x < 0) return false;
+        f = fwd_place(p, slot.x);
+        f.first = slot.y;
+        f.nk = slot.z;
         return true;
     };
 
     if (warp == 0) {
         if (lane == 0) {
-            uint32_t nq = 0, nkv = 0;  // Q loads and K / V steps issued
+            uint32_t nq = 0, nkv = 0, nt = 0;  // Q loads, K / V steps and tile slots issued
             int t = static_cast<int>(blockIdx.x);
             for (uint32_t n = 0;; ++n) {
                 if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                tile_slot[n & 1u] = t;
-                mbar_arrive(tile_full(n & 1u));
-                if (t < 0) break;
-                const FwdTile f = fwd_tile(p, t);
+                const FwdTile f = t >= 0 ? fwd_tile(p, t) : FwdTile{};
+                *reinterpret_cast<int4*>(smem_raw + L::kTileSlot + 16 * (n & 1u)) = make_int4(t, f.first, f.nk, 0);
+                ++nt;
+                if (t < 0) {
+                    mbar_arrive(tile_full(n & 1u));
+                    break;
+                }
+                // the intervals of the tiles' rows land on the same barrier
+                const uint32_t rows = base + L::kRowSlot + 2048u * (n & 1u);
+                const bool two = f.q0[1] < p.n_blocks * kRows;  // tile B may lie behind the last block
+                mbar_arrive_expect_tx(tile_full(n & 1u), two ? 2048 : 1024);
+                bulk_load_1d(rows, p.plan.rows + f.q0[0], 1024, tile_full(n & 1u));
+                if (two) bulk_load_1d(rows + 1024, p.plan.rows + f.q0[1], 1024, tile_full(n & 1u));
                 if (f.nk > 0) {
                     // Q once the previous tile's scores are formed
                     if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
@@ -539,6 +575,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 const uint32_t u = ring_uses(nkv, NS, s);
                 if (u > 0) mbar_wait_fast(kv_full(s), (u - 1) & 1u, p.status, kSiteDrain);
             }
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t u = ring_uses(nt, 2, s);
+                if (u > 0) mbar_wait_fast(tile_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+            }
         }
     } else if (warp == 1) {
         // the whole warp runs the issue loop; its elected lane carries each instruction
@@ -571,9 +611,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
-            int t;
-            if (!take_tile(n, t) || t < 0) break;
-            const int nk = fwd_tile(p, t).nk;
+            FwdTile f;
+            int2 unused;
+            if (!take_tile(n, f, 0, 0, unused)) break;
+            const int nk = f.nk;
             if (nk == 0) continue;
             if (!warp_wait(q_full, nq & 1u, p.status) || !kv_ready(g)) break;
             ++nq;
@@ -615,13 +656,13 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         uint32_t g = 0, nd = 0;  // steps and tiles with steps so far
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
-            int t;
-            if (!take_tile(n, t) || t < 0) break;
-            const FwdTile f = fwd_tile(p, t);
+            FwdTile f;
+            int2 see;
+            if (!take_tile(n, f, x, row, see)) break;
             const int h = x ? f.h[1] : f.h[0];
             const int q = (x ? f.q0[1] : f.q0[0]) + row;
             const bool valid = q < p.tokens;
-            const int2 see = valid ? p.plan.rows[q] : make_int2(0, 0);
+            if (!valid) see = make_int2(0, 0);
             const bool empty = see.y <= see.x;
             const float slope2 = M != kDocPlain && p.slopes ? p.slopes[h] * kLog2e : 0.f;
             // -1e30, not -infinity: a row that has seen no key yet keeps finite differences
@@ -662,7 +703,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 128; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], s[c]);
+                for (int c = 0; c < 128; c += 2) mx8[(c >> 1) & 7] = max3(mx8[(c >> 1) & 7], s[c], s[c + 1]);
                 float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                  fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 mx *= sc;
@@ -1533,8 +1574,12 @@ DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const flo
     p.scale = 1.f / sqrtf(static_cast<float>(s.head_dim));
     p.scale_log2 = kLog2e * p.scale;
     p.cap_log2 = cap * kLog2e;
-    p.cap_rate = cap > 0.f ? fminf(p.scale / cap, 1e37f) : 0.f;
+    p.cap_rate = cap > 0.f ? p.scale / cap : 0.f;
     p.cap_exp = 2.f * kLog2e * p.cap_rate;
+    const double tanh_poly[5] = {0.999999434947, -0.333282515696, 0.132589833556, -0.0500563036011, 0.0129296314219};
+    double power = p.cap_rate;  // cap_rate^(2 k + 1)
+    for (int k = 0; k < 5; ++k, power *= static_cast<double>(p.cap_rate) * p.cap_rate)
+        p.cap_poly[k] = static_cast<float>(tanh_poly[k] * power);
     p.tokens = s.tokens;
     p.n_heads = s.n_heads;
     p.n_kv_heads = s.n_kv_heads;
@@ -1649,7 +1694,7 @@ bool word_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 
 zb_status document_ok(int32_t tokens, int32_t nh, int32_t nkv, int32_t hd, const void* plan, const float* slopes, float cap) {
     if (!tokens_ok(tokens) || !heads_ok(nh, nkv, hd) || (hd != 64 && hd != 128)) return ZB_ERR_SHAPE;
-    if (!rows_ok(plan, tokens) || !word_ok(slopes) || !(cap >= 0.f && cap <= 1e30f)) return ZB_ERR_ARG;
+    if (!rows_ok(plan, tokens) || !word_ok(slopes) || !(cap == 0.f || (cap >= 1e-3f && cap <= 1e5f))) return ZB_ERR_ARG;
     return ZB_OK;
 }
 

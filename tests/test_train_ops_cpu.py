@@ -184,7 +184,7 @@ def test_document_refusals(zblib):
         for kw in (dict(d=96), dict(d=32), dict(nkv=3), dict(nkv=0), dict(t=-1), dict(t=(1 << 24) + 1)):
             refused("ZB_ERR_SHAPE", call, **kw)
         for kw in (dict(qkv=None), dict(a=FAKE + 2), dict(lse=None), dict(p=None), dict(p=FAKE + 8), dict(slopes=FAKE + 2),
-                   dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf"))):
+                   dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")), dict(cap=1e-4), dict(cap=1e6)):
             refused("ZB_ERR_ARG", call, **kw)
     refused("ZB_ERR_ARG", bwd, da=None)
     refused("ZB_ERR_ARG", bwd, dqkv=FAKE + 4)
