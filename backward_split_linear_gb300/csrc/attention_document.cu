@@ -165,7 +165,7 @@ __device__ __forceinline__ float score2(const DocArgs& p, float dot, float slope
 
 // One query row and head by a whole warp: a and lse.
 template <int D>
-__device__ __noinline__ void document_forward_row(const DocArgs& p, int i, int h, int lane) {
+__device__ __forceinline__ void document_forward_row(const DocArgs& p, int i, int h, int lane) {
     const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
     const int g = h / (p.n_heads / p.n_kv_heads);
     const uint16_t* k = p.qkv + (p.n_heads + g) * D;
@@ -250,6 +250,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split_pair(uint64_t r, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // s <- tanh(x), x = s / (cap sqrt(d)), for N columns of a row.  Where all of a
 // warp's |x| are at most 3/4 (scores below 3/4 of the cap, the usual case), an odd
 // polynomial of degree 9 on the FMA pipe, relative error below 6e-7: x P(x^2), P a
@@ -261,16 +281,19 @@ template <int N>
 __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], fabsf(s[c]));
+    for (int c = 0; c < N; c += 2) top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
     if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.cap_rate <= 0.75f)) {
+        uint64_t k[5];
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const float u = s[c] * s[c];
-            float r = fmaf(p.cap_poly[4], u, p.cap_poly[3]);
-            r = fmaf(r, u, p.cap_poly[2]);
-            r = fmaf(r, u, p.cap_poly[1]);
-            r = fmaf(r, u, p.cap_poly[0]);
-            s[c] *= r;
+        for (int e = 0; e < 5; ++e) k[e] = pair_of(p.cap_poly[e], p.cap_poly[e]);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const uint64_t x = pair_of(s[c], s[c + 1]), u = mul_pair(x, x);
+            uint64_t r = fma_pair(k[4], u, k[3]);
+            r = fma_pair(r, u, k[2]);
+            r = fma_pair(r, u, k[1]);
+            r = fma_pair(r, u, k[0]);
+            split_pair(mul_pair(x, r), s[c], s[c + 1]);
         }
     } else {
 #pragma unroll
@@ -278,32 +301,24 @@ __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
     }
 }
 
-// -inf outside the columns [lo, hi) of a row, by selects.  A warp whose rows all
-// see every column skips it, and one side's test when only the other cuts.
-template <int N>
-__device__ __forceinline__ void hide_scores(float (&s)[N], int lo, int hi) {
-    if (!__all_sync(0xffffffffu, hi >= N)) {
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const uint32_t mk = 0u - static_cast<uint32_t>(c < hi);
-            s[c] = __uint_as_float((__float_as_uint(s[c]) & mk) | (0xff800000u & ~mk));
-        }
-    }
-    if (!__all_sync(0xffffffffu, lo <= 0)) {
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const uint32_t mk = 0u - static_cast<uint32_t>(c >= lo);
-            s[c] = __uint_as_float((__float_as_uint(s[c]) & mk) | (0xff800000u & ~mk));
-        }
-    }
+// Bit c: column c of 32 lies in [lo, hi).
+__device__ __forceinline__ uint32_t columns_in(int lo, int hi) {
+    const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
+    const uint32_t below_lo = lo >= 32 ? 0xffffffffu : lo <= 0 ? 0u : (1u << lo) - 1u;
+    return below_hi & ~below_lo;
 }
 
-// Zeros outside [lo, hi): the gradients' form, for N columns from `first` on.
+// `hidden` outside the columns [lo, hi) of a row: a select per element on a bit of
+// one word per 32 columns, for both ends at once.  A warp whose rows all see the 32
+// columns skips them.
 template <int N>
-__device__ __forceinline__ void hide_grads(float* s, int first, int lo, int hi) {
-    if (!__all_sync(0xffffffffu, lo <= first && hi >= first + N)) {
+__device__ __forceinline__ void hide_columns(float* s, int lo, int hi, float hidden) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = keep_if(s[c], (first + c >= lo) & (first + c < hi));
+    for (int b = 0; b < N; b += 32) {
+        const uint32_t in = columns_in(lo - b, hi - b);
+        if (__all_sync(0xffffffffu, in == 0xffffffffu)) continue;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[b + c] = (in & (1u << c)) ? s[b + c] : hidden;
     }
 }
 
@@ -316,32 +331,46 @@ __device__ __forceinline__ int2 block_range(const int2* blocks, int b, int n_blo
 }
 
 __device__ __forceinline__ bool finite32(const float (&v)[32]) {
-    float m = 0.f;  // 0 v is NaN for a v that is not finite
+    float m[4] = {0.f, 0.f, 0.f, 0.f};  // 0 v is NaN for a v that is not finite
 #pragma unroll
-    for (int e = 0; e < 32; ++e) m = fmaf(v[e], 0.f, m);
-    return m == 0.f;
+    for (int e = 0; e < 32; ++e) m[e & 3] = fmaf(v[e], 0.f, m[e & 3]);
+    return (m[0] + m[1]) + (m[2] + m[3]) == 0.f;
 }
 
-// 32 bytes of one row in one instruction: the lanes of a warp store to 32 rows, and
-// each row costs the store unit a pass, however few of its bytes are written.
-__device__ __forceinline__ void store_bytes32(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-__device__ __forceinline__ void store32(uint16_t* dst, const float (&v)[32], float f) {
+// Results leave through shared memory and TMA: a warp packs 32 rows of 64 columns
+// into 4 KiB (128-byte rows, 128-byte swizzle; 64-byte rows have theirs) and one
+// thread stores the box, rows behind the tensor clipped.  Stored from registers, each lane to its own row, a
+// tile's results held its warps for about 5000 cycles, three passes over its keys;
+// the copy runs beside the next tile's work.
+constexpr uint32_t kStageBytes = 4096;
+template <int kRowBytes = 128>
+__device__ __forceinline__ void stage32(uint32_t stage, int lane, int half, const float (&v)[32], float f, bool zero) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(v[16 * k + 2 * e] * f, v[16 * k + 2 * e + 1] * f);
-        store_bytes32(dst + 16 * k, w);
+    for (int k = 0; k < 4; ++k) {
+        uint4 w = make_uint4(pack_bf16x2(v[8 * k] * f, v[8 * k + 1] * f), pack_bf16x2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                             pack_bf16x2(v[8 * k + 4] * f, v[8 * k + 5] * f), pack_bf16x2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+        if (zero) w = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t at = static_cast<uint32_t>(lane * kRowBytes + (4 * half + k) * 16);
+        st_shared_v4(stage + (at ^ (((at >> 7) & (kRowBytes / 16 - 1)) << 4)), w);
     }
 }
-__device__ __forceinline__ void store32_zero(uint16_t* dst) {
-    const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    store_bytes32(dst, zero);
-    store_bytes32(dst + 16, zero);
+__device__ __forceinline__ void store_stage(const CUtensorMap* map, uint32_t stage, int lane, int col, int row) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(map, stage, col, row);
+        bulk_commit_group();
+    }
+}
+// The stage may be written again: its last store has read it.
+__device__ __forceinline__ void stage_free(int lane) {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+}
+// This warp's stores have been written, before some of their rows are written again.
+__device__ __forceinline__ void stores_done(int lane) {
+    if (lane == 0) bulk_wait_group_all();
+    __syncwarp();
 }
 
 __device__ __forceinline__ void load_tmem32(uint32_t t, float (&v)[32]) {
@@ -353,6 +382,17 @@ __device__ __forceinline__ void load_tmem32(uint32_t t, float (&v)[32]) {
 }
 
 // ------------------------------------------------------------------------ forward
+
+// Every warp of a warpgroup takes part.  A claim waits until the releases of the
+// other warpgroups of the block have made room.
+template <int N>
+__device__ __forceinline__ void registers_release() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_claim() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Cancels the launch of the next CTA of the grid that has not started and
 // writes its place to `slot` (16 bytes), completing on `bar`: the CTA takes that
@@ -426,14 +466,15 @@ struct DocFwdSmem {
     static constexpr uint32_t kTile = D * 256;
     static constexpr uint32_t kQ = 0;           // Q of tile A, then Q of tile B
     static constexpr uint32_t kKV = 2 * kTile;  // stage s: K at kKV + 2 s kTile, V after it
-    static constexpr uint32_t kAnswer = kKV + 2 * kStages * kTile;  // 16 bytes
+    static constexpr uint32_t kStage = kKV + 2 * kStages * kTile;  // results, 4 KiB a row warp
+    static constexpr uint32_t kAnswer = kStage + 8 * kStageBytes;   // 16 bytes
     static constexpr uint32_t kBars = kAnswer + 16;
     // Q full / empty, the K / V ring, S, P and done of both tiles, tile slots full / empty, answer, drain
     static constexpr int kNumBars = 2 + 2 * kStages + 6 + 4 + 2;
     static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
     static constexpr uint32_t kTileSlot = kTmemSlot + 16;  // two slots of a tile's number, first key block and steps
-    static constexpr uint32_t kRowSlot = kTileSlot + 2 * 16;  // and of its rows' intervals, 1 KiB a tile
-    static constexpr size_t kUsed = kRowSlot + 2 * 2 * 1024;
+    static constexpr uint32_t kRowSlot = kTileSlot + 2 * 16;  // and of its rows' intervals
+    static constexpr size_t kUsed = kRowSlot + 2 * 1024;
     static constexpr size_t kBytes = kUsed > kMinSmem ? kUsed : kMinSmem;
 };
 
@@ -442,9 +483,18 @@ struct DocFwdSmem {
 // the next, and the next tile's Q loads as soon as the last scores of the
 // current one are formed, while its softmax, last product and stores run.  A
 // tile that sees nothing (padding) has no steps.
+//
+// Three warpgroups: warp 0 loads, warp 1 issues products (warps 2 and 3 only hold
+// their place), warps 4-7 and 8-11 are the softmax rows of tiles A and B.  The
+// first hands registers to the other two.
+constexpr int kDocFwdThreads = 384;
+constexpr int kDocFwdFew = 56, kDocFwdMany = 224;
+static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * 168, "registers of the launch: 168 a thread");
+
 template <int D, int M>
-__global__ void __launch_bounds__(kAttnBwdThreads, 1)
-    document_fwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ DocArgs p) {
+__global__ void __launch_bounds__(kDocFwdThreads, 1)
+    document_fwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ DocArgs p) {
     using L = DocFwdSmem<D>;
     constexpr int NS = L::kStages;
     constexpr uint32_t kTile = L::kTile;
@@ -505,16 +555,19 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     auto take_tile = [&](uint32_t n, FwdTile& f, int x, int row, int2& see) {
         if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
         const int4 slot = tile_slot[n & 1u];
-        see = row_slot[((n & 1u) * 2 + x) * kRows + row];
+        see = row_slot[(n & 1u) * kRows + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(tile_empty(n & 1u));
         if (slot.x < 0) return false;
         f = fwd_place(p, slot.x);
         f.first = slot.y;
         f.nk = slot.z;
+        if (f.q0[x] != f.q0[0]) see = f.q0[x] < p.n_blocks * kRows ? p.plan.rows[f.q0[x] + row] : make_int2(0, 0);
         return true;
     };
 
+    if (warp < 4) {
+    registers_release<kDocFwdFew>();
     if (warp == 0) {
         if (lane == 0) {
             uint32_t nq = 0, nkv = 0, nt = 0;  // Q loads, K / V steps and tile slots issued
@@ -528,12 +581,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                     mbar_arrive(tile_full(n & 1u));
                     break;
                 }
-                // the intervals of the tiles' rows land on the same barrier
-                const uint32_t rows = base + L::kRowSlot + 2048u * (n & 1u);
-                const bool two = f.q0[1] < p.n_blocks * kRows;  // tile B may lie behind the last block
-                mbar_arrive_expect_tx(tile_full(n & 1u), two ? 2048 : 1024);
-                bulk_load_1d(rows, p.plan.rows + f.q0[0], 1024, tile_full(n & 1u));
-                if (two) bulk_load_1d(rows + 1024, p.plan.rows + f.q0[1], 1024, tile_full(n & 1u));
+                // the intervals of tile A's rows land on the same barrier (tile B's own rows,
+                // in odd groups, are read where they are needed)
+                mbar_arrive_expect_tx(tile_full(n & 1u), 1024);
+                bulk_load_1d(base + L::kRowSlot + 1024u * (n & 1u), p.plan.rows + f.q0[0], 1024, tile_full(n & 1u));
                 if (f.nk > 0) {
                     // Q once the previous tile's scores are formed
                     if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
@@ -646,9 +697,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         }
         umma_commit_elected(leader, drain);
         mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    }
     } else {
-        // ---------------- softmax rows: warps 2-5 tile A, warps 6-9 tile B
-        const int x = (warp - 2) >> 2;
+        registers_claim<kDocFwdMany>();
+        // ---------------- softmax rows: warps 4-7 tile A, warps 8-11 tile B
+        const int x = (warp - 4) >> 2;
         const int qw = warp & 3;
         const int row = qw * 32 + lane;
         const uint32_t t_row = static_cast<uint32_t>(qw * 32) << 16;
@@ -697,7 +750,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                     for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], mul, -slope2 * fabsf(static_cast<float>(c) - at));
                     sc = 1.f;
                 }
-                hide_scores(s, see.x - k0, see.y - k0);
+                hide_columns<128>(s, see.x - k0, see.y - k0, -INFINITY);
                 // eight running maxima and sums, not one chain of 128 dependent operations
                 float mx8[8];
 #pragma unroll
@@ -747,37 +800,40 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                 warp_arrive(p_full(x), lane);
             }
             if (!ok) break;
-            uint16_t* dst = p.out + (static_cast<int64_t>(q) * p.n_heads + h) * D;
             bool again = false;  // not finite: formed again below
+            float inv = 0.f;
             if (f.nk > 0) {
                 if (!warp_wait(done(x), nd & 1u, p.status)) break;
                 ++nd;
                 tc_fence_after();
-                const float inv = 1.f / l;
+                inv = 1.f / l;
                 again = !(fabsf(inv) <= 3e38f);
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    load_tmem32(to + t_row + 32 * c, o);
-                    again |= !finite32(o);
-                    if (valid && !empty) store32(dst + 32 * c, o, inv);
-                }
-                tc_fence_before();
             }
-            if (valid) {
-                if (empty)
+            const uint32_t stage = base + L::kStage + kStageBytes * static_cast<uint32_t>(warp - 4);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) store32_zero(dst + 32 * c);
-                p.lse_out[static_cast<int64_t>(h) * p.ld_stat + q] = empty ? -INFINITY : m + lg2(l);
+            for (int c = 0; c < D / 64; ++c) {
+                float o[2][32] = {};
+                if (f.nk > 0) {
+                    load_tmem32(to + t_row + 64 * c, o[0]);
+                    load_tmem32(to + t_row + 64 * c + 32, o[1]);
+                    again |= !finite32(o[0]) || !finite32(o[1]);
+                }
+                stage_free(lane);
+                stage32(stage, lane, 0, o[0], inv, empty);
+                stage32(stage, lane, 1, o[1], inv, empty);
+                if (q - lane < p.tokens) store_stage(&map_a, stage, lane, h * D + 64 * c, q - lane);
             }
+            tc_fence_before();
+            if (valid) p.lse_out[static_cast<int64_t>(h) * p.ld_stat + q] = empty ? -INFINITY : m + lg2(l);
             uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
+            if (redo) stores_done(lane);
             while (redo) {
                 const int src = __ffs(redo) - 1;
                 redo &= redo - 1;
-                __syncwarp();  // the row's first results are written before they are written over
                 document_forward_row<D>(p, q - lane + src, h, lane);
             }
         }
+        stage_free(lane);  // shared memory outlives the stores that read it
     }
 
     tc_fence_before();
@@ -794,14 +850,17 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 // by warp 10, two groups of row warps with 64 key columns each.
 template <int D>
 struct DocDqSmem {
-    static constexpr int kKStages = 3, kVStages = 2;
+    // One V stage where the results' 32 KiB leave no room for two: V[g + 1] lands while
+    // the row warps still turn dP[g] into dS[g].
+    static constexpr int kKStages = 3, kVStages = D == 64 ? 2 : 1;
     static constexpr uint32_t kTile = D * 256;
     static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile;
     static constexpr uint32_t kV = kK + kKStages * kTile;
-    static constexpr uint32_t kBars = kV + kVStages * kTile;
-    // q full / empty, the K ring (full, empty), the V ring (empty), S (2), dP,
+    static constexpr uint32_t kStage = kV + kVStages * kTile;  // results, 4 KiB a row warp
+    static constexpr uint32_t kBars = kStage + 8 * kStageBytes;
+    // q full / empty, the K ring (full, empty), the V ring (full, empty), S (2), dP,
     // dS (2), done, drain, the two tile slots (full, empty), dQ issued (2), dP issued (2)
-    static constexpr int kNumBars = 2 + 2 * kKStages + kVStages + 2 + 5 + 4 + 4;
+    static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 2 + 5 + 4 + 4;
     static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
     static constexpr uint32_t kTileSlot = kTmemSlot + 8;  // the tile number held by each slot (two ints)
     static constexpr size_t kUsed = kTileSlot + 8;
@@ -822,19 +881,21 @@ __device__ __forceinline__ DqTile dq_tile(const DocArgs& p, int t) {
 }
 
 template <int D, int M>
-__device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CUtensorMap& map_do, const DocArgs& p,
-                                            uint8_t* smem_raw) {
+__device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CUtensorMap& map_do, const CUtensorMap& map_dq,
+                                            const DocArgs& p, uint8_t* smem_raw) {
     using L = DocDqSmem<D>;
     constexpr int NK = L::kKStages, NV = L::kVStages;
     constexpr uint32_t kTile = L::kTile;
     const uint32_t base = smem_addr(smem_raw);
-    const uint32_t s_q = base + L::kQ, s_do = base + L::kDO, s_k = base + L::kK, s_v = base + L::kV;
+    const uint32_t s_q = base + L::kQ, s_do = base + L::kDO, s_k = base + L::kK, s_v = base + L::kV,
+                   s_stage = base + L::kStage;
     const uint32_t bars = base + L::kBars;
     const uint32_t q_full = bars, q_empty = bars + 8u;
     auto k_full = [&](uint32_t s) { return bars + 8u * (2 + s); };
     auto k_empty = [&](uint32_t s) { return bars + 8u * (2 + NK + s); };
-    auto v_empty = [&](uint32_t s) { return bars + 8u * (2 + 2 * NK + s); };
-    constexpr int kB = 2 + 2 * NK + NV;
+    auto v_full = [&](uint32_t s) { return bars + 8u * (2 + 2 * NK + s); };
+    auto v_empty = [&](uint32_t s) { return bars + 8u * (2 + 2 * NK + NV + s); };
+    constexpr int kB = 2 + 2 * NK + 2 * NV;
     auto s_full = [&](uint32_t b) { return bars + 8u * (kB + b); };
     const uint32_t dp_full = bars + 8u * (kB + 2), done = bars + 8u * (kB + 3), drain = bars + 8u * (kB + 4);
     auto ds_full = [&](uint32_t g) { return bars + 8u * (kB + 5 + (g & 1u)); };
@@ -857,7 +918,10 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             mbar_init(k_full(s), 1);
             mbar_init(k_empty(s), 1);
         }
-        for (int s = 0; s < NV; ++s) mbar_init(v_empty(s), 1);
+        for (int s = 0; s < NV; ++s) {
+            mbar_init(v_full(s), 1);
+            mbar_init(v_empty(s), 1);
+        }
         mbar_init(s_full(0), 1);
         mbar_init(s_full(1), 1);
         mbar_init(dp_full, 1);
@@ -901,7 +965,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 mbar_arrive(tile_full(n & 1u));
                 return t;
             };
-            uint32_t nq = 0, nkf = 0;  // Q / dO loads and K / V steps issued
+            uint32_t nq = 0, nkf = 0, nvf = 0;  // Q / dO, K and V loads issued
             int t = fetch(0);
             for (uint32_t n = 0; t >= 0; ++n) {
                 const DqTile tl = dq_tile(p, t);
@@ -918,13 +982,14 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 int t_next = tl.nk > 0 ? -2 : fetch(n + 1);
                 for (int j = 0; j < tl.nk; ++j) {
                     const uint32_t u = nkf;
-                    // K[j] and V[j] land on one barrier: one wait per step for the MMA warp
                     if (!mbar_wait_fast(k_empty(u % NK), ((u / NK) & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                    if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                    mbar_arrive_expect_tx(k_full(u % NK), 2 * kTile);
+                    mbar_arrive_expect_tx(k_full(u % NK), kTile);
                     load_tile<D>(s_k + (u % NK) * kTile, &map_qkv, k_full(u % NK), kcol, (tl.kb0 + j) * kRows);
-                    load_tile<D>(s_v + (u % NV) * kTile, &map_qkv, k_full(u % NK), vcol, (tl.kb0 + j) * kRows);
                     ++nkf;
+                    if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(v_full(u % NV), kTile);
+                    load_tile<D>(s_v + (u % NV) * kTile, &map_qkv, v_full(u % NV), vcol, (tl.kb0 + j) * kRows);
+                    ++nvf;
                     // the next tile's number at this tile's last load, and its Q and dO into L2
                     if (j == tl.nk - 1) {
                         t_next = fetch(n + 1);
@@ -942,6 +1007,10 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             for (int s = 0; s < NK; ++s) {
                 const uint32_t u = ring_uses(nkf, NK, s);
                 if (u > 0) mbar_wait_fast(k_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+            }
+            for (int s = 0; s < NV; ++s) {
+                const uint32_t u = ring_uses(nvf, NV, s);
+                if (u > 0) mbar_wait_fast(v_full(s), (u - 1) & 1u, p.status, kSiteDrain);
             }
         }
     } else if (warp == 1) {
@@ -961,13 +1030,16 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             return true;
         };
         auto issue_dp = [&](uint32_t g) {
-            const uint32_t st = g % NV;  // V[g] landed with K[g] (issue_s(g) waited for both)
+            const uint32_t st = g % NV;
+            if (!warp_wait(v_full(st), (g / NV) & 1u, p.status)) return false;
+            tc_fence_after();
             const uint64_t v_desc = kdesc_base(s_v + st * kTile);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 umma_bf16_elected(leader, t_dp, kdesc_at(do_desc, kk), kdesc_at(v_desc, kk), idesc_s, kk > 0);
             umma_commit_elected(leader, dp_full);
             umma_commit_elected(leader, v_empty(st));
+            return true;
         };
         // S[g] overwrites the S buffer of step g - 2 once the dQ warp has issued
         // dQ[g - 2], which reads dS[g - 2] from it; dP[g] overwrites dP[g - 1]
@@ -996,11 +1068,10 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             tc_fence_after();
             // the MMA order per step is S[g+1], dP[g+1] (here) beside dQ[g] (the dQ warp)
             for (int j = 0; j < nk; ++j, ++g) {
-                if (!may_issue_s(g) || !issue_s(g) || !may_issue_dp(g)) {
+                if (!may_issue_s(g) || !issue_s(g) || !may_issue_dp(g) || !issue_dp(g)) {
                     ok = false;
                     break;
                 }
-                issue_dp(g);
                 tc_fence_before();
                 if (leader) mbar_arrive(dp_issued(g));
                 // Q and dO are free for the next tile once its last S and dP are done
@@ -1107,7 +1178,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
 #pragma unroll
                 for (int i = 0; i < 64; ++i) pr[i] *= __uint_as_float(rp[i]) - dv;
                 // hidden pairs last: their P or dP may be anything
-                hide_grads<64>(pr, 0, see.x - c0, see.y - c0);
+                hide_columns<64>(pr, see.x - c0, see.y - c0, 0.f);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t w[16];
@@ -1124,34 +1195,33 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             // group gi stores dQ columns [D/2 gi, D/2 (gi + 1)); the tile's next
             // dQ product waits for this group's next dS arrival, after these loads
             constexpr int kChunks = D / 64;  // 32-column chunks of this group's half
-            uint16_t* dst = p.out + static_cast<int64_t>(q) * ((p.n_heads + 2 * p.n_kv_heads) * D) + tl.h * D;
+            const uint32_t stage = s_stage + kStageBytes * static_cast<uint32_t>(warp - 2);
             bool again = false;
+            float r[kChunks][32] = {};
             if (tl.nk > 0) {
                 if (!warp_wait(done, nd & 1u, p.status)) break;
                 ++nd;
                 tc_fence_after();
                 const uint32_t t_q = t_dq + (static_cast<uint32_t>(qw * 32) << 16) + 32u * (gi * kChunks);
-                float r[kChunks][32];
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) load_tmem32(t_q + 32 * c, r[c]);
                 tc_fence_before();
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    again |= !finite32(r[c]);
-                    if (valid && !empty) store32(dst + 32 * (gi * kChunks + c), r[c], p.scale);
-                }
+                for (int c = 0; c < kChunks; ++c) again |= !finite32(r[c]);
             }
-            if (valid && empty)
+            stage_free(lane);
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) store32_zero(dst + 32 * (gi * kChunks + c));
+            for (int c = 0; c < kChunks; ++c) stage32<D>(stage, lane, c, r[c], p.scale, empty);
+            if (q - lane < p.tokens) store_stage(&map_dq, stage, lane, tl.h * D + gi * (D / 2), q - lane);
             uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
+            if (redo) stores_done(lane);
             while (redo) {
                 const int src = __ffs(redo) - 1;
                 redo &= redo - 1;
-                __syncwarp();
                 document_dq_row<D>(p, q - lane + src, tl.h, lane, gi * (D / 2), (gi + 1) * (D / 2));
             }
         }
+        stage_free(lane);  // shared memory outlives the stores that read it
     }
 
     tc_fence_before();
@@ -1189,8 +1259,8 @@ constexpr size_t doc_bwd_smem() {
 }
 
 template <int D, int M>
-__device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const CUtensorMap& map_do, const DocArgs& p,
-                                             uint8_t* smem_raw) {
+__device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const CUtensorMap& map_do, const CUtensorMap& map_out,
+                                             const DocArgs& p, uint8_t* smem_raw) {
     using L = DocDkvSmem<D>;
     constexpr int NQ = L::kQStages, ND = L::kDoStages, NT = L::kStatStages, NA = L::kAugStages;
     constexpr uint32_t kTile = L::kTile;
@@ -1475,7 +1545,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                         }
                     }
                 }
-                hide_grads<32>(pr + 32 * c, 32 * c, lo, hi);
+                hide_columns<32>(pr + 32 * c, lo - 32 * c, hi - 32 * c, 0.f);
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
@@ -1503,7 +1573,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 float ds[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) ds[j] = pr[32 * c + j] * __uint_as_float(rp[32 * c + j]);
-                hide_grads<32>(ds, 32 * c, lo, hi);  // a hidden column's dP may be anything
+                hide_columns<32>(ds, lo - 32 * c, hi - 32 * c, 0.f);  // a hidden column's dP may be anything
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(ds[2 * e], ds[2 * e + 1]);
@@ -1517,24 +1587,28 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
         if (ok && warp_wait(done, 0, p.status)) {
             tc_fence_after();
             const uint32_t t_acc = (gi == 0 ? t_dk : t_dv) + (static_cast<uint32_t>(qw * 32) << 16);
-            uint16_t* dst = p.out + k * width + (gi == 0 ? kcol : vcol);
             const float sc = gi == 0 ? p.scale : 1.f;
+            // every product has been formed: the Q stages serve the results, D / 64 boxes a warp
+            const uint32_t stage = s_q + kStageBytes * static_cast<uint32_t>((warp - 2) * (D / 64));
             bool again = false;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                float r[32];
-                load_tmem32(t_acc + 32 * c, r);
-                again |= !finite32(r);
-                if (valid && !empty) store32(dst + 32 * c, r, sc);
-                if (valid && empty) store32_zero(dst + 32 * c);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                float r[2][32];
+                load_tmem32(t_acc + 64 * c, r[0]);
+                load_tmem32(t_acc + 64 * c + 32, r[1]);
+                again |= !finite32(r[0]) || !finite32(r[1]);
+                stage32(stage + c * kStageBytes, lane, 0, r[0], sc, empty);
+                stage32(stage + c * kStageBytes, lane, 1, r[1], sc, empty);
+                if (k - lane < p.tokens) store_stage(&map_out, stage + c * kStageBytes, lane, (gi == 0 ? kcol : vcol) + 64 * c, k - lane);
             }
             uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
+            if (redo) stores_done(lane);
             while (redo) {
                 const int src = __ffs(redo) - 1;
                 redo &= redo - 1;
-                __syncwarp();
                 document_dkv_row<D>(p, k - lane + src, g, lane, gi == 1);
             }
+            stage_free(lane);  // shared memory outlives the stores that read it
         }
     }
 
@@ -1553,6 +1627,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
 template <int D, int M>
 __global__ void __launch_bounds__(kAttnDqThreads, 1)
     document_bwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ CUtensorMap map_do,
+                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_dq,
                         const __grid_constant__ DocArgs p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if (smem_addr(smem_raw) & 1023u) {  // the tiles' 128-byte swizzle needs a 1 KiB-aligned start
@@ -1560,9 +1635,9 @@ __global__ void __launch_bounds__(kAttnDqThreads, 1)
         return;
     }
     if (static_cast<int>(blockIdx.x) < p.n_blocks * p.n_kv_heads)
-        document_dkv<D, M>(map_qkv, map_do, p, smem_raw);
+        document_dkv<D, M>(map_qkv, map_do, map_out, p, smem_raw);
     else
-        document_dq<D, M>(map_qkv, map_do, p, smem_raw);
+        document_dq<D, M>(map_qkv, map_do, map_dq, p, smem_raw);
 }
 
 DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const float* slopes, float cap) {
@@ -1598,10 +1673,11 @@ cudaError_t forward(const DocArgs& p, cudaStream_t stream) {
     std::call_once(once, [] { err = set_smem(document_fwd_kernel<D, M>, DocFwdSmem<D>::kBytes); });
     if (err != cudaSuccess) return err;
     const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
-    CUtensorMap map;
-    if (!attn_map(&map, p.qkv, p.tokens, width, width)) return cudaErrorInvalidValue;
+    CUtensorMap map, out;
+    if (!attn_map(&map, p.qkv, p.tokens, width, width) || !attn_map(&out, p.out, p.tokens, p.n_heads * D, p.n_heads * D, 32))
+        return cudaErrorInvalidValue;
     const int64_t tiles = static_cast<int64_t>(fwd_tiles(p));
-    document_fwd_kernel<D, M><<<static_cast<unsigned>(tiles), kAttnBwdThreads, DocFwdSmem<D>::kBytes, stream>>>(map, p);
+    document_fwd_kernel<D, M><<<static_cast<unsigned>(tiles), kDocFwdThreads, DocFwdSmem<D>::kBytes, stream>>>(map, out, p);
     return cudaGetLastError();
 }
 
@@ -1612,8 +1688,9 @@ cudaError_t backward(const DocArgs& p, const uint16_t* a, float* dvec, bool d_re
     std::call_once(once, [] { err = set_smem(document_bwd_kernel<D, M>, doc_bwd_smem<D>()); });
     if (err != cudaSuccess) return err;
     const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
-    CUtensorMap mq, md;
-    if (!attn_map(&mq, p.qkv, p.tokens, width, width) || !attn_map(&md, p.da, p.tokens, p.n_heads * D, p.n_heads * D))
+    CUtensorMap mq, md, mo, mdq;  // dq leaves in boxes of half a head
+    if (!attn_map(&mq, p.qkv, p.tokens, width, width) || !attn_map(&md, p.da, p.tokens, p.n_heads * D, p.n_heads * D) ||
+        !attn_map(&mo, p.out, p.tokens, width, width, 32) || !attn_map(&mdq, p.out, p.tokens, width, width, 32, D / 2))
         return cudaErrorInvalidValue;
     if (d_ready) {
         const cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream);
@@ -1627,7 +1704,7 @@ cudaError_t backward(const DocArgs& p, const uint16_t* a, float* dvec, bool d_re
     }
     const int64_t dkv = static_cast<int64_t>(p.n_blocks) * p.n_kv_heads;
     const int64_t dq = std::min<int64_t>(static_cast<int64_t>(p.n_blocks) * p.n_heads, sm_count());
-    document_bwd_kernel<D, M><<<static_cast<unsigned>(dkv + dq), kAttnDqThreads, doc_bwd_smem<D>(), stream>>>(mq, md, p);
+    document_bwd_kernel<D, M><<<static_cast<unsigned>(dkv + dq), kAttnDqThreads, doc_bwd_smem<D>(), stream>>>(mq, md, mo, mdq, p);
     return cudaGetLastError();
 }
 
