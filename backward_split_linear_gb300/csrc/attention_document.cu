@@ -264,6 +264,11 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -298,6 +303,18 @@ __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
     } else {
 #pragma unroll
         for (int c = 0; c < N; ++c) s[c] = 1.f - __fdividef(2.f, 1.f + ex2(s[c] * p.cap_exp));
+    }
+}
+
+// s <- mul s - slope |c - at| for N columns c of a row.
+template <int N>
+__device__ __forceinline__ void bias_scores(float* s, float mul, float slope, float at) {
+    const uint64_t mul2 = pair_of(mul, mul), step2 = pair_of(-slope, -slope), at2 = pair_of(-at, -at);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        float a, b;
+        split_pair(add_pair(pair_of(static_cast<float>(c), static_cast<float>(c + 1)), at2), a, b);
+        split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, mul_pair(step2, pair_of(fabsf(a), fabsf(b)))), s[c], s[c + 1]);
     }
 }
 
@@ -746,8 +763,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 }
                 if (M == kDocBias || (M == kDocCap && p.slopes)) {
                     const float mul = M == kDocBias ? p.scale_log2 : p.cap_log2, at = static_cast<float>(q - k0);
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = fmaf(s[c], mul, -slope2 * fabsf(static_cast<float>(c) - at));
+                    bias_scores<128>(s, mul, slope2, at);
                     sc = 1.f;
                 }
                 hide_columns<128>(s, see.x - k0, see.y - k0, -INFINITY);
@@ -781,20 +797,25 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     }
                     m = m_new;
                 }
-                float sum8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pair_of(sc, sc), m2 = pair_of(-m, -m);
+                uint64_t sum[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float a = ex2(fmaf(s[32 * c + 2 * e], sc, -m));
-                        const float b = ex2(fmaf(s[32 * c + 2 * e + 1], sc, -m));
-                        sum8[e & 7] += a + b;
+                        float a, b;
+                        split_pair(fma_pair(pair_of(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, m2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[e & 3] = add_pair(sum[e & 3], pair_of(a, b));
                         w[e] = pack_bf16x2(a, b);  // P to bf16: the tensor cores' operand; l sums it unrounded
                     }
                     tmem_store_16(ts + t_row + 16 * c, w);
                 }
-                l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+                float la, lb;
+                split_pair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])), la, lb);
+                l += la + lb;
                 tmem_wait_store();
                 tc_fence_before();
                 warp_arrive(p_full(x), lane);
