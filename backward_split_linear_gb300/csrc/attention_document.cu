@@ -318,6 +318,42 @@ __device__ __forceinline__ void bias_scores(float* s, float mul, float slope, fl
     }
 }
 
+// s <- 2^(mul s - slope |c - at| + add) for N columns.
+template <bool kSlope, int N>
+__device__ __forceinline__ void exp_scores(float* s, float mul, float slope, float at, float add) {
+    const uint64_t mul2 = pair_of(mul, mul), add2 = pair_of(add, add), step2 = pair_of(-slope, -slope), at2 = pair_of(-at, -at);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        uint64_t rest = add2;
+        float a, b;
+        if (kSlope) {
+            split_pair(add_pair(pair_of(static_cast<float>(c), static_cast<float>(c + 1)), at2), a, b);
+            rest = fma_pair(step2, pair_of(fabsf(a), fabsf(b)), add2);
+        }
+        split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest), a, b);
+        s[c] = ex2(a);
+        s[c + 1] = ex2(b);
+    }
+}
+// s <- s (v + add), and s <- s (1 - t^2).
+template <int N>
+__device__ __forceinline__ void times_sum(float* s, const uint32_t* v, float add) {
+    const uint64_t add2 = pair_of(add, add);
+#pragma unroll
+    for (int c = 0; c < N; c += 2)
+        split_pair(mul_pair(pair_of(s[c], s[c + 1]), add_pair(pair_of(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), add2)),
+                   s[c], s[c + 1]);
+}
+template <int N>
+__device__ __forceinline__ void times_cap_slope(float* s, const float* t) {
+    const uint64_t one2 = pair_of(1.f, 1.f), minus2 = pair_of(-1.f, -1.f);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const uint64_t x = pair_of(t[c], t[c + 1]);
+        split_pair(mul_pair(pair_of(s[c], s[c + 1]), fma_pair(mul_pair(x, minus2), x, one2)), s[c], s[c + 1]);
+    }
+}
+
 // Bit c: column c of 32 lies in [lo, hi).
 __device__ __forceinline__ uint32_t columns_in(int lo, int hi) {
     const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -584,137 +620,137 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     };
 
     if (warp < 4) {
-    registers_release<kDocFwdFew>();
-    if (warp == 0) {
-        if (lane == 0) {
-            uint32_t nq = 0, nkv = 0, nt = 0;  // Q loads, K / V steps and tile slots issued
-            int t = static_cast<int>(blockIdx.x);
-            for (uint32_t n = 0;; ++n) {
-                if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                const FwdTile f = t >= 0 ? fwd_tile(p, t) : FwdTile{};
-                *reinterpret_cast<int4*>(smem_raw + L::kTileSlot + 16 * (n & 1u)) = make_int4(t, f.first, f.nk, 0);
-                ++nt;
-                if (t < 0) {
-                    mbar_arrive(tile_full(n & 1u));
-                    break;
+        registers_release<kDocFwdFew>();
+        if (warp == 0) {
+            if (lane == 0) {
+                uint32_t nq = 0, nkv = 0, nt = 0;  // Q loads, K / V steps and tile slots issued
+                int t = static_cast<int>(blockIdx.x);
+                for (uint32_t n = 0;; ++n) {
+                    if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    const FwdTile f = t >= 0 ? fwd_tile(p, t) : FwdTile{};
+                    *reinterpret_cast<int4*>(smem_raw + L::kTileSlot + 16 * (n & 1u)) = make_int4(t, f.first, f.nk, 0);
+                    ++nt;
+                    if (t < 0) {
+                        mbar_arrive(tile_full(n & 1u));
+                        break;
+                    }
+                    // the intervals of tile A's rows land on the same barrier (tile B's own rows,
+                    // in odd groups, are read where they are needed)
+                    mbar_arrive_expect_tx(tile_full(n & 1u), 1024);
+                    bulk_load_1d(base + L::kRowSlot + 1024u * (n & 1u), p.plan.rows + f.q0[0], 1024, tile_full(n & 1u));
+                    if (f.nk > 0) {
+                        // Q once the previous tile's scores are formed
+                        if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                        mbar_arrive_expect_tx(q_full, 2 * kTile);
+                        load_tile<D>(s_q, &map_qkv, q_full, f.h[0] * D, f.q0[0]);
+                        load_tile<D>(s_q + kTile, &map_qkv, q_full, f.h[1] * D, f.q0[1]);
+                        ++nq;
+                    }
+                    const int kcol = (p.n_heads + f.g) * D, vcol = (p.n_heads + p.n_kv_heads + f.g) * D;
+                    bool ok = true;
+                    for (int j = 0; j < f.nk; ++j) {
+                        const uint32_t st = nkv % NS;
+                        if (!mbar_wait_fast(kv_empty(st), ((nkv / NS) & 1u) ^ 1u, p.status, kSiteAttn)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(kv_full(st), 2 * kTile);
+                        const int k0 = (f.first + j) * kRows;
+                        load_tile<D>(s_kv + 2 * st * kTile, &map_qkv, kv_full(st), kcol, k0);
+                        load_tile<D>(s_kv + (2 * st + 1) * kTile, &map_qkv, kv_full(st), vcol, k0);
+                        ++nkv;
+                    }
+                    if (!ok) break;
+                    // the next tile's number after this tile's last load, a ring's depth before its end
+                    mbar_arrive_expect_tx(answer_full, 16);
+                    next_cta_request(s_answer, answer_full);
+                    if (!mbar_wait_fast(answer_full, n & 1u, p.status, kSiteAttn)) break;
+                    t = next_cta_answer(s_answer);
+                    fence_proxy_async_smem();  // the answer is read before another one is written over it
+                    if (t >= 0) {
+                        const FwdTile nx = fwd_tile(p, t);
+                        prefetch_tile<D>(&map_qkv, nx.h[0] * D, nx.q0[0]);
+                        if (nx.q0[1] < p.tokens) prefetch_tile<D>(&map_qkv, nx.h[1] * D, nx.q0[1]);
+                    }
                 }
-                // the intervals of tile A's rows land on the same barrier (tile B's own rows,
-                // in odd groups, are read where they are needed)
-                mbar_arrive_expect_tx(tile_full(n & 1u), 1024);
-                bulk_load_1d(base + L::kRowSlot + 1024u * (n & 1u), p.plan.rows + f.q0[0], 1024, tile_full(n & 1u));
-                if (f.nk > 0) {
-                    // Q once the previous tile's scores are formed
-                    if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                    mbar_arrive_expect_tx(q_full, 2 * kTile);
-                    load_tile<D>(s_q, &map_qkv, q_full, f.h[0] * D, f.q0[0]);
-                    load_tile<D>(s_q + kTile, &map_qkv, q_full, f.h[1] * D, f.q0[1]);
-                    ++nq;
+                // no copy may land after the CTA has gone
+                if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
+                for (int s = 0; s < NS; ++s) {
+                    const uint32_t u = ring_uses(nkv, NS, s);
+                    if (u > 0) mbar_wait_fast(kv_full(s), (u - 1) & 1u, p.status, kSiteDrain);
                 }
-                const int kcol = (p.n_heads + f.g) * D, vcol = (p.n_heads + p.n_kv_heads + f.g) * D;
-                bool ok = true;
-                for (int j = 0; j < f.nk; ++j) {
-                    const uint32_t st = nkv % NS;
-                    if (!mbar_wait_fast(kv_empty(st), ((nkv / NS) & 1u) ^ 1u, p.status, kSiteAttn)) {
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t u = ring_uses(nt, 2, s);
+                    if (u > 0) mbar_wait_fast(tile_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+                }
+            }
+        } else if (warp == 1) {
+            // the whole warp runs the issue loop; its elected lane carries each instruction
+            const uint32_t leader = elect_one_sync();
+            constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
+            constexpr uint32_t idesc_o = mma_idesc_bf16(128, D, false, true);
+            auto issue_s = [&](int x, uint32_t g) {
+                const uint64_t a_desc = kdesc_base(s_q + static_cast<uint32_t>(x) * kTile),
+                               b_desc = kdesc_base(s_kv + 2 * (g % NS) * kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16_elected(leader, t_s(x), kdesc_at(a_desc, kk), kdesc_at(b_desc, kk), idesc_s, kk > 0);
+                umma_commit_elected(leader, s_full(x));
+            };
+            auto issue_pv = [&](int x, uint32_t g, bool first) {
+                if (!warp_wait(p_full(x), g & 1u, p.status)) return false;
+                tc_fence_after();
+                const uint64_t v_desc = mndesc_base(s_kv + (2 * (g % NS) + 1) * kTile);
+#pragma unroll
+                for (int kk = 0; kk < kRows / 16; ++kk)
+                    umma_bf16_ts_elected(leader, t_o(x), t_s(x) + 8 * kk, mndesc_at(v_desc, kk), idesc_o,
+                                         (!first || kk > 0) ? 1u : 0u);
+                return true;
+            };
+            auto kv_ready = [&](uint32_t g) {
+                if (!warp_wait(kv_full(g % NS), (g / NS) & 1u, p.status)) return false;
+                tc_fence_after();
+                return true;
+            };
+            uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                FwdTile f;
+                int2 unused;
+                if (!take_tile(n, f, 0, 0, unused)) break;
+                const int nk = f.nk;
+                if (nk == 0) continue;
+                if (!warp_wait(q_full, nq & 1u, p.status) || !kv_ready(g)) break;
+                ++nq;
+                issue_s(0, g);
+                issue_s(1, g);
+                if (nk == 1) umma_commit_elected(leader, q_empty);
+                for (int j = 0; j < nk; ++j, ++g) {
+                    const bool more = j + 1 < nk;
+                    if (!issue_pv(0, g, j == 0) || (more && !kv_ready(g + 1))) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(kv_full(st), 2 * kTile);
-                    const int k0 = (f.first + j) * kRows;
-                    load_tile<D>(s_kv + 2 * st * kTile, &map_qkv, kv_full(st), kcol, k0);
-                    load_tile<D>(s_kv + (2 * st + 1) * kTile, &map_qkv, kv_full(st), vcol, k0);
-                    ++nkv;
-                }
-                if (!ok) break;
-                // the next tile's number after this tile's last load, a ring's depth before its end
-                mbar_arrive_expect_tx(answer_full, 16);
-                next_cta_request(s_answer, answer_full);
-                if (!mbar_wait_fast(answer_full, n & 1u, p.status, kSiteAttn)) break;
-                t = next_cta_answer(s_answer);
-                fence_proxy_async_smem();  // the answer is read before another one is written over it
-                if (t >= 0) {
-                    const FwdTile nx = fwd_tile(p, t);
-                    prefetch_tile<D>(&map_qkv, nx.h[0] * D, nx.q0[0]);
-                    if (nx.q0[1] < p.tokens) prefetch_tile<D>(&map_qkv, nx.h[1] * D, nx.q0[1]);
+                    if (more)
+                        issue_s(0, g + 1);
+                    else
+                        umma_commit_elected(leader, done(0));
+                    if (!issue_pv(1, g, j == 0)) {
+                        ok = false;
+                        break;
+                    }
+                    umma_commit_elected(leader, kv_empty(g % NS));
+                    if (more)
+                        issue_s(1, g + 1);
+                    else
+                        umma_commit_elected(leader, done(1));
+                    // Q is free for the next tile once its last scores are formed
+                    if (j + 2 == nk) umma_commit_elected(leader, q_empty);
                 }
             }
-            // no copy may land after the CTA has gone
-            if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
-            for (int s = 0; s < NS; ++s) {
-                const uint32_t u = ring_uses(nkv, NS, s);
-                if (u > 0) mbar_wait_fast(kv_full(s), (u - 1) & 1u, p.status, kSiteDrain);
-            }
-            for (int s = 0; s < 2; ++s) {
-                const uint32_t u = ring_uses(nt, 2, s);
-                if (u > 0) mbar_wait_fast(tile_full(s), (u - 1) & 1u, p.status, kSiteDrain);
-            }
+            umma_commit_elected(leader, drain);
+            mbar_wait_fast(drain, 0, p.status, kSiteDrain);
         }
-    } else if (warp == 1) {
-        // the whole warp runs the issue loop; its elected lane carries each instruction
-        const uint32_t leader = elect_one_sync();
-        constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
-        constexpr uint32_t idesc_o = mma_idesc_bf16(128, D, false, true);
-        auto issue_s = [&](int x, uint32_t g) {
-            const uint64_t a_desc = kdesc_base(s_q + static_cast<uint32_t>(x) * kTile),
-                           b_desc = kdesc_base(s_kv + 2 * (g % NS) * kTile);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                umma_bf16_elected(leader, t_s(x), kdesc_at(a_desc, kk), kdesc_at(b_desc, kk), idesc_s, kk > 0);
-            umma_commit_elected(leader, s_full(x));
-        };
-        auto issue_pv = [&](int x, uint32_t g, bool first) {
-            if (!warp_wait(p_full(x), g & 1u, p.status)) return false;
-            tc_fence_after();
-            const uint64_t v_desc = mndesc_base(s_kv + (2 * (g % NS) + 1) * kTile);
-#pragma unroll
-            for (int kk = 0; kk < kRows / 16; ++kk)
-                umma_bf16_ts_elected(leader, t_o(x), t_s(x) + 8 * kk, mndesc_at(v_desc, kk), idesc_o,
-                                     (!first || kk > 0) ? 1u : 0u);
-            return true;
-        };
-        auto kv_ready = [&](uint32_t g) {
-            if (!warp_wait(kv_full(g % NS), (g / NS) & 1u, p.status)) return false;
-            tc_fence_after();
-            return true;
-        };
-        uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
-        bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            FwdTile f;
-            int2 unused;
-            if (!take_tile(n, f, 0, 0, unused)) break;
-            const int nk = f.nk;
-            if (nk == 0) continue;
-            if (!warp_wait(q_full, nq & 1u, p.status) || !kv_ready(g)) break;
-            ++nq;
-            issue_s(0, g);
-            issue_s(1, g);
-            if (nk == 1) umma_commit_elected(leader, q_empty);
-            for (int j = 0; j < nk; ++j, ++g) {
-                const bool more = j + 1 < nk;
-                if (!issue_pv(0, g, j == 0) || (more && !kv_ready(g + 1))) {
-                    ok = false;
-                    break;
-                }
-                if (more)
-                    issue_s(0, g + 1);
-                else
-                    umma_commit_elected(leader, done(0));
-                if (!issue_pv(1, g, j == 0)) {
-                    ok = false;
-                    break;
-                }
-                umma_commit_elected(leader, kv_empty(g % NS));
-                if (more)
-                    issue_s(1, g + 1);
-                else
-                    umma_commit_elected(leader, done(1));
-                // Q is free for the next tile once its last scores are formed
-                if (j + 2 == nk) umma_commit_elected(leader, q_empty);
-            }
-        }
-        umma_commit_elected(leader, drain);
-        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
-    }
     } else {
         registers_claim<kDocFwdMany>();
         // ---------------- softmax rows: warps 4-7 tile A, warps 8-11 tile B
@@ -1169,23 +1205,19 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 }
                 const float x = static_cast<float>(q - c0);
                 if constexpr (M == kDocPlain) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) pr[i] = ex2(fmaf(pr[i], p.scale_log2, -lse));
+                    exp_scores<false, 64>(pr, p.scale_log2, 0.f, x, -lse);
                 } else if constexpr (M == kDocBias) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        pr[i] = ex2(fmaf(pr[i], p.scale_log2, fmaf(-slope2, fabsf(static_cast<float>(i) - x), -lse)));
+                    exp_scores<true, 64>(pr, p.scale_log2, slope2, x, -lse);
                 } else {
+                    float th[64];
                     cap_tanh<64>(p, pr);
-                    if (p.slopes) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            pr[i] = ex2(fmaf(pr[i], p.cap_log2, fmaf(-slope2, fabsf(static_cast<float>(i) - x), -lse))) *
-                                    fmaf(-pr[i], pr[i], 1.f);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) pr[i] = ex2(fmaf(pr[i], p.cap_log2, -lse)) * fmaf(-pr[i], pr[i], 1.f);
-                    }
+                    for (int i = 0; i < 64; ++i) th[i] = pr[i];
+                    if (p.slopes)
+                        exp_scores<true, 64>(pr, p.cap_log2, slope2, x, -lse);
+                    else
+                        exp_scores<false, 64>(pr, p.cap_log2, 0.f, x, -lse);
+                    times_cap_slope<64>(pr, th);
                 }
                 if (!warp_wait(dp_full, g & 1u, p.status)) {
                     ok = false;
@@ -1196,8 +1228,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 tmem_load_32(t_dp + t_row, *reinterpret_cast<uint32_t(*)[32]>(rp));
                 tmem_load_32(t_dp + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rp + 32));
                 tmem_wait_load();
-#pragma unroll
-                for (int i = 0; i < 64; ++i) pr[i] *= __uint_as_float(rp[i]) - dv;
+                times_sum<64>(pr, rp, -dv);
                 // hidden pairs last: their P or dP may be anything
                 hide_columns<64>(pr, see.x - c0, see.y - c0, 0.f);
 #pragma unroll
@@ -1544,26 +1575,24 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             for (int c = 0; c < 2; ++c) {
                 float th[32];
                 if constexpr (M == kDocPlain) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) pr[32 * c + j] = ex2(pr[32 * c + j] * p.scale_log2);
+                    exp_scores<false, 32>(pr + 32 * c, p.scale_log2, 0.f, x, 0.f);
                 } else if constexpr (M == kDocBias) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        pr[32 * c + j] = ex2(fmaf(pr[32 * c + j], p.scale_log2, -slope2 * fabsf(static_cast<float>(32 * c + j) - x)));
+                    exp_scores<true, 32>(pr + 32 * c, p.scale_log2, slope2, x - 32 * c, 0.f);
                 } else {
                     const float4* lse4 = reinterpret_cast<const float4*>(p.lse + static_cast<int64_t>(h) * p.ld_stat + qc0 + 32 * c);
                     cap_tanh<32>(p, pr + 32 * c);
 #pragma unroll
+                    for (int j = 0; j < 32; ++j) th[j] = pr[32 * c + j];
+                    if (p.slopes) bias_scores<32>(pr + 32 * c, p.cap_log2, slope2, x - 32 * c);
+                    const float cap2 = p.slopes ? 1.f : p.cap_log2;
+#pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 v = lse4[e];
-                        const float lse[4] = {v.x, v.y, v.z, v.w};
+                        float* s = pr + 32 * c + 4 * e;
+                        split_pair(fma_pair(pair_of(s[0], s[1]), pair_of(cap2, cap2), pair_of(-v.x, -v.y)), s[0], s[1]);
+                        split_pair(fma_pair(pair_of(s[2], s[3]), pair_of(cap2, cap2), pair_of(-v.z, -v.w)), s[2], s[3]);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int j = 4 * e + u;
-                            th[j] = pr[32 * c + j];
-                            const float dist = p.slopes ? slope2 * fabsf(static_cast<float>(32 * c + j) - x) : 0.f;
-                            pr[32 * c + j] = ex2(fmaf(th[j], p.cap_log2, -lse[u] - dist));
-                        }
+                        for (int u = 0; u < 4; ++u) s[u] = ex2(s[u]);
                     }
                 }
                 hide_columns<32>(pr + 32 * c, lo - 32 * c, hi - 32 * c, 0.f);
@@ -1572,10 +1601,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
                 // packed columns 16 c .. 16 c + 15 of the group's columns, all read above
                 tmem_store_16(t_s + t_row + 16 * c, w);
-                if constexpr (M == kDocCap) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) pr[32 * c + j] *= fmaf(-th[j], th[j], 1.f);
-                }
+                if constexpr (M == kDocCap) times_cap_slope<32>(pr + 32 * c, th);
                 tmem_wait_store();
                 tc_fence_before();
                 warp_arrive(p_full(c), lane);
@@ -1591,9 +1617,8 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             tmem_wait_load();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float ds[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) ds[j] = pr[32 * c + j] * __uint_as_float(rp[32 * c + j]);
+                float* ds = pr + 32 * c;
+                times_sum<32>(ds, rp + 32 * c, 0.f);
                 hide_columns<32>(ds, lo - 32 * c, hi - 32 * c, 0.f);  // a hidden column's dP may be anything
                 uint32_t w[16];
 #pragma unroll
