@@ -192,7 +192,7 @@ __device__ __forceinline__ void document_forward_row(const DocArgs& p, int i, in
 
 // Columns [c0, c1) of dq of one query row and head.
 template <int D>
-__device__ __forceinline__ void document_dq_row(const DocArgs& p, int i, int h, int lane, int c0, int c1) {
+__device__ __noinline__ void document_dq_row(const DocArgs& p, int i, int h, int lane, int c0, int c1) {
     const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
     const int g = h / (p.n_heads / p.n_kv_heads);
     const uint16_t* k = p.qkv + (p.n_heads + g) * D;
@@ -215,9 +215,9 @@ __device__ __forceinline__ void document_dq_row(const DocArgs& p, int i, int h, 
     store_row<D>(p.out + i * width + h * D, lane, acc, p.scale, c0, c1);
 }
 
-// Columns [c0, c1) of dk (or dv, with `value`) of one key row and kv head.
+// dk (or dv, with `value`) of one key row and kv head.
 template <int D>
-__device__ __forceinline__ void document_dkv_row(const DocArgs& p, int j, int g, int lane, bool value, int c0, int c1) {
+__device__ __noinline__ void document_dkv_row(const DocArgs& p, int j, int g, int lane, bool value) {
     const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
     const int group = p.n_heads / p.n_kv_heads;
     const int64_t kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
@@ -238,7 +238,7 @@ __device__ __forceinline__ void document_dkv_row(const DocArgs& p, int j, int g,
             for (int c = 0; c < D / 32; ++c) acc[c] += w * (value ? y[c] : x[c]);
         }
     }
-    store_row<D>(p.out + j * width + (value ? vcol : kcol), lane, acc, value ? 1.f : p.scale, c0, c1);
+    store_row<D>(p.out + j * width + (value ? vcol : kcol), lane, acc, value ? 1.f : p.scale, 0, D);
 }
 
 // ------------------------------------------------------------------------ scores on the tensor-core path
@@ -541,8 +541,8 @@ struct DocFwdSmem {
 // their place), warps 4-7 and 8-11 are the softmax rows of tiles A and B.  The
 // first hands registers to the other two.
 constexpr int kDocFwdThreads = 384;
-constexpr int kDocFwdRegs = 168, kDocFwdFew = 56, kDocFwdMany = 224;
-static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * kDocFwdRegs, "registers of the launch");
+constexpr int kDocFwdFew = 56, kDocFwdMany = 224;
+static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * 168, "registers of the launch: 168 a thread");
 
 template <int D, int M>
 __global__ void __launch_bounds__(kDocFwdThreads, 1)
@@ -901,26 +901,10 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     }
 }
 
-// ------------------------------------------------------------------------ backward: common
-
-// Five warpgroups: warp 0 loads, warps 1 and 2 issue products (dK / dV: warp 2
-// prepares the statistics), warp 3 only holds its place; warps 4-19 are row warps,
-// four groups with 32 of a step's 128 columns each, one row a thread.  Row warps
-// wait for products, tensor memory and one another's chains most of the time, so
-// four of them share a scheduler: with eight warps of 64 columns a capped step took
-// 2.1 us, a plain one 1.3 us.
-constexpr int kDocBwdThreads = 640, kDocMma2Warp = 2, kDocRowWarps = 16;
-constexpr int kDocBwdRegs = 96, kDocBwdFew = 64, kDocBwdMany = 104;
-static_assert(kDocBwdFew + 4 * kDocBwdMany <= 5 * kDocBwdRegs, "registers of the launch");
-
-// Tensor-memory column of the packed bf16 operand of K step kk (16 rows of the
-// contraction): group kk / 2 packs its 32 columns into the first 16 of them.
-__device__ __forceinline__ uint32_t doc_packed_col(int kk) { return static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1)); }
-
 // ------------------------------------------------------------------------ backward: dq
 
 // The causal core's dQ tiles and pipeline (attention.cu): S and dP by warp 1, dQ
-// by warp 2, four groups of row warps with 32 key columns each.
+// by warp 10, two groups of row warps with 64 key columns each.
 template <int D>
 struct DocDqSmem {
     // One V stage where the results' 32 KiB leave no room for two: V[g + 1] lands while
@@ -1001,9 +985,9 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
         mbar_init(done, 1);
         mbar_init(drain, 2);  // both MMA warps
         for (int s = 0; s < 2; ++s) {
-            mbar_init(ds_full(s), kDocRowWarps);
+            mbar_init(ds_full(s), 8);
             mbar_init(tile_full(s), 1);
-            mbar_init(tile_empty(s), 2 + kDocRowWarps);  // the two MMA warps and the row warps
+            mbar_init(tile_empty(s), 10);  // the two MMA warps and the eight row warps
             mbar_init(dq_issued(s), 1);
             mbar_init(dp_issued(s), 1);
         }
@@ -1016,8 +1000,8 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
-    // columns: S buffers 0-127 and 128-255 (dS packed into the first 16 of every 32
-    // columns of a buffer once read), dP 256-383, dQ 384..
+    // columns: S buffers 0-127 and 128-255 (dS packed into columns 0-31 and
+    // 64-95 of a buffer once read), dP 256-383, dQ 384..
     const uint32_t t_dp = tmem_base + 256, t_dq = tmem_base + 384;
     auto t_s = [&](uint32_t g) { return tmem_base + 128u * (g & 1u); };
     auto take_tile = [&](uint32_t n, int& t) {
@@ -1028,172 +1012,168 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
         return true;
     };
 
-    if (warp < 4) {
-        registers_release<kDocBwdFew>();
-        if (warp == 0) {
-            if (lane == 0) {
-                auto fetch = [&](uint32_t n) {
-                    if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) return -2;
-                    int t = atomicAdd(p.counter, 1);
-                    if (t >= n_tiles) t = -1;
-                    tile_slot[n & 1u] = t;
-                    mbar_arrive(tile_full(n & 1u));
-                    return t;
-                };
-                uint32_t nq = 0, nkf = 0, nvf = 0;  // Q / dO, K and V loads issued
-                int t = fetch(0);
-                for (uint32_t n = 0; t >= 0; ++n) {
-                    const DqTile tl = dq_tile(p, t);
-                    if (tl.nk > 0) {
-                        // Q and dO once the previous tile's S and dP products are done
-                        if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                        mbar_arrive_expect_tx(q_full, 2 * kTile);
-                        load_tile<D>(s_q, &map_qkv, q_full, tl.h * D, tl.q0);
-                        load_tile<D>(s_do, &map_do, q_full, tl.h * D, tl.q0);
-                        ++nq;
-                    }
-                    const int g = tl.h / group;
-                    const int kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
-                    int t_next = tl.nk > 0 ? -2 : fetch(n + 1);
-                    for (int j = 0; j < tl.nk; ++j) {
-                        const uint32_t u = nkf;
-                        if (!mbar_wait_fast(k_empty(u % NK), ((u / NK) & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                        mbar_arrive_expect_tx(k_full(u % NK), kTile);
-                        load_tile<D>(s_k + (u % NK) * kTile, &map_qkv, k_full(u % NK), kcol, (tl.kb0 + j) * kRows);
-                        ++nkf;
-                        if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn)) break;
-                        mbar_arrive_expect_tx(v_full(u % NV), kTile);
-                        load_tile<D>(s_v + (u % NV) * kTile, &map_qkv, v_full(u % NV), vcol, (tl.kb0 + j) * kRows);
-                        ++nvf;
-                        // the next tile's number at this tile's last load, and its Q and dO into L2
-                        if (j == tl.nk - 1) {
-                            t_next = fetch(n + 1);
-                            if (t_next >= 0) {
-                                const DqTile nx = dq_tile(p, t_next);
-                                prefetch_tile<D>(&map_qkv, nx.h * D, nx.q0);
-                                prefetch_tile<D>(&map_do, nx.h * D, nx.q0);
-                            }
+    if (warp == 0) {
+        if (lane == 0) {
+            auto fetch = [&](uint32_t n) {
+                if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) return -2;
+                int t = atomicAdd(p.counter, 1);
+                if (t >= n_tiles) t = -1;
+                tile_slot[n & 1u] = t;
+                mbar_arrive(tile_full(n & 1u));
+                return t;
+            };
+            uint32_t nq = 0, nkf = 0, nvf = 0;  // Q / dO, K and V loads issued
+            int t = fetch(0);
+            for (uint32_t n = 0; t >= 0; ++n) {
+                const DqTile tl = dq_tile(p, t);
+                if (tl.nk > 0) {
+                    // Q and dO once the previous tile's S and dP products are done
+                    if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(q_full, 2 * kTile);
+                    load_tile<D>(s_q, &map_qkv, q_full, tl.h * D, tl.q0);
+                    load_tile<D>(s_do, &map_do, q_full, tl.h * D, tl.q0);
+                    ++nq;
+                }
+                const int g = tl.h / group;
+                const int kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
+                int t_next = tl.nk > 0 ? -2 : fetch(n + 1);
+                for (int j = 0; j < tl.nk; ++j) {
+                    const uint32_t u = nkf;
+                    if (!mbar_wait_fast(k_empty(u % NK), ((u / NK) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(k_full(u % NK), kTile);
+                    load_tile<D>(s_k + (u % NK) * kTile, &map_qkv, k_full(u % NK), kcol, (tl.kb0 + j) * kRows);
+                    ++nkf;
+                    if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    mbar_arrive_expect_tx(v_full(u % NV), kTile);
+                    load_tile<D>(s_v + (u % NV) * kTile, &map_qkv, v_full(u % NV), vcol, (tl.kb0 + j) * kRows);
+                    ++nvf;
+                    // the next tile's number at this tile's last load, and its Q and dO into L2
+                    if (j == tl.nk - 1) {
+                        t_next = fetch(n + 1);
+                        if (t_next >= 0) {
+                            const DqTile nx = dq_tile(p, t_next);
+                            prefetch_tile<D>(&map_qkv, nx.h * D, nx.q0);
+                            prefetch_tile<D>(&map_do, nx.h * D, nx.q0);
                         }
                     }
-                    t = t_next;  // -2 after a failed wait ends the loop
                 }
-                // no copy may land after the CTA has gone
-                if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
-                for (int s = 0; s < NK; ++s) {
-                    const uint32_t u = ring_uses(nkf, NK, s);
-                    if (u > 0) mbar_wait_fast(k_full(s), (u - 1) & 1u, p.status, kSiteDrain);
-                }
-                for (int s = 0; s < NV; ++s) {
-                    const uint32_t u = ring_uses(nvf, NV, s);
-                    if (u > 0) mbar_wait_fast(v_full(s), (u - 1) & 1u, p.status, kSiteDrain);
-                }
+                t = t_next;  // -2 after a failed wait ends the loop
             }
-        } else if (warp == 1) {
-            // ---------------- S and dP products
-            const uint32_t leader = elect_one_sync();
-            constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
-            const uint64_t q_desc = kdesc_base(s_q), do_desc = kdesc_base(s_do);
-            auto issue_s = [&](uint32_t g) {
-                const uint32_t st = g % NK;
-                if (!warp_wait(k_full(st), (g / NK) & 1u, p.status)) return false;
-                tc_fence_after();
-                const uint64_t k_desc = kdesc_base(s_k + st * kTile);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_elected(leader, t_s(g), kdesc_at(q_desc, kk), kdesc_at(k_desc, kk), idesc_s, kk > 0);
-                umma_commit_elected(leader, s_full(g & 1u));
-                return true;
-            };
-            auto issue_dp = [&](uint32_t g) {
-                const uint32_t st = g % NV;
-                if (!warp_wait(v_full(st), (g / NV) & 1u, p.status)) return false;
-                tc_fence_after();
-                const uint64_t v_desc = kdesc_base(s_v + st * kTile);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_elected(leader, t_dp, kdesc_at(do_desc, kk), kdesc_at(v_desc, kk), idesc_s, kk > 0);
-                umma_commit_elected(leader, dp_full);
-                umma_commit_elected(leader, v_empty(st));
-                return true;
-            };
-            // S[g] overwrites the S buffer of step g - 2 once the dQ warp has issued
-            // dQ[g - 2], which reads dS[g - 2] from it; dP[g] overwrites dP[g - 1]
-            // once the row warps are done with it.
-            auto may_issue_s = [&](uint32_t g) {
-                if (g < 2) return true;
-                if (!warp_wait(dq_issued(g - 2), ((g - 2) >> 1) & 1u, p.status)) return false;
-                tc_fence_after();
-                return true;
-            };
-            auto may_issue_dp = [&](uint32_t g) {
-                if (g < 1) return true;
-                if (!warp_wait(ds_full(g - 1), ((g - 1) >> 1) & 1u, p.status)) return false;
-                tc_fence_after();
-                return true;
-            };
-            uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
-            bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                int t;
-                if (!take_tile(n, t) || t < 0) break;
-                const int nk = dq_tile(p, t).nk;
-                if (nk == 0) continue;
-                if (!warp_wait(q_full, nq & 1u, p.status)) break;
-                ++nq;
-                tc_fence_after();
-                // the MMA order per step is S[g+1], dP[g+1] (here) beside dQ[g] (the dQ warp)
-                for (int j = 0; j < nk; ++j, ++g) {
-                    if (!may_issue_s(g) || !issue_s(g) || !may_issue_dp(g) || !issue_dp(g)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_before();
-                    if (leader) mbar_arrive(dp_issued(g));
-                    // Q and dO are free for the next tile once its last S and dP are done
-                    if (j + 1 == nk) umma_commit_elected(leader, q_empty);
-                }
+            // no copy may land after the CTA has gone
+            if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
+            for (int s = 0; s < NK; ++s) {
+                const uint32_t u = ring_uses(nkf, NK, s);
+                if (u > 0) mbar_wait_fast(k_full(s), (u - 1) & 1u, p.status, kSiteDrain);
             }
-            umma_commit_elected(leader, drain);
-            mbar_wait_fast(drain, 0, p.status, kSiteDrain);
-        } else if (warp == kDocMma2Warp) {
-            // ---------------- dQ products
-            const uint32_t leader = elect_one_sync();
-            constexpr uint32_t idesc_q = mma_idesc_bf16(128, D, false, true);
-            uint32_t g = 0;
-            bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                int t;
-                if (!take_tile(n, t) || t < 0) break;
-                const int nk = dq_tile(p, t).nk;
-                if (nk == 0) continue;
-                for (int j = 0; j < nk; ++j, ++g) {
-                    if (!warp_wait(ds_full(g), (g >> 1) & 1u, p.status) ||
-                        (j + 1 < nk && !warp_wait(dp_issued(g + 1), ((g + 1) >> 1) & 1u, p.status))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t k_mn = mndesc_base(s_k + (g % NK) * kTile);
-#pragma unroll
-                    for (int kk = 0; kk < kRows / 16; ++kk)
-                        umma_bf16_ts_elected(leader, t_dq, t_s(g) + doc_packed_col(kk), mndesc_at(k_mn, kk), idesc_q,
-                                             (j > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit_elected(leader, k_empty(g % NK));
-                    tc_fence_before();
-                    if (leader) mbar_arrive(dq_issued(g));
-                }
-                if (ok) umma_commit_elected(leader, done);
+            for (int s = 0; s < NV; ++s) {
+                const uint32_t u = ring_uses(nvf, NV, s);
+                if (u > 0) mbar_wait_fast(v_full(s), (u - 1) & 1u, p.status, kSiteDrain);
             }
-            umma_commit_elected(leader, drain);
-            mbar_wait_fast(drain, 0, p.status, kSiteDrain);
         }
+    } else if (warp == 1) {
+        // ---------------- S and dP products
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
+        const uint64_t q_desc = kdesc_base(s_q), do_desc = kdesc_base(s_do);
+        auto issue_s = [&](uint32_t g) {
+            const uint32_t st = g % NK;
+            if (!warp_wait(k_full(st), (g / NK) & 1u, p.status)) return false;
+            tc_fence_after();
+            const uint64_t k_desc = kdesc_base(s_k + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_s(g), kdesc_at(q_desc, kk), kdesc_at(k_desc, kk), idesc_s, kk > 0);
+            umma_commit_elected(leader, s_full(g & 1u));
+            return true;
+        };
+        auto issue_dp = [&](uint32_t g) {
+            const uint32_t st = g % NV;
+            if (!warp_wait(v_full(st), (g / NV) & 1u, p.status)) return false;
+            tc_fence_after();
+            const uint64_t v_desc = kdesc_base(s_v + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_dp, kdesc_at(do_desc, kk), kdesc_at(v_desc, kk), idesc_s, kk > 0);
+            umma_commit_elected(leader, dp_full);
+            umma_commit_elected(leader, v_empty(st));
+            return true;
+        };
+        // S[g] overwrites the S buffer of step g - 2 once the dQ warp has issued
+        // dQ[g - 2], which reads dS[g - 2] from it; dP[g] overwrites dP[g - 1]
+        // once the row warps are done with it.
+        auto may_issue_s = [&](uint32_t g) {
+            if (g < 2) return true;
+            if (!warp_wait(dq_issued(g - 2), ((g - 2) >> 1) & 1u, p.status)) return false;
+            tc_fence_after();
+            return true;
+        };
+        auto may_issue_dp = [&](uint32_t g) {
+            if (g < 1) return true;
+            if (!warp_wait(ds_full(g - 1), ((g - 1) >> 1) & 1u, p.status)) return false;
+            tc_fence_after();
+            return true;
+        };
+        uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const int nk = dq_tile(p, t).nk;
+            if (nk == 0) continue;
+            if (!warp_wait(q_full, nq & 1u, p.status)) break;
+            ++nq;
+            tc_fence_after();
+            // the MMA order per step is S[g+1], dP[g+1] (here) beside dQ[g] (the dQ warp)
+            for (int j = 0; j < nk; ++j, ++g) {
+                if (!may_issue_s(g) || !issue_s(g) || !may_issue_dp(g) || !issue_dp(g)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_before();
+                if (leader) mbar_arrive(dp_issued(g));
+                // Q and dO are free for the next tile once its last S and dP are done
+                if (j + 1 == nk) umma_commit_elected(leader, q_empty);
+            }
+        }
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    } else if (warp == kDqWarp) {
+        // ---------------- dQ products
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_q = mma_idesc_bf16(128, D, false, true);
+        uint32_t g = 0;
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            int t;
+            if (!take_tile(n, t) || t < 0) break;
+            const int nk = dq_tile(p, t).nk;
+            if (nk == 0) continue;
+            for (int j = 0; j < nk; ++j, ++g) {
+                if (!warp_wait(ds_full(g), (g >> 1) & 1u, p.status) ||
+                    (j + 1 < nk && !warp_wait(dp_issued(g + 1), ((g + 1) >> 1) & 1u, p.status))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t k_mn = mndesc_base(s_k + (g % NK) * kTile);
+#pragma unroll
+                for (int kk = 0; kk < kRows / 16; ++kk)
+                    umma_bf16_ts_elected(leader, t_dq, t_s(g) + packed_col(kk), mndesc_at(k_mn, kk), idesc_q,
+                                         (j > 0 || kk > 0) ? 1u : 0u);
+                umma_commit_elected(leader, k_empty(g % NK));
+                tc_fence_before();
+                if (leader) mbar_arrive(dq_issued(g));
+            }
+            if (ok) umma_commit_elected(leader, done);
+        }
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
     } else {
-        registers_claim<kDocBwdMany>();
-        // ---------------- row warps: group gi takes key columns 32 gi .. 32 gi + 31 of every step
-        const int gi = (warp - 4) >> 2;
+        // ---------------- row warps: group gi takes key columns 64 gi .. 64 gi + 63 of every step
+        const int gi = (warp - 2) >> 2;
         const int qw = warp & 3;
         const int row = qw * 32 + lane;
-        const uint32_t t_row = (static_cast<uint32_t>(qw * 32) << 16) + 32u * gi;
+        const uint32_t t_row = (static_cast<uint32_t>(qw * 32) << 16) + 64u * gi;
         uint32_t g = 0, nd = 0;  // steps and tiles with steps so far
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
@@ -1208,79 +1188,89 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             const float dv = empty ? 0.f : p.dvec[static_cast<int64_t>(tl.h) * p.ld_stat + q];
             const float slope2 = M != kDocPlain && p.slopes ? p.slopes[tl.h] * kLog2e : 0.f;
             for (int j = 0; j < tl.nk; ++j, ++g) {
-                const int c0 = (tl.kb0 + j) * kRows + 32 * gi;
+                const int c0 = (tl.kb0 + j) * kRows + 64 * gi;
                 if (!warp_wait(s_full(g & 1u), (g >> 1) & 1u, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                float pr[32];  // P, times the cap's derivative
-                load_tmem32(t_s(g) + t_row, pr);
+                float pr[64];  // P, times the cap's derivative
+                {
+                    uint32_t rs[64];
+                    tmem_load_32(t_s(g) + t_row, *reinterpret_cast<uint32_t(*)[32]>(rs));
+                    tmem_load_32(t_s(g) + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rs + 32));
+                    tmem_wait_load();
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) pr[i] = __uint_as_float(rs[i]);
+                }
                 const float x = static_cast<float>(q - c0);
                 if constexpr (M == kDocPlain) {
-                    exp_scores<false, 32>(pr, p.scale_log2, 0.f, x, -lse);
+                    exp_scores<false, 64>(pr, p.scale_log2, 0.f, x, -lse);
                 } else if constexpr (M == kDocBias) {
-                    exp_scores<true, 32>(pr, p.scale_log2, slope2, x, -lse);
+                    exp_scores<true, 64>(pr, p.scale_log2, slope2, x, -lse);
                 } else {
-                    float th[32];
-                    cap_tanh<32>(p, pr);
+                    float th[64];
+                    cap_tanh<64>(p, pr);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) th[i] = pr[i];
+                    for (int i = 0; i < 64; ++i) th[i] = pr[i];
                     if (p.slopes)
-                        exp_scores<true, 32>(pr, p.cap_log2, slope2, x, -lse);
+                        exp_scores<true, 64>(pr, p.cap_log2, slope2, x, -lse);
                     else
-                        exp_scores<false, 32>(pr, p.cap_log2, 0.f, x, -lse);
-                    times_cap_slope<32>(pr, th);
+                        exp_scores<false, 64>(pr, p.cap_log2, 0.f, x, -lse);
+                    times_cap_slope<64>(pr, th);
                 }
                 if (!warp_wait(dp_full, g & 1u, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t rp[32];
-                tmem_load_32(t_dp + t_row, rp);
+                uint32_t rp[64];
+                tmem_load_32(t_dp + t_row, *reinterpret_cast<uint32_t(*)[32]>(rp));
+                tmem_load_32(t_dp + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rp + 32));
                 tmem_wait_load();
-                times_sum<32>(pr, rp, -dv);
+                times_sum<64>(pr, rp, -dv);
                 // hidden pairs last: their P or dP may be anything
-                hide_columns<32>(pr, see.x - c0, see.y - c0, 0.f);
-                uint32_t w[16];
+                hide_columns<64>(pr, see.x - c0, see.y - c0, 0.f);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
-                // the first 16 of the group's S columns, all read above
-                tmem_store_16(t_s(g) + t_row, w);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
+                    // packed columns 16 c .. 16 c + 15 of the group's S columns, all read above
+                    tmem_store_16(t_s(g) + t_row + 16 * c, w);
+                }
                 tmem_wait_store();
                 tc_fence_before();
                 warp_arrive(ds_full(g), lane);
             }
             if (!ok) break;
-            // group gi stores dQ columns [32 gi, 32 gi + 32) (heads of 64: groups 0 and 1);
-            // the tile's next dQ product waits for this group's next dS arrival, after
-            // these loads
-            const uint32_t stage = s_stage + kStageBytes / 2 * static_cast<uint32_t>(warp - 4);
-            const bool mine = 32 * gi < D;
+            // group gi stores dQ columns [D/2 gi, D/2 (gi + 1)); the tile's next
+            // dQ product waits for this group's next dS arrival, after these loads
+            constexpr int kChunks = D / 64;  // 32-column chunks of this group's half
+            const uint32_t stage = s_stage + kStageBytes * static_cast<uint32_t>(warp - 2);
             bool again = false;
-            float r[32] = {};
+            float r[kChunks][32] = {};
             if (tl.nk > 0) {
                 if (!warp_wait(done, nd & 1u, p.status)) break;
                 ++nd;
-                if (mine) {
-                    tc_fence_after();
-                    load_tmem32(t_dq + t_row, r);
-                    tc_fence_before();
-                    again = !finite32(r);
-                }
+                tc_fence_after();
+                const uint32_t t_q = t_dq + (static_cast<uint32_t>(qw * 32) << 16) + 32u * (gi * kChunks);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) load_tmem32(t_q + 32 * c, r[c]);
+                tc_fence_before();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) again |= !finite32(r[c]);
             }
-            if (mine) {
-                stage_free(lane);
-                stage32<64>(stage, lane, 0, r, p.scale, empty);
-                if (q - lane < p.tokens) store_stage(&map_dq, stage, lane, tl.h * D + 32 * gi, q - lane);
-            }
+            stage_free(lane);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) stage32<D>(stage, lane, c, r[c], p.scale, empty);
+            if (q - lane < p.tokens) store_stage(&map_dq, stage, lane, tl.h * D + gi * (D / 2), q - lane);
             uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
             if (redo) stores_done(lane);
             while (redo) {
                 const int src = __ffs(redo) - 1;
                 redo &= redo - 1;
-                document_dq_row<D>(p, q - lane + src, tl.h, lane, 32 * gi, 32 * gi + 32);
+                document_dq_row<D>(p, q - lane + src, tl.h, lane, gi * (D / 2), (gi + 1) * (D / 2));
             }
         }
         stage_free(lane);  // shared memory outlives the stores that read it
@@ -1311,7 +1301,7 @@ struct DocDkvSmem {
     static constexpr uint32_t kAug = kOnes + 2 * kAugTile;      // stage s: the B operand of step s
     static constexpr uint32_t kStat = kAug + kAugStages * kAugTile;  // stage s: lse (512 bytes) then D (512 bytes)
     static constexpr uint32_t kBars = kStat + 1024 * kStatStages;
-    static constexpr int kNumBars = 1 + 2 * (kQStages + kStatStages) + kAugStages + 6;
+    static constexpr int kNumBars = 1 + 2 * (kQStages + kStatStages) + kAugStages + 8;
     static constexpr size_t kUsed = kBars + 8 * kNumBars + 16;
 };
 
@@ -1326,7 +1316,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
     using L = DocDkvSmem<D>;
     constexpr int NQ = L::kQStages, ND = L::kDoStages, NT = L::kStatStages, NA = L::kAugStages;
     constexpr uint32_t kTile = L::kTile;
-    constexpr int kThreads = kDocBwdThreads, kStats = kDocMma2Warp;
+    constexpr int kThreads = kAttnDqThreads, kStats = kDqWarp;  // warp 10: statistics
     const uint32_t base = smem_addr(smem_raw);
     const uint32_t s_k = base + L::kK, s_v = base + L::kV, s_q = base + L::kQ, s_do = base + L::kDO,
                    s_ones = base + L::kOnes, s_aug = base + L::kAug, s_stat = base + L::kStat;
@@ -1340,8 +1330,11 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
     auto aug_empty = [&](int s) { return bars + 8u * (1 + 2 * NQ + 2 * NT + s); };
     constexpr int kB = 1 + 2 * (NQ + NT) + NA;
     static_assert(NQ == ND, "Q and dO share their ring position and release");
-    const uint32_t s_full = bars + 8u * kB, dp_full = bars + 8u * (kB + 1), p_full = bars + 8u * (kB + 2),
-                   ds_full = bars + 8u * (kB + 3), done = bars + 8u * (kB + 4), drain = bars + 8u * (kB + 5);
+    // p_full(c) / ds_full(c): chunk c (32 query columns of each group) of P^T / dS^T is packed
+    auto p_full = [&](int c) { return bars + 8u * (kB + 2 + c); };
+    auto ds_full = [&](int c) { return bars + 8u * (kB + 4 + c); };
+    const uint32_t s_full = bars + 8u * kB, dp_full = bars + 8u * (kB + 1), done = bars + 8u * (kB + 6),
+                   drain = bars + 8u * (kB + 7);
     const uint32_t tmem_slot = bars + 8u * L::kNumBars;
     volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - base));
 
@@ -1391,8 +1384,10 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
         for (int s = 0; s < NA; ++s) mbar_init(aug_empty(s), 1);
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(p_full, kDocRowWarps);
-        mbar_init(ds_full, kDocRowWarps);
+        for (int c = 0; c < 2; ++c) {
+            mbar_init(p_full(c), 8);
+            mbar_init(ds_full(c), 8);
+        }
         mbar_init(done, 1);
         mbar_init(drain, 1);
         mbar_fence_init();
@@ -1404,142 +1399,160 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
-    // columns: S^T 0-127 (P^T packed into the first 16 of every 32 once read), dP^T
+    // columns: S^T 0-127 (P^T packed into 0-31 and 64-95 once read), dP^T
     // 128-255 (dS^T likewise), dV 256.., dK 256 + D..
     const uint32_t t_s = tmem_base, t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 256 + D;
 
-    if (warp < 4) {
-        registers_release<kDocBwdFew>();
-        if (warp == 0) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(kv_full, 2 * kTile);
-                load_tile<D>(s_k, &map_qkv, kv_full, kcol, k0);
-                load_tile<D>(s_v, &map_qkv, kv_full, vcol, k0);
-                uint32_t nq = 0, nt = 0;
-                for (int i = 0; i < n_steps; ++i) {
-                    const int h = g * group + i % group;
-                    const int r0 = (range.x + i / group) * kRows;
-                    if (!mbar_wait_fast(st_empty(i % NT), ((i / NT) & 1) ^ 1u, p.status, kSiteAttn)) break;
-                    const uint32_t stat = s_stat + 1024u * (i % NT);
-                    mbar_arrive_expect_tx(st_full(i % NT), 1024);
-                    bulk_load_1d(stat, p.lse + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
-                    bulk_load_1d(stat + 512, p.dvec + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
-                    ++nt;
-                    // Q[i] and dO[i] land on one barrier (with the statistics operand); one
-                    // release covers both stages (dK[i - 2], after dV[i - 2], read the last of them)
-                    if (!mbar_wait_fast(q_empty(i % NQ), ((i / NQ) & 1) ^ 1u, p.status, kSiteAttn)) break;
-                    mbar_arrive_expect_tx(q_full(i % NQ), 2 * kTile);
-                    load_tile<D>(s_q + (i % NQ) * kTile, &map_qkv, q_full(i % NQ), h * D, r0);
-                    load_tile<D>(s_do + (i % ND) * kTile, &map_do, q_full(i % NQ), h * D, r0);
-                    ++nq;
-                }
-                mbar_wait_fast(kv_full, 0, p.status, kSiteDrain);
-                for (int s = 0; s < NQ; ++s) {
-                    const uint32_t u = ring_uses(nq, NQ, s);
-                    if (u > 0) mbar_wait_fast(q_full(s), (u - 1) & 1, p.status, kSiteDrain);
-                }
-                for (int s = 0; s < NT; ++s) {
-                    const uint32_t u = ring_uses(nt, NT, s);
-                    if (u > 0) mbar_wait_fast(st_full(s), (u - 1) & 1, p.status, kSiteDrain);
-                }
-            }
-        } else if (warp == 1) {
-            // the whole warp runs the issue loop; its elected lane carries each instruction
-            const uint32_t leader = elect_one_sync();
-            constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
-            constexpr uint32_t idesc_g = mma_idesc_bf16(128, D, false, true);
-            const uint64_t k_desc = kdesc_base(s_k), v_desc = kdesc_base(s_v);
-            const uint64_t ones_lse = aug_desc(s_ones), ones_d = aug_desc(s_ones + L::kAugTile);
-            auto issue_s = [&](int i) {
-                const int st = i % NQ;
-                // Q tile i and statistics operand i % NA (NA = NQ) complete one phase together
-                if (!warp_wait(q_full(st), (i / NQ) & 1, p.status)) return false;
-                tc_fence_after();
-                const uint64_t q_desc = kdesc_base(s_q + st * kTile);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_elected(leader, t_s, kdesc_at(k_desc, kk), kdesc_at(q_desc, kk), idesc_s, kk > 0);
-                if constexpr (M != kDocCap)
-                    umma_bf16_elected(leader, t_s, ones_lse, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
-                umma_commit_elected(leader, s_full);
-                return true;
-            };
-            auto issue_dp = [&](int i) {  // after issue_s(i), which waited for dO[i] and the statistics too
-                const int st = i % ND;
-                const uint64_t do_desc = kdesc_base(s_do + st * kTile);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_elected(leader, t_dp, kdesc_at(v_desc, kk), kdesc_at(do_desc, kk), idesc_s, kk > 0);
-                umma_bf16_elected(leader, t_dp, ones_d, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
-                umma_commit_elected(leader, dp_full);
-                umma_commit_elected(leader, aug_empty(i % NA));
-                return true;
-            };
-            bool ok = warp_wait(kv_full, 0, p.status) && issue_s(0) && issue_dp(0);
-            for (int i = 0; ok && i < n_steps; ++i) {
-                const uint64_t do_mn = mndesc_base(s_do + (i % ND) * kTile);
-                if (!warp_wait(p_full, i & 1, p.status)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kRows / 16; ++kk)
-                    umma_bf16_ts_elected(leader, t_dv, t_s + doc_packed_col(kk), mndesc_at(do_mn, kk), idesc_g,
-                                         (i > 0 || kk > 0) ? 1u : 0u);
-                // S^T[i+1] overwrites the S^T buffer after dV[i] has read P^T[i] from it
-                if (i + 1 < n_steps && !issue_s(i + 1)) break;
-                const uint64_t q_mn = mndesc_base(s_q + (i % NQ) * kTile);
-                if (!warp_wait(ds_full, i & 1, p.status)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kRows / 16; ++kk)
-                    umma_bf16_ts_elected(leader, t_dk, t_dp + doc_packed_col(kk), mndesc_at(q_mn, kk), idesc_g,
-                                         (i > 0 || kk > 0) ? 1u : 0u);
-                // Q[i] and dO[i]: dK[i] is the last product that reads either
-                umma_commit_elected(leader, q_empty(i % NQ));
-                if (i + 1 < n_steps && !issue_dp(i + 1)) break;
-            }
-            umma_commit_elected(leader, done);
-            umma_commit_elected(leader, drain);
-            mbar_wait_fast(drain, 0, p.status, kSiteDrain);
-        } else if (warp == kStats) {
-            // ---------------- statistics warp: step i's lse and D into B operand i % NA
-            const float inv_c = 1.f / p.scale_log2;
+    if (warp == 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(kv_full, 2 * kTile);
+            load_tile<D>(s_k, &map_qkv, kv_full, kcol, k0);
+            load_tile<D>(s_v, &map_qkv, kv_full, vcol, k0);
+            uint32_t nq = 0, nt = 0;
             for (int i = 0; i < n_steps; ++i) {
-                if (!warp_wait(st_full(i % NT), (i / NT) & 1, p.status) ||
-                    !warp_wait(aug_empty(i % NA), ((i / NA) & 1) ^ 1u, p.status))
-                    break;
-                const float* stat = reinterpret_cast<const float*>(smem_raw + L::kStat + 1024u * (i % NT));
-                uint8_t* aug = smem_raw + L::kAug + (i % NA) * L::kAugTile;
+                const int h = g * group + i % group;
+                const int r0 = (range.x + i / group) * kRows;
+                if (!mbar_wait_fast(st_empty(i % NT), ((i / NT) & 1) ^ 1u, p.status, kSiteAttn)) break;
+                const uint32_t stat = s_stat + 1024u * (i % NT);
+                mbar_arrive_expect_tx(st_full(i % NT), 1024);
+                bulk_load_1d(stat, p.lse + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
+                bulk_load_1d(stat + 512, p.dvec + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
+                ++nt;
+                // Q[i] and dO[i] land on one barrier (with the statistics operand); one
+                // release covers both stages (dK[i - 2], after dV[i - 2], read the last of them)
+                if (!mbar_wait_fast(q_empty(i % NQ), ((i / NQ) & 1) ^ 1u, p.status, kSiteAttn)) break;
+                mbar_arrive_expect_tx(q_full(i % NQ), 2 * kTile);
+                load_tile<D>(s_q + (i % NQ) * kTile, &map_qkv, q_full(i % NQ), h * D, r0);
+                load_tile<D>(s_do + (i % ND) * kTile, &map_do, q_full(i % NQ), h * D, r0);
+                ++nq;
+            }
+            mbar_wait_fast(kv_full, 0, p.status, kSiteDrain);
+            for (int s = 0; s < NQ; ++s) {
+                const uint32_t u = ring_uses(nq, NQ, s);
+                if (u > 0) mbar_wait_fast(q_full(s), (u - 1) & 1, p.status, kSiteDrain);
+            }
+            for (int s = 0; s < NT; ++s) {
+                const uint32_t u = ring_uses(nt, NT, s);
+                if (u > 0) mbar_wait_fast(st_full(s), (u - 1) & 1, p.status, kSiteDrain);
+            }
+        }
+    } else if (warp == 1) {
+        // the whole warp runs the issue loop; its elected lane carries each instruction
+        const uint32_t leader = elect_one_sync();
+        constexpr uint32_t idesc_s = mma_idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idesc_g = mma_idesc_bf16(128, D, false, true);
+        const uint64_t k_desc = kdesc_base(s_k), v_desc = kdesc_base(s_v);
+        const uint64_t ones_lse = aug_desc(s_ones), ones_d = aug_desc(s_ones + L::kAugTile);
+        auto issue_s = [&](int i) {
+            const int st = i % NQ;
+            // Q tile i and statistics operand i % NA (NA = NQ) complete one phase together
+            if (!warp_wait(q_full(st), (i / NQ) & 1, p.status)) return false;
+            tc_fence_after();
+            const uint64_t q_desc = kdesc_base(s_q + st * kTile);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int r = lane + 32 * u;
-                    // statistics of rows that see nothing, or behind the last row, reach
-                    // hidden columns only, whatever they hold
-                    if constexpr (M != kDocCap)
-                        *reinterpret_cast<uint2*>(aug + aug_offset(r, 0)) = split3_bf16(-stat[r] * inv_c);
-                    *reinterpret_cast<uint2*>(aug + aug_offset(r, 1)) = split3_bf16(-stat[128 + r]);
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_s, kdesc_at(k_desc, kk), kdesc_at(q_desc, kk), idesc_s, kk > 0);
+            if constexpr (M != kDocCap)
+                umma_bf16_elected(leader, t_s, ones_lse, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
+            umma_commit_elected(leader, s_full);
+            return true;
+        };
+        auto issue_dp = [&](int i) {  // after issue_s(i), which waited for dO[i] and the statistics too
+            const int st = i % ND;
+            const uint64_t do_desc = kdesc_base(s_do + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_bf16_elected(leader, t_dp, kdesc_at(v_desc, kk), kdesc_at(do_desc, kk), idesc_s, kk > 0);
+            umma_bf16_elected(leader, t_dp, ones_d, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
+            umma_commit_elected(leader, dp_full);
+            umma_commit_elected(leader, aug_empty(i % NA));
+            return true;
+        };
+        bool ok = warp_wait(kv_full, 0, p.status) && issue_s(0) && issue_dp(0);
+        // K steps of dV / dK in the order their P^T / dS^T chunks are packed:
+        // chunk c of group g holds the K steps 4 g + 2 c and 4 g + 2 c + 1
+        constexpr int kOrder[8] = {0, 1, 4, 5, 2, 3, 6, 7};
+        for (int i = 0; ok && i < n_steps; ++i) {
+            const uint64_t do_mn = mndesc_base(s_do + (i % ND) * kTile);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (!warp_wait(p_full(c), i & 1, p.status)) {
+                    ok = false;
+                    break;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(q_full(i % NQ));
-                    mbar_arrive(st_empty(i % NT));
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = kOrder[4 * c + e];
+                    umma_bf16_ts_elected(leader, t_dv, t_s + packed_col(kk), mndesc_at(do_mn, kk), idesc_g,
+                                         (i > 0 || kk > 0) ? 1u : 0u);
                 }
+            }
+            if (!ok) break;
+            // S^T[i+1] overwrites the S^T buffer after dV[i] has read P^T[i] from it
+            if (i + 1 < n_steps && !issue_s(i + 1)) break;
+            const uint64_t q_mn = mndesc_base(s_q + (i % NQ) * kTile);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (!warp_wait(ds_full(c), i & 1, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = kOrder[4 * c + e];
+                    umma_bf16_ts_elected(leader, t_dk, t_dp + packed_col(kk), mndesc_at(q_mn, kk), idesc_g,
+                                         (i > 0 || kk > 0) ? 1u : 0u);
+                }
+            }
+            if (!ok) break;
+            // Q[i] and dO[i]: dK[i] is the last product that reads either
+            umma_commit_elected(leader, q_empty(i % NQ));
+            if (i + 1 < n_steps && !issue_dp(i + 1)) break;
+        }
+        umma_commit_elected(leader, done);
+        umma_commit_elected(leader, drain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+    } else if (warp == kStats) {
+        // ---------------- statistics warp: step i's lse and D into B operand i % NA
+        const float inv_c = 1.f / p.scale_log2;
+        for (int i = 0; i < n_steps; ++i) {
+            if (!warp_wait(st_full(i % NT), (i / NT) & 1, p.status) ||
+                !warp_wait(aug_empty(i % NA), ((i / NA) & 1) ^ 1u, p.status))
+                break;
+            const float* stat = reinterpret_cast<const float*>(smem_raw + L::kStat + 1024u * (i % NT));
+            uint8_t* aug = smem_raw + L::kAug + (i % NA) * L::kAugTile;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int r = lane + 32 * u;
+                // statistics of rows that see nothing, or behind the last row, reach
+                // hidden columns only, whatever they hold
+                if constexpr (M != kDocCap)
+                    *reinterpret_cast<uint2*>(aug + aug_offset(r, 0)) = split3_bf16(-stat[r] * inv_c);
+                *reinterpret_cast<uint2*>(aug + aug_offset(r, 1)) = split3_bf16(-stat[128 + r]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(q_full(i % NQ));
+                mbar_arrive(st_empty(i % NT));
             }
         }
     } else {
-        registers_claim<kDocBwdMany>();
-        // ---------------- row warps: group gi takes query columns 32 gi .. 32 gi + 31 of every step
-        const int gi = (warp - 4) >> 2;
+        // ---------------- two groups of four warps, one key row per thread in each:
+        // group gi takes query columns 64 gi .. 64 gi + 63 of every step
+        const int gi = (warp - 2) >> 2;
         const int qw = warp & 3;
         const int row = qw * 32 + lane;
         const int k = k0 + row;
         const bool valid = k < p.tokens;
         const int2 see = valid ? p.plan.cols[k] : make_int2(0, 0);
         const bool empty = see.y <= see.x;
-        const uint32_t t_row = (static_cast<uint32_t>(qw * 32) << 16) + 32u * gi;
+        const uint32_t t_row = (static_cast<uint32_t>(qw * 32) << 16) + 64u * gi;
         bool ok = true;
         for (int i = 0; i < n_steps; ++i) {
-            const int qc0 = (range.x + i / group) * kRows + 32 * gi;  // query of this group's first column
+            const int qc0 = (range.x + i / group) * kRows + 64 * gi;  // query of this group's first column
             const int h = g * group + i % group;
             const float slope2 = M != kDocPlain && p.slopes ? p.slopes[h] * kLog2e : 0.f;
             const float x = static_cast<float>(k - qc0);  // the column at distance 0
@@ -1549,83 +1562,97 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 break;
             }
             tc_fence_after();
-            float pr[32];  // P; after the first pass, times the cap's derivative
-            load_tmem32(t_s + t_row, pr);
-            float th[32];
-            if constexpr (M == kDocPlain) {
-                exp_scores<false, 32>(pr, p.scale_log2, 0.f, x, 0.f);
-            } else if constexpr (M == kDocBias) {
-                exp_scores<true, 32>(pr, p.scale_log2, slope2, x, 0.f);
-            } else {
-                const float4* lse4 = reinterpret_cast<const float4*>(p.lse + static_cast<int64_t>(h) * p.ld_stat + qc0);
-                cap_tanh<32>(p, pr);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) th[j] = pr[j];
-                if (p.slopes) bias_scores<32>(pr, p.cap_log2, slope2, x);
-                const float cap2 = p.slopes ? 1.f : p.cap_log2;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 v = lse4[e];
-                    float* s = pr + 4 * e;
-                    split_pair(fma_pair(pair_of(s[0], s[1]), pair_of(cap2, cap2), pair_of(-v.x, -v.y)), s[0], s[1]);
-                    split_pair(fma_pair(pair_of(s[2], s[3]), pair_of(cap2, cap2), pair_of(-v.z, -v.w)), s[2], s[3]);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) s[u] = ex2(s[u]);
-                }
-            }
-            hide_columns<32>(pr, lo, hi, 0.f);
+            float pr[64];  // P; after the first pass, times the cap's derivative
             {
+                uint32_t rs[64];
+                tmem_load_32(t_s + t_row, *reinterpret_cast<uint32_t(*)[32]>(rs));
+                tmem_load_32(t_s + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rs + 32));
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 64; ++j) pr[j] = __uint_as_float(rs[j]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float th[32];
+                if constexpr (M == kDocPlain) {
+                    exp_scores<false, 32>(pr + 32 * c, p.scale_log2, 0.f, x, 0.f);
+                } else if constexpr (M == kDocBias) {
+                    exp_scores<true, 32>(pr + 32 * c, p.scale_log2, slope2, x - 32 * c, 0.f);
+                } else {
+                    const float4* lse4 = reinterpret_cast<const float4*>(p.lse + static_cast<int64_t>(h) * p.ld_stat + qc0 + 32 * c);
+                    cap_tanh<32>(p, pr + 32 * c);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) th[j] = pr[32 * c + j];
+                    if (p.slopes) bias_scores<32>(pr + 32 * c, p.cap_log2, slope2, x - 32 * c);
+                    const float cap2 = p.slopes ? 1.f : p.cap_log2;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 v = lse4[e];
+                        float* s = pr + 32 * c + 4 * e;
+                        split_pair(fma_pair(pair_of(s[0], s[1]), pair_of(cap2, cap2), pair_of(-v.x, -v.y)), s[0], s[1]);
+                        split_pair(fma_pair(pair_of(s[2], s[3]), pair_of(cap2, cap2), pair_of(-v.z, -v.w)), s[2], s[3]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) s[u] = ex2(s[u]);
+                    }
+                }
+                hide_columns<32>(pr + 32 * c, lo - 32 * c, hi - 32 * c, 0.f);
                 uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
-                // the first 16 of the group's columns, all read above
-                tmem_store_16(t_s + t_row, w);
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
+                // packed columns 16 c .. 16 c + 15 of the group's columns, all read above
+                tmem_store_16(t_s + t_row + 16 * c, w);
+                if constexpr (M == kDocCap) times_cap_slope<32>(pr + 32 * c, th);
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(p_full(c), lane);
             }
-            if constexpr (M == kDocCap) times_cap_slope<32>(pr, th);
-            tmem_wait_store();
-            tc_fence_before();
-            warp_arrive(p_full, lane);
             if (!warp_wait(dp_full, i & 1, p.status)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            uint32_t rp[32];
-            tmem_load_32(t_dp + t_row, rp);
+            uint32_t rp[64];
+            tmem_load_32(t_dp + t_row, *reinterpret_cast<uint32_t(*)[32]>(rp));
+            tmem_load_32(t_dp + t_row + 32, *reinterpret_cast<uint32_t(*)[32]>(rp + 32));
             tmem_wait_load();
-            times_sum<32>(pr, rp, 0.f);
-            hide_columns<32>(pr, lo, hi, 0.f);  // a hidden column's dP may be anything
-            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
-            tmem_store_16(t_dp + t_row, w);
-            tmem_wait_store();
-            tc_fence_before();
-            warp_arrive(ds_full, lane);
+            for (int c = 0; c < 2; ++c) {
+                float* ds = pr + 32 * c;
+                times_sum<32>(ds, rp + 32 * c, 0.f);
+                hide_columns<32>(ds, lo - 32 * c, hi - 32 * c, 0.f);  // a hidden column's dP may be anything
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(ds[2 * e], ds[2 * e + 1]);
+                tmem_store_16(t_dp + t_row + 16 * c, w);
+                tmem_wait_store();
+                tc_fence_before();
+                warp_arrive(ds_full(c), lane);
+            }
         }
-        // groups 0 and 1 store the halves of dK, groups 2 and 3 those of dV
+        // group 0 stores dK, group 1 dV
         if (ok && warp_wait(done, 0, p.status)) {
             tc_fence_after();
-            const bool value = gi >= 2;
-            const int c0 = (gi & 1) * (D / 2);
-            const uint32_t t_acc = (value ? t_dv : t_dk) + (static_cast<uint32_t>(qw * 32) << 16) + static_cast<uint32_t>(c0);
-            // every product has been formed: the Q stages serve the results
-            const uint32_t stage = s_q + kStageBytes * static_cast<uint32_t>(warp - 4);
+            const uint32_t t_acc = (gi == 0 ? t_dk : t_dv) + (static_cast<uint32_t>(qw * 32) << 16);
+            const float sc = gi == 0 ? p.scale : 1.f;
+            // every product has been formed: the Q stages serve the results, D / 64 boxes a warp
+            const uint32_t stage = s_q + kStageBytes * static_cast<uint32_t>((warp - 2) * (D / 64));
             bool again = false;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-                float r[32];
-                load_tmem32(t_acc + 32 * c, r);
-                again |= !finite32(r);
-                stage32<D>(stage, lane, c, r, value ? 1.f : p.scale, empty);
+                float r[2][32];
+                load_tmem32(t_acc + 64 * c, r[0]);
+                load_tmem32(t_acc + 64 * c + 32, r[1]);
+                again |= !finite32(r[0]) || !finite32(r[1]);
+                stage32(stage + c * kStageBytes, lane, 0, r[0], sc, empty);
+                stage32(stage + c * kStageBytes, lane, 1, r[1], sc, empty);
+                if (k - lane < p.tokens) store_stage(&map_out, stage + c * kStageBytes, lane, (gi == 0 ? kcol : vcol) + 64 * c, k - lane);
             }
-            if (k - lane < p.tokens) store_stage(&map_out, stage, lane, (value ? vcol : kcol) + c0, k - lane);
             uint32_t redo = __ballot_sync(0xffffffffu, again && valid && !empty);
             if (redo) stores_done(lane);
             while (redo) {
                 const int src = __ffs(redo) - 1;
                 redo &= redo - 1;
-                document_dkv_row<D>(p, k - lane + src, g, lane, value, c0, c0 + D / 2);
+                document_dkv_row<D>(p, k - lane + src, g, lane, gi == 1);
             }
             stage_free(lane);  // shared memory outlives the stores that read it
         }
@@ -1644,7 +1671,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
 // free.  (The causal core runs them on two streams, which costs a small call a
 // fork and a join, and makes one stream and counter the whole device's.)
 template <int D, int M>
-__global__ void __launch_bounds__(kDocBwdThreads, 1)
+__global__ void __launch_bounds__(kAttnDqThreads, 1)
     document_bwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ CUtensorMap map_do,
                         const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_dq,
                         const __grid_constant__ DocArgs p) {
@@ -1685,21 +1712,11 @@ DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const flo
 
 DocMode mode_of(const DocArgs& p) { return p.cap > 0.f ? kDocCap : p.slopes ? kDocBias : kDocPlain; }
 
-// A kernel whose warpgroups trade registers must have been launched with as many as
-// they claim in all, or the last claim would wait for ever.
-template <typename K>
-cudaError_t prepare_kernel(K kern, size_t smem, int regs) {
-    cudaFuncAttributes attr;
-    const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    return attr.numRegs >= regs ? set_smem(kern, smem) : cudaErrorInvalidConfiguration;
-}
-
 template <int D, int M>
 cudaError_t forward(const DocArgs& p, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] { err = prepare_kernel(document_fwd_kernel<D, M>, DocFwdSmem<D>::kBytes, kDocFwdRegs); });
+    std::call_once(once, [] { err = set_smem(document_fwd_kernel<D, M>, DocFwdSmem<D>::kBytes); });
     if (err != cudaSuccess) return err;
     const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
     CUtensorMap map, out;
@@ -1714,12 +1731,12 @@ template <int D, int M>
 cudaError_t backward(const DocArgs& p, const uint16_t* a, float* dvec, bool d_ready, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] { err = prepare_kernel(document_bwd_kernel<D, M>, doc_bwd_smem<D>(), kDocBwdRegs); });
+    std::call_once(once, [] { err = set_smem(document_bwd_kernel<D, M>, doc_bwd_smem<D>()); });
     if (err != cudaSuccess) return err;
     const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
-    CUtensorMap mq, md, mo, mdq;  // dk and dv leave in boxes of half a head, dq of 32 columns
+    CUtensorMap mq, md, mo, mdq;  // dq leaves in boxes of half a head
     if (!attn_map(&mq, p.qkv, p.tokens, width, width) || !attn_map(&md, p.da, p.tokens, p.n_heads * D, p.n_heads * D) ||
-        !attn_map(&mo, p.out, p.tokens, width, width, 32, D / 2) || !attn_map(&mdq, p.out, p.tokens, width, width, 32, 32))
+        !attn_map(&mo, p.out, p.tokens, width, width, 32) || !attn_map(&mdq, p.out, p.tokens, width, width, 32, D / 2))
         return cudaErrorInvalidValue;
     if (d_ready) {
         const cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(int), stream);
@@ -1733,7 +1750,7 @@ cudaError_t backward(const DocArgs& p, const uint16_t* a, float* dvec, bool d_re
     }
     const int64_t dkv = static_cast<int64_t>(p.n_blocks) * p.n_kv_heads;
     const int64_t dq = std::min<int64_t>(static_cast<int64_t>(p.n_blocks) * p.n_heads, sm_count());
-    document_bwd_kernel<D, M><<<static_cast<unsigned>(dkv + dq), kDocBwdThreads, doc_bwd_smem<D>(), stream>>>(mq, md, mo, mdq, p);
+    document_bwd_kernel<D, M><<<static_cast<unsigned>(dkv + dq), kAttnDqThreads, doc_bwd_smem<D>(), stream>>>(mq, md, mo, mdq, p);
     return cudaGetLastError();
 }
 
