@@ -112,17 +112,20 @@ struct DocArgs {
     float cap, scale;
     float scale_log2;      // log2(e) / sqrt(d)
     float cap_log2;        // cap log2(e)
-    float cap_rate;        // 1 / (cap sqrt(d))
-    float cap_poly[5];     // tanh(s cap_rate) / s as a polynomial in s^2
+    float cap_limit;       // the square of 3/4 cap sqrt(d)
+    float cap_poly[5];     // tanh(s / (cap sqrt(d))) / s as a polynomial in s^2
     float cap_exp;         // 2 log2(e) / (cap sqrt(d)): the exponent of e^(2 s / cap) per unit of q . k
     int tokens, n_heads, n_kv_heads, ld_stat, n_blocks;
     int* status;
 };
 
-// How scores are modified: not at all, by the distance, or by the cap (and the
-// distance).  Every kernel exists once for each, so that a plain batch pays for
-// neither.
-enum DocMode : int { kDocPlain = 0, kDocBias = 1, kDocCap = 2 };
+// How scores are modified: not at all, by the distance, by the cap, or by both.
+// Every kernel exists once for each: what a batch does not use would cost it
+// instructions, and room in the instruction caches (the capped backward took 7 %
+// longer with the distance's code beside it, never run).
+enum DocMode : int { kDocPlain = 0, kDocBias = 1, kDocCap = 2, kDocCapBias = 3 };
+__host__ __device__ constexpr bool mode_caps(int m) { return m >= kDocCap; }
+__host__ __device__ constexpr bool mode_biases(int m) { return m == kDocBias || m == kDocCapBias; }
 
 // ------------------------------------------------------------------------ row by row
 
@@ -287,7 +290,7 @@ __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < N; c += 2) top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
-    if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.cap_rate <= 0.75f)) {
+    if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= p.cap_limit)) {
         uint64_t k[5];
 #pragma unroll
         for (int e = 0; e < 5; ++e) k[e] = pair_of(p.cap_poly[e], p.cap_poly[e]);
@@ -306,31 +309,47 @@ __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
     }
 }
 
-// s <- mul s - slope |c - at| for N columns c of a row.
-template <int N>
-__device__ __forceinline__ void bias_scores(float* s, float mul, float slope, float at) {
-    const uint64_t mul2 = pair_of(mul, mul), step2 = pair_of(-slope, -slope), at2 = pair_of(-at, -at);
+// s <- mul s - slope |c - at| + add for N columns c of a row, and its power of two.
+// Where the warp's columns all lie on one side of their rows' distance 0 the distance
+// is linear: one multiply-add of the column number, without an absolute value.
+// (kSides: with that form as well; under a cap its code would only crowd the rest out
+// of the instruction caches.)
+template <bool kExp, int N, bool kSides>
+__device__ __forceinline__ void bias_scores(float* s, float mul, float slope, float at, float add) {
+    const uint64_t mul2 = pair_of(mul, mul);
+    const bool before = kSides && __all_sync(0xffffffffu, at >= static_cast<float>(N - 1));
+    if (before || (kSides && __all_sync(0xffffffffu, at <= 0.f))) {
+        const float step = before ? slope : -slope;
+        const uint64_t step2 = pair_of(step, step);
+        const float base = fmaf(-step, at, add);
+        const uint64_t base2 = pair_of(base, base);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const uint64_t rest = fma_pair(step2, pair_of(static_cast<float>(c), static_cast<float>(c + 1)), base2);
+            split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest), s[c], s[c + 1]);
+            if (kExp) s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
+        }
+        return;
+    }
+    const uint64_t step2 = pair_of(-slope, -slope), at2 = pair_of(-at, -at), add2 = pair_of(add, add);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
         float a, b;
         split_pair(add_pair(pair_of(static_cast<float>(c), static_cast<float>(c + 1)), at2), a, b);
-        split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, mul_pair(step2, pair_of(fabsf(a), fabsf(b)))), s[c], s[c + 1]);
+        const uint64_t rest = fma_pair(step2, pair_of(fabsf(a), fabsf(b)), add2);
+        split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest), s[c], s[c + 1]);
+        if (kExp) s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
     }
 }
 
-// s <- 2^(mul s - slope |c - at| + add) for N columns.
-template <bool kSlope, int N>
-__device__ __forceinline__ void exp_scores(float* s, float mul, float slope, float at, float add) {
-    const uint64_t mul2 = pair_of(mul, mul), add2 = pair_of(add, add), step2 = pair_of(-slope, -slope), at2 = pair_of(-at, -at);
+// s <- 2^(mul s + add).
+template <int N>
+__device__ __forceinline__ void exp_scores(float* s, float mul, float add) {
+    const uint64_t mul2 = pair_of(mul, mul), add2 = pair_of(add, add);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-        uint64_t rest = add2;
         float a, b;
-        if (kSlope) {
-            split_pair(add_pair(pair_of(static_cast<float>(c), static_cast<float>(c + 1)), at2), a, b);
-            rest = fma_pair(step2, pair_of(fabsf(a), fabsf(b)), add2);
-        }
-        split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest), a, b);
+        split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, add2), a, b);
         s[c] = ex2(a);
         s[c + 1] = ex2(b);
     }
@@ -366,6 +385,7 @@ __device__ __forceinline__ uint32_t columns_in(int lo, int hi) {
 // columns skips them.
 template <int N>
 __device__ __forceinline__ void hide_columns(float* s, int lo, int hi, float hidden) {
+    if (__all_sync(0xffffffffu, lo <= 0 && hi >= N)) return;
 #pragma unroll
     for (int b = 0; b < N; b += 32) {
         const uint32_t in = columns_in(lo - b, hi - b);
@@ -525,7 +545,7 @@ struct DocFwdSmem {
     // Q full / empty, the K / V ring, S, P and done of both tiles, tile slots full / empty, answer, drain
     static constexpr int kNumBars = 2 + 2 * kStages + 6 + 4 + 2;
     static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
-    static constexpr uint32_t kTileSlot = kTmemSlot + 16;  // two slots of a tile's number, first key block and steps
+    static constexpr uint32_t kTileSlot = kTmemSlot + 16;  // two slots of a tile's place, first key block and steps
     static constexpr uint32_t kRowSlot = kTileSlot + 2 * 16;  // and of its rows' intervals
     static constexpr size_t kUsed = kRowSlot + 2 * 1024;
     static constexpr size_t kBytes = kUsed > kMinSmem ? kUsed : kMinSmem;
@@ -541,8 +561,8 @@ struct DocFwdSmem {
 // their place), warps 4-7 and 8-11 are the softmax rows of tiles A and B.  The
 // first hands registers to the other two.
 constexpr int kDocFwdThreads = 384;
-constexpr int kDocFwdFew = 56, kDocFwdMany = 224;
-static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * 168, "registers of the launch: 168 a thread");
+constexpr int kDocFwdRegs = 168, kDocFwdFew = 56, kDocFwdMany = 224;
+static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * kDocFwdRegs, "registers of the launch");
 
 template <int D, int M>
 __global__ void __launch_bounds__(kDocFwdThreads, 1)
@@ -603,20 +623,18 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     // buffer once read), O_A 256.., O_B 384..
     auto t_s = [&](int x) { return tmem_base + 128u * static_cast<uint32_t>(x); };
     auto t_o = [&](int x) { return tmem_base + 256u + 128u * static_cast<uint32_t>(x); };
-    // A consumer warp's view of tile slot n & 1 (-1: none left), after which the
-    // warp releases the slot; `see`: its row of tile x's intervals.
-    auto take_tile = [&](uint32_t n, FwdTile& f, int x, int row, int2& see) {
+    // Tile B is the next head, or (odd groups) the next query block.
+    const bool two_heads = (p.n_heads / p.n_kv_heads) % 2 == 0;
+    // A consumer warp's view of tile slot n & 1: the first query row of tile A (-1: no
+    // tile left), its head, the first key block and the steps; `see`: the intervals of
+    // its row of tile A.  Then the warp releases the slot.
+    auto take_tile = [&](uint32_t n, int row, int4& tile, int2& see) {
         if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
-        const int4 slot = tile_slot[n & 1u];
+        tile = tile_slot[n & 1u];
         see = row_slot[(n & 1u) * kRows + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(tile_empty(n & 1u));
-        if (slot.x < 0) return false;
-        f = fwd_place(p, slot.x);
-        f.first = slot.y;
-        f.nk = slot.z;
-        if (f.q0[x] != f.q0[0]) see = f.q0[x] < p.n_blocks * kRows ? p.plan.rows[f.q0[x] + row] : make_int2(0, 0);
-        return true;
+        return tile.x >= 0;
     };
 
     if (warp < 4) {
@@ -628,7 +646,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 for (uint32_t n = 0;; ++n) {
                     if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) break;
                     const FwdTile f = t >= 0 ? fwd_tile(p, t) : FwdTile{};
-                    *reinterpret_cast<int4*>(smem_raw + L::kTileSlot + 16 * (n & 1u)) = make_int4(t, f.first, f.nk, 0);
+                    *reinterpret_cast<int4*>(smem_raw + L::kTileSlot + 16 * (n & 1u)) = t < 0 ? make_int4(-1, 0, 0, 0) : make_int4(f.q0[0], f.h[0], f.first, f.nk);
                     ++nt;
                     if (t < 0) {
                         mbar_arrive(tile_full(n & 1u));
@@ -715,10 +733,10 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
             uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
             bool ok = true;
             for (uint32_t n = 0; ok; ++n) {
-                FwdTile f;
+                int4 tile;
                 int2 unused;
-                if (!take_tile(n, f, 0, 0, unused)) break;
-                const int nk = f.nk;
+                if (!take_tile(n, 0, tile, unused)) break;
+                const int nk = tile.w;
                 if (nk == 0) continue;
                 if (!warp_wait(q_full, nq & 1u, p.status) || !kv_ready(g)) break;
                 ++nq;
@@ -762,18 +780,20 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
         uint32_t g = 0, nd = 0;  // steps and tiles with steps so far
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
-            FwdTile f;
+            int4 tile;
             int2 see;
-            if (!take_tile(n, f, x, row, see)) break;
-            const int h = x ? f.h[1] : f.h[0];
-            const int q = (x ? f.q0[1] : f.q0[0]) + row;
+            if (!take_tile(n, row, tile, see)) break;
+            const int first = tile.z, nk = tile.w;
+            const int h = two_heads ? tile.y + x : tile.y;
+            const int q = (two_heads ? tile.x : tile.x + x * kRows) + row;
             const bool valid = q < p.tokens;
+            if (!two_heads && x && valid) see = p.plan.rows[q];
             if (!valid) see = make_int2(0, 0);
             const bool empty = see.y <= see.x;
-            const float slope2 = M != kDocPlain && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+            const float slope2 = mode_biases(M) ? p.slopes[h] * kLog2e : 0.f;
             // -1e30, not -infinity: a row that has seen no key yet keeps finite differences
             float m = -1e30f, l = 0.f;
-            for (int j = 0; j < f.nk; ++j, ++g) {
+            for (int j = 0; j < nk; ++j, ++g) {
                 if (!warp_wait(s_full(x), g & 1u, p.status)) {
                     ok = false;
                     break;
@@ -789,17 +809,18 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(r[e]);
                 }
-                const int k0 = (f.first + j) * kRows;
+                const int k0 = (first + j) * kRows;
                 // unmodified (and capped, undistanced) scores are scaled below and in the exponent's FMA
                 float sc = 1.f;
                 if constexpr (M == kDocPlain) sc = p.scale_log2;
-                if constexpr (M == kDocCap) {
-                    cap_tanh<128>(p, s);
+                if constexpr (mode_caps(M)) {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) cap_tanh<32>(p, s + c);
                     sc = p.cap_log2;
                 }
-                if (M == kDocBias || (M == kDocCap && p.slopes)) {
+                if constexpr (mode_biases(M)) {
                     const float mul = M == kDocBias ? p.scale_log2 : p.cap_log2, at = static_cast<float>(q - k0);
-                    bias_scores<128>(s, mul, slope2, at);
+                    bias_scores<false, 128, M == kDocBias>(s, mul, slope2, at, 0.f);
                     sc = 1.f;
                 }
                 hide_columns<128>(s, see.x - k0, see.y - k0, -INFINITY);
@@ -859,7 +880,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
             if (!ok) break;
             bool again = false;  // not finite: formed again below
             float inv = 0.f;
-            if (f.nk > 0) {
+            if (nk > 0) {
                 if (!warp_wait(done(x), nd & 1u, p.status)) break;
                 ++nd;
                 tc_fence_after();
@@ -870,7 +891,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 float o[2][32] = {};
-                if (f.nk > 0) {
+                if (nk > 0) {
                     load_tmem32(to + t_row + 64 * c, o[0]);
                     load_tmem32(to + t_row + 64 * c + 32, o[1]);
                     again |= !finite32(o[0]) || !finite32(o[1]);
@@ -1186,7 +1207,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             const bool empty = see.y <= see.x;
             const float lse = empty ? 0.f : p.lse[static_cast<int64_t>(tl.h) * p.ld_stat + q];
             const float dv = empty ? 0.f : p.dvec[static_cast<int64_t>(tl.h) * p.ld_stat + q];
-            const float slope2 = M != kDocPlain && p.slopes ? p.slopes[tl.h] * kLog2e : 0.f;
+            const float slope2 = mode_biases(M) ? p.slopes[tl.h] * kLog2e : 0.f;
             for (int j = 0; j < tl.nk; ++j, ++g) {
                 const int c0 = (tl.kb0 + j) * kRows + 64 * gi;
                 if (!warp_wait(s_full(g & 1u), (g >> 1) & 1u, p.status)) {
@@ -1205,18 +1226,19 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 }
                 const float x = static_cast<float>(q - c0);
                 if constexpr (M == kDocPlain) {
-                    exp_scores<false, 64>(pr, p.scale_log2, 0.f, x, -lse);
+                    exp_scores<64>(pr, p.scale_log2, -lse);
                 } else if constexpr (M == kDocBias) {
-                    exp_scores<true, 64>(pr, p.scale_log2, slope2, x, -lse);
+                    bias_scores<true, 64, true>(pr, p.scale_log2, slope2, x, -lse);
                 } else {
                     float th[64];
-                    cap_tanh<64>(p, pr);
+                    cap_tanh<32>(p, pr);
+                    cap_tanh<32>(p, pr + 32);
 #pragma unroll
                     for (int i = 0; i < 64; ++i) th[i] = pr[i];
-                    if (p.slopes)
-                        exp_scores<true, 64>(pr, p.cap_log2, slope2, x, -lse);
+                    if constexpr (mode_biases(M))
+                        bias_scores<true, 64, false>(pr, p.cap_log2, slope2, x, -lse);
                     else
-                        exp_scores<false, 64>(pr, p.cap_log2, 0.f, x, -lse);
+                        exp_scores<64>(pr, p.cap_log2, -lse);
                     times_cap_slope<64>(pr, th);
                 }
                 if (!warp_wait(dp_full, g & 1u, p.status)) {
@@ -1452,7 +1474,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 umma_bf16_elected(leader, t_s, kdesc_at(k_desc, kk), kdesc_at(q_desc, kk), idesc_s, kk > 0);
-            if constexpr (M != kDocCap)
+            if constexpr (!mode_caps(M))
                 umma_bf16_elected(leader, t_s, ones_lse, aug_desc(s_aug + (i % NA) * L::kAugTile), idesc_s, 1u);
             umma_commit_elected(leader, s_full);
             return true;
@@ -1528,7 +1550,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 const int r = lane + 32 * u;
                 // statistics of rows that see nothing, or behind the last row, reach
                 // hidden columns only, whatever they hold
-                if constexpr (M != kDocCap)
+                if constexpr (!mode_caps(M))
                     *reinterpret_cast<uint2*>(aug + aug_offset(r, 0)) = split3_bf16(-stat[r] * inv_c);
                 *reinterpret_cast<uint2*>(aug + aug_offset(r, 1)) = split3_bf16(-stat[128 + r]);
             }
@@ -1554,7 +1576,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
         for (int i = 0; i < n_steps; ++i) {
             const int qc0 = (range.x + i / group) * kRows + 64 * gi;  // query of this group's first column
             const int h = g * group + i % group;
-            const float slope2 = M != kDocPlain && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+            const float slope2 = mode_biases(M) ? p.slopes[h] * kLog2e : 0.f;
             const float x = static_cast<float>(k - qc0);  // the column at distance 0
             const int lo = see.x - qc0, hi = see.y - qc0;  // this key's queries
             if (!warp_wait(s_full, i & 1, p.status)) {
@@ -1575,16 +1597,16 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             for (int c = 0; c < 2; ++c) {
                 float th[32];
                 if constexpr (M == kDocPlain) {
-                    exp_scores<false, 32>(pr + 32 * c, p.scale_log2, 0.f, x, 0.f);
+                    exp_scores<32>(pr + 32 * c, p.scale_log2, 0.f);
                 } else if constexpr (M == kDocBias) {
-                    exp_scores<true, 32>(pr + 32 * c, p.scale_log2, slope2, x - 32 * c, 0.f);
+                    bias_scores<true, 32, true>(pr + 32 * c, p.scale_log2, slope2, x - 32 * c, 0.f);
                 } else {
                     const float4* lse4 = reinterpret_cast<const float4*>(p.lse + static_cast<int64_t>(h) * p.ld_stat + qc0 + 32 * c);
                     cap_tanh<32>(p, pr + 32 * c);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) th[j] = pr[32 * c + j];
-                    if (p.slopes) bias_scores<32>(pr + 32 * c, p.cap_log2, slope2, x - 32 * c);
-                    const float cap2 = p.slopes ? 1.f : p.cap_log2;
+                    if constexpr (mode_biases(M)) bias_scores<false, 32, false>(pr + 32 * c, p.cap_log2, slope2, x - 32 * c, 0.f);
+                    const float cap2 = mode_biases(M) ? 1.f : p.cap_log2;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 v = lse4[e];
@@ -1601,7 +1623,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(pr[32 * c + 2 * e], pr[32 * c + 2 * e + 1]);
                 // packed columns 16 c .. 16 c + 15 of the group's columns, all read above
                 tmem_store_16(t_s + t_row + 16 * c, w);
-                if constexpr (M == kDocCap) times_cap_slope<32>(pr + 32 * c, th);
+                if constexpr (mode_caps(M)) times_cap_slope<32>(pr + 32 * c, th);
                 tmem_wait_store();
                 tc_fence_before();
                 warp_arrive(p_full(c), lane);
@@ -1695,11 +1717,12 @@ DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const flo
     p.scale = 1.f / sqrtf(static_cast<float>(s.head_dim));
     p.scale_log2 = kLog2e * p.scale;
     p.cap_log2 = cap * kLog2e;
-    p.cap_rate = cap > 0.f ? p.scale / cap : 0.f;
-    p.cap_exp = 2.f * kLog2e * p.cap_rate;
+    const float cap_rate = cap > 0.f ? p.scale / cap : 0.f;
+    p.cap_limit = cap > 0.f ? 0.75f / cap_rate : 0.f;
+    p.cap_exp = 2.f * kLog2e * cap_rate;
     const double tanh_poly[5] = {0.999999434947, -0.333282515696, 0.132589833556, -0.0500563036011, 0.0129296314219};
-    double power = p.cap_rate;  // cap_rate^(2 k + 1)
-    for (int k = 0; k < 5; ++k, power *= static_cast<double>(p.cap_rate) * p.cap_rate)
+    double power = cap_rate;  // cap_rate^(2 k + 1)
+    for (int k = 0; k < 5; ++k, power *= static_cast<double>(cap_rate) * cap_rate)
         p.cap_poly[k] = static_cast<float>(tanh_poly[k] * power);
     p.tokens = s.tokens;
     p.n_heads = s.n_heads;
@@ -1710,13 +1733,25 @@ DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const flo
     return p;
 }
 
-DocMode mode_of(const DocArgs& p) { return p.cap > 0.f ? kDocCap : p.slopes ? kDocBias : kDocPlain; }
+DocMode mode_of(const DocArgs& p) {
+    return p.cap > 0.f ? (p.slopes ? kDocCapBias : kDocCap) : (p.slopes ? kDocBias : kDocPlain);
+}
+
+// A kernel whose warpgroups trade registers must have been launched with as many as
+// they claim in all, or the last claim would wait for ever.
+template <typename K>
+cudaError_t prepare_kernel(K kern, size_t smem, int regs) {
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    return attr.numRegs >= regs ? set_smem(kern, smem) : cudaErrorInvalidConfiguration;
+}
 
 template <int D, int M>
 cudaError_t forward(const DocArgs& p, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] { err = set_smem(document_fwd_kernel<D, M>, DocFwdSmem<D>::kBytes); });
+    std::call_once(once, [] { err = prepare_kernel(document_fwd_kernel<D, M>, DocFwdSmem<D>::kBytes, kDocFwdRegs); });
     if (err != cudaSuccess) return err;
     const int width = (p.n_heads + 2 * p.n_kv_heads) * D;
     CUtensorMap map, out;
@@ -1759,7 +1794,8 @@ cudaError_t forward_mode(const DocArgs& p, cudaStream_t stream) {
     switch (mode_of(p)) {
         case kDocPlain: return forward<D, kDocPlain>(p, stream);
         case kDocBias: return forward<D, kDocBias>(p, stream);
-        default: return forward<D, kDocCap>(p, stream);
+        case kDocCap: return forward<D, kDocCap>(p, stream);
+        default: return forward<D, kDocCapBias>(p, stream);
     }
 }
 
@@ -1768,7 +1804,8 @@ cudaError_t backward_mode(const DocArgs& p, const uint16_t* a, float* dvec, bool
     switch (mode_of(p)) {
         case kDocPlain: return backward<D, kDocPlain>(p, a, dvec, d_ready, stream);
         case kDocBias: return backward<D, kDocBias>(p, a, dvec, d_ready, stream);
-        default: return backward<D, kDocCap>(p, a, dvec, d_ready, stream);
+        case kDocCap: return backward<D, kDocCap>(p, a, dvec, d_ready, stream);
+        default: return backward<D, kDocCapBias>(p, a, dvec, d_ready, stream);
     }
 }
 
