@@ -542,9 +542,10 @@ struct DocFwdSmem {
     static constexpr uint32_t kStage = kKV + 2 * kStages * kTile;  // results, 4 KiB a row warp
     static constexpr uint32_t kAnswer = kStage + 8 * kStageBytes;   // 16 bytes
     static constexpr uint32_t kBars = kAnswer + 16;
-    // Q full / empty, the K / V ring, S, P and done of both tiles, tile slots full / empty, answer, drain
-    static constexpr int kNumBars = 2 + 2 * kStages + 6 + 4 + 2;
-    static constexpr uint32_t kTmemSlot = kBars + 8 * kNumBars;
+    // Q full / empty, the K / V ring, S, P and PV of both tiles (two of each in turn), tile slots full / empty,
+    // answer, drain
+    static constexpr int kNumBars = 2 + 2 * kStages + 12 + 4 + 2;
+    static constexpr uint32_t kTmemSlot = (kBars + 8 * kNumBars + 15) / 16 * 16;
     static constexpr uint32_t kTileSlot = kTmemSlot + 16;  // two slots of a tile's place, first key block and steps
     static constexpr uint32_t kRowSlot = kTileSlot + 2 * 16;  // and of its rows' intervals
     static constexpr size_t kUsed = kRowSlot + 2 * 1024;
@@ -583,12 +584,15 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     auto kv_full = [&](uint32_t s) { return bars + 8u * (2 + s); };
     auto kv_empty = [&](uint32_t s) { return bars + 8u * (2 + NS + s); };
     constexpr int kB = 2 + 2 * NS;
-    auto s_full = [&](int x) { return bars + 8u * (kB + x); };
-    auto p_full = [&](int x) { return bars + 8u * (kB + 2 + x); };
-    auto done = [&](int x) { return bars + 8u * (kB + 4 + x); };
-    auto tile_full = [&](uint32_t s) { return bars + 8u * (kB + 6 + s); };
-    auto tile_empty = [&](uint32_t s) { return bars + 8u * (kB + 8 + s); };
-    const uint32_t answer_full = bars + 8u * (kB + 10), drain = bars + 8u * (kB + 11);
+    // Step g of tile x.  Two barriers in turn: a third score buffer lets a tile's scores
+    // run one step ahead of its softmax, so one warp of it can be a step ahead of
+    // another, and its arrival must not count for the step before.
+    auto s_full = [&](int x, uint32_t g) { return bars + 8u * (kB + 2 * x + (g & 1u)); };
+    auto p_full = [&](int x, uint32_t g) { return bars + 8u * (kB + 4 + 2 * x + (g & 1u)); };
+    auto pv_done = [&](int x, uint32_t g) { return bars + 8u * (kB + 8 + 2 * x + (g & 1u)); };
+    auto tile_full = [&](uint32_t s) { return bars + 8u * (kB + 12 + s); };
+    auto tile_empty = [&](uint32_t s) { return bars + 8u * (kB + 14 + s); };
+    const uint32_t answer_full = bars + 8u * (kB + 16), drain = bars + 8u * (kB + 17);
     const uint32_t tmem_slot = base + L::kTmemSlot;
     volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + L::kTmemSlot);
     const int4* tile_slot = reinterpret_cast<const int4*>(smem_raw + L::kTileSlot);
@@ -603,9 +607,11 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
             mbar_init(kv_empty(s), 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(s_full(x), 1);
-            mbar_init(p_full(x), 4);
-            mbar_init(done(x), 1);
+            for (uint32_t g = 0; g < 2; ++g) {
+                mbar_init(s_full(x, g), 1);
+                mbar_init(p_full(x, g), 4);
+                mbar_init(pv_done(x, g), 1);
+            }
             mbar_init(tile_full(x), 1);
             mbar_init(tile_empty(x), 9);  // the MMA warp and the eight row warps
         }
@@ -619,10 +625,14 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
-    // columns: S_A 0-127, S_B 128-255 (P packed into the first 64 columns of its
-    // buffer once read), O_A 256.., O_B 384..
-    auto t_s = [&](int x) { return tmem_base + 128u * static_cast<uint32_t>(x); };
-    auto t_o = [&](int x) { return tmem_base + 256u + 128u * static_cast<uint32_t>(x); };
+    // Tensor memory, heads of 128: S_A 0-127, S_B 128-255, O_A 256-383, O_B 384-511.
+    // Heads of 64 leave room for a third score buffer: the tiles' score blocks A0, B0,
+    // A1, B1, .. take buffers 0-127, 128-255, 256-383 in turn, O_A is 384-447, O_B
+    // 448-511.  P is packed into the first 64 columns of its scores' buffer.
+    auto t_s = [&](int x, uint32_t g) {
+        return tmem_base + 128u * (D == 64 ? (2u * g + static_cast<uint32_t>(x)) % 3u : static_cast<uint32_t>(x));
+    };
+    auto t_o = [&](int x) { return tmem_base + (D == 64 ? 384u + 64u * x : 256u + 128u * x); };
     // Tile B is the next head, or (odd groups) the next query block.
     const bool two_heads = (p.n_heads / p.n_kv_heads) % 2 == 0;
     // A consumer warp's view of tile slot n & 1: the first query row of tile A (-1: no
@@ -712,17 +722,18 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                                b_desc = kdesc_base(s_kv + 2 * (g % NS) * kTile);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_elected(leader, t_s(x), kdesc_at(a_desc, kk), kdesc_at(b_desc, kk), idesc_s, kk > 0);
-                umma_commit_elected(leader, s_full(x));
+                    umma_bf16_elected(leader, t_s(x, g), kdesc_at(a_desc, kk), kdesc_at(b_desc, kk), idesc_s, kk > 0);
+                umma_commit_elected(leader, s_full(x, g));
             };
             auto issue_pv = [&](int x, uint32_t g, bool first) {
-                if (!warp_wait(p_full(x), g & 1u, p.status)) return false;
+                if (!warp_wait(p_full(x, g), (g >> 1) & 1u, p.status)) return false;
                 tc_fence_after();
                 const uint64_t v_desc = mndesc_base(s_kv + (2 * (g % NS) + 1) * kTile);
 #pragma unroll
                 for (int kk = 0; kk < kRows / 16; ++kk)
-                    umma_bf16_ts_elected(leader, t_o(x), t_s(x) + 8 * kk, mndesc_at(v_desc, kk), idesc_o,
+                    umma_bf16_ts_elected(leader, t_o(x), t_s(x, g) + 8 * kk, mndesc_at(v_desc, kk), idesc_o,
                                          (!first || kk > 0) ? 1u : 0u);
+                umma_commit_elected(leader, pv_done(x, g));
                 return true;
             };
             auto kv_ready = [&](uint32_t g) {
@@ -743,27 +754,29 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 issue_s(0, g);
                 issue_s(1, g);
                 if (nk == 1) umma_commit_elected(leader, q_empty);
+                // Heads of 128: PV_A[j], S_A[j+1], PV_B[j], S_B[j+1]; S_X[j+1] overwrites
+                // P_X[j].  Heads of 64: S_A[j+1], PV_A[j], S_B[j+1], PV_B[j]; S_A[j+1]
+                // overwrites P_B[j-1], S_B[j+1] P_A[j]: a tile's next scores are there when
+                // its softmax has finished the last ones.
                 for (int j = 0; j < nk; ++j, ++g) {
                     const bool more = j + 1 < nk;
-                    if (!issue_pv(0, g, j == 0) || (more && !kv_ready(g + 1))) {
-                        ok = false;
-                        break;
-                    }
-                    if (more)
+                    ok = false;
+                    if (D == 64 && more) {
+                        if (!kv_ready(g + 1)) break;
                         issue_s(0, g + 1);
-                    else
-                        umma_commit_elected(leader, done(0));
-                    if (!issue_pv(1, g, j == 0)) {
-                        ok = false;
-                        break;
                     }
+                    if (!issue_pv(0, g, j == 0)) break;
+                    if (D == 128 && more) {
+                        if (!kv_ready(g + 1)) break;
+                        issue_s(0, g + 1);
+                    }
+                    if (D == 64 && more) issue_s(1, g + 1);
+                    if (!issue_pv(1, g, j == 0)) break;
                     umma_commit_elected(leader, kv_empty(g % NS));
-                    if (more)
-                        issue_s(1, g + 1);
-                    else
-                        umma_commit_elected(leader, done(1));
+                    if (D == 128 && more) issue_s(1, g + 1);
                     // Q is free for the next tile once its last scores are formed
                     if (j + 2 == nk) umma_commit_elected(leader, q_empty);
+                    ok = true;
                 }
             }
             umma_commit_elected(leader, drain);
@@ -776,8 +789,8 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
         const int qw = warp & 3;
         const int row = qw * 32 + lane;
         const uint32_t t_row = static_cast<uint32_t>(qw * 32) << 16;
-        const uint32_t ts = t_s(x), to = t_o(x);
-        uint32_t g = 0, nd = 0;  // steps and tiles with steps so far
+        const uint32_t to = t_o(x);
+        uint32_t g = 0;  // steps so far
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
             int4 tile;
@@ -794,11 +807,12 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
             // -1e30, not -infinity: a row that has seen no key yet keeps finite differences
             float m = -1e30f, l = 0.f;
             for (int j = 0; j < nk; ++j, ++g) {
-                if (!warp_wait(s_full(x), g & 1u, p.status)) {
+                if (!warp_wait(s_full(x, g), (g >> 1) & 1u, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const uint32_t ts = t_s(x, g);
                 float s[128];
                 {
                     uint32_t r[128];
@@ -839,7 +853,12 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     // A row's maximum rose far above its reference: the warp rescales
                     // O and l of all its rows to their new maxima (warp-wide
                     // tensor-memory loads and stores; rescaling to any larger
-                    // reference is exact).  PV_X[j-1] completed before S_X[j].
+                    // reference is exact), after PV_X[j-1].
+                    if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                     const float m_new = fmaxf(m, mx);
                     const float alpha = ex2(m - m_new);
                     l *= alpha;
@@ -875,14 +894,13 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 l += la + lb;
                 tmem_wait_store();
                 tc_fence_before();
-                warp_arrive(p_full(x), lane);
+                warp_arrive(p_full(x, g), lane);
             }
             if (!ok) break;
             bool again = false;  // not finite: formed again below
             float inv = 0.f;
             if (nk > 0) {
-                if (!warp_wait(done(x), nd & 1u, p.status)) break;
-                ++nd;
+                if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status)) break;
                 tc_fence_after();
                 inv = 1.f / l;
                 again = !(fabsf(inv) <= 3e38f);
