@@ -56,6 +56,11 @@ class zb_rotary_config(ctypes.Structure):
                 ("context", c_double), ("low", c_double), ("high", c_double)]
 
 
+class zb_attention_options(ctypes.Structure):
+    _fields_ = [("rotary_dim", c_int32), ("rotary_pairs", c_int32), ("turns", c_void_p), ("magnitude", c_float),
+                ("cap", c_float), ("slopes", c_void_p)]
+
+
 class zb_adamw_tensor(ctypes.Structure):
     _fields_ = [("param", c_void_p), ("master", c_void_p), ("grad", c_void_p), ("m", c_void_p), ("v", c_void_p),
                 ("m_scale", c_void_p), ("v_scale", c_void_p), ("count", c_int64), ("weight_decay", c_float),
@@ -71,7 +76,7 @@ ROTARY_PAIRS = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 KERNEL_CLASSES = ["gemm_forward", "gemm_backward_input", "gemm_backward_weight", "row_backward_input",
                   "row_backward_weight", "row_forward", "attn_forward", "attn_backward", "stash_copy"]
-ATTENTION_KINDS = {"standin": 0, "causal": 1}
+ATTENTION_KINDS = {"standin": 0, "causal": 1, "document": 2}
 
 
 class zb_layer_params(ctypes.Structure):
@@ -141,6 +146,9 @@ _SIGS = {
                                   c_size_t, ctypes.POINTER(c_void_p)]),
     "zb_stage_destroy": (c_int32, [c_void_p]),
     "zb_stage_forward": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p]),
+    "zb_stage_forward_documents": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+                                             c_void_p]),
+    "zb_stage_set_attention": (c_int32, [c_void_p, ctypes.POINTER(zb_attention_options)]),
     "zb_backward_input": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
     "zb_backward_weight": (c_int32, [c_void_p, c_int32, c_void_p]),
     "zb_wgrad_flush": (c_int32, [c_void_p, c_void_p]),
@@ -514,6 +522,16 @@ def zb_stage_destroy(st):
 
 def zb_stage_forward(st, mb, x, tokens, y, stream=None):
     _check(lib().zb_stage_forward(st, mb, _ptr(x), tokens, _ptr(y), _stream(stream)), "zb_stage_forward")
+
+
+def zb_stage_forward_documents(st, mb, x, tokens, doc_offsets, prefix_len, n_docs, y, stream=None):
+    _check(lib().zb_stage_forward_documents(st, mb, _ptr(x), tokens, _ptr(doc_offsets), _ptr(prefix_len), n_docs, _ptr(y),
+                                            _stream(stream)), "zb_stage_forward_documents")
+
+
+def zb_stage_set_attention(st, rotary_dim=0, pairs="half", turns=None, magnitude=1.0, cap=0.0, slopes=None):
+    opt = zb_attention_options(rotary_dim, ROTARY_PAIRS[pairs], _ptr(turns), magnitude, cap, _ptr(slopes))
+    _check(lib().zb_stage_set_attention(st, ctypes.byref(opt)), "zb_stage_set_attention")
 
 
 def zb_backward_input(st, mb, dy, dx, stream=None):

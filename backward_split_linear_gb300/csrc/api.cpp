@@ -8,6 +8,7 @@
 // their W; at most max_inflight microbatches are held; weight gradients are
 // accumulated in place in fixed buffers).
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -17,8 +18,10 @@
 #include <cuda_runtime.h>
 
 #include "../../include/zb.h"
+#include "attention_document.h"
 #include "checks.h"
 #include "launch.h"
+#include "operators.h"
 
 using zbk::Epilogue;
 using zbk::GemmArgs;
@@ -454,7 +457,7 @@ struct Region {
 // What one layer keeps for B and W.
 struct LayerSlot {
     Region x, r1, n1, a, h, r2, n2, gu, s, dy, dn2, dh, dqkv, dn1;
-    Region qkv, lse;  // causal attention only: its input and row statistics, for B
+    Region qkv, lse;  // softmax attention only: its input (turned to its positions) and row statistics, for B
 };
 
 enum class MbState { Forwarded, BackwardInputDone };
@@ -469,9 +472,11 @@ struct Layout {
     std::vector<LayerSlot> layers;
     size_t slot_bytes = 0;  // stash bytes of one microbatch
     size_t qkv_tmp = kNone;      // forward temporary, offset from the workspace start
-    size_t da_tmp = kNone;       // causal attention: gradient of a, B temporary
-    size_t dvec = kNone;         // causal attention: rowsum(dO * O), B temporary
-    int32_t ld_stat = 0;         // causal attention: floats per head row of lse / dvec
+    Region plan, positions;      // document attention: the slot's plan and its rows' places
+    size_t da_tmp = kNone;       // softmax attention: gradient of a, B temporary
+    size_t dvec = kNone;         // softmax attention: rowsum(dO * O), B temporary (document
+                                 // attention: with the tile counter behind it)
+    int32_t ld_stat = 0;         // softmax attention: floats per head row of lse / dvec
     size_t gamma_scratch = kNone;
     size_t gamma_scratch_bytes = 0;
     size_t split_flags = kNone;  // K-split scratch of the GEMMs (flags, then partial tiles)
@@ -487,9 +492,9 @@ zb_status check_config(const zb_stage_config* c) {
     if (c->n_layers < 1 || c->n_layers > 4096 || c->max_inflight < 1 || c->max_inflight > 4096 ||
         !(c->eps >= 0.f) || c->max_tokens < 1 || c->max_tokens > kMaxTokens)
         return ZB_ERR_ARG;
-    if (c->attention != ZB_ATTN_STANDIN && c->attention != ZB_ATTN_CAUSAL) return ZB_ERR_ARG;
-    if (c->attention == ZB_ATTN_STANDIN && c->seq_len != 0) return ZB_ERR_ARG;
-    if (c->attention == ZB_ATTN_CAUSAL && c->kind != ZB_LAYER_TRANSFORMER) return ZB_ERR_ARG;
+    if (c->attention < ZB_ATTN_STANDIN || c->attention > ZB_ATTN_DOCUMENT) return ZB_ERR_ARG;
+    if (c->attention != ZB_ATTN_CAUSAL && c->seq_len != 0) return ZB_ERR_ARG;
+    if (c->attention != ZB_ATTN_STANDIN && c->kind != ZB_LAYER_TRANSFORMER) return ZB_ERR_ARG;
     switch (c->kind) {
         case ZB_LAYER_LINEAR:
             if (c->n_layers != 1) return ZB_ERR_ARG;
@@ -502,7 +507,7 @@ zb_status check_config(const zb_stage_config* c) {
             if (!feature_ok(c->hidden) || !feature_ok(c->ffn)) return ZB_ERR_SHAPE;
             if (!heads_ok(c->n_heads, c->n_kv_heads, c->head_dim) || c->n_heads * c->head_dim != c->hidden)
                 return ZB_ERR_SHAPE;
-            if (c->attention == ZB_ATTN_CAUSAL && !causal_ok(c->n_heads, c->n_kv_heads, c->head_dim, c->seq_len))
+            if (c->attention != ZB_ATTN_STANDIN && !causal_ok(c->n_heads, c->n_kv_heads, c->head_dim, c->seq_len))
                 return ZB_ERR_SHAPE;
             return ZB_OK;
     }
@@ -538,7 +543,7 @@ Layout make_layout(const zb_stage_config& c) {
                 s.dh = take(T * H * 2);
                 s.dqkv = take(T * static_cast<size_t>(qkv_width(c)) * 2);
                 s.dn1 = take(T * H * 2);
-                if (c.attention == ZB_ATTN_CAUSAL) {
+                if (c.attention != ZB_ATTN_STANDIN) {
                     s.qkv = take(T * static_cast<size_t>(qkv_width(c)) * 2);
                     s.lse = take(static_cast<size_t>(c.n_heads) * stat_stride(c.max_tokens) * 4);
                 }
@@ -554,13 +559,17 @@ Layout make_layout(const zb_stage_config& c) {
         }
         L.layers.push_back(s);
     }
+    if (c.attention == ZB_ATTN_DOCUMENT) {
+        L.plan = take(zbk::doc_plan_bytes(c.max_tokens));
+        L.positions = take(round_up(T * 4));
+    }
     size_t total = off;
-    if (c.kind == ZB_LAYER_TRANSFORMER && c.attention == ZB_ATTN_CAUSAL) {
+    if (c.kind == ZB_LAYER_TRANSFORMER && c.attention != ZB_ATTN_STANDIN) {
         L.ld_stat = stat_stride(c.max_tokens);
         L.da_tmp = total;
         total += round_up(T * H * 2);
         L.dvec = total;
-        total += round_up(static_cast<size_t>(c.n_heads) * L.ld_stat * 4);
+        total += round_up(zbk::document_scratch_bytes(c.n_heads, L.ld_stat));
     } else if (c.kind == ZB_LAYER_TRANSFORMER) {
         L.qkv_tmp = total;
         total += round_up(T * static_cast<size_t>(qkv_width(c)) * 2);
@@ -637,6 +646,7 @@ struct zb_stage {
     int32_t inflight = 0;
     int32_t peak = 0;
     bool split_zeroed = false;  // K-split flags cleared on the device
+    zb_attention_options opt{};  // softmax attention: rotary positions, cap, slopes
 
     template <typename T = void>
     T* at(int slot, const Region& r) const {
@@ -645,6 +655,13 @@ struct zb_stage {
 };
 
 namespace {
+
+// The documents of a microbatch (device arrays); offsets null: one document.
+struct Documents {
+    const int32_t* offsets = nullptr;
+    const int32_t* prefix = nullptr;
+    int32_t n = 1;
+};
 
 // Runs `fn` (which enqueues on `s`); with tracing on, brackets it with events
 // and books `launches` kernels doing `flops` / `bytes` of algorithmic work.
@@ -714,8 +731,29 @@ zb_status stash_copy(zb_stage* st, void* dst, const void* src, size_t bytes, cud
     });
 }
 
+zbk::DocShape doc_shape(const zb_stage* st, int t) {
+    const zb_stage_config& c = st->cfg;
+    return {t, c.n_heads, c.n_kv_heads, c.head_dim, st->lay.ld_stat};
+}
+
+// The rotary positions of the q and k heads of a qkv tensor (or their gradient), in
+// place.  Rows are counted from their document's start, or from the microbatch's.
+zb_status stage_rotary(zb_stage* st, int slot, void* qkv, int t, bool forward, cudaStream_t s) {
+    const zb_stage_config& c = st->cfg;
+    const zb_attention_options& o = st->opt;
+    if (o.rotary_dim == 0) return ZB_OK;
+    const int32_t* positions = c.attention == ZB_ATTN_DOCUMENT ? st->at<int32_t>(slot, st->lay.positions) : nullptr;
+    const double heads = c.n_heads + c.n_kv_heads;
+    return traced(st, forward ? ZB_KCLASS_ROW_FORWARD : ZB_KCLASS_ROW_BACKWARD_INPUT, 1, 0.0,
+                  4.0 * t * heads * o.rotary_dim + 4.0 * t, s, [&] {
+                      return cuda_status(zbk::launch_rotary(qkv, qkv_width(c), qkv, qkv_width(c), positions, o.turns, o.magnitude,
+                                                            t, c.n_heads + c.n_kv_heads, c.head_dim, o.rotary_dim,
+                                                            o.rotary_pairs == ZB_ROTARY_HALF, forward ? 1.f : -1.f, s));
+                  });
+}
+
 // F of one microbatch already holding `slot`.
-zb_status stage_forward_body(zb_stage* st, int slot, const void* x, int t, void* y, cudaStream_t s) {
+zb_status stage_forward_body(zb_stage* st, int slot, const void* x, int t, const Documents& docs, void* y, cudaStream_t s) {
     const zb_stage_config& c = st->cfg;
     const int H = c.hidden, F = c.ffn, Q = qkv_width(c);
     const double T = t;
@@ -729,14 +767,19 @@ zb_status stage_forward_body(zb_stage* st, int slot, const void* x, int t, void*
             return run_linear_forward(st->at(slot, st->lay.layers[0].x), p.w, nullptr, y, t, H, F, s, &ws);
         });
     }
+    if (c.attention == ZB_ATTN_DOCUMENT)
+        ZB_TRY(traced(st, ZB_KCLASS_ROW_FORWARD, 1, 0.0, static_cast<double>(zbk::doc_plan_bytes(t)) + 4.0 * T, s, [&] {
+            return cuda_status(zbk::launch_document_plan(docs.offsets, docs.prefix, docs.n, t, st->at(slot, st->lay.plan),
+                                                         st->at<int32_t>(slot, st->lay.positions), s));
+        }));
     for (int l = 0; l < c.n_layers; ++l) {
         const zb_layer_params& p = st->prm[l];
         const LayerSlot& L = st->lay.layers[l];
         void* xin = st->at(slot, L.x);
         void* yout = l + 1 < c.n_layers ? st->at(slot, st->lay.layers[l + 1].x) : y;
         if (c.kind == ZB_LAYER_TRANSFORMER) {
-            const bool causal = c.attention == ZB_ATTN_CAUSAL;
-            void* qkv = causal ? st->at(slot, L.qkv) : st->ws + st->lay.qkv_tmp;
+            const bool softmax = c.attention != ZB_ATTN_STANDIN;
+            void* qkv = softmax ? st->at(slot, L.qkv) : st->ws + st->lay.qkv_tmp;
             ZB_TRY(traced(st, ZB_KCLASS_ROW_FORWARD, 1, 0.0, 4.0 * T * H + 4.0 * T, s, [&] {
                 return cuda_status(zbk::launch_rmsnorm_forward(xin, p.gamma1, c.eps, st->at(slot, L.n1),
                                                                st->at<float>(slot, L.r1), t, H, s));
@@ -744,7 +787,15 @@ zb_status stage_forward_body(zb_stage* st, int slot, const void* x, int t, void*
             ZB_TRY(traced(st, ZB_KCLASS_GEMM_FORWARD, 1, gemm_flops(T, Q, H), fwd_bytes(T, Q, H, false), s, [&] {
                 return run_linear_forward(st->at(slot, L.n1), p.w_qkv, nullptr, qkv, t, H, Q, s, &ws);
             }));
-            if (causal) {
+            ZB_TRY(stage_rotary(st, slot, qkv, t, true, s));
+            if (c.attention == ZB_ATTN_DOCUMENT) {
+                // the visible pairs are known on the device only: booked without FLOPs
+                ZB_TRY(traced(st, ZB_KCLASS_ATTN_FORWARD, 1, 0.0, 2.0 * T * (Q + H) + 4.0 * T * c.n_heads, s, [&] {
+                    return cuda_status(zbk::launch_document_forward(doc_shape(st, t), qkv, st->at(slot, L.a),
+                                                                    st->at<float>(slot, L.lse), st->at(slot, st->lay.plan),
+                                                                    st->opt.slopes, st->opt.cap, s));
+                }));
+            } else if (softmax) {
                 const double pairs = causal_pairs(t, c.seq_len) * c.n_heads;
                 ZB_TRY(traced(st, ZB_KCLASS_ATTN_FORWARD, 1, 4.0 * c.head_dim * pairs, 2.0 * T * (Q + H) + 4.0 * T * c.n_heads, s,
                               [&] {
@@ -829,7 +880,7 @@ zb_status stage_backward_input_body(zb_stage* st, int slot, const void* dy, void
             void* dqkv = st->at(slot, L.dqkv);
             void* dn1 = st->at(slot, L.dn1);
             const double kv = static_cast<double>(c.n_kv_heads) * c.head_dim;
-            if (c.attention == ZB_ATTN_CAUSAL) {
+            if (c.attention != ZB_ATTN_STANDIN) {
                 // a3: output projection B into a temporary, then the attention backward
                 // (dK/dV, dQ) writes every column of dqkv.  D = rowsum(da * a) per
                 // head comes from the GEMM's epilogue when the CTA-pair kernel
@@ -844,14 +895,22 @@ zb_status stage_backward_input_body(zb_stage* st, int slot, const void* dy, void
                                                                                s, &ws)
                                                    : run_backward_input(dh, p.w_o, da, t, H, H, H, s, &ws);
                               }));
-                const double pairs = causal_pairs(t, c.seq_len) * c.n_heads;
-                ZB_TRY(traced(st, ZB_KCLASS_ATTN_BACKWARD, d_in_gemm ? 2 : 3, 10.0 * c.head_dim * pairs,
-                              2.0 * T * (2.0 * Q + (d_in_gemm ? 1.0 : 2.0) * H) + 8.0 * T * c.n_heads, s, [&] {
-                                  return cuda_status(zbk::launch_attention_causal_backward(
-                                      attn_shape(t, c.n_heads, c.n_kv_heads, c.head_dim, c.seq_len, st->lay.ld_stat),
-                                      st->at(slot, L.qkv), st->at(slot, L.a), da, st->at<float>(slot, L.lse), dvec,
-                                      dqkv, s, d_in_gemm));
-                              }));
+                const double bytes = 2.0 * T * (2.0 * Q + (d_in_gemm ? 1.0 : 2.0) * H) + 8.0 * T * c.n_heads;
+                if (c.attention == ZB_ATTN_DOCUMENT) {
+                    ZB_TRY(traced(st, ZB_KCLASS_ATTN_BACKWARD, d_in_gemm ? 1 : 2, 0.0, bytes, s, [&] {
+                        return cuda_status(zbk::launch_document_backward(
+                            doc_shape(st, t), st->at(slot, L.qkv), st->at(slot, L.a), da, st->at<float>(slot, L.lse), dqkv,
+                            st->at(slot, st->lay.plan), st->opt.slopes, st->opt.cap, dvec, s, d_in_gemm));
+                    }));
+                } else {
+                    const double pairs = causal_pairs(t, c.seq_len) * c.n_heads;
+                    ZB_TRY(traced(st, ZB_KCLASS_ATTN_BACKWARD, d_in_gemm ? 2 : 3, 10.0 * c.head_dim * pairs, bytes, s, [&] {
+                        return cuda_status(zbk::launch_attention_causal_backward(
+                            attn_shape(t, c.n_heads, c.n_kv_heads, c.head_dim, c.seq_len, st->lay.ld_stat),
+                            st->at(slot, L.qkv), st->at(slot, L.a), da, st->at<float>(slot, L.lse), dvec, dqkv, s, d_in_gemm));
+                    }));
+                }
+                ZB_TRY(stage_rotary(st, slot, dqkv, t, false, s));
             } else {
                 // a3: output projection B (into the q columns of dqkv) and the stand-in backward
                 ZB_TRY(traced(st, ZB_KCLASS_GEMM_BACKWARD_INPUT, 1, gemm_flops(T, H, H), dgrad_bytes(T, H, H), s,
@@ -962,8 +1021,10 @@ extern "C" zb_status zb_stage_destroy(zb_stage_t st) {
     return ZB_OK;
 }
 
-extern "C" zb_status zb_stage_forward(zb_stage_t st, int32_t mb, const void* x, int32_t tokens, void* y,
-                                      void* stream) {
+namespace {
+
+zb_status stage_forward_entry(zb_stage_t st, int32_t mb, const void* x, int32_t tokens, const Documents& docs, void* y,
+                              void* stream) {
     if (!st || mb < 0) return ZB_ERR_ARG;
     if (tokens < 0 || tokens > st->cfg.max_tokens) return ZB_ERR_SHAPE;
     if (!rows_ok(x, tokens) || !rows_ok(y, tokens)) return ZB_ERR_ARG;
@@ -977,11 +1038,48 @@ extern "C" zb_status zb_stage_forward(zb_stage_t st, int32_t mb, const void* x, 
     if (slot < 0) return ZB_ERR_STASH_FULL;
     ZB_TRY(device_ok());
     if (st->cfg.attention == ZB_ATTN_CAUSAL && zbk::attention_prepare() != cudaSuccess) return ZB_ERR_CUDA;
-    ZB_TRY(stage_forward_body(st, slot, x, tokens, y, as_stream(stream)));
+    ZB_TRY(stage_forward_body(st, slot, x, tokens, docs, y, as_stream(stream)));
     st->slot_used[slot] = 1;
     st->mbs[mb] = MbEntry{MbState::Forwarded, slot, tokens};
     st->inflight += 1;
     st->peak = std::max(st->peak, st->inflight);
+    return ZB_OK;
+}
+
+}  // namespace
+
+extern "C" zb_status zb_stage_forward(zb_stage_t st, int32_t mb, const void* x, int32_t tokens, void* y,
+                                      void* stream) {
+    return stage_forward_entry(st, mb, x, tokens, Documents{}, y, stream);
+}
+
+extern "C" zb_status zb_stage_forward_documents(zb_stage_t st, int32_t mb, const void* x, int32_t tokens,
+                                                const int32_t* doc_offsets, const int32_t* prefix_len, int32_t n_docs,
+                                                void* y, void* stream) {
+    if (!st || st->cfg.attention != ZB_ATTN_DOCUMENT || n_docs < 1 || (!doc_offsets && n_docs != 1)) return ZB_ERR_ARG;
+    for (const void* p : {static_cast<const void*>(doc_offsets), static_cast<const void*>(prefix_len)})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return ZB_ERR_ARG;
+    Documents docs;
+    docs.offsets = doc_offsets;
+    docs.prefix = prefix_len;
+    docs.n = n_docs;
+    return stage_forward_entry(st, mb, x, tokens, docs, y, stream);
+}
+
+extern "C" zb_status zb_stage_set_attention(zb_stage_t st, const zb_attention_options* opt) {
+    if (!st || !opt) return ZB_ERR_ARG;
+    const zb_stage_config& c = st->cfg;
+    if (c.attention == ZB_ATTN_STANDIN) return ZB_ERR_ARG;
+    if (st->inflight != 0) return ZB_ERR_ORDER;  // B must see what F saw
+    if (opt->rotary_dim != 0) {
+        if (opt->rotary_dim < 16 || opt->rotary_dim % 16 != 0 || opt->rotary_dim > c.head_dim) return ZB_ERR_SHAPE;
+        if ((opt->rotary_pairs != ZB_ROTARY_HALF && opt->rotary_pairs != ZB_ROTARY_INTERLEAVED) || !fixed_ok(opt->turns) ||
+            !(std::fabs(opt->magnitude) <= 3.4e38f))
+            return ZB_ERR_ARG;
+    }
+    if (!zbk::cap_ok(opt->cap) || (reinterpret_cast<uintptr_t>(opt->slopes) & 3u)) return ZB_ERR_ARG;
+    if (c.attention == ZB_ATTN_CAUSAL && (opt->cap != 0.f || opt->slopes)) return ZB_ERR_ARG;
+    st->opt = *opt;
     return ZB_OK;
 }
 

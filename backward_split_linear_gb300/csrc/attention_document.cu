@@ -1872,7 +1872,7 @@ bool word_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 
 zb_status document_ok(int32_t tokens, int32_t nh, int32_t nkv, int32_t hd, const void* plan, const float* slopes, float cap) {
     if (!tokens_ok(tokens) || !heads_ok(nh, nkv, hd) || (hd != 64 && hd != 128)) return ZB_ERR_SHAPE;
-    if (!rows_ok(plan, tokens) || !word_ok(slopes) || !(cap == 0.f || (cap >= 1e-3f && cap <= 1e5f))) return ZB_ERR_ARG;
+    if (!rows_ok(plan, tokens) || !word_ok(slopes) || !cap_ok(cap)) return ZB_ERR_ARG;
     return ZB_OK;
 }
 

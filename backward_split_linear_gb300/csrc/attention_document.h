@@ -2,10 +2,9 @@
 // scores' modifications, and the row-by-row forms.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
-
-#include "device_common.cuh"
 
 namespace zbk {
 
@@ -35,6 +34,10 @@ inline DocPlan doc_plan(const void* plan, int64_t tokens) {
     p.k_blocks = p.q_blocks + nb;
     return p;
 }
+
+// The caps that the kernels take: none, or a size at which its polynomial's
+// coefficients are normal float32 numbers.
+inline bool cap_ok(float cap) { return cap == 0.f || (cap >= 1e-3f && cap <= 1e5f); }
 
 struct DocShape {
     int tokens, n_heads, n_kv_heads, head_dim, ld_stat;

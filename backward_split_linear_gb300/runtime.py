@@ -75,8 +75,27 @@ class Stage:
             for t in g.values():
                 t.zero_()
 
-    def forward(self, mb, x, y, stream=None):
-        zb.zb_stage_forward(self.handle, mb, x, x.shape[0], y, stream)
+    def set_attention(self, rotary_dim=0, pairs="half", base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0,
+                      high=None, cap=0.0, slopes=None):
+        """Rotary positions, a tanh cap and distance slopes of the stage's softmax attention (see `zb_stage_set_attention`;
+        the frequencies' arguments are those of `binding.zb_rotary_frequencies`).  `slopes`: float32 [n_heads]."""
+        turns, magnitude = None, 1.0
+        if rotary_dim:
+            values, magnitude = zb.zb_rotary_frequencies(rotary_dim, base, scaling, factor, context, low, high)
+            turns = torch.from_numpy(np.array(values, dtype=np.uint64).view(np.int64)).to(self.workspace.device)
+        zb.zb_stage_set_attention(self.handle, rotary_dim, pairs, turns, magnitude, cap, slopes)
+        self.attention_tensors = (turns, slopes)  # the library keeps their addresses
+
+    def forward(self, mb, x, y, stream=None, documents=None, prefix=None):
+        """`documents`: int32 row offsets of packed documents (attention "document"), `prefix` their prefix lengths."""
+        if documents is None and prefix is None:
+            zb.zb_stage_forward(self.handle, mb, x, x.shape[0], y, stream)
+            return
+        for t, n in ((documents, None), (prefix, documents.numel() - 1 if documents is not None else 1)):
+            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n)):
+                raise zb.ZBError(-1, "Stage.forward (documents and prefix are contiguous int32)")
+        zb.zb_stage_forward_documents(self.handle, mb, x, x.shape[0], documents, prefix,
+                                      documents.numel() - 1 if documents is not None else 1, y, stream)
 
     def backward_input(self, mb, dy, dx, stream=None):
         zb.zb_backward_input(self.handle, mb, dy, dx, stream)

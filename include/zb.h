@@ -509,8 +509,11 @@ typedef enum {
 /* The attention core A of a TRANSFORMER layer. */
 typedef enum {
     ZB_ATTN_STANDIN = 0,  /* weight-free stand-in a_h = q_h + k_j + v_j (per token) */
-    ZB_ATTN_CAUSAL = 1    /* causal softmax attention, as zb_op_attention_causal_forward;
+    ZB_ATTN_CAUSAL = 1,   /* causal softmax attention, as zb_op_attention_causal_forward;
                              the stash also keeps qkv and the row log-sum-exp */
+    ZB_ATTN_DOCUMENT = 2  /* softmax attention inside packed documents, as
+                             zb_op_attention_document_forward; the stash also keeps qkv, the row
+                             log-sum-exp and the microbatch's plan (seq_len must be 0) */
 } zb_attention_kind;
 
 typedef struct {
@@ -567,6 +570,37 @@ zb_status zb_stage_destroy(zb_stage_t st);
 zb_status zb_stage_forward(zb_stage_t st, int32_t mb, const void* x, int32_t tokens,
                            void* y, void* stream);
 
+/* F of a microbatch of packed documents, for a ZB_ATTN_DOCUMENT stage:
+ * doc_offsets, prefix_len and n_docs as in zb_op_attention_document_plan (device
+ * arrays that `stream` reads during this call's work; the plan made from them is
+ * stashed for B).  On such a stage zb_stage_forward is the call with one
+ * document of all rows. */
+zb_status zb_stage_forward_documents(zb_stage_t st, int32_t mb, const void* x, int32_t tokens,
+                                     const int32_t* doc_offsets, const int32_t* prefix_len,
+                                     int32_t n_docs, void* y, void* stream);
+
+/* How a stage's softmax attention reads its q and k heads and scores them.
+ * Rotary positions (rotary_dim > 0) turn the q and k heads in place between the
+ * qkv projection and the attention core, and their gradients back in B; a row's
+ * position is its place in its document (ZB_ATTN_DOCUMENT) or in the microbatch
+ * (ZB_ATTN_CAUSAL: scores depend on differences only).  cap and slopes as in
+ * zb_op_attention_document_forward (ZB_ATTN_DOCUMENT only).  turns and slopes are
+ * device memory that must outlive the stage.  ZB_STASH_QKV then holds the turned
+ * heads. */
+typedef struct {
+    int32_t rotary_dim;        /* 0: no positions */
+    int32_t rotary_pairs;      /* zb_rotary_pairs */
+    const uint64_t* turns;     /* [rotary_dim / 2], as zb_rotary_frequencies writes them */
+    float magnitude;
+    float cap;                 /* 0: none */
+    const float* slopes;       /* [n_heads] or NULL */
+} zb_attention_options;
+
+/* Sets them (a new stage has none).  Errors: ZB_ERR_ARG (a stand-in stage, an
+ * option the stage's kind does not have), ZB_ERR_SHAPE (rotary_dim),
+ * ZB_ERR_ORDER (microbatches in flight). */
+zb_status zb_stage_set_attention(zb_stage_t st, const zb_attention_options* opt);
+
 /* B of microbatch `mb` [G1][G2]: from dy[T, out] computes dx[T, hidden]
  * through every layer, top first, and keeps each linear's dY for the
  * deferred W.  Only dX-side products run here.
@@ -622,8 +656,8 @@ typedef enum {
     ZB_STASH_DH,       /* gradient of h [T, H], TRANSFORMER; written by B */
     ZB_STASH_DQKV,     /* [T, (nh + 2 nkv) hd], TRANSFORMER; written by B */
     ZB_STASH_DN1,      /* dqkv W_qkv [T, H], TRANSFORMER; written by B */
-    ZB_STASH_QKV,      /* attention input [T, (nh + 2 nkv) hd], ZB_ATTN_CAUSAL only */
-    ZB_STASH_LSE,      /* float32 [nh, zb_op_attention_stat_stride(max_tokens)], ZB_ATTN_CAUSAL only */
+    ZB_STASH_QKV,      /* attention input [T, (nh + 2 nkv) hd], softmax attention only */
+    ZB_STASH_LSE,      /* float32 [nh, zb_op_attention_stat_stride(max_tokens)], softmax attention only */
     ZB_STASH_COUNT
 } zb_stash_tensor;
 
@@ -652,11 +686,12 @@ typedef enum {
     ZB_KCLASS_GEMM_BACKWARD_INPUT,   /* B GEMMs, incl. the fused SwiGLU backward and the causal
                                         attention's D in the output projection's dgrad */
     ZB_KCLASS_GEMM_BACKWARD_WEIGHT,  /* W GEMMs (float32 accumulation) */
-    ZB_KCLASS_ROW_BACKWARD_INPUT,    /* B row kernels: RMSNorm backward, stand-in backward */
+    ZB_KCLASS_ROW_BACKWARD_INPUT,    /* B row kernels: RMSNorm backward, stand-in backward, rotary backward */
     ZB_KCLASS_ROW_BACKWARD_WEIGHT,   /* W row kernels: gamma-gradient reduction */
-    ZB_KCLASS_ROW_FORWARD,           /* F row kernels */
-    ZB_KCLASS_ATTN_FORWARD,          /* F causal attention */
-    ZB_KCLASS_ATTN_BACKWARD,         /* B causal attention (dK/dV and dQ kernels, and the rowsum kernel
+    ZB_KCLASS_ROW_FORWARD,           /* F row kernels, rotary and the documents' plan among them */
+    ZB_KCLASS_ATTN_FORWARD,          /* F softmax attention (document attention: booked without FLOPs, its
+                                        visible pairs being known on the device only) */
+    ZB_KCLASS_ATTN_BACKWARD,         /* B softmax attention (dK/dV and dQ, and the rowsum kernel
                                         when the output projection's dgrad does not form D) */
     ZB_KCLASS_STASH_COPY,            /* the stash copies of the caller's x (F) and dy (B):
                                         device-to-device cudaMemcpyAsync, not a kernel of the

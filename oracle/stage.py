@@ -35,6 +35,12 @@ Readings where the pages are silent (the pages show a single linear only):
     sequence takes the remaining tokens).  No position encoding is applied.
     Tokens mix only inside a sequence, so the concatenated-batch identity
     holds for microbatches made of whole sequences.
+  - "document": softmax attention inside packed documents (``train_ops``), with
+    ``shp["offsets"]`` (and optionally ``shp["prefix"]``, ``shp["cap"]``,
+    ``shp["slopes"]``) of the microbatch.
+  With ``shp["rotary"] = (frequencies, magnitude, pairs)`` the q and k heads of
+  both softmax forms first turn to their rows' positions, counted from the
+  document's start ("causal": from the microbatch's).
 * Weight gradients accumulate: the caller's float64 accumulators start at zero
   and every W adds into them (section "Memory Management & Activation
   Rollback": gradients are accumulated in place in fixed buffers).
@@ -42,6 +48,8 @@ Readings where the pages are silent (the pages show a single linear only):
 from __future__ import annotations
 
 import numpy as np
+
+from . import train_ops
 
 # ----------------------------------------------------------------------------
 # shapes
@@ -207,16 +215,45 @@ def attention_causal_grad(da, qkv, n_heads, n_kv_heads, head_dim, seq_len):
     return np.concatenate([dq.reshape(t, -1), dk.reshape(t, -1), dv.reshape(t, -1)], axis=1)
 
 
+def _turned(qkv, shp, backward=False):
+    """qkv with the q and k heads turned to their positions (or a gradient turned back)."""
+    if not shp.get("rotary"):
+        return qkv
+    f, magnitude, pairs = shp["rotary"]
+    t, n, d = qkv.shape[0], shp["n_heads"] + shp["n_kv_heads"], shp["head_dim"]
+    pos = np.arange(t)
+    if shp["attention"] == "document":
+        off = shp["offsets"]
+        start = np.zeros(t, dtype=np.int64)
+        for i in range(len(off) - 1):
+            start[off[i]:off[i + 1]] = off[i]
+        pos = np.where((pos >= off[0]) & (pos < off[-1]), pos - start, 0)
+    out = qkv.copy()
+    out[:, : n * d] = train_ops.rotary(qkv[:, : n * d].reshape(t, n, d), pos, f, magnitude, pairs, backward).reshape(t, n * d)
+    return out
+
+
 def attention_forward(qkv, shp):
+    qkv = _turned(qkv, shp)
+    if shp.get("attention", "standin") == "document":
+        see = train_ops.document_visible(qkv.shape[0], shp["offsets"], shp.get("prefix"))
+        return train_ops.document_attention(qkv, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"], see, shp.get("cap", 0.0),
+                                            shp.get("slopes"))[0]
     if shp.get("attention", "standin") == "causal":
         return attention_causal(qkv, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"], shp.get("seq_len", 0))
     return attention_standin(qkv, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"])
 
 
 def attention_backward(da, qkv, shp):
+    qkv = _turned(qkv, shp)
+    if shp.get("attention", "standin") == "document":
+        see = train_ops.document_visible(qkv.shape[0], shp["offsets"], shp.get("prefix"))
+        grad = train_ops.document_attention_grad(da, qkv, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"], see,
+                                                 shp.get("cap", 0.0), shp.get("slopes"))
+        return _turned(grad, shp, backward=True)
     if shp.get("attention", "standin") == "causal":
-        return attention_causal_grad(da, qkv, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"],
-                                     shp.get("seq_len", 0))
+        return _turned(attention_causal_grad(da, qkv, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"],
+                                             shp.get("seq_len", 0)), shp, backward=True)
     return attention_standin_grad(da, shp["n_heads"], shp["n_kv_heads"], shp["head_dim"])
 
 

@@ -215,3 +215,68 @@ def test_oracle_documents_are_independent_and_causal():
     dy = np.random.default_rng(4).standard_normal((t, 2 * d))
     np.testing.assert_allclose(O.document_attention_grad(dy, x, nh, nkv, d, see),
                                S.attention_causal_grad(dy, x, nh, nkv, d, 4), atol=1e-12)
+
+
+# ---------------------------------------------------------------- stages of documents
+
+
+def test_document_stage_refusals(zblib):
+    tf = dict(kind="transformer", n_layers=2, hidden=256, ffn=512, n_heads=4, n_kv_heads=2, head_dim=64, max_tokens=256,
+              max_inflight=2)
+    standin = zb.zb_stage_workspace_bytes(zb.make_config(**tf))
+    cfg = zb.make_config(**tf, attention="document")
+    size = zb.zb_stage_workspace_bytes(cfg)
+    assert size > standin
+    assert zb.zb_stage_workspace_bytes(zb.make_config(**tf, attention="document", seq_len=128)) == 0
+    assert zb.zb_stage_workspace_bytes(zb.make_config("mlp", 2, 256, 512, attention="document")) == 0
+    names = ("w_qkv", "dw_qkv", "w_o", "dw_o", "w_gu", "dw_gu", "w_down", "dw_down", "gamma1", "dgamma1", "gamma2", "dgamma2")
+    layers = [{k: FAKE for k in names}] * 2
+    st = zb.zb_stage_create(cfg, layers, FAKE, size)
+    try:
+        opts = zb.zb_stage_set_attention
+        opts(st)
+        opts(st, 32, "interleaved", FAKE, 1.2, 30.0, FAKE)
+        refused("ZB_ERR_SHAPE", opts, st, 24, "half", FAKE)
+        refused("ZB_ERR_SHAPE", opts, st, 80, "half", FAKE)           # wider than a head
+        refused("ZB_ERR_ARG", opts, st, 64, "half", None)
+        refused("ZB_ERR_ARG", opts, st, 64, "half", FAKE, float("nan"))
+        refused("ZB_ERR_ARG", opts, st, cap=-1.0)
+        refused("ZB_ERR_ARG", opts, st, slopes=FAKE + 2)
+        fwd = zb.zb_stage_forward_documents
+        refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, FAKE, None, 0, FAKE, 0)
+        refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, None, None, 2, FAKE, 0)
+        refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, FAKE + 2, None, 2, FAKE, 0)
+        refused("ZB_ERR_SHAPE", fwd, st, 0, FAKE, 257, FAKE, None, 2, FAKE, 0)
+    finally:
+        zb.zb_stage_destroy(st)
+    causal = zb.make_config(**tf, attention="causal")
+    st = zb.zb_stage_create(causal, layers, FAKE, zb.zb_stage_workspace_bytes(causal))
+    try:
+        zb.zb_stage_set_attention(st, 64, "half", FAKE)
+        refused("ZB_ERR_ARG", zb.zb_stage_set_attention, st, cap=10.0)
+        refused("ZB_ERR_ARG", zb.zb_stage_forward_documents, st, 0, FAKE, 10, FAKE, None, 2, FAKE, 0)
+    finally:
+        zb.zb_stage_destroy(st)
+    st = zb.zb_stage_create(zb.make_config(**tf), layers, FAKE, standin)
+    try:
+        refused("ZB_ERR_ARG", zb.zb_stage_set_attention, st)
+    finally:
+        zb.zb_stage_destroy(st)
+
+
+def test_oracle_document_stage_split_equals_differences():
+    """The oracle's B of a layer with rotary positions and document attention against central differences of its F."""
+    from oracle import stage as S
+
+    rng = np.random.default_rng(9)
+    T, H, F, nh, nkv, hd = 14, 32, 24, 4, 2, 8
+    prm = {k: 0.3 * rng.standard_normal(s) for k, s in S.weight_shapes("transformer", H, F, nh, nkv, hd).items()}
+    shp = dict(kind="transformer", hidden=H, ffn=F, n_heads=nh, n_kv_heads=nkv, head_dim=hd, eps=1e-5, attention="document",
+               offsets=[1, 6, 12], prefix=[2, 0], cap=3.0, slopes=[0.1, 0.0, 0.2, 0.05],
+               rotary=(np.array([1.0, 0.1]), 1.2, "interleaved"))
+    x, dy, u = (rng.standard_normal((T, H)) for _ in range(3))
+    _, saved = S.layer_forward(x, prm, shp)
+    dx, _ = S.layer_backward_input(dy, prm, saved, shp)
+    h = 1e-5
+    f = lambda z: np.sum(S.layer_forward(z, prm, shp)[0] * dy)  # noqa: E731
+    assert abs((f(x + h * u) - f(x - h * u)) / (2 * h) - np.sum(dx * u)) < 1e-6 * max(1.0, abs(np.sum(dx * u)))
