@@ -21,6 +21,7 @@
 // reproducible by any IEEE implementation of the formulas.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "checks.h"
 #include "device_common.cuh"
@@ -31,24 +32,27 @@ namespace {
 
 constexpr int kAdamThreads = 256;
 constexpr int kPerThread = 8;
-constexpr int kChunk = kAdamThreads * kPerThread;  // elements per block
+constexpr int kChunk = kAdamThreads * kPerThread;  // elements a block takes at a time
 constexpr int kStateBlock = 256;                   // elements per 8-bit scale: one warp's
 constexpr float kMTop = 245760.f;                  // 15 * 2^14, the value of m's largest code
 constexpr float kVTop = 16106127360.f;             // 15 * 2^30, the value of v's largest code
-constexpr int kMaxAdamTensors = 64;                // per launch
 
-// The tensors of one launch, and the first chunk of each (first[n]: all chunks).
+// The tensors of one launch, and the first chunk of each (first[n]: all chunks).  The
+// table is a kernel parameter, copied at every launch, so short lists have a small one
+// (12 tensors: a launch takes the host about 3 us less).
+constexpr int kFewTensors = 16, kManyTensors = 64;
+template <int N>
 struct AdamTable {
-    zb_adamw_tensor t[kMaxAdamTensors];
-    int64_t first[kMaxAdamTensors + 1];
+    zb_adamw_tensor t[N];
+    int first[N + 1];
     int n;
     int index0;  // number of t[0] in the caller's list (for the hash)
 };
-
 // Where adamw_unpack_kernel writes the moments of each tensor of a table.
+template <int N>
 struct AdamUnpack {
-    float* m[kMaxAdamTensors];
-    float* v[kMaxAdamTensors];
+    float* m[N];
+    float* v[N];
 };
 
 struct AdamArgs {
@@ -63,7 +67,8 @@ struct AdamArgs {
 };
 
 // The tensor that chunk c belongs to: the last one that starts at or before it.
-__device__ __forceinline__ int find_tensor(const AdamTable& tab, int64_t c) {
+template <int N>
+__device__ __forceinline__ int find_tensor(const AdamTable<N>& tab, int c) {
     int lo = 0, hi = tab.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -75,9 +80,10 @@ __device__ __forceinline__ int find_tensor(const AdamTable& tab, int64_t c) {
     return lo;
 }
 
-// Eight consecutive values from e on, zero past the end.
+// Eight consecutive values from e on, zero past the end (kFull: there are eight).
+template <bool kFull>
 __device__ __forceinline__ void load8f(const float* p, int64_t e, int64_t n, float (&v)[8]) {
-    if (e + 8 <= n) {
+    if (kFull || e + 8 <= n) {
         const float4 a = *reinterpret_cast<const float4*>(p + e), b = *reinterpret_cast<const float4*>(p + e + 4);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
@@ -85,8 +91,9 @@ __device__ __forceinline__ void load8f(const float* p, int64_t e, int64_t n, flo
         for (int k = 0; k < 8; ++k) v[k] = e + k < n ? p[e + k] : 0.f;
     }
 }
+template <bool kFull>
 __device__ __forceinline__ void store8f(float* p, int64_t e, int64_t n, const float (&v)[8]) {
-    if (e + 8 <= n) {
+    if (kFull || e + 8 <= n) {
         *reinterpret_cast<float4*>(p + e) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4*>(p + e + 4) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
@@ -95,8 +102,9 @@ __device__ __forceinline__ void store8f(float* p, int64_t e, int64_t n, const fl
             if (e + k < n) p[e + k] = v[k];
     }
 }
+template <bool kFull>
 __device__ __forceinline__ void load8h(const uint16_t* p, int64_t e, int64_t n, float (&v)[8]) {
-    if (e + 8 <= n) {
+    if (kFull || e + 8 <= n) {
         const uint4 q = *reinterpret_cast<const uint4*>(p + e);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -109,8 +117,9 @@ __device__ __forceinline__ void load8h(const uint16_t* p, int64_t e, int64_t n, 
         for (int k = 0; k < 8; ++k) v[k] = e + k < n ? __uint_as_float(static_cast<uint32_t>(p[e + k]) << 16) : 0.f;
     }
 }
+template <bool kFull>
 __device__ __forceinline__ void store8h(uint16_t* p, int64_t e, int64_t n, const uint32_t (&w)[4]) {
-    if (e + 8 <= n) {
+    if (kFull || e + 8 <= n) {
         *reinterpret_cast<uint4*>(p + e) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
@@ -118,16 +127,18 @@ __device__ __forceinline__ void store8h(uint16_t* p, int64_t e, int64_t n, const
             if (e + k < n) p[e + k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
     }
 }
+template <bool kFull>
 __device__ __forceinline__ uint2 load8b(const uint8_t* p, int64_t e, int64_t n) {
-    if (e + 8 <= n) return *reinterpret_cast<const uint2*>(p + e);
+    if (kFull || e + 8 <= n) return *reinterpret_cast<const uint2*>(p + e);
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (e + k < n) w[k >> 2] |= static_cast<uint32_t>(p[e + k]) << (8 * (k & 3));
     return make_uint2(w[0], w[1]);
 }
+template <bool kFull>
 __device__ __forceinline__ void store8b(uint8_t* p, int64_t e, int64_t n, uint2 q) {
-    if (e + 8 <= n) {
+    if (kFull || e + 8 <= n) {
         *reinterpret_cast<uint2*>(p + e) = q;
     } else {
         const uint32_t w[2] = {q.x, q.y};
@@ -144,17 +155,28 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// The grid's value of a code without its sign.  The float whose upper bits are
-// the code plus 1040 is twice the value, or the value plus 8 for the codes below
-// 8, and the smaller of the two readings is the right one on both sides.
-__device__ __forceinline__ float code_value(uint32_t c) {
-    const float x = __uint_as_float((c + 1040u) << 20);
-    return fminf(0.5f * x, x - 8.f);
+// Byte k of w in bits 20 to 27.
+__device__ __forceinline__ uint32_t code_field(uint32_t w, int k) { return k < 3 ? w << (20 - 8 * k) : w >> 4; }
+// The grid's value of a code without its sign, given in bits 20 to 27.  The float with
+// those bits under the exponent 128 is a quarter of (8 + f) 2^e, which is twice the
+// value, or the value plus 8 for the codes below 8; the smaller of the two readings is
+// the right one on both sides.
+__device__ __forceinline__ float code_value(uint32_t field) {
+    const float x = __uint_as_float(0x40000000u | field);
+    return fminf(x + x, fmaf(4.f, x, -8.f));
 }
 // The code of a scaled value z >= 0, in bits 20 to 27: the inverse, rounded up when
-// the remainder's 20 bits and `noise` << 4 carry (16 bits; 0x8000: to the nearest).
+// the remainder's 20 bits and `noise4` carry (16 bits above four; 0x80000: to the
+// nearest).
 __device__ __forceinline__ uint32_t code_bits(float z, uint32_t noise4) {
     return __float_as_uint(fmaxf(z + z, __fadd_rn(z, 8.f))) + noise4 - (1040u << 20);
+}
+__device__ __forceinline__ float decode_m(uint32_t w, int k, float scale) {
+    const uint32_t sign = (k < 3 ? w << (24 - 8 * k) : w) & 0x80000000u;
+    return __uint_as_float(__float_as_uint(__fmul_rn(code_value(code_field(w, k) & 0x07F00000u), scale)) | sign);
+}
+__device__ __forceinline__ float decode_v(uint32_t w, int k, float scale) {
+    return __fmul_rn(code_value(code_field(w, k) & 0x0FF00000u), scale);
 }
 // Bits 20 to 27 of four words as four bytes.
 __device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -173,91 +195,78 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     return y;
 }
 
-template <bool kState8>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable tab, const AdamArgs a) {
-    // A scale that is not finite (an overflowed or NaN gradient norm) skips the step.
-    float gs = 1.f;
-    if (a.grad_scale) {
-        gs = *a.grad_scale;
-        if (!(fabsf(gs) <= 3.402823466e38f)) return;
-    }
-    const int64_t chunk = blockIdx.x;
-    const int ti = find_tensor(tab, chunk);
-    const zb_adamw_tensor& t = tab.t[ti];
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a launch's elements share.
+struct AdamStep {
+    float gs, decay, rate, rbias2;
+    uint32_t key;
+};
+
+// Eight elements a thread, 256 a warp, from e on.  Whole warps run on (the 8-bit
+// scales are reduced across a warp); elements past the end hold zeros and are not
+// stored.  kFull: all of the warp's elements exist.
+template <bool kState8, bool kFull>
+__device__ __forceinline__ void adamw_elements(const zb_adamw_tensor& t, const AdamArgs& a, const AdamStep& st, int64_t e) {
     const int64_t n = t.count;
-    const int64_t e = (chunk - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
-    const float lr = a.lr_dev ? *a.lr_dev : a.lr;
-    float bias1 = a.bias1, rbias2 = a.rsqrt_bias2;
-    uint32_t step = a.step;
-    if (a.step_dev) {
-        const int64_t s = *a.step_dev;
-        step = static_cast<uint32_t>(s);
-        bias1 = -expm1f(static_cast<float>(s) * a.log_beta1);
-        rbias2 = rsqrtf(-expm1f(static_cast<float>(s) * a.log_beta2));
-    }
-    // Whole warps run on (the 8-bit scales are reduced across a warp); elements
-    // past the end hold zeros and are not stored.
     float g[8], m[8], v[8], p[8];
     if (t.grad_dtype == ZB_F32)
-        load8f(static_cast<const float*>(t.grad), e, n, g);
+        load8f<kFull>(static_cast<const float*>(t.grad), e, n, g);
     else
-        load8h(static_cast<const uint16_t*>(t.grad), e, n, g);
-    const float* p32 = t.master ? t.master : static_cast<const float*>(t.param);
+        load8h<kFull>(static_cast<const uint16_t*>(t.grad), e, n, g);
     if (t.master || t.param_dtype == ZB_F32)
-        load8f(p32, e, n, p);
+        load8f<kFull>(t.master ? t.master : static_cast<const float*>(t.param), e, n, p);
     else
-        load8h(static_cast<const uint16_t*>(t.param), e, n, p);
+        load8h<kFull>(static_cast<const uint16_t*>(t.param), e, n, p);
     const int64_t block = e / kStateBlock;
-    const bool in = e - (threadIdx.x & 31) * kPerThread < n;  // this warp's block exists
     if constexpr (kState8) {
-        const uint2 cm = load8b(static_cast<const uint8_t*>(t.m), e, n), cv = load8b(static_cast<const uint8_t*>(t.v), e, n);
-        const float sm = in ? t.m_scale[block] : 0.f, sv = in ? t.v_scale[block] : 0.f;
+        const uint2 cm = load8b<kFull>(static_cast<const uint8_t*>(t.m), e, n),
+                    cv = load8b<kFull>(static_cast<const uint8_t*>(t.v), e, n);
+        const float sm = t.m_scale[block], sv = t.v_scale[block];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint32_t c = ((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u;
-            const float x = __fmul_rn(code_value(c & 127u), sm);
-            m[k] = c > 127u ? -x : x;
-            v[k] = __fmul_rn(code_value(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u), sv);
+            m[k] = decode_m(k < 4 ? cm.x : cm.y, k & 3, sm);
+            v[k] = decode_v(k < 4 ? cv.x : cv.y, k & 3, sv);
         }
     } else {
-        load8f(static_cast<const float*>(t.m), e, n, m);
-        load8f(static_cast<const float*>(t.v), e, n, v);
+        load8f<kFull>(static_cast<const float*>(t.m), e, n, m);
+        load8f<kFull>(static_cast<const float*>(t.v), e, n, v);
     }
-    const float decay = 1.f - lr * t.weight_decay, rate = lr / bias1;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float gk = a.grad_scale ? __fmul_rn(g[k], gs) : g[k];
+        const float gk = a.grad_scale ? __fmul_rn(g[k], st.gs) : g[k];
         m[k] = __fadd_rn(__fmul_rn(m[k], a.beta1), __fmul_rn(gk, a.one_minus_beta1));
         v[k] = __fadd_rn(__fmul_rn(v[k], a.beta2), __fmul_rn(__fmul_rn(gk, gk), a.one_minus_beta2));
-        p[k] = p[k] * decay - rate * __fdividef(m[k], fmaf(sqrt_approx(v[k]), rbias2, a.eps));
+        p[k] = p[k] * st.decay - st.rate * (m[k] * rcp_approx(fmaf(sqrt_approx(v[k]), st.rbias2, a.eps)));
     }
     uint32_t noise[8];
     if (a.stochastic) {
-        const uint32_t key = mix32(mix32(a.seed ^ (step * 0x9E3779B1u)) + static_cast<uint32_t>(tab.index0 + ti) * 0x85EBCA77u);
-        // elements past 2^32 start another stream
-        const uint32_t k2 = key + static_cast<uint32_t>(static_cast<uint64_t>(e) >> 32) * 0x632BE5ABu;
+        // mix32(element ^ key): e is a multiple of 8, so the eight words differ in their
+        // low bits alone and share the first shift; elements past 2^32 start another stream
+        uint32_t x = static_cast<uint32_t>(e) ^ (st.key + static_cast<uint32_t>(static_cast<uint64_t>(e) >> 32) * 0x632BE5ABu);
+        x ^= x >> 16;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) noise[k] = mix32(static_cast<uint32_t>(e + k) ^ k2);
+        for (uint32_t k = 0; k < 8; ++k) {
+            uint32_t r = (x ^ k) * 0x7FEB352Du;
+            r = (r ^ (r >> 15)) * 0x846CA68Bu;
+            noise[k] = r ^ (r >> 16);
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) noise[k] = 0x80008000u;
     }
     if constexpr (kState8) {
         float mm = 0.f, mv = 0.f;
-        if (e + 8 <= n) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 8; ++k)
+            if (kFull || e + k < n) {
                 mm = fmaxf(mm, fabsf(m[k]));
                 mv = fmaxf(mv, v[k]);
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (e + k < n) {
-                    mm = fmaxf(mm, fabsf(m[k]));
-                    mv = fmaxf(mv, v[k]);
-                }
-        }
         mm = warp_max(mm);
         mv = warp_max(mv);
         const float tiny = 1.17549435e-38f;
@@ -273,21 +282,21 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
             cv[k] = code_bits(z, (noise[k] >> 12) & 0xFFFF0u);
             if (z > 0.f) cv[k] = max(cv[k], 1u << 20);
         }
-        store8b(static_cast<uint8_t*>(t.m), e, n,
-                make_uint2(pack_codes(cm[0], cm[1], cm[2], cm[3]), pack_codes(cm[4], cm[5], cm[6], cm[7])));
-        store8b(static_cast<uint8_t*>(t.v), e, n,
-                make_uint2(pack_codes(cv[0], cv[1], cv[2], cv[3]), pack_codes(cv[4], cv[5], cv[6], cv[7])));
-        if (in && (threadIdx.x & 31) == 0) {
+        store8b<kFull>(static_cast<uint8_t*>(t.m), e, n,
+                       make_uint2(pack_codes(cm[0], cm[1], cm[2], cm[3]), pack_codes(cm[4], cm[5], cm[6], cm[7])));
+        store8b<kFull>(static_cast<uint8_t*>(t.v), e, n,
+                       make_uint2(pack_codes(cv[0], cv[1], cv[2], cv[3]), pack_codes(cv[4], cv[5], cv[6], cv[7])));
+        if ((threadIdx.x & 31) == 0) {
             t.m_scale[block] = sm;
             t.v_scale[block] = sv;
         }
     } else {
-        store8f(static_cast<float*>(t.m), e, n, m);
-        store8f(static_cast<float*>(t.v), e, n, v);
+        store8f<kFull>(static_cast<float*>(t.m), e, n, m);
+        store8f<kFull>(static_cast<float*>(t.v), e, n, v);
     }
-    if (t.master) store8f(t.master, e, n, p);
+    if (t.master) store8f<kFull>(t.master, e, n, p);
     if (t.param_dtype == ZB_F32) {
-        store8f(static_cast<float*>(t.param), e, n, p);
+        store8f<kFull>(static_cast<float*>(t.param), e, n, p);
         return;
     }
     uint32_t w[4];
@@ -309,30 +318,66 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
     }
-    store8h(static_cast<uint16_t*>(t.param), e, n, w);
+    store8h<kFull>(static_cast<uint16_t*>(t.param), e, n, w);
+}
+
+// Bound by HBM with float32 moments.  With 8-bit ones the codecs' instructions all but
+// bind it: five blocks an SM (51 registers) ran one 8B-shaped layer's step and its
+// read-back in 1058 us, four in 1105, six in 1112; blocks that loop over four chunks, to
+// share the setup, in 1225.
+template <bool kState8, int N>
+__global__ void __launch_bounds__(kAdamThreads, kState8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamTable<N> tab, const __grid_constant__ AdamArgs a) {
+    AdamStep st;
+    // A scale that is not finite (an overflowed or NaN gradient norm) skips the step.
+    st.gs = 1.f;
+    if (a.grad_scale) {
+        st.gs = *a.grad_scale;
+        if (!(fabsf(st.gs) <= 3.402823466e38f)) return;
+    }
+    const int chunk = static_cast<int>(blockIdx.x);
+    const int ti = find_tensor(tab, chunk);
+    const zb_adamw_tensor& t = tab.t[ti];
+    const float lr = a.lr_dev ? *a.lr_dev : a.lr;
+    float bias1 = a.bias1;
+    st.rbias2 = a.rsqrt_bias2;
+    uint32_t step = a.step;
+    if (a.step_dev) {
+        const int64_t s = *a.step_dev;
+        step = static_cast<uint32_t>(s);
+        bias1 = -expm1f(static_cast<float>(s) * a.log_beta1);
+        st.rbias2 = rsqrtf(-expm1f(static_cast<float>(s) * a.log_beta2));
+    }
+    st.decay = 1.f - lr * t.weight_decay;
+    st.rate = lr / bias1;
+    st.key = mix32(mix32(a.seed ^ (step * 0x9E3779B1u)) + static_cast<uint32_t>(tab.index0 + ti) * 0x85EBCA77u);
+    const int64_t e = static_cast<int64_t>(chunk - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
+    const int64_t warp_e = e - (threadIdx.x & 31) * kPerThread;
+    if (warp_e + kStateBlock <= t.count)
+        adamw_elements<kState8, true>(t, a, st, e);
+    else if (warp_e < t.count)
+        adamw_elements<kState8, false>(t, a, st, e);
 }
 
 // The 8-bit moments as float32 values.
-__global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid_constant__ AdamTable tab,
-                                                                    const __grid_constant__ AdamUnpack out) {
-    const int64_t chunk = blockIdx.x;
+template <int N>
+__global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid_constant__ AdamTable<N> tab,
+                                                                    const __grid_constant__ AdamUnpack<N> out) {
+    const int chunk = static_cast<int>(blockIdx.x);
     const int ti = find_tensor(tab, chunk);
     const zb_adamw_tensor& t = tab.t[ti];
     const int64_t n = t.count;
-    const int64_t e = (chunk - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
+    const int64_t e = static_cast<int64_t>(chunk - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
     if (e >= n) return;
-    const uint2 cm = load8b(static_cast<const uint8_t*>(t.m), e, n), cv = load8b(static_cast<const uint8_t*>(t.v), e, n);
+    const uint2 cm = load8b<false>(static_cast<const uint8_t*>(t.m), e, n), cv = load8b<false>(static_cast<const uint8_t*>(t.v), e, n);
     const float sm = t.m_scale[e / kStateBlock], sv = t.v_scale[e / kStateBlock];
     float m[8], v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const uint32_t c = ((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u;
-        const float x = __fmul_rn(code_value(c & 127u), sm);
-        m[k] = c > 127u ? -x : x;
-        v[k] = __fmul_rn(code_value(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u), sv);
+        m[k] = decode_m(k < 4 ? cm.x : cm.y, k & 3, sm);
+        v[k] = decode_v(k < 4 ? cv.x : cv.y, k & 3, sv);
     }
-    store8f(out.m[ti], e, n, m);
-    store8f(out.v[ti], e, n, v);
+    store8f<false>(out.m[ti], e, n, m);
+    store8f<false>(out.v[ti], e, n, v);
 }
 
 // Sums of squares.  The chunks of a launch go round-robin to a fixed number of
@@ -343,10 +388,12 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid
 constexpr int kNormChunks = 4;       // chunks of a block in flight
 constexpr int kNormBlocks = 1216;    // eight blocks on each of 152 SMs
 
-// Sum of squares of thread `threadIdx.x`'s elements of chunks blockIdx.x + i gridDim.x.
-template <typename T>
-__device__ __forceinline__ T thread_squares(const AdamTable& tab, int64_t chunks) {
+// Sum of squares of thread `threadIdx.x`'s elements of chunks blockIdx.x + i gridDim.x;
+// `top`: the largest of their sizes.
+template <typename T, int N>
+__device__ __forceinline__ T thread_squares(const AdamTable<N>& tab, int chunks, float& top) {
     T s[8] = {};
+    top = 0.f;
     for (int64_t c0 = blockIdx.x; c0 < chunks; c0 += static_cast<int64_t>(kNormChunks) * gridDim.x) {
         float g[kNormChunks][8];
 #pragma unroll
@@ -355,90 +402,110 @@ __device__ __forceinline__ T thread_squares(const AdamTable& tab, int64_t chunks
 #pragma unroll
             for (int k = 0; k < 8; ++k) g[i][k] = 0.f;
             if (c < chunks) {
-                const int ti = find_tensor(tab, c);
+                const int ti = find_tensor(tab, static_cast<int>(c));
                 const zb_adamw_tensor& t = tab.t[ti];
                 const int64_t e = (c - tab.first[ti]) * kChunk + threadIdx.x * kPerThread;
                 if (t.grad_dtype == ZB_F32)
-                    load8f(static_cast<const float*>(t.grad), e, t.count, g[i]);
+                    load8f<false>(static_cast<const float*>(t.grad), e, t.count, g[i]);
                 else
-                    load8h(static_cast<const uint16_t*>(t.grad), e, t.count, g[i]);
+                    load8h<false>(static_cast<const uint16_t*>(t.grad), e, t.count, g[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < kNormChunks; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] += static_cast<T>(g[i][k]) * static_cast<T>(g[i][k]);
+            for (int k = 0; k < 8; ++k) {
+                s[k] += static_cast<T>(g[i][k]) * static_cast<T>(g[i][k]);
+                top = fmaxf(top, fabsf(g[i][k]));
+            }
     }
     return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
-__global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid_constant__ AdamTable tab, int64_t chunks,
+template <int N>
+__global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid_constant__ AdamTable<N> tab, int chunks,
                                                                     double* part) {
     __shared__ double red[kAdamThreads / 32];
-    float sum = thread_squares<float>(tab, chunks);
-    // squares that leave float32's range (or all but leave it) are summed again in float64, by the whole warp
-    const bool ok = sum <= 1e30f && sum >= 1e-25f;
+    float top;
+    float sum = thread_squares<float>(tab, chunks, top);
+    // squares that leave float32's range (or all but leave it) are summed again in
+    // float64, by the whole warp
+    const bool ok = sum <= 1e30f && (sum >= 1e-25f || top == 0.f);
     double total;
     if (__all_sync(0xffffffffu, ok)) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         total = sum;
     } else {
-        total = thread_squares<double>(tab, chunks);
+        total = thread_squares<double>(tab, chunks, top);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = total;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double t = 0.0;
-        for (int w = 0; w < kAdamThreads / 32; ++w) t += red[w];
-        part[blockIdx.x] = t;
+    if (threadIdx.x < 8) {
+        total = red[threadIdx.x];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffu, total, o);
+        if (threadIdx.x == 0) part[blockIdx.x] = total;
     }
 }
 
 // out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)).
-__global__ void __launch_bounds__(1024) norm_final_kernel(const double* part, int64_t n, float max_norm, float* out) {
-    __shared__ double red[32];
+__global__ void __launch_bounds__(256) norm_final_kernel(const double* part, int64_t n, float max_norm, float* out) {
+    __shared__ double red[8];
     double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) sum += part[i];
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * 256) {
+        double v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i0 + k * 256 < n ? part[i0 + k * 256] : 0.0;
+        sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double total = 0.0;
-        for (int w = 0; w < 32; ++w) total += red[w];
-        const double norm = sqrt(total);
-        out[0] = static_cast<float>(norm);
-        // a NaN or infinite norm gives a NaN coefficient, which skips the step
-        out[1] = isfinite(norm) ? static_cast<float>(fmin(1.0, max_norm / (norm + 1e-6))) : __int_as_float(0x7FC00000);
+    if (threadIdx.x < 8) {
+        sum = red[threadIdx.x];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffu, sum, o);
+        if (threadIdx.x == 0) {
+            // float32's square root where the sum is in its range: float64's takes longer than all the rest
+            const float norm = sum > 1e-30 && sum < 1e30 ? sqrtf(static_cast<float>(sum)) : static_cast<float>(sqrt(sum));
+            out[0] = norm;
+            // a NaN or infinite norm gives a NaN coefficient, which skips the step
+            out[1] = fabsf(norm) <= 3.402823466e38f ? fminf(1.f, max_norm / (norm + 1e-6f)) : __int_as_float(0x7FC00000);
+        }
     }
 }
 
 int64_t chunks_of(int64_t count, int64_t per) { return (count + per - 1) / per; }
 
-// Calls fn(table, chunks) for every group of up to kMaxAdamTensors tensors;
+// Calls fn(table, chunks, first tensor) for every group of tensors that fits a table;
 // empty tensors take no chunk.
-template <typename Fn>
-cudaError_t for_tables(const zb_adamw_tensor* ts, int n, int64_t per, Fn&& fn) {
-    for (int i0 = 0; i0 < n; i0 += kMaxAdamTensors) {
-        AdamTable tab{};
-        tab.n = std::min(kMaxAdamTensors, n - i0);
+template <int N, typename Fn>
+cudaError_t for_groups(const zb_adamw_tensor* ts, int n, int per, Fn&& fn) {
+    for (int i0 = 0; i0 < n; i0 += N) {
+        AdamTable<N> tab;
+        tab.n = std::min(N, n - i0);
         tab.index0 = i0;
         int64_t c = 0;
         for (int i = 0; i < tab.n; ++i) {
             tab.t[i] = ts[i0 + i];
-            tab.first[i] = c;
+            tab.first[i] = static_cast<int>(c);
             c += chunks_of(ts[i0 + i].count, per);
+            if (c > 0x7fffffff) return cudaErrorInvalidValue;
         }
-        tab.first[tab.n] = c;
+        tab.first[tab.n] = static_cast<int>(c);
         if (c == 0) continue;
-        if (c > 0x7fffffff) return cudaErrorInvalidValue;
         const cudaError_t e = fn(tab, c, i0);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+template <typename Fn>
+cudaError_t for_tables(const zb_adamw_tensor* ts, int n, int per, Fn&& fn) {
+    return n <= kFewTensors ? for_groups<kFewTensors>(ts, n, per, fn) : for_groups<kManyTensors>(ts, n, per, fn);
 }
 
 constexpr int64_t kMaxCount = int64_t(1) << 40;
@@ -476,7 +543,7 @@ extern "C" zb_status zb_op_adamw_step(const zb_adamw_tensor* tensors, int32_t n,
     if (!cfg) return ZB_ERR_ARG;
     ZB_TRY(tensors_ok(tensors, n));
     if (cfg->state_bits != 32 && cfg->state_bits != 8) return ZB_ERR_ARG;
-    if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps > 0.0) ||
+    if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps >= 1e-30) ||
         !std::isfinite(cfg->eps) || !std::isfinite(cfg->lr) || (!step_device && step < 1))
         return ZB_ERR_ARG;
     auto word_ok = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
@@ -511,7 +578,7 @@ extern "C" zb_status zb_op_adamw_step(const zb_adamw_tensor* tensors, int32_t n,
     a.lr_dev = lr_device;
     a.step_dev = step_device;
     cudaStream_t s = as_stream(stream);
-    return cuda_status(for_tables(tensors, n, kChunk, [&](const AdamTable& tab, int64_t c, int) {
+    return cuda_status(for_tables(tensors, n, kChunk, [&](const auto& tab, int64_t c, int) {
         if (state8)
             adamw_kernel<true><<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, a);
         else
@@ -530,8 +597,8 @@ extern "C" zb_status zb_op_adamw_unpack(const zb_adamw_tensor* tensors, int32_t 
     }
     ZB_TRY(device_ok());
     cudaStream_t s = as_stream(stream);
-    return cuda_status(for_tables(tensors, n, kChunk, [&](const AdamTable& tab, int64_t c, int i0) {
-        AdamUnpack out{};
+    return cuda_status(for_tables(tensors, n, kChunk, [&](const auto& tab, int64_t c, int i0) {
+        AdamUnpack<std::extent<decltype(tab.t)>::value> out;
         for (int i = 0; i < tab.n; ++i) {
             out.m[i] = m[i0 + i];
             out.v[i] = v[i0 + i];
@@ -543,7 +610,7 @@ extern "C" zb_status zb_op_adamw_unpack(const zb_adamw_tensor* tensors, int32_t 
 
 extern "C" size_t zb_op_grad_norm_scratch_bytes(const zb_adamw_tensor* tensors, int32_t n) {
     if (tensors_ok(tensors, n) != ZB_OK) return 0;
-    const int64_t launches = (n + kMaxAdamTensors - 1) / kMaxAdamTensors;
+    const int64_t launches = (n + kManyTensors - 1) / kManyTensors;
     return static_cast<size_t>(std::max<int64_t>(launches, 1)) * kNormBlocks * sizeof(double);
 }
 
@@ -558,13 +625,13 @@ extern "C" zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, 
     cudaStream_t s = as_stream(stream);
     double* part = static_cast<double*>(scratch);
     int64_t done = 0;
-    const cudaError_t e = for_tables(tensors, n, kChunk, [&](const AdamTable& tab, int64_t c, int) {
+    const cudaError_t e = for_tables(tensors, n, kChunk, [&](const auto& tab, int64_t c, int) {
         const int64_t blocks = std::min<int64_t>(c, kNormBlocks);
-        norm_partial_kernel<<<static_cast<unsigned>(blocks), kAdamThreads, 0, s>>>(tab, c, part + done);
+        norm_partial_kernel<<<static_cast<unsigned>(blocks), kAdamThreads, 0, s>>>(tab, static_cast<int>(c), part + done);
         done += blocks;
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return ZB_ERR_CUDA;
-    norm_final_kernel<<<1, 1024, 0, s>>>(part, done, max_norm, out);
+    norm_final_kernel<<<1, 256, 0, s>>>(part, done, max_norm, out);
     return cuda_status(cudaGetLastError());
 }

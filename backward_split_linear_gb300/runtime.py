@@ -167,6 +167,7 @@ class AdamW:
         nbytes = zb.zb_op_grad_norm_scratch_bytes(self.table, len(self.tensors))
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.norm = torch.zeros(4, dtype=torch.float32, device=device)  # norm, clip coefficient
+        self.norm_views = (self.norm[0], self.norm[1])
         self.stage = None
         self._states = None
 
@@ -193,7 +194,7 @@ class AdamW:
     def grad_norm(self, max_norm=1.0, stream=None):
         """(norm, clip coefficient) of all the gradients: float32 scalars on the device, rewritten by the next call."""
         zb.zb_op_grad_norm(self.table, len(self.tensors), max_norm, self.norm, self.scratch, self.scratch.numel(), stream)
-        return self.norm[0], self.norm[1]
+        return self.norm_views
 
     def step(self, grad_scale=None, stream=None):
         """One update.  A stage's weights must not change between F and W of a microbatch: its microbatches must all have

@@ -447,7 +447,7 @@ typedef struct {
 } zb_adamw_tensor;
 
 typedef struct {
-    double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps > 0 */
+    double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps >= 1e-30 */
     int32_t state_bits;           /* 32 or 8 */
     int32_t stochastic;
     uint32_t seed;
