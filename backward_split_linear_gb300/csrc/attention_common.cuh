@@ -63,8 +63,8 @@ __device__ __forceinline__ float lg2(float x) {
 
 // A wait taken by every lane of a warp, with one verdict for the warp (the
 // tensor-memory loads that follow are warp-wide).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status) {
-    const bool ok = mbar_wait_fast(bar, parity, status, kSiteAttn);
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status, uint64_t limit_ns = kWaitLimitNs) {
+    const bool ok = mbar_wait_fast(bar, parity, status, kSiteAttn, limit_ns);
     return __all_sync(0xffffffffu, ok);
 }
 

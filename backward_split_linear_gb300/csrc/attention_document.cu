@@ -117,6 +117,7 @@ struct DocArgs {
     float cap_exp;         // 2 log2(e) / (cap sqrt(d)): the exponent of e^(2 s / cap) per unit of q . k
     int tokens, n_heads, n_kv_heads, ld_stat, n_blocks;
     int* status;
+    uint64_t wait_ns;      // the limit of every wait
 };
 
 // How scores are modified: not at all, by the distance, by the cap, or by both.
@@ -154,6 +155,14 @@ __device__ __forceinline__ float dot_rows(const float (&a)[N], const float (&b)[
     return s;
 }
 
+// Keys (or queries) whose rows are on their way together: one at a time, a row by row
+// pass waits for memory.
+constexpr int kAtOnce = 4;
+constexpr uint64_t kRowPairNs = 1000;  // nanoseconds that a pair may take, for the waits' limits
+
+// What a plan's row may walk, whatever the plan's memory holds.
+__device__ __forceinline__ int2 inside(int2 see, int tokens) { return make_int2(max(see.x, 0), min(see.y, tokens)); }
+
 // The score in base-2 units, and the cap's derivative.
 __device__ __forceinline__ float score2(const DocArgs& p, float dot, float slope, int dist, float& slope_cap) {
     float s = dot * p.scale;
@@ -176,18 +185,28 @@ __device__ __forceinline__ void document_forward_row(const DocArgs& p, int i, in
     const float slope = p.slopes ? p.slopes[h] : 0.f;
     float q[D / 32], acc[D / 32] = {};
     load_row<D>(p.qkv + i * width + h * D, lane, q);
-    const int2 see = p.plan.rows[i];
+    const int2 see = inside(p.plan.rows[i], p.tokens);
     float m = -INFINITY, l = 0.f;
-    for (int j = see.x; j < see.y; ++j) {
-        float x[D / 32], unused;
-        load_row<D>(k + j * width, lane, x);
-        const float s = score2(p, dot_rows(q, x), slope, abs(i - j), unused);
-        const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - top), e = exp2f(s - top);
-        m = top;
-        l = l * f + e;
-        load_row<D>(v + j * width, lane, x);
+    for (int j0 = see.x; j0 < see.y && l == l; j0 += kAtOnce) {  // once l is NaN, so is everything
+        float x[kAtOnce][D / 32], y[kAtOnce][D / 32], dot[kAtOnce], unused;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) acc[c] = acc[c] * f + e * x[c];
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int64_t j = min(j0 + u, see.y - 1);
+            load_row<D>(k + j * width, lane, x[u]);
+            load_row<D>(v + j * width, lane, y[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) dot[u] = dot_rows(q, x[u]);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (j0 + u >= see.y) break;
+            const float s = score2(p, dot[u], slope, abs(i - j0 - u), unused);
+            const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - top), e = exp2f(s - top);
+            m = top;
+            l = l * f + e;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) acc[c] = acc[c] * f + e * y[u][c];
+        }
     }
     store_row<D>(p.out + (static_cast<int64_t>(i) * p.n_heads + h) * D, lane, acc, 1.f / l, 0, D);
     if (lane == 0) p.lse_out[static_cast<int64_t>(h) * p.ld_stat + i] = m + log2f(l);
@@ -205,15 +224,28 @@ __device__ __noinline__ void document_dq_row(const DocArgs& p, int i, int h, int
     load_row<D>(p.qkv + i * width + h * D, lane, q);
     load_row<D>(p.da + (static_cast<int64_t>(i) * p.n_heads + h) * D, lane, dy);
     const float lse = p.lse[static_cast<int64_t>(h) * p.ld_stat + i], dsum = p.dvec[static_cast<int64_t>(h) * p.ld_stat + i];
-    const int2 see = p.plan.rows[i];
-    for (int j = see.x; j < see.y; ++j) {
-        float x[D / 32], y[D / 32], f;
-        load_row<D>(k + j * width, lane, x);
-        load_row<D>(v + j * width, lane, y);
-        const float e = exp2f(score2(p, dot_rows(q, x), slope, abs(i - j), f) - lse);
-        const float ds = e * (dot_rows(dy, y) - dsum) * f;
+    const int2 see = inside(p.plan.rows[i], p.tokens);
+    float ds = 0.f;
+    for (int j0 = see.x; j0 < see.y && ds == ds; j0 += kAtOnce) {  // a NaN ds makes every sum NaN
+        float x[kAtOnce][D / 32], dot[kAtOnce], dp[kAtOnce], f;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) acc[c] += ds * x[c];
+        for (int u = 0; u < kAtOnce; ++u) {
+            float y[D / 32];
+            const int64_t j = min(j0 + u, see.y - 1);
+            load_row<D>(k + j * width, lane, x[u]);
+            load_row<D>(v + j * width, lane, y);
+            dot[u] = dot_rows(q, x[u]);
+            dp[u] = dot_rows(dy, y);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (j0 + u >= see.y) break;
+            const float e = exp2f(score2(p, dot[u], slope, abs(i - j0 - u), f) - lse);
+            ds = e * (dp[u] - dsum) * f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) acc[c] += ds * x[u][c];
+            if (ds != ds) break;
+        }
     }
     store_row<D>(p.out + i * width + h * D, lane, acc, p.scale, c0, c1);
 }
@@ -227,18 +259,32 @@ __device__ __noinline__ void document_dkv_row(const DocArgs& p, int j, int g, in
     float k[D / 32], v[D / 32], acc[D / 32] = {};
     load_row<D>(p.qkv + j * width + kcol, lane, k);
     load_row<D>(p.qkv + j * width + vcol, lane, v);
-    const int2 see = p.plan.cols[j];
-    for (int h = g * group; h < (g + 1) * group; ++h) {
+    const int2 see = inside(p.plan.cols[j], p.tokens);
+    float w = 0.f;
+    for (int h = g * group; h < (g + 1) * group && w == w; ++h) {
         const float slope = p.slopes ? p.slopes[h] : 0.f;
-        for (int i = see.x; i < see.y; ++i) {
-            float x[D / 32], y[D / 32], f;
-            load_row<D>(p.qkv + i * width + h * D, lane, x);
-            load_row<D>(p.da + (static_cast<int64_t>(i) * p.n_heads + h) * D, lane, y);
-            const float lse = p.lse[static_cast<int64_t>(h) * p.ld_stat + i], dsum = p.dvec[static_cast<int64_t>(h) * p.ld_stat + i];
-            const float e = exp2f(score2(p, dot_rows(k, x), slope, abs(i - j), f) - lse);
-            const float w = value ? e : e * (dot_rows(v, y) - dsum) * f;
+        const float* lse = p.lse + static_cast<int64_t>(h) * p.ld_stat;
+        const float* dsum = p.dvec + static_cast<int64_t>(h) * p.ld_stat;
+        for (int i0 = see.x; i0 < see.y && w == w; i0 += kAtOnce) {  // a NaN weight makes every sum NaN
+            float x[kAtOnce][D / 32], y[kAtOnce][D / 32], dot[kAtOnce], dp[kAtOnce], f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) acc[c] += w * (value ? y[c] : x[c]);
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int64_t i = min(i0 + u, see.y - 1);
+                load_row<D>(p.qkv + i * width + h * D, lane, x[u]);
+                load_row<D>(p.da + (i * p.n_heads + h) * D, lane, y[u]);
+                dot[u] = dot_rows(k, x[u]);
+                dp[u] = dot_rows(v, y[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int i = i0 + u;
+                if (i >= see.y) break;
+                const float e = exp2f(score2(p, dot[u], slope, abs(i - j), f) - lse[i]);
+                w = value ? e : e * (dp[u] - dsum[i]) * f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) acc[c] += w * (value ? y[u][c] : x[u][c]);
+                if (w != w) break;
+            }
         }
     }
     store_row<D>(p.out + j * width + (value ? vcol : kcol), lane, acc, value ? 1.f : p.scale, 0, D);
@@ -639,7 +685,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     // tile left), its head, the first key block and the steps; `see`: the intervals of
     // its row of tile A.  Then the warp releases the slot.
     auto take_tile = [&](uint32_t n, int row, int4& tile, int2& see) {
-        if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
+        if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status, p.wait_ns)) return false;
         tile = tile_slot[n & 1u];
         see = row_slot[(n & 1u) * kRows + row];
         __syncwarp();
@@ -654,7 +700,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 uint32_t nq = 0, nkv = 0, nt = 0;  // Q loads, K / V steps and tile slots issued
                 int t = static_cast<int>(blockIdx.x);
                 for (uint32_t n = 0;; ++n) {
-                    if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                     const FwdTile f = t >= 0 ? fwd_tile(p, t) : FwdTile{};
                     *reinterpret_cast<int4*>(smem_raw + L::kTileSlot + 16 * (n & 1u)) = t < 0 ? make_int4(-1, 0, 0, 0) : make_int4(f.q0[0], f.h[0], f.first, f.nk);
                     ++nt;
@@ -668,7 +714,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     bulk_load_1d(base + L::kRowSlot + 1024u * (n & 1u), p.plan.rows + f.q0[0], 1024, tile_full(n & 1u));
                     if (f.nk > 0) {
                         // Q once the previous tile's scores are formed
-                        if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                        if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                         mbar_arrive_expect_tx(q_full, 2 * kTile);
                         load_tile<D>(s_q, &map_qkv, q_full, f.h[0] * D, f.q0[0]);
                         load_tile<D>(s_q + kTile, &map_qkv, q_full, f.h[1] * D, f.q0[1]);
@@ -678,7 +724,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     bool ok = true;
                     for (int j = 0; j < f.nk; ++j) {
                         const uint32_t st = nkv % NS;
-                        if (!mbar_wait_fast(kv_empty(st), ((nkv / NS) & 1u) ^ 1u, p.status, kSiteAttn)) {
+                        if (!mbar_wait_fast(kv_empty(st), ((nkv / NS) & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) {
                             ok = false;
                             break;
                         }
@@ -692,7 +738,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     // the next tile's number after this tile's last load, a ring's depth before its end
                     mbar_arrive_expect_tx(answer_full, 16);
                     next_cta_request(s_answer, answer_full);
-                    if (!mbar_wait_fast(answer_full, n & 1u, p.status, kSiteAttn)) break;
+                    if (!mbar_wait_fast(answer_full, n & 1u, p.status, kSiteAttn, p.wait_ns)) break;
                     t = next_cta_answer(s_answer);
                     fence_proxy_async_smem();  // the answer is read before another one is written over it
                     if (t >= 0) {
@@ -702,14 +748,14 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     }
                 }
                 // no copy may land after the CTA has gone
-                if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
+                if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain, p.wait_ns);
                 for (int s = 0; s < NS; ++s) {
                     const uint32_t u = ring_uses(nkv, NS, s);
-                    if (u > 0) mbar_wait_fast(kv_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+                    if (u > 0) mbar_wait_fast(kv_full(s), (u - 1) & 1u, p.status, kSiteDrain, p.wait_ns);
                 }
                 for (int s = 0; s < 2; ++s) {
                     const uint32_t u = ring_uses(nt, 2, s);
-                    if (u > 0) mbar_wait_fast(tile_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+                    if (u > 0) mbar_wait_fast(tile_full(s), (u - 1) & 1u, p.status, kSiteDrain, p.wait_ns);
                 }
             }
         } else if (warp == 1) {
@@ -726,7 +772,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 umma_commit_elected(leader, s_full(x, g));
             };
             auto issue_pv = [&](int x, uint32_t g, bool first) {
-                if (!warp_wait(p_full(x, g), (g >> 1) & 1u, p.status)) return false;
+                if (!warp_wait(p_full(x, g), (g >> 1) & 1u, p.status, p.wait_ns)) return false;
                 tc_fence_after();
                 const uint64_t v_desc = mndesc_base(s_kv + (2 * (g % NS) + 1) * kTile);
 #pragma unroll
@@ -737,7 +783,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 return true;
             };
             auto kv_ready = [&](uint32_t g) {
-                if (!warp_wait(kv_full(g % NS), (g / NS) & 1u, p.status)) return false;
+                if (!warp_wait(kv_full(g % NS), (g / NS) & 1u, p.status, p.wait_ns)) return false;
                 tc_fence_after();
                 return true;
             };
@@ -749,7 +795,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 if (!take_tile(n, 0, tile, unused)) break;
                 const int nk = tile.w;
                 if (nk == 0) continue;
-                if (!warp_wait(q_full, nq & 1u, p.status) || !kv_ready(g)) break;
+                if (!warp_wait(q_full, nq & 1u, p.status, p.wait_ns) || !kv_ready(g)) break;
                 ++nq;
                 issue_s(0, g);
                 issue_s(1, g);
@@ -780,7 +826,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 }
             }
             umma_commit_elected(leader, drain);
-            mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+            mbar_wait_fast(drain, 0, p.status, kSiteDrain, p.wait_ns);
         }
     } else {
         registers_claim<kDocFwdMany>();
@@ -807,7 +853,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
             // -1e30, not -infinity: a row that has seen no key yet keeps finite differences
             float m = -1e30f, l = 0.f;
             for (int j = 0; j < nk; ++j, ++g) {
-                if (!warp_wait(s_full(x, g), (g >> 1) & 1u, p.status)) {
+                if (!warp_wait(s_full(x, g), (g >> 1) & 1u, p.status, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -854,7 +900,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     // O and l of all its rows to their new maxima (warp-wide
                     // tensor-memory loads and stores; rescaling to any larger
                     // reference is exact), after PV_X[j-1].
-                    if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status)) {
+                    if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -900,7 +946,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
             bool again = false;  // not finite: formed again below
             float inv = 0.f;
             if (nk > 0) {
-                if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status)) break;
+                if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status, p.wait_ns)) break;
                 tc_fence_after();
                 inv = 1.f / l;
                 again = !(fabsf(inv) <= 3e38f);
@@ -1044,7 +1090,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
     const uint32_t t_dp = tmem_base + 256, t_dq = tmem_base + 384;
     auto t_s = [&](uint32_t g) { return tmem_base + 128u * (g & 1u); };
     auto take_tile = [&](uint32_t n, int& t) {
-        if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status)) return false;
+        if (!warp_wait(tile_full(n & 1u), (n >> 1) & 1u, p.status, p.wait_ns)) return false;
         t = tile_slot[n & 1u];
         __syncwarp();
         if (lane == 0) mbar_arrive(tile_empty(n & 1u));
@@ -1054,7 +1100,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
     if (warp == 0) {
         if (lane == 0) {
             auto fetch = [&](uint32_t n) {
-                if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn)) return -2;
+                if (!mbar_wait_fast(tile_empty(n & 1u), ((n >> 1) & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) return -2;
                 int t = atomicAdd(p.counter, 1);
                 if (t >= n_tiles) t = -1;
                 tile_slot[n & 1u] = t;
@@ -1067,7 +1113,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 const DqTile tl = dq_tile(p, t);
                 if (tl.nk > 0) {
                     // Q and dO once the previous tile's S and dP products are done
-                    if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    if (!mbar_wait_fast(q_empty, (nq & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                     mbar_arrive_expect_tx(q_full, 2 * kTile);
                     load_tile<D>(s_q, &map_qkv, q_full, tl.h * D, tl.q0);
                     load_tile<D>(s_do, &map_do, q_full, tl.h * D, tl.q0);
@@ -1078,11 +1124,11 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 int t_next = tl.nk > 0 ? -2 : fetch(n + 1);
                 for (int j = 0; j < tl.nk; ++j) {
                     const uint32_t u = nkf;
-                    if (!mbar_wait_fast(k_empty(u % NK), ((u / NK) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    if (!mbar_wait_fast(k_empty(u % NK), ((u / NK) & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                     mbar_arrive_expect_tx(k_full(u % NK), kTile);
                     load_tile<D>(s_k + (u % NK) * kTile, &map_qkv, k_full(u % NK), kcol, (tl.kb0 + j) * kRows);
                     ++nkf;
-                    if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn)) break;
+                    if (!mbar_wait_fast(v_empty(u % NV), ((u / NV) & 1u) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                     mbar_arrive_expect_tx(v_full(u % NV), kTile);
                     load_tile<D>(s_v + (u % NV) * kTile, &map_qkv, v_full(u % NV), vcol, (tl.kb0 + j) * kRows);
                     ++nvf;
@@ -1099,14 +1145,14 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                 t = t_next;  // -2 after a failed wait ends the loop
             }
             // no copy may land after the CTA has gone
-            if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain);
+            if (nq > 0) mbar_wait_fast(q_full, (nq - 1) & 1u, p.status, kSiteDrain, p.wait_ns);
             for (int s = 0; s < NK; ++s) {
                 const uint32_t u = ring_uses(nkf, NK, s);
-                if (u > 0) mbar_wait_fast(k_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+                if (u > 0) mbar_wait_fast(k_full(s), (u - 1) & 1u, p.status, kSiteDrain, p.wait_ns);
             }
             for (int s = 0; s < NV; ++s) {
                 const uint32_t u = ring_uses(nvf, NV, s);
-                if (u > 0) mbar_wait_fast(v_full(s), (u - 1) & 1u, p.status, kSiteDrain);
+                if (u > 0) mbar_wait_fast(v_full(s), (u - 1) & 1u, p.status, kSiteDrain, p.wait_ns);
             }
         }
     } else if (warp == 1) {
@@ -1116,7 +1162,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
         const uint64_t q_desc = kdesc_base(s_q), do_desc = kdesc_base(s_do);
         auto issue_s = [&](uint32_t g) {
             const uint32_t st = g % NK;
-            if (!warp_wait(k_full(st), (g / NK) & 1u, p.status)) return false;
+            if (!warp_wait(k_full(st), (g / NK) & 1u, p.status, p.wait_ns)) return false;
             tc_fence_after();
             const uint64_t k_desc = kdesc_base(s_k + st * kTile);
 #pragma unroll
@@ -1127,7 +1173,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
         };
         auto issue_dp = [&](uint32_t g) {
             const uint32_t st = g % NV;
-            if (!warp_wait(v_full(st), (g / NV) & 1u, p.status)) return false;
+            if (!warp_wait(v_full(st), (g / NV) & 1u, p.status, p.wait_ns)) return false;
             tc_fence_after();
             const uint64_t v_desc = kdesc_base(s_v + st * kTile);
 #pragma unroll
@@ -1142,13 +1188,13 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
         // once the row warps are done with it.
         auto may_issue_s = [&](uint32_t g) {
             if (g < 2) return true;
-            if (!warp_wait(dq_issued(g - 2), ((g - 2) >> 1) & 1u, p.status)) return false;
+            if (!warp_wait(dq_issued(g - 2), ((g - 2) >> 1) & 1u, p.status, p.wait_ns)) return false;
             tc_fence_after();
             return true;
         };
         auto may_issue_dp = [&](uint32_t g) {
             if (g < 1) return true;
-            if (!warp_wait(ds_full(g - 1), ((g - 1) >> 1) & 1u, p.status)) return false;
+            if (!warp_wait(ds_full(g - 1), ((g - 1) >> 1) & 1u, p.status, p.wait_ns)) return false;
             tc_fence_after();
             return true;
         };
@@ -1159,7 +1205,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             if (!take_tile(n, t) || t < 0) break;
             const int nk = dq_tile(p, t).nk;
             if (nk == 0) continue;
-            if (!warp_wait(q_full, nq & 1u, p.status)) break;
+            if (!warp_wait(q_full, nq & 1u, p.status, p.wait_ns)) break;
             ++nq;
             tc_fence_after();
             // the MMA order per step is S[g+1], dP[g+1] (here) beside dQ[g] (the dQ warp)
@@ -1175,7 +1221,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             }
         }
         umma_commit_elected(leader, drain);
-        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain, p.wait_ns);
     } else if (warp == kDqWarp) {
         // ---------------- dQ products
         const uint32_t leader = elect_one_sync();
@@ -1188,8 +1234,8 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             const int nk = dq_tile(p, t).nk;
             if (nk == 0) continue;
             for (int j = 0; j < nk; ++j, ++g) {
-                if (!warp_wait(ds_full(g), (g >> 1) & 1u, p.status) ||
-                    (j + 1 < nk && !warp_wait(dp_issued(g + 1), ((g + 1) >> 1) & 1u, p.status))) {
+                if (!warp_wait(ds_full(g), (g >> 1) & 1u, p.status, p.wait_ns) ||
+                    (j + 1 < nk && !warp_wait(dp_issued(g + 1), ((g + 1) >> 1) & 1u, p.status, p.wait_ns))) {
                     ok = false;
                     break;
                 }
@@ -1206,7 +1252,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             if (ok) umma_commit_elected(leader, done);
         }
         umma_commit_elected(leader, drain);
-        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain, p.wait_ns);
     } else {
         // ---------------- row warps: group gi takes key columns 64 gi .. 64 gi + 63 of every step
         const int gi = (warp - 2) >> 2;
@@ -1228,7 +1274,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             const float slope2 = mode_biases(M) ? p.slopes[tl.h] * kLog2e : 0.f;
             for (int j = 0; j < tl.nk; ++j, ++g) {
                 const int c0 = (tl.kb0 + j) * kRows + 64 * gi;
-                if (!warp_wait(s_full(g & 1u), (g >> 1) & 1u, p.status)) {
+                if (!warp_wait(s_full(g & 1u), (g >> 1) & 1u, p.status, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -1259,7 +1305,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
                         exp_scores<64>(pr, p.cap_log2, -lse);
                     times_cap_slope<64>(pr, th);
                 }
-                if (!warp_wait(dp_full, g & 1u, p.status)) {
+                if (!warp_wait(dp_full, g & 1u, p.status, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -1291,7 +1337,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
             bool again = false;
             float r[kChunks][32] = {};
             if (tl.nk > 0) {
-                if (!warp_wait(done, nd & 1u, p.status)) break;
+                if (!warp_wait(done, nd & 1u, p.status, p.wait_ns)) break;
                 ++nd;
                 tc_fence_after();
                 const uint32_t t_q = t_dq + (static_cast<uint32_t>(qw * 32) << 16) + 32u * (gi * kChunks);
@@ -1452,7 +1498,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             for (int i = 0; i < n_steps; ++i) {
                 const int h = g * group + i % group;
                 const int r0 = (range.x + i / group) * kRows;
-                if (!mbar_wait_fast(st_empty(i % NT), ((i / NT) & 1) ^ 1u, p.status, kSiteAttn)) break;
+                if (!mbar_wait_fast(st_empty(i % NT), ((i / NT) & 1) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                 const uint32_t stat = s_stat + 1024u * (i % NT);
                 mbar_arrive_expect_tx(st_full(i % NT), 1024);
                 bulk_load_1d(stat, p.lse + static_cast<int64_t>(h) * p.ld_stat + r0, 512, st_full(i % NT));
@@ -1460,20 +1506,20 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 ++nt;
                 // Q[i] and dO[i] land on one barrier (with the statistics operand); one
                 // release covers both stages (dK[i - 2], after dV[i - 2], read the last of them)
-                if (!mbar_wait_fast(q_empty(i % NQ), ((i / NQ) & 1) ^ 1u, p.status, kSiteAttn)) break;
+                if (!mbar_wait_fast(q_empty(i % NQ), ((i / NQ) & 1) ^ 1u, p.status, kSiteAttn, p.wait_ns)) break;
                 mbar_arrive_expect_tx(q_full(i % NQ), 2 * kTile);
                 load_tile<D>(s_q + (i % NQ) * kTile, &map_qkv, q_full(i % NQ), h * D, r0);
                 load_tile<D>(s_do + (i % ND) * kTile, &map_do, q_full(i % NQ), h * D, r0);
                 ++nq;
             }
-            mbar_wait_fast(kv_full, 0, p.status, kSiteDrain);
+            mbar_wait_fast(kv_full, 0, p.status, kSiteDrain, p.wait_ns);
             for (int s = 0; s < NQ; ++s) {
                 const uint32_t u = ring_uses(nq, NQ, s);
-                if (u > 0) mbar_wait_fast(q_full(s), (u - 1) & 1, p.status, kSiteDrain);
+                if (u > 0) mbar_wait_fast(q_full(s), (u - 1) & 1, p.status, kSiteDrain, p.wait_ns);
             }
             for (int s = 0; s < NT; ++s) {
                 const uint32_t u = ring_uses(nt, NT, s);
-                if (u > 0) mbar_wait_fast(st_full(s), (u - 1) & 1, p.status, kSiteDrain);
+                if (u > 0) mbar_wait_fast(st_full(s), (u - 1) & 1, p.status, kSiteDrain, p.wait_ns);
             }
         }
     } else if (warp == 1) {
@@ -1486,7 +1532,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
         auto issue_s = [&](int i) {
             const int st = i % NQ;
             // Q tile i and statistics operand i % NA (NA = NQ) complete one phase together
-            if (!warp_wait(q_full(st), (i / NQ) & 1, p.status)) return false;
+            if (!warp_wait(q_full(st), (i / NQ) & 1, p.status, p.wait_ns)) return false;
             tc_fence_after();
             const uint64_t q_desc = kdesc_base(s_q + st * kTile);
 #pragma unroll
@@ -1508,7 +1554,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             umma_commit_elected(leader, aug_empty(i % NA));
             return true;
         };
-        bool ok = warp_wait(kv_full, 0, p.status) && issue_s(0) && issue_dp(0);
+        bool ok = warp_wait(kv_full, 0, p.status, p.wait_ns) && issue_s(0) && issue_dp(0);
         // K steps of dV / dK in the order their P^T / dS^T chunks are packed:
         // chunk c of group g holds the K steps 4 g + 2 c and 4 g + 2 c + 1
         constexpr int kOrder[8] = {0, 1, 4, 5, 2, 3, 6, 7};
@@ -1516,7 +1562,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             const uint64_t do_mn = mndesc_base(s_do + (i % ND) * kTile);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                if (!warp_wait(p_full(c), i & 1, p.status)) {
+                if (!warp_wait(p_full(c), i & 1, p.status, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -1534,7 +1580,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             const uint64_t q_mn = mndesc_base(s_q + (i % NQ) * kTile);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                if (!warp_wait(ds_full(c), i & 1, p.status)) {
+                if (!warp_wait(ds_full(c), i & 1, p.status, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -1553,13 +1599,13 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
         }
         umma_commit_elected(leader, done);
         umma_commit_elected(leader, drain);
-        mbar_wait_fast(drain, 0, p.status, kSiteDrain);
+        mbar_wait_fast(drain, 0, p.status, kSiteDrain, p.wait_ns);
     } else if (warp == kStats) {
         // ---------------- statistics warp: step i's lse and D into B operand i % NA
         const float inv_c = 1.f / p.scale_log2;
         for (int i = 0; i < n_steps; ++i) {
-            if (!warp_wait(st_full(i % NT), (i / NT) & 1, p.status) ||
-                !warp_wait(aug_empty(i % NA), ((i / NA) & 1) ^ 1u, p.status))
+            if (!warp_wait(st_full(i % NT), (i / NT) & 1, p.status, p.wait_ns) ||
+                !warp_wait(aug_empty(i % NA), ((i / NA) & 1) ^ 1u, p.status, p.wait_ns))
                 break;
             const float* stat = reinterpret_cast<const float*>(smem_raw + L::kStat + 1024u * (i % NT));
             uint8_t* aug = smem_raw + L::kAug + (i % NA) * L::kAugTile;
@@ -1597,7 +1643,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             const float slope2 = mode_biases(M) ? p.slopes[h] * kLog2e : 0.f;
             const float x = static_cast<float>(k - qc0);  // the column at distance 0
             const int lo = see.x - qc0, hi = see.y - qc0;  // this key's queries
-            if (!warp_wait(s_full, i & 1, p.status)) {
+            if (!warp_wait(s_full, i & 1, p.status, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -1646,7 +1692,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
                 tc_fence_before();
                 warp_arrive(p_full(c), lane);
             }
-            if (!warp_wait(dp_full, i & 1, p.status)) {
+            if (!warp_wait(dp_full, i & 1, p.status, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -1670,7 +1716,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
             }
         }
         // group 0 stores dK, group 1 dV
-        if (ok && warp_wait(done, 0, p.status)) {
+        if (ok && warp_wait(done, 0, p.status, p.wait_ns)) {
             tc_fence_after();
             const uint32_t t_acc = (gi == 0 ? t_dk : t_dv) + (static_cast<uint32_t>(qw * 32) << 16);
             const float sc = gi == 0 ? p.scale : 1.f;
@@ -1748,6 +1794,8 @@ DocArgs doc_args(const DocShape& s, const void* qkv, const void* plan, const flo
     p.ld_stat = s.ld_stat;
     p.n_blocks = static_cast<int>(doc_blocks(s.tokens));
     p.status = status_word();
+    // a warp may be forming 32 rows over, one by one, while others wait for it
+    p.wait_ns = kWaitLimitNs + static_cast<uint64_t>(s.tokens) * 32u * kRowPairNs;
     return p;
 }
 

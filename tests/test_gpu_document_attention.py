@@ -263,6 +263,43 @@ def test_values_that_are_not_finite_stay_where_they_are_seen(bad, cap, bias, d):
     assert_near(dqkv[unseen][:, nh * d:], rd[unseen][:, nh * d:], "dk, dv")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_rows_with_values_that_are_not_finite(d):
+    """One infinite value that every row sees sends every row to the pass over its own pairs: 12000 keys a row.  The
+    other columns are those of clean inputs; batches of nothing but NaN give NaN, and end soon."""
+    t, nh, nkv = 12000, 2, 1
+    qkv, da = draw(21, t, nh, nkv, d)
+    plan = make_plan(t, None)
+    x = qkv.clone()
+    x[0, (nh + nkv) * d] = float("inf")
+    a, lse = forward(x, t, nh, nkv, d, plan)
+    b, lse_b = forward(qkv, t, nh, nkv, d, plan)
+    a3, b3 = a.view(t, nh, d), b.view(t, nh, d)
+    assert torch.isposinf(a3[:, :, 0]).all()
+    # both within one bar of the same numbers
+    assert float((a3[:, :, 1:].double() - b3[:, :, 1:].double()).norm()) <= 2 * FRO_TOL * float(b3.double().norm())
+    assert float((lse - lse_b)[:, :t].abs().max()) <= 2.0 ** -10
+    dy = da.clone()
+    dy[:, ::d] = 0.0  # the infinite column's gradient: 0 times infinity is NaN in D, so a and x lose it
+    x[0, (nh + nkv) * d] = 0.0
+    a3[:, :, 0] = 0.0
+    da2 = dy.clone()
+    da2[t - 1, 1] = float("inf")  # every key of the last row, and its dq
+    dqkv = backward(x, a, da2, lse, t, nh, nkv, d, plan)
+    want = backward(x, a, dy, lse, t, nh, nkv, d, plan)
+    w = nh * d
+    assert float((dqkv[:t - 1, :w].double() - want[:t - 1, :w].double()).norm()) <= 2 * FRO_TOL * float(want[:, :w].double().norm())
+    assert not torch.isfinite(dqkv[t - 1, :d].float()).any() and torch.isfinite(dqkv[:, d:w].float()).all()
+    dv, dv_want = dqkv[:, w + nkv * d:].double(), want[:, w + nkv * d:].double()
+    assert torch.isposinf(dv[:, 1]).all()
+    rest = [c for c in range(d) if c != 1]
+    assert float((dv[:, rest] - dv_want[:, rest]).norm()) <= 2 * FRO_TOL * float(dv_want.norm())
+    x.fill_(float("nan"))
+    a, lse = forward(x, t, nh, nkv, d, plan)
+    dqkv = backward(x, a, dy, lse, t, nh, nkv, d, plan)
+    assert torch.isnan(a).all() and torch.isnan(lse[:, :t]).all() and torch.isnan(dqkv).all()
+
+
 def test_plan_intervals_and_positions():
     t, offsets, prefix = 300, [7, 100, 100, 290], [20, 3, 0]
     pos = torch.full((t + 1,), -7, dtype=torch.int32, device="cuda")
