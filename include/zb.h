@@ -323,7 +323,7 @@ zb_status zb_op_attention_causal_backward(const void* qkv, const void* a, const 
  *    The attention calls must get a plan made for the same `tokens`.
  *
  * slopes: float32 [n_heads] on the device, finite, or NULL; a constant, which
- * gets no gradient.  cap: 0 (none) or from 1e-3 to 1e5.  lse as in the causal core.
+ * gets no gradient.  cap: 0 (none) or from 1e-3 to 512.  lse as in the causal core.
  * scratch: device memory of at least
  * zb_op_attention_document_scratch_bytes(tokens, n_heads) bytes, contents
  * ignored; calls that share it must not overlap on the GPU.  hd is 64 or 128.

@@ -222,6 +222,21 @@ def test_large_scores_and_rising_maxima():
         assert_near(a, ra, "a")
 
 
+@pytest.mark.parametrize("cap,q_scale", [(1e-3, 2.0 ** -10), (1e-3, 1.0), (512.0, 32.0), (512.0, 256.0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_smallest_and_the_largest_cap(cap, q_scale, d):
+    """Scores below the cap and far above it.  Scores around 512 leave a nearly one-hot softmax, whose dq and dk cancel:
+    there a alone is compared."""
+    t, nh, nkv, offsets = 600, 2, 1, [0, 350, 600]
+    qkv, da = draw(31, t, nh, nkv, d, q_scale)
+    see, plan = visible(t, offsets), make_plan(t, offsets)
+    a, lse = forward(qkv, t, nh, nkv, d, plan, cap)
+    ra, _, rd = reference(qkv, nh, nkv, d, see, cap, None, da)
+    assert_near(a, ra, "a")
+    if cap < 1.0:
+        assert_near(backward(qkv, a, da, lse, t, nh, nkv, d, plan, cap), rd, "dqkv")
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (5.0, False), (0.0, True)])
 @pytest.mark.parametrize("d", [64, 128])

@@ -184,7 +184,7 @@ def test_document_refusals(zblib):
         for kw in (dict(d=96), dict(d=32), dict(nkv=3), dict(nkv=0), dict(t=-1), dict(t=(1 << 24) + 1)):
             refused("ZB_ERR_SHAPE", call, **kw)
         for kw in (dict(qkv=None), dict(a=FAKE + 2), dict(lse=None), dict(p=None), dict(p=FAKE + 8), dict(slopes=FAKE + 2),
-                   dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")), dict(cap=1e-4), dict(cap=1e6)):
+                   dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")), dict(cap=1e-4), dict(cap=513.0), dict(cap=1e6)):
             refused("ZB_ERR_ARG", call, **kw)
     refused("ZB_ERR_ARG", bwd, da=None)
     refused("ZB_ERR_ARG", bwd, dqkv=FAKE + 4)
@@ -241,6 +241,7 @@ def test_document_stage_refusals(zblib):
         refused("ZB_ERR_ARG", opts, st, 64, "half", None)
         refused("ZB_ERR_ARG", opts, st, 64, "half", FAKE, float("nan"))
         refused("ZB_ERR_ARG", opts, st, cap=-1.0)
+        refused("ZB_ERR_ARG", opts, st, cap=600.0)
         refused("ZB_ERR_ARG", opts, st, slopes=FAKE + 2)
         fwd = zb.zb_stage_forward_documents
         refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, FAKE, None, 0, FAKE, 0)
