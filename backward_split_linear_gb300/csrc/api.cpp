@@ -1056,7 +1056,9 @@ extern "C" zb_status zb_stage_forward(zb_stage_t st, int32_t mb, const void* x, 
 extern "C" zb_status zb_stage_forward_documents(zb_stage_t st, int32_t mb, const void* x, int32_t tokens,
                                                 const int32_t* doc_offsets, const int32_t* prefix_len, int32_t n_docs,
                                                 void* y, void* stream) {
-    if (!st || st->cfg.attention != ZB_ATTN_DOCUMENT || n_docs < 1 || (!doc_offsets && n_docs != 1)) return ZB_ERR_ARG;
+    if (!st || st->cfg.attention != ZB_ATTN_DOCUMENT || n_docs < 1 || n_docs > zbk::kMaxDocuments ||
+        (!doc_offsets && n_docs != 1))
+        return ZB_ERR_ARG;
     for (const void* p : {static_cast<const void*>(doc_offsets), static_cast<const void*>(prefix_len)})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return ZB_ERR_ARG;
     Documents docs;

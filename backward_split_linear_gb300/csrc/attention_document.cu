@@ -1938,7 +1938,7 @@ extern "C" zb_status zb_op_attention_document_plan(const int32_t* doc_offsets, c
                                                    int32_t tokens, void* plan, size_t plan_bytes, int32_t* positions,
                                                    void* stream) {
     if (!tokens_ok(tokens)) return ZB_ERR_SHAPE;
-    if (n_docs < 1 || (!doc_offsets && n_docs != 1) || !word_ok(doc_offsets) || !word_ok(prefix_len) || !word_ok(positions))
+    if (n_docs < 1 || n_docs > kMaxDocuments || (!doc_offsets && n_docs != 1) || !word_ok(doc_offsets) || !word_ok(prefix_len) || !word_ok(positions))
         return ZB_ERR_ARG;
     if (tokens > 0 && (!plan || !aligned16(plan) || plan_bytes < doc_plan_bytes(tokens))) return ZB_ERR_WORKSPACE;
     ZB_TRY(device_ok());

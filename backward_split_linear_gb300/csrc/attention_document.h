@@ -22,6 +22,7 @@ struct DocPlan {
 };
 
 constexpr int kDocBlock = 128;
+constexpr int kMaxDocuments = 1 << 28;  // the search for a row's document adds two of their numbers
 
 __host__ __device__ inline int64_t doc_blocks(int64_t tokens) { return (tokens + kDocBlock - 1) / kDocBlock; }
 inline size_t doc_plan_bytes(int64_t tokens) { return static_cast<size_t>(doc_blocks(tokens)) * (2 * kDocBlock + 2) * sizeof(int2); }

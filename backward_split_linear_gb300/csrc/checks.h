@@ -30,6 +30,7 @@ inline bool tokens_ok(int32_t t) { return t >= 0 && t <= kMaxTokens; }
 
 inline bool heads_ok(int32_t nh, int32_t nkv, int32_t hd) {
     if (nh <= 0 || nkv <= 0 || hd <= 0 || hd % 8 != 0 || nh % nkv != 0) return false;
+    if (nh > kMaxFeature / hd) return false;  // the products below would pass 32 bits
     if (!feature_ok(nh * hd) || !feature_ok((nh + 2 * nkv) * hd)) return false;
     return true;
 }

@@ -305,7 +305,7 @@ zb_status zb_op_attention_causal_backward(const void* qkv, const void* a, const 
  * The plan turns a batch's offsets into what the kernels read; one plan serves
  * every layer's forward and backward of that batch.
  *  - doc_offsets: int32 [n_docs + 1] on the device, not decreasing: document d is
- *    the rows [doc_offsets[d], doc_offsets[d + 1]) (it may be empty).  NULL with
+ *    the rows [doc_offsets[d], doc_offsets[d + 1]) (it may be empty); at most 2^28.  NULL with
  *    n_docs = 1: all rows are one document.  Offsets are data and are not
  *    checked: values that decrease give an unspecified mask, but no access
  *    outside the tensors.

@@ -166,6 +166,7 @@ def test_document_refusals(zblib):
 
     refused("ZB_ERR_SHAPE", plan, t=-1)
     refused("ZB_ERR_ARG", plan, n=0)
+    refused("ZB_ERR_ARG", plan, n=(1 << 28) + 1)
     refused("ZB_ERR_ARG", plan, off=None)            # no offsets: one document
     refused("ZB_ERR_ARG", plan, off=FAKE + 2)
     refused("ZB_ERR_ARG", plan, pos=FAKE + 1)
@@ -181,7 +182,8 @@ def test_document_refusals(zblib):
         zb.zb_op_attention_document_backward(qkv, a, da, lse, dqkv, p, slopes, cap, t, nh, nkv, d, s, size, stream=0)
 
     for call in (fwd, bwd):
-        for kw in (dict(d=96), dict(d=32), dict(nkv=3), dict(nkv=0), dict(t=-1), dict(t=(1 << 24) + 1)):
+        for kw in (dict(d=96), dict(d=32), dict(nkv=3), dict(nkv=0), dict(t=-1), dict(t=(1 << 24) + 1),
+                   dict(nh=(1 << 26) + 64, nkv=1)):
             refused("ZB_ERR_SHAPE", call, **kw)
         for kw in (dict(qkv=None), dict(a=FAKE + 2), dict(lse=None), dict(p=None), dict(p=FAKE + 8), dict(slopes=FAKE + 2),
                    dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")), dict(cap=1e-4), dict(cap=513.0), dict(cap=1e6)):
@@ -246,6 +248,7 @@ def test_document_stage_refusals(zblib):
         fwd = zb.zb_stage_forward_documents
         refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, FAKE, None, 0, FAKE, 0)
         refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, None, None, 2, FAKE, 0)
+        refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, FAKE, None, (1 << 28) + 1, FAKE, 0)
         refused("ZB_ERR_ARG", fwd, st, 0, FAKE, 10, FAKE + 2, None, 2, FAKE, 0)
         refused("ZB_ERR_SHAPE", fwd, st, 0, FAKE, 257, FAKE, None, 2, FAKE, 0)
     finally:
