@@ -269,7 +269,11 @@ __device__ __forceinline__ void adamw_elements(const zb_adamw_tensor& t, const A
             }
         mm = warp_max(mm);
         mv = warp_max(mv);
-        const float tiny = 1.17549435e-38f;
+        // a value that is not finite takes the largest code: its scale, were it infinite,
+        // would make NaN of the block's other values
+        const float tiny = 1.17549435e-38f, huge = 3.402823466e38f;
+        mm = fminf(mm, huge);
+        mv = fminf(mv, huge);
         const float sm = fmaxf(__fmul_rn(mm, 1.f / kMTop), tiny), sv = fmaxf(__fmul_rn(mv, 1.f / kVTop), tiny);
         const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
         uint32_t cm[8], cv[8];

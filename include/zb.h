@@ -418,6 +418,7 @@ zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t
  *    other seven bits.  A step sets each scale to the block's largest value
  *    times 1 / 245760 (m) or 1 / (15 2^30) (v), the largest codes' values, and
  *    never below the smallest normal float; a nonzero v never gets the code 0.
+ *    Values that are not finite count as the largest (a NaN: of its block).
  *    New states are all-zero bytes, scales included.
  *  - stochastic != 0: 8-bit codes, and bf16 params without a master copy,
  *    round up with the probability of their remainder, by a hash of (seed, t,

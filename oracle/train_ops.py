@@ -187,8 +187,9 @@ def pack(x, signed, noise16):
     n = x.size
     blocks = -(-n // BLOCK)
     ax = np.abs(np.pad(x, (0, blocks * BLOCK - n))).reshape(blocks, BLOCK)
-    scale = np.maximum(ax.max(axis=1) * (F32(1.0) / top), np.finfo(F32).tiny).astype(F32)
-    z = np.minimum(ax * (F32(1.0) / scale)[:, None], top).reshape(-1)[:n]
+    most = np.minimum(np.fmax.reduce(ax, axis=1), np.finfo(F32).max)  # values that are not finite count as the largest
+    scale = np.maximum(most * (F32(1.0) / top), np.finfo(F32).tiny).astype(F32)
+    z = np.fmin(ax * (F32(1.0) / scale)[:, None], top).reshape(-1)[:n]
     grid = code_values(False)
     low = z < F32(8.0)
     zz = np.where(low, z + F32(8.0), z).astype(np.float64)  # the subnormal codes are spaced as those of [8, 16)

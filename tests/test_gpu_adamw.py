@@ -165,6 +165,30 @@ def test_extreme_moments_in_8_bits(cuda_device):
     assert torch.isfinite(dev["master"]).all()
 
 
+@pytest.mark.parametrize("stochastic", [False, True])
+def test_values_out_of_range_spare_their_block_in_8_bits(cuda_device, stochastic):
+    """A gradient whose square overflows, an infinite and a NaN one: the moments of the elements beside them are the
+    stated codes, and the next step's parameters are finite."""
+    n, bad = 1024, {5: 2e19, 300: float("inf"), 301: -float("inf"), 700: float("nan")}
+    dev, host = draw(np.random.default_rng(11), n, 8, master=False, param="f32")
+    for i, g in bad.items():
+        dev["grad"][i] = g
+        host["grad"][i] = g
+    opt = AdamW([dev], state_bits=8, step=3, stochastic=stochastic, seed=8, **HYPER)
+    opt.step()
+    m, v = O.moments_f32(host["grad"], host["m"], host["v"], HYPER["beta1"], HYPER["beta2"])
+    noise = O.noise32(8, 4, 0, n) if stochastic else np.full(n, 0x80008000, dtype=np.uint64)
+    for name, x, signed, bits16 in (("m", m, True, noise & np.uint64(0xFFFF)), ("v", v, False, noise >> np.uint64(16))):
+        codes, scales = O.pack(x, signed, bits16)
+        assert np.isfinite(scales).all() and np.array_equal(dev[name + "_scale"].cpu().numpy(), scales)
+        ok = ~np.isnan(x)  # a NaN's sign is the hardware's
+        assert np.array_equal(dev[name].cpu().numpy()[ok], codes[ok])
+    dev["grad"].fill_(1e-3)
+    opt.step()
+    others = torch.tensor([i for i in range(n) if i not in bad], device="cuda")
+    assert torch.isfinite(dev["param"][others]).all()
+
+
 def test_stochastic_rounding_follows_a_slow_average(cuda_device):
     """v against a constant gradient: the nearest code cannot move by 5 % of a step, the stochastic one does.  Over 8192
     elements the mean's spread is 1/8 of a value / sqrt(8192), 0.14 %; four of those over 60 steps' geometric sum."""
