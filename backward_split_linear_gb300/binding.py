@@ -458,8 +458,8 @@ def adamw_table(tensors):
             x = t.get(name)
             if x is None and name == "master":
                 continue
-            if x is None or x.dtype != dtype or x.numel() != count or not x.is_contiguous():
-                raise ZBError(-1, f"adamw_table ({name}: {count} contiguous values of {dtype})")
+            if x is None or x.dtype != dtype or x.numel() != count or not x.is_contiguous() or x.device != param.device:
+                raise ZBError(-1, f"adamw_table ({name}: {count} contiguous values of {dtype} on param's device)")
         if not param.is_contiguous():
             raise ZBError(-1, "adamw_table (param must be contiguous)")
         arr[i] = zb_adamw_tensor(_ptr(param), _ptr(t.get("master")), _ptr(grad), _ptr(t["m"]), _ptr(t["v"]),

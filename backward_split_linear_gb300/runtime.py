@@ -80,6 +80,9 @@ class Stage:
         """Rotary positions, a tanh cap and distance slopes of the stage's softmax attention (see `zb_stage_set_attention`;
         the frequencies' arguments are those of `binding.zb_rotary_frequencies`).  `slopes`: float32 [n_heads]."""
         turns, magnitude = None, 1.0
+        if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.numel() != self.cfg.n_heads
+                                   or slopes.device != self.workspace.device):
+            raise zb.ZBError(-1, "Stage.set_attention (slopes are float32 [n_heads] on the stage's device)")
         if rotary_dim:
             values, magnitude = zb.zb_rotary_frequencies(rotary_dim, base, scaling, factor, context, low, high)
             turns = torch.from_numpy(np.array(values, dtype=np.uint64).view(np.int64)).to(self.workspace.device)
@@ -92,8 +95,9 @@ class Stage:
             zb.zb_stage_forward(self.handle, mb, x, x.shape[0], y, stream)
             return
         for t, n in ((documents, None), (prefix, documents.numel() - 1 if documents is not None else 1)):
-            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n)):
-                raise zb.ZBError(-1, "Stage.forward (documents and prefix are contiguous int32)")
+            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.device != x.device
+                                  or (n is not None and t.numel() != n)):
+                raise zb.ZBError(-1, "Stage.forward (documents and prefix are contiguous int32 beside x)")
         zb.zb_stage_forward_documents(self.handle, mb, x, x.shape[0], documents, prefix,
                                       documents.numel() - 1 if documents is not None else 1, y, stream)
 
@@ -163,7 +167,10 @@ class AdamW:
         want = torch.uint8 if state_bits == 8 else torch.float32
         if any(t["m"].dtype != want or t["v"].dtype != want for t in self.tensors):
             raise zb.ZBError(-1, f"AdamW (moments of {state_bits} bits are {want})")
-        device = self.tensors[0]["param"].device if self.tensors else "cuda"
+        device = self.tensors[0]["param"].device if self.tensors else torch.device("cuda")
+        for name, t in [("step_device", step_device), ("lr_device", lr_device)] + [("param", t["param"]) for t in self.tensors]:
+            if t is not None and t.device.type != device.type:
+                raise zb.ZBError(-1, f"AdamW ({name} lies on another device)")
         nbytes = zb.zb_op_grad_norm_scratch_bytes(self.table, len(self.tensors))
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.norm = torch.zeros(4, dtype=torch.float32, device=device)  # norm, clip coefficient
@@ -197,10 +204,12 @@ class AdamW:
         return self.norm_views
 
     def step(self, grad_scale=None, stream=None):
-        """One update.  A stage's weights must not change between F and W of a microbatch: its microbatches must all have
+        """One update (one that a scale which is not finite skips counts too).  A stage's weights must not change between F and W of a microbatch: its microbatches must all have
         run their W."""
         if self.stage is not None and self.stage.stats()[0] != 0:
             raise zb.ZBError(-3, "AdamW.step (microbatches of the stage still wait for their W)")
+        if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.device.type != self.norm.device.type):
+            raise zb.ZBError(-1, "AdamW.step (grad_scale is a float32 beside the tensors)")
         zb.zb_op_adamw_step(self.table, len(self.tensors), self.cfg, self.steps + 1, grad_scale, self.lr_device,
                             self.step_device, stream)
         self.steps += 1
