@@ -137,6 +137,21 @@ def test_stash_feeds_the_oracle():
     st.close()
 
 
+def test_tensors_of_the_host_are_refused():
+    inp = synth.stage_inputs("transformer", 1, 256, 512, 2, 1, 128, tokens=128, n_mb=1, seed=3)
+    st = Stage.from_synth("transformer", 1, 256, 512, 2, 1, 128, 1e-5, 128, 1, inp["params"], attention="document")
+    x, y = (torch.zeros(128, 256, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    off = torch.tensor([0, 128], dtype=torch.int32)
+    for call in (lambda: st.set_attention(slopes=torch.zeros(2)), lambda: st.set_attention(slopes=torch.zeros(1, device="cuda")),
+                 lambda: st.forward(0, x, y, documents=off), lambda: st.forward(0, x, y, prefix=off[1:]),
+                 lambda: st.forward(0, x, y, documents=off.cuda(), prefix=off.cuda())):
+        with pytest.raises(zb.ZBError) as e:
+            call()
+        assert e.value.name == "ZB_ERR_ARG"
+    st.forward(0, x, y, documents=off.cuda())  # and the stage still works
+    st.close()
+
+
 def test_rotary_in_a_causal_stage():
     L, H, F, nh, nkv, hd, T = 1, 256, 512, 4, 2, 64, 300
     inp = synth.stage_inputs("transformer", L, H, F, nh, nkv, hd, tokens=T, n_mb=1, seed=6)

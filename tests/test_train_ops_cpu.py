@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from backward_split_linear_gb300 import binding as zb
+from backward_split_linear_gb300.runtime import AdamW
 from oracle import train_ops as O
 
 FAKE = 1 << 20  # never dereferenced: the calls below fail their checks before any device call
@@ -96,6 +97,10 @@ def test_adamw_table_refusals(zblib):
                dict(master=torch.zeros(300, dtype=torch.bfloat16)), dict(grad=torch.zeros(600)[::2]), dict(v=None)):
         refused("ZB_ERR_ARG", zb.adamw_table, [tensors(**kw)])
     refused("ZB_ERR_ARG", zb.adamw_table, [tensors(bits=8, m_scale=torch.zeros(1))])
+    refused("ZB_ERR_ARG", zb.adamw_table, [tensors(m=torch.zeros(300, device="meta"))])
+    apart = torch.zeros((), device="meta")
+    refused("ZB_ERR_ARG", AdamW, [tensors()], lr_device=apart)
+    refused("ZB_ERR_ARG", AdamW([tensors()]).step, grad_scale=apart)
 
 
 def test_adamw_refusals(zblib):
