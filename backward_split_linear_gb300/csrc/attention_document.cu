@@ -359,29 +359,35 @@ __device__ __forceinline__ void cap_tanh(const DocArgs& p, float* s) {
 // Where the warp's columns all lie on one side of their rows' distance 0 the distance
 // is linear: one multiply-add of the column number, without an absolute value.
 // (kSides: with that form as well; under a cap its code would only crowd the rest out
-// of the instruction caches.)
+// of the instruction caches.)  Column numbers come as eight's start and the place in
+// it: a constant pair (c, c + 1) for every two columns takes two moves each.
 template <bool kExp, int N, bool kSides>
 __device__ __forceinline__ void bias_scores(float* s, float mul, float slope, float at, float add) {
     const uint64_t mul2 = pair_of(mul, mul);
     const bool before = kSides && __all_sync(0xffffffffu, at >= static_cast<float>(N - 1));
     if (before || (kSides && __all_sync(0xffffffffu, at <= 0.f))) {
         const float step = before ? slope : -slope;
-        const uint64_t step2 = pair_of(step, step);
         const float base = fmaf(-step, at, add);
-        const uint64_t base2 = pair_of(base, base);
+        uint64_t part[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[e] = pair_of(step * (2 * e), step * (2 * e + 1));
 #pragma unroll
         for (int c = 0; c < N; c += 2) {
-            const uint64_t rest = fma_pair(step2, pair_of(static_cast<float>(c), static_cast<float>(c + 1)), base2);
-            split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest), s[c], s[c + 1]);
+            const float rest = fmaf(static_cast<float>(c & ~7), step, base);
+            split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, add_pair(part[(c >> 1) & 3], pair_of(rest, rest))), s[c], s[c + 1]);
             if (kExp) s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
         }
         return;
     }
-    const uint64_t step2 = pair_of(-slope, -slope), at2 = pair_of(-at, -at), add2 = pair_of(add, add);
+    const uint64_t step2 = pair_of(-slope, -slope), add2 = pair_of(add, add);
+    uint64_t part[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[e] = pair_of(2.f * e, 2.f * e + 1.f);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
+        const float c8 = static_cast<float>(c & ~7) - at;
         float a, b;
-        split_pair(add_pair(pair_of(static_cast<float>(c), static_cast<float>(c + 1)), at2), a, b);
+        split_pair(add_pair(part[(c >> 1) & 3], pair_of(c8, c8)), a, b);
         const uint64_t rest = fma_pair(step2, pair_of(fabsf(a), fabsf(b)), add2);
         split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest), s[c], s[c + 1]);
         if (kExp) s[c] = ex2(s[c]), s[c + 1] = ex2(s[c + 1]);
@@ -878,9 +884,28 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     for (int c = 0; c < 128; c += 32) cap_tanh<32>(p, s + c);
                     sc = p.cap_log2;
                 }
+                // Distances: in a block whose keys all lie on one side of the warp's rows
+                // (all but the diagonal's) a score is mul s + step c + base.  Its step
+                // (c mod 8) is added here and the rest, which eight columns share, to their
+                // maximum and in the exponent: 64 constant pairs (c, c + 1) would cost two
+                // moves each.
+                float step = 0.f, off = 0.f;
                 if constexpr (mode_biases(M)) {
                     const float mul = M == kDocBias ? p.scale_log2 : p.cap_log2, at = static_cast<float>(q - k0);
-                    bias_scores<false, 128, M == kDocBias>(s, mul, slope2, at, 0.f);
+                    const bool before = __all_sync(0xffffffffu, at >= 127.f);
+                    if (before || __all_sync(0xffffffffu, at <= 0.f)) {
+                        step = before ? slope2 : -slope2;
+                        off = -step * at;
+                        const uint64_t mul2 = pair_of(mul, mul);
+                        uint64_t rest[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) rest[e] = pair_of(step * (2 * e), step * (2 * e + 1));
+#pragma unroll
+                        for (int c = 0; c < 128; c += 2)
+                            split_pair(fma_pair(pair_of(s[c], s[c + 1]), mul2, rest[(c >> 1) & 3]), s[c], s[c + 1]);
+                    } else {
+                        bias_scores<false, 128, false>(s, mul, slope2, at, 0.f);
+                    }
                     sc = 1.f;
                 }
                 hide_columns<128>(s, see.x - k0, see.y - k0, -INFINITY);
@@ -888,8 +913,16 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 float mx8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+                if constexpr (mode_biases(M)) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 2) mx8[(c >> 1) & 7] = max3(mx8[(c >> 1) & 7], s[c], s[c + 1]);
+                    for (int c = 0; c < 128; c += 8) {
+                        const float m8 = max3(max3(max3(s[c], s[c + 1], s[c + 2]), s[c + 3], s[c + 4]), s[c + 5], fmaxf(s[c + 6], s[c + 7]));
+                        mx8[(c >> 3) & 7] = fmaxf(mx8[(c >> 3) & 7], m8 + fmaf(static_cast<float>(c), step, off));
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2) mx8[(c >> 1) & 7] = max3(mx8[(c >> 1) & 7], s[c], s[c + 1]);
+                }
                 float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                  fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 mx *= sc;
@@ -927,7 +960,13 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float a, b;
-                        split_pair(fma_pair(pair_of(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, m2), a, b);
+                        if constexpr (mode_biases(M)) {
+                            const int c8 = (32 * c + 2 * e) & ~7;
+                            const float add = fmaf(static_cast<float>(c8), step, off - m);
+                            split_pair(add_pair(pair_of(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), pair_of(add, add)), a, b);
+                        } else {
+                            split_pair(fma_pair(pair_of(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, m2), a, b);
+                        }
                         a = ex2(a);
                         b = ex2(b);
                         sum[e & 3] = add_pair(sum[e & 3], pair_of(a, b));
