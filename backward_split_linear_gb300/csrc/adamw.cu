@@ -23,6 +23,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "chained.cuh"
 #include "checks.h"
 #include "device_common.cuh"
 
@@ -331,6 +332,7 @@ __device__ __forceinline__ void adamw_elements(const zb_adamw_tensor& t, const A
 // share the setup, in 1225.
 template <bool kState8, int N>
 __global__ void __launch_bounds__(kAdamThreads, kState8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamTable<N> tab, const __grid_constant__ AdamArgs a) {
+    wait_for_previous();
     AdamStep st;
     // A scale that is not finite (an overflowed or NaN gradient norm) skips the step.
     st.gs = 1.f;
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kAdamThreads, kState8 ? 5 : 4) adamw_kernel(co
 template <int N>
 __global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid_constant__ AdamTable<N> tab,
                                                                     const __grid_constant__ AdamUnpack<N> out) {
+    wait_for_previous();
     const int chunk = static_cast<int>(blockIdx.x);
     const int ti = find_tensor(tab, chunk);
     const zb_adamw_tensor& t = tab.t[ti];
@@ -430,6 +433,7 @@ template <int N>
 __global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid_constant__ AdamTable<N> tab, int chunks,
                                                                     double* part) {
     __shared__ double red[kAdamThreads / 32];
+    wait_for_previous();
     float top;
     float sum = thread_squares<float>(tab, chunks, top);
     // squares that leave float32's range (or all but leave it) are summed again in
@@ -458,6 +462,7 @@ __global__ void __launch_bounds__(kAdamThreads) norm_partial_kernel(const __grid
 // out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)).
 __global__ void __launch_bounds__(256) norm_final_kernel(const double* part, int64_t n, float max_norm, float* out) {
     __shared__ double red[8];
+    wait_for_previous();
     double sum = 0.0;
     for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * 256) {
         double v[8];
@@ -584,10 +589,8 @@ extern "C" zb_status zb_op_adamw_step(const zb_adamw_tensor* tensors, int32_t n,
     cudaStream_t s = as_stream(stream);
     return cuda_status(for_tables(tensors, n, kChunk, [&](const auto& tab, int64_t c, int) {
         if (state8)
-            adamw_kernel<true><<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, a);
-        else
-            adamw_kernel<false><<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, a);
-        return cudaGetLastError();
+            return launch_chained(adamw_kernel<true, std::extent<decltype(tab.t)>::value>, static_cast<unsigned>(c), kAdamThreads, 0, s, tab, a);
+        return launch_chained(adamw_kernel<false, std::extent<decltype(tab.t)>::value>, static_cast<unsigned>(c), kAdamThreads, 0, s, tab, a);
     }));
 }
 
@@ -607,8 +610,8 @@ extern "C" zb_status zb_op_adamw_unpack(const zb_adamw_tensor* tensors, int32_t 
             out.m[i] = m[i0 + i];
             out.v[i] = v[i0 + i];
         }
-        adamw_unpack_kernel<<<static_cast<unsigned>(c), kAdamThreads, 0, s>>>(tab, out);
-        return cudaGetLastError();
+        return launch_chained(adamw_unpack_kernel<std::extent<decltype(tab.t)>::value>, static_cast<unsigned>(c), kAdamThreads, 0, s, tab,
+                              out);
     }));
 }
 
@@ -631,11 +634,11 @@ extern "C" zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, 
     int64_t done = 0;
     const cudaError_t e = for_tables(tensors, n, kChunk, [&](const auto& tab, int64_t c, int) {
         const int64_t blocks = std::min<int64_t>(c, kNormBlocks);
-        norm_partial_kernel<<<static_cast<unsigned>(blocks), kAdamThreads, 0, s>>>(tab, static_cast<int>(c), part + done);
+        double* at = part + done;
         done += blocks;
-        return cudaGetLastError();
+        return launch_chained(norm_partial_kernel<std::extent<decltype(tab.t)>::value>, static_cast<unsigned>(blocks), kAdamThreads, 0, s,
+                              tab, static_cast<int>(c), at);
     });
     if (e != cudaSuccess) return ZB_ERR_CUDA;
-    norm_final_kernel<<<1, 256, 0, s>>>(part, done, max_norm, out);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_chained(norm_final_kernel, 1, 256, 0, s, part, done, max_norm, out));
 }

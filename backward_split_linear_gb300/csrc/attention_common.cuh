@@ -7,6 +7,7 @@
 
 #include <mutex>
 
+#include "chained.cuh"
 #include "device_common.cuh"
 
 namespace zbk {
@@ -132,6 +133,7 @@ template <int D>
 __global__ void attn_causal_rowsum_kernel(const uint16_t* __restrict__ da, const uint16_t* __restrict__ a, float* dvec,
                                           int tokens, int n_heads, int ld_stat, int* counter = nullptr) {
     // the tile counter of the kernel that follows on the stream, if it has one
+    wait_for_previous();
     if (counter && blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
     constexpr int kLanesPerRow = D / 8;
     constexpr int kRowsPerPass = 32 / kLanesPerRow;

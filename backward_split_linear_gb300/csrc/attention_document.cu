@@ -28,6 +28,7 @@
 // a finite batch that code never runs.
 #include "attention_common.cuh"
 #include "attention_document.h"
+#include "chained.cuh"
 #include "checks.h"
 
 namespace zbk {
@@ -46,6 +47,7 @@ __global__ void __launch_bounds__(kDocBlock) document_plan_kernel(const int32_t*
                                                                   int tokens, int2* rows, int2* cols, int2* q_blocks,
                                                                   int2* k_blocks, int32_t* positions) {
     __shared__ int red[4][4];
+    wait_for_previous();
     const int i = blockIdx.x * kDocBlock + threadIdx.x;
     int s = 0, e = 0, pre = 0;
     if (i < tokens) {
@@ -674,6 +676,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
+    wait_for_previous();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
@@ -1121,6 +1124,7 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
+    wait_for_previous();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
@@ -1521,6 +1525,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
+    wait_for_previous();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
@@ -1863,8 +1868,8 @@ cudaError_t forward(const DocArgs& p, cudaStream_t stream) {
     if (!attn_map(&map, p.qkv, p.tokens, width, width) || !attn_map(&out, p.out, p.tokens, p.n_heads * D, p.n_heads * D, 32))
         return cudaErrorInvalidValue;
     const int64_t tiles = static_cast<int64_t>(fwd_tiles(p));
-    document_fwd_kernel<D, M><<<static_cast<unsigned>(tiles), kDocFwdThreads, DocFwdSmem<D>::kBytes, stream>>>(map, out, p);
-    return cudaGetLastError();
+    return launch_chained(document_fwd_kernel<D, M>, static_cast<unsigned>(tiles), kDocFwdThreads, DocFwdSmem<D>::kBytes, stream, map,
+                          out, p);
 }
 
 template <int D, int M>
@@ -1883,15 +1888,14 @@ cudaError_t backward(const DocArgs& p, const uint16_t* a, float* dvec, bool d_re
         if (e != cudaSuccess) return e;
     } else {
         const int64_t warps = (static_cast<int64_t>(p.tokens) * p.n_heads + 7) / 8;  // 8 rows per warp
-        attn_causal_rowsum_kernel<D><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(
-            p.da, a, dvec, p.tokens, p.n_heads, p.ld_stat, p.counter);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_chained(attn_causal_rowsum_kernel<D>, static_cast<unsigned>((warps + 7) / 8), 256, 0, stream, p.da, a,
+                                             dvec, p.tokens, p.n_heads, p.ld_stat, p.counter);
         if (e != cudaSuccess) return e;
     }
     const int64_t dkv = static_cast<int64_t>(p.n_blocks) * p.n_kv_heads;
     const int64_t dq = std::min<int64_t>(static_cast<int64_t>(p.n_blocks) * p.n_heads, sm_count());
-    document_bwd_kernel<D, M><<<static_cast<unsigned>(dkv + dq), kAttnDqThreads, doc_bwd_smem<D>(), stream>>>(mq, md, mo, mdq, p);
-    return cudaGetLastError();
+    return launch_chained(document_bwd_kernel<D, M>, static_cast<unsigned>(dkv + dq), kAttnDqThreads, doc_bwd_smem<D>(), stream, mq, md,
+                          mo, mdq, p);
 }
 
 template <int D>
@@ -1920,10 +1924,9 @@ cudaError_t launch_document_plan(const int32_t* offsets, const int32_t* prefix, 
                                  int32_t* positions, cudaStream_t stream) {
     if (tokens <= 0) return cudaSuccess;
     const DocPlan p = doc_plan(plan, tokens);
-    document_plan_kernel<<<static_cast<unsigned>(doc_blocks(tokens)), kDocBlock, 0, stream>>>(
-        offsets, prefix, n_docs, tokens, const_cast<int2*>(p.rows), const_cast<int2*>(p.cols), const_cast<int2*>(p.q_blocks),
-        const_cast<int2*>(p.k_blocks), positions);
-    return cudaGetLastError();
+    return launch_chained(document_plan_kernel, static_cast<unsigned>(doc_blocks(tokens)), kDocBlock, 0, stream, offsets, prefix, n_docs,
+                          tokens, const_cast<int2*>(p.rows), const_cast<int2*>(p.cols), const_cast<int2*>(p.q_blocks),
+                          const_cast<int2*>(p.k_blocks), positions);
 }
 
 cudaError_t launch_document_forward(const DocShape& s, const void* qkv, void* a, float* lse, const void* plan,

@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "chained.cuh"
 #include "checks.h"
 #include "device_common.cuh"
 #include "operators.h"
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs p)
             }
         }
     };
+    wait_for_previous();
     load(group);
     float2 cs[8];
     if (turned) {
@@ -163,11 +165,8 @@ cudaError_t launch_rotary(const void* x, int64_t ld_x, void* y, int64_t ld_y, co
     p.groups = (n_heads + kRotHeads - 1) / kRotHeads;
     p.threads = static_cast<int64_t>(tokens) * p.columns * p.groups;
     const unsigned grid = static_cast<unsigned>((p.threads + kRotThreads - 1) / kRotThreads);
-    if (half)
-        rotary_kernel<true><<<grid, kRotThreads, 0, stream>>>(p);
-    else
-        rotary_kernel<false><<<grid, kRotThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return half ? launch_chained(rotary_kernel<true>, grid, kRotThreads, 0, stream, p)
+                : launch_chained(rotary_kernel<false>, grid, kRotThreads, 0, stream, p);
 }
 
 }  // namespace zbk
