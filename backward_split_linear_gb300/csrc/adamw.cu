@@ -326,8 +326,8 @@ __device__ __forceinline__ void adamw_elements(const zb_adamw_tensor& t, const A
     store8h<kFull>(static_cast<uint16_t*>(t.param), e, n, w);
 }
 
-// Bound by HBM with float32 moments.  With 8-bit ones the codecs' instructions all but
-// bind it: five blocks an SM (51 registers) ran one 8B-shaped layer's step and its
+// Bound by HBM with float32 moments: 218 M elements in 912 us, 7.2 TB/s.  With 8-bit ones the
+// codecs' instructions all but bind it (80 % of issue slots): five blocks an SM (51 registers) ran one 8B-shaped layer's step and its
 // read-back in 1058 us, four in 1105, six in 1112; blocks that loop over four chunks, to
 // share the setup, in 1225.
 template <bool kState8, int N>
@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_unpack_kernel(const __grid
 // blocks, whatever the device, and each block writes one float64: a fixed
 // partition and order, so the norm is the same bits every time.  Squares are summed
 // in float32, eight sums a thread: FP64 units are scarce, and positive terms'
-// rounding errors average out (about 1e-7 of the norm measured).
+// rounding errors average out (about 1e-7 of the norm measured).  Bound by HBM: 218 M
+// float32 gradients in 122 us, 7.2 TB/s.
 constexpr int kNormChunks = 4;       // chunks of a block in flight
 constexpr int kNormBlocks = 1216;    // eight blocks on each of 152 SMs
 

@@ -41,8 +41,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// One block per 128 rows, one row per thread.  Offsets are data: whatever they
-// hold, every interval written lies inside [0, tokens].
+// One block per 128 rows, one row per thread; a binary search finds the row's
+// document.  Offsets are data: whatever they hold, every interval written lies
+// inside [0, tokens].  Bound by a launch's latency: 2.8 us at 4096 tokens.
 __global__ void __launch_bounds__(kDocBlock) document_plan_kernel(const int32_t* offsets, const int32_t* prefix, int n_docs,
                                                                   int tokens, int2* rows, int2* cols, int2* q_blocks,
                                                                   int2* k_blocks, int32_t* positions) {
@@ -615,6 +616,17 @@ struct DocFwdSmem {
 // Three warpgroups: warp 0 loads, warp 1 issues products (warps 2 and 3 only hold
 // their place), warps 4-7 and 8-11 are the softmax rows of tiles A and B.  The
 // first hands registers to the other two.
+//
+// Bound by the softmax rows: a step of two tiles takes 2700 to 2900 cycles where
+// its products take 2048 (heads of 128), and 4000 cycles lie between two tiles
+// (last product, normalising, stores, first scores).  32 heads of 128 on 8, 4096
+// tokens: 9 documents in 41 us (2.2 M pairs in visible blocks, 880 TFLOP/s of
+// theirs), 2 with a cap in 93; 16 heads of 64, one document of 16384 with a bias in
+// 600 (916 TFLOP/s of its visible pairs).  Slower: sixteen row warps of half the
+// columns (50 and 826 us), a quarter of the exponentials as polynomials on the FMA
+// pipe (46 and 714: the exponential unit is 36 % busy), scores loaded in four parts
+// beside the work on them (49 and 722), four more warps that store the results
+// while the rows go on (43 and 630).
 constexpr int kDocFwdThreads = 384;
 constexpr int kDocFwdRegs = 168, kDocFwdFew = 56, kDocFwdMany = 224;
 static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * kDocFwdRegs, "registers of the launch");
@@ -1031,7 +1043,8 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
 // ------------------------------------------------------------------------ backward: dq
 
 // The causal core's dQ tiles and pipeline (attention.cu): S and dP by warp 1, dQ
-// by warp 10, two groups of row warps with 64 key columns each.
+// by warp 10, two groups of row warps with 64 key columns each.  Bound, as dK / dV
+// below, by the row warps and the chain from one product to the next.
 template <int D>
 struct DocDqSmem {
     // One V stage where the results' 32 KiB leave no room for two: V[g + 1] lands while
@@ -1418,7 +1431,8 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
 // The causal core's dK / dV pipeline (attention.cu).  lse enters the score
 // product as an extra K step where scores are linear in q . k; a cap applies to
 // the product alone, so there the row warps read lse themselves (broadcast reads
-// that the L1 serves).
+// that the L1 serves).  A plain step takes 2900 cycles where its products take 2176:
+// S^T, P^T, dV and the next S^T follow one another.
 template <int D>
 struct DocDkvSmem {
     static constexpr int kQStages = 2, kDoStages = 2, kStatStages = 2, kAugStages = 2;
@@ -1800,6 +1814,9 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
 // CTAs form dK and dV, the rest, one per SM at most, take dQ tiles as SMs come
 // free.  (The causal core runs them on two streams, which costs a small call a
 // fork and a join, and makes one stream and counter the whole device's.)
+// 32 heads of 128 on 8, 4096 tokens: 9 documents in 98 us (tensor pipe 58 % busy), 4
+// with prefixes and a cap in 243.  Sixteen row warps of half the columns took 123 and
+// 262 with the row sums, against 118 and 269 then: kept at eight for the plain form.
 template <int D, int M>
 __global__ void __launch_bounds__(kAttnDqThreads, 1)
     document_bwd_kernel(const __grid_constant__ CUtensorMap map_qkv, const __grid_constant__ CUtensorMap map_do,
