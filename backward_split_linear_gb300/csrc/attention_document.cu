@@ -613,6 +613,11 @@ struct DocFwdSmem {
 // current one are formed, while its softmax, last product and stores run.  A
 // tile that sees nothing (padding) has no steps.
 //
+// Key blocks are taken from the last to the first: a row meets its own key, and with
+// a distance bias its largest scores, in its first block, and its accumulator is
+// seldom rescaled (from first to last, a tile of a steep slope rescaled at every
+// step, 700 cycles of 2800).
+//
 // Three warpgroups: warp 0 loads, warp 1 issues products (warps 2 and 3 only hold
 // their place), warps 4-7 and 8-11 are the softmax rows of tiles A and B.  The
 // first hands registers to the other two.
@@ -750,7 +755,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                             break;
                         }
                         mbar_arrive_expect_tx(kv_full(st), 2 * kTile);
-                        const int k0 = (f.first + j) * kRows;
+                        const int k0 = (f.first + f.nk - 1 - j) * kRows;
                         load_tile<D>(s_kv + 2 * st * kTile, &map_qkv, kv_full(st), kcol, k0);
                         load_tile<D>(s_kv + (2 * st + 1) * kTile, &map_qkv, kv_full(st), vcol, k0);
                         ++nkv;
@@ -890,7 +895,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(r[e]);
                 }
-                const int k0 = (first + j) * kRows;
+                const int k0 = (first + nk - 1 - j) * kRows;  // the diagonal first
                 // unmodified (and capped, undistanced) scores are scaled below and in the exponent's FMA
                 float sc = 1.f;
                 if constexpr (M == kDocPlain) sc = p.scale_log2;
