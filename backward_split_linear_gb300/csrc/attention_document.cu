@@ -946,31 +946,33 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                  fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 mx *= sc;
-                if (j == 0) {
-                    m = fmaxf(m, mx);
-                } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                    // A row's maximum rose far above its reference: the warp rescales
-                    // O and l of all its rows to their new maxima (warp-wide
-                    // tensor-memory loads and stores; rescaling to any larger
-                    // reference is exact), after PV_X[j-1].
-                    if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                // A row's maximum rose far above its reference: the warp rescales O and l of
+                // all its rows to their new maxima (warp-wide tensor-memory loads and
+                // stores; rescaling to any larger reference is exact), after PV_X[j-1].  Rows
+                // that have seen no key yet hold zeros and take their first maximum freely.
+                if (__any_sync(0xffffffffu, mx > m + 8.f)) {
                     const float m_new = fmaxf(m, mx);
-                    const float alpha = ex2(m - m_new);
-                    l *= alpha;
+                    if (__any_sync(0xffffffffu, mx > m + 8.f && l > 0.f)) {
+                        if (!warp_wait(pv_done(x, g - 1), ((g - 1) >> 1) & 1u, p.status, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float alpha = ex2(m - m_new);
+                        l *= alpha;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t r[32];
-                        tmem_load_32(to + t_row + 32 * c, r);
-                        tmem_wait_load();
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t r[32];
+                            tmem_load_32(to + t_row + 32 * c, r);
+                            tmem_wait_load();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                        tmem_store_32(to + t_row + 32 * c, r);
+                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                            tmem_store_32(to + t_row + 32 * c, r);
+                        }
+                        m = m_new;
+                    } else if (!(l > 0.f)) {
+                        m = m_new;
                     }
-                    m = m_new;
                 }
                 const uint64_t sc2 = pair_of(sc, sc), m2 = pair_of(-m, -m);
                 uint64_t sum[4] = {0u, 0u, 0u, 0u};
