@@ -327,7 +327,7 @@ __device__ __forceinline__ void adamw_elements(const zb_adamw_tensor& t, const A
 }
 
 // Bound by HBM with float32 moments: 218 M elements in 912 us, 7.2 TB/s.  With 8-bit ones the
-// codecs' instructions all but bind it (80 % of issue slots): five blocks an SM (51 registers) ran one 8B-shaped layer's step and its
+// codecs' instructions all but bind it (80 % of issue slots): five blocks an SM (48 registers) ran one 8B-shaped layer's step and its
 // read-back in 1058 us, four in 1105, six in 1112; blocks that loop over four chunks, to
 // share the setup, in 1225.
 template <bool kState8, int N>

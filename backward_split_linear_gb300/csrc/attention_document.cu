@@ -623,15 +623,18 @@ struct DocFwdSmem {
 // first hands registers to the other two.
 //
 // Bound by the softmax rows: a step of two tiles takes 2700 to 2900 cycles where
-// its products take 2048 (heads of 128), and 4000 cycles lie between two tiles
-// (last product, normalising, stores, first scores).  32 heads of 128 on 8, 4096
-// tokens: 9 documents in 41 us (2.2 M pairs in visible blocks, 880 TFLOP/s of
-// theirs), 2 with a cap in 93; 16 heads of 64, one document of 16384 with a bias in
-// 600 (916 TFLOP/s of its visible pairs).  Slower: sixteen row warps of half the
-// columns (50 and 826 us), a quarter of the exponentials as polynomials on the FMA
-// pipe (46 and 714: the exponential unit is 36 % busy), scores loaded in four parts
-// beside the work on them (49 and 722), four more warps that store the results
-// while the rows go on (43 and 630).
+// its products take 2048 (heads of 128; 4900 with a cap, 1500 of them for tanh, 900
+// for the exponential, 1400 until the next scores), and 4000 cycles lie between two
+// tiles (last product, normalising, stores, first scores).  32 heads of 128 on 8,
+// 4096 tokens: 9 documents in 40 us (2.2 M pairs in visible blocks, 900 TFLOP/s of
+// theirs), 2 with a cap in 94; 16 heads of 64, one document of 16384 with a bias in
+// 530 (1037 TFLOP/s of its visible pairs).  Slower, each against its time then (9
+// documents; bias): sixteen row warps of half the columns (45 -> 50 us; 805 -> 826),
+// a quarter of the exponentials as polynomials on the FMA pipe (45 -> 46; 645 -> 714:
+// the exponential unit is 36 % busy), scores loaded in four parts beside the work on
+// them (45 -> 49; 604 -> 722), four more warps that store the results while the rows
+// go on (41 -> 43; 601 -> 630), at heads of 128 steps of 64 keys with two score
+// buffers a tile (40 -> 42; a bias over 8192 rows 198 -> 232).
 constexpr int kDocFwdThreads = 384;
 constexpr int kDocFwdRegs = 168, kDocFwdFew = 56, kDocFwdMany = 224;
 static_assert(kDocFwdFew + 2 * kDocFwdMany <= 3 * kDocFwdRegs, "registers of the launch");
