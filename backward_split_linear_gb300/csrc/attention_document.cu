@@ -204,7 +204,8 @@ __device__ __forceinline__ void document_forward_row(const DocArgs& p, int i, in
         for (int u = 0; u < kAtOnce; ++u) {
             if (j0 + u >= see.y) break;
             const float s = score2(p, dot[u], slope, abs(i - j0 - u), unused);
-            const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - top), e = exp2f(s - top);
+            // a score of -infinity has no weight; ahead of every finite one, s - top would be NaN
+            const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - top), e = s == -INFINITY ? 0.f : exp2f(s - top);
             m = top;
             l = l * f + e;
 #pragma unroll

@@ -449,3 +449,35 @@ def test_the_plain_form_equals_the_oracle():
     np.testing.assert_allclose(rd, grad, atol=1e-11)
     live = see.any(1)
     np.testing.assert_allclose(rl[:, live], lse[:, live], atol=1e-11)
+
+
+@pytest.mark.parametrize("mode", ["plain", "cap", "bias"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_first", [1, 6])
+@pytest.mark.parametrize("key", [float("inf"), 3e38])
+def test_keys_of_no_weight_before_the_others(key, n_first, d, mode):
+    """A document's first keys score -infinity (an infinite value, or a product past float32's range): they have no weight
+    beside the finite scores behind them, whatever a document in the same tile holds.  Under a cap they score -cap."""
+    t, nh, nkv, offsets, cap = 300, 4, 2, [0, 60, 290], 5.0 if mode == "cap" else 0.0
+    qkv, da = draw(41, t, nh, nkv, d)
+    x = qkv.view(t, nh + 2 * nkv, d)
+    x[:, :nh, 3] = -(x[:, :nh, 3].abs() + 4.0)  # 4 times 3e38: past the range
+    x[60:60 + n_first, nh:nh + nkv, 3] = key
+    slopes = slopes_of(nh) if mode == "bias" else None
+    see = O.document_visible(t, offsets)
+    ra, rl = (torch.from_numpy(y).cuda() for y in O.document_attention(
+        qkv.double().cpu().numpy(), nh, nkv, d, see, cap, None if slopes is None else slopes.double().cpu().numpy()))
+    bad = qkv.clone()
+    bad.view(t, nh + 2 * nkv, d)[20, nh + nkv:] = float("nan")  # the values of a key of the first document
+    plan = make_plan(t, offsets)
+    a, lse = forward(bad, t, nh, nkv, d, plan, cap, slopes)
+    keep = torch.arange(60 if cap else 60 + n_first, 290, device="cuda")
+    assert_near(a[keep], ra[keep], "a")
+    assert_lse(lse[:, keep], rl[:, keep], keep.numel())
+    if math.isinf(key) and not cap:
+        assert torch.isnan(a[60:60 + n_first]).all()  # no key but those
+    if math.isinf(key) or cap:
+        return  # the formula's dq is 0 times infinity; the cap's slope at 3e38 is 0, as is its dk
+    rd = reference(qkv, nh, nkv, d, visible(t, offsets), cap, slopes, da)[2]
+    dqkv = backward(bad, a, da, lse, t, nh, nkv, d, plan, cap, slopes)
+    assert_near(dqkv[keep], rd[keep], "dqkv")
