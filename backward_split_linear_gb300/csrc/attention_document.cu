@@ -1497,19 +1497,7 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
     const int kb = static_cast<int>(blockIdx.x) / p.n_kv_heads;  // in one long document, the most work first
     const int g = static_cast<int>(blockIdx.x) % p.n_kv_heads;
     const int k0 = kb * kRows;
-    const int2 range = block_range(p.plan.k_blocks, kb, p.n_blocks);
-    const int n_steps = group * (range.y - range.x);  // (query block, head of the group) pairs
     const int kcol = (p.n_heads + g) * D, vcol = (p.n_heads + p.n_kv_heads + g) * D;
-    const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
-    if (n_steps == 0) {  // keys that nothing sees
-        for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
-            const int r = e / (D / 4), c = e % (D / 4);  // 16-byte pieces: D / 8 of dk, then D / 8 of dv
-            if (k0 + r < p.tokens)
-                *reinterpret_cast<uint4*>(p.out + (k0 + r) * width + (c < D / 8 ? kcol + 8 * c : vcol + 8 * (c - D / 8))) =
-                    make_uint4(0u, 0u, 0u, 0u);
-        }
-        return;
-    }
 
     // The constant A operands of the statistics step (ones in bf16 columns 0-2
     // for lse, 8-10 for D) and zeros in the B operands' unused columns; the
@@ -1554,11 +1542,21 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
+    const int2 range = block_range(p.plan.k_blocks, kb, p.n_blocks);
+    const int n_steps = group * (range.y - range.x);  // (query block, head of the group) pairs
     // columns: S^T 0-127 (P^T packed into 0-31 and 64-95 once read), dP^T
     // 128-255 (dS^T likewise), dV 256.., dK 256 + D..
     const uint32_t t_s = tmem_base, t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 256 + D;
 
-    if (warp == 0) {
+    if (n_steps == 0) {  // keys that nothing sees
+        const int64_t width = static_cast<int64_t>(p.n_heads + 2 * p.n_kv_heads) * D;
+        for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
+            const int r = e / (D / 4), c = e % (D / 4);  // 16-byte pieces: D / 8 of dk, then D / 8 of dv
+            if (k0 + r < p.tokens)
+                *reinterpret_cast<uint4*>(p.out + (k0 + r) * width + (c < D / 8 ? kcol + 8 * c : vcol + 8 * (c - D / 8))) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        }
+    } else if (warp == 0) {
         if (lane == 0) {
             mbar_arrive_expect_tx(kv_full, 2 * kTile);
             load_tile<D>(s_k, &map_qkv, kv_full, kcol, k0);

@@ -9,7 +9,9 @@ namespace zbk {
 
 // Returns once the kernels before this one on its stream have ended and their writes
 // are visible.  Every block of a kernel launched by `launch_chained` calls it before
-// its first access to global memory; elsewhere it returns at once.
+// its first access to global memory (the status word aside, which is only ever set), on
+// every path: a later kernel takes this one's end for the end of those before it.
+// Elsewhere it returns at once.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>

@@ -240,3 +240,46 @@ def test_kernel_class_names_follow_the_header():
     body = text[text.index("    ZB_KCLASS_GEMM_FORWARD = 0"):text.index("} zb_kernel_class;")]
     names = [n.lower() for n in re.findall(r"ZB_KCLASS_([A-Z_]+)", body) if n != "COUNT"]
     assert names == zb.KERNEL_CLASSES
+
+
+# ---------------------------------------------------------------- chained launches
+
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(HEADER)), "backward_split_linear_gb300", "csrc")
+
+
+def _closed(text, at, pair):
+    """The place behind the bracket that closes the one before `at`."""
+    depth = 1
+    while depth:
+        depth += (text[at] == pair[0]) - (text[at] == pair[1])
+        at += 1
+    return at
+
+
+def _body(source, name):
+    """The body of function `name`."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, source)).read())
+    for m in re.finditer(rf"\b{name}\(", text):
+        rest = _closed(text, m.end(), "()")
+        brace = re.match(r"\s*\{", text[rest:])
+        if brace:
+            start = rest + brace.end()
+            return text[start:_closed(text, start, "{}")]
+
+
+@pytest.mark.parametrize("source,kernels", [
+    ("attention_document.cu", {"document_plan_kernel", "document_fwd_kernel", "document_dq", "document_dkv"}),
+    ("attention_common.cuh", {"attn_causal_rowsum_kernel"}), ("rotary.cu", {"rotary_kernel"}),
+    ("adamw.cu", {"adamw_kernel", "adamw_unpack_kernel", "norm_partial_kernel", "norm_final_kernel"})])
+def test_chained_kernels_wait_before_they_touch_memory(source, kernels):
+    """A block of a chained kernel may start while the kernel before it still writes: nothing that lies in global memory
+    is read or written ahead of the wait, and no block leaves without it (the guards of the start address and, in the
+    rotary kernel, of the threads behind the last one aside)."""
+    for name in kernels:
+        head, rest = _body(source, name).split("wait_for_previous();")
+        head = re.sub(r"if \(base & 1023u\) \{.*?return;\s*\}", "", head, flags=re.S)
+        head = head.replace("if (id >= p.threads) return;", "")
+        for touch in (r"block_range\(", r"p\.plan", r"p\.(out|lse|lse_out|dvec|slopes|counter)\b", r"\boffsets\[", r"positions\[",
+                      r"load8[fhb]", r"\*a\.", r"\breturn;", r"\bload\(group\)"):
+            assert not re.search(touch, head), f"{name}: {touch} ahead of the wait"
