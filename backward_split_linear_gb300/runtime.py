@@ -59,6 +59,8 @@ class Stage:
             layers.append(d)
             self.grads.append(g)
         self.handle = zb.zb_stage_create(self.cfg, layers, self.ws_ptr, self.ws_bytes)
+        # every table that the library was given (see set_attention), the frequencies' by their values
+        self.turns, self.slopes = {}, []
 
     @staticmethod
     def from_synth(kind, n_layers, hidden, ffn, n_heads=0, n_kv_heads=0, head_dim=0, eps=1e-5,
@@ -78,16 +80,21 @@ class Stage:
     def set_attention(self, rotary_dim=0, pairs="half", base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0,
                       high=None, cap=0.0, slopes=None):
         """Rotary positions, a tanh cap and distance slopes of the stage's softmax attention (see `zb_stage_set_attention`;
-        the frequencies' arguments are those of `binding.zb_rotary_frequencies`).  `slopes`: float32 [n_heads]."""
+        the frequencies' arguments are those of `binding.zb_rotary_frequencies`).  `slopes`: float32 [n_heads].  The stage
+        keeps the tables of earlier calls: a stream may still hold kernels that read them, and a captured graph always does."""
         turns, magnitude = None, 1.0
         if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.numel() != self.cfg.n_heads
                                    or slopes.device != self.workspace.device):
             raise zb.ZBError(-1, "Stage.set_attention (slopes are float32 [n_heads] on the stage's device)")
         if rotary_dim:
             values, magnitude = zb.zb_rotary_frequencies(rotary_dim, base, scaling, factor, context, low, high)
-            turns = torch.from_numpy(np.array(values, dtype=np.uint64).view(np.int64)).to(self.workspace.device)
+            turns = self.turns.get(tuple(values))
+            if turns is None:
+                turns = torch.from_numpy(np.array(values, dtype=np.uint64).view(np.int64)).to(self.workspace.device)
+                self.turns[tuple(values)] = turns
+        if slopes is not None and not any(slopes is t for t in self.slopes):
+            self.slopes.append(slopes)
         zb.zb_stage_set_attention(self.handle, rotary_dim, pairs, turns, magnitude, cap, slopes)
-        self.attention_tensors = (turns, slopes)  # the library keeps their addresses
 
     def forward(self, mb, x, y, stream=None, documents=None, prefix=None):
         """`documents`: int32 row offsets of packed documents (attention "document"), `prefix` their prefix lengths."""

@@ -228,3 +228,52 @@ def test_a_captured_stage_step_replays():
         st.close()
     for a, b in zip(runs["eager"], runs["graph"]):
         assert torch.equal(a, b)
+
+
+def test_new_attention_options_leave_the_old_tables_in_place():
+    """A graph captured under one set of frequencies and slopes, and steps still queued on another stream, read their own
+    after the stage has been given others and small tensors have been made."""
+    L, H, F, nh, nkv, hd, T = 1, 256, 512, 4, 2, 64, 300
+    inp = synth.stage_inputs("transformer", L, H, F, nh, nkv, hd, tokens=T, n_mb=1, seed=12)
+    st = Stage.from_synth("transformer", L, H, F, nh, nkv, hd, 1e-5, T, 1, inp["params"], attention="document")
+    x, dy = bf16_from_bits(inp["x"][0]), bf16_from_bits(inp["dy"][0])
+    y, dx = (torch.empty(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    off = ints([0, 77, 290])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        st.forward(0, x, y, s, documents=off)
+        st.backward_input(0, dy, dx, s)
+        st.backward_weight(0, s)
+
+    def first():
+        st.set_attention(rotary_dim=64, slopes=torch.exp2(-torch.arange(1.0, nh + 1, device="cuda")))
+        s.wait_stream(torch.cuda.current_stream())
+
+    def others():
+        st.set_attention(rotary_dim=32, base=100.0, slopes=torch.full((nh,), 0.25, device="cuda"))
+        return [torch.full((n,), 3, dtype=torch.int64, device="cuda") for n in [32, 16, 2] * 50]
+
+    first()
+    step()
+    s.synchronize()
+    want = y.clone(), dx.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    kept = others()
+    y.zero_(), dx.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+    first()
+    y.zero_(), dx.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        step()  # queued, not waited for
+    kept += others()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+    st.close()

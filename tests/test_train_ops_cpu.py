@@ -289,3 +289,34 @@ def test_oracle_document_stage_split_equals_differences():
     h = 1e-5
     f = lambda z: np.sum(S.layer_forward(z, prm, shp)[0] * dy)  # noqa: E731
     assert abs((f(x + h * u) - f(x - h * u)) / (2 * h) - np.sum(dx * u)) < 1e-6 * max(1.0, abs(np.sum(dx * u)))
+
+
+def test_a_stage_keeps_the_tables_it_was_given(zblib):
+    """The library and the kernels on a stream have their addresses: a second set_attention gives none of them back."""
+    import gc
+    import weakref
+
+    from backward_split_linear_gb300 import synth
+    from backward_split_linear_gb300.runtime import Stage
+
+    inp = synth.stage_inputs("transformer", 1, 256, 512, 2, 1, 128, tokens=8, n_mb=1, seed=1)
+    st = Stage.from_synth("transformer", 1, 256, 512, 2, 1, 128, 1e-5, 128, 1, inp["params"], device="cpu", attention="document")
+    given, seen = [], []
+    real = zb.zb_stage_set_attention
+
+    def note(handle, rotary_dim, pairs, turns, magnitude, cap, slopes):
+        given.append([None if t is None else weakref.ref(t) for t in (turns, slopes)])
+        seen.append(turns.data_ptr() if turns is not None else 0)
+        real(handle, rotary_dim, pairs, turns, magnitude, cap, slopes)
+
+    zb.zb_stage_set_attention = note
+    try:
+        for base in (1e4, 5e5, 1e4):
+            st.set_attention(rotary_dim=64, base=base, slopes=torch.ones(2))
+        st.set_attention()
+    finally:
+        zb.zb_stage_set_attention = real
+    gc.collect()
+    assert all(ref is None or ref() is not None for pair in given for ref in pair)
+    assert seen[0] == seen[2] != seen[1]  # the same frequencies again take no new table
+    st.close()
