@@ -163,7 +163,7 @@ class AdamW:
 
     def __init__(self, tensors, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, state_bits=32, stochastic=False, seed=0, step=0,
                  step_device=None, lr_device=None):
-        self.tensors = list(tensors)
+        self.tensors = [dict(t) for t in tensors]  # the table has their addresses: not the caller's dicts, which may change
         self.table = zb.adamw_table(self.tensors)
         self.cfg = zb.make_adamw_config(lr, beta1, beta2, eps, state_bits, stochastic, seed)
         self.steps = step

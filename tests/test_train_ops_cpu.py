@@ -320,3 +320,17 @@ def test_a_stage_keeps_the_tables_it_was_given(zblib):
     assert all(ref is None or ref() is not None for pair in given for ref in pair)
     assert seen[0] == seen[2] != seen[1]  # the same frequencies again take no new table
     st.close()
+
+
+def test_adamw_keeps_the_tensors_that_its_table_points_to(zblib):
+    import gc
+    import weakref
+
+    t = tensors(bits=8)
+    opt = AdamW([t], state_bits=8)
+    refs = [weakref.ref(x) for x in t.values()]
+    for name in list(t):
+        t[name] = None  # a caller that swaps its gradients, or lets them go
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    assert opt.table[0].grad == opt.tensors[0]["grad"].data_ptr()
