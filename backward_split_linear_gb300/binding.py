@@ -191,12 +191,23 @@ def _current_stream():
     import torch
 
     torch.cuda.current_stream()  # initialises CUDA, or says why it cannot be
-    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-    if raw is None or device is None:
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
         _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
     else:
-        _current_stream = lambda: raw(device())  # noqa: E731
+        _current_stream = lambda: raw(_current_device())  # noqa: E731
     return _current_stream()
+
+
+def _current_device():
+    """The number of torch's current device, without the second look at CUDA's state that torch.cuda.current_device()
+    takes."""
+    global _current_device
+    import torch
+
+    torch.cuda.current_device()  # initialises CUDA, or says why it cannot be
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
 
 
 def _ptr(t):
@@ -437,7 +448,7 @@ def zb_op_rotary_backward(dy, dx, positions, turns, magnitude, tokens, n_heads, 
 
 def adamw_table(tensors):
     """The C array of a list of dicts: param, grad, m, v, and where they apply master, m_scale, v_scale, weight_decay
-    (tensors, whose dtypes and sizes it takes).  The table holds addresses: keep the tensors alive."""
+    (tensors of one device, whose dtypes and sizes it takes).  The table holds addresses: keep the tensors alive."""
     import torch
 
     codes = {torch.bfloat16: 0, torch.float32: 1}
@@ -460,8 +471,8 @@ def adamw_table(tensors):
                 continue
             if x is None or x.dtype != dtype or x.numel() != count or not x.is_contiguous() or x.device != param.device:
                 raise ZBError(-1, f"adamw_table ({name}: {count} contiguous values of {dtype} on param's device)")
-        if not param.is_contiguous():
-            raise ZBError(-1, "adamw_table (param must be contiguous)")
+        if not param.is_contiguous() or param.device != tensors[0]["param"].device:
+            raise ZBError(-1, "adamw_table (param must be contiguous, and on the first one's device)")
         arr[i] = zb_adamw_tensor(_ptr(param), _ptr(t.get("master")), _ptr(grad), _ptr(t["m"]), _ptr(t["v"]),
                                  _ptr(t.get("m_scale")), _ptr(t.get("v_scale")), n, t.get("weight_decay", 0.0),
                                  codes[param.dtype], codes[grad.dtype], 0)

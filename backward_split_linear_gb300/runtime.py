@@ -168,16 +168,14 @@ class AdamW:
         self.cfg = zb.make_adamw_config(lr, beta1, beta2, eps, state_bits, stochastic, seed)
         self.steps = step
         self.step_device, self.lr_device = step_device, lr_device
-        for name, t, dtype in (("step_device", step_device, torch.int64), ("lr_device", lr_device, torch.float32)):
-            if t is not None and t.dtype != dtype:
-                raise zb.ZBError(-1, f"AdamW ({name} is {dtype})")
         want = torch.uint8 if state_bits == 8 else torch.float32
         if any(t["m"].dtype != want or t["v"].dtype != want for t in self.tensors):
             raise zb.ZBError(-1, f"AdamW (moments of {state_bits} bits are {want})")
-        device = self.tensors[0]["param"].device if self.tensors else torch.device("cuda")
-        for name, t in [("step_device", step_device), ("lr_device", lr_device)] + [("param", t["param"]) for t in self.tensors]:
-            if t is not None and t.device.type != device.type:
-                raise zb.ZBError(-1, f"AdamW ({name} lies on another device)")
+        device = self.tensors[0]["param"].device if self.tensors else torch.device("cuda", zb._current_device())
+        self.device = device
+        self.index = device.index if device.type == "cuda" else None
+        self._check_scalar("AdamW", "step_device", step_device, torch.int64)
+        self._check_scalar("AdamW", "lr_device", lr_device, torch.float32)
         nbytes = zb.zb_op_grad_norm_scratch_bytes(self.table, len(self.tensors))
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.norm = torch.zeros(4, dtype=torch.float32, device=device)  # norm, clip coefficient
@@ -205,18 +203,29 @@ class AdamW:
         opt.stage = stage
         return opt
 
+    def _check_scalar(self, call, name, t, dtype):
+        if t is not None and (t.dtype != dtype or t.numel() != 1 or t.device != self.device):
+            raise zb.ZBError(-1, f"{call} ({name} is one {dtype} on {self.device}, the tensors' device)")
+
+    def _check_device(self, call):
+        """The library launches on the current device, whose kernels must not read another one's memory or the host's."""
+        if self.index is None or self.index != zb._current_device():
+            raise zb.ZBError(-1, f"AdamW.{call} (the tensors lie on {self.device}, which is not the current device)")
+
     def grad_norm(self, max_norm=1.0, stream=None):
         """(norm, clip coefficient) of all the gradients: float32 scalars on the device, rewritten by the next call."""
+        self._check_device("grad_norm")
         zb.zb_op_grad_norm(self.table, len(self.tensors), max_norm, self.norm, self.scratch, self.scratch.numel(), stream)
         return self.norm_views
 
     def step(self, grad_scale=None, stream=None):
-        """One update (one that a scale which is not finite skips counts too).  A stage's weights must not change between F and W of a microbatch: its microbatches must all have
-        run their W."""
+        """One update (one that a scale which is not finite skips counts too).  A stage's weights must not change between F
+        and W of a microbatch: its microbatches must all have run their W."""
         if self.stage is not None and self.stage.stats()[0] != 0:
             raise zb.ZBError(-3, "AdamW.step (microbatches of the stage still wait for their W)")
-        if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.device.type != self.norm.device.type):
-            raise zb.ZBError(-1, "AdamW.step (grad_scale is a float32 beside the tensors)")
+        if grad_scale is not self.norm_views[1]:
+            self._check_scalar("AdamW.step", "grad_scale", grad_scale, torch.float32)
+        self._check_device("step")
         zb.zb_op_adamw_step(self.table, len(self.tensors), self.cfg, self.steps + 1, grad_scale, self.lr_device,
                             self.step_device, stream)
         self.steps += 1
@@ -225,6 +234,7 @@ class AdamW:
         """[(m, v)] as float32 values; 8-bit states are written into buffers that the next call rewrites."""
         if self.cfg.state_bits != 8:
             return [(t["m"], t["v"]) for t in self.tensors]
+        self._check_device("unpack_states")
         if self._states is None:
             self._states = [tuple(torch.empty(t["m"].numel(), dtype=torch.float32, device=t["m"].device) for _ in range(2))
                             for t in self.tensors]

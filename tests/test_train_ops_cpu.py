@@ -334,3 +334,58 @@ def test_adamw_keeps_the_tensors_that_its_table_points_to(zblib):
     gc.collect()
     assert all(r() is not None for r in refs)
     assert opt.table[0].grad == opt.tensors[0]["grad"].data_ptr()
+
+
+class Elsewhere:
+    """A tensor of some device, as far as the checks look at one."""
+
+    def __init__(self, like, device):
+        self.like, self.device = like, torch.device(device)
+
+    dtype = property(lambda self: self.like.dtype)
+
+    def numel(self):
+        return self.like.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+def on(device, **kw):
+    return {k: Elsewhere(t, device) for k, t in tensors(**kw).items()}
+
+
+def test_adamw_takes_one_device(zblib, monkeypatch):
+    """A launch reads every tensor from the current device: another index of the same type is another device."""
+    zb.adamw_table([on("cuda:1"), on("cuda:1")])
+    refused("ZB_ERR_ARG", zb.adamw_table, [on("cuda:0"), on("cuda:1")])
+    refused("ZB_ERR_ARG", zb.adamw_table, [on("cuda:0"), tensors()])
+    one, number = torch.zeros(()), torch.zeros((), dtype=torch.int64)
+    for kw in (dict(lr_device=Elsewhere(one, "cuda:1")), dict(step_device=Elsewhere(number, "cuda:1")),
+               dict(lr_device=Elsewhere(torch.zeros(0), "cuda:0")), dict(step_device=Elsewhere(number.new_zeros(2), "cuda:0")),
+               dict(step_device=Elsewhere(one, "cuda:0"))):
+        refused("ZB_ERR_ARG", AdamW, [on("cuda:0")], **kw)
+    launched = []
+    for name in ("zb_op_adamw_step", "zb_op_grad_norm", "zb_op_adamw_unpack"):
+        monkeypatch.setattr(zb, name, lambda *a, **kw: launched.append(a))
+    for bits in (32, 8):
+        opt = AdamW([tensors(bits=bits)], state_bits=bits)  # the host's: no call may launch
+        refused("ZB_ERR_ARG", opt.step)
+        refused("ZB_ERR_ARG", opt.grad_norm)
+        if bits == 8:
+            refused("ZB_ERR_ARG", opt.unpack_states)
+        opt.device, opt.index = torch.device("cuda:1"), 1  # as if all of it lay there
+        monkeypatch.setattr(zb, "_current_device", lambda: 0)
+        refused("ZB_ERR_ARG", opt.step)
+        refused("ZB_ERR_ARG", opt.grad_norm)
+        monkeypatch.setattr(zb, "_current_device", lambda: 1)
+        for scale in (Elsewhere(one, "cuda:0"), Elsewhere(torch.zeros(0), "cuda:1"), Elsewhere(number, "cuda:1"), one):
+            refused("ZB_ERR_ARG", opt.step, grad_scale=scale)
+        assert not launched and opt.steps == 0
+        opt.step(grad_scale=Elsewhere(one, "cuda:1"))
+        opt.grad_norm()
+        assert len(launched) == 2 and opt.steps == 1
+        launched.clear()
