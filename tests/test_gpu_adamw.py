@@ -281,3 +281,58 @@ def test_a_stage_takes_a_step(cuda_device, bits):
         if "master" in t:
             assert torch.equal(t["param"].reshape(-1), t["master"].reshape(-1).to(torch.bfloat16))
     st.close()
+
+
+def test_bf16_parameters_round_up_with_the_probability_of_their_remainder(cuda_device):
+    """Bit for bit where the float32 result, known to its bar, does not lie at a carry: the bar is 2^-22 of the value
+    beside a bf16 step of 2^-8, so fewer than one in 2^10 elements is undecided."""
+    n = 70001
+    dev, host = draw(np.random.default_rng(21), n, 32, master=False)
+    opt = AdamW([dev | {"weight_decay": 0.1}], stochastic=True, seed=77, step=2, **HYPER)
+    opt.step()
+    f64 = {k: host[k].astype(np.float64) for k in ("p", "grad", "m", "v")}
+    p, _, _ = O.adamw(f64["p"], f64["grad"], f64["m"], f64["v"], 3, decay=0.1, **HYPER)
+    bar = 3 * 2.0 ** -24 * np.abs(f64["p"]) + 16 * 2.0 ** -24 * np.abs(p - f64["p"]) + 1e-37
+    noise = ((O.noise32(77, 3, 0, n) * np.uint64(0x9E3779B1)) & np.uint64(0xFFFFFFFF)) >> np.uint64(16)
+    low, high = ((np.maximum(np.abs(p) + s * bar, 0.0).astype(np.float32).view(np.uint32) + noise.astype(np.uint32)) >> 16
+                 for s in (-1.0, 1.0))
+    decided = (low == high) & (np.abs(p) > bar)
+    assert decided.sum() > n - n // 1024
+    got = dev["param"].view(torch.int16).cpu().numpy().view(np.uint16).astype(np.uint32)
+    assert np.array_equal(got[decided] & 0x7FFF, low[decided])
+    assert np.array_equal((got >> 15)[decided] == 1, (p < 0)[decided])
+
+
+def test_a_parameter_below_half_a_step_moves_on_average(cuda_device):
+    """Parameters of 1 with an update of 1e-3, against bf16 steps of 2^-8 below 1: rounded to the nearest none moves; with
+    noise the mean does.  One element spreads by at most half a step, so 2^16 of them by 2^-17: six of those."""
+    n = 1 << 16
+    for stochastic in (False, True):
+        dev, _ = draw(np.random.default_rng(22), n, 32, master=False, zero=True)
+        dev["param"].fill_(1.0)
+        dev["grad"].fill_(1.0)
+        AdamW([dev], stochastic=stochastic, seed=3, **{**HYPER, "lr": 1e-3}).step()  # m / sqrt(v) is 1 in the first step
+        mean = float(dev["param"].double().mean())
+        assert mean == 1.0 if not stochastic else abs(mean - (1.0 - 1e-3)) < 6 * 2.0 ** -17
+
+
+def test_the_nearest_code_stands_still(cuda_device):
+    """The slow average of test_stochastic_rounding_follows_a_slow_average rounded to the nearest code, over the same
+    steps: the codes are the oracle's, and their mean misses the average by more than the 2 % that the noise keeps to.
+    (An element is pulled by 5 % of its distance from 0.81e-6 and moves a code by half of 1e-6 / 15 or more: at 13 / 15
+    of its block's 0.956e-6, 7 % above the average, it stands.)"""
+    n = 8192
+    dev, host = draw(np.random.default_rng(10), n, 8, zero=True)
+    opt = AdamW([dev], state_bits=8, **HYPER)
+    m, v = host["m"], host["v"]
+    for step in range(61):
+        g = np.full(n, 0.9e-3 if step else 1e-3, dtype=np.float32)
+        g[::256] = 1e-3
+        dev["grad"].copy_(torch.from_numpy(g))
+        opt.step()
+        m, v = O.moments_f32(g, m, v, HYPER["beta1"], HYPER["beta2"])
+        m, v = (O.unpack(*O.pack(x, signed, 0x8000), signed) for x, signed in ((m, True), (v, False)))
+    got = opt.unpack_states()[0]
+    assert np.array_equal(got[0].cpu().numpy(), m) and np.array_equal(got[1].cpu().numpy(), v)
+    want = 1e-6 * 0.05 * 0.95 ** 60 + 0.81e-6 * (1 - 0.95 ** 60)
+    assert abs(v.reshape(-1, 256)[:, 1:].mean() - want) > 0.02 * want
