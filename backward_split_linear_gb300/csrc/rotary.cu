@@ -199,21 +199,23 @@ extern "C" zb_status zb_rotary_frequencies(const zb_rotary_config* cfg, uint64_t
     if (cfg->scaling >= ZB_ROTARY_SCALE_YARN &&
         (!(context >= 1.0) || !std::isfinite(context) || !(cfg->low > 0.0) || !(cfg->high > cfg->low) || !std::isfinite(cfg->high)))
         return ZB_ERR_ARG;
-    double mag = 1.0, ramp_low = 0.0, ramp_span = 1.0;
+    double mag = 1.0, ramp_low = 0.0, ramp_end = 1.0;
     if (cfg->scaling == ZB_ROTARY_SCALE_NTK) base *= std::pow(factor, rot / (rot - 2.0));
     if (!std::isfinite(base)) return ZB_ERR_ARG;
     if (cfg->scaling == ZB_ROTARY_SCALE_YARN) {
         // the pair that makes `turns` turns over the original context
         auto at = [&](double n) { return rot * std::log(context / (n * two_pi)) / (2.0 * std::log(base)); };
         ramp_low = std::max(std::floor(at(cfg->high)), 0.0);
-        ramp_span = std::max(std::min(std::ceil(at(cfg->low)), rot - 1.0) - ramp_low, 1e-3);
+        ramp_end = std::min(std::ceil(at(cfg->low)), rot - 1.0);
         mag = 0.1 * std::log(factor) + 1.0;
     }
     for (int i = 0; i < rot / 2; ++i) {
         double f = std::pow(base, -2.0 * i / rot);
         if (cfg->scaling == ZB_ROTARY_SCALE_LINEAR) f /= factor;
         if (cfg->scaling == ZB_ROTARY_SCALE_YARN) {
-            const double r = std::min(1.0, std::max(0.0, (i - ramp_low) / ramp_span));
+            // (a context of a few tokens: no pair makes `low` turns, and the ramp ends before it starts)
+            const double r = ramp_end > ramp_low ? std::min(1.0, std::max(0.0, (i - ramp_low) / (ramp_end - ramp_low)))
+                                                 : i >= ramp_end ? 1.0 : 0.0;
             f = f / factor * r + f * (1.0 - r);
         }
         if (cfg->scaling == ZB_ROTARY_SCALE_BANDED) {

@@ -375,8 +375,8 @@ typedef enum {
     ZB_ROTARY_SCALE_LINEAR = 1, /* f_i / factor: positions interpolated */
     ZB_ROTARY_SCALE_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) */
     ZB_ROTARY_SCALE_YARN = 3,   /* f_i / factor for pairs below `low` turns over the original
-                                   context, f_i above `high`, a ramp over the pair number in
-                                   between; g = 0.1 ln(factor) + 1 */
+                                   context, f_i above `high`, a ramp over the pair number (from
+                                   pair 0 on) in between; g = 0.1 ln(factor) + 1 */
     ZB_ROTARY_SCALE_BANDED = 4  /* the same with a ramp over the turns, and g = 1 */
 } zb_rotary_scaling;
 

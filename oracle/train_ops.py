@@ -39,7 +39,7 @@ def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=0.
     if scaling == "yarn":
         pair_of = lambda turns: rot * np.log(context / (2.0 * np.pi * turns)) / (2.0 * np.log(base))  # noqa: E731
         lo, hi = max(np.floor(pair_of(high)), 0.0), min(np.ceil(pair_of(low)), rot - 1.0)
-        ramp = np.array([min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in pairs])
+        ramp = np.array([min(1.0, max(0.0, (i - lo) / (hi - lo))) if hi > lo else float(i >= hi) for i in pairs])
         return (f / factor) * ramp + f * (1.0 - ramp), 0.1 * np.log(factor) + 1.0
     return f, 1.0
 

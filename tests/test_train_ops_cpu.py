@@ -389,3 +389,19 @@ def test_adamw_takes_one_device(zblib, monkeypatch):
         opt.grad_norm()
         assert len(launched) == 2 and opt.steps == 1
         launched.clear()
+
+
+@pytest.mark.parametrize("context", [1.0, 2.0, 4.0, 6.0, 6.5, 7.0, 50.0, 300.0, 8192.0, 1e7])
+@pytest.mark.parametrize("rot,base", [(16, 10000.0), (128, 500000.0), (64, 3.0)])
+def test_yarn_keeps_and_stretches_the_pairs_it_says(zblib, rot, base, context):
+    """Pairs of fewer than `low` turns over the original context are stretched in full, pairs of more than `high` kept, the
+    shortest contexts included.  In radians half a unit of the 64-bit fraction of a turn is 2 pi 2^-65."""
+    near = dict(rtol=64 * 2.0 ** -53, atol=2.0 * np.pi * 2.0 ** -65)
+    factor, low, high = 8.0, 1.0, 32.0
+    turns, _ = zb.zb_rotary_frequencies(rot, base, "yarn", factor, context, low, high)
+    got = np.array([t / 2.0 ** 64 for t in turns]) * 2.0 * np.pi
+    f = base ** (-2.0 * np.arange(rot // 2) / rot)
+    made = context * f / (2.0 * np.pi)
+    for which, want in ((made < low * (1 - 1e-9), f / factor), (made > high * (1 + 1e-9), f)):
+        np.testing.assert_allclose(got[which], want[which], **near)
+    np.testing.assert_allclose(O.rotary_frequencies(rot, base, "yarn", factor, context, low, high)[0], got, **near)
