@@ -23,9 +23,10 @@
 // Values that are not finite.  The tensor cores multiply every row of a tile
 // with every other, and 0 times NaN is NaN: a hidden key's value, or a query of
 // another document, would reach rows that do not see it.  Scores are selected,
-// not multiplied, where they are hidden; and a result row that is not finite is
-// formed again from its visible pairs alone, by the row-by-row code below.  In
-// a finite batch that code never runs.
+// not multiplied, where they are hidden; padding's rows of an operand become zeros;
+// and a result row that is not finite is formed again from its visible pairs
+// alone, by the row-by-row code below.  In a batch of finite documents that
+// code never runs.
 #include "attention_common.cuh"
 #include "attention_document.h"
 #include "chained.cuh"
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kDocBlock) document_plan_kernel(const int32_t*
     __shared__ int red[4][4];
     wait_for_previous();
     const int i = blockIdx.x * kDocBlock + threadIdx.x;
-    int s = 0, e = 0, pre = 0;
+    int s = 0, e = 0, pre = 0, border = 0;
     if (i < tokens) {
         if (offsets) {
             int lo = 0, hi = n_docs;  // the last offset at or before row i
@@ -61,8 +62,9 @@ __global__ void __launch_bounds__(kDocBlock) document_plan_kernel(const int32_t*
                 else
                     hi = mid - 1;
             }
+            border = clampi(offsets[lo], 0, tokens);  // where padding ends, or where it starts
             if (lo < n_docs) {
-                s = clampi(offsets[lo], 0, tokens);
+                s = border;
                 e = clampi(offsets[lo + 1], 0, tokens);
                 if (prefix) pre = prefix[lo];
             }
@@ -74,8 +76,8 @@ __global__ void __launch_bounds__(kDocBlock) document_plan_kernel(const int32_t*
     }
     const bool in = e > s;
     const int pend = in ? s + clampi(pre, 0, e - s) : 0;  // end of the prefix
-    const int2 row = in ? make_int2(s, max(i + 1, pend)) : make_int2(0, 0);
-    const int2 col = in ? make_int2(i < pend ? s : i, e) : make_int2(0, 0);
+    const int2 row = in ? make_int2(s, max(i + 1, pend)) : make_int2(border, border);
+    const int2 col = in ? make_int2(i < pend ? s : i, e) : make_int2(border, border);
     rows[i] = row;
     cols[i] = col;
     if (positions && i < tokens) positions[i] = in ? i - s : 0;
@@ -459,6 +461,41 @@ __device__ __forceinline__ int2 block_range(const int2* blocks, int b, int n_blo
     return make_int2(first, min(max(r.y, first), n_blocks));
 }
 
+// Padding: rows before the first document and behind the last, which see nothing and
+// which nothing sees.  They hold anything, NaN as well as what a fresh allocation left,
+// and a product over a tile would carry that into all its rows.  So the warp that issues
+// the products makes their rows of such an operand zeros in shared memory first.  (Formed
+// again pair by pair, as for what a document itself holds, the backward of a document of
+// 4000 rows behind which 96 rows were NaN took 182 ms, 32 heads of 128; with zeros 0.3.
+// By the row warps, the test alone cost batches without padding 1 to 2 %; here at most 1.)
+//
+// The rows that are not padding, [x, y): empty intervals of the first and the last row
+// say where it ends and starts.
+__device__ __forceinline__ int2 document_rows(const DocArgs& p) {
+    const int2 a = p.plan.rows[0], b = p.plan.rows[p.tokens - 1];
+    return make_int2(a.y <= a.x ? a.x : 0, b.y <= b.x ? b.x : 0x7fffffff);
+}
+__device__ __forceinline__ bool has_padding(int r0, int2 live) { return r0 < live.x || r0 + kRows > live.y; }
+// By the warp that issues the products, while it would wait for the row warps: zeros in the
+// padding rows of a tile of D columns whose first row is the tensor's r0 (boxes of 128
+// 128-byte rows; the swizzle permutes within a row), or of two tiles `other` bytes apart.
+template <int D>
+__device__ __forceinline__ void zero_padding(uint32_t tile, int r0, int2 live, int lane, uint32_t other = 0) {
+    constexpr int kLanes = D / 8;  // 16 bytes a lane
+    // rows before `head` and from `tail` on, inside the tile whatever the plan's memory holds
+    const int head = min(live.x - r0, kRows), tail = max(live.y - r0, 0);
+    const uint32_t at = tile + static_cast<uint32_t>((lane % kLanes >> 3) * 16384 + (lane & 7) * 16);
+    const int first = head > 0 ? 0 : tail, end = tail < kRows ? kRows : head;
+#pragma unroll 1
+    for (int i = first + lane / kLanes; i < end; i += 32 / kLanes)
+        if (i < head || i >= tail) {
+            st_shared_v4(at + static_cast<uint32_t>(i * 128), make_uint4(0u, 0u, 0u, 0u));
+            if (other) st_shared_v4(at + static_cast<uint32_t>(i * 128) + other, make_uint4(0u, 0u, 0u, 0u));
+        }
+    fence_proxy_async_smem();  // the products read through the other proxy
+    __syncwarp();
+}
+
 __device__ __forceinline__ bool finite32(const float (&v)[32]) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};  // 0 v is NaN for a v that is not finite
 #pragma unroll
@@ -817,6 +854,7 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 tc_fence_after();
                 return true;
             };
+            const int2 live = document_rows(p);
             uint32_t g = 0, nq = 0;  // steps and tiles with steps so far
             bool ok = true;
             for (uint32_t n = 0; ok; ++n) {
@@ -836,7 +874,9 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                 // its softmax has finished the last ones.
                 for (int j = 0; j < nk; ++j, ++g) {
                     const bool more = j + 1 < nk;
+                    const int k0 = (tile.z + nk - 1 - j) * kRows;
                     ok = false;
+                    if (has_padding(k0, live)) zero_padding<D>(s_kv + (2 * (g % NS) + 1) * kTile, k0, live, lane);  // V[g]
                     if (D == 64 && more) {
                         if (!kv_ready(g + 1)) break;
                         issue_s(0, g + 1);
@@ -1293,14 +1333,24 @@ __device__ __forceinline__ void document_dq(const CUtensorMap& map_qkv, const CU
         // ---------------- dQ products
         const uint32_t leader = elect_one_sync();
         constexpr uint32_t idesc_q = mma_idesc_bf16(128, D, false, true);
+        const int2 live = document_rows(p);
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
             int t;
             if (!take_tile(n, t) || t < 0) break;
-            const int nk = dq_tile(p, t).nk;
+            const DqTile tl = dq_tile(p, t);
+            const int nk = tl.nk;
             if (nk == 0) continue;
             for (int j = 0; j < nk; ++j, ++g) {
+                const int k0 = (tl.kb0 + j) * kRows;
+                if (has_padding(k0, live)) {  // K[g], once S[g] has read it
+                    if (!warp_wait(s_full(g & 1u), (g >> 1) & 1u, p.status, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_padding<D>(s_k + (g % NK) * kTile, k0, live, lane);
+                }
                 if (!warp_wait(ds_full(g), (g >> 1) & 1u, p.status, p.wait_ns) ||
                     (j + 1 < nk && !warp_wait(dp_issued(g + 1), ((g + 1) >> 1) & 1u, p.status, p.wait_ns))) {
                     ok = false;
@@ -1625,7 +1675,15 @@ __device__ __forceinline__ void document_dkv(const CUtensorMap& map_qkv, const C
         // K steps of dV / dK in the order their P^T / dS^T chunks are packed:
         // chunk c of group g holds the K steps 4 g + 2 c and 4 g + 2 c + 1
         constexpr int kOrder[8] = {0, 1, 4, 5, 2, 3, 6, 7};
+        // steps before pad_end and from pad_start on have padding among their queries
+        const int2 live = document_rows(p);
+        const int pad_end = has_padding(range.x * kRows, live) ? group : 0;
+        const int pad_start = n_steps - (has_padding((range.y - 1) * kRows, live) ? group : 0);
         for (int i = 0; ok && i < n_steps; ++i) {
+            if (i < pad_end || i >= pad_start) {  // Q[i] and dO[i], once S[i] and dP[i] have read them
+                if (!warp_wait(s_full, i & 1, p.status, p.wait_ns) || !warp_wait(dp_full, i & 1, p.status, p.wait_ns)) break;
+                zero_padding<D>(s_q + (i % NQ) * kTile, (range.x + i / group) * kRows, live, lane, s_do - s_q);
+            }
             const uint64_t do_mn = mndesc_base(s_do + (i % ND) * kTile);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {

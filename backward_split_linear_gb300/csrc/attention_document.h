@@ -13,7 +13,8 @@ namespace zbk {
 // Both are intervals: a document is one, and a prefix key is seen by all of it.
 // Per 128-row block: the key blocks [q_blocks.x, q_blocks.y) that any of its
 // rows sees, the query blocks [k_blocks.x, k_blocks.y) that see any of its keys.
-// Every array covers whole blocks; rows behind T are empty.
+// Every array covers whole blocks; rows behind T are empty.  So are padding's, as (x, x)
+// with x where the documents start (rows before them) or end.
 struct DocPlan {
     const int2* rows;
     const int2* cols;

@@ -465,8 +465,9 @@ def test_keys_of_no_weight_before_the_others(key, n_first, d, mode):
     x[60:60 + n_first, nh:nh + nkv, 3] = key
     slopes = slopes_of(nh) if mode == "bias" else None
     see = O.document_visible(t, offsets)
-    ra, rl = (torch.from_numpy(y).cuda() for y in O.document_attention(
-        qkv.double().cpu().numpy(), nh, nkv, d, see, cap, None if slopes is None else slopes.double().cpu().numpy()))
+    with np.errstate(invalid="ignore"):
+        ra, rl = (torch.from_numpy(y).cuda() for y in O.document_attention(
+            qkv.double().cpu().numpy(), nh, nkv, d, see, cap, None if slopes is None else slopes.double().cpu().numpy()))
     bad = qkv.clone()
     bad.view(t, nh + 2 * nkv, d)[20, nh + nkv:] = float("nan")  # the values of a key of the first document
     plan = make_plan(t, offsets)
@@ -481,3 +482,29 @@ def test_keys_of_no_weight_before_the_others(key, n_first, d, mode):
     rd = reference(qkv, nh, nkv, d, visible(t, offsets), cap, slopes, da)[2]
     dqkv = backward(bad, a, da, lse, t, nh, nkv, d, plan, cap, slopes)
     assert_near(dqkv[keep], rd[keep], "dqkv")
+
+
+@pytest.mark.parametrize("mode", ["plain", "bias", "cap"])
+@pytest.mark.parametrize("nh,nkv,d", [(4, 2, 64), (4, 1, 128), (3, 3, 64), (3, 1, 128)])
+def test_padding_gives_the_same_bits_whatever_it_holds(nh, nkv, d, mode):
+    """Rows before the first and behind the last document, inside tiles that documents share and in tiles of their own."""
+    t, offsets, prefix, cap = 900, [200, 330, 700], [20, 0], 5.0 if mode == "cap" else 0.0
+    qkv, da = draw(51, t, nh, nkv, d)
+    slopes = slopes_of(nh) if mode == "bias" else None
+    plan = make_plan(t, offsets, prefix)
+    pad = [slice(0, 200), slice(700, t)]
+    kept = None
+    # infinite scores, hidden as they are, would take a warp to the other form of the cap's tanh
+    for value in (0.0, float("nan")) + (() if cap else (float("inf"), -float("inf"), 3e38)):
+        x, dy = qkv.clone(), da.clone()
+        for rows in pad:
+            x[rows], dy[rows] = value, value
+        a, lse = forward(x, t, nh, nkv, d, plan, cap, slopes)
+        dqkv = backward(x, a, dy, lse, t, nh, nkv, d, plan, cap, slopes)
+        assert torch.isneginf(lse[:, 700:t]).all() and all(not y[rows].any() for y in (a, dqkv) for rows in pad)
+        if kept is None:
+            kept = a, lse, dqkv
+            ra, _, rd = reference(x, nh, nkv, d, visible(t, offsets, prefix), cap, slopes, dy)
+            assert_near(a, ra, "a")
+            assert_near(dqkv, rd, "dqkv")
+        assert torch.equal(a, kept[0]) and torch.equal(dqkv, kept[2]) and torch.equal(lse[:, :t], kept[1][:, :t])
