@@ -876,11 +876,11 @@ __global__ void __launch_bounds__(kDocFwdThreads, 1)
                     const bool more = j + 1 < nk;
                     const int k0 = (tile.z + nk - 1 - j) * kRows;
                     ok = false;
-                    if (has_padding(k0, live)) zero_padding<D>(s_kv + (2 * (g % NS) + 1) * kTile, k0, live, lane);  // V[g]
                     if (D == 64 && more) {
                         if (!kv_ready(g + 1)) break;
                         issue_s(0, g + 1);
                     }
+                    if (has_padding(k0, live)) zero_padding<D>(s_kv + (2 * (g % NS) + 1) * kTile, k0, live, lane);  // V[g]
                     if (!issue_pv(0, g, j == 0)) break;
                     if (D == 128 && more) {
                         if (!kv_ready(g + 1)) break;
