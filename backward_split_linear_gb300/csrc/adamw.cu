@@ -149,7 +149,8 @@ __device__ __forceinline__ void store8b(uint8_t* p, int64_t e, int64_t n, uint2 
     }
 }
 
-// The xorshift-multiply mixing of a 32-bit word.
+// A 32-bit hash of xorshifts and multiplications: constants and shifts are the ones that C. Wellons published in 2018
+// as the result of a search for the least bias.
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x = (x ^ (x >> 16)) * 0x7FEB352Du;
     x = (x ^ (x >> 15)) * 0x846CA68Bu;
@@ -328,8 +329,8 @@ __device__ __forceinline__ void adamw_elements(const zb_adamw_tensor& t, const A
 
 // Bound by HBM with float32 moments: 218 M elements in 912 us, 7.2 TB/s.  With 8-bit ones the
 // codecs' instructions all but bind it (80 % of issue slots): five blocks an SM (48 registers) ran one 8B-shaped layer's step and its
-// read-back in 1058 us, four in 1105, six in 1112; blocks that loop over four chunks, to
-// share the setup, in 1225.
+// read-back in 1058 us, four in 1105, six in 1112 (at 48 registers a thread stores 24 bytes and loads 16 in
+// its stack frame, which that includes); blocks that loop over four chunks, to share the setup, in 1225.
 template <bool kState8, int N>
 __global__ void __launch_bounds__(kAdamThreads, kState8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamTable<N> tab, const __grid_constant__ AdamArgs a) {
     wait_for_previous();

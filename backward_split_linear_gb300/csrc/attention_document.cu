@@ -117,7 +117,7 @@ struct DocArgs {
     float cap, scale;
     float scale_log2;      // log2(e) / sqrt(d)
     float cap_log2;        // cap log2(e)
-    float cap_limit;       // the square of 3/4 cap sqrt(d)
+    float cap_limit;       // 3/4 cap sqrt(d): the polynomial's range
     float cap_poly[5];     // tanh(s / (cap sqrt(d))) / s as a polynomial in s^2
     float cap_exp;         // 2 log2(e) / (cap sqrt(d)): the exponent of e^(2 s / cap) per unit of q . k
     int tokens, n_heads, n_kv_heads, ld_stat, n_blocks;
@@ -665,11 +665,11 @@ struct DocFwdSmem {
 // for the exponential, 1400 until the next scores), and 4000 cycles lie between two
 // tiles (last product, normalising, stores, first scores).  32 heads of 128 on 8,
 // 4096 tokens: 9 documents in 40 us (2.2 M pairs in visible blocks, 900 TFLOP/s of
-// theirs), 2 with a cap in 94; 16 heads of 64, one document of 16384 with a bias in
-// 530 (1037 TFLOP/s of its visible pairs).  Slower, each against its time then (9
+// theirs), 2 with a cap in 95; 16 heads of 64, one document of 16384 with a bias in
+// 532 (1034 TFLOP/s of its visible pairs).  Slower, each against its time then (9
 // documents; bias): sixteen row warps of half the columns (45 -> 50 us; 805 -> 826),
 // a quarter of the exponentials as polynomials on the FMA pipe (45 -> 46; 645 -> 714:
-// the exponential unit is 36 % busy), scores loaded in four parts beside the work on
+// the exponential unit, now 44 % busy, does not bind), scores loaded in four parts beside the work on
 // them (45 -> 49; 604 -> 722), four more warps that store the results while the rows
 // go on (41 -> 43; 601 -> 630), at heads of 128 steps of 64 keys with two score
 // buffers a tile (40 -> 42; a bias over 8192 rows 198 -> 232).

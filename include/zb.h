@@ -577,7 +577,10 @@ zb_status zb_stage_forward(zb_stage_t st, int32_t mb, const void* x, int32_t tok
  * doc_offsets, prefix_len and n_docs as in zb_op_attention_document_plan (device
  * arrays that `stream` reads during this call's work; the plan made from them is
  * stashed for B).  On such a stage zb_stage_forward is the call with one
- * document of all rows. */
+ * document of all rows.  Rows outside the documents are padding to the attention
+ * alone: its a, and the gradient it hands on, are zeros there.  Every other step
+ * takes them as rows of the batch, and W sums over all of them, so their x has to
+ * be finite and their dy zero (or what it should add to the weights' gradients). */
 zb_status zb_stage_forward_documents(zb_stage_t st, int32_t mb, const void* x, int32_t tokens,
                                      const int32_t* doc_offsets, const int32_t* prefix_len,
                                      int32_t n_docs, void* y, void* stream);

@@ -155,6 +155,8 @@ M_TOP, V_TOP, BLOCK = F32(15 * 2 ** 14), F32(15 * 2 ** 30), 256
 
 
 def mix32(x):
+    """A 32-bit hash of xorshifts and multiplications, with the constants that C. Wellons published in 2018 as the result of
+    a search for the least bias."""
     x = np.asarray(x, dtype=np.uint64) & np.uint64(0xFFFFFFFF)
     x = ((x ^ (x >> np.uint64(16))) * np.uint64(0x7FEB352D)) & np.uint64(0xFFFFFFFF)
     x = ((x ^ (x >> np.uint64(15))) * np.uint64(0x846CA68B)) & np.uint64(0xFFFFFFFF)
