@@ -316,9 +316,9 @@ zb_status zb_op_attention_causal_backward(const void* qkv, const void* a, const 
  *    included).  Their a and dqkv are zeros and their lse is -infinity.  The
  *    same holds across documents: a value that is not finite in one document
  *    reaches no row of another, and a key's reaches no query that does not see
- *    it.  (Padding costs no time for what it holds.  The rows that share a
- *    128-row block with a document's value that is not finite are formed again
- *    pair by pair, some hundred times slower.)
+ *    it.  (Padding costs no time for what it holds.  A document with a value
+ *    that is not finite, or with rows in the same 128-row block as another's, has
+ *    rows formed again pair by pair, some hundred times slower.)
  *  - positions: int32 [tokens], receives each row's place in its document (0
  *    for padding), for the rotary positions; may be NULL.
  *  - plan: zb_op_attention_document_plan_bytes(tokens) bytes of device memory.
