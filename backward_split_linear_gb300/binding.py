@@ -72,6 +72,20 @@ class zb_adamw_config(ctypes.Structure):
                 ("state_bits", c_int32), ("stochastic", c_int32), ("seed", ctypes.c_uint32), ("reserved", c_int32)]
 
 
+class zb_checkpoint(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
+
+
+class zb_residual_norm(ctypes.Structure):
+    _fields_ = [("post_norm", c_int32), ("pre_norm", c_int32), ("gate_kind", c_int32), ("reserved", c_int32),
+                ("post_gamma", c_void_p), ("post_beta", c_void_p), ("pre_gamma", c_void_p), ("pre_beta", c_void_p),
+                ("gate", c_void_p), ("residual_scale", c_float), ("branch_scale", c_float), ("post_eps", c_float),
+                ("pre_eps", c_float)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "relu2": 5}
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+GATE_KINDS = {"none": 0, "channel": 1, "token": 2}
 ROTARY_PAIRS = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 KERNEL_CLASSES = ["gemm_forward", "gemm_backward_input", "gemm_backward_weight", "row_backward_input",
@@ -132,6 +146,27 @@ _SIGS = {
                              + [c_void_p]),
     "zb_op_rotary_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_float] + [c_int32] * 5
                               + [c_void_p]),
+    "zb_op_checkpoint_pack": (c_int32, [c_void_p, ctypes.POINTER(zb_checkpoint), c_int32, c_int32, c_void_p]),
+    "zb_op_checkpoint_unpack": (c_int32, [ctypes.POINTER(zb_checkpoint), c_void_p, c_int32, c_int32, c_void_p]),
+    "zb_op_linear_activation_forward": (c_int32, [c_void_p] * 6 + [ctypes.POINTER(zb_checkpoint)] * 2 + [c_int32] * 4
+                                        + [c_void_p]),
+    "zb_op_backward_input_activation_scratch_bytes": (c_size_t, [c_int32, c_int32]),
+    "zb_op_backward_input_activation": (c_int32, [c_void_p] * 3 + [ctypes.POINTER(zb_checkpoint), c_void_p, c_void_p]
+                                        + [c_int32] * 4 + [c_void_p, c_size_t, c_void_p]),
+    "zb_op_activation_backward": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(zb_checkpoint), c_void_p] + [c_int32] * 3
+                                  + [c_void_p]),
+    "zb_op_backward_bias_scratch_bytes": (c_size_t, [c_int32, c_int32]),
+    "zb_op_backward_bias": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t, c_void_p]),
+    "zb_op_backward_weight_checkpoint_scratch_bytes": (c_size_t, [c_int32, c_int32]),
+    "zb_op_backward_weight_checkpoint": (c_int32, [c_void_p, ctypes.POINTER(zb_checkpoint), c_void_p] + [c_int32] * 3
+                                         + [c_void_p, c_size_t, c_void_p]),
+    "zb_op_residual_norm_forward": (c_int32, [ctypes.POINTER(zb_residual_norm)] + [c_void_p] * 4
+                                    + [ctypes.POINTER(zb_checkpoint), c_void_p, c_int32, c_int32, c_void_p]),
+    "zb_op_residual_norm_backward_input": (c_int32, [ctypes.POINTER(zb_residual_norm)] + [c_void_p] * 9
+                                           + [c_int32, c_int32, c_void_p]),
+    "zb_op_residual_norm_backward_weight_scratch_bytes": (c_size_t, [c_int32, c_int32]),
+    "zb_op_residual_norm_backward_weight": (c_int32, [ctypes.POINTER(zb_residual_norm)] + [c_void_p] * 10
+                                            + [c_int32, c_int32, c_void_p, c_size_t, c_void_p]),
     "zb_op_adamw_step": (c_int32, [ctypes.POINTER(zb_adamw_tensor), c_int32, ctypes.POINTER(zb_adamw_config), c_int64,
                                    c_void_p, c_void_p, c_void_p, c_void_p]),
     "zb_op_adamw_unpack": (c_int32, [ctypes.POINTER(zb_adamw_tensor), c_int32, ctypes.POINTER(c_void_p),
@@ -441,6 +476,113 @@ def zb_op_rotary_backward(dy, dx, positions, turns, magnitude, tokens, n_heads, 
     _check(lib().zb_op_rotary_backward(_ptr(dy), dense if ld_x is None else ld_x, _ptr(dx), dense if ld_y is None else ld_y,
                                        _ptr(positions), _ptr(turns), magnitude, tokens, n_heads, head_dim, rotary_dim,
                                        ROTARY_PAIRS[pairs], _stream(stream)), "zb_op_rotary_backward")
+
+
+# ---------------------------------------------------------------- biased linears, 8-bit checkpoints
+
+
+def _packed(p):
+    """A checkpoint given as (codes, scales), or None."""
+    if p is None:
+        return None
+    return ctypes.byref(zb_checkpoint(_ptr(p[0]), _ptr(p[1])))
+
+
+def _size(scratch, scratch_bytes):
+    """Bytes of a scratch tensor whose size is not given."""
+    if scratch_bytes is not None:
+        return scratch_bytes
+    return 0 if scratch is None else scratch.numel() * scratch.element_size()
+
+
+def zb_op_checkpoint_pack(x, packed, tokens, width, stream=None):
+    """`packed`: the tuple (codes [tokens, width], scales [tokens, width / 32]) of uint8 tensors, here and below."""
+    _check(lib().zb_op_checkpoint_pack(_ptr(x), _packed(packed), tokens, width, _stream(stream)), "zb_op_checkpoint_pack")
+
+
+def zb_op_checkpoint_unpack(packed, x, tokens, width, stream=None):
+    _check(lib().zb_op_checkpoint_unpack(_packed(packed), _ptr(x), tokens, width, _stream(stream)), "zb_op_checkpoint_unpack")
+
+
+def zb_op_linear_activation_forward(x, w, bias, residual, y, tokens, in_features, out_features, activation="none", z=None,
+                                    z_packed=None, y_packed=None, stream=None):
+    _check(lib().zb_op_linear_activation_forward(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z),
+                                                 _packed(z_packed), _packed(y_packed), tokens, in_features, out_features,
+                                                 ACTIVATIONS[activation], _stream(stream)), "zb_op_linear_activation_forward")
+
+
+def zb_op_backward_input_activation_scratch_bytes(tokens, in_features):
+    return lib().zb_op_backward_input_activation_scratch_bytes(tokens, in_features)
+
+
+def zb_op_backward_input_activation(dy, w, z, dz, tokens, in_features, out_features, activation, z_packed=None, dbias=None,
+                                    scratch=None, scratch_bytes=None, stream=None):
+    """scratch is read with dbias only; its size defaults to the tensor's."""
+    _check(lib().zb_op_backward_input_activation(_ptr(dy), _ptr(w), _ptr(z), _packed(z_packed), _ptr(dz), _ptr(dbias), tokens,
+                                                 in_features, out_features, ACTIVATIONS[activation], _ptr(scratch),
+                                                 _size(scratch, scratch_bytes), _stream(stream)),
+           "zb_op_backward_input_activation")
+
+
+def zb_op_activation_backward(dy, z, dz, tokens, width, activation, z_packed=None, stream=None):
+    _check(lib().zb_op_activation_backward(_ptr(dy), _ptr(z), _packed(z_packed), _ptr(dz), tokens, width,
+                                           ACTIVATIONS[activation], _stream(stream)), "zb_op_activation_backward")
+
+
+def zb_op_backward_bias_scratch_bytes(tokens, out_features):
+    return lib().zb_op_backward_bias_scratch_bytes(tokens, out_features)
+
+
+def zb_op_backward_bias(dy, dbias, tokens, out_features, scratch, scratch_bytes=None, stream=None):
+    _check(lib().zb_op_backward_bias(_ptr(dy), _ptr(dbias), tokens, out_features, _ptr(scratch), _size(scratch, scratch_bytes),
+                                     _stream(stream)), "zb_op_backward_bias")
+
+
+def zb_op_backward_weight_checkpoint_scratch_bytes(tokens, in_features):
+    return lib().zb_op_backward_weight_checkpoint_scratch_bytes(tokens, in_features)
+
+
+def zb_op_backward_weight_checkpoint(dy, x_packed, dw, tokens, in_features, out_features, scratch, scratch_bytes=None,
+                                     stream=None):
+    _check(lib().zb_op_backward_weight_checkpoint(_ptr(dy), _packed(x_packed), _ptr(dw), tokens, in_features, out_features,
+                                                  _ptr(scratch), _size(scratch, scratch_bytes), _stream(stream)),
+           "zb_op_backward_weight_checkpoint")
+
+
+# ---------------------------------------------------------------- norms around a block
+
+
+def make_residual_norm(post="none", pre="none", gate_kind="none", gate=None, post_gamma=None, post_beta=None, pre_gamma=None,
+                       pre_beta=None, residual_scale=1.0, branch_scale=1.0, post_eps=1e-5, pre_eps=1e-5):
+    """The options and parameters of the residual_norm calls.  It keeps the tensors alive."""
+    op = zb_residual_norm(NORM_KINDS[post], NORM_KINDS[pre], GATE_KINDS[gate_kind], 0, _ptr(post_gamma), _ptr(post_beta),
+                          _ptr(pre_gamma), _ptr(pre_beta), _ptr(gate), residual_scale, branch_scale, post_eps, pre_eps)
+    op.tensors = (post_gamma, post_beta, pre_gamma, pre_beta, gate)
+    return op
+
+
+def zb_op_residual_norm_forward(op, x, y, h, n, stats, tokens, hidden, n_packed=None, stream=None):
+    _check(lib().zb_op_residual_norm_forward(ctypes.byref(op), _ptr(x), _ptr(y), _ptr(h), _ptr(n), _packed(n_packed),
+                                             _ptr(stats), tokens, hidden, _stream(stream)), "zb_op_residual_norm_forward")
+
+
+def zb_op_residual_norm_backward_input(op, dn, dres, h, y, stats, dh, dy, tokens, hidden, dx=None, dgate=None, stream=None):
+    _check(lib().zb_op_residual_norm_backward_input(ctypes.byref(op), _ptr(dn), _ptr(dres), _ptr(h), _ptr(y), _ptr(stats),
+                                                    _ptr(dh), _ptr(dx), _ptr(dy), _ptr(dgate), tokens, hidden,
+                                                    _stream(stream)), "zb_op_residual_norm_backward_input")
+
+
+def zb_op_residual_norm_backward_weight_scratch_bytes(tokens, hidden):
+    return lib().zb_op_residual_norm_backward_weight_scratch_bytes(tokens, hidden)
+
+
+def zb_op_residual_norm_backward_weight(op, dn, h, dh, y, stats, tokens, hidden, scratch, scratch_bytes=None,
+                                        dpost_gamma=None, dpost_beta=None, dpre_gamma=None, dpre_beta=None, dgate=None,
+                                        stream=None):
+    _check(lib().zb_op_residual_norm_backward_weight(ctypes.byref(op), _ptr(dn), _ptr(h), _ptr(dh), _ptr(y), _ptr(stats),
+                                                     _ptr(dpost_gamma), _ptr(dpost_beta), _ptr(dpre_gamma), _ptr(dpre_beta),
+                                                     _ptr(dgate), tokens, hidden, _ptr(scratch), _size(scratch, scratch_bytes),
+                                                     _stream(stream)), "zb_op_residual_norm_backward_weight")
 
 
 # ---------------------------------------------------------------- AdamW

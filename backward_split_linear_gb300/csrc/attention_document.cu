@@ -549,17 +549,6 @@ __device__ __forceinline__ void load_tmem32(uint32_t t, float (&v)[32]) {
 
 // ------------------------------------------------------------------------ forward
 
-// Every warp of a warpgroup takes part.  A claim waits until the releases of the
-// other warpgroups of the block have made room.
-template <int N>
-__device__ __forceinline__ void registers_release() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void registers_claim() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Cancels the launch of the next CTA of the grid that has not started and
 // writes its place to `slot` (16 bytes), completing on `bar`: the CTA takes that
 // one's work.  Tiles go to whichever CTA is free, with no counter in memory that

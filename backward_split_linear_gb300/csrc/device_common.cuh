@@ -240,6 +240,19 @@ static __device__ __noinline__ bool wait_value(const uint32_t* p, uint32_t v, in
     }
 }
 
+// ---------------------------------------------------------------- registers
+
+// Every warp of a warpgroup takes part.  A claim waits until the releases of the
+// other warpgroups of the block have made room.
+template <int N>
+__device__ __forceinline__ void registers_release() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_claim() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

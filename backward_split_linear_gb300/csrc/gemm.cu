@@ -33,6 +33,7 @@
 #include <vector>
 
 #include "device_common.cuh"
+#include "gemm_common.h"
 #include "launch.h"
 
 namespace zbk {
@@ -1490,6 +1491,19 @@ cudaError_t prepare(const GemmArgs& g, bool allow_split, CUtensorMap& ma, CUtens
 }
 
 }  // namespace
+
+bool gemm_encode_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld, uint32_t box_cols,
+                     uint32_t box_rows, CUtensorMapSwizzle swizzle, CUtensorMapDataType dtype) {
+    return encode_map(map, ptr, rows, cols, ld, box_cols, box_rows, swizzle, dtype);
+}
+
+int gemm_raster(int tiles_m, int tiles_n, int bm, int bn, int k, int grid, bool* group_m) {
+    const Raster r = choose_raster(tiles_m, tiles_n, bm, bn, k, grid);
+    *group_m = r.group_m;
+    return r.group;
+}
+
+int gemm_pairs() { return pair_max_clusters(); }
 
 bool gemm_takes_pair(int m, int n) { return m >= kPairM && n >= kPairN; }
 

@@ -1,0 +1,981 @@
+// Linear layers with a bias, an activation and a residual, forward and split backward:
+//   F   z = x w^T + bias, y = act(z) + residual, and z and y as checkpoints (bf16 or 8 bits)
+//   B   dz = (dy w) act'(z), and the bias gradient sum_t dz of the layer that made z
+//   W   dw += dy^T x from an 8-bit checkpoint of x
+//
+// One kernel for all three: a CTA pair computes 256 x 256 tiles with tcgen05.mma
+// (cta_group::2, bf16 in, float32 in tensor memory), operands by TMA through a ring of six
+// 64-deep stages, two accumulators, one persistent pair per two SMs.  Warp 0 loads, warp 1
+// issues the MMAs (2 and 3 only fill their warpgroup), warps 4-11 are the epilogue: warp w
+// reads the 32 tensor-memory lanes 32 (w % 4) ... and one half of the columns.  Eight epilogue warps rather than the four of
+// the plain GEMM because an epilogue here costs up to a hundred instructions an element
+// (erfc, two 8-bit blocks), which has to stay below the tile's MMAs.
+//
+// Sums.  The tensor core drops what falls below its accumulator's last bit, always towards
+// zero: over 4096 terms a sum of products comes out 4e-6 short, over 16384 1.9e-5 (measured
+// against float64), where float32 sums that round to nearest stay below 1e-6.  bf16 results do not
+// show that, float32 gradients do.  So where results are float32 sums (W, and B with a bias gradient) an
+// accumulator only holds 512 terms: the epilogue warps then add it to sums in their
+// registers, while the MMAs fill the other accumulator.
+#include <algorithm>
+#include <mutex>
+
+#include "checkpoint.cuh"
+#include "checks.h"
+#include "device_common.cuh"
+#include "gemm_common.h"
+#include "operators.h"
+
+namespace zbk {
+
+namespace {
+
+constexpr int kLinThreads = 384;
+constexpr int kLinEpiWarps = 8;
+constexpr int kLinStages = 6;
+constexpr int kLinTile = 256;  // rows and columns of a pair's tile
+constexpr int kLinHalf = 128;  // rows (A) and columns (B) that each CTA loads
+constexpr int kLinBK = 64;
+constexpr uint32_t kLinOperand = kLinHalf * kLinBK * 2;  // 16 KiB
+constexpr uint32_t kLinMnBlock = 64 * kLinBK * 2;        // a 64-wide block of an MN-major tile
+constexpr uint32_t kLinBox = 4096;                       // staging per epilogue warp
+constexpr uint32_t kLinTmemCols = 512;
+constexpr int kLinBars = 2 * kLinStages + 5;
+constexpr size_t kLinSmem = 1024 + kLinStages * 2 * kLinOperand + kLinEpiWarps * kLinBox + kLinBars * 8 + 16;
+static_assert(kLinSmem <= 232448, "shared memory");
+// Registers a thread: 384 x 168 at launch, of which 128 x 64 + 256 x 216 are used.
+constexpr int kLinFewRegs = 64, kLinManyRegs = 216;
+constexpr int kLinSumBlocks = 8;  // k blocks (512 terms) that stay in tensor memory
+
+enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
+
+struct LinParams {
+    int m, n, k_blocks;
+    int tiles_m, tiles_n, group, group_m;
+    // tiles from narrow_from on (a short last wave) are two units of 128 columns each
+    int narrow_from, num_units;
+    int act;
+    const float* bias;         // F: [n] or NULL
+    const uint16_t* residual;  // F: [m, n] or NULL
+    uint16_t* z;               // F: written, B: read; [m, n] or NULL
+    uint8_t* z_codes;          // the same in 8 bits: [m, n] and [m, n / 32]
+    uint8_t* z_scales;
+    uint8_t* y_codes;          // F: y in 8 bits
+    uint8_t* y_scales;
+    float* col_sums;           // B: [ceil(m / 32)][n] sums of dz over 32 rows each, or NULL
+    int* status;
+};
+
+struct LinUnit {
+    int tile, half;
+    bool narrow;
+};
+
+__device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
+    LinUnit w{u, 0, false};
+    if (u >= p.narrow_from) {
+        const int v = u - p.narrow_from;
+        w.tile = p.narrow_from + (v >> 1);
+        w.half = v & 1;
+        w.narrow = true;
+    }
+    return w;
+}
+
+__device__ __forceinline__ void lin_tile(const LinParams& p, int tile, int& tm, int& tn) {
+    const int across = p.group_m ? p.tiles_n : p.tiles_m, along = p.group_m ? p.tiles_m : p.tiles_n;
+    const int g = tile / (p.group * across), in = tile - g * p.group * across;
+    const int size = min(p.group, along - g * p.group);
+    const int a = g * p.group + in % size, b = in / size;
+    tm = p.group_m ? a : b;
+    tn = p.group_m ? b : a;
+}
+
+// ---------------------------------------------------------------- activations
+//
+// gelu through erfc and gelu_tanh through the logistic function (0.5 (1 + tanh u) =
+// 1 / (1 + exp(-2 u))): neither cancels where the activation is small.  A NaN stays one.
+
+__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+constexpr float kTanhA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kTanhB = 0.044715f;
+
+template <int kAct>
+__device__ __forceinline__ float act_value(float z) {
+    if (kAct == ZB_ACT_RELU) return z < 0.f ? 0.f : z;
+    if (kAct == ZB_ACT_RELU2) return z < 0.f ? 0.f : z * z;
+    if (kAct == ZB_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    if (kAct == ZB_ACT_GELU_TANH) return z * logistic(kTanhA * (z + kTanhB * z * z * z));
+    if (kAct == ZB_ACT_SILU) return z * logistic(z);
+    return z;
+}
+
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+    if (kAct == ZB_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+    if (kAct == ZB_ACT_RELU2) return z <= 0.f ? 0.f : 2.f * z;
+    // behind +-30 the slopes below are 0 or 1 to the last bit; their terms would pass the range
+    const float c = z > 30.f ? 30.f : (z < -30.f ? -30.f : z);
+    if (kAct == ZB_ACT_GELU) return 0.5f * erfcf(c * -0.70710678118654752f) + 0.3989422804014327f * c * __expf(-0.5f * c * c);
+    if (kAct == ZB_ACT_GELU_TANH) {
+        const float s = logistic(kTanhA * (c + kTanhB * c * c * c));
+        return s + c * s * (1.f - s) * kTanhA * (1.f + 3.f * kTanhB * c * c);
+    }
+    if (kAct == ZB_ACT_SILU) {
+        const float s = logistic(c);
+        return s * (1.f + c * (1.f - s));
+    }
+    return 1.f;
+}
+
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f(i);
+}
+
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+    switch (act) {
+        case ZB_ACT_RELU: each<N>([&](int i) { v[i] = act_value<ZB_ACT_RELU>(v[i]); }); break;
+        case ZB_ACT_GELU: each<N>([&](int i) { v[i] = act_value<ZB_ACT_GELU>(v[i]); }); break;
+        case ZB_ACT_GELU_TANH: each<N>([&](int i) { v[i] = act_value<ZB_ACT_GELU_TANH>(v[i]); }); break;
+        case ZB_ACT_SILU: each<N>([&](int i) { v[i] = act_value<ZB_ACT_SILU>(v[i]); }); break;
+        case ZB_ACT_RELU2: each<N>([&](int i) { v[i] = act_value<ZB_ACT_RELU2>(v[i]); }); break;
+        default: break;
+    }
+}
+
+// d[i] *= act'(z[i])
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, float (&d)[N], const float (&z)[N]) {
+    switch (act) {
+        case ZB_ACT_RELU: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_RELU>(z[i]); }); break;
+        case ZB_ACT_GELU: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_GELU>(z[i]); }); break;
+        case ZB_ACT_GELU_TANH: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_GELU_TANH>(z[i]); }); break;
+        case ZB_ACT_SILU: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_SILU>(z[i]); }); break;
+        case ZB_ACT_RELU2: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_RELU2>(z[i]); }); break;
+        default: break;
+    }
+}
+
+// ---------------------------------------------------------------- epilogue of 32 columns of a row
+
+__device__ __forceinline__ void to_words(const float (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+}
+
+// A box of 32 rows x 32 bf16 columns, 64 bytes a row, in the 64-byte TMA swizzle (16-byte
+// word j of row r at word j ^ ((r >> 1) & 3)).
+__device__ __forceinline__ void words_to_box(uint32_t box, int lane, const uint32_t (&w)[16]) {
+    const uint32_t row = box + static_cast<uint32_t>(lane) * 64u, sw = (static_cast<uint32_t>(lane) >> 1) & 3u;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+        st_shared_v4(row + ((j ^ sw) << 4), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+}
+
+// Scale bytes of consecutive 32-column blocks leave two at a time: a row of n / 32 bytes
+// keeps no more than 2-byte alignment (n is a multiple of 64, so blocks come in pairs).
+struct ScalePair {
+    uint32_t first;
+    __device__ __forceinline__ void put(uint8_t* scales, int64_t at, int c, uint32_t scale, bool ok) {
+        if ((c & 1) == 0)
+            first = scale;
+        else if (ok)
+            *reinterpret_cast<uint16_t*>(scales + at - 1) = static_cast<uint16_t>(first | (scale << 8));
+    }
+};
+
+struct LinRow {
+    ScalePair z, y;
+};
+
+// F.  `v` is the product on entry.  Writes z and the 8-bit checkpoints and leaves y's words in `yw`.
+__device__ __forceinline__ void forward_chunk(const LinParams& p, LinRow& row, float (&v)[32], int m, int n, int c, bool ok,
+                                              uint32_t (&yw)[16]) {
+    const int64_t at = static_cast<int64_t>(m) * p.n + n;
+    uint4 res[4];
+    if (p.residual && ok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) res[j] = reinterpret_cast<const uint4*>(p.residual + at)[j];
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + n) + j);
+            v[4 * j] += b.x;
+            v[4 * j + 1] += b.y;
+            v[4 * j + 2] += b.z;
+            v[4 * j + 3] += b.w;
+        }
+    }
+    if (p.z || p.z_codes) {
+        uint32_t zw[16];
+        to_words(v, zw);
+        if (p.z) {
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<uint4*>(p.z + at)[j] = make_uint4(zw[4 * j], zw[4 * j + 1], zw[4 * j + 2], zw[4 * j + 3]);
+            }
+        }
+        if (p.z_codes) {
+            uint4 lo, hi;
+            const uint32_t scale = pack_block(zw, lo, hi);
+            if (ok) {
+                reinterpret_cast<uint4*>(p.z_codes + at)[0] = lo;
+                reinterpret_cast<uint4*>(p.z_codes + at)[1] = hi;
+            }
+            row.z.put(p.z_scales, at >> 5, c, scale, ok);
+        }
+    }
+    act_values(p.act, v);
+    if (p.residual && ok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t rw[4] = {res[j].x, res[j].y, res[j].z, res[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[8 * j + 2 * e] += bf16_lo(rw[e]);
+                v[8 * j + 2 * e + 1] += bf16_hi(rw[e]);
+            }
+        }
+    }
+    to_words(v, yw);
+    if (p.y_codes) {
+        uint4 lo, hi;
+        const uint32_t scale = pack_block(yw, lo, hi);
+        if (ok) {
+            reinterpret_cast<uint4*>(p.y_codes + at)[0] = lo;
+            reinterpret_cast<uint4*>(p.y_codes + at)[1] = hi;
+        }
+        row.y.put(p.y_scales, at >> 5, c, scale, ok);
+    }
+}
+
+// The words that hold 32 values of z: 16 (bf16), or 8 and a scale.
+struct ZWords {
+    uint4 w[4];
+    uint32_t scale;
+};
+
+__device__ __forceinline__ void load_z(const LinParams& p, int64_t at, bool ok, ZWords& z) {
+    if (!ok || p.act == ZB_ACT_NONE) return;
+    if (p.z_codes) {
+        z.w[0] = reinterpret_cast<const uint4*>(p.z_codes + at)[0];
+        z.w[1] = reinterpret_cast<const uint4*>(p.z_codes + at)[1];
+        z.scale = p.z_scales[at >> 5];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z.w[j] = reinterpret_cast<const uint4*>(p.z + at)[j];
+    }
+}
+
+__device__ __forceinline__ void z_values(const LinParams& p, const ZWords& z, float (&v)[32]) {
+    if (p.z_codes) {
+        const float unit = unpack_unit(z.scale);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {z.w[j].x, z.w[j].y, z.w[j].z, z.w[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float q[4];
+                unpack_codes(w[e], unit, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[16 * j + 4 * e + i] = q[i];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w[4] = {z.w[j].x, z.w[j].y, z.w[j].z, z.w[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[8 * j + 2 * e] = bf16_lo(w[e]);
+                v[8 * j + 2 * e + 1] = bf16_hi(w[e]);
+            }
+        }
+    }
+}
+
+// Sums over the warp's 32 lanes (rows) of 32 columns; lane l gets column l's.  Five rounds
+// of a transposing reduction (31 shuffles), in a fixed order.
+__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float keep = upper ? v[i + off] : v[i];
+            const float send = upper ? v[i] : v[i + off];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+    return v[0];
+}
+
+// B.  `v` is the product on entry; leaves dz's words in `dw` and adds its columns up.
+__device__ __forceinline__ void backward_chunk(const LinParams& p, float (&v)[32], const ZWords& zw, int m, int n, int row0,
+                                               int lane, bool ok, uint32_t (&dw)[16]) {
+    if (p.act != ZB_ACT_NONE) {
+        float z[32];
+        z_values(p, zw, z);
+        act_slopes(p.act, v, z);
+    }
+    to_words(v, dw);
+    if (p.col_sums) {
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        const float s = column_sums(v, lane);
+        p.col_sums[static_cast<int64_t>(row0 >> 5) * p.n + n + lane] = s;
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+
+// kSums: the accumulators are added up in registers every kLinSumBlocks k blocks.
+template <bool A_MN, bool B_MN, int EPI, bool kSums>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t s_a = base, s_b = base + kLinStages * kLinOperand;
+    const uint32_t s_out = s_b + kLinStages * kLinOperand;
+    const uint32_t bars = s_out + kLinEpiWarps * kLinBox;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (kLinStages + s); };
+    auto tfull_bar = [&](int a) { return bars + 8u * (2 * kLinStages + a); };
+    auto tempty_bar = [&](int a) { return bars + 8u * (2 * kLinStages + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (2 * kLinStages + 4);
+    const uint32_t tmem_slot = bars + 8u * kLinBars;
+    volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - raw));
+
+    int* const status = p.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int chunk_blocks = kSums ? kLinSumBlocks : p.k_blocks;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kLinStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 2 * kLinEpiWarps);  // one lane of each epilogue warp of the pair
+        }
+        mbar_init(drain_bar, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        tma_prefetch_map(&map_out);
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, kLinTmemCols);
+    tc_fence_before();
+    cluster_sync_all();  // barriers of both CTAs initialised, tensor memory allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint32_t peer_base = ld_shared_cluster_u32(map_to_cta(tmem_slot, rank ^ 1u));
+    const bool usable = peer_base == tmem_base;  // both CTAs must hold the accumulators at the same columns
+    if (!usable && threadIdx.x == 0) atomicCAS(status, 0, kSitePairTmem);
+
+    if (warp < 4) {
+        registers_release<kLinFewRegs>();
+        if (usable && warp == 0) {
+            if (lane == 0) {
+                // ---------------- TMA producer (both CTAs)
+                uint32_t n_fills = 0;
+                int stage = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int u = pair; ok && u < p.num_units; u += npairs) {
+                    const LinUnit w = lin_unit(p, u);
+                    int tm, tn;
+                    lin_tile(p, w.tile, tm, tn);
+                    const int m0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf;
+                    // a narrow unit's 128 columns split 64 / 64 between the CTAs; the boxes stay
+                    // whole, and what they hold past those columns is not read
+                    const int n0 = tn * kLinTile + (w.narrow ? w.half * kLinHalf + static_cast<int>(rank) * (kLinHalf / 2)
+                                                             : static_cast<int>(rank) * kLinHalf);
+                    for (int kb = 0; kb < p.k_blocks; ++kb) {
+                        if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb_local = full_bar(stage);
+                        if (leader) mbar_arrive_expect_tx(fb_local, 4 * kLinOperand);
+                        const uint32_t fb = map_to_cta(fb_local, 0);
+                        const int k0 = kb * kLinBK;
+                        const uint32_t a_dst = s_a + stage * kLinOperand, b_dst = s_b + stage * kLinOperand;
+                        if constexpr (A_MN) {
+                            tma_load_2d_pair(a_dst, &map_a, fb, m0, k0);
+                            tma_load_2d_pair(a_dst + kLinMnBlock, &map_a, fb, m0 + 64, k0);
+                        } else {
+                            tma_load_2d_pair(a_dst, &map_a, fb, k0, m0);
+                        }
+                        if constexpr (B_MN) {
+                            tma_load_2d_pair(b_dst, &map_b, fb, n0, k0);
+                            tma_load_2d_pair(b_dst + kLinMnBlock, &map_b, fb, n0 + 64, k0);
+                        } else {
+                            tma_load_2d_pair(b_dst, &map_b, fb, k0, n0);
+                        }
+                        ++n_fills;
+                        if (++stage == kLinStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                // Loads must land before shared memory goes away: rank 0 sees its full
+                // barriers complete; rank 1 sees the MMA release each stage.
+                for (int s = 0; s < kLinStages; ++s) {
+                    const uint32_t uses = ring_uses(n_fills, kLinStages, s);
+                    if (uses > 0) {
+                        if (leader)
+                            mbar_wait_cluster(full_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
+                        else
+                            mbar_wait_cluster(empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
+                    }
+                }
+            }
+        } else if (usable && warp == 1) {
+            if (leader) {
+                // ---------------- MMA issuer (rank 0): a converged warp, its elected lane carries each instruction
+                const uint32_t issuer = elect_one_sync();
+                constexpr uint32_t idesc_wide = mma_idesc_bf16(kLinTile, kLinTile, A_MN, B_MN);
+                constexpr uint32_t idesc_narrow = mma_idesc_bf16(kLinTile, kLinHalf, A_MN, B_MN);
+                int stage = 0;
+                uint32_t phase = 0;
+                uint32_t it = 0;
+                bool ok = true;
+                for (int u = pair; ok && u < p.num_units; u += npairs) {
+                    const uint32_t idesc = lin_unit(p, u).narrow ? idesc_narrow : idesc_wide;
+                    for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_blocks, ++it) {
+                        const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
+                        if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem_base + acc * kLinTile;
+                        const int kb1 = min(kc + chunk_blocks, p.k_blocks);
+                        for (int kb = kc; kb < kb1; ++kb) {
+                            if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t a0 = s_a + stage * kLinOperand, b0 = s_b + stage * kLinOperand;
+#pragma unroll
+                            for (int k = 0; k < kLinBK / 16; ++k) {
+                                const uint64_t ad = A_MN ? smem_desc_sw128(a0 + k * 2048, kLinMnBlock, 1024)
+                                                         : smem_desc_sw128(a0 + k * 32, 16, 1024);
+                                const uint64_t bd = B_MN ? smem_desc_sw128(b0 + k * 2048, kLinMnBlock, 1024)
+                                                         : smem_desc_sw128(b0 + k * 32, 16, 1024);
+                                umma_bf16_pair_elected(issuer, d, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
+                            }
+                            umma_commit_pair_elected(issuer, empty_bar(stage), 0x3);
+                            if (++stage == kLinStages) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                        if (ok) umma_commit_pair_elected(issuer, tfull_bar(acc), 0x3);
+                    }
+                }
+                umma_commit_pair_elected(issuer, drain_bar, 0x1);
+                mbar_wait(drain_bar, 0, status, kSiteDrain, kWaitLimitNs);
+            }
+        }
+    } else {
+        registers_claim<kLinManyRegs>();
+        if (usable) {
+            // ---------------- epilogue (both CTAs)
+            const int q = warp & 3, half = (warp - 4) >> 2;
+            const uint32_t box0 = s_out + static_cast<uint32_t>(warp - 4) * kLinBox;
+            const uint32_t tlane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+            uint32_t n_stored = 0, it = 0;
+            bool alive = true;
+            auto acquire = [&]() {  // one verdict per warp: the tensor-memory loads are warp-wide
+                alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(it & 1u), (it >> 1) & 1u, status, kSiteEpiTmemFull));
+                tc_fence_after();
+                return alive;
+            };
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = tempty_bar(it & 1u);
+                    if (leader)
+                        mbar_arrive(bar);
+                    else
+                        mbar_arrive_cluster(map_to_cta(bar, 0));
+                }
+                ++it;
+            };
+            for (int u = pair; alive && u < p.num_units; u += npairs) {
+                const LinUnit w = lin_unit(p, u);
+                int tm, tn;
+                lin_tile(p, w.tile, tm, tn);
+                const int row0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf + q * 32;  // first of this warp's rows
+                const int m = row0 + lane;
+                const bool row_ok = m < p.m;
+                // this warp's columns: half of the unit's, 32 at a time
+                const int cols = w.narrow ? kLinHalf / 2 : kLinHalf;
+                const int col0 = half * cols;
+                const int n_base = tn * kLinTile + (w.narrow ? w.half * kLinHalf : 0) + col0;
+                LinRow row;
+                // What remains of a chunk once its product `v` is in registers.
+                auto finish = [&](float (&v)[32], const ZWords& zw, int c) {
+                    const int n = n_base + 32 * c;
+                    const bool ok = row_ok && n < p.n;
+                    if (row0 >= p.m || n >= p.n) return;  // warp-uniform: nothing of the box is inside
+                    uint32_t box = box0;
+                    if constexpr (EPI == kLinAccumulate) {
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+                        const uint32_t at = box + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; ++j)
+                            st_shared_v4(at + ((j ^ (static_cast<uint32_t>(lane) & 7u)) << 4),
+                                         make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                    __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+                    } else {
+                        uint32_t out[16];
+                        if constexpr (EPI == kLinForward)
+                            forward_chunk(p, row, v, m, n, c, ok, out);
+                        else
+                            backward_chunk(p, v, zw, m, n, row0, lane, ok, out);
+                        // two boxes in turn: one is rewritten after the store before last has read it
+                        box += (n_stored & 1u) * (kLinBox / 2);
+                        if (lane == 0) bulk_wait_group_read<1>();
+                        __syncwarp();
+                        words_to_box(box, lane, out);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {  // rows past M and columns past N are dropped
+                        if constexpr (EPI == kLinAccumulate)
+                            tma_reduce_add_2d(&map_out, box, n, row0);
+                        else
+                            tma_store_2d(&map_out, box, n, row0);
+                        bulk_commit_group();
+                    }
+                    ++n_stored;
+                };
+                auto z_of = [&](int c) {
+                    ZWords zw{};
+                    if constexpr (EPI == kLinActivationBackward) {
+                        const int n = n_base + 32 * c;
+                        load_z(p, static_cast<int64_t>(m) * p.n + n, row_ok && n < p.n, zw);
+                    }
+                    return zw;
+                };
+                if constexpr (kSums) {
+                    float sum[4][32];
+                    for (int kc = 0; alive && kc < p.k_blocks; kc += chunk_blocks) {
+                        if (!acquire()) break;
+                        const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (32 * c < cols) {
+                                uint32_t r[32];
+                                tmem_load_32(t0 + 32u * c, r);
+                                tmem_wait_load();
+                                if (kc == 0) {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) sum[c][i] = __uint_as_float(r[i]);
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
+                                }
+                            }
+                        }
+                        release();
+                    }
+                    if (!alive) break;
+                    if constexpr (EPI == kLinAccumulate) {
+                        const ZWords unused{};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (32 * c < cols) finish(sum[c], unused, c);
+                    } else {
+                        // one copy of the long code: the sums move down 32 columns at a time
+#pragma unroll 1
+                        for (int c = 0; 32 * c < cols; ++c) {
+                            const ZWords zw = z_of(c);
+                            finish(sum[0], zw, c);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                sum[0][i] = sum[1][i];
+                                sum[1][i] = sum[2][i];
+                                sum[2][i] = sum[3][i];
+                            }
+                        }
+                    }
+                } else {
+                    if (!acquire()) break;
+                    const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
+#pragma unroll 1
+                    for (int c = 0; 32 * c < cols; ++c) {
+                        const ZWords zw = z_of(c);
+                        uint32_t r[32];
+                        tmem_load_32(t0 + 32u * c, r);
+                        tmem_wait_load();
+                        if (32 * (c + 1) >= cols) release();
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                        finish(v, zw, c);
+                    }
+                }
+            }
+            // the boxes must stay until the last stores have read them, and all of it be written
+            if (lane == 0) bulk_wait_group_all();
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync_all();  // neither CTA leaves while the other may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kLinTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- bias gradient
+//
+// dbias[j] += sum over rows.  Two passes in a fixed order: sums over parts of the rows
+// ([parts][n] float32), then their sum.  B's epilogue writes the first (parts of 32 rows);
+// a bias without an activation behind it has column_parts_kernel.
+
+constexpr int kColThreads = 256;
+constexpr int kColGroups = 8;  // row groups of a block; a thread takes 8 columns
+constexpr int kColUnroll = 4;
+constexpr int kColTargetBlocks = 1216;  // 8 blocks of 256 threads on each of 152 SMs
+
+int column_parts(int tokens, int width) {
+    const int across = (width + 255) / 256;
+    return std::max(1, std::min((kColTargetBlocks + across - 1) / across, (tokens + kColGroups - 1) / kColGroups));
+}
+
+// Block (x, y): columns 256 x ..., the y-th part of the rows.  Bound by HBM.
+__global__ void __launch_bounds__(kColThreads) column_parts_kernel(const uint16_t* __restrict__ dy, float* __restrict__ parts,
+                                                                   int tokens, int width) {
+    __shared__ float sums[kColGroups][256];
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+    const int col = blockIdx.x * 256 + 8 * lane;
+    const int per = (tokens + gridDim.y - 1) / gridDim.y;
+    const int t0 = blockIdx.y * per, t1 = min(tokens, t0 + per);
+    float acc[8] = {};
+    if (col < width) {
+        for (int tb = t0 + group; tb < t1; tb += kColGroups * kColUnroll) {
+            uint4 v[kColUnroll];
+#pragma unroll
+            for (int i = 0; i < kColUnroll; ++i) {
+                const int t = tb + i * kColGroups;
+                v[i] = t < t1 ? *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(t) * width + col) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kColUnroll; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[2 * e] += bf16_lo(w[e]);
+                    acc[2 * e + 1] += bf16_hi(w[e]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[group][8 * lane + e] = acc[e];
+    __syncthreads();
+    const int j = blockIdx.x * 256 + threadIdx.x;
+    if (j < width) {
+        float s = 0.f;
+#pragma unroll
+        for (int g = 0; g < kColGroups; ++g) s += sums[g][threadIdx.x];
+        parts[static_cast<int64_t>(blockIdx.y) * width + j] = s;
+    }
+}
+
+// A block finishes 32 columns: thread (c, g) adds the parts g, g + 8, ... of column c.
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ parts, float* out, int n_parts, int width) {
+    __shared__ float sums[8][32];
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int j = blockIdx.x * 32 + c;
+    float s = 0.f;
+    for (int q0 = g; q0 < n_parts; q0 += 64) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = q0 + 8 * i < n_parts ? parts[static_cast<int64_t>(q0 + 8 * i) * width + j] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    sums[g][c] = s;
+    __syncthreads();
+    if (g == 0) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sums[k][c];
+        out[j] += t;
+    }
+}
+
+void launch_column_sum(const float* parts, float* out, int n_parts, int width, cudaStream_t stream) {
+    column_sum_kernel<<<width / 32, 256, 0, stream>>>(parts, out, n_parts, width);  // width is a multiple of 64
+}
+
+// ---------------------------------------------------------------- the activation alone
+
+// dz = dy act'(z), 8 elements a thread.  Bound by HBM.
+__global__ void __launch_bounds__(256) activation_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
+                                                                  const uint8_t* __restrict__ codes,
+                                                                  const uint8_t* __restrict__ scales, uint16_t* dz,
+                                                                  int64_t chunks, int act) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= chunks) return;
+    const uint4 dv = reinterpret_cast<const uint4*>(dy)[i];
+    const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
+    float d[8], x[8];
+    if (act == ZB_ACT_NONE) {
+        reinterpret_cast<uint4*>(dz)[i] = dv;
+        return;
+    }
+    if (codes) {
+        const uint2 c = reinterpret_cast<const uint2*>(codes)[i];
+        const float unit = unpack_unit(scales[i >> 2]);
+        float q[4];
+        unpack_codes(c.x, unit, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = q[e];
+        unpack_codes(c.y, unit, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 + e] = q[e];
+    } else {
+        const uint4 zv = reinterpret_cast<const uint4*>(z)[i];
+        const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = bf16_lo(zw[e]);
+            x[2 * e + 1] = bf16_hi(zw[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        d[2 * e] = bf16_lo(dw[e]);
+        d[2 * e + 1] = bf16_hi(dw[e]);
+    }
+    act_slopes(act, d, x);
+    reinterpret_cast<uint4*>(dz)[i] = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
+                                                 pack_bf16x2(d[6], d[7]));
+}
+
+// ---------------------------------------------------------------- launches
+
+template <bool A_MN, bool B_MN, int EPI, bool kSums>
+cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p, int k, cudaStream_t stream) {
+    constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap ma, mb, mo;
+    bool ok = A_MN ? gemm_encode_map(&ma, a, k, p.m, p.m, 64, kLinBK, k128, kBf16)
+                   : gemm_encode_map(&ma, a, p.m, k, k, 64, kLinHalf, k128, kBf16);
+    ok = ok && (B_MN ? gemm_encode_map(&mb, b, k, p.n, p.n, 64, kLinBK, k128, kBf16)
+                     : gemm_encode_map(&mb, b, p.n, k, k, 64, kLinHalf, k128, kBf16));
+    ok = ok && (EPI == kLinAccumulate
+                    ? gemm_encode_map(&mo, out, p.m, p.n, p.n, 32, 32, k128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32)
+                    : gemm_encode_map(&mo, out, p.m, p.n, p.n, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, kBf16));
+    if (!ok) return cudaErrorInvalidValue;
+    p.status = status_word();
+    if (!p.status) return cudaErrorInvalidDevice;
+
+    auto kern = linear_kernel<A_MN, B_MN, EPI, kSums>;
+    static std::mutex mu;
+    static int pairs_of[64] = {};
+    int dev = 0, pairs = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!pairs_of[dev]) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLinSmem));
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(sm_count()));
+            cfg.blockDim = dim3(kLinThreads);
+            cfg.dynamicSmemBytes = kLinSmem;
+            e = cudaOccupancyMaxActiveClusters(&pairs_of[dev], kern, &cfg);
+            if (e != cudaSuccess) return e;
+            if (pairs_of[dev] < 1) return cudaErrorInvalidConfiguration;
+        }
+        pairs = pairs_of[dev];
+    }
+    p.k_blocks = (k + kLinBK - 1) / kLinBK;
+    p.tiles_m = (p.m + kLinTile - 1) / kLinTile;
+    p.tiles_n = (p.n + kLinTile - 1) / kLinTile;
+    const int tiles = p.tiles_m * p.tiles_n;
+    bool group_m = false;
+    p.group = gemm_raster(p.tiles_m, p.tiles_n, kLinTile, kLinTile, k, std::min(tiles, pairs), &group_m);
+    p.group_m = group_m ? 1 : 0;
+    // A last wave that would keep at most half of the pairs busy runs as halves of 128
+    // columns on twice as many: each output element takes the same steps.
+    const int rem = tiles % pairs;
+    p.narrow_from = rem > 0 && 2 * rem <= pairs ? tiles - rem : tiles;
+    p.num_units = p.narrow_from + 2 * (tiles - p.narrow_from);
+    kern<<<2 * std::min(p.num_units, pairs), kLinThreads, kLinSmem, stream>>>(ma, mb, mo, p);
+    return cudaGetLastError();
+}
+
+bool activation_ok(int32_t act) { return act >= ZB_ACT_NONE && act <= ZB_ACT_RELU2; }
+
+// Codes and scales of a checkpoint with `tokens` rows.
+bool checkpoint_ok(const zb_checkpoint* c, int32_t tokens) {
+    return c && rows_ok(c->codes, tokens) && rows_ok(c->scales, tokens);
+}
+
+}  // namespace
+
+}  // namespace zbk
+
+extern "C" zb_status zb_op_linear_activation_forward(const void* x, const void* w, const float* bias, const void* residual,
+                                                     void* y, void* z, const zb_checkpoint* z_packed,
+                                                     const zb_checkpoint* y_packed, int32_t tokens, int32_t in_features,
+                                                     int32_t out_features, int32_t activation, void* stream) {
+    using namespace zbk;
+    if (!activation_ok(activation) || (z && z_packed)) return ZB_ERR_ARG;
+    if (!tokens_ok(tokens) || !feature_ok(in_features) || !feature_ok(out_features)) return ZB_ERR_SHAPE;
+    if (!rows_ok(x, tokens) || !fixed_ok(w) || !rows_ok(y, tokens) || (bias && !aligned16(bias)) ||
+        (residual && !aligned16(residual)) || (z && !aligned16(z)) || (z_packed && !checkpoint_ok(z_packed, tokens)) ||
+        (y_packed && !checkpoint_ok(y_packed, tokens)))
+        return ZB_ERR_ARG;
+    ZB_TRY(device_ok());
+    if (tokens == 0) return ZB_OK;
+    LinParams p{};
+    p.m = tokens;
+    p.n = out_features;
+    p.act = activation;
+    p.bias = bias;
+    p.residual = static_cast<const uint16_t*>(residual);
+    p.z = static_cast<uint16_t*>(z);
+    if (z_packed) {
+        p.z_codes = static_cast<uint8_t*>(z_packed->codes);
+        p.z_scales = static_cast<uint8_t*>(z_packed->scales);
+    }
+    if (y_packed) {
+        p.y_codes = static_cast<uint8_t*>(y_packed->codes);
+        p.y_scales = static_cast<uint8_t*>(y_packed->scales);
+    }
+    return cuda_status(launch_linear<false, false, kLinForward, false>(x, w, y, p, in_features, as_stream(stream)));
+}
+
+extern "C" size_t zb_op_backward_input_activation_scratch_bytes(int32_t tokens, int32_t in_features) {
+    if (!zbk::tokens_ok(tokens) || !zbk::feature_ok(in_features)) return 0;
+    return static_cast<size_t>((tokens + 31) / 32) * static_cast<size_t>(in_features) * sizeof(float);
+}
+
+extern "C" zb_status zb_op_backward_input_activation(const void* dy, const void* w, const void* z,
+                                                     const zb_checkpoint* z_packed, void* dz, float* dbias, int32_t tokens,
+                                                     int32_t in_features, int32_t out_features, int32_t activation,
+                                                     void* scratch, size_t scratch_bytes, void* stream) {
+    using namespace zbk;
+    if (!activation_ok(activation) || (z && z_packed)) return ZB_ERR_ARG;
+    if (!tokens_ok(tokens) || !feature_ok(in_features) || !feature_ok(out_features)) return ZB_ERR_SHAPE;
+    if (!rows_ok(dy, tokens) || !fixed_ok(w) || !rows_ok(dz, tokens) || (z && !aligned16(z)) ||
+        (z_packed && !checkpoint_ok(z_packed, tokens)) || (dbias && !aligned16(dbias)) ||
+        (tokens > 0 && activation != ZB_ACT_NONE && !z && !z_packed))
+        return ZB_ERR_ARG;
+    if (dbias && tokens > 0 &&
+        (!fixed_ok(scratch) || scratch_bytes < zb_op_backward_input_activation_scratch_bytes(tokens, in_features)))
+        return ZB_ERR_WORKSPACE;
+    ZB_TRY(device_ok());
+    if (tokens == 0) return ZB_OK;
+    LinParams p{};
+    p.m = tokens;
+    p.n = in_features;
+    p.act = activation;
+    p.z = static_cast<uint16_t*>(const_cast<void*>(z));
+    if (z_packed) {
+        p.z_codes = static_cast<uint8_t*>(z_packed->codes);
+        p.z_scales = static_cast<uint8_t*>(z_packed->scales);
+    }
+    cudaStream_t s = as_stream(stream);
+    if (!dbias) return cuda_status(launch_linear<false, true, kLinActivationBackward, false>(dy, w, dz, p, out_features, s));
+    p.col_sums = static_cast<float*>(scratch);
+    ZB_TRY(cuda_status(launch_linear<false, true, kLinActivationBackward, true>(dy, w, dz, p, out_features, s)));
+    launch_column_sum(p.col_sums, dbias, (tokens + 31) / 32, in_features, s);
+    return cuda_status(cudaGetLastError());
+}
+
+extern "C" zb_status zb_op_activation_backward(const void* dy, const void* z, const zb_checkpoint* z_packed, void* dz,
+                                               int32_t tokens, int32_t width, int32_t activation, void* stream) {
+    using namespace zbk;
+    if (!activation_ok(activation) || (z && z_packed)) return ZB_ERR_ARG;
+    if (!tokens_ok(tokens) || !feature_ok(width)) return ZB_ERR_SHAPE;
+    if (!rows_ok(dy, tokens) || !rows_ok(dz, tokens) || (z && !aligned16(z)) ||
+        (z_packed && !checkpoint_ok(z_packed, tokens)) || (tokens > 0 && activation != ZB_ACT_NONE && !z && !z_packed))
+        return ZB_ERR_ARG;
+    ZB_TRY(device_ok());
+    if (tokens == 0) return ZB_OK;
+    const int64_t chunks = static_cast<int64_t>(tokens) * (width / 8);
+    const int64_t grid = (chunks + 255) / 256;
+    if (grid > 0x7fffffff) return ZB_ERR_SHAPE;
+    activation_backward_kernel<<<static_cast<unsigned>(grid), 256, 0, as_stream(stream)>>>(
+        static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z),
+        z_packed ? static_cast<const uint8_t*>(z_packed->codes) : nullptr,
+        z_packed ? static_cast<const uint8_t*>(z_packed->scales) : nullptr, static_cast<uint16_t*>(dz), chunks, activation);
+    return cuda_status(cudaGetLastError());
+}
+
+extern "C" size_t zb_op_backward_bias_scratch_bytes(int32_t tokens, int32_t out_features) {
+    if (!zbk::tokens_ok(tokens) || !zbk::feature_ok(out_features)) return 0;
+    return static_cast<size_t>(zbk::column_parts(tokens, out_features)) * static_cast<size_t>(out_features) * sizeof(float);
+}
+
+extern "C" zb_status zb_op_backward_bias(const void* dy, float* dbias, int32_t tokens, int32_t out_features, void* scratch,
+                                         size_t scratch_bytes, void* stream) {
+    using namespace zbk;
+    if (!tokens_ok(tokens) || !feature_ok(out_features)) return ZB_ERR_SHAPE;
+    if (!rows_ok(dy, tokens) || !fixed_ok(dbias)) return ZB_ERR_ARG;
+    if (tokens > 0 && (!fixed_ok(scratch) || scratch_bytes < zb_op_backward_bias_scratch_bytes(tokens, out_features)))
+        return ZB_ERR_WORKSPACE;
+    ZB_TRY(device_ok());
+    if (tokens == 0) return ZB_OK;
+    const int parts = column_parts(tokens, out_features);
+    cudaStream_t s = as_stream(stream);
+    const dim3 grid((out_features + 255) / 256, parts);
+    column_parts_kernel<<<grid, kColThreads, 0, s>>>(static_cast<const uint16_t*>(dy), static_cast<float*>(scratch), tokens,
+                                                     out_features);
+    launch_column_sum(static_cast<const float*>(scratch), dbias, parts, out_features, s);
+    return cuda_status(cudaGetLastError());
+}
+
+extern "C" size_t zb_op_backward_weight_checkpoint_scratch_bytes(int32_t tokens, int32_t in_features) {
+    if (!zbk::tokens_ok(tokens) || !zbk::feature_ok(in_features)) return 0;
+    return static_cast<size_t>(tokens) * static_cast<size_t>(in_features) * 2;
+}
+
+extern "C" zb_status zb_op_backward_weight_checkpoint(const void* dy, const zb_checkpoint* x, float* dw, int32_t tokens,
+                                                      int32_t in_features, int32_t out_features, void* scratch,
+                                                      size_t scratch_bytes, void* stream) {
+    using namespace zbk;
+    if (!tokens_ok(tokens) || !feature_ok(in_features) || !feature_ok(out_features)) return ZB_ERR_SHAPE;
+    if (!rows_ok(dy, tokens) || !checkpoint_ok(x, tokens) || !fixed_ok(dw)) return ZB_ERR_ARG;
+    if (tokens > 0 &&
+        (!fixed_ok(scratch) || scratch_bytes < zb_op_backward_weight_checkpoint_scratch_bytes(tokens, in_features)))
+        return ZB_ERR_WORKSPACE;
+    ZB_TRY(device_ok());
+    if (tokens == 0) return ZB_OK;
+    cudaStream_t s = as_stream(stream);
+    ZB_TRY(cuda_status(launch_unpack(x->codes, x->scales, scratch, tokens, in_features, s)));
+    LinParams p{};
+    p.m = out_features;
+    p.n = in_features;
+    return cuda_status(launch_linear<true, true, kLinAccumulate, true>(dy, scratch, dw, p, tokens, s));
+}

@@ -404,6 +404,135 @@ zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t
                                 int32_t rotary_dim, int32_t pairs, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Linear layers with a bias, an activation and a residual: the feed-forward block
+ * without a gated product, beside zb_op_linear_forward and the SwiGLU calls.
+ * With z = x w^T + bias and y = act(z) + residual:
+ *   F  y, and on request z and y as checkpoints for B and W;
+ *   B  dz = (dy w) act'(z), where w is the linear BEHIND the activation and dy its
+ *      output gradient; dbias += sum_t dz is the bias gradient of the layer that made z;
+ *   W  dw += dy^T x ([G1]) with x from an 8-bit checkpoint.
+ *  - act: none; max(z, 0); z Phi(z); its tanh form z / (1 + exp(-2 sqrt(2/pi) (z +
+ *    0.044715 z^3))); z / (1 + exp(-z)); max(z, 0)^2.  The slope of the two with a corner
+ *    is 0 there.  A NaN in z gives a NaN in y and (act other than none) in dz.
+ *  - bias and dbias: float32 [out].  residual, z, y, dz: bf16 [T, out].  Any of bias,
+ *    residual, z and the checkpoints may be NULL; z in bf16 and in 8 bits is not both.
+ *  - z is rounded to bf16 before it is packed, y is computed from z before that: the
+ *    packed forms are the bits that zb_op_checkpoint_pack gives for the bf16 ones.
+ *  - y may be residual, and dz may be z; other outputs overlap no input.
+ *  - dbias adds the float32 dz, ahead of their rounding.  It and W hold their sums in
+ *    float32 registers that take 512 terms at a time from tensor memory, whose own sums
+ *    round towards zero (zb_op_backward_weight leaves all T terms there).
+ *  - Fixed orders throughout: the same bits every time.
+ *  - scratch: device memory of at least the bytes the _scratch_bytes call names, contents
+ *    ignored; only needed with dbias.  Calls that share it must not overlap on the GPU,
+ *    captured and replayed ones included. */
+typedef enum {
+    ZB_ACT_NONE = 0,
+    ZB_ACT_RELU = 1,
+    ZB_ACT_GELU = 2,
+    ZB_ACT_GELU_TANH = 3,
+    ZB_ACT_SILU = 4,
+    ZB_ACT_RELU2 = 5
+} zb_activation;
+
+/* An activation [T, width] in 8 bits.  scales: one byte per 32 consecutive columns of a
+ * row, [T, width / 32]; codes: one byte per element, [T, width], its sign in bit 7 and a
+ * magnitude m in the others.  A code's value is +-m 2^(scale - 127).  Packing takes the
+ * smallest scale from 1 to 248 at which the block's largest magnitude is below 127.5 units and rounds
+ * to the nearest unit, ties to even; the largest bf16 numbers round to 127 units.  So
+ * values are off by half a unit at most, 2^-7 of the block's largest.  They are bf16
+ * numbers exactly.  A block that holds a NaN or an infinity gets the scale 255 and reads
+ * as NaN.  Both arrays are 16-byte aligned; rows lie densely one behind another, so the
+ * checkpoints of consecutive microbatches can be one. */
+typedef struct {
+    void* codes;
+    void* scales;
+} zb_checkpoint;
+
+zb_status zb_op_checkpoint_pack(const void* x, const zb_checkpoint* packed, int32_t tokens, int32_t width, void* stream);
+zb_status zb_op_checkpoint_unpack(const zb_checkpoint* packed, void* x, int32_t tokens, int32_t width, void* stream);
+
+zb_status zb_op_linear_activation_forward(const void* x, const void* w, const float* bias, const void* residual, void* y,
+                                          void* z, const zb_checkpoint* z_packed, const zb_checkpoint* y_packed,
+                                          int32_t tokens, int32_t in_features, int32_t out_features, int32_t activation,
+                                          void* stream);
+
+/* dy[T, out], w[out, in]; z and dz [T, in]; dbias [in] or NULL.  With ZB_ACT_NONE z is
+ * not read and may be NULL. */
+size_t zb_op_backward_input_activation_scratch_bytes(int32_t tokens, int32_t in_features);
+zb_status zb_op_backward_input_activation(const void* dy, const void* w, const void* z, const zb_checkpoint* z_packed,
+                                          void* dz, float* dbias, int32_t tokens, int32_t in_features, int32_t out_features,
+                                          int32_t activation, void* scratch, size_t scratch_bytes, void* stream);
+
+/* The activation alone, for a layer whose y is not followed by a linear: dz = dy act'(z),
+ * all [T, width].  dz may be dy. */
+zb_status zb_op_activation_backward(const void* dy, const void* z, const zb_checkpoint* z_packed, void* dz, int32_t tokens,
+                                    int32_t width, int32_t activation, void* stream);
+
+/* W of a bias: dbias[out] (float32) += sum_t dy[t, :]. */
+size_t zb_op_backward_bias_scratch_bytes(int32_t tokens, int32_t out_features);
+zb_status zb_op_backward_bias(const void* dy, float* dbias, int32_t tokens, int32_t out_features, void* scratch,
+                              size_t scratch_bytes, void* stream);
+
+/* W of a linear whose input was kept in 8 bits: dw[out, in] (float32) += dy[T, out]^T x[T, in],
+ * each element of dw one float32 add per call.  scratch as above (it holds x's bf16 values). */
+size_t zb_op_backward_weight_checkpoint_scratch_bytes(int32_t tokens, int32_t in_features);
+zb_status zb_op_backward_weight_checkpoint(const void* dy, const zb_checkpoint* x, float* dw, int32_t tokens,
+                                           int32_t in_features, int32_t out_features, void* scratch, size_t scratch_bytes,
+                                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norms on both sides of a block, with its gate and residual scales, in one pass over
+ * the rows.  With x the residual stream that entered the block and y the block's output:
+ *   F  u = PostNorm(y),  h = a x + b gate u,  n = PreNorm(h): the next block's input;
+ *   B  dh = dres + PreNorm'(dn),  dx = a dh,  dgate = b u dh (per token),  dy = PostNorm'(b gate dh);
+ *   W  the norms' gammas and betas, and the gate per channel, each += over the tokens.
+ * Norm(v) = gamma (v - mean) rstd + beta over the row; ZB_NORM_RMS has mean 0 and no beta;
+ * ZB_NORM_NONE is the identity (no u norm; no n, then n and dn are NULL).
+ *  - x, y, h, n, dn, dres, dh, dx, dy: bf16 [T, hidden]; gammas and betas float32 [hidden]
+ *    (a layer norm's beta may be NULL); gate: float32 [hidden] (CHANNEL), or bf16 [T, hidden]
+ *    (TOKEN), which gets its gradient dgate in B.
+ *  - h is rounded to bf16 and n is the norm of the rounded h, so that B and W, which read
+ *    the stored h, differentiate what F computed.  Everything else is float32 between load
+ *    and store.  n may be NULL where n_packed is given (the bits that packing n gives).
+ *  - stats: float32 [T, 4]: post mean, post rstd, pre mean, pre rstd; 0 for what is not
+ *    there.  F writes it, B and W read it.
+ *  - dh is the whole gradient of h, kept for W; with a = 1 it is dx too, and dx may be NULL.
+ *    dres may be NULL where there is a pre norm (nothing else reads h).  y may be NULL in B
+ *    without a post norm or dgate; dgate may be NULL.
+ *  - h may be x; dh may be dres or dn.  Other outputs overlap no input.
+ *  - In W a gradient that is NULL is not formed, and what only it would read may be NULL.
+ *  - hidden is at most 32768.  Rows of padding give rows of padding: no row reads another
+ *    but in W, which adds all of them.  Fixed orders: the same bits every time. */
+typedef enum { ZB_NORM_NONE = 0, ZB_NORM_RMS = 1, ZB_NORM_LAYER = 2 } zb_norm_kind;
+typedef enum { ZB_GATE_NONE = 0, ZB_GATE_CHANNEL = 1, ZB_GATE_TOKEN = 2 } zb_gate_kind;
+
+typedef struct {
+    int32_t post_norm, pre_norm;  /* zb_norm_kind */
+    int32_t gate_kind;            /* zb_gate_kind */
+    int32_t reserved;
+    const float* post_gamma;
+    const float* post_beta;
+    const float* pre_gamma;
+    const float* pre_beta;
+    const void* gate;
+    float residual_scale, branch_scale; /* a, b: finite */
+    float post_eps, pre_eps;            /* in [0, 1] */
+} zb_residual_norm;
+
+zb_status zb_op_residual_norm_forward(const zb_residual_norm* op, const void* x, const void* y, void* h, void* n,
+                                      const zb_checkpoint* n_packed, float* stats, int32_t tokens, int32_t hidden,
+                                      void* stream);
+zb_status zb_op_residual_norm_backward_input(const zb_residual_norm* op, const void* dn, const void* dres, const void* h,
+                                             const void* y, const float* stats, void* dh, void* dx, void* dy, void* dgate,
+                                             int32_t tokens, int32_t hidden, void* stream);
+size_t zb_op_residual_norm_backward_weight_scratch_bytes(int32_t tokens, int32_t hidden);
+zb_status zb_op_residual_norm_backward_weight(const zb_residual_norm* op, const void* dn, const void* h, const void* dh,
+                                              const void* y, const float* stats, float* dpost_gamma, float* dpost_beta,
+                                              float* dpre_gamma, float* dpre_beta, float* dgate, int32_t tokens,
+                                              int32_t hidden, void* scratch, size_t scratch_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * AdamW: the optimizer step that the weight gradients of a flush wait for
  * ([G3]: accumulators are complete after the last W; [G1]: only the optimizer
  * step needs W).  One call updates any number of tensors:
