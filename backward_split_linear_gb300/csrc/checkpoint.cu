@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t* __re
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     if (i >= halves) return;
     const uint32_t scale = pack_scale(top);
-    const float f = pack_factor(scale);
+    const uint32_t f = pack_factor(scale);
     uint32_t c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[e] = scale == kPackNotFinite ? 0u : pack_codes(w[2 * e], w[2 * e + 1], f);
@@ -42,15 +42,13 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const uint8_t* __r
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kPackThreads + threadIdx.x;
     if (i >= halves) return;
     const uint4 cv = reinterpret_cast<const uint4*>(codes)[i];
-    const float unit = unpack_unit(scales[i >> 1]);
+    const uint32_t unit = unpack_unit(scales[i >> 1]);
     const uint32_t c[4] = {cv.x, cv.y, cv.z, cv.w};
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        float v[4];
-        unpack_codes(c[e], unit, v);
-        w[2 * e] = pack_bf16x2(v[0], v[1]);
-        w[2 * e + 1] = pack_bf16x2(v[2], v[3]);
+        w[2 * e] = unpack_pair<0>(c[e], unit);
+        w[2 * e + 1] = unpack_pair<1>(c[e], unit);
     }
     reinterpret_cast<uint4*>(x)[2 * i] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4*>(x)[2 * i + 1] = make_uint4(w[4], w[5], w[6], w[7]);

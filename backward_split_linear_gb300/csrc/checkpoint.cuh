@@ -29,21 +29,22 @@ __device__ __forceinline__ uint32_t pack_scale(uint32_t top) {
     return static_cast<uint32_t>(min(max(s, 1), 248));
 }
 
-// 2^(127 - scale), which takes magnitudes to units.
-__device__ __forceinline__ float pack_factor(uint32_t scale) { return __uint_as_float((254u - min(scale, 253u)) << 23); }
+// 2^(127 - scale), which takes magnitudes to units, as a pair of bf16 numbers.
+__device__ __forceinline__ uint32_t pack_factor(uint32_t scale) { return ((254u - min(scale, 253u)) << 7) * 0x00010001u; }
 
-// Four codes from two pairs of bf16 numbers.  |x| factor + 1.5 2^23 rounds to the nearest
-// even unit in its last bits; only the largest bf16 number would pass 127 (scale 248).
-__device__ __forceinline__ uint32_t pack_codes(uint32_t w0, uint32_t w1, float factor) {
-    constexpr float kBig = 12582912.f;
-    const float a = fminf(fmaf(fabsf(bf16_lo(w0)), factor, kBig), kBig + 127.f);
-    const float b = fminf(fmaf(fabsf(bf16_hi(w0)), factor, kBig), kBig + 127.f);
-    const float c = fminf(fmaf(fabsf(bf16_lo(w1)), factor, kBig), kBig + 127.f);
-    const float d = fminf(fmaf(fabsf(bf16_hi(w1)), factor, kBig), kBig + 127.f);
-    const uint32_t ab = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
-    const uint32_t cd = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
-    const uint32_t mags = __byte_perm(ab, cd, 0x5410);
-    return (mags & 0x7f7f7f7fu) | (__byte_perm(w0, w1, 0x7531) & 0x80808080u);
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// Four codes from two pairs of bf16 numbers.  From 128 to 256 a bf16 number is a whole one,
+// so |x| factor + 128 rounds to the nearest even unit, with the magnitude in its seven
+// mantissa bits.  Only the largest bf16 number would pass 127 units (at scale 248).
+__device__ __forceinline__ uint32_t pack_codes(uint32_t w0, uint32_t w1, uint32_t factor) {
+    const uint32_t a = fma_bf16x2(__vminu2(w0 & 0x7fff7fffu, 0x7f7e7f7eu), factor, 0x43004300u);
+    const uint32_t b = fma_bf16x2(__vminu2(w1 & 0x7fff7fffu, 0x7f7e7f7eu), factor, 0x43004300u);
+    return __byte_perm(a, b, 0x6420) | (__byte_perm(w0, w1, 0x7531) & 0x80808080u);
 }
 
 // One whole block: 16 words of bf16 pairs to 8 words of codes; returns the scale byte.
@@ -52,7 +53,7 @@ __device__ __forceinline__ uint32_t pack_block(const uint32_t (&w)[16], uint4& l
 #pragma unroll
     for (int i = 0; i < 16; ++i) top2 = pack_top2(top2, w[i]);
     const uint32_t scale = pack_scale(max(top2 & 0xffffu, top2 >> 16));
-    const float f = pack_factor(scale);
+    const uint32_t f = pack_factor(scale);
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = scale == kPackNotFinite ? 0u : pack_codes(w[2 * i], w[2 * i + 1], f);
@@ -61,20 +62,19 @@ __device__ __forceinline__ uint32_t pack_block(const uint32_t (&w)[16], uint4& l
     return scale;
 }
 
-// The unit 2^(scale - 127) of a block; NaN for one that was not finite.  A scale of 0 (which
-// packing never writes) stands for 0.
-__device__ __forceinline__ float unpack_unit(uint32_t scale) {
-    return scale == kPackNotFinite ? __uint_as_float(0x7fffffffu) : __uint_as_float(scale << 23);
+// The unit 2^(scale - 127) of a block, as a pair of bf16 numbers; NaN for one that was not
+// finite.  A scale of 0 (which packing never writes) stands for 0.
+__device__ __forceinline__ uint32_t unpack_unit(uint32_t scale) {
+    return scale == kPackNotFinite ? 0x7fff7fffu : (scale << 7) * 0x00010001u;
 }
 
-// Four codes as float32 values.
-__device__ __forceinline__ void unpack_codes(uint32_t c, float unit, float (&v)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t byte = (c >> (8 * i)) & 0xffu;
-        const float mag = __uint_as_float(0x4b000000u | (byte & 0x7fu)) - 8388608.f;
-        v[i] = __uint_as_float(__float_as_uint(mag * unit) ^ ((byte & 0x80u) << 24));
-    }
+// Codes 2 kHalf and 2 kHalf + 1 of the four in `c` as a pair of bf16 numbers: 128 + m from the
+// bits, less 128, times the unit, all exact.
+template <int kHalf>
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t c, uint32_t unit) {
+    const uint32_t m = __byte_perm(c & 0x7f7f7f7fu, 0x43434343u, kHalf ? 0x4342 : 0x4140);
+    const uint32_t v = fma_bf16x2(fma_bf16x2(m, 0x3f803f80u, 0xc300c300u), unit, 0x80008000u);
+    return v ^ (__byte_perm(c, 0u, kHalf ? 0x3424 : 0x1404) & 0x80008000u);
 }
 
 }  // namespace zbk

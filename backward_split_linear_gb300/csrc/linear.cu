@@ -46,6 +46,9 @@ static_assert(kLinSmem <= 232448, "shared memory");
 // Registers a thread: 384 x 168 at launch, of which 128 x 64 + 256 x 216 are used.
 constexpr int kLinFewRegs = 64, kLinManyRegs = 216;
 constexpr int kLinSumBlocks = 8;  // k blocks (512 terms) that stay in tensor memory
+// Twice as many in a tile's first two accumulators where others follow: while the epilogue
+// warps work on the tile before, the MMAs get that far and no further.
+constexpr int kLinFirstSums = 48;  // from so many k blocks on
 
 enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
 
@@ -93,69 +96,162 @@ __device__ __forceinline__ void lin_tile(const LinParams& p, int tile, int& tm, 
 
 // ---------------------------------------------------------------- activations
 //
-// gelu through erfc and gelu_tanh through the logistic function (0.5 (1 + tanh u) =
+// Two values at a time, for the packed float32 instructions.  gelu goes through the normal
+// distribution's tail and gelu_tanh through the logistic function (0.5 (1 + tanh u) =
 // 1 / (1 + exp(-2 u))): neither cancels where the activation is small.  A NaN stays one.
 
-__device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-constexpr float kTanhA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+__device__ __forceinline__ float2 exp2_fast(float2 x) {
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 reciprocal_fast(float2 x) {
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+}
+
+// The smaller (larger) of two numbers; a NaN stays one.
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// Behind +-30 an activation's slope is 0 or 1 to the last bit, and its terms would pass the range.
+constexpr float kActMost = 30.f;
+__device__ __forceinline__ float2 act_clamp(float2 z) {
+    return make_float2(max_nan(min_nan(z.x, kActMost), -kActMost), max_nan(min_nan(z.y, kActMost), -kActMost));
+}
+
+// The standard normal distribution's tail beyond a >= 0, and exp(-a^2 / 2).  The tail is
+// 0.5 exp(-x^2) erfcx(x), x = a / sqrt(2), with the scaled function erfcx(x) as t Q(t), t = 1 / (1 +
+// 0.42 x) (the form of Hastings, "Approximations for Digital Computers", with a Q of degree
+// 7 fitted here to erfcx over 0 <= x <= 9.6: off by 1.8e-7 of it at most; the float32
+// steps add 1e-6 for a up to 5).  With erfcf and expf the epilogue bounded B: 431 us for the 8B-shaped
+// down projection with a bias gradient, 354 with this in scalar steps.
+__device__ __forceinline__ float2 normal_tail(float2 a, float2& e) {
+    const float2 t = reciprocal_fast(__ffma2_rn(both(0.29698485f), a, both(1.0f)));
+    e = exp2_fast(__fmul2_rn(__fmul2_rn(a, a), both(-0.72134752f)));
+    float2 q = both(0.03501970320940018f);
+    q = __ffma2_rn(q, t, both(-0.1597243994474411f));
+    q = __ffma2_rn(q, t, both(0.21963188052177429f));
+    q = __ffma2_rn(q, t, both(-0.06460575759410858f));
+    q = __ffma2_rn(q, t, both(0.13401812314987183f));
+    q = __ffma2_rn(q, t, both(0.0974719300866127f));
+    q = __ffma2_rn(q, t, both(0.11977513879537582f));
+    q = __ffma2_rn(q, t, both(0.1184132993221283f));
+    return __fmul2_rn(__fmul2_rn(q, t), e);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
+// 1 / (1 + exp(-z w)), with w' = -w log2(e)
+__device__ __forceinline__ float2 logistic(float2 z, float2 w) {
+    return reciprocal_fast(__fadd2_rn(exp2_fast(__fmul2_rn(z, w)), both(1.0f)));
+}
+
+__device__ __forceinline__ float2 tanh_weight(float2 z) {
+    return __ffma2_rn(__fmul2_rn(z, z), both(-kTanhA * kTanhB * kLog2e), both(-kTanhA * kLog2e));
+}
+
 template <int kAct>
-__device__ __forceinline__ float act_value(float z) {
-    if (kAct == ZB_ACT_RELU) return z < 0.f ? 0.f : z;
-    if (kAct == ZB_ACT_RELU2) return z < 0.f ? 0.f : z * z;
-    if (kAct == ZB_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    if (kAct == ZB_ACT_GELU_TANH) return z * logistic(kTanhA * (z + kTanhB * z * z * z));
-    if (kAct == ZB_ACT_SILU) return z * logistic(z);
+__device__ __forceinline__ float2 act_value(float2 z) {
+    if constexpr (kAct == ZB_ACT_RELU) return make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
+    if constexpr (kAct == ZB_ACT_RELU2) {
+        const float2 m = make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
+        return __fmul2_rn(m, m);
+    }
+    if constexpr (kAct == ZB_ACT_GELU) {  // max(z, 0) - |z| tail(|z|)
+        const float2 a = make_float2(min_nan(fabsf(z.x), kActMost), min_nan(fabsf(z.y), kActMost));
+        float2 e;
+        const float2 tail = normal_tail(a, e);
+        return __ffma2_rn(make_float2(-a.x, -a.y), tail, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+    }
+    if constexpr (kAct == ZB_ACT_GELU_TANH) return __fmul2_rn(z, logistic(z, tanh_weight(z)));
+    if constexpr (kAct == ZB_ACT_SILU) return __fmul2_rn(z, logistic(z, both(-kLog2e)));
     return z;
 }
 
 template <int kAct>
-__device__ __forceinline__ float act_slope(float z) {
-    if (kAct == ZB_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-    if (kAct == ZB_ACT_RELU2) return z <= 0.f ? 0.f : 2.f * z;
-    // behind +-30 the slopes below are 0 or 1 to the last bit; their terms would pass the range
-    const float c = z > 30.f ? 30.f : (z < -30.f ? -30.f : z);
-    if (kAct == ZB_ACT_GELU) return 0.5f * erfcf(c * -0.70710678118654752f) + 0.3989422804014327f * c * __expf(-0.5f * c * c);
-    if (kAct == ZB_ACT_GELU_TANH) {
-        const float s = logistic(kTanhA * (c + kTanhB * c * c * c));
-        return s + c * s * (1.f - s) * kTanhA * (1.f + 3.f * kTanhB * c * c);
+__device__ __forceinline__ float2 act_slope(float2 z) {
+    if constexpr (kAct == ZB_ACT_RELU)
+        return make_float2(z.x > 0.f ? 1.f : (z.x <= 0.f ? 0.f : z.x), z.y > 0.f ? 1.f : (z.y <= 0.f ? 0.f : z.y));
+    if constexpr (kAct == ZB_ACT_RELU2) return __fmul2_rn(make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f)), both(2.f));
+    const float2 c = act_clamp(z);
+    if constexpr (kAct == ZB_ACT_GELU) {  // 1/2 +- (1/2 - tail) + z phi(z)
+        float2 e;
+        const float2 tail = normal_tail(make_float2(fabsf(c.x), fabsf(c.y)), e);
+        float2 body = __ffma2_rn(tail, both(-1.f), both(0.5f));
+        body = make_float2(copysignf(body.x, c.x), copysignf(body.y, c.y));
+        return __fadd2_rn(__ffma2_rn(__fmul2_rn(c, both(0.3989422804014327f)), e, body), both(0.5f));
     }
-    if (kAct == ZB_ACT_SILU) {
-        const float s = logistic(c);
-        return s * (1.f + c * (1.f - s));
+    if constexpr (kAct == ZB_ACT_GELU_TANH) {  // s + c s (1 - s) 2u', 2u' = A (1 + 3 B c^2)
+        const float2 s = logistic(c, tanh_weight(c));
+        const float2 left = __ffma2_rn(s, make_float2(-s.x, -s.y), s);  // s - s^2
+        const float2 du = __ffma2_rn(__fmul2_rn(c, c), both(3.f * kTanhA * kTanhB), both(kTanhA));
+        return __ffma2_rn(__fmul2_rn(c, left), du, s);
     }
-    return 1.f;
+    if constexpr (kAct == ZB_ACT_SILU) {  // s + c s (1 - s)
+        const float2 s = logistic(c, both(-kLog2e));
+        return __ffma2_rn(c, __ffma2_rn(s, make_float2(-s.x, -s.y), s), s);
+    }
+    return both(1.f);
 }
 
-template <int N, typename F>
-__device__ __forceinline__ void each(F&& f) {
+template <int kAct, int N>
+__device__ __forceinline__ void act_values_of(float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f(i);
+    for (int i = 0; i < N; i += 2) {
+        const float2 y = act_value<kAct>(make_float2(v[i], v[i + 1]));
+        v[i] = y.x;
+        v[i + 1] = y.y;
+    }
 }
 
 template <int N>
 __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     switch (act) {
-        case ZB_ACT_RELU: each<N>([&](int i) { v[i] = act_value<ZB_ACT_RELU>(v[i]); }); break;
-        case ZB_ACT_GELU: each<N>([&](int i) { v[i] = act_value<ZB_ACT_GELU>(v[i]); }); break;
-        case ZB_ACT_GELU_TANH: each<N>([&](int i) { v[i] = act_value<ZB_ACT_GELU_TANH>(v[i]); }); break;
-        case ZB_ACT_SILU: each<N>([&](int i) { v[i] = act_value<ZB_ACT_SILU>(v[i]); }); break;
-        case ZB_ACT_RELU2: each<N>([&](int i) { v[i] = act_value<ZB_ACT_RELU2>(v[i]); }); break;
+        case ZB_ACT_RELU: act_values_of<ZB_ACT_RELU>(v); break;
+        case ZB_ACT_GELU: act_values_of<ZB_ACT_GELU>(v); break;
+        case ZB_ACT_GELU_TANH: act_values_of<ZB_ACT_GELU_TANH>(v); break;
+        case ZB_ACT_SILU: act_values_of<ZB_ACT_SILU>(v); break;
+        case ZB_ACT_RELU2: act_values_of<ZB_ACT_RELU2>(v); break;
         default: break;
     }
 }
 
 // d[i] *= act'(z[i])
+template <int kAct, int N>
+__device__ __forceinline__ void act_slopes_of(float (&d)[N], const float (&z)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 y = __fmul2_rn(make_float2(d[i], d[i + 1]), act_slope<kAct>(make_float2(z[i], z[i + 1])));
+        d[i] = y.x;
+        d[i + 1] = y.y;
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void act_slopes(int act, float (&d)[N], const float (&z)[N]) {
     switch (act) {
-        case ZB_ACT_RELU: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_RELU>(z[i]); }); break;
-        case ZB_ACT_GELU: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_GELU>(z[i]); }); break;
-        case ZB_ACT_GELU_TANH: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_GELU_TANH>(z[i]); }); break;
-        case ZB_ACT_SILU: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_SILU>(z[i]); }); break;
-        case ZB_ACT_RELU2: each<N>([&](int i) { d[i] *= act_slope<ZB_ACT_RELU2>(z[i]); }); break;
+        case ZB_ACT_RELU: act_slopes_of<ZB_ACT_RELU>(d, z); break;
+        case ZB_ACT_GELU: act_slopes_of<ZB_ACT_GELU>(d, z); break;
+        case ZB_ACT_GELU_TANH: act_slopes_of<ZB_ACT_GELU_TANH>(d, z); break;
+        case ZB_ACT_SILU: act_slopes_of<ZB_ACT_SILU>(d, z); break;
+        case ZB_ACT_RELU2: act_slopes_of<ZB_ACT_RELU2>(d, z); break;
         default: break;
     }
 }
@@ -205,10 +301,12 @@ __device__ __forceinline__ void forward_chunk(const LinParams& p, LinRow& row, f
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + n) + j);
-            v[4 * j] += b.x;
-            v[4 * j + 1] += b.y;
-            v[4 * j + 2] += b.z;
-            v[4 * j + 3] += b.w;
+            const float2 lo = __fadd2_rn(make_float2(v[4 * j], v[4 * j + 1]), make_float2(b.x, b.y));
+            const float2 hi = __fadd2_rn(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(b.z, b.w));
+            v[4 * j] = lo.x;
+            v[4 * j + 1] = lo.y;
+            v[4 * j + 2] = hi.x;
+            v[4 * j + 3] = hi.y;
         }
     }
     if (p.z || p.z_codes) {
@@ -275,16 +373,17 @@ __device__ __forceinline__ void load_z(const LinParams& p, int64_t at, bool ok, 
 
 __device__ __forceinline__ void z_values(const LinParams& p, const ZWords& z, float (&v)[32]) {
     if (p.z_codes) {
-        const float unit = unpack_unit(z.scale);
+        const uint32_t unit = unpack_unit(z.scale);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t w[4] = {z.w[j].x, z.w[j].y, z.w[j].z, z.w[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float q[4];
-                unpack_codes(w[e], unit, q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[16 * j + 4 * e + i] = q[i];
+                const uint32_t lo = unpack_pair<0>(w[e], unit), hi = unpack_pair<1>(w[e], unit);
+                v[16 * j + 4 * e] = bf16_lo(lo);
+                v[16 * j + 4 * e + 1] = bf16_hi(lo);
+                v[16 * j + 4 * e + 2] = bf16_lo(hi);
+                v[16 * j + 4 * e + 3] = bf16_hi(hi);
             }
         }
     } else {
@@ -361,7 +460,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int chunk_blocks = kSums ? kLinSumBlocks : p.k_blocks;
+    // k blocks of the accumulator that starts at block kc
+    auto chunk_at = [&](int kc) {
+        if (!kSums) return p.k_blocks;
+        return p.k_blocks >= kLinFirstSums && kc < 4 * kLinSumBlocks ? 2 * kLinSumBlocks : kLinSumBlocks;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kLinStages; ++s) {
@@ -458,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 bool ok = true;
                 for (int u = pair; ok && u < p.num_units; u += npairs) {
                     const uint32_t idesc = lin_unit(p, u).narrow ? idesc_narrow : idesc_wide;
-                    for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_blocks, ++it) {
+                    for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_at(kc), ++it) {
                         const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
                         if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
                             ok = false;
@@ -466,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         }
                         tc_fence_after();
                         const uint32_t d = tmem_base + acc * kLinTile;
-                        const int kb1 = min(kc + chunk_blocks, p.k_blocks);
+                        const int kb1 = min(kc + chunk_at(kc), p.k_blocks);
                         for (int kb = kc; kb < kb1; ++kb) {
                             if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
                                 ok = false;
@@ -581,7 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 };
                 if constexpr (kSums) {
                     float sum[4][32];
-                    for (int kc = 0; alive && kc < p.k_blocks; kc += chunk_blocks) {
+                    for (int kc = 0; alive && kc < p.k_blocks; kc += chunk_at(kc)) {
                         if (!acquire()) break;
                         const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
 #pragma unroll
@@ -608,16 +711,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         for (int c = 0; c < 4; ++c)
                             if (32 * c < cols) finish(sum[c], unused, c);
                     } else {
-                        // one copy of the long code: the sums move down 32 columns at a time
+                        // two copies of the long code rather than four: the sums move down
 #pragma unroll 1
-                        for (int c = 0; 32 * c < cols; ++c) {
-                            const ZWords zw = z_of(c);
-                            finish(sum[0], zw, c);
+                        for (int c = 0; 32 * c < cols; c += 2) {
+                            finish(sum[0], z_of(c), c);
+                            finish(sum[1], z_of(c + 1), c + 1);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                sum[0][i] = sum[1][i];
-                                sum[1][i] = sum[2][i];
-                                sum[2][i] = sum[3][i];
+                                sum[0][i] = sum[2][i];
+                                sum[1][i] = sum[3][i];
                             }
                         }
                     }
@@ -752,14 +854,14 @@ __global__ void __launch_bounds__(256) activation_backward_kernel(const uint16_t
     }
     if (codes) {
         const uint2 c = reinterpret_cast<const uint2*>(codes)[i];
-        const float unit = unpack_unit(scales[i >> 2]);
-        float q[4];
-        unpack_codes(c.x, unit, q);
+        const uint32_t unit = unpack_unit(scales[i >> 2]);
+        const uint32_t w[4] = {unpack_pair<0>(c.x, unit), unpack_pair<1>(c.x, unit), unpack_pair<0>(c.y, unit),
+                               unpack_pair<1>(c.y, unit)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = q[e];
-        unpack_codes(c.y, unit, q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 + e] = q[e];
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = bf16_lo(w[e]);
+            x[2 * e + 1] = bf16_hi(w[e]);
+        }
     } else {
         const uint4 zv = reinterpret_cast<const uint4*>(z)[i];
         const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
@@ -872,6 +974,9 @@ extern "C" zb_status zb_op_linear_activation_forward(const void* x, const void* 
         p.y_codes = static_cast<uint8_t*>(y_packed->codes);
         p.y_scales = static_cast<uint8_t*>(y_packed->scales);
     }
+    // 8-bit codes are whole numbers: a sum that is short by 4e-6 moves some across a border
+    if (z_packed || y_packed)
+        return cuda_status(launch_linear<false, false, kLinForward, true>(x, w, y, p, in_features, as_stream(stream)));
     return cuda_status(launch_linear<false, false, kLinForward, false>(x, w, y, p, in_features, as_stream(stream)));
 }
 

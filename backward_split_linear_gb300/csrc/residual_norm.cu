@@ -10,6 +10,7 @@
 // memory where a row has more than one warp.  Both are bound by HBM.
 #include <algorithm>
 
+#include "chained.cuh"
 #include "checkpoint.cuh"
 #include "checks.h"
 #include "device_common.cuh"
@@ -36,59 +37,72 @@ struct NormParams {
     int hidden, post, pre;
 };
 
+// Eight values as four pairs, for the packed float32 instructions.
 struct F8 {
-    float v[8];
+    float2 p[4];
 };
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 __device__ __forceinline__ F8 widen(const uint4& q) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    F8 r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        r.v[2 * e] = bf16_lo(w[e]);
-        r.v[2 * e + 1] = bf16_hi(w[e]);
-    }
-    return r;
+    return F8{{make_float2(bf16_lo(q.x), bf16_hi(q.x)), make_float2(bf16_lo(q.y), bf16_hi(q.y)),
+               make_float2(bf16_lo(q.z), bf16_hi(q.z)), make_float2(bf16_lo(q.w), bf16_hi(q.w))}};
 }
 
 __device__ __forceinline__ uint4 narrow(const F8& f) {
-    return make_uint4(pack_bf16x2(f.v[0], f.v[1]), pack_bf16x2(f.v[2], f.v[3]), pack_bf16x2(f.v[4], f.v[5]),
-                      pack_bf16x2(f.v[6], f.v[7]));
+    return make_uint4(pack_bf16x2(f.p[0].x, f.p[0].y), pack_bf16x2(f.p[1].x, f.p[1].y), pack_bf16x2(f.p[2].x, f.p[2].y),
+                      pack_bf16x2(f.p[3].x, f.p[3].y));
 }
 
 __device__ __forceinline__ F8 load_f8(const float* p) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
 __device__ __forceinline__ uint4 load_q(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void store_q(uint16_t* p, const uint4& q) { *reinterpret_cast<uint4*>(p) = q; }
+
+// v * scale + shift of the normed value: scale = rstd, shift = -mean rstd, one rounding.
+__device__ __forceinline__ void affine(F8& v, float scale, float shift) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.p[e] = __ffma2_rn(v.p[e], both(scale), both(shift));
+}
+
+__device__ __forceinline__ void times(F8& v, const F8& g) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.p[e] = __fmul2_rn(v.p[e], g.p[e]);
+}
+
+// v gamma + beta
+__device__ __forceinline__ void weigh(F8& v, const float* gamma, const float* beta, int at) {
+    const F8 g = load_f8(gamma + at);
+    if (beta) {
+        const F8 b = load_f8(beta + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v.p[e] = __ffma2_rn(v.p[e], g.p[e], b.p[e]);
+    } else {
+        times(v, g);
+    }
+}
 
 // Sums of (s0, s1) over the threads of a row.  Each use of `round` has shared memory of its
 // own, so that one barrier a sum is enough.
 template <int kRow>
-__device__ __forceinline__ float2 row_sum(float s0, float s1, float2 (*red)[32], int round) {
+__device__ __forceinline__ float2 row_sum(float2 s, float2 (*red)[32], int round) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        s = __fadd2_rn(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
     if constexpr (kRow > 32) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) red[round][warp] = make_float2(s0, s1);
+        if (lane == 0) red[round][warp] = s;
         __syncthreads();
         constexpr int kWarps = kRow / 32;
-        const float2 part = lane < kWarps ? red[round][lane] : make_float2(0.f, 0.f);
-        s0 = part.x;
-        s1 = part.y;
+        s = red[round][lane & (kWarps - 1)];
 #pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1) {
-            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-        }
-        s0 = __shfl_sync(0xffffffffu, s0, 0);
-        s1 = __shfl_sync(0xffffffffu, s1, 0);
+        for (int o = kWarps / 2; o > 0; o >>= 1)
+            s = __fadd2_rn(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
     }
-    return make_float2(s0, s1);
+    return s;
 }
 
 // Rows of a block, kRow threads each (one row where a row has more than a warp).
@@ -97,122 +111,122 @@ __host__ __device__ constexpr int norm_rows() {
     return kRow == 32 ? 4 : 1;
 }
 
-// Mean and 1 / sqrt(variance + eps) of a row whose thread holds kPer groups of 8 values.  The
-// variance is of the differences from the mean: a second sum, which a mean far from zero
-// cannot spoil.
-template <int kRow, int kPer>
-__device__ __forceinline__ float2 moments(const F8 (&v)[kPer], const bool (&in)[kPer], int kind, float eps, int hidden,
+// Blocks that an SM takes at once with `regs` registers a thread.
+template <int kRow>
+__host__ __device__ constexpr int norm_blocks(int regs) {
+    return 65536 / (kRow * norm_rows<kRow>() * regs) > 1 ? 65536 / (kRow * norm_rows<kRow>() * regs) : 1;
+}
+
+// Mean and 1 / sqrt(variance + eps) of a row whose thread holds kPer groups of 8 values
+// (zeros past the row's end, unless kFull).  A layer norm's variance is of the differences from
+// the mean: a second sum, which a mean far from zero cannot spoil.
+template <int kRow, int kPer, bool kFull>
+__device__ __forceinline__ float2 moments(const F8 (&v)[kPer], int tid, int chunks, int kind, float eps, float inv,
                                           float2 (*red)[32], int round) {
-    const float inv = 1.f / static_cast<float>(hidden);
+    float2 q = both(0.f);
     float mean = 0.f;
     if (kind == ZB_NORM_LAYER) {
-        float s = 0.f;
+        float2 s = both(0.f);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += in[i] ? v[i].v[e] : 0.f;
-        mean = row_sum<kRow>(s, 0.f, red, round).x * inv;
-    }
-    float q = 0.f;
+            for (int e = 0; e < 4; ++e) s = __fadd2_rn(s, v[i].p[e]);
+        mean = row_sum<kRow>(make_float2(s.x + s.y, 0.f), red, round).x * inv;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+        for (int i = 0; i < kPer; ++i) {
+            if (!kFull && tid + i * kRow >= chunks) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = v[i].v[e] - mean;
-            q += in[i] ? d * d : 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const float2 d = __fadd2_rn(v[i].p[e], both(-mean));
+                q = __ffma2_rn(d, d, q);
+            }
         }
-    const float var = row_sum<kRow>(q, 0.f, red, round + 1).x * inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q = __ffma2_rn(v[i].p[e], v[i].p[e], q);
+    }
+    const float var = row_sum<kRow>(make_float2(q.x + q.y, 0.f), red, round + 1).x * inv;
     return make_float2(mean, rsqrtf(var + eps));
 }
 
-template <int kRow, int kPer>
-__global__ void __launch_bounds__(kRow * norm_rows<kRow>()) residual_norm_forward_kernel(const __grid_constant__ NormParams p,
-                                                                                         int tokens) {
+template <int kRow, int kPer, bool kFull>
+__global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(80))
+    residual_norm_forward_kernel(const __grid_constant__ NormParams p, int tokens) {
     __shared__ float2 red[4][32];
+    wait_for_previous();
     const int tid = kRow == 32 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = kRow == 32 ? static_cast<int64_t>(blockIdx.x) * norm_rows<kRow>() + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= tokens) return;  // whole warps
     const int64_t base = row * p.hidden;
     const int chunks = p.hidden >> 3;
-    bool in[kPer];
-    uint4 xq[kPer], gq[kPer];
+    const float inv = 1.f / static_cast<float>(p.hidden);
+    auto inside = [&](int i) { return kFull || tid + i * kRow < chunks; };
+    uint4 xq[kPer];
     F8 u[kPer];
+    {
+        uint4 yq[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int c = tid + i * kRow;
-        in[i] = c < chunks;
-        uint4 yq = make_uint4(0, 0, 0, 0);
-        if (in[i]) {
-            yq = load_q(p.y + base + 8 * c);
-            xq[i] = load_q(p.x + base + 8 * c);
-            if (p.gate_token) gq[i] = load_q(p.gate_token + base + 8 * c);
-        }
-        u[i] = widen(yq);
+        for (int i = 0; i < kPer; ++i)
+            yq[i] = inside(i) ? load_q(p.y + base + 8 * (tid + i * kRow)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (inside(i)) xq[i] = load_q(p.x + base + 8 * (tid + i * kRow));
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) u[i] = widen(yq[i]);
     }
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.post != ZB_NORM_NONE) {
-        const float2 m = moments<kRow, kPer>(u, in, p.post, p.post_eps, p.hidden, red, 0);
+        const float2 m = moments<kRow, kPer, kFull>(u, tid, chunks, p.post, p.post_eps, inv, red, 0);
         st.x = m.x;
         st.y = m.y;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int c = tid + i * kRow;
-        if (!in[i]) continue;
+        if (!inside(i)) continue;
+        const int at = 8 * (tid + i * kRow);
         if (p.post != ZB_NORM_NONE) {
-            const F8 g = load_f8(p.post_gamma + 8 * c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[i].v[e] = (u[i].v[e] - st.x) * st.y * g.v[e];
-            if (p.post_beta) {
-                const F8 b = load_f8(p.post_beta + 8 * c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[i].v[e] += b.v[e];
-            }
+            affine(u[i], st.y, -st.x * st.y);
+            weigh(u[i], p.post_gamma, p.post_beta, at);
         }
-        if (p.gate_channel || p.gate_token) {
-            const F8 g = p.gate_channel ? load_f8(p.gate_channel + 8 * c) : widen(gq[i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[i].v[e] *= g.v[e];
-        }
+        if (p.gate_channel)
+            times(u[i], load_f8(p.gate_channel + at));
+        else if (p.gate_token)
+            times(u[i], widen(load_q(p.gate_token + base + at)));
         const F8 x = widen(xq[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[i].v[e] = p.a * x.v[e] + p.b * u[i].v[e];
+        for (int e = 0; e < 4; ++e) u[i].p[e] = __ffma2_rn(u[i].p[e], both(p.b), __fmul2_rn(x.p[e], both(p.a)));
         const uint4 hq = narrow(u[i]);
-        *reinterpret_cast<uint4*>(p.h + base + 8 * c) = hq;
+        store_q(p.h + base + at, hq);
         u[i] = widen(hq);  // n is the norm of the h that is stored
     }
     if (p.pre != ZB_NORM_NONE) {
-        const float2 m = moments<kRow, kPer>(u, in, p.pre, p.pre_eps, p.hidden, red, 2);
+        const float2 m = moments<kRow, kPer, kFull>(u, tid, chunks, p.pre, p.pre_eps, inv, red, 2);
         st.z = m.x;
         st.w = m.y;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int c = tid + i * kRow;
+            const int at = 8 * (tid + i * kRow);
             uint4 nq = make_uint4(0, 0, 0, 0);
-            if (in[i]) {
-                const F8 g = load_f8(p.pre_gamma + 8 * c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[i].v[e] = (u[i].v[e] - st.z) * st.w * g.v[e];
-                if (p.pre_beta) {
-                    const F8 b = load_f8(p.pre_beta + 8 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) u[i].v[e] += b.v[e];
-                }
+            if (inside(i)) {
+                affine(u[i], st.w, -st.z * st.w);
+                weigh(u[i], p.pre_gamma, p.pre_beta, at);
                 nq = narrow(u[i]);
-                if (p.n) *reinterpret_cast<uint4*>(p.n + base + 8 * c) = nq;
+                if (p.n) store_q(p.n + base + at, nq);
             }
             if (p.codes) {  // four threads hold a block of 32 (a row has a multiple of 8 chunks)
-                uint32_t top2 = pack_top2(pack_top2(pack_top2(pack_top2(0u, nq.x), nq.y), nq.z), nq.w);
+                const uint32_t top2 = pack_top2(pack_top2(pack_top2(pack_top2(0u, nq.x), nq.y), nq.z), nq.w);
                 uint32_t top = max(top2 & 0xffffu, top2 >> 16);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (in[i]) {
+                if (inside(i)) {
                     const uint32_t scale = pack_scale(top);
-                    const float f = pack_factor(scale);
+                    const uint32_t f = pack_factor(scale);
                     const bool fine = scale != kPackNotFinite;
-                    reinterpret_cast<uint2*>(p.codes + base)[c] =
+                    *reinterpret_cast<uint2*>(p.codes + base + at) =
                         make_uint2(fine ? pack_codes(nq.x, nq.y, f) : 0u, fine ? pack_codes(nq.z, nq.w, f) : 0u);
-                    if ((tid & 3) == 0) p.scales[(base >> 5) + (c >> 2)] = static_cast<uint8_t>(scale);
+                    if ((tid & 3) == 0) p.scales[(base + at) >> 5] = static_cast<uint8_t>(scale);
                 }
             }
         }
@@ -222,10 +236,11 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>()) residual_norm_forwar
 
 // The input gradient of a norm of rows: d is the gradient of the normed values `hat`:
 //   rstd (d - hat mean(d hat) - [layer] mean(d)).
-template <int kRow, int kPer>
-__global__ void __launch_bounds__(kRow * norm_rows<kRow>()) residual_norm_backward_kernel(const __grid_constant__ NormParams p,
-                                                                                          int tokens) {
+template <int kRow, int kPer, bool kFull>
+__global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(128))
+    residual_norm_backward_kernel(const __grid_constant__ NormParams p, int tokens) {
     __shared__ float2 red[2][32];
+    wait_for_previous();
     const int tid = kRow == 32 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = kRow == 32 ? static_cast<int64_t>(blockIdx.x) * norm_rows<kRow>() + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= tokens) return;  // whole warps
@@ -233,200 +248,186 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>()) residual_norm_backwa
     const int chunks = p.hidden >> 3;
     const float inv = 1.f / static_cast<float>(p.hidden);
     const bool pre = p.pre != ZB_NORM_NONE, post = p.post != ZB_NORM_NONE;
-    const float4 st = p.stats[row];
+    auto inside = [&](int i) { return kFull || tid + i * kRow < chunks; };
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 nq[kPer], hq[kPer], rq[kPer], yq[kPer], gq[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int c = tid + i * kRow;
-        const bool in = c < chunks;
-        nq[i] = in && pre ? load_q(p.dn + base + 8 * c) : zero;
-        hq[i] = in && pre ? load_q(p.h + base + 8 * c) : zero;
-        rq[i] = in && p.dres ? load_q(p.dres + base + 8 * c) : zero;
-        yq[i] = in && p.y ? load_q(p.y + base + 8 * c) : zero;
-        gq[i] = in && p.gate_token ? load_q(p.gate_token + base + 8 * c) : zero;
-    }
+    uint4 nq[kPer], hq[kPer], yq[kPer];
     F8 dh[kPer];
-    if (pre) {
-        float s0 = 0.f, s1 = 0.f;
+    const float4 st = p.stats[row];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = tid + i * kRow;
-            if (c < chunks) {
-                const F8 d = widen(nq[i]), h = widen(hq[i]), g = load_f8(p.pre_gamma + 8 * c);
+    for (int i = 0; i < kPer; ++i) nq[i] = pre && inside(i) ? load_q(p.dn + base + 8 * (tid + i * kRow)) : zero;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = d.v[e] * g.v[e];
-                    s0 += v * ((h.v[e] - st.z) * st.w);
-                    s1 += v;
-                }
-            }
-        }
-        const float2 s = row_sum<kRow>(s0, s1, red, 0);
-        const float m0 = s.x * inv, m1 = p.pre == ZB_NORM_LAYER ? s.y * inv : 0.f;
+    for (int i = 0; i < kPer; ++i) hq[i] = pre && inside(i) ? load_q(p.h + base + 8 * (tid + i * kRow)) : zero;
+    {
+        uint4 rq[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = tid + i * kRow;
-            dh[i] = widen(rq[i]);
-            if (c < chunks) {
-                const F8 d = widen(nq[i]), h = widen(hq[i]), g = load_f8(p.pre_gamma + 8 * c);
+        for (int i = 0; i < kPer; ++i) rq[i] = p.dres && inside(i) ? load_q(p.dres + base + 8 * (tid + i * kRow)) : zero;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dh[i].v[e] += st.w * (d.v[e] * g.v[e] - (h.v[e] - st.z) * st.w * m0 - m1);
-            }
-        }
-    } else {
+        for (int i = 0; i < kPer; ++i) yq[i] = p.y && inside(i) ? load_q(p.y + base + 8 * (tid + i * kRow)) : zero;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) dh[i] = widen(rq[i]);
     }
-    float s0 = 0.f, s1 = 0.f;
+    if (pre) {
+        const float shift = -st.z * st.w;
+        float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int c = tid + i * kRow;
-        if (c >= chunks) continue;
-        *reinterpret_cast<uint4*>(p.dh + base + 8 * c) = narrow(dh[i]);
-        if (p.dx) {
-            F8 dx;
+        for (int i = 0; i < kPer; ++i) {
+            if (!inside(i)) continue;
+            F8 d = widen(nq[i]), hat = widen(hq[i]);
+            times(d, load_f8(p.pre_gamma + 8 * (tid + i * kRow)));
+            affine(hat, st.w, shift);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx.v[e] = p.a * dh[i].v[e];
-            *reinterpret_cast<uint4*>(p.dx + base + 8 * c) = narrow(dx);
-        }
-        // dh becomes du, the gradient of what the gate multiplies (times the norm's weight)
-        const F8 y = widen(yq[i]);
-        F8 g{{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}};
-        if (post) g = load_f8(p.post_gamma + 8 * c);
-        if (p.dgate) {
-            F8 dg, b{};
-            if (p.post_beta) b = load_f8(p.post_beta + 8 * c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float u = post ? (y.v[e] - st.x) * st.y * g.v[e] + b.v[e] : y.v[e];
-                dg.v[e] = p.b * dh[i].v[e] * u;
+            for (int e = 0; e < 4; ++e) {
+                s0 = __ffma2_rn(d.p[e], hat.p[e], s0);
+                s1 = __fadd2_rn(s1, d.p[e]);
             }
-            *reinterpret_cast<uint4*>(p.dgate + base + 8 * c) = narrow(dg);
         }
-        if (p.gate_channel || p.gate_token) {
-            const F8 gate = p.gate_channel ? load_f8(p.gate_channel + 8 * c) : widen(gq[i]);
+        const float2 s = row_sum<kRow>(make_float2(s0.x + s0.y, s1.x + s1.y), red, 0);
+        const float m0 = -st.w * (s.x * inv), m1 = p.pre == ZB_NORM_LAYER ? -st.w * (s.y * inv) : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dh[i].v[e] *= gate.v[e];
-        }
+        for (int i = 0; i < kPer; ++i) {
+            if (!inside(i)) continue;
+            F8 d = widen(nq[i]), hat = widen(hq[i]);
+            times(d, load_f8(p.pre_gamma + 8 * (tid + i * kRow)));
+            affine(hat, st.w, shift);
+            affine(hat, m0, m1);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            dh[i].v[e] *= p.b * g.v[e];
-            s0 += dh[i].v[e] * ((y.v[e] - st.x) * st.y);
-            s1 += dh[i].v[e];
+            for (int e = 0; e < 4; ++e) dh[i].p[e] = __fadd2_rn(__ffma2_rn(d.p[e], both(st.w), hat.p[e]), dh[i].p[e]);
         }
     }
-    float m0 = 0.f, m1 = 0.f, rstd = 1.f;
+    const float shift = -st.x * st.y;
+    float2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (!inside(i)) continue;
+        const int at = 8 * (tid + i * kRow);
+        store_q(p.dh + base + at, narrow(dh[i]));
+        if (p.dx) {
+            F8 dx = dh[i];
+            affine(dx, p.a, 0.f);
+            store_q(p.dx + base + at, narrow(dx));
+        }
+        // dh becomes the gradient of what the gate multiplies, then of the normed y
+        affine(dh[i], p.b, 0.f);
+        if (p.dgate) {
+            F8 u = widen(yq[i]);
+            if (post) {
+                affine(u, st.y, shift);
+                weigh(u, p.post_gamma, p.post_beta, at);
+            }
+            times(u, dh[i]);
+            store_q(p.dgate + base + at, narrow(u));
+        }
+        if (p.gate_channel)
+            times(dh[i], load_f8(p.gate_channel + at));
+        else if (p.gate_token)
+            times(dh[i], widen(load_q(p.gate_token + base + at)));
+        if (post) {
+            times(dh[i], load_f8(p.post_gamma + at));
+            F8 hat = widen(yq[i]);
+            affine(hat, st.y, shift);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s0 = __ffma2_rn(dh[i].p[e], hat.p[e], s0);
+                s1 = __fadd2_rn(s1, dh[i].p[e]);
+            }
+        }
+    }
+    float m0 = 0.f, m1 = 0.f;
     if (post) {
-        const float2 s = row_sum<kRow>(s0, s1, red, 1);
-        m0 = s.x * inv;
-        m1 = p.post == ZB_NORM_LAYER ? s.y * inv : 0.f;
-        rstd = st.y;
+        const float2 s = row_sum<kRow>(make_float2(s0.x + s0.y, s1.x + s1.y), red, 1);
+        m0 = -st.y * (s.x * inv);
+        m1 = p.post == ZB_NORM_LAYER ? -st.y * (s.y * inv) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int c = tid + i * kRow;
-        if (c >= chunks) continue;
+        if (!inside(i)) continue;
         if (post) {
-            const F8 y = widen(yq[i]);
+            F8 hat = widen(yq[i]);
+            affine(hat, st.y, shift);
+            affine(hat, m0, m1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dh[i].v[e] = rstd * (dh[i].v[e] - (y.v[e] - st.x) * st.y * m0 - m1);
+            for (int e = 0; e < 4; ++e) dh[i].p[e] = __ffma2_rn(dh[i].p[e], both(st.y), hat.p[e]);
         }
-        *reinterpret_cast<uint4*>(p.dy + base + 8 * c) = narrow(dh[i]);
+        store_q(p.dy + base + 8 * (tid + i * kRow), narrow(dh[i]));
     }
 }
 
 // ---------------------------------------------------------------- weight gradients
 //
-// Four sums over the rows for every column: dn, dn hhat, gdh, gdh yhat, where gdh is dh
-// (times the gate per token) and yhat the normed y (y itself without a post norm).  A gate
-// per channel is a factor of the sums, so dgate and the post norm's gradients come from the
-// same two.  Two passes in a fixed order: parts of the rows ([parts][4][hidden]), then their sum.
+// Two pairs of sums over the rows for every column: dn and dn hhat; gdh and gdh yhat, where
+// gdh is dh (times the gate per token) and yhat the normed y (y itself without a post norm).
+// A gate per channel is a factor of the sums, so dgate and the post norm's gradients come
+// from the same two.  Two passes in a fixed order: sums over parts of the rows
+// ([parts][4][hidden]), then over the parts.
 
 constexpr int kWThreads = 256;
 constexpr int kWGroups = 8;
-constexpr int kWUnroll = 2;
-constexpr int kWTargetBlocks = 608;  // 4 blocks of 256 threads on each of 152 SMs
+constexpr int kWUnroll = 4;
+constexpr int kWTargetBlocks = 608;  // of each pair: 4 blocks of 256 threads on each of 152 SMs
 
 int norm_parts(int tokens, int hidden) {
     const int across = (hidden + 255) / 256;
     return std::max(1, std::min((kWTargetBlocks + across - 1) / across, (tokens + kWGroups - 1) / kWGroups));
 }
 
+// Block (x, y, z): columns 256 x ..., the y-th part of the rows, pair first + z.  Bound by HBM.
 __global__ void __launch_bounds__(kWThreads) residual_norm_parts_kernel(const __grid_constant__ NormParams p,
-                                                                        float* __restrict__ parts, int tokens, bool pre,
-                                                                        bool branch) {
-    __shared__ float sums[kWGroups][256];
+                                                                        float* __restrict__ parts, int tokens, int first) {
+    __shared__ float sums[2][kWGroups][256];
+    const bool branch = first + static_cast<int>(blockIdx.z) == 1;
     const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
     const int col = blockIdx.x * 256 + 8 * lane;
     const int per = (tokens + gridDim.y - 1) / gridDim.y;
     const int t0 = blockIdx.y * per, t1 = min(tokens, t0 + per);
-    const bool post = p.post != ZB_NORM_NONE;
-    float acc[4][8] = {};
+    const uint16_t* d_of = branch ? p.dh : p.dn;
+    const uint16_t* v_of = branch ? p.y : p.h;
+    const uint16_t* gate = branch ? p.gate_token : nullptr;
+    const bool normed = !branch || p.post != ZB_NORM_NONE;
+    F8 s0{}, s1{};
     if (col < p.hidden) {
         for (int tb = t0 + group; tb < t1; tb += kWGroups * kWUnroll) {
-            uint4 nq[kWUnroll], hq[kWUnroll], dq[kWUnroll], yq[kWUnroll], gq[kWUnroll];
-            float4 st[kWUnroll];
+            uint4 dq[kWUnroll], vq[kWUnroll], gq[kWUnroll];
+            float2 st[kWUnroll];  // mean, rstd
 #pragma unroll
             for (int i = 0; i < kWUnroll; ++i) {
                 const int t = tb + i * kWGroups;
+                dq[i] = vq[i] = gq[i] = make_uint4(0, 0, 0, 0);
+                st[i] = make_float2(0.f, 1.f);
                 if (t >= t1) continue;
                 const int64_t at = static_cast<int64_t>(t) * p.hidden + col;
-                st[i] = p.stats[t];
-                if (pre) {
-                    nq[i] = load_q(p.dn + at);
-                    hq[i] = load_q(p.h + at);
-                }
-                if (branch) {
-                    dq[i] = load_q(p.dh + at);
-                    yq[i] = load_q(p.y + at);
-                    if (p.gate_token) gq[i] = load_q(p.gate_token + at);
-                }
+                dq[i] = load_q(d_of + at);
+                vq[i] = load_q(v_of + at);
+                if (gate) gq[i] = load_q(gate + at);
+                if (normed) st[i] = reinterpret_cast<const float2*>(p.stats)[2 * static_cast<int64_t>(t) + (branch ? 0 : 1)];
             }
 #pragma unroll
             for (int i = 0; i < kWUnroll; ++i) {
-                if (tb + i * kWGroups >= t1) continue;
-                if (pre) {
-                    const F8 d = widen(nq[i]), h = widen(hq[i]);
+                F8 d = widen(dq[i]), hat = widen(vq[i]);
+                if (gate) times(d, widen(gq[i]));
+                affine(hat, st[i].y, -st[i].x * st[i].y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[0][e] += d.v[e];
-                        acc[1][e] += d.v[e] * ((h.v[e] - st[i].z) * st[i].w);
-                    }
-                }
-                if (branch) {
-                    F8 d = widen(dq[i]);
-                    const F8 y = widen(yq[i]);
-                    if (p.gate_token) {
-                        const F8 g = widen(gq[i]);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) d.v[e] *= g.v[e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[2][e] += d.v[e];
-                        acc[3][e] += d.v[e] * (post ? (y.v[e] - st[i].x) * st[i].y : y.v[e]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    s0.p[e] = __fadd2_rn(s0.p[e], d.p[e]);
+                    s1.p[e] = __ffma2_rn(d.p[e], hat.p[e], s1.p[e]);
                 }
             }
         }
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2*>(&sums[0][group][8 * lane + 2 * e]) = s0.p[e];
+        *reinterpret_cast<float2*>(&sums[1][group][8 * lane + 2 * e]) = s1.p[e];
+    }
+    __syncthreads();
     const int j = blockIdx.x * 256 + threadIdx.x;
-    float* out = parts + static_cast<int64_t>(blockIdx.y) * 4 * p.hidden;
+    if (j >= p.hidden) return;
+    float* out = parts + (static_cast<int64_t>(blockIdx.y) * 4 + (branch ? 2 : 0)) * p.hidden + j;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (k < 2 ? !pre : !branch) continue;
-        __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[group][8 * lane + e] = acc[k][e];
-        __syncthreads();
-        if (j < p.hidden) {
-            float s = 0.f;
-#pragma unroll
-            for (int g = 0; g < kWGroups; ++g) s += sums[g][threadIdx.x];
-            out[static_cast<int64_t>(k) * p.hidden + j] = s;
-        }
+        for (int g = 0; g < kWGroups; ++g) s += sums[k][g][threadIdx.x];
+        out[static_cast<int64_t>(k) * p.hidden] = s;
     }
 }
 
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(256) residual_norm_sum_kernel(const __grid_con
                                                                 const float* __restrict__ parts, int n_parts, bool pre,
                                                                 bool branch) {
     __shared__ float sums[4][8][32];
+    wait_for_previous();
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + c;
 #pragma unroll
@@ -514,38 +516,33 @@ zb_status norm_params(const zb_residual_norm* op, int32_t tokens, int32_t hidden
     return ZB_OK;
 }
 
-// Threads of a row: the fewest that hold it with four groups of 8 values each.
-template <template <int, int> class K>
+// Threads of a row: the fewest that hold it with four groups of 8 values each; kFull where it
+// fills them all.
+template <template <int, int, bool> class K>
 cudaError_t launch_rows(const NormParams& p, int tokens, cudaStream_t stream) {
     const int chunks = p.hidden / 8;
     const unsigned rows = static_cast<unsigned>(tokens), packed_rows = (rows + 3) / 4;
-    if (chunks <= 32)
-        K<32, 1>::get()<<<packed_rows, 128, 0, stream>>>(p, tokens);
-    else if (chunks <= 64)
-        K<32, 2>::get()<<<packed_rows, 128, 0, stream>>>(p, tokens);
-    else if (chunks <= 128)
-        K<32, 4>::get()<<<packed_rows, 128, 0, stream>>>(p, tokens);
-    else if (chunks <= 256)
-        K<64, 4>::get()<<<rows, 64, 0, stream>>>(p, tokens);
-    else if (chunks <= 512)
-        K<128, 4>::get()<<<rows, 128, 0, stream>>>(p, tokens);
-    else if (chunks <= 1024)
-        K<256, 4>::get()<<<rows, 256, 0, stream>>>(p, tokens);
-    else if (chunks <= 2048)
-        K<512, 4>::get()<<<rows, 512, 0, stream>>>(p, tokens);
-    else
-        K<1024, 4>::get()<<<rows, 1024, 0, stream>>>(p, tokens);
-    return cudaGetLastError();
+    auto go = [&](auto full, auto some, int most, unsigned grid, unsigned block) {
+        return launch_chained(chunks == most ? full : some, grid, block, 0, stream, p, tokens);
+    };
+    if (chunks <= 32) return go(K<32, 1, true>::get(), K<32, 1, false>::get(), 32, packed_rows, 128);
+    if (chunks <= 64) return go(K<32, 2, true>::get(), K<32, 2, false>::get(), 64, packed_rows, 128);
+    if (chunks <= 128) return go(K<32, 4, true>::get(), K<32, 4, false>::get(), 128, packed_rows, 128);
+    if (chunks <= 256) return go(K<64, 4, true>::get(), K<64, 4, false>::get(), 256, rows, 64);
+    if (chunks <= 512) return go(K<128, 4, true>::get(), K<128, 4, false>::get(), 512, rows, 128);
+    if (chunks <= 1024) return go(K<256, 4, true>::get(), K<256, 4, false>::get(), 1024, rows, 256);
+    if (chunks <= 2048) return go(K<512, 4, true>::get(), K<512, 4, false>::get(), 2048, rows, 512);
+    return go(K<1024, 4, true>::get(), K<1024, 4, false>::get(), 4096, rows, 1024);
 }
 
-template <int kRow, int kPer>
+template <int kRow, int kPer, bool kFull>
 struct ForwardKernel {
-    static auto get() { return residual_norm_forward_kernel<kRow, kPer>; }
+    static auto get() { return &residual_norm_forward_kernel<kRow, kPer, kFull>; }
 };
 
-template <int kRow, int kPer>
+template <int kRow, int kPer, bool kFull>
 struct BackwardKernel {
-    static auto get() { return residual_norm_backward_kernel<kRow, kPer>; }
+    static auto get() { return &residual_norm_backward_kernel<kRow, kPer, kFull>; }
 };
 
 }  // namespace
@@ -636,9 +633,10 @@ extern "C" zb_status zb_op_residual_norm_backward_weight(const zb_residual_norm*
     p.stats = reinterpret_cast<float4*>(const_cast<float*>(stats));
     const int parts = norm_parts(tokens, hidden);
     cudaStream_t s = as_stream(stream);
-    const dim3 grid((hidden + 255) / 256, parts);
-    residual_norm_parts_kernel<<<grid, kWThreads, 0, s>>>(p, static_cast<float*>(scratch), tokens, pre, branch);
+    const dim3 grid((hidden + 255) / 256, parts, pre && branch ? 2 : 1);
+    residual_norm_parts_kernel<<<grid, kWThreads, 0, s>>>(p, static_cast<float*>(scratch), tokens, pre ? 0 : 1);
+    ZB_TRY(cuda_status(cudaGetLastError()));
     const NormGrads out{dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, dgate};
-    residual_norm_sum_kernel<<<hidden / 32, 256, 0, s>>>(p, out, static_cast<const float*>(scratch), parts, pre, branch);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_chained(residual_norm_sum_kernel, static_cast<unsigned>(hidden / 32), 256, 0, s, p, out,
+                                      static_cast<const float*>(scratch), parts, pre, branch));
 }

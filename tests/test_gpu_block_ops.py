@@ -96,9 +96,12 @@ def test_forward(cuda_device, t, k, n, kind):
     assert torch.equal(y2, y)
     codes, scales = O.pack(take(z, t))
     assert np.array_equal(take_packed(z8, t)[0], codes) and np.array_equal(take_packed(z8, t)[1], scales)
-    # y may be the residual; nothing but y is asked for
+    # nothing but y is asked for (its sums are then taken in another order), and y may be the residual
+    y3 = out_rows(t, n)
+    zb.zb_op_linear_activation_forward(xd, wd, bias_dev, rd, y3, t, k, n, kind)
+    within(take(y3, t), a + res, bar, "y alone")
     zb.zb_op_linear_activation_forward(xd, wd, bias_dev, rd, rd, t, k, n, kind)
-    assert torch.equal(rd, y[:t])
+    assert torch.equal(rd, y3[:t])
     no_waits_ran_out()
 
 
