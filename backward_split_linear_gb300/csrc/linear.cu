@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "chained.cuh"
 #include "checkpoint.cuh"
 #include "checks.h"
 #include "device_common.cuh"
@@ -45,9 +46,11 @@ constexpr size_t kLinSmem = 1024 + kLinStages * 2 * kLinOperand + kLinEpiWarps *
 static_assert(kLinSmem <= 232448, "shared memory");
 // Registers a thread: 384 x 168 at launch, of which 128 x 64 + 256 x 216 are used.
 constexpr int kLinFewRegs = 64, kLinManyRegs = 216;
-constexpr int kLinSumBlocks = 8;  // k blocks (512 terms) that stay in tensor memory
-// Twice as many in a tile's first two accumulators where others follow: while the epilogue
-// warps work on the tile before, the MMAs get that far and no further.
+// k blocks (of 64 terms) that stay in tensor memory at a time.  8 where the results are float32;
+// twice as many in a tile's first two accumulators where enough others follow: while the
+// epilogue warps work on the tile before, the MMAs get that far and no further.  F's 8-bit
+// codes only need what float32 arithmetic would give them, and take 16.
+constexpr int kLinSumBlocks = 8;
 constexpr int kLinFirstSums = 48;  // from so many k blocks on
 
 enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
@@ -58,6 +61,7 @@ struct LinParams {
     // tiles from narrow_from on (a short last wave) are two units of 128 columns each
     int narrow_from, num_units;
     int act;
+    bool wide;                 // z, residual and codes start at 32-byte boundaries
     const float* bias;         // F: [n] or NULL
     const uint16_t* residual;  // F: [m, n] or NULL
     uint16_t* z;               // F: written, B: read; [m, n] or NULL
@@ -272,6 +276,31 @@ __device__ __forceinline__ void words_to_box(uint32_t box, int lane, const uint3
         st_shared_v4(row + ((j ^ sw) << 4), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
 }
 
+// 32 bytes of a row, a whole sector in one access where the tensor starts at one (`wide`).
+// In two of 16 every sector went to L2 twice: 348 against XXX us for an 8B-shaped layer with z and y in 8 bits.
+__device__ __forceinline__ void store_sector(void* p, bool wide, const uint4& a, const uint4& b) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                     "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = a;
+        static_cast<uint4*>(p)[1] = b;
+    }
+}
+
+__device__ __forceinline__ void load_sector(const void* p, bool wide, uint4& a, uint4& b) {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p)
+                     : "memory");
+    } else {
+        a = static_cast<const uint4*>(p)[0];
+        b = static_cast<const uint4*>(p)[1];
+    }
+}
+
 // Scale bytes of consecutive 32-column blocks leave two at a time: a row of n / 32 bytes
 // keeps no more than 2-byte alignment (n is a multiple of 64, so blocks come in pairs).
 struct ScalePair {
@@ -294,8 +323,8 @@ __device__ __forceinline__ void forward_chunk(const LinParams& p, LinRow& row, f
     const int64_t at = static_cast<int64_t>(m) * p.n + n;
     uint4 res[4];
     if (p.residual && ok) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) res[j] = reinterpret_cast<const uint4*>(p.residual + at)[j];
+        load_sector(p.residual + at, p.wide, res[0], res[1]);
+        load_sector(p.residual + at + 16, p.wide, res[2], res[3]);
     }
     if (p.bias) {
 #pragma unroll
@@ -315,17 +344,15 @@ __device__ __forceinline__ void forward_chunk(const LinParams& p, LinRow& row, f
         if (p.z) {
             if (ok) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<uint4*>(p.z + at)[j] = make_uint4(zw[4 * j], zw[4 * j + 1], zw[4 * j + 2], zw[4 * j + 3]);
+                for (int j = 0; j < 2; ++j)
+                    store_sector(p.z + at + 16 * j, p.wide, make_uint4(zw[8 * j], zw[8 * j + 1], zw[8 * j + 2], zw[8 * j + 3]),
+                                 make_uint4(zw[8 * j + 4], zw[8 * j + 5], zw[8 * j + 6], zw[8 * j + 7]));
             }
         }
         if (p.z_codes) {
             uint4 lo, hi;
             const uint32_t scale = pack_block(zw, lo, hi);
-            if (ok) {
-                reinterpret_cast<uint4*>(p.z_codes + at)[0] = lo;
-                reinterpret_cast<uint4*>(p.z_codes + at)[1] = hi;
-            }
+            if (ok) store_sector(p.z_codes + at, p.wide, lo, hi);
             row.z.put(p.z_scales, at >> 5, c, scale, ok);
         }
     }
@@ -345,10 +372,7 @@ __device__ __forceinline__ void forward_chunk(const LinParams& p, LinRow& row, f
     if (p.y_codes) {
         uint4 lo, hi;
         const uint32_t scale = pack_block(yw, lo, hi);
-        if (ok) {
-            reinterpret_cast<uint4*>(p.y_codes + at)[0] = lo;
-            reinterpret_cast<uint4*>(p.y_codes + at)[1] = hi;
-        }
+        if (ok) store_sector(p.y_codes + at, p.wide, lo, hi);
         row.y.put(p.y_scales, at >> 5, c, scale, ok);
     }
 }
@@ -362,12 +386,11 @@ struct ZWords {
 __device__ __forceinline__ void load_z(const LinParams& p, int64_t at, bool ok, ZWords& z) {
     if (!ok || p.act == ZB_ACT_NONE) return;
     if (p.z_codes) {
-        z.w[0] = reinterpret_cast<const uint4*>(p.z_codes + at)[0];
-        z.w[1] = reinterpret_cast<const uint4*>(p.z_codes + at)[1];
+        load_sector(p.z_codes + at, p.wide, z.w[0], z.w[1]);
         z.scale = p.z_scales[at >> 5];
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z.w[j] = reinterpret_cast<const uint4*>(p.z + at)[j];
+        load_sector(p.z + at, p.wide, z.w[0], z.w[1]);
+        load_sector(p.z + at + 16, p.wide, z.w[2], z.w[3]);
     }
 }
 
@@ -463,6 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     // k blocks of the accumulator that starts at block kc
     auto chunk_at = [&](int kc) {
         if (!kSums) return p.k_blocks;
+        if (EPI == kLinForward) return 2 * kLinSumBlocks;
         return p.k_blocks >= kLinFirstSums && kc < 4 * kLinSumBlocks ? 2 * kLinSumBlocks : kLinSumBlocks;
     };
 
@@ -674,6 +698,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     }
                     ++n_stored;
                 };
+                // the bias's 128 bytes of each chunk into L1, ahead of the loads that every lane makes
+                if constexpr (EPI == kLinForward) {
+                    if (p.bias && 32 * lane < cols && n_base + 32 * lane < p.n)
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + n_base + 32 * lane));
+                }
                 auto z_of = [&](int c) {
                     ZWords zw{};
                     if constexpr (EPI == kLinActivationBackward) {
@@ -684,6 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 };
                 if constexpr (kSums) {
                     float sum[4][32];
+                    ZWords zw = z_of(0);  // always one chunk ahead of its use
                     for (int kc = 0; alive && kc < p.k_blocks; kc += chunk_at(kc)) {
                         if (!acquire()) break;
                         const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
@@ -698,7 +728,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                     for (int i = 0; i < 32; ++i) sum[c][i] = __uint_as_float(r[i]);
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
+                                    for (int i = 0; i < 32; i += 2) {
+                                        const float2 t = __fadd2_rn(make_float2(sum[c][i], sum[c][i + 1]),
+                                                                    make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+                                        sum[c][i] = t.x;
+                                        sum[c][i + 1] = t.y;
+                                    }
                                 }
                             }
                         }
@@ -714,8 +749,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         // two copies of the long code rather than four: the sums move down
 #pragma unroll 1
                         for (int c = 0; 32 * c < cols; c += 2) {
-                            finish(sum[0], z_of(c), c);
-                            finish(sum[1], z_of(c + 1), c + 1);
+                            const ZWords next = z_of(c + 1);
+                            finish(sum[0], zw, c);
+                            if (32 * (c + 2) < cols) zw = z_of(c + 2);
+                            finish(sum[1], next, c + 1);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 sum[0][i] = sum[2][i];
@@ -724,11 +761,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         }
                     }
                 } else {
+                    ZWords zw = z_of(0);  // always one chunk ahead of its use
                     if (!acquire()) break;
                     const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
 #pragma unroll 1
                     for (int c = 0; 32 * c < cols; ++c) {
-                        const ZWords zw = z_of(c);
+                        const ZWords now = zw;
+                        if (32 * (c + 1) < cols) zw = z_of(c + 1);
                         uint32_t r[32];
                         tmem_load_32(t0 + 32u * c, r);
                         tmem_wait_load();
@@ -736,7 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                        finish(v, zw, c);
+                        finish(v, now, c);
                     }
                 }
             }
@@ -812,15 +851,16 @@ __global__ void __launch_bounds__(kColThreads) column_parts_kernel(const uint16_
 // A block finishes 32 columns: thread (c, g) adds the parts g, g + 8, ... of column c.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ parts, float* out, int n_parts, int width) {
     __shared__ float sums[8][32];
+    wait_for_previous();
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + c;
     float s = 0.f;
-    for (int q0 = g; q0 < n_parts; q0 += 64) {
-        float v[8];
+    for (int q0 = g; q0 < n_parts; q0 += 128) {
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = q0 + 8 * i < n_parts ? parts[static_cast<int64_t>(q0 + 8 * i) * width + j] : 0.f;
+        for (int i = 0; i < 16; ++i) v[i] = q0 + 8 * i < n_parts ? parts[static_cast<int64_t>(q0 + 8 * i) * width + j] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[i];
+        for (int i = 0; i < 16; ++i) s += v[i];
     }
     sums[g][c] = s;
     __syncthreads();
@@ -832,8 +872,8 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
     }
 }
 
-void launch_column_sum(const float* parts, float* out, int n_parts, int width, cudaStream_t stream) {
-    column_sum_kernel<<<width / 32, 256, 0, stream>>>(parts, out, n_parts, width);  // width is a multiple of 64
+cudaError_t launch_column_sum(const float* parts, float* out, int n_parts, int width, cudaStream_t stream) {
+    return launch_chained(column_sum_kernel, static_cast<unsigned>(width / 32), 256, 0, stream, parts, out, n_parts, width);
 }
 
 // ---------------------------------------------------------------- the activation alone
@@ -898,6 +938,9 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     if (!ok) return cudaErrorInvalidValue;
     p.status = status_word();
     if (!p.status) return cudaErrorInvalidDevice;
+    const uintptr_t starts = reinterpret_cast<uintptr_t>(p.residual) | reinterpret_cast<uintptr_t>(p.z) |
+                             reinterpret_cast<uintptr_t>(p.z_codes) | reinterpret_cast<uintptr_t>(p.y_codes);
+    p.wide = starts % 32 == 0;
 
     auto kern = linear_kernel<A_MN, B_MN, EPI, kSums>;
     static std::mutex mu;
@@ -1014,8 +1057,7 @@ extern "C" zb_status zb_op_backward_input_activation(const void* dy, const void*
     if (!dbias) return cuda_status(launch_linear<false, true, kLinActivationBackward, false>(dy, w, dz, p, out_features, s));
     p.col_sums = static_cast<float*>(scratch);
     ZB_TRY(cuda_status(launch_linear<false, true, kLinActivationBackward, true>(dy, w, dz, p, out_features, s)));
-    launch_column_sum(p.col_sums, dbias, (tokens + 31) / 32, in_features, s);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_column_sum(p.col_sums, dbias, (tokens + 31) / 32, in_features, s));
 }
 
 extern "C" zb_status zb_op_activation_backward(const void* dy, const void* z, const zb_checkpoint* z_packed, void* dz,
@@ -1057,8 +1099,8 @@ extern "C" zb_status zb_op_backward_bias(const void* dy, float* dbias, int32_t t
     const dim3 grid((out_features + 255) / 256, parts);
     column_parts_kernel<<<grid, kColThreads, 0, s>>>(static_cast<const uint16_t*>(dy), static_cast<float*>(scratch), tokens,
                                                      out_features);
-    launch_column_sum(static_cast<const float*>(scratch), dbias, parts, out_features, s);
-    return cuda_status(cudaGetLastError());
+    ZB_TRY(cuda_status(cudaGetLastError()));
+    return cuda_status(launch_column_sum(static_cast<const float*>(scratch), dbias, parts, out_features, s));
 }
 
 extern "C" size_t zb_op_backward_weight_checkpoint_scratch_bytes(int32_t tokens, int32_t in_features) {

@@ -59,7 +59,12 @@ __device__ __forceinline__ F8 load_f8(const float* p) {
     return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
-__device__ __forceinline__ uint4 load_q(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+// A row's data pass by L1, which keeps the parameters that every row reads.
+__device__ __forceinline__ uint4 load_q(const uint16_t* p) {
+    uint4 q;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p));
+    return q;
+}
 __device__ __forceinline__ void store_q(uint16_t* p, const uint4& q) { *reinterpret_cast<uint4*>(p) = q; }
 
 // v * scale + shift of the normed value: scale = rstd, shift = -mean rstd, one rounding.
@@ -371,7 +376,8 @@ int norm_parts(int tokens, int hidden) {
 }
 
 // Block (x, y, z): columns 256 x ..., the y-th part of the rows, pair first + z.  Bound by HBM.
-__global__ void __launch_bounds__(kWThreads) residual_norm_parts_kernel(const __grid_constant__ NormParams p,
+template <bool kTokenGate>
+__global__ void __launch_bounds__(kWThreads, kTokenGate ? 3 : 4) residual_norm_parts_kernel(const __grid_constant__ NormParams p,
                                                                         float* __restrict__ parts, int tokens, int first) {
     __shared__ float sums[2][kWGroups][256];
     const bool branch = first + static_cast<int>(blockIdx.z) == 1;
@@ -381,29 +387,32 @@ __global__ void __launch_bounds__(kWThreads) residual_norm_parts_kernel(const __
     const int t0 = blockIdx.y * per, t1 = min(tokens, t0 + per);
     const uint16_t* d_of = branch ? p.dh : p.dn;
     const uint16_t* v_of = branch ? p.y : p.h;
-    const uint16_t* gate = branch ? p.gate_token : nullptr;
+    const uint16_t* gate = kTokenGate && branch ? p.gate_token : nullptr;
     const bool normed = !branch || p.post != ZB_NORM_NONE;
     F8 s0{}, s1{};
     if (col < p.hidden) {
         for (int tb = t0 + group; tb < t1; tb += kWGroups * kWUnroll) {
-            uint4 dq[kWUnroll], vq[kWUnroll], gq[kWUnroll];
+            uint4 dq[kWUnroll], vq[kWUnroll], gq[kTokenGate ? kWUnroll : 1];
             float2 st[kWUnroll];  // mean, rstd
 #pragma unroll
             for (int i = 0; i < kWUnroll; ++i) {
                 const int t = tb + i * kWGroups;
-                dq[i] = vq[i] = gq[i] = make_uint4(0, 0, 0, 0);
+                dq[i] = vq[i] = make_uint4(0, 0, 0, 0);
+                if constexpr (kTokenGate) gq[i] = dq[i];
                 st[i] = make_float2(0.f, 1.f);
                 if (t >= t1) continue;
                 const int64_t at = static_cast<int64_t>(t) * p.hidden + col;
                 dq[i] = load_q(d_of + at);
                 vq[i] = load_q(v_of + at);
-                if (gate) gq[i] = load_q(gate + at);
+                if constexpr (kTokenGate)
+                    if (gate) gq[i] = load_q(gate + at);
                 if (normed) st[i] = reinterpret_cast<const float2*>(p.stats)[2 * static_cast<int64_t>(t) + (branch ? 0 : 1)];
             }
 #pragma unroll
             for (int i = 0; i < kWUnroll; ++i) {
                 F8 d = widen(dq[i]), hat = widen(vq[i]);
-                if (gate) times(d, widen(gq[i]));
+                if constexpr (kTokenGate)
+                    if (gate) times(d, widen(gq[i]));
                 affine(hat, st[i].y, -st[i].x * st[i].y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -435,29 +444,28 @@ struct NormGrads {
     float *post_gamma, *post_beta, *pre_gamma, *pre_beta, *gate;
 };
 
-__global__ void __launch_bounds__(256) residual_norm_sum_kernel(const __grid_constant__ NormParams p, const NormGrads out,
-                                                                const float* __restrict__ parts, int n_parts, bool pre,
-                                                                bool branch) {
+// A block finishes 32 columns: warp (k, g) adds the parts g, g + 8, ... of sum k.
+__global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const __grid_constant__ NormParams p, const NormGrads out,
+                                                                 const float* __restrict__ parts, int n_parts, bool pre,
+                                                                 bool branch) {
     __shared__ float sums[4][8][32];
     wait_for_previous();
-    const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int c = threadIdx.x & 31, k0 = (threadIdx.x >> 5) & 3, g = threadIdx.x >> 7;
     const int j = blockIdx.x * 32 + c;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (k < 2 ? !pre : !branch) continue;
+    if (k0 < 2 ? pre : branch) {
         float s = 0.f;
         for (int q0 = g; q0 < n_parts; q0 += 64) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = q0 + 8 * i < n_parts ? parts[(static_cast<int64_t>(q0 + 8 * i) * 4 + k) * p.hidden + j] : 0.f;
+                v[i] = q0 + 8 * i < n_parts ? parts[(static_cast<int64_t>(q0 + 8 * i) * 4 + k0) * p.hidden + j] : 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += v[i];
         }
-        sums[k][g][c] = s;
+        sums[k0][g][c] = s;
     }
     __syncthreads();
-    if (g != 0) return;
+    if (threadIdx.x >= 32) return;
     float t[4] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -634,9 +642,10 @@ extern "C" zb_status zb_op_residual_norm_backward_weight(const zb_residual_norm*
     const int parts = norm_parts(tokens, hidden);
     cudaStream_t s = as_stream(stream);
     const dim3 grid((hidden + 255) / 256, parts, pre && branch ? 2 : 1);
-    residual_norm_parts_kernel<<<grid, kWThreads, 0, s>>>(p, static_cast<float*>(scratch), tokens, pre ? 0 : 1);
+    auto kern = p.gate_token ? residual_norm_parts_kernel<true> : residual_norm_parts_kernel<false>;
+    kern<<<grid, kWThreads, 0, s>>>(p, static_cast<float*>(scratch), tokens, pre ? 0 : 1);
     ZB_TRY(cuda_status(cudaGetLastError()));
     const NormGrads out{dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, dgate};
-    return cuda_status(launch_chained(residual_norm_sum_kernel, static_cast<unsigned>(hidden / 32), 256, 0, s, p, out,
+    return cuda_status(launch_chained(residual_norm_sum_kernel, static_cast<unsigned>(hidden / 32), 1024, 0, s, p, out,
                                       static_cast<const float*>(scratch), parts, pre, branch));
 }
