@@ -23,14 +23,15 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t* __re
     uint32_t top2 = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top2 = pack_top2(top2, w[e]);
-    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    uint32_t top = pack_top(top2);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     if (i >= halves) return;
     const uint32_t scale = pack_scale(top);
     const uint32_t f = pack_factor(scale);
     uint32_t c[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = scale == kPackNotFinite ? 0u : pack_codes(w[2 * e], w[2 * e + 1], f);
+    for (int e = 0; e < 4; ++e)
+        c[e] = top < kPackLargest ? pack_codes(w[2 * e], w[2 * e + 1], f) : pack_codes_slow(w[2 * e], w[2 * e + 1], f, scale);
     reinterpret_cast<uint4*>(codes)[i] = make_uint4(c[0], c[1], c[2], c[3]);
     if ((threadIdx.x & 1) == 0) scales[i >> 1] = static_cast<uint8_t>(scale);
 }

@@ -6,7 +6,7 @@
 
 namespace zbk {
 
-// Row-major matrix of `rows` x `cols` with row stride `ld` elements (bf16 or float32), in
+// Row-major matrix of `rows` x `cols` with row stride `ld` elements (bf16, float32 or bytes), in
 // boxes of box_cols x box_rows; zero fill out of range on loads, no writes there on stores.
 bool gemm_encode_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld, uint32_t box_cols,
                      uint32_t box_rows, CUtensorMapSwizzle swizzle, CUtensorMapDataType dtype);

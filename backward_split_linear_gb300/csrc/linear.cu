@@ -15,7 +15,7 @@
 // zero: over 4096 terms a sum of products comes out 4e-6 short, over 16384 1.9e-5 (measured
 // against float64), where float32 sums that round to nearest stay below 1e-6.  bf16 results do not
 // show that, float32 gradients do.  So where results are float32 sums (W, and B with a bias gradient) an
-// accumulator only holds 512 terms: the epilogue warps then add it to sums in their
+// accumulator holds few terms: the epilogue warps then add it to sums in their
 // registers, while the MMAs fill the other accumulator.
 #include <algorithm>
 #include <mutex>
@@ -32,6 +32,7 @@ namespace zbk {
 namespace {
 
 constexpr int kLinThreads = 384;
+constexpr int kLinFirstWarps = 4;  // loads, MMAs, two idle
 constexpr int kLinEpiWarps = 8;
 constexpr int kLinStages = 6;
 constexpr int kLinTile = 256;  // rows and columns of a pair's tile
@@ -39,21 +40,32 @@ constexpr int kLinHalf = 128;  // rows (A) and columns (B) that each CTA loads
 constexpr int kLinBK = 64;
 constexpr uint32_t kLinOperand = kLinHalf * kLinBK * 2;  // 16 KiB
 constexpr uint32_t kLinMnBlock = 64 * kLinBK * 2;        // a 64-wide block of an MN-major tile
-constexpr uint32_t kLinBox = 4096;                       // staging per epilogue warp
+constexpr uint32_t kLinStaging = 32768;                  // of all epilogue warps
 constexpr uint32_t kLinTmemCols = 512;
-constexpr int kLinBars = 2 * kLinStages + 5;
-constexpr size_t kLinSmem = 1024 + kLinStages * 2 * kLinOperand + kLinEpiWarps * kLinBox + kLinBars * 8 + 16;
+constexpr int kLinBars = 2 * kLinStages + 5 + 2 * kLinEpiWarps;
+constexpr size_t kLinSmem = 1024 + kLinStages * 2 * kLinOperand + kLinStaging + kLinBars * 8 + 16;
 static_assert(kLinSmem <= 232448, "shared memory");
 // Registers a thread: 384 x 168 at launch, of which 128 x 64 + 256 x 216 are used.
 constexpr int kLinFewRegs = 64, kLinManyRegs = 216;
-// k blocks (of 64 terms) that stay in tensor memory at a time.  8 where the results are float32;
-// twice as many in a tile's first two accumulators where enough others follow: while the
-// epilogue warps work on the tile before, the MMAs get that far and no further.  F's 8-bit
-// codes only need what float32 arithmetic would give them, and take 16.
-constexpr int kLinSumBlocks = 8;
-constexpr int kLinFirstSums = 48;  // from so many k blocks on
 
 enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
+
+// k blocks (of 64 terms) that stay in tensor memory at a time: 8 where the results are
+// float32, 12 for F's 8-bit codes, which only need what float32 arithmetic would give them.
+// Where the epilogue is long, a tile's first two accumulators hold more: while its warps
+// work on the tile before, the MMAs get that far and no further.  8B-shaped, gelu, z in 8 bits, K = 4096: B
+// with a bias gradient 307 us with 8 throughout, XXX with 18 (its float32 sum is then 8.9e-7 off, one in
+// float32 arithmetic 6.2e-7), 300 with 20 (1.0e-6).
+template <int EPI>
+__host__ __device__ constexpr int lin_sum_blocks() {
+    return EPI == kLinForward ? 12 : 8;
+}
+template <int EPI>
+__device__ __forceinline__ int lin_first_blocks(int k_blocks) {
+    if (EPI == kLinForward) return max(lin_sum_blocks<EPI>(), min(16, k_blocks / 2));
+    if (EPI == kLinActivationBackward) return max(lin_sum_blocks<EPI>(), min(18, k_blocks / 3));
+    return lin_sum_blocks<EPI>();
+}
 
 struct LinParams {
     int m, n, k_blocks;
@@ -383,30 +395,36 @@ struct ZWords {
     uint32_t scale;
 };
 
-__device__ __forceinline__ void load_z(const LinParams& p, int64_t at, bool ok, ZWords& z) {
-    if (!ok || p.act == ZB_ACT_NONE) return;
-    if (p.z_codes) {
-        load_sector(p.z_codes + at, p.wide, z.w[0], z.w[1]);
-        z.scale = p.z_scales[at >> 5];
+// A lane's row of a box of z, as TMA loaded it: 64 bytes in the 64-byte swizzle, or 32 of codes.
+__device__ __forceinline__ void box_to_z(uint32_t box, int lane, bool packed, ZWords& z) {
+    const uint32_t l = static_cast<uint32_t>(lane);
+    if (packed) {
+        z.w[0] = ld_shared_v4(box + 32u * l);
+        z.w[1] = ld_shared_v4(box + 32u * l + 16u);
     } else {
-        load_sector(p.z + at, p.wide, z.w[0], z.w[1]);
-        load_sector(p.z + at + 16, p.wide, z.w[2], z.w[3]);
+        const uint32_t sw = (l >> 1) & 3u;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) z.w[j] = ld_shared_v4(box + 64u * l + ((j ^ sw) << 4));
     }
 }
 
-__device__ __forceinline__ void z_values(const LinParams& p, const ZWords& z, float (&v)[32]) {
-    if (p.z_codes) {
+// d[i] *= act'(z[i]), four words' values at a time
+template <int kAct>
+__device__ __forceinline__ void slopes_of(const ZWords& z, bool packed, float (&d)[32]) {
+    auto pair = [&](int i, uint32_t w) {
+        const float2 y = __fmul2_rn(make_float2(d[i], d[i + 1]), act_slope<kAct>(make_float2(bf16_lo(w), bf16_hi(w))));
+        d[i] = y.x;
+        d[i + 1] = y.y;
+    };
+    if (packed) {
         const uint32_t unit = unpack_unit(z.scale);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t w[4] = {z.w[j].x, z.w[j].y, z.w[j].z, z.w[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = unpack_pair<0>(w[e], unit), hi = unpack_pair<1>(w[e], unit);
-                v[16 * j + 4 * e] = bf16_lo(lo);
-                v[16 * j + 4 * e + 1] = bf16_hi(lo);
-                v[16 * j + 4 * e + 2] = bf16_lo(hi);
-                v[16 * j + 4 * e + 3] = bf16_hi(hi);
+                pair(16 * j + 4 * e, unpack_pair<0>(w[e], unit));
+                pair(16 * j + 4 * e + 2, unpack_pair<1>(w[e], unit));
             }
         }
     } else {
@@ -414,11 +432,19 @@ __device__ __forceinline__ void z_values(const LinParams& p, const ZWords& z, fl
         for (int j = 0; j < 4; ++j) {
             const uint32_t w[4] = {z.w[j].x, z.w[j].y, z.w[j].z, z.w[j].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[8 * j + 2 * e] = bf16_lo(w[e]);
-                v[8 * j + 2 * e + 1] = bf16_hi(w[e]);
-            }
+            for (int e = 0; e < 4; ++e) pair(8 * j + 2 * e, w[e]);
         }
+    }
+}
+
+__device__ __forceinline__ void slopes(int act, const ZWords& z, bool packed, float (&d)[32]) {
+    switch (act) {
+        case ZB_ACT_RELU: slopes_of<ZB_ACT_RELU>(z, packed, d); break;
+        case ZB_ACT_GELU: slopes_of<ZB_ACT_GELU>(z, packed, d); break;
+        case ZB_ACT_GELU_TANH: slopes_of<ZB_ACT_GELU_TANH>(z, packed, d); break;
+        case ZB_ACT_SILU: slopes_of<ZB_ACT_SILU>(z, packed, d); break;
+        case ZB_ACT_RELU2: slopes_of<ZB_ACT_RELU2>(z, packed, d); break;
+        default: break;
     }
 }
 
@@ -438,43 +464,39 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
     return v[0];
 }
 
-// B.  `v` is the product on entry; leaves dz's words in `dw` and adds its columns up.
-__device__ __forceinline__ void backward_chunk(const LinParams& p, float (&v)[32], const ZWords& zw, int m, int n, int row0,
-                                               int lane, bool ok, uint32_t (&dw)[16]) {
-    if (p.act != ZB_ACT_NONE) {
-        float z[32];
-        z_values(p, zw, z);
-        act_slopes(p.act, v, z);
-    }
-    to_words(v, dw);
-    if (p.col_sums) {
-        if (!ok) {
+// B's column sums of a chunk of dz.
+__device__ __forceinline__ void add_columns(const LinParams& p, float (&v)[32], int n, int row0, int lane, bool ok) {
+    if (!ok) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        const float s = column_sums(v, lane);
-        p.col_sums[static_cast<int64_t>(row0 >> 5) * p.n + n + lane] = s;
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
     }
+    p.col_sums[static_cast<int64_t>(row0 >> 5) * p.n + n + lane] = column_sums(v, lane);
 }
 
 // ---------------------------------------------------------------- kernel
 
-// kSums: the accumulators are added up in registers every kLinSumBlocks k blocks.
+// kSums: the accumulators are added up in registers every few k blocks (lin_sum_blocks).
 template <bool A_MN, bool B_MN, int EPI, bool kSums>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinParams p) {
+                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
+                  const __grid_constant__ LinParams p) {
+    constexpr int kChunks = 4;  // 32-column chunks of a warp in a whole tile
+    constexpr uint32_t kBox = kLinStaging / kLinEpiWarps;
+    constexpr uint32_t kOutBox = EPI == kLinAccumulate ? 4096 : 2048;
+    constexpr int kBoxes = kBox / kOutBox;    // used in turn
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t s_a = base, s_b = base + kLinStages * kLinOperand;
     const uint32_t s_out = s_b + kLinStages * kLinOperand;
-    const uint32_t bars = s_out + kLinEpiWarps * kLinBox;
+    const uint32_t bars = s_out + kLinStaging;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (kLinStages + s); };
     auto tfull_bar = [&](int a) { return bars + 8u * (2 * kLinStages + a); };
     auto tempty_bar = [&](int a) { return bars + 8u * (2 * kLinStages + 2 + a); };
     const uint32_t drain_bar = bars + 8u * (2 * kLinStages + 4);
+    const uint32_t side_bars = drain_bar + 8u;  // B: two of each epilogue warp, for its boxes of z
     const uint32_t tmem_slot = bars + 8u * kLinBars;
     volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - raw));
 
@@ -486,8 +508,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     // k blocks of the accumulator that starts at block kc
     auto chunk_at = [&](int kc) {
         if (!kSums) return p.k_blocks;
-        if (EPI == kLinForward) return 2 * kLinSumBlocks;
-        return p.k_blocks >= kLinFirstSums && kc < 4 * kLinSumBlocks ? 2 * kLinSumBlocks : kLinSumBlocks;
+        const int first = lin_first_blocks<EPI>(p.k_blocks);
+        return kc < 2 * first ? first : lin_sum_blocks<EPI>();
     };
 
     if (threadIdx.x == 0) {
@@ -500,6 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             mbar_init(tempty_bar(a), 2 * kLinEpiWarps);  // one lane of each epilogue warp of the pair
         }
         mbar_init(drain_bar, 1);
+        for (int i = 0; i < 2 * kLinEpiWarps; ++i) mbar_init(side_bars + 8u * i, 1);
         mbar_fence_init();
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
@@ -514,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     const bool usable = peer_base == tmem_base;  // both CTAs must hold the accumulators at the same columns
     if (!usable && threadIdx.x == 0) atomicCAS(status, 0, kSitePairTmem);
 
-    if (warp < 4) {
+    if (warp < kLinFirstWarps) {
         registers_release<kLinFewRegs>();
         if (usable && warp == 0) {
             if (lane == 0) {
@@ -626,10 +649,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         registers_claim<kLinManyRegs>();
         if (usable) {
             // ---------------- epilogue (both CTAs)
-            const int q = warp & 3, half = (warp - 4) >> 2;
-            const uint32_t box0 = s_out + static_cast<uint32_t>(warp - 4) * kLinBox;
+            const int q = warp & 3, half = (warp - kLinFirstWarps) >> 2;
+            const int warp_at = warp - kLinFirstWarps;
+            const uint32_t box0 = s_out + static_cast<uint32_t>(warp_at) * kBox;
             const uint32_t tlane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
             uint32_t n_stored = 0, it = 0;
+            uint32_t asked = 0, done = 0;  // boxes of z requested (lane 0) and used
             bool alive = true;
             auto acquire = [&]() {  // one verdict per warp: the tensor-memory loads are warp-wide
                 alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(it & 1u), (it >> 1) & 1u, status, kSiteEpiTmemFull));
@@ -648,43 +673,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 }
                 ++it;
             };
+            // B's z comes by TMA into the box that dz leaves from, one chunk ahead: loads into
+            // registers waited for the memory although their results were not used yet (a warp
+            // has six scoreboards, and the activations take them all).
+            const bool reads_z = EPI == kLinActivationBackward && p.act != ZB_ACT_NONE;
+            auto row0_of = [&](int tm) { return tm * kLinTile + static_cast<int>(rank) * kLinHalf + q * 32; };
+            auto ask_z = [&](int n, int row0) {
+                const uint32_t bar = side_bars + 8u * (2 * warp_at + (asked & 1u));
+                mbar_arrive_expect_tx(bar, p.z_codes ? 1024u : 2048u);
+                tma_load_2d(box0 + (asked & 1u) * kOutBox, &map_z, bar, n, row0);
+                ++asked;
+            };
+            auto columns_of = [&](const LinUnit& w, int tn) {  // a warp's first column
+                return tn * kLinTile + (w.narrow ? w.half * kLinHalf + half * (kLinHalf / 2) : half * kLinHalf);
+            };
+            LinUnit next = lin_unit(p, pair);
+            int next_tm, next_tn;
+            lin_tile(p, next.tile, next_tm, next_tn);
+            if (reads_z && lane == 0) ask_z(columns_of(next, next_tn), row0_of(next_tm));
             for (int u = pair; alive && u < p.num_units; u += npairs) {
-                const LinUnit w = lin_unit(p, u);
-                int tm, tn;
-                lin_tile(p, w.tile, tm, tn);
-                const int row0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf + q * 32;  // first of this warp's rows
+                const LinUnit w = next;
+                const int tm = next_tm, tn = next_tn;
+                // the next unit's divisions while this one's MMAs run
+                next = lin_unit(p, min(u + npairs, p.num_units - 1));
+                lin_tile(p, next.tile, next_tm, next_tn);
+                const int row0 = row0_of(tm);  // first of this warp's rows
                 const int m = row0 + lane;
                 const bool row_ok = m < p.m;
                 // this warp's columns: half of the unit's, 32 at a time
                 const int cols = w.narrow ? kLinHalf / 2 : kLinHalf;
                 const int col0 = half * cols;
-                const int n_base = tn * kLinTile + (w.narrow ? w.half * kLinHalf : 0) + col0;
+                const int n_base = columns_of(w, tn);
                 LinRow row;
+                // B: the scales of this row's four blocks, 2-byte aligned as they are
+                uint32_t scales = 0;
+                if constexpr (EPI == kLinActivationBackward) {
+                    if (reads_z && p.z_codes && n_base < p.n) {
+                        const uint8_t* at = p.z_scales + ((static_cast<int64_t>(min(m, p.m - 1)) * p.n + n_base) >> 5);
+                        scales = *reinterpret_cast<const uint16_t*>(at);
+                        if (cols > 64 && n_base + 64 < p.n)
+                            scales |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at + 2)) << 16;
+                    }
+                }
                 // What remains of a chunk once its product `v` is in registers.
-                auto finish = [&](float (&v)[32], const ZWords& zw, int c) {
+                auto finish = [&](float (&v)[32], int c) {
+                    if (!alive) return;
                     const int n = n_base + 32 * c;
                     const bool ok = row_ok && n < p.n;
-                    if (row0 >= p.m || n >= p.n) return;  // warp-uniform: nothing of the box is inside
-                    uint32_t box = box0;
-                    if constexpr (EPI == kLinAccumulate) {
-                        if (lane == 0) bulk_wait_group_read<0>();
+                    const bool inside = row0 < p.m && n < p.n;  // warp-uniform: some of the box is
+                    const uint32_t at = reads_z ? done : n_stored;
+                    const uint32_t box = box0 + (at % kBoxes) * kOutBox;
+                    uint32_t out[16];
+                    if (reads_z) {
+                        if (lane == 0) {
+                            bulk_wait_group_read<0>();  // the other box's store has read it
+                            if (32 * (c + 1) < cols)
+                                ask_z(n + 32, row0);
+                            else if (u + npairs < p.num_units)
+                                ask_z(columns_of(next, next_tn), row0_of(next_tm));
+                        }
                         __syncwarp();
-                        const uint32_t at = box + static_cast<uint32_t>(lane) * 128u;
+                        alive = __all_sync(0xffffffffu, mbar_wait(side_bars + 8u * (2 * warp_at + (done & 1u)), (done >> 1) & 1u,
+                                                                  status, kSiteEpiSideInput));
+                        if (!alive) return;
+                        ++done;
+                    }
+                    if (!inside) return;
+                    if constexpr (EPI == kLinForward) forward_chunk(p, row, v, m, n, c, ok, out);
+                    if constexpr (EPI == kLinActivationBackward) {
+                        ZWords zw{};
+                        if (reads_z) {
+                            box_to_z(box, lane, p.z_codes != nullptr, zw);
+                            zw.scale = (scales >> (8 * c)) & 0xffu;
+                        }
+                        slopes(p.act, zw, p.z_codes != nullptr, v);
+                        to_words(v, out);
+                    }
+                    // the box's last store has read it, its z is in registers
+                    if (!reads_z && lane == 0) bulk_wait_group_read<kBoxes - 1>();
+                    __syncwarp();
+                    if constexpr (EPI == kLinAccumulate) {
+                        const uint32_t to = box + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
                         for (uint32_t j = 0; j < 8; ++j)
-                            st_shared_v4(at + ((j ^ (static_cast<uint32_t>(lane) & 7u)) << 4),
+                            st_shared_v4(to + ((j ^ (static_cast<uint32_t>(lane) & 7u)) << 4),
                                          make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
                                                     __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
                     } else {
-                        uint32_t out[16];
-                        if constexpr (EPI == kLinForward)
-                            forward_chunk(p, row, v, m, n, c, ok, out);
-                        else
-                            backward_chunk(p, v, zw, m, n, row0, lane, ok, out);
-                        // two boxes in turn: one is rewritten after the store before last has read it
-                        box += (n_stored & 1u) * (kLinBox / 2);
-                        if (lane == 0) bulk_wait_group_read<1>();
-                        __syncwarp();
                         words_to_box(box, lane, out);
                     }
                     fence_proxy_async_smem();
@@ -697,28 +772,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         bulk_commit_group();
                     }
                     ++n_stored;
+                    // last: the box's store, which the next chunk waits for, runs meanwhile
+                    if constexpr (EPI == kLinActivationBackward && kSums) add_columns(p, v, n, row0, lane, ok);
                 };
                 // the bias's 128 bytes of each chunk into L1, ahead of the loads that every lane makes
                 if constexpr (EPI == kLinForward) {
                     if (p.bias && 32 * lane < cols && n_base + 32 * lane < p.n)
                         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + n_base + 32 * lane));
                 }
-                auto z_of = [&](int c) {
-                    ZWords zw{};
-                    if constexpr (EPI == kLinActivationBackward) {
-                        const int n = n_base + 32 * c;
-                        load_z(p, static_cast<int64_t>(m) * p.n + n, row_ok && n < p.n, zw);
-                    }
-                    return zw;
-                };
                 if constexpr (kSums) {
-                    float sum[4][32];
-                    ZWords zw = z_of(0);  // always one chunk ahead of its use
+                    float sum[kChunks][32];
                     for (int kc = 0; alive && kc < p.k_blocks; kc += chunk_at(kc)) {
                         if (!acquire()) break;
                         const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kChunks; ++c) {
                             if (32 * c < cols) {
                                 uint32_t r[32];
                                 tmem_load_32(t0 + 32u * c, r);
@@ -741,18 +809,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     }
                     if (!alive) break;
                     if constexpr (EPI == kLinAccumulate) {
-                        const ZWords unused{};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (32 * c < cols) finish(sum[c], unused, c);
+                        for (int c = 0; c < kChunks; ++c)
+                            if (32 * c < cols) finish(sum[c], c);
                     } else {
                         // two copies of the long code rather than four: the sums move down
 #pragma unroll 1
                         for (int c = 0; 32 * c < cols; c += 2) {
-                            const ZWords next = z_of(c + 1);
-                            finish(sum[0], zw, c);
-                            if (32 * (c + 2) < cols) zw = z_of(c + 2);
-                            finish(sum[1], next, c + 1);
+                            finish(sum[0], c);
+                            finish(sum[1], c + 1);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 sum[0][i] = sum[2][i];
@@ -761,13 +826,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         }
                     }
                 } else {
-                    ZWords zw = z_of(0);  // always one chunk ahead of its use
                     if (!acquire()) break;
                     const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
 #pragma unroll 1
                     for (int c = 0; 32 * c < cols; ++c) {
-                        const ZWords now = zw;
-                        if (32 * (c + 1) < cols) zw = z_of(c + 1);
                         uint32_t r[32];
                         tmem_load_32(t0 + 32u * c, r);
                         tmem_wait_load();
@@ -775,12 +837,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                        finish(v, now, c);
+                        finish(v, c);
                     }
                 }
             }
-            // the boxes must stay until the last stores have read them, and all of it be written
-            if (lane == 0) bulk_wait_group_all();
+            // the boxes must stay until the last stores have read them, and all of it be written;
+            // a box of z still in flight (a wait gave up) must land
+            if (lane == 0) {
+                bulk_wait_group_all();
+                for (; done < asked; ++done) mbar_drain(side_bars + 8u * (2 * warp_at + (done & 1)), (done >> 1) & 1u, kWaitLimitNs);
+            }
         }
     }
 
@@ -935,6 +1001,12 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     ok = ok && (EPI == kLinAccumulate
                     ? gemm_encode_map(&mo, out, p.m, p.n, p.n, 32, 32, k128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32)
                     : gemm_encode_map(&mo, out, p.m, p.n, p.n, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, kBf16));
+    // B: boxes of z, or a map that nothing reads through
+    CUtensorMap mz = ma;
+    if (EPI == kLinActivationBackward && p.act != ZB_ACT_NONE)
+        ok = ok && (p.z_codes ? gemm_encode_map(&mz, p.z_codes, p.m, p.n, p.n, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                                CU_TENSOR_MAP_DATA_TYPE_UINT8)
+                              : gemm_encode_map(&mz, p.z, p.m, p.n, p.n, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, kBf16));
     if (!ok) return cudaErrorInvalidValue;
     p.status = status_word();
     if (!p.status) return cudaErrorInvalidDevice;
@@ -974,7 +1046,7 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     const int rem = tiles % pairs;
     p.narrow_from = rem > 0 && 2 * rem <= pairs ? tiles - rem : tiles;
     p.num_units = p.narrow_from + 2 * (tiles - p.narrow_from);
-    kern<<<2 * std::min(p.num_units, pairs), kLinThreads, kLinSmem, stream>>>(ma, mb, mo, p);
+    kern<<<2 * std::min(p.num_units, pairs), kLinThreads, kLinSmem, stream>>>(ma, mb, mo, mz, p);
     return cudaGetLastError();
 }
 

@@ -222,15 +222,15 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(80
             }
             if (p.codes) {  // four threads hold a block of 32 (a row has a multiple of 8 chunks)
                 const uint32_t top2 = pack_top2(pack_top2(pack_top2(pack_top2(0u, nq.x), nq.y), nq.z), nq.w);
-                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+                uint32_t top = pack_top(top2);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 if (inside(i)) {
                     const uint32_t scale = pack_scale(top);
                     const uint32_t f = pack_factor(scale);
-                    const bool fine = scale != kPackNotFinite;
                     *reinterpret_cast<uint2*>(p.codes + base + at) =
-                        make_uint2(fine ? pack_codes(nq.x, nq.y, f) : 0u, fine ? pack_codes(nq.z, nq.w, f) : 0u);
+                        top < kPackLargest ? make_uint2(pack_codes(nq.x, nq.y, f), pack_codes(nq.z, nq.w, f))
+                                           : make_uint2(pack_codes_slow(nq.x, nq.y, f, scale), pack_codes_slow(nq.z, nq.w, f, scale));
                     if ((tid & 3) == 0) p.scales[(base + at) >> 5] = static_cast<uint8_t>(scale);
                 }
             }
