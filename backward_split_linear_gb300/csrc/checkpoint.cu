@@ -1,4 +1,5 @@
 // Packing activations into 8 bits, and back.  The format is checkpoint.cuh's.
+#include "chained.cuh"
 #include "checkpoint.cuh"
 #include "checks.h"
 #include "operators.h"
@@ -11,8 +12,9 @@ constexpr int kPackThreads = 256;
 
 // Two threads a block of 32: each loads 16 elements (two 16-byte words), the larger of
 // their largest magnitudes gives the scale.  Bound by HBM.
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ codes,
-                                                            uint8_t* __restrict__ scales, int64_t halves) {
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t* x, uint8_t* codes, uint8_t* scales, int64_t halves) {
+    release_next();
+    wait_for_previous();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kPackThreads + threadIdx.x;
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     if (i < halves) {
@@ -37,9 +39,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint16_t* __re
 }
 
 // 16 elements a thread.  Bound by HBM.
-__global__ void __launch_bounds__(kPackThreads) unpack_kernel(const uint8_t* __restrict__ codes,
-                                                              const uint8_t* __restrict__ scales, uint16_t* __restrict__ x,
+__global__ void __launch_bounds__(kPackThreads) unpack_kernel(const uint8_t* codes, const uint8_t* scales, uint16_t* x,
                                                               int64_t halves) {
+    release_next();
+    wait_for_previous();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kPackThreads + threadIdx.x;
     if (i >= halves) return;
     const uint4 cv = reinterpret_cast<const uint4*>(codes)[i];
@@ -68,9 +71,8 @@ cudaError_t launch_unpack(const void* codes, const void* scales, void* x, int to
     int64_t halves;
     unsigned grid;
     if (!halves_of(tokens, width, &halves, &grid)) return cudaErrorInvalidValue;
-    unpack_kernel<<<grid, kPackThreads, 0, stream>>>(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
-                                                     static_cast<uint16_t*>(x), halves);
-    return cudaGetLastError();
+    return launch_chained(unpack_kernel, grid, kPackThreads, 0, stream, static_cast<const uint8_t*>(codes),
+                          static_cast<const uint8_t*>(scales), static_cast<uint16_t*>(x), halves);
 }
 
 }  // namespace zbk
@@ -85,10 +87,8 @@ extern "C" zb_status zb_op_checkpoint_pack(const void* x, const zb_checkpoint* p
         return ZB_ERR_ARG;
     ZB_TRY(device_ok());
     if (tokens == 0) return ZB_OK;
-    pack_kernel<<<grid, kPackThreads, 0, as_stream(stream)>>>(static_cast<const uint16_t*>(x),
-                                                              static_cast<uint8_t*>(packed->codes),
-                                                              static_cast<uint8_t*>(packed->scales), halves);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_chained(pack_kernel, grid, kPackThreads, 0, as_stream(stream), static_cast<const uint16_t*>(x),
+                                      static_cast<uint8_t*>(packed->codes), static_cast<uint8_t*>(packed->scales), halves));
 }
 
 extern "C" zb_status zb_op_checkpoint_unpack(const zb_checkpoint* packed, void* x, int32_t tokens, int32_t width,

@@ -70,8 +70,8 @@ __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
 struct LinParams {
     int m, n, k_blocks;
     int tiles_m, tiles_n, group, group_m;
-    // tiles from narrow_from on (a short last wave) are two units of 128 columns each
-    int narrow_from, num_units;
+    // tiles from narrow_from on (a short last wave) are `parts` units of 256 / parts columns each
+    int narrow_from, parts, num_units;
     int act;
     bool wide;                 // z, residual and codes start at 32-byte boundaries
     const float* bias;         // F: [n] or NULL
@@ -86,19 +86,14 @@ struct LinParams {
 };
 
 struct LinUnit {
-    int tile, half;
-    bool narrow;
+    int tile, part;
+    int cols;  // 256, 128 or 64
 };
 
 __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
-    LinUnit w{u, 0, false};
-    if (u >= p.narrow_from) {
-        const int v = u - p.narrow_from;
-        w.tile = p.narrow_from + (v >> 1);
-        w.half = v & 1;
-        w.narrow = true;
-    }
-    return w;
+    if (u < p.narrow_from) return LinUnit{u, 0, kLinTile};
+    const int v = u - p.narrow_from, shift = p.parts >> 1;  // 1, 2 or 4 parts
+    return LinUnit{p.narrow_from + (v >> shift), v & (p.parts - 1), kLinTile >> shift};
 }
 
 __device__ __forceinline__ void lin_tile(const LinParams& p, int tile, int& tm, int& tn) {
@@ -317,8 +312,11 @@ __device__ __forceinline__ void load_sector(const void* p, bool wide, uint4& a, 
 // keeps no more than 2-byte alignment (n is a multiple of 64, so blocks come in pairs).
 struct ScalePair {
     uint32_t first;
+    bool alone;  // the warp has one block of the row
     __device__ __forceinline__ void put(uint8_t* scales, int64_t at, int c, uint32_t scale, bool ok) {
-        if ((c & 1) == 0)
+        if (alone) {
+            if (ok) scales[at] = static_cast<uint8_t>(scale);
+        } else if ((c & 1) == 0)
             first = scale;
         else if (ok)
             *reinterpret_cast<uint16_t*>(scales + at - 1) = static_cast<uint16_t>(first | (scale << 8));
@@ -341,7 +339,7 @@ __device__ __forceinline__ void forward_chunk(const LinParams& p, LinRow& row, f
     if (p.bias) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + n) + j);
+            const float4 b = reinterpret_cast<const float4*>(p.bias + n)[j];
             const float2 lo = __fadd2_rn(make_float2(v[4 * j], v[4 * j + 1]), make_float2(b.x, b.y));
             const float2 hi = __fadd2_rn(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(b.z, b.w));
             v[4 * j] = lo.x;
@@ -530,7 +528,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot, kLinTmemCols);
     tc_fence_before();
+    release_next();
     cluster_sync_all();  // barriers of both CTAs initialised, tensor memory allocated
+    wait_for_previous();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
     const uint32_t peer_base = ld_shared_cluster_u32(map_to_cta(tmem_slot, rank ^ 1u));
@@ -551,17 +551,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     int tm, tn;
                     lin_tile(p, w.tile, tm, tn);
                     const int m0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf;
-                    // a narrow unit's 128 columns split 64 / 64 between the CTAs; the boxes stay
-                    // whole, and what they hold past those columns is not read
-                    const int n0 = tn * kLinTile + (w.narrow ? w.half * kLinHalf + static_cast<int>(rank) * (kLinHalf / 2)
-                                                             : static_cast<int>(rank) * kLinHalf);
+                    // each CTA loads half of a unit's columns: two boxes of 64, or one, of which a
+                    // unit of 64 columns reads half
+                    const int n0 = tn * kLinTile + w.part * w.cols + static_cast<int>(rank) * (w.cols / 2);
+                    const bool whole = w.cols == kLinTile;
                     for (int kb = 0; kb < p.k_blocks; ++kb) {
                         if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
                             ok = false;
                             break;
                         }
                         const uint32_t fb_local = full_bar(stage);
-                        if (leader) mbar_arrive_expect_tx(fb_local, 4 * kLinOperand);
+                        if (leader) mbar_arrive_expect_tx(fb_local, whole ? 4 * kLinOperand : 3 * kLinOperand);
                         const uint32_t fb = map_to_cta(fb_local, 0);
                         const int k0 = kb * kLinBK;
                         const uint32_t a_dst = s_a + stage * kLinOperand, b_dst = s_b + stage * kLinOperand;
@@ -573,9 +573,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         }
                         if constexpr (B_MN) {
                             tma_load_2d_pair(b_dst, &map_b, fb, n0, k0);
-                            tma_load_2d_pair(b_dst + kLinMnBlock, &map_b, fb, n0 + 64, k0);
+                            if (whole) tma_load_2d_pair(b_dst + kLinMnBlock, &map_b, fb, n0 + 64, k0);
                         } else {
                             tma_load_2d_pair(b_dst, &map_b, fb, k0, n0);
+                            if (whole) tma_load_2d_pair(b_dst + kLinMnBlock, &map_b, fb, k0, n0 + 64);
                         }
                         ++n_fills;
                         if (++stage == kLinStages) {
@@ -600,14 +601,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             if (leader) {
                 // ---------------- MMA issuer (rank 0): a converged warp, its elected lane carries each instruction
                 const uint32_t issuer = elect_one_sync();
-                constexpr uint32_t idesc_wide = mma_idesc_bf16(kLinTile, kLinTile, A_MN, B_MN);
-                constexpr uint32_t idesc_narrow = mma_idesc_bf16(kLinTile, kLinHalf, A_MN, B_MN);
+                constexpr uint32_t idesc_whole = mma_idesc_bf16(kLinTile, kLinTile, A_MN, B_MN);
+                constexpr uint32_t idesc_half = mma_idesc_bf16(kLinTile, kLinTile / 2, A_MN, B_MN);
+                constexpr uint32_t idesc_quarter = mma_idesc_bf16(kLinTile, kLinTile / 4, A_MN, B_MN);
                 int stage = 0;
                 uint32_t phase = 0;
                 uint32_t it = 0;
                 bool ok = true;
                 for (int u = pair; ok && u < p.num_units; u += npairs) {
-                    const uint32_t idesc = lin_unit(p, u).narrow ? idesc_narrow : idesc_wide;
+                    const int width = lin_unit(p, u).cols;
+                    const uint32_t idesc = width == kLinTile ? idesc_whole : width == kLinTile / 2 ? idesc_half : idesc_quarter;
                     for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_at(kc), ++it) {
                         const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
                         if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
@@ -685,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 ++asked;
             };
             auto columns_of = [&](const LinUnit& w, int tn) {  // a warp's first column
-                return tn * kLinTile + (w.narrow ? w.half * kLinHalf + half * (kLinHalf / 2) : half * kLinHalf);
+                return tn * kLinTile + w.part * w.cols + half * (w.cols / 2);
             };
             LinUnit next = lin_unit(p, pair);
             int next_tm, next_tn;
@@ -701,16 +704,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 const int m = row0 + lane;
                 const bool row_ok = m < p.m;
                 // this warp's columns: half of the unit's, 32 at a time
-                const int cols = w.narrow ? kLinHalf / 2 : kLinHalf;
+                const int cols = w.cols / 2;
                 const int col0 = half * cols;
                 const int n_base = columns_of(w, tn);
                 LinRow row;
+                row.z.alone = row.y.alone = cols == 32;
                 // B: the scales of this row's four blocks, 2-byte aligned as they are
                 uint32_t scales = 0;
                 if constexpr (EPI == kLinActivationBackward) {
                     if (reads_z && p.z_codes && n_base < p.n) {
                         const uint8_t* at = p.z_scales + ((static_cast<int64_t>(min(m, p.m - 1)) * p.n + n_base) >> 5);
-                        scales = *reinterpret_cast<const uint16_t*>(at);
+                        // (a single block may be the second of its pair)
+                        scales = cols > 32 ? *reinterpret_cast<const uint16_t*>(at) : *at;
                         if (cols > 64 && n_base + 64 < p.n)
                             scales |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at + 2)) << 16;
                     }
@@ -817,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 #pragma unroll 1
                         for (int c = 0; 32 * c < cols; c += 2) {
                             finish(sum[0], c);
-                            finish(sum[1], c + 1);
+                            if (32 * (c + 1) < cols) finish(sum[1], c + 1);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 sum[0][i] = sum[2][i];
@@ -841,10 +846,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     }
                 }
             }
-            // the boxes must stay until the last stores have read them, and all of it be written;
-            // a box of z still in flight (a wait gave up) must land
+            // the boxes must stay until the last stores have read them; a box of z still in
+            // flight (a wait gave up) must land
             if (lane == 0) {
-                bulk_wait_group_all();
+                bulk_wait_group_read<0>();
                 for (; done < asked; ++done) mbar_drain(side_bars + 8u * (2 * warp_at + (done & 1)), (done >> 1) & 1u, kWaitLimitNs);
             }
         }
@@ -874,14 +879,17 @@ int column_parts(int tokens, int width) {
     return std::max(1, std::min((kColTargetBlocks + across - 1) / across, (tokens + kColGroups - 1) / kColGroups));
 }
 
-// Block (x, y): columns 256 x ..., the y-th part of the rows.  Bound by HBM.
-__global__ void __launch_bounds__(kColThreads) column_parts_kernel(const uint16_t* __restrict__ dy, float* __restrict__ parts,
-                                                                   int tokens, int width) {
+// Block x + y across: columns 256 x ..., the y-th part of the rows.  Bound by HBM.
+__global__ void __launch_bounds__(kColThreads) column_parts_kernel(const uint16_t* dy, float* parts, int tokens, int width,
+                                                                   int n_parts) {
     __shared__ float sums[kColGroups][256];
+    release_next();
+    wait_for_previous();
+    const int across = (width + 255) / 256, bx = blockIdx.x % across, by = blockIdx.x / across;
     const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
-    const int col = blockIdx.x * 256 + 8 * lane;
-    const int per = (tokens + gridDim.y - 1) / gridDim.y;
-    const int t0 = blockIdx.y * per, t1 = min(tokens, t0 + per);
+    const int col = bx * 256 + 8 * lane;
+    const int per = (tokens + n_parts - 1) / n_parts;
+    const int t0 = by * per, t1 = min(tokens, t0 + per);
     float acc[8] = {};
     if (col < width) {
         for (int tb = t0 + group; tb < t1; tb += kColGroups * kColUnroll) {
@@ -905,18 +913,19 @@ __global__ void __launch_bounds__(kColThreads) column_parts_kernel(const uint16_
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[group][8 * lane + e] = acc[e];
     __syncthreads();
-    const int j = blockIdx.x * 256 + threadIdx.x;
+    const int j = bx * 256 + threadIdx.x;
     if (j < width) {
         float s = 0.f;
 #pragma unroll
         for (int g = 0; g < kColGroups; ++g) s += sums[g][threadIdx.x];
-        parts[static_cast<int64_t>(blockIdx.y) * width + j] = s;
+        parts[static_cast<int64_t>(by) * width + j] = s;
     }
 }
 
 // A block finishes 32 columns: thread (c, g) adds the parts g, g + 8, ... of column c.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ parts, float* out, int n_parts, int width) {
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* parts, float* out, int n_parts, int width) {
     __shared__ float sums[8][32];
+    release_next();
     wait_for_previous();
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + c;
@@ -945,10 +954,12 @@ cudaError_t launch_column_sum(const float* parts, float* out, int n_parts, int w
 // ---------------------------------------------------------------- the activation alone
 
 // dz = dy act'(z), 8 elements a thread.  Bound by HBM.
-__global__ void __launch_bounds__(256) activation_backward_kernel(const uint16_t* dy, const uint16_t* __restrict__ z,
-                                                                  const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales, uint16_t* dz,
+__global__ void __launch_bounds__(256) activation_backward_kernel(const uint16_t* dy, const uint16_t* z,
+                                                                  const uint8_t* codes,
+                                                                  const uint8_t* scales, uint16_t* dz,
                                                                   int64_t chunks, int act) {
+    release_next();
+    wait_for_previous();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= chunks) return;
     const uint4 dv = reinterpret_cast<const uint4*>(dy)[i];
@@ -997,7 +1008,7 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     bool ok = A_MN ? gemm_encode_map(&ma, a, k, p.m, p.m, 64, kLinBK, k128, kBf16)
                    : gemm_encode_map(&ma, a, p.m, k, k, 64, kLinHalf, k128, kBf16);
     ok = ok && (B_MN ? gemm_encode_map(&mb, b, k, p.n, p.n, 64, kLinBK, k128, kBf16)
-                     : gemm_encode_map(&mb, b, p.n, k, k, 64, kLinHalf, k128, kBf16));
+                     : gemm_encode_map(&mb, b, p.n, k, k, 64, kLinHalf / 2, k128, kBf16));
     ok = ok && (EPI == kLinAccumulate
                     ? gemm_encode_map(&mo, out, p.m, p.n, p.n, 32, 32, k128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32)
                     : gemm_encode_map(&mo, out, p.m, p.n, p.n, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, kBf16));
@@ -1041,13 +1052,15 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     bool group_m = false;
     p.group = gemm_raster(p.tiles_m, p.tiles_n, kLinTile, kLinTile, k, std::min(tiles, pairs), &group_m);
     p.group_m = group_m ? 1 : 0;
-    // A last wave that would keep at most half of the pairs busy runs as halves of 128
-    // columns on twice as many: each output element takes the same steps.
+    // A last wave that would keep at most half (a quarter) of the pairs busy runs as units of
+    // half (a quarter) of a tile's columns on twice (four times) as many: each output element
+    // takes the same steps.
     const int rem = tiles % pairs;
-    p.narrow_from = rem > 0 && 2 * rem <= pairs ? tiles - rem : tiles;
-    p.num_units = p.narrow_from + 2 * (tiles - p.narrow_from);
-    kern<<<2 * std::min(p.num_units, pairs), kLinThreads, kLinSmem, stream>>>(ma, mb, mo, mz, p);
-    return cudaGetLastError();
+    p.parts = rem == 0 || 2 * rem > pairs ? 1 : 4 * rem > pairs ? 2 : 4;
+    p.narrow_from = p.parts == 1 ? tiles : tiles - rem;
+    p.num_units = p.narrow_from + p.parts * (tiles - p.narrow_from);
+    return launch_chained(kern, 2u * static_cast<unsigned>(std::min(p.num_units, pairs)), kLinThreads, kLinSmem, stream, ma, mb, mo,
+                          mz, p);
 }
 
 bool activation_ok(int32_t act) { return act >= ZB_ACT_NONE && act <= ZB_ACT_RELU2; }
@@ -1145,11 +1158,10 @@ extern "C" zb_status zb_op_activation_backward(const void* dy, const void* z, co
     const int64_t chunks = static_cast<int64_t>(tokens) * (width / 8);
     const int64_t grid = (chunks + 255) / 256;
     if (grid > 0x7fffffff) return ZB_ERR_SHAPE;
-    activation_backward_kernel<<<static_cast<unsigned>(grid), 256, 0, as_stream(stream)>>>(
-        static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z),
-        z_packed ? static_cast<const uint8_t*>(z_packed->codes) : nullptr,
-        z_packed ? static_cast<const uint8_t*>(z_packed->scales) : nullptr, static_cast<uint16_t*>(dz), chunks, activation);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_chained(
+        activation_backward_kernel, static_cast<unsigned>(grid), 256, 0, as_stream(stream), static_cast<const uint16_t*>(dy),
+        static_cast<const uint16_t*>(z), z_packed ? static_cast<const uint8_t*>(z_packed->codes) : nullptr,
+        z_packed ? static_cast<const uint8_t*>(z_packed->scales) : nullptr, static_cast<uint16_t*>(dz), chunks, activation));
 }
 
 extern "C" size_t zb_op_backward_bias_scratch_bytes(int32_t tokens, int32_t out_features) {
@@ -1168,10 +1180,9 @@ extern "C" zb_status zb_op_backward_bias(const void* dy, float* dbias, int32_t t
     if (tokens == 0) return ZB_OK;
     const int parts = column_parts(tokens, out_features);
     cudaStream_t s = as_stream(stream);
-    const dim3 grid((out_features + 255) / 256, parts);
-    column_parts_kernel<<<grid, kColThreads, 0, s>>>(static_cast<const uint16_t*>(dy), static_cast<float*>(scratch), tokens,
-                                                     out_features);
-    ZB_TRY(cuda_status(cudaGetLastError()));
+    const unsigned grid = static_cast<unsigned>((out_features + 255) / 256 * parts);
+    ZB_TRY(cuda_status(launch_chained(column_parts_kernel, grid, kColThreads, 0, s, static_cast<const uint16_t*>(dy),
+                                      static_cast<float*>(scratch), tokens, out_features, parts)));
     return cuda_status(launch_column_sum(static_cast<const float*>(scratch), dbias, parts, out_features, s));
 }
 

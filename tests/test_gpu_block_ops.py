@@ -181,8 +181,8 @@ def test_backward_input(cuda_device, t, k, n, kind, eight):
     slip = (k / 16 + 4) * 2.0 ** -22 * mass
     bar = HALF * np.abs(ds * slope) + 2.0 ** -12 * np.abs(ds * slope) + 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * slip
     within(take(dz, t), ds * slope, bar, "dz")
-    # at most 1152 terms at a time on the tensor cores, k / 512 sums in registers
-    slip = ((min(k, 1152) / 16 + 4) * 2.0 ** -22 + (k / 512) * 2.0 ** -24) * mass
+    # 512 terms at a time on the tensor cores (sums this short), k / 512 sums in registers
+    slip = ((min(k, 512) / 16 + 4) * 2.0 ** -22 + (k / 512) * 2.0 ** -24) * mass
     each = 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * slip + t * 2.0 ** -24 * np.abs(ds * slope)
     within(dbias.cpu().numpy(), before + (ds * slope).sum(0), each.sum(0) + 2.0 ** -22 * np.abs(before), "dbias")
     # without the bias gradient, and over z itself
