@@ -11,13 +11,14 @@ namespace zbk {
 // are visible.  Every block of a kernel launched by `launch_chained` calls it before
 // its first access to global memory (the status word aside, which is only ever set), on
 // every path: a later kernel takes this one's end for the end of those before it.
-// Elsewhere it returns at once.  Such a kernel runs while earlier ones still write, so nothing
-// that they may write is read through __ldg or `const __restrict__`.
+// Elsewhere it returns at once.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets a kernel that `launch_chained` put behind this one start once every block of this one
 // has called it or ended, where the SMs have room: its setup then runs beside this kernel's
-// work, up to its own wait_for_previous, which still waits for this kernel's end.
+// work, up to its own wait_for_previous, which still waits for this kernel's end.  What a
+// kernel that calls this writes is not read through the non-coherent path (__ldg, `const
+// __restrict__`) by one that may follow: activations, gradients and scratch; parameters may be.
 __device__ __forceinline__ void release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>

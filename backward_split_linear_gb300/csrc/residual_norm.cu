@@ -54,12 +54,13 @@ __device__ __forceinline__ uint4 narrow(const F8& f) {
                       pack_bf16x2(f.p[3].x, f.p[3].y));
 }
 
-// Parameters.  As an instruction of its own: the compiler keeps plain loads behind the stores of
-// a row's other columns, which no parameter overlaps (70B-shaped backward 83 against 75 us).
+// Parameters.  They are constant from before a kernel that may run ahead of this one's start
+// (release_next) to this one's end, so they may be read ahead of this kernel's stores, which the
+// 70B-shaped backward is 10 us faster for (77 against 87).
 __device__ __forceinline__ F8 load_f8(const float* p) {
     float4 a, b;
-    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w) : "l"(p));
-    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w) : "l"(p + 4));
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w) : "l"(p));
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w) : "l"(p + 4));
     return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
