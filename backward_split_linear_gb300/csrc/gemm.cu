@@ -1503,8 +1503,6 @@ int gemm_raster(int tiles_m, int tiles_n, int bm, int bn, int k, int grid, bool*
     return r.group;
 }
 
-int gemm_pairs() { return pair_max_clusters(); }
-
 bool gemm_takes_pair(int m, int n) { return m >= kPairM && n >= kPairN; }
 
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t stream) {

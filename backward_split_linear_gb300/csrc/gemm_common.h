@@ -15,7 +15,4 @@ bool gemm_encode_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t co
 // *group_m: groups of tile rows (else of tile columns).
 int gemm_raster(int tiles_m, int tiles_n, int bm, int bn, int k, int grid, bool* group_m);
 
-// CTA pairs that run at once on the current device (0 on an error).
-int gemm_pairs();
-
 }  // namespace zbk

@@ -873,10 +873,11 @@ constexpr int kColThreads = 256;
 constexpr int kColGroups = 8;  // row groups of a block; a thread takes 8 columns
 constexpr int kColUnroll = 4;
 constexpr int kColTargetBlocks = 1216;  // 8 blocks of 256 threads on each of 152 SMs
+constexpr int kColMostParts = 152;      // the second pass is short where the first has few columns
 
 int column_parts(int tokens, int width) {
     const int across = (width + 255) / 256;
-    return std::max(1, std::min((kColTargetBlocks + across - 1) / across, (tokens + kColGroups - 1) / kColGroups));
+    return std::max(1, std::min({(kColTargetBlocks + across - 1) / across, kColMostParts, (tokens + kColGroups - 1) / kColGroups}));
 }
 
 // Block x + y across: columns 256 x ..., the y-th part of the rows.  Bound by HBM.
@@ -1001,7 +1002,7 @@ __global__ void __launch_bounds__(256) activation_backward_kernel(const uint16_t
 // ---------------------------------------------------------------- launches
 
 template <bool A_MN, bool B_MN, int EPI, bool kSums>
-cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p, int k, cudaStream_t stream) {
+cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p, int k, cudaStream_t stream) try {
     constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap ma, mb, mo;
@@ -1061,6 +1062,8 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     p.num_units = p.narrow_from + p.parts * (tiles - p.narrow_from);
     return launch_chained(kern, 2u * static_cast<unsigned>(std::min(p.num_units, pairs)), kLinThreads, kLinSmem, stream, ma, mb, mo,
                           mz, p);
+} catch (...) {  // the tile order is kept in a map, which may not get its memory
+    return cudaErrorMemoryAllocation;
 }
 
 bool activation_ok(int32_t act) { return act >= ZB_ACT_NONE && act <= ZB_ACT_RELU2; }

@@ -376,10 +376,11 @@ constexpr int kWThreads = 256;
 constexpr int kWGroups = 8;
 constexpr int kWUnroll = 4;
 constexpr int kWTargetBlocks = 608;  // of each pair: 4 blocks of 256 threads on each of 152 SMs
+constexpr int kWMostParts = 152;     // few columns: 16384 rows of 256 in 19 us (608 parts: 29)
 
 int norm_parts(int tokens, int hidden) {
     const int across = (hidden + 255) / 256;
-    return std::max(1, std::min((kWTargetBlocks + across - 1) / across, (tokens + kWGroups - 1) / kWGroups));
+    return std::max(1, std::min({(kWTargetBlocks + across - 1) / across, kWMostParts, (tokens + kWGroups - 1) / kWGroups}));
 }
 
 // Block x + across (y + parts z): columns 256 x ..., the y-th part of the rows, pair first + z.

@@ -105,6 +105,102 @@ def test_forward(cuda_device, t, k, n, kind):
     no_waits_ran_out()
 
 
+def same_packed(p, x, t):
+    """The 8-bit form that an epilogue wrote is the one that packing the bf16 tensor gives."""
+    codes, scales = torch.empty_like(p[0][:t]), torch.empty_like(p[1][:t])
+    zb.zb_op_checkpoint_pack(x, (codes, scales), t, x.shape[1])
+    assert torch.equal(codes, p[0][:t]) and torch.equal(scales, p[1][:t])
+    assert torch.all(p[0][t:] == 77) and torch.all(p[1][t:] == 77)
+
+
+def product_slip(mass, k, most):
+    """Bound of a product's error (the module's docstring) with sums of `most` terms at a time on the tensor cores."""
+    return ((min(k, most) / 16 + 4) * 2.0 ** -22 + (k / 512) * 2.0 ** -24) * mass
+
+
+# long inner sizes (sums in registers, the first ones longer), and outputs of several waves of tiles whose last is cut in two
+# or in four
+LONG = [(130, 4160, 320), (70, 1216, 192), (40, 2304, 64), (2600, 64, 2112), (2600, 128, 2048), (300, 64, 12672)]
+
+
+@pytest.mark.parametrize("t,k,n", LONG)
+def test_long_and_wide(cuda_device, t, k, n):
+    rng = np.random.default_rng(k + n)
+    xb, x = draw_bf16(rng, (t, k))
+    wb, w = draw_bf16(rng, (n, k), std=1.0 / np.sqrt(k))
+    bias, bias_dev = draw_f32(rng, n)
+    xd, wd = bf16_from_bits(xb), bf16_from_bits(wb)
+    y, z, y8, z8 = out_rows(t, n), out_rows(t, n), packed_rows(t, n), packed_rows(t, n)
+    zb.zb_op_linear_activation_forward(xd, wd, bias_dev, None, y, t, k, n, "silu", z=z, y_packed=y8)
+    zz = x @ w.T + bias
+    mass = np.abs(x) @ np.abs(w).T + np.abs(bias)
+    slip = product_slip(mass, k, 1280)
+    within(take(z, t), zz, HALF * np.abs(zz) + slip, "z")
+    a = O.act(zz, "silu")
+    within(take(y, t), a, (HALF + 2.0 ** -12) * np.abs(a) + 2.0 ** -18 + 1.2 * slip, "y")
+    y2 = out_rows(t, n)
+    zb.zb_op_linear_activation_forward(xd, wd, bias_dev, None, y2, t, k, n, "silu", z_packed=z8)
+    assert torch.equal(y2, y)
+    same_packed(y8, y[:t], t)
+    same_packed(z8, z[:t], t)
+    plain = out_rows(t, n)
+    zb.zb_op_linear_activation_forward(xd, wd, bias_dev, None, plain, t, k, n, "silu")
+    within(take(plain, t), a, (HALF + 2.0 ** -12) * np.abs(a) + 2.0 ** -18 + 1.2 * product_slip(mass, k, k), "y alone")
+    # B back through it: dy [t, k] of a linear [k, n] behind the activation
+    db, dy = draw_bf16(rng, (t, k))
+    w2 = bf16_from_bits(wb).t().contiguous()
+    zq = O.unpack(take(z8[0], t), take(z8[1], t))
+    ds, slope = dy @ w.T, O.act_slope(zq, "silu")
+    mass = np.abs(dy) @ np.abs(w).T
+    before, dbias = draw_f32(rng, n)
+    scratch = scratch_of(zb.zb_op_backward_input_activation_scratch_bytes(t, n))
+    for with_bias in (True, False):
+        dz = out_rows(t, n)
+        zb.zb_op_backward_input_activation(bf16_from_bits(db), w2, None, dz, t, n, k, "silu", z_packed=(z8[0], z8[1]),
+                                           dbias=dbias if with_bias else None, scratch=scratch)
+        slip = product_slip(mass, k, 1152 if with_bias else k)
+        bar = (HALF + 2.0 ** -12) * np.abs(ds * slope) + 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * slip
+        within(take(dz, t), ds * slope, bar, "dz")
+    each = 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * product_slip(mass, k, 1152) + t * 2.0 ** -24 * np.abs(ds * slope)
+    within(dbias.cpu().numpy(), before + (ds * slope).sum(0), each.sum(0) + 2.0 ** -22 * np.abs(before), "dbias")
+    no_waits_ran_out()
+
+
+@pytest.mark.parametrize("shift", [8, 24])
+def test_tensors_at_16_byte_starts(cuda_device, shift):
+    """Tensors that start 16 bytes off a 32-byte boundary give the same bits as aligned ones."""
+    t, k, n = 70, 128, 192
+
+    def off(x):
+        """A copy of x that starts `shift` bf16 elements (codes: 16 bytes) into its storage."""
+        at = shift if x.dtype == torch.bfloat16 else 16
+        room = torch.zeros(x.numel() + at, dtype=x.dtype, device="cuda")
+        room[at:].copy_(x.reshape(-1))
+        return room[at:].view(x.shape)
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    x, w, res, dy, w2 = draw(t, k), draw(n, k), draw(t, n), draw(t, k), draw(k, n)
+    bias = torch.randn(n, generator=g, device="cuda")
+    got = []
+    for place in (lambda v: v, off):
+        y, z = place(torch.zeros_like(res)), place(torch.zeros_like(res))
+        y8 = tuple(place(torch.zeros(t, c, dtype=torch.uint8, device="cuda")) for c in (n, n // 32))
+        z8 = tuple(place(torch.zeros(t, c, dtype=torch.uint8, device="cuda")) for c in (n, n // 32))
+        zb.zb_op_linear_activation_forward(place(x), place(w), bias, place(res), y, t, k, n, "gelu", z=z, y_packed=y8)
+        zb.zb_op_checkpoint_pack(z, z8, t, n)
+        dz, dz8 = place(torch.zeros_like(res)), place(torch.zeros_like(res))
+        zb.zb_op_backward_input_activation(place(dy), place(w2), z, dz, t, n, k, "gelu")
+        zb.zb_op_backward_input_activation(place(dy), place(w2), None, dz8, t, n, k, "gelu", z_packed=z8)
+        dw = torch.zeros(k, n, device="cuda")
+        scratch = scratch_of(zb.zb_op_backward_weight_checkpoint_scratch_bytes(t, n))
+        zb.zb_op_backward_weight_checkpoint(place(dy), y8, dw, t, n, k, scratch)
+        got.append([y, z, *y8, *z8, dz, dz8, dw])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_forward_without_options(cuda_device):
     t, k, n = 200, 128, 128
     rng = np.random.default_rng(0)
@@ -276,7 +372,7 @@ def test_unpack_any_bytes(cuda_device):
 
 
 @pytest.mark.parametrize("t,k,n", [(1, 64, 64), (63, 128, 64), (64, 64, 128), (65, 320, 192), (700, 512, 256), (513, 1088, 320),
-                                   (1500, 256, 576)])
+                                   (1500, 256, 576), (4200, 64, 128), (64, 2624, 2688)])
 def test_weight_from_8_bits(cuda_device, t, k, n):
     rng = np.random.default_rng(t + k)
     db, dy = draw_bf16(rng, (t, n))
@@ -289,7 +385,7 @@ def test_weight_from_8_bits(cuda_device, t, k, n):
     scratch = scratch_of(zb.zb_op_backward_weight_checkpoint_scratch_bytes(t, k))
     zb.zb_op_backward_weight_checkpoint(bf16_from_bits(db), p, guard, t, k, n, scratch)
     v = O.unpack(codes, scales)
-    slip = ((min(t, 512) / 16 + 4) * 2.0 ** -22 + (t / 512 + 1) * 2.0 ** -24) * (np.abs(dy).T @ np.abs(v))
+    slip = product_slip(np.abs(dy).T @ np.abs(v), t, 512)
     ref = before + dy.T @ v
     within(take(guard, n), ref, slip + 2.0 ** -23 * (np.abs(before) + np.abs(ref)), "dw")
     again = f32(before)
