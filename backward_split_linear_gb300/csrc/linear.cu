@@ -50,21 +50,16 @@ constexpr int kLinFewRegs = 64, kLinManyRegs = 216;
 
 enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
 
-// k blocks (of 64 terms) that stay in tensor memory at a time: 8 where the results are
-// float32, 12 for F's 8-bit codes, which only need what float32 arithmetic would give them.
-// Where the epilogue is long, a tile's first two accumulators hold more: while its warps
-// work on the tile before, the MMAs get that far and no further.  8B-shaped, gelu, z in 8 bits, K = 4096: B
-// with a bias gradient 307 us with 8 throughout, XXX with 18 (its float32 sum is then 8.9e-7 off, one in
-// float32 arithmetic 6.2e-7), 300 with 20 (1.0e-6).
-template <int EPI>
-__host__ __device__ constexpr int lin_sum_blocks() {
-    return EPI == kLinForward ? 12 : 8;
-}
+// k blocks (of 64 terms) that stay in tensor memory at a time.  Where the epilogue is long, a
+// tile's first two accumulators hold more: while its warps work on the tile before, the MMAs get
+// that far and no further.  8B-shaped B with gelu, z in 8 bits and a bias gradient (K = 4096), that
+// sum's error behind the time: 312 us with 14 first (6.7e-7), 301 with 16 (7.8e-7), 298 with 18
+// (8.9e-7); the plain form's in float32 arithmetic is 6.2e-7 off.
+constexpr int kLinSumBlocks = 8;
 template <int EPI>
 __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
-    if (EPI == kLinForward) return max(lin_sum_blocks<EPI>(), min(16, k_blocks / 2));
-    if (EPI == kLinActivationBackward) return max(lin_sum_blocks<EPI>(), min(18, k_blocks / 3));
-    return lin_sum_blocks<EPI>();
+    if (EPI == kLinAccumulate) return kLinSumBlocks;
+    return max(kLinSumBlocks, min(16, k_blocks / (EPI == kLinForward ? 2 : 3)));
 }
 
 struct LinParams {
@@ -473,7 +468,7 @@ __device__ __forceinline__ void add_columns(const LinParams& p, float (&v)[32], 
 
 // ---------------------------------------------------------------- kernel
 
-// kSums: the accumulators are added up in registers every few k blocks (lin_sum_blocks).
+// kSums: the accumulators are added up in registers every few k blocks (kLinSumBlocks).
 template <bool A_MN, bool B_MN, int EPI, bool kSums>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -507,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     auto chunk_at = [&](int kc) {
         if (!kSums) return p.k_blocks;
         const int first = lin_first_blocks<EPI>(p.k_blocks);
-        return kc < 2 * first ? first : lin_sum_blocks<EPI>();
+        return kc < 2 * first ? first : kLinSumBlocks;
     };
 
     if (threadIdx.x == 0) {

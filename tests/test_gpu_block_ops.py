@@ -134,7 +134,7 @@ def test_long_and_wide(cuda_device, t, k, n):
     zb.zb_op_linear_activation_forward(xd, wd, bias_dev, None, y, t, k, n, "silu", z=z, y_packed=y8)
     zz = x @ w.T + bias
     mass = np.abs(x) @ np.abs(w).T + np.abs(bias)
-    slip = product_slip(mass, k, 1280)
+    slip = product_slip(mass, k, 1024)
     within(take(z, t), zz, HALF * np.abs(zz) + slip, "z")
     a = O.act(zz, "silu")
     within(take(y, t), a, (HALF + 2.0 ** -12) * np.abs(a) + 2.0 ** -18 + 1.2 * slip, "y")
@@ -158,10 +158,10 @@ def test_long_and_wide(cuda_device, t, k, n):
         dz = out_rows(t, n)
         zb.zb_op_backward_input_activation(bf16_from_bits(db), w2, None, dz, t, n, k, "silu", z_packed=(z8[0], z8[1]),
                                            dbias=dbias if with_bias else None, scratch=scratch)
-        slip = product_slip(mass, k, 1152 if with_bias else k)
+        slip = product_slip(mass, k, 1024 if with_bias else k)
         bar = (HALF + 2.0 ** -12) * np.abs(ds * slope) + 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * slip
         within(take(dz, t), ds * slope, bar, "dz")
-    each = 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * product_slip(mass, k, 1152) + t * 2.0 ** -24 * np.abs(ds * slope)
+    each = 2.0 ** -18 * np.abs(ds) + (np.abs(slope) + 0.1) * product_slip(mass, k, 1024) + t * 2.0 ** -24 * np.abs(ds * slope)
     within(dbias.cpu().numpy(), before + (ds * slope).sum(0), each.sum(0) + 2.0 ** -22 * np.abs(before), "dbias")
     no_waits_ran_out()
 
