@@ -65,8 +65,10 @@ __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
 struct LinParams {
     int m, n, k_blocks;
     int tiles_m, tiles_n, group, group_m;
-    // tiles from narrow_from on (a short last wave) are `parts` units of 256 / parts columns each
+    // tiles from narrow_from on (a short last wave) are `parts` units of 256 / parts columns each;
+    // with K split, the pairs of a unit
     int narrow_from, parts, num_units;
+    uint32_t a_bytes;  // of one CTA's A tile: few rows have a box of as many (rounded up to 8)
     int act;
     bool wide;                 // z, residual and codes start at 32-byte boundaries
     const float* bias;         // F: [n] or NULL
@@ -98,6 +100,23 @@ __device__ __forceinline__ void lin_tile(const LinParams& p, int tile, int& tm, 
     const int a = g * p.group + in % size, b = in / size;
     tm = p.group_m ? a : b;
     tn = p.group_m ? b : a;
+}
+
+// Which of a unit's operand boxes CTA `rank` loads: none of rows past M or columns past N.  What
+// its tiles then hold reaches rows and columns of the result that are not stored.
+struct LinBoxes {
+    bool a;
+    int b;  // boxes of 64 columns
+    uint32_t bytes;
+};
+
+__device__ __forceinline__ LinBoxes lin_boxes(const LinParams& p, int tm, int col0, int cols, int rank) {
+    LinBoxes x;
+    x.a = tm * kLinTile + rank * kLinHalf < p.m;
+    const int n0 = col0 + rank * (cols / 2);
+    x.b = n0 >= p.n ? 0 : cols == kLinTile && n0 + 64 < p.n ? 2 : 1;
+    x.bytes = (x.a ? p.a_bytes : 0u) + static_cast<uint32_t>(x.b) * kLinMnBlock;
+    return x;
 }
 
 // ---------------------------------------------------------------- activations
@@ -548,30 +567,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const int m0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf;
                     // each CTA loads half of a unit's columns: two boxes of 64, or one, of which a
                     // unit of 64 columns reads half
-                    const int n0 = tn * kLinTile + w.part * w.cols + static_cast<int>(rank) * (w.cols / 2);
-                    const bool whole = w.cols == kLinTile;
+                    const int col0 = tn * kLinTile + w.part * w.cols;
+                    const int n0 = col0 + static_cast<int>(rank) * (w.cols / 2);
+                    const LinBoxes boxes = lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank));
+                    const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank ^ 1u)).bytes;
                     for (int kb = 0; kb < p.k_blocks; ++kb) {
                         if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
                             ok = false;
                             break;
                         }
                         const uint32_t fb_local = full_bar(stage);
-                        if (leader) mbar_arrive_expect_tx(fb_local, whole ? 4 * kLinOperand : 3 * kLinOperand);
+                        if (leader) mbar_arrive_expect_tx(fb_local, bytes);
                         const uint32_t fb = map_to_cta(fb_local, 0);
                         const int k0 = kb * kLinBK;
                         const uint32_t a_dst = s_a + stage * kLinOperand, b_dst = s_b + stage * kLinOperand;
-                        if constexpr (A_MN) {
-                            tma_load_2d_pair(a_dst, &map_a, fb, m0, k0);
-                            tma_load_2d_pair(a_dst + kLinMnBlock, &map_a, fb, m0 + 64, k0);
-                        } else {
-                            tma_load_2d_pair(a_dst, &map_a, fb, k0, m0);
+                        if (boxes.a) {
+                            if constexpr (A_MN) {
+                                tma_load_2d_pair(a_dst, &map_a, fb, m0, k0);
+                                tma_load_2d_pair(a_dst + kLinMnBlock, &map_a, fb, m0 + 64, k0);
+                            } else {
+                                tma_load_2d_pair(a_dst, &map_a, fb, k0, m0);
+                            }
                         }
-                        if constexpr (B_MN) {
-                            tma_load_2d_pair(b_dst, &map_b, fb, n0, k0);
-                            if (whole) tma_load_2d_pair(b_dst + kLinMnBlock, &map_b, fb, n0 + 64, k0);
-                        } else {
-                            tma_load_2d_pair(b_dst, &map_b, fb, k0, n0);
-                            if (whole) tma_load_2d_pair(b_dst + kLinMnBlock, &map_b, fb, k0, n0 + 64);
+                        for (int j = 0; j < boxes.b; ++j) {
+                            if constexpr (B_MN)
+                                tma_load_2d_pair(b_dst + j * kLinMnBlock, &map_b, fb, n0 + 64 * j, k0);
+                            else
+                                tma_load_2d_pair(b_dst + j * kLinMnBlock, &map_b, fb, k0, n0 + 64 * j);
                         }
                         ++n_fills;
                         if (++stage == kLinStages) {
@@ -858,6 +880,283 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------- few tiles: K split in a cluster
+//
+// Outputs of so few tiles that most SMs would idle, over a long K (a pair takes 0.2 us for every 64
+// terms, however few rows and columns there are).  A cluster of 2 or 4 CTA pairs computes one 256 x
+// 128 unit, each pair over its share of K.  The partial sums go to shared memory, where the
+// operands were, and every CTA finishes some of the unit's 32 x 32 blocks from all pairs' partial
+// sums, added in the order of the pairs.  11 rows, K = 6720, 64 columns: 24.1 us on one pair, 13.0 on two, 10.0
+// on four, 10.1 on eight; 185 rows, K = 11520, 1088 columns: 39.3, 21.5, 20.1.  At K = 1024 it loses (256 rows,
+// 1024 columns: 8.2 against 9.3), at 2048 it gains (64 rows, 2048 columns: 10.6 against 9.1).
+
+constexpr int kSplitUnit = 128;       // columns of a unit
+constexpr int kSplitTasks = 4 * 4;    // 32 x 32 blocks of a CTA's 128 x 128
+constexpr int kSplitMinBlocks = 32;   // k blocks from which a split pays
+
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t caddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(caddr)
+                 : "memory");
+    return v;
+}
+
+// 16-byte word j of row r of a 128 x 128 float32 block: eight consecutive rows cover all banks.
+__device__ __forceinline__ uint32_t partial_at(uint32_t base, int r, uint32_t j) {
+    return base + static_cast<uint32_t>(r) * 512u + ((j ^ (static_cast<uint32_t>(r) & 31u)) << 4);
+}
+
+template <bool A_MN, bool B_MN, int EPI, bool kSums>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t s_a = base, s_b = base + kLinStages * kLinOperand;
+    const uint32_t s_out = s_b + kLinStages * kLinOperand;
+    const uint32_t bars = s_out + kLinStaging;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (kLinStages + s); };
+    auto tfull_bar = [&](int a) { return bars + 8u * (2 * kLinStages + a); };
+    auto tempty_bar = [&](int a) { return bars + 8u * (2 * kLinStages + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (2 * kLinStages + 4);
+    const uint32_t tmem_slot = bars + 8u * kLinBars;
+    volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - raw));
+
+    int* const status = p.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t cta = cluster_ctarank(), rank = cta & 1u, first = cta & ~1u;  // first: the pair's rank 0
+    const bool leader = rank == 0;
+    const int split = static_cast<int>(cta >> 1), splits = p.parts;
+    const int unit = static_cast<int>(blockIdx.x) / (2 * splits);
+    const int tm = unit % p.tiles_m, tn = unit / p.tiles_m;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(split) * p.k_blocks / splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * p.k_blocks / splits);
+    // k blocks of the accumulator that starts at block kc
+    auto chunk_end = [&](int kc) { return kSums ? min(kc + kLinSumBlocks, kb1) : kb1; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kLinStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 2 * kLinEpiWarps);
+        }
+        mbar_init(drain_bar, 1);
+        mbar_fence_init();
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        tma_prefetch_map(&map_out);
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, kLinTmemCols);
+    tc_fence_before();
+    release_next();
+    cluster_sync_all();
+    wait_for_previous();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint32_t peer_base = ld_shared_cluster_u32(map_to_cta(tmem_slot, cta ^ 1u));
+    const bool usable = peer_base == tmem_base;
+    if (!usable && threadIdx.x == 0) atomicCAS(status, 0, kSitePairTmem);
+    bool alive = usable;
+
+    if (usable && warp == 0) {
+        if (lane == 0) {
+            uint32_t n_fills = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            const int m0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf;
+            const int col0 = tn * kSplitUnit, n0 = col0 + static_cast<int>(rank) * (kSplitUnit / 2);
+            const LinBoxes boxes = lin_boxes(p, tm, col0, kSplitUnit, static_cast<int>(rank));
+            const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, kSplitUnit, static_cast<int>(rank ^ 1u)).bytes;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) break;
+                if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
+                const uint32_t fb = map_to_cta(full_bar(stage), first);
+                const int k0 = kb * kLinBK;
+                const uint32_t a_dst = s_a + stage * kLinOperand, b_dst = s_b + stage * kLinOperand;
+                if (boxes.a) {
+                    if constexpr (A_MN) {
+                        tma_load_2d_pair(a_dst, &map_a, fb, m0, k0);
+                        tma_load_2d_pair(a_dst + kLinMnBlock, &map_a, fb, m0 + 64, k0);
+                    } else {
+                        tma_load_2d_pair(a_dst, &map_a, fb, k0, m0);
+                    }
+                }
+                if (boxes.b) {
+                    if constexpr (B_MN)
+                        tma_load_2d_pair(b_dst, &map_b, fb, n0, k0);
+                    else
+                        tma_load_2d_pair(b_dst, &map_b, fb, k0, n0);
+                }
+                ++n_fills;
+                if (++stage == kLinStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            for (int s = 0; s < kLinStages; ++s) {
+                const uint32_t uses = ring_uses(n_fills, kLinStages, s);
+                if (uses > 0) mbar_wait_cluster(leader ? full_bar(s) : empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain);
+            }
+        }
+    } else if (usable && warp == 1) {
+        if (leader) {
+            const uint32_t issuer = elect_one_sync();
+            constexpr uint32_t idesc = mma_idesc_bf16(kLinTile, kSplitUnit, A_MN, B_MN);
+            const uint16_t both_ctas = static_cast<uint16_t>(3u << first);
+            int stage = 0;
+            uint32_t phase = 0, it = 0;
+            bool ok = true;
+            for (int kc = kb0; ok && kc < kb1; kc = chunk_end(kc), ++it) {
+                const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * kLinTile;
+                for (int kb = kc; kb < chunk_end(kc); ++kb) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = s_a + stage * kLinOperand, b0 = s_b + stage * kLinOperand;
+#pragma unroll
+                    for (int k = 0; k < kLinBK / 16; ++k) {
+                        const uint64_t ad = A_MN ? smem_desc_sw128(a0 + k * 2048, kLinMnBlock, 1024)
+                                                 : smem_desc_sw128(a0 + k * 32, 16, 1024);
+                        const uint64_t bd = B_MN ? smem_desc_sw128(b0 + k * 2048, kLinMnBlock, 1024)
+                                                 : smem_desc_sw128(b0 + k * 32, 16, 1024);
+                        umma_bf16_pair_elected(issuer, d, ad, bd, idesc, (kb != kc || k != 0) ? 1u : 0u);
+                    }
+                    umma_commit_pair_elected(issuer, empty_bar(stage), both_ctas);
+                    if (++stage == kLinStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) umma_commit_pair_elected(issuer, tfull_bar(acc), both_ctas);
+            }
+            umma_commit_pair_elected(issuer, drain_bar, static_cast<uint16_t>(1u << first));
+            mbar_wait(drain_bar, 0, status, kSiteDrain, kWaitLimitNs);
+        }
+    } else if (usable && warp >= kLinFirstWarps) {
+        // this pair's sums of 32 rows and 64 columns into the CTA's 128 x 128 block
+        const int q = warp & 3, half = (warp - kLinFirstWarps) >> 2;
+        const uint32_t tlane = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(64 * half);
+        float sum[2][32];
+        uint32_t it = 0;
+        for (int kc = kb0; kc < kb1; kc = chunk_end(kc), ++it) {
+            const uint32_t acc = it & 1u;
+            alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(acc), (it >> 1) & 1u, status, kSiteEpiTmemFull));
+            if (!alive) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_load_32(tlane + acc * kLinTile + 32u * c, r);
+                tmem_wait_load();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[c][i] = kc == kb0 ? __uint_as_float(r[i]) : sum[c][i] + __uint_as_float(r[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(tempty_bar(acc));
+                else
+                    mbar_arrive_cluster(map_to_cta(tempty_bar(acc), first));
+            }
+        }
+        // the MMAs that read the operands are done with them in both CTAs of the pair
+        if (alive) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    st_shared_v4(partial_at(s_a, q * 32 + lane, 16u * half + 8u * c + j),
+                                 make_uint4(__float_as_uint(sum[c][4 * j]), __float_as_uint(sum[c][4 * j + 1]),
+                                            __float_as_uint(sum[c][4 * j + 2]), __float_as_uint(sum[c][4 * j + 3])));
+        }
+    }
+
+    cluster_sync_all();  // every pair's partial sums are there
+    const int per_cta = kSplitTasks / splits;
+    const int warp_at = warp - kLinFirstWarps;
+    if (alive && warp_at >= 0 && warp_at < per_cta) {
+        const int task = split * per_cta + warp_at, q = task & 3, c = task >> 2;
+        const int row0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf + q * 32, m = row0 + lane;
+        const int n = tn * kSplitUnit + 32 * c;
+        if (row0 < p.m && n < p.n) {
+            const bool ok = m < p.m;
+            float v[32];
+            for (int s = 0; s < splits; ++s) {
+                const uint32_t from = map_to_cta(s_a, 2u * s + rank);
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    const float4 t = ld_shared_cluster_f4(partial_at(from, q * 32 + lane, 8u * c + j));
+                    v[4 * j] = s == 0 ? t.x : v[4 * j] + t.x;
+                    v[4 * j + 1] = s == 0 ? t.y : v[4 * j + 1] + t.y;
+                    v[4 * j + 2] = s == 0 ? t.z : v[4 * j + 2] + t.z;
+                    v[4 * j + 3] = s == 0 ? t.w : v[4 * j + 3] + t.w;
+                }
+            }
+            const uint32_t box = s_out + static_cast<uint32_t>(warp_at) * (kLinStaging / kLinEpiWarps);
+            uint32_t out[16];
+            if constexpr (EPI == kLinForward) {
+                LinRow row;
+                row.z.alone = row.y.alone = true;
+                forward_chunk(p, row, v, m, n, 0, ok, out);
+            }
+            if constexpr (EPI == kLinActivationBackward) {
+                if (p.act != ZB_ACT_NONE) {
+                    ZWords zw{};
+                    const int64_t at = static_cast<int64_t>(min(m, p.m - 1)) * p.n + n;
+                    if (p.z_codes) {
+                        load_sector(p.z_codes + at, p.wide, zw.w[0], zw.w[1]);
+                        zw.scale = p.z_scales[at >> 5];
+                    } else {
+                        load_sector(p.z + at, p.wide, zw.w[0], zw.w[1]);
+                        load_sector(p.z + at + 16, p.wide, zw.w[2], zw.w[3]);
+                    }
+                    slopes(p.act, zw, p.z_codes != nullptr, v);
+                }
+                to_words(v, out);
+            }
+            if constexpr (EPI == kLinAccumulate) {
+                const uint32_t to = box + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    st_shared_v4(to + ((j ^ (static_cast<uint32_t>(lane) & 7u)) << 4),
+                                 make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                            __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+            } else {
+                words_to_box(box, lane, out);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (EPI == kLinAccumulate)
+                    tma_reduce_add_2d(&map_out, box, n, row0);
+                else
+                    tma_store_2d(&map_out, box, n, row0);
+                bulk_commit_group();
+            }
+            if constexpr (EPI == kLinActivationBackward && kSums) add_columns(p, v, n, row0, lane, ok);
+            if (lane == 0) bulk_wait_group_read<0>();
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync_all();  // no CTA leaves while another may still read its partial sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kLinTmemCols);
+    }
+}
+
 // ---------------------------------------------------------------- bias gradient
 //
 // dbias[j] += sum over rows.  Two passes in a fixed order: sums over parts of the rows
@@ -996,13 +1295,67 @@ __global__ void __launch_bounds__(256) activation_backward_kernel(const uint16_t
 
 // ---------------------------------------------------------------- launches
 
+// How many CTA pairs of a kernel fit on the current device at once, and how many clusters of 2
+// and 4 pairs of its split form.
+struct LinFit {
+    int pairs;
+    int clusters[2];
+};
+
+cudaError_t lin_fit(const void* kern, const void* split_kern, LinFit* fit) {
+    LinFit f{};
+    for (const void* k : {kern, split_kern}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLinSmem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count()));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kLinSmem;
+    cudaError_t e = cudaOccupancyMaxActiveClusters(&f.pairs, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (f.pairs < 1) return cudaErrorInvalidConfiguration;
+    for (int i = 0; i < 2; ++i) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {4u << i, 1, 1};
+        cfg.gridDim = dim3(static_cast<unsigned>(sm_count()) / (4u << i) * (4u << i));
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&f.clusters[i], split_kern, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    *fit = f;
+    return cudaSuccess;
+}
+
+// A chained launch in clusters of a size given here.
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), unsigned grid, unsigned cluster, cudaStream_t stream, A&&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {cluster, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kLinSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 template <bool A_MN, bool B_MN, int EPI, bool kSums>
 cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p, int k, cudaStream_t stream) try {
     constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap ma, mb, mo;
+    const uint32_t a_rows = A_MN ? kLinHalf : static_cast<uint32_t>(std::min(kLinHalf, (p.m + 7) / 8 * 8));
+    p.a_bytes = a_rows * kLinBK * 2;
     bool ok = A_MN ? gemm_encode_map(&ma, a, k, p.m, p.m, 64, kLinBK, k128, kBf16)
-                   : gemm_encode_map(&ma, a, p.m, k, k, 64, kLinHalf, k128, kBf16);
+                   : gemm_encode_map(&ma, a, p.m, k, k, 64, a_rows, k128, kBf16);
     ok = ok && (B_MN ? gemm_encode_map(&mb, b, k, p.n, p.n, 64, kLinBK, k128, kBf16)
                      : gemm_encode_map(&mb, b, p.n, k, k, 64, kLinHalf / 2, k128, kBf16));
     ok = ok && (EPI == kLinAccumulate
@@ -1022,29 +1375,35 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     p.wide = starts % 32 == 0;
 
     auto kern = linear_kernel<A_MN, B_MN, EPI, kSums>;
+    auto split_kern = linear_split_kernel<A_MN, B_MN, EPI, kSums>;
     static std::mutex mu;
-    static int pairs_of[64] = {};
-    int dev = 0, pairs = 0;
+    static LinFit fits[64] = {};
+    int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    LinFit fit;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!pairs_of[dev]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLinSmem));
+        if (!fits[dev].pairs) {
+            const cudaError_t e = lin_fit(reinterpret_cast<const void*>(kern), reinterpret_cast<const void*>(split_kern), &fits[dev]);
             if (e != cudaSuccess) return e;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(sm_count()));
-            cfg.blockDim = dim3(kLinThreads);
-            cfg.dynamicSmemBytes = kLinSmem;
-            e = cudaOccupancyMaxActiveClusters(&pairs_of[dev], kern, &cfg);
-            if (e != cudaSuccess) return e;
-            if (pairs_of[dev] < 1) return cudaErrorInvalidConfiguration;
         }
-        pairs = pairs_of[dev];
+        fit = fits[dev];
     }
+    const int pairs = fit.pairs;
     p.k_blocks = (k + kLinBK - 1) / kLinBK;
     p.tiles_m = (p.m + kLinTile - 1) / kLinTile;
     p.tiles_n = (p.n + kLinTile - 1) / kLinTile;
     const int tiles = p.tiles_m * p.tiles_n;
+
+    // K split: the most pairs a unit for which all units run at once.
+    const int units = p.tiles_m * ((p.n + kSplitUnit - 1) / kSplitUnit);
+    for (int i = 1; i >= 0; --i) {
+        const int splits = 2 << i;
+        if (units > fit.clusters[i] || p.k_blocks < kSplitMinBlocks) continue;
+        p.parts = splits;
+        return launch_clusters(split_kern, static_cast<unsigned>(units * 2 * splits), 2u * splits, stream, ma, mb, mo, p);
+    }
+
     bool group_m = false;
     p.group = gemm_raster(p.tiles_m, p.tiles_n, kLinTile, kLinTile, k, std::min(tiles, pairs), &group_m);
     p.group_m = group_m ? 1 : 0;
