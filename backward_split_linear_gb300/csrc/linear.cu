@@ -1171,7 +1171,7 @@ constexpr int kColMostParts = 152;      // the second pass is short where the fi
 
 int column_parts(int tokens, int width) {
     const int across = (width + 255) / 256;
-    return std::max(1, std::min({(kColTargetBlocks + across - 1) / across, kColMostParts, (tokens + kColGroups - 1) / kColGroups}));
+    return std::max(1, std::min({kColTargetBlocks / across, kColMostParts, (tokens + kColGroups - 1) / kColGroups}));
 }
 
 // Block x + y across: columns 256 x ..., the y-th part of the rows.  Bound by HBM.

@@ -162,7 +162,7 @@ __device__ __forceinline__ float2 moments(const F8 (&v)[kPer], int tid, int chun
 }
 
 template <int kRow, int kPer, bool kFull>
-__global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(80))
+__global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(kRow == 512 ? 64 : 80))
     residual_norm_forward_kernel(const __grid_constant__ NormParams p, int tokens) {
     __shared__ float2 red[4][32];
     release_next();
@@ -374,19 +374,22 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
 
 constexpr int kWThreads = 256;
 constexpr int kWGroups = 8;
-constexpr int kWUnroll = 4;
-constexpr int kWTargetBlocks = 608;  // of each pair: 4 blocks of 256 threads on each of 152 SMs
+constexpr int kWUnroll = 2;
+// Blocks of each pair, at most: 3 of 256 threads on each of 152 SMs, six for both pairs, all at
+// once.  With a few more a second round starts: 8597 rows of 3776 columns in 60 us with 615 of 608 that
+// fit, 45 with 450.
+constexpr int kWTargetBlocks = 456;
 constexpr int kWMostParts = 152;     // few columns: 16384 rows of 256 in 19 us (608 parts: 29)
 
 int norm_parts(int tokens, int hidden) {
     const int across = (hidden + 255) / 256;
-    return std::max(1, std::min({(kWTargetBlocks + across - 1) / across, kWMostParts, (tokens + kWGroups - 1) / kWGroups}));
+    return std::max(1, std::min({kWTargetBlocks / across, kWMostParts, (tokens + kWGroups - 1) / kWGroups}));
 }
 
 // Block x + across (y + parts z): columns 256 x ..., the y-th part of the rows, pair first + z.
 // Bound by HBM.
 template <bool kTokenGate>
-__global__ void __launch_bounds__(kWThreads, kTokenGate ? 3 : 4) residual_norm_parts_kernel(const __grid_constant__ NormParams p,
+__global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6) residual_norm_parts_kernel(const __grid_constant__ NormParams p,
                                                                         float* parts, int tokens, int first, int n_parts) {
     __shared__ float sums[2][kWGroups][256];
     release_next();
