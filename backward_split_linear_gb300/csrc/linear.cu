@@ -65,6 +65,7 @@ __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
 struct LinParams {
     int m, n, k_blocks;
     int tiles_m, tiles_n, group, group_m;
+    int tile_n;  // columns of a tile: 256, or fewer where that fills the last wave
     // tiles from narrow_from on (a short last wave) are `parts` units of 256 / parts columns each;
     // with K split, the pairs of a unit
     int narrow_from, parts, num_units;
@@ -84,11 +85,11 @@ struct LinParams {
 
 struct LinUnit {
     int tile, part;
-    int cols;  // 256, 128 or 64
+    int cols;  // tile_n, 128 or 64
 };
 
 __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
-    if (u < p.narrow_from) return LinUnit{u, 0, kLinTile};
+    if (u < p.narrow_from) return LinUnit{u, 0, p.tile_n};
     const int v = u - p.narrow_from, shift = p.parts >> 1;  // 1, 2 or 4 parts
     return LinUnit{p.narrow_from + (v >> shift), v & (p.parts - 1), kLinTile >> shift};
 }
@@ -114,7 +115,7 @@ __device__ __forceinline__ LinBoxes lin_boxes(const LinParams& p, int tm, int co
     LinBoxes x;
     x.a = tm * kLinTile + rank * kLinHalf < p.m;
     const int n0 = col0 + rank * (cols / 2);
-    x.b = n0 >= p.n ? 0 : cols == kLinTile && n0 + 64 < p.n ? 2 : 1;
+    x.b = n0 >= p.n ? 0 : cols > kLinHalf && n0 + 64 < p.n ? 2 : 1;
     x.bytes = (x.a ? p.a_bytes : 0u) + static_cast<uint32_t>(x.b) * kLinMnBlock;
     return x;
 }
@@ -298,7 +299,8 @@ __device__ __forceinline__ void words_to_box(uint32_t box, int lane, const uint3
 }
 
 // 32 bytes of a row, a whole sector in one access where the tensor starts at one (`wide`).
-// In two of 16 every sector went to L2 twice: 348 against XXX us for an 8B-shaped layer with z and y in 8 bits.
+// In two of 16 every sector went to L2 twice: 348 against 325 us for an 8B-shaped layer with z and y in 8 bits
+// (sustained clocks).
 __device__ __forceinline__ void store_sector(void* p, bool wide, const uint4& a, const uint4& b) {
     if (wide) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
@@ -567,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const int m0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf;
                     // each CTA loads half of a unit's columns: two boxes of 64, or one, of which a
                     // unit of 64 columns reads half
-                    const int col0 = tn * kLinTile + w.part * w.cols;
+                    const int col0 = tn * p.tile_n + w.part * w.cols;
                     const int n0 = col0 + static_cast<int>(rank) * (w.cols / 2);
                     const LinBoxes boxes = lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank));
                     const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank ^ 1u)).bytes;
@@ -618,16 +620,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             if (leader) {
                 // ---------------- MMA issuer (rank 0): a converged warp, its elected lane carries each instruction
                 const uint32_t issuer = elect_one_sync();
-                constexpr uint32_t idesc_whole = mma_idesc_bf16(kLinTile, kLinTile, A_MN, B_MN);
-                constexpr uint32_t idesc_half = mma_idesc_bf16(kLinTile, kLinTile / 2, A_MN, B_MN);
-                constexpr uint32_t idesc_quarter = mma_idesc_bf16(kLinTile, kLinTile / 4, A_MN, B_MN);
                 int stage = 0;
                 uint32_t phase = 0;
                 uint32_t it = 0;
                 bool ok = true;
                 for (int u = pair; ok && u < p.num_units; u += npairs) {
-                    const int width = lin_unit(p, u).cols;
-                    const uint32_t idesc = width == kLinTile ? idesc_whole : width == kLinTile / 2 ? idesc_half : idesc_quarter;
+                    const uint32_t idesc = mma_idesc_bf16(kLinTile, lin_unit(p, u).cols, A_MN, B_MN);
                     for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_at(kc), ++it) {
                         const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
                         if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
@@ -704,8 +702,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 tma_load_2d(box0 + (asked & 1u) * kOutBox, &map_z, bar, n, row0);
                 ++asked;
             };
+            auto first_columns = [](const LinUnit& w) { return (w.cols / 32 + 1) / 2 * 32; };  // of half 0
             auto columns_of = [&](const LinUnit& w, int tn) {  // a warp's first column
-                return tn * kLinTile + w.part * w.cols + half * (w.cols / 2);
+                return tn * p.tile_n + w.part * w.cols + half * first_columns(w);
             };
             LinUnit next = lin_unit(p, pair);
             int next_tm, next_tn;
@@ -721,20 +720,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 const int m = row0 + lane;
                 const bool row_ok = m < p.m;
                 // this warp's columns: half of the unit's, 32 at a time
-                const int cols = w.cols / 2;
-                const int col0 = half * cols;
+                const int cols = half == 0 ? first_columns(w) : w.cols - first_columns(w);
+                const int col0 = half * first_columns(w);
                 const int n_base = columns_of(w, tn);
                 LinRow row;
-                row.z.alone = row.y.alone = cols == 32;
-                // B: the scales of this row's four blocks, 2-byte aligned as they are
-                uint32_t scales = 0;
+                row.z.alone = row.y.alone = (cols | n_base) % 64 != 0;
+                uint32_t scales = 0;  // B: of this row's blocks, a byte each
                 if constexpr (EPI == kLinActivationBackward) {
-                    if (reads_z && p.z_codes && n_base < p.n) {
+                    if (reads_z && p.z_codes) {
                         const uint8_t* at = p.z_scales + ((static_cast<int64_t>(min(m, p.m - 1)) * p.n + n_base) >> 5);
-                        // (a single block may be the second of its pair)
-                        scales = cols > 32 ? *reinterpret_cast<const uint16_t*>(at) : *at;
-                        if (cols > 64 && n_base + 64 < p.n)
-                            scales |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(at + 2)) << 16;
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+                            if (32 * c < cols && n_base + 32 * c < p.n) scales |= static_cast<uint32_t>(at[c]) << (8 * c);
                     }
                 }
                 // What remains of a chunk once its product `v` is in registers.
@@ -1329,6 +1326,18 @@ cudaError_t lin_fit(const void* kern, const void* split_kern, LinFit* fit) {
     return cudaSuccess;
 }
 
+// Columns of a tile: 256, or the fewest of 224, 192 and 160 with which a single wave that holds over
+// half of the pairs still is one.  1000 rows, K = 14336, 4096 columns: 64 tiles of 256 columns in 71.7 us,
+// 76 of 224 in 69.1; 1024 rows, K = 4096: 26.8 and 25.4.  (Two waves lose: 1533 rows, K = 3264, 4800 columns
+// take 32.6 us in 114 tiles of 256 columns and 35.2 in 150 of 192.)
+int lin_tile_columns(int tiles_m, int n, int pairs) {
+    auto tiles = [&](int w) { return static_cast<int64_t>(tiles_m) * ((n + w - 1) / w); };
+    if (tiles(kLinTile) > pairs || 2 * tiles(kLinTile) <= pairs) return kLinTile;
+    for (int w : {160, 192, 224})
+        if (tiles(w) <= pairs) return w;
+    return kLinTile;
+}
+
 // A chained launch in clusters of a size given here.
 template <typename... P, typename... A>
 cudaError_t launch_clusters(void (*kernel)(P...), unsigned grid, unsigned cluster, cudaStream_t stream, A&&... args) {
@@ -1392,9 +1401,6 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     const int pairs = fit.pairs;
     p.k_blocks = (k + kLinBK - 1) / kLinBK;
     p.tiles_m = (p.m + kLinTile - 1) / kLinTile;
-    p.tiles_n = (p.n + kLinTile - 1) / kLinTile;
-    const int tiles = p.tiles_m * p.tiles_n;
-
     // K split: the most pairs a unit for which all units run at once.
     const int units = p.tiles_m * ((p.n + kSplitUnit - 1) / kSplitUnit);
     for (int i = 1; i >= 0; --i) {
@@ -1404,13 +1410,16 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
         return launch_clusters(split_kern, static_cast<unsigned>(units * 2 * splits), 2u * splits, stream, ma, mb, mo, p);
     }
 
+    p.tile_n = lin_tile_columns(p.tiles_m, p.n, pairs);
+    p.tiles_n = (p.n + p.tile_n - 1) / p.tile_n;
+    const int tiles = p.tiles_m * p.tiles_n;
     bool group_m = false;
-    p.group = gemm_raster(p.tiles_m, p.tiles_n, kLinTile, kLinTile, k, std::min(tiles, pairs), &group_m);
+    p.group = gemm_raster(p.tiles_m, p.tiles_n, kLinTile, p.tile_n, k, std::min(tiles, pairs), &group_m);
     p.group_m = group_m ? 1 : 0;
     // A last wave that would keep at most half (a quarter) of the pairs busy runs as units of
     // half (a quarter) of a tile's columns on twice (four times) as many: each output element
     // takes the same steps.
-    const int rem = tiles % pairs;
+    const int rem = p.tile_n == kLinTile ? tiles % pairs : 0;
     p.parts = rem == 0 || 2 * rem > pairs ? 1 : 4 * rem > pairs ? 2 : 4;
     p.narrow_from = p.parts == 1 ? tiles : tiles - rem;
     p.num_units = p.narrow_from + p.parts * (tiles - p.narrow_from);

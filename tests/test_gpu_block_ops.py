@@ -118,9 +118,10 @@ def product_slip(mass, k, most):
     return ((min(k, most) / 16 + 4) * 2.0 ** -22 + (k / 512) * 2.0 ** -24) * mass
 
 
-# long inner sizes (sums in registers, the first ones longer), and outputs of several waves of tiles whose last is cut in two
-# or in four
-LONG = [(130, 4160, 320), (70, 1216, 192), (40, 2304, 64), (2600, 64, 2112), (2600, 128, 2048), (300, 64, 12672)]
+# long inner sizes (sums in registers, the first ones longer; K split among CTA pairs), outputs of several waves of tiles whose
+# last is cut in two or in four, and of one wave of tiles narrower than 256 columns
+LONG = [(130, 4160, 320), (70, 1216, 192), (40, 2304, 64), (2600, 64, 2112), (2600, 128, 2048), (300, 64, 12672),
+        (1000, 64, 4096), (1300, 64, 1984), (520, 128, 4160)]
 
 
 @pytest.mark.parametrize("t,k,n", LONG)
