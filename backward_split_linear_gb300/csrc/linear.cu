@@ -544,8 +544,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot, kLinTmemCols);
     tc_fence_before();
-    release_next();
     cluster_sync_all();  // barriers of both CTAs initialised, tensor memory allocated
+    release_next();
     wait_for_previous();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
@@ -950,8 +950,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot, kLinTmemCols);
     tc_fence_before();
-    release_next();
     cluster_sync_all();
+    release_next();
     wait_for_previous();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot_ptr;
