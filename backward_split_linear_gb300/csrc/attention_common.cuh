@@ -128,9 +128,10 @@ __device__ __forceinline__ uint2 split3_bf16(float v) {
 // load instruction covers 512 contiguous bytes of each tensor, and a warp
 // takes 8 consecutive rows.  All of a warp's loads are issued before the first
 // sum: with a reduction between one pair of rows and the next, the kernel ran
-// at about 0.6 of the HBM bandwidth.
+// at about 0.6 of the HBM bandwidth.  da and a are no `__restrict__` pointers: the loads stay behind
+// the wait for a kernel that may still be writing them.
 template <int D>
-__global__ void attn_causal_rowsum_kernel(const uint16_t* __restrict__ da, const uint16_t* __restrict__ a, float* dvec,
+__global__ void attn_causal_rowsum_kernel(const uint16_t* da, const uint16_t* a, float* dvec,
                                           int tokens, int n_heads, int ld_stat, int* counter = nullptr) {
     // the tile counter of the kernel that follows on the stream, if it has one
     wait_for_previous();

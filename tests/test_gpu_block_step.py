@@ -215,3 +215,39 @@ def test_one_row_and_a_non_finite_one(cuda_device):
     for k in ("n0", "y1", "n1", "dy0"):
         assert not torch.all(torch.isfinite(bufs[1][k][40])), k
     assert zb.zb_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("t", [40, 1000])
+def test_projection_into_document_attention(cuda_device, t):
+    """The output projection's B, and the attention's backward right behind it on the stream: the attention's first kernel may
+    start beside the projection's, and reads its result only once that has ended."""
+    nh, nkv, d, out = 8, 4, 128, 1024
+    g = torch.Generator()
+    g.manual_seed(t)
+    bf = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    qkv, w, dys = bf(t, (nh + 2 * nkv) * d), bf(out, nh * d), [bf(t, out) for _ in range(8)]
+    new = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
+    plan = new(zb.zb_op_attention_document_plan_bytes(t), dtype=torch.uint8)
+    offsets = torch.tensor([0, t // 3, t], dtype=torch.int32, device="cuda")
+    zb.zb_op_attention_document_plan(offsets, None, 2, t, plan, plan.numel())
+    a, lse = new(t, nh * d), new(nh, max(128, (t + 127) // 128 * 128), dtype=torch.float32)
+    zb.zb_op_attention_document_forward(qkv, a, lse, plan, None, 0.0, t, nh, nkv, d)
+    scratch = new(zb.zb_op_attention_document_scratch_bytes(t, nh), dtype=torch.uint8)
+
+    def run(wait):
+        da, outs = new(t, nh * d), []
+        for dy in dys:
+            dqkv = new(t, (nh + 2 * nkv) * d)
+            outs.append(dqkv)
+            zb.zb_op_backward_input_activation(dy, w, None, da, t, nh * d, out, "none")
+            if wait:
+                torch.cuda.synchronize()
+            zb.zb_op_attention_document_backward(qkv, a, da, lse, dqkv, plan, None, 0.0, t, nh, nkv, d, scratch, scratch.numel())
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    for x, y in zip(run(True), run(False)):
+        assert torch.equal(x, y)
+    assert zb.zb_device_status() == (0, 0)
