@@ -7,7 +7,11 @@
 //
 // F and B take a row in one pass: its threads hold all of it in registers, so that every
 // tensor is read and written once; the sums over the row go through shuffles, and shared
-// memory where a row has more than one warp.  Both are bound by HBM.
+// memory where a row has more than one warp.  The data is bound by HBM, a row by its latency: loads,
+// two sums, stores (6 us for 4096 columns), of which an SM has as many at a time as its registers
+// hold.  So blocks bring the rows behind theirs into L2.  GB300, bytes at 6.8 TB/s in brackets: F with an
+// 8-bit output 33.5 us for 4096 rows of 4096 columns (22.4) and 59 for 8192 columns (44.7); B
+// 38.3 (29.7) and 71.5 (59.4).
 #include <algorithm>
 
 #include "chained.cuh"
@@ -56,8 +60,8 @@ __device__ __forceinline__ uint4 narrow(const F8& f) {
 }
 
 // Parameters.  They are constant from before a kernel that may run ahead of this one's start
-// (release_next) to this one's end, so they may be read ahead of this kernel's stores, which the
-// 70B-shaped backward is 10 us faster for (77 against 87).
+// (release_next) to this one's end, so they may be read ahead of this kernel's stores, which
+// took 10 us off the 70B-shaped backward (87 to 77, before rows came ahead into L2).
 __device__ __forceinline__ F8 load_f8(const float* p) {
     float4 a, b;
     asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w) : "l"(p));
@@ -78,10 +82,16 @@ __device__ __forceinline__ void prefetch_row(const uint16_t* p, int64_t at, int 
 
 __device__ __forceinline__ void store_q(uint16_t* p, const uint4& q) { *reinterpret_cast<uint4*>(p) = q; }
 
-// v * scale + shift of the normed value: scale = rstd, shift = -mean rstd, one rounding.
 __device__ __forceinline__ void affine(F8& v, float scale, float shift) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v.p[e] = __ffma2_rn(v.p[e], both(scale), both(shift));
+}
+
+// The normed value.  The difference first, which is exact where the mean is near: v rstd - mean rstd
+// in one step would leave half a last place of mean rstd, 0.015 for a row of thousands.
+__device__ __forceinline__ void centered(F8& v, float mean, float rstd) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.p[e] = __fmul2_rn(__fadd2_rn(v.p[e], both(-mean)), both(rstd));
 }
 
 __device__ __forceinline__ void times(F8& v, const F8& g) {
@@ -147,7 +157,7 @@ __device__ __forceinline__ float2 moments(const F8 (&v)[kPer], int tid, int chun
         for (int i = 0; i < kPer; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s = __fadd2_rn(s, v[i].p[e]);
-        mean = row_sum<kRow>(make_float2(s.x + s.y, 0.f), red, round).x * inv;
+        mean = row_sum<kRow>(make_float2(s.x + s.y, 0.f), red, round).x / static_cast<float>(8 * chunks);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (!kFull && tid + i * kRow >= chunks) continue;
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(kR
         if (!inside(i)) continue;
         const int at = 8 * (tid + i * kRow);
         if (p.post != ZB_NORM_NONE) {
-            affine(u[i], st.y, -st.x * st.y);
+            centered(u[i], st.x, st.y);
             weigh(u[i], p.post_gamma, p.post_beta, at);
         }
         if (p.gate_channel)
@@ -233,7 +243,7 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(kR
             const int at = 8 * (tid + i * kRow);
             uint4 nq = make_uint4(0, 0, 0, 0);
             if (inside(i)) {
-                affine(u[i], st.w, -st.z * st.w);
+                centered(u[i], st.z, st.w);
                 weigh(u[i], p.pre_gamma, p.pre_beta, at);
                 nq = narrow(u[i]);
                 if (p.n) store_q(p.n + base + at, nq);
@@ -299,14 +309,13 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
         for (int i = 0; i < kPer; ++i) dh[i] = widen(rq[i]);
     }
     if (pre) {
-        const float shift = -st.z * st.w;
         float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (!inside(i)) continue;
             F8 d = widen(nq[i]), hat = widen(hq[i]);
             times(d, load_f8(p.pre_gamma + 8 * (tid + i * kRow)));
-            affine(hat, st.w, shift);
+            centered(hat, st.z, st.w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 s0 = __ffma2_rn(d.p[e], hat.p[e], s0);
@@ -320,13 +329,12 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
             if (!inside(i)) continue;
             F8 d = widen(nq[i]), hat = widen(hq[i]);
             times(d, load_f8(p.pre_gamma + 8 * (tid + i * kRow)));
-            affine(hat, st.w, shift);
+            centered(hat, st.z, st.w);
             affine(hat, m0, m1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) dh[i].p[e] = __fadd2_rn(__ffma2_rn(d.p[e], both(st.w), hat.p[e]), dh[i].p[e]);
         }
     }
-    const float shift = -st.x * st.y;
     float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
         if (p.dgate) {
             F8 u = widen(yq[i]);
             if (post) {
-                affine(u, st.y, shift);
+                centered(u, st.x, st.y);
                 weigh(u, p.post_gamma, p.post_beta, at);
             }
             times(u, dh[i]);
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
         if (post) {
             times(dh[i], load_f8(p.post_gamma + at));
             F8 hat = widen(yq[i]);
-            affine(hat, st.y, shift);
+            centered(hat, st.x, st.y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 s0 = __ffma2_rn(dh[i].p[e], hat.p[e], s0);
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
         if (!inside(i)) continue;
         if (post) {
             F8 hat = widen(yq[i]);
-            affine(hat, st.y, shift);
+            centered(hat, st.x, st.y);
             affine(hat, m0, m1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) dh[i].p[e] = __ffma2_rn(dh[i].p[e], both(st.y), hat.p[e]);
@@ -407,10 +415,10 @@ int norm_parts(int tokens, int hidden) {
 }
 
 // Block x + across (y + parts z): columns 256 x ..., the y-th part of the rows, pair first + z.
-// Bound by HBM.
-template <bool kTokenGate>
-__global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6) residual_norm_parts_kernel(const __grid_constant__ NormParams p,
-                                                                        float* parts, int tokens, int first, int n_parts) {
+// Bound by HBM.  kMeans: a layer norm is among them (8B-shaped sums take 26.0 us without one, 27.1 with).
+template <bool kTokenGate, bool kMeans>
+__global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6)
+    residual_norm_parts_kernel(const __grid_constant__ NormParams p, float* parts, int tokens, int first, int n_parts) {
     __shared__ float sums[2][kWGroups][256];
     release_next();
     wait_for_previous();
@@ -428,13 +436,12 @@ __global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6) residual_norm_p
     F8 s0{}, s1{};
     if (col < p.hidden) {
         for (int tb = t0 + group; tb < t1; tb += kWGroups * kWUnroll) {
-            uint4 dq[kWUnroll], vq[kWUnroll], gq[kTokenGate ? kWUnroll : 1];
+            uint4 dq[kWUnroll], vq[kWUnroll], gq[kTokenGate ? kWUnroll : 1] = {};
             float2 st[kWUnroll];  // mean, rstd
 #pragma unroll
             for (int i = 0; i < kWUnroll; ++i) {
                 const int t = tb + i * kWGroups;
                 dq[i] = vq[i] = make_uint4(0, 0, 0, 0);
-                if constexpr (kTokenGate) gq[i] = dq[i];
                 st[i] = make_float2(0.f, 1.f);
                 if (t >= t1) continue;
                 const int64_t at = static_cast<int64_t>(t) * p.hidden + col;
@@ -446,14 +453,19 @@ __global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6) residual_norm_p
             }
 #pragma unroll
             for (int i = 0; i < kWUnroll; ++i) {
-                F8 d = widen(dq[i]), hat = widen(vq[i]);
-                if constexpr (kTokenGate)
-                    if (gate) times(d, widen(gq[i]));
-                affine(hat, st[i].y, -st[i].x * st[i].y);
+                const uint4& gi = gq[kTokenGate ? i : 0];
+                const uint32_t dw[4] = {dq[i].x, dq[i].y, dq[i].z, dq[i].w}, vw[4] = {vq[i].x, vq[i].y, vq[i].z, vq[i].w};
+                const uint32_t gw[4] = {gi.x, gi.y, gi.z, gi.w};
+                // pair by pair: in steps of eight values, six blocks' registers do not hold them (layer norms 28.5 us, 27.1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s0.p[e] = __fadd2_rn(s0.p[e], d.p[e]);
-                    s1.p[e] = __ffma2_rn(d.p[e], hat.p[e], s1.p[e]);
+                    float2 d = make_float2(bf16_lo(dw[e]), bf16_hi(dw[e])), hat = make_float2(bf16_lo(vw[e]), bf16_hi(vw[e]));
+                    if constexpr (kTokenGate)
+                        if (gate) d = __fmul2_rn(d, make_float2(bf16_lo(gw[e]), bf16_hi(gw[e])));
+                    if constexpr (kMeans) hat = __fadd2_rn(hat, both(-st[i].x));
+                    hat = __fmul2_rn(hat, both(st[i].y));
+                    s0.p[e] = __fadd2_rn(s0.p[e], d);
+                    s1.p[e] = __ffma2_rn(d, hat, s1.p[e]);
                 }
             }
         }
@@ -684,7 +696,9 @@ extern "C" zb_status zb_op_residual_norm_backward_weight(const zb_residual_norm*
     const int parts = norm_parts(tokens, hidden);
     cudaStream_t s = as_stream(stream);
     const unsigned grid = static_cast<unsigned>((hidden + 255) / 256 * parts * (pre && branch ? 2 : 1));
-    auto kern = p.gate_token ? &residual_norm_parts_kernel<true> : &residual_norm_parts_kernel<false>;
+    const bool means = p.pre == ZB_NORM_LAYER || p.post == ZB_NORM_LAYER;
+    auto kern = p.gate_token ? (means ? &residual_norm_parts_kernel<true, true> : &residual_norm_parts_kernel<true, false>)
+                             : (means ? &residual_norm_parts_kernel<false, true> : &residual_norm_parts_kernel<false, false>);
     ZB_TRY(cuda_status(launch_chained(kern, grid, kWThreads, 0, s, p, static_cast<float*>(scratch), tokens, pre ? 0 : 1, parts)));
     const NormGrads out{dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, dgate};
     return cuda_status(launch_chained(residual_norm_sum_kernel, static_cast<unsigned>(hidden / 32), 1024, 0, s, p, out,

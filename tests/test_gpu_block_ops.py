@@ -544,6 +544,39 @@ def test_residual_norm(cuda_device, t, w, post, pre, gate, beta):
         assert torch.equal(one, grads[k]), k
 
 
+@pytest.mark.parametrize("w", [64, 320, 4096, 4160, 11712])
+def test_layer_norm_of_constant_rows(cuda_device, w):
+    """A row of one value is its mean: the sum of w < 2^14 equal numbers of 8 bits is exact in float32, and so is its w-th part.
+    The normed row is then 0, whatever the value: what is left is beta, rounded once, and gamma gets no gradient."""
+    rng = np.random.default_rng(w)
+    values = torch.tensor([1000.0, -0.37, 5e4, 0.0, 3e-5, -2.5], device="cuda").to(torch.bfloat16)
+    t = values.numel()
+    rows, zero = values[:, None].expand(t, w).contiguous(), torch.zeros(t, w, dtype=torch.bfloat16, device="cuda")
+    gamma, beta = draw_f32(rng, w)[1], draw_f32(rng, w)[1]
+    want = beta.to(torch.bfloat16).expand(t, w)
+    op = zb.make_residual_norm(post="layer", post_gamma=gamma, post_beta=beta)
+    h, stats, dy, dh = out_rows(t, w), out_rows(t, 4, torch.float32), out_rows(t, w), out_rows(t, w)
+    zb.zb_op_residual_norm_forward(op, zero, rows, h, None, stats, t, w)
+    assert torch.equal(h[:t], want) and torch.equal(stats[:t, 0], values.float())
+    before = draw_f32(rng, w)[1]
+    got, d = before.clone(), bf16_from_bits(draw_bf16(rng, (t, w))[0])
+    scratch = scratch_of(zb.zb_op_residual_norm_backward_weight_scratch_bytes(t, w))
+    zb.zb_op_residual_norm_backward_weight(op, None, None, d, rows, stats, t, w, scratch, dpost_gamma=got)
+    assert torch.equal(got, before)
+    op = zb.make_residual_norm(pre="layer", pre_gamma=gamma, pre_beta=beta)
+    n = out_rows(t, w)
+    zb.zb_op_residual_norm_forward(op, rows, zero, h, n, stats, t, w)
+    assert torch.equal(h[:t], rows) and torch.equal(n[:t], want)
+    got = before.clone()
+    zb.zb_op_residual_norm_backward_weight(op, d, rows, None, None, stats, t, w, scratch, dpre_gamma=got)
+    assert torch.equal(got, before)
+    # dh over dn
+    zb.zb_op_residual_norm_backward_input(op, d, zero, rows, None, stats, dh, dy, t, w)
+    over = d.clone()
+    zb.zb_op_residual_norm_backward_input(op, over, zero, rows, None, stats, over, dy, t, w)
+    assert torch.equal(over, dh[:t])
+
+
 def test_no_rows(cuda_device):
     op = zb.make_residual_norm(post="rms", post_gamma=torch.ones(64, device="cuda"))
     g = torch.ones(64, device="cuda")
