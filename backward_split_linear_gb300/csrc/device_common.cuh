@@ -25,7 +25,7 @@ enum WaitSite : int {
     kSiteSplitFlag = 7,      // K-split epilogue waiting for the other half's partial tile
     kSiteAttn = 8,           // attention kernels (any of their pipeline waits)
     kSiteSelftest = 9,       // zb_selftest_wait_timeout
-    kSiteEpiSideInput = 10,  // epilogue waiting for side-input boxes (g and u) loaded by TMA
+    kSiteEpiSideInput = 10,  // epilogue waiting for side-input boxes (g and u, z) loaded by TMA
 };
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait

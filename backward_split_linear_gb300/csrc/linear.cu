@@ -8,15 +8,19 @@
 // 64-deep stages, two accumulators, one persistent pair per two SMs.  Warp 0 loads, warp 1
 // issues the MMAs (2 and 3 only fill their warpgroup), warps 4-11 are the epilogue: warp w
 // reads the 32 tensor-memory lanes 32 (w % 4) ... and one half of the columns.  Eight epilogue warps rather than the four of
-// the plain GEMM because an epilogue here costs up to a hundred instructions an element
-// (erfc, two 8-bit blocks), which has to stay below the tile's MMAs.
+// the plain GEMM because an epilogue here costs up to 3500 cycles per 32 x 32 block (gelu, two 8-bit
+// blocks), which has to stay below the tile's MMAs.
 //
 // Sums.  The tensor core drops what falls below its accumulator's last bit, always towards
 // zero: over 4096 terms a sum of products comes out 4e-6 short, over 16384 1.9e-5 (measured
 // against float64), where float32 sums that round to nearest stay below 1e-6.  bf16 results do not
-// show that, float32 gradients do.  So where results are float32 sums (W, and B with a bias gradient) an
-// accumulator holds few terms: the epilogue warps then add it to sums in their
-// registers, while the MMAs fill the other accumulator.
+// show that, float32 gradients and the borders of 8-bit codes do.  So where results are float32
+// sums or codes (W, B with a bias gradient, F with an 8-bit output) an accumulator holds few terms:
+// the epilogue warps then add it to sums in their registers, while the MMAs fill the other accumulator.
+//
+// GB300, 4096 rows of an 8B-shaped layer (4096 x 14336; 252.5 us at the measured peak of 1905
+// TFLOP/s): F with gelu, z and y in 8 bits 287 us, B with gelu from 8 bits and a bias gradient 290, W 277
+// (and 10 for its operand's unpacking); 320, 310 and 305 once the power cap holds the clocks.
 #include <algorithm>
 #include <mutex>
 
@@ -54,7 +58,8 @@ enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
 // tile's first two accumulators hold more: while its warps work on the tile before, the MMAs get
 // that far and no further.  8B-shaped B with gelu, z in 8 bits and a bias gradient (K = 4096), that
 // sum's error behind the time: 312 us with 14 first (6.7e-7), 301 with 16 (7.8e-7), 298 with 18
-// (8.9e-7); the plain form's in float32 arithmetic is 6.2e-7 off.
+// (8.9e-7); the plain form's in float32 arithmetic is 6.2e-7 off.  F with two 8-bit outputs (gelu): 303 us
+// with 20 first and 12 behind them, 320 with 16 and 8 (sustained clocks), taken for the codes' sake.
 constexpr int kLinSumBlocks = 8;
 template <int EPI>
 __device__ __forceinline__ int lin_first_blocks(int k_blocks) {

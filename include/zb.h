@@ -616,7 +616,7 @@ zb_status zb_op_grad_norm(const zb_adamw_tensor* tensors, int32_t n, float max_n
  *   7  K-split epilogue waiting for the other half's partial tile
  *   8  attention kernels (any of their pipeline waits)
  *   9  zb_selftest_wait_timeout
- *   10 GEMM epilogue waiting for SwiGLU side inputs loaded by TMA
+ *   10 GEMM epilogue waiting for side inputs (SwiGLU's, an activation's) loaded by TMA
  * Reading synchronises `stream`; `reset` != 0 clears the word afterwards.
  * Returns ZB_ERR_DEVICE_TIMEOUT when the word was set, ZB_OK otherwise. */
 zb_status zb_device_status(void* stream, int32_t reset, int32_t* code);
