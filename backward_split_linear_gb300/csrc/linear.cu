@@ -19,8 +19,9 @@
 // the epilogue warps then add it to sums in their registers, while the MMAs fill the other accumulator.
 //
 // GB300, 4096 rows of an 8B-shaped layer (4096 x 14336; 252.5 us at the measured peak of 1905
-// TFLOP/s): F with gelu, z and y in 8 bits 287 us, B with gelu from 8 bits and a bias gradient 290, W 277
-// (and 10 for its operand's unpacking); 320, 310 and 305 once the power cap holds the clocks.
+// TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 272
+// (and 10 for its operand's unpacking); 306, 306 and 310 once the power cap holds the clocks, where
+// a plain F takes 269 and a plain W 302.
 #include <algorithm>
 #include <mutex>
 
@@ -56,15 +57,15 @@ enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
 
 // k blocks (of 64 terms) that stay in tensor memory at a time.  Where the epilogue is long, a
 // tile's first two accumulators hold more: while its warps work on the tile before, the MMAs get
-// that far and no further.  8B-shaped B with gelu, z in 8 bits and a bias gradient (K = 4096), that
-// sum's error behind the time: 312 us with 14 first (6.7e-7), 301 with 16 (7.8e-7), 298 with 18
-// (8.9e-7); the plain form's in float32 arithmetic is 6.2e-7 off.  F with two 8-bit outputs (gelu): 303 us
-// with 20 first and 12 behind them, 320 with 16 and 8 (sustained clocks), taken for the codes' sake.
+// that far and no further.  8B-shaped (K = 4096), with 12, 14, 16 and 18 blocks first: B with gelu, z in 8
+// bits and a bias gradient takes 281, 275, 274 and 274 us, and that gradient is off by 5.9e-7, 6.7e-7,
+// 7.8e-7 and 8.9e-7 (the plain form in float32 arithmetic by 6.2e-7); F with gelu, z and y in 8 bits 286,
+// 279, 272 and 270 us, y's values off by 1.2e-4, 1.3e-4, 1.4e-4 and 1.5e-4 (1.2e-4).
 constexpr int kLinSumBlocks = 8;
 template <int EPI>
 __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
     if (EPI == kLinAccumulate) return kLinSumBlocks;
-    return max(kLinSumBlocks, min(16, k_blocks / (EPI == kLinForward ? 2 : 3)));
+    return max(kLinSumBlocks, EPI == kLinForward ? min(16, k_blocks / 2) : min(14, k_blocks / 3));
 }
 
 struct LinParams {
@@ -494,6 +495,16 @@ __device__ __forceinline__ void add_columns(const LinParams& p, float (&v)[32], 
 
 // ---------------------------------------------------------------- kernel
 
+// An epilogue warp is done with an accumulator: its loads from tensor memory have returned, and a
+// tcgen05 fence orders them.  No other memory is meant, so the arrival is relaxed.  A release waits
+// until the warp's stores of the tile before are out, a thousand cycles a warp and one warp after
+// another, with the MMAs waiting for all of them: 283 us against 272 for F with two 8-bit outputs, 281
+// against 269 for B with a bias gradient.  The waits are of the CTA's scope for the same reason: TMA, commits and
+// these arrivals are all that the barriers tell of.
+__device__ __forceinline__ void arrive_empty(uint32_t caddr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
 // kSums: the accumulators are added up in registers every few k blocks (kLinSumBlocks).
 template <bool A_MN, bool B_MN, int EPI, bool kSums>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
@@ -579,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const LinBoxes boxes = lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank));
                     const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank ^ 1u)).bytes;
                     for (int kb = 0; kb < p.k_blocks; ++kb) {
-                        if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
+                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
                             ok = false;
                             break;
                         }
@@ -615,9 +626,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const uint32_t uses = ring_uses(n_fills, kLinStages, s);
                     if (uses > 0) {
                         if (leader)
-                            mbar_wait_cluster(full_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
+                            mbar_wait(full_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
                         else
-                            mbar_wait_cluster(empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
+                            mbar_wait(empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
                     }
                 }
             }
@@ -633,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const uint32_t idesc = mma_idesc_bf16(kLinTile, lin_unit(p, u).cols, A_MN, B_MN);
                     for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_at(kc), ++it) {
                         const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
-                        if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
+                        if (!__all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
                             ok = false;
                             break;
                         }
@@ -641,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         const uint32_t d = tmem_base + acc * kLinTile;
                         const int kb1 = min(kc + chunk_at(kc), p.k_blocks);
                         for (int kb = kc; kb < kb1; ++kb) {
-                            if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
+                            if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
                                 ok = false;
                                 break;
                             }
@@ -680,7 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             uint32_t asked = 0, done = 0;  // boxes of z requested (lane 0) and used
             bool alive = true;
             auto acquire = [&]() {  // one verdict per warp: the tensor-memory loads are warp-wide
-                alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(it & 1u), (it >> 1) & 1u, status, kSiteEpiTmemFull));
+                alive = __all_sync(0xffffffffu, mbar_wait(tfull_bar(it & 1u), (it >> 1) & 1u, status, kSiteEpiTmemFull));
                 tc_fence_after();
                 return alive;
             };
@@ -688,11 +699,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t bar = tempty_bar(it & 1u);
-                    if (leader)
-                        mbar_arrive(bar);
-                    else
-                        mbar_arrive_cluster(map_to_cta(bar, 0));
+                    arrive_empty(map_to_cta(tempty_bar(it & 1u), 0));
                 }
                 ++it;
             };
@@ -718,9 +725,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             for (int u = pair; alive && u < p.num_units; u += npairs) {
                 const LinUnit w = next;
                 const int tm = next_tm, tn = next_tn;
-                // the next unit's divisions while this one's MMAs run
-                next = lin_unit(p, min(u + npairs, p.num_units - 1));
-                lin_tile(p, next.tile, next_tm, next_tn);
                 const int row0 = row0_of(tm);  // first of this warp's rows
                 const int m = row0 + lane;
                 const bool row_ok = m < p.m;
@@ -731,14 +735,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 LinRow row;
                 row.z.alone = row.y.alone = (cols | n_base) % 64 != 0;
                 uint32_t scales = 0;  // B: of this row's blocks, a byte each
-                if constexpr (EPI == kLinActivationBackward) {
-                    if (reads_z && p.z_codes) {
-                        const uint8_t* at = p.z_scales + ((static_cast<int64_t>(min(m, p.m - 1)) * p.n + n_base) >> 5);
+                // What a unit needs besides its sums, while its MMAs run: z's scales, and the place of
+                // the next unit.
+                auto look_ahead = [&]() {
+                    if constexpr (EPI == kLinActivationBackward) {
+                        if (reads_z && p.z_codes) {
+                            const uint8_t* at = p.z_scales + ((static_cast<int64_t>(min(m, p.m - 1)) * p.n + n_base) >> 5);
 #pragma unroll
-                        for (int c = 0; c < kChunks; ++c)
-                            if (32 * c < cols && n_base + 32 * c < p.n) scales |= static_cast<uint32_t>(at[c]) << (8 * c);
+                            for (int c = 0; c < kChunks; ++c)
+                                if (32 * c < cols && n_base + 32 * c < p.n) scales |= static_cast<uint32_t>(at[c]) << (8 * c);
+                        }
                     }
-                }
+                    next = lin_unit(p, min(u + npairs, p.num_units - 1));
+                    lin_tile(p, next.tile, next_tm, next_tn);
+                };
                 // What remains of a chunk once its product `v` is in registers.
                 auto finish = [&](float (&v)[32], int c) {
                     if (!alive) return;
@@ -806,7 +816,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 }
                 if constexpr (kSums) {
                     float sum[kChunks][32];
-                    for (int kc = 0; alive && kc < p.k_blocks; kc += chunk_at(kc)) {
+                    // The first accumulator without a wait between its columns, and what can wait
+                    // behind it: the MMAs may stand still for it, after a tile whose epilogue was longer
+                    // than two accumulators (F 272 -> 266 us, B 284 -> 279).
+                    if (!acquire()) break;
+                    {
+                        const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
+                        uint32_t r[kChunks][32];
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) tmem_load_32(t0 + 32u * c, r[c]);  // of narrow units too many
+                        tmem_wait_load();
+                        release();
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[c][i] = __uint_as_float(r[c][i]);
+                    }
+                    look_ahead();
+                    for (int kc = chunk_at(0); alive && kc < p.k_blocks; kc += chunk_at(kc)) {
                         if (!acquire()) break;
                         const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
 #pragma unroll
@@ -815,17 +842,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                 uint32_t r[32];
                                 tmem_load_32(t0 + 32u * c, r);
                                 tmem_wait_load();
-                                if (kc == 0) {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) sum[c][i] = __uint_as_float(r[i]);
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 32; i += 2) {
-                                        const float2 t = __fadd2_rn(make_float2(sum[c][i], sum[c][i + 1]),
-                                                                    make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
-                                        sum[c][i] = t.x;
-                                        sum[c][i + 1] = t.y;
-                                    }
+                                for (int i = 0; i < 32; i += 2) {
+                                    const float2 t = __fadd2_rn(make_float2(sum[c][i], sum[c][i + 1]),
+                                                                make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+                                    sum[c][i] = t.x;
+                                    sum[c][i + 1] = t.y;
                                 }
                             }
                         }
@@ -850,6 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         }
                     }
                 } else {
+                    look_ahead();
                     if (!acquire()) break;
                     const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
 #pragma unroll 1
@@ -975,7 +998,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const LinBoxes boxes = lin_boxes(p, tm, col0, kSplitUnit, static_cast<int>(rank));
             const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, kSplitUnit, static_cast<int>(rank ^ 1u)).bytes;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) break;
+                if (!mbar_wait(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) break;
                 if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
                 const uint32_t fb = map_to_cta(full_bar(stage), first);
                 const int k0 = kb * kLinBK;
@@ -1002,7 +1025,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             for (int s = 0; s < kLinStages; ++s) {
                 const uint32_t uses = ring_uses(n_fills, kLinStages, s);
-                if (uses > 0) mbar_wait_cluster(leader ? full_bar(s) : empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain);
+                if (uses > 0) mbar_wait(leader ? full_bar(s) : empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain);
             }
         }
     } else if (usable && warp == 1) {
@@ -1015,11 +1038,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = true;
             for (int kc = kb0; ok && kc < kb1; kc = chunk_end(kc), ++it) {
                 const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kLinTile;
                 for (int kb = kc; kb < chunk_end(kc); ++kb) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
                         ok = false;
                         break;
                     }
@@ -1052,7 +1075,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint32_t it = 0;
         for (int kc = kb0; kc < kb1; kc = chunk_end(kc), ++it) {
             const uint32_t acc = it & 1u;
-            alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(acc), (it >> 1) & 1u, status, kSiteEpiTmemFull));
+            alive = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), (it >> 1) & 1u, status, kSiteEpiTmemFull));
             if (!alive) break;
             tc_fence_after();
 #pragma unroll
@@ -1066,10 +1089,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (leader)
-                    mbar_arrive(tempty_bar(acc));
-                else
-                    mbar_arrive_cluster(map_to_cta(tempty_bar(acc), first));
+                arrive_empty(map_to_cta(tempty_bar(acc), first));
             }
         }
         // the MMAs that read the operands are done with them in both CTAs of the pair
