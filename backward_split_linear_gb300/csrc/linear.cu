@@ -60,12 +60,15 @@ enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
 // that far and no further.  8B-shaped (K = 4096), with 12, 14, 16 and 18 blocks first: B with gelu, z in 8
 // bits and a bias gradient takes 281, 275, 274 and 274 us, and that gradient is off by 5.9e-7, 6.7e-7,
 // 7.8e-7 and 8.9e-7 (the plain form in float32 arithmetic by 6.2e-7); F with gelu, z and y in 8 bits 286,
-// 279, 272 and 270 us, y's values off by 1.2e-4, 1.3e-4, 1.4e-4 and 1.5e-4 (1.2e-4).
+// 279, 272 and 270 us, y's values off by 1.2e-4, 1.3e-4, 1.4e-4 and 1.5e-4 (1.2e-4).  Codes show sums that are
+// long for their K: 2112 terms with 16 blocks first put three times as many on the other side of a
+// border as float32 sums do, 640 with 8 likewise.  So F's are a third of K at most, which costs time where
+// the MMAs then wait for the epilogue (4096 rows, 1024 -> 4096: 48.5 us instead of 43.2 with 8 blocks).
 constexpr int kLinSumBlocks = 8;
 template <int EPI>
 __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
     if (EPI == kLinAccumulate) return kLinSumBlocks;
-    return max(kLinSumBlocks, EPI == kLinForward ? min(16, k_blocks / 2) : min(14, k_blocks / 3));
+    return EPI == kLinForward ? max(4, min(16, k_blocks / 3)) : max(kLinSumBlocks, min(14, k_blocks / 3));
 }
 
 struct LinParams {
@@ -539,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     auto chunk_at = [&](int kc) {
         if (!kSums) return p.k_blocks;
         const int first = lin_first_blocks<EPI>(p.k_blocks);
-        return kc < 2 * first ? first : kLinSumBlocks;
+        return kc < 2 * first ? first : min(first, kLinSumBlocks);
     };
 
     if (threadIdx.x == 0) {

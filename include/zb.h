@@ -420,8 +420,9 @@ zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t
  *    packed forms are the bits that zb_op_checkpoint_pack gives for the bf16 ones.
  *  - y may be residual, and dz may be z; other outputs overlap no input.
  *  - dbias adds the float32 dz, ahead of their rounding.  It and W hold their sums in
- *    float32 registers that take 512 to 1024 terms at a time from tensor memory, whose own
- *    sums round towards zero (zb_op_backward_weight leaves all T terms there).
+ *    float32 registers that take 512 to 896 terms at a time from tensor memory, whose own
+ *    sums round towards zero (zb_op_backward_weight leaves all T terms there); F with a
+ *    packed output likewise, a third of the terms at a time, from 256 to 1024.
  *  - Fixed orders throughout: the same bits every time.
  *  - scratch: device memory of at least the bytes the _scratch_bytes call names, contents
  *    ignored; only needed with dbias.  Calls that share it must not overlap on the GPU,
