@@ -19,8 +19,8 @@
 // the epilogue warps then add it to sums in their registers, while the MMAs fill the other accumulator.
 //
 // GB300, 4096 rows of an 8B-shaped layer (4096 x 14336; 252.5 us at the measured peak of 1905
-// TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 272
-// (and 10 for its operand's unpacking); 306, 306 and 310 once the power cap holds the clocks, where
+// TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 261
+// (and 9 for its operand's unpacking); 306, 306 and 310 once the power cap holds the clocks, where
 // a plain F takes 269 and a plain W 302.
 #include <algorithm>
 #include <mutex>
@@ -70,6 +70,14 @@ __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
     if (EPI == kLinAccumulate) return kLinSumBlocks;
     return EPI == kLinForward ? max(4, min(16, k_blocks / 3)) : max(kLinSumBlocks, min(14, k_blocks / 3));
 }
+
+// W pauses before each box of dw.  All SMs finish their tiles at about the same time, and the next tile's
+// loads waited 4000 cycles, instead of 1200, behind 20 MB of additions; spread over the time of two accumulators these
+// let them through.  14336 x 4096 columns, with the
+// operand's unpacking: 286 -> 272 us with 4096 rows (277 with 100 ns; 600 gain 1 %), 172 -> 161 with 2048,
+// 124 -> 116 with 1024.  Not where a tile has fewer than two accumulators (512 rows: 108 -> 110)
+// and not on a pair's last tile.
+constexpr unsigned kLinPauseNs = 300;
 
 struct LinParams {
     int m, n, k_blocks;
@@ -787,7 +795,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         to_words(v, out);
                     }
                     // the box's last store has read it, its z is in registers
-                    if (!reads_z && lane == 0) bulk_wait_group_read<kBoxes - 1>();
+                    if (!reads_z && lane == 0) {
+                        bulk_wait_group_read<kBoxes - 1>();
+                        if (EPI == kLinAccumulate && u + npairs < p.num_units && p.k_blocks >= 2 * kLinSumBlocks) __nanosleep(kLinPauseNs);
+                    }
                     __syncwarp();
                     if constexpr (EPI == kLinAccumulate) {
                         const uint32_t to = box + static_cast<uint32_t>(lane) * 128u;
