@@ -11,6 +11,10 @@ Bar: relative Frobenius error.  A bf16 tensor costs 1.6e-3 (a uniform error of h
 gradient here has at most 8 bf16 tensors and 3 packed ones behind it, and they add in quadrature: sqrt(8 (1.6e-3)^2 + 3
 (6.6e-3)^2) = 1.23e-2, times 1.5 for layers that amplify them (the norms' gammas and the slopes reach 1.2).
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -250,4 +254,91 @@ def test_projection_into_document_attention(cuda_device, t):
 
     for x, y in zip(run(True), run(False)):
         assert torch.equal(x, y)
+    assert zb.zb_device_status() == (0, 0)
+
+
+FIRST_CALL = """
+import torch
+import test_gpu_block_step as step
+par, mbs = step.parameters(4, "gelu"), step.cuda_batches([step.microbatch(5, 200)])
+block = step.Block(par)
+bufs = [block.buffers(200)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+    block.step(mbs[0], bufs[0])
+graph.replay()
+torch.cuda.synchronize()
+ref, ref_bufs = step.eager(par, mbs)
+step.assert_same(block, bufs, ref, ref_bufs)
+assert step.zb.zb_device_status() == (0, 0)
+"""
+
+
+def test_first_call_inside_a_capture(cuda_device):
+    """A process whose first calls are captured: nothing is set up ahead of them that a capture would refuse."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Tensors of 4.3e9 elements, all zeros but for the last row: it comes out as it does in a call of its own, and its
+    products, the only ones that are not zero, are the weight gradients."""
+    t, w = 2 ** 20 + 37, 4096
+    g = torch.Generator()
+    g.manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    zeros = lambda width, dtype=torch.bfloat16: torch.zeros(t, width, dtype=dtype, device="cuda")  # noqa: E731
+    one = lambda width, dtype=torch.bfloat16: torch.zeros(1, width, dtype=dtype, device="cuda")  # noqa: E731
+    row, small = n(1, w).to(torch.bfloat16), n(1, 64).to(torch.bfloat16)
+    big, big_small = zeros(w), zeros(64)
+    big[-1], big_small[-1] = row[0], small[0]
+
+    # packing, F and B
+    codes, scales = zeros(w, torch.uint8), zeros(w // 32, torch.uint8)
+    c1, s1 = one(w, torch.uint8), one(w // 32, torch.uint8)
+    zb.zb_op_checkpoint_pack(big, (codes, scales), t, w)
+    zb.zb_op_checkpoint_pack(row, (c1, s1), 1, w)
+    assert torch.equal(codes[-1:], c1) and torch.equal(scales[-1:], s1)
+    weight, bias = (n(w, 64) / 8).to(torch.bfloat16), n(w)
+    y, y1 = zeros(w), one(w)
+    zb.zb_op_linear_activation_forward(big_small, weight, bias, None, y, t, 64, w, "gelu", z_packed=(codes, scales))
+    zb.zb_op_linear_activation_forward(small, weight, bias, None, y1, 1, 64, w, "gelu", z_packed=(c1, s1))
+    assert torch.equal(y[-1:], y1) and torch.equal(codes[-1:], c1) and torch.equal(scales[-1:], s1)
+    back = (n(64, w) / 8).to(torch.bfloat16)
+    db, db1 = (torch.zeros(w, device="cuda") for _ in range(2))
+    scratch = torch.empty(zb.zb_op_backward_input_activation_scratch_bytes(t, w), dtype=torch.uint8, device="cuda")
+    zb.zb_op_backward_input_activation(big_small, back, None, y, t, w, 64, "gelu", z_packed=(codes, scales), dbias=db, scratch=scratch)
+    zb.zb_op_backward_input_activation(small, back, None, y1, 1, w, 64, "gelu", z_packed=(c1, s1), dbias=db1, scratch=scratch)
+    assert torch.equal(y[-1:], y1) and torch.equal(db, db1) and torch.any(db != 0.0)
+    assert torch.all(y[-2] == 0.0)
+
+    # W from 8 bits
+    zb.zb_op_checkpoint_pack(big, (codes, scales), t, w)
+    scratch = torch.empty(zb.zb_op_backward_weight_checkpoint_scratch_bytes(t, w), dtype=torch.uint8, device="cuda")
+    dw = torch.zeros(64, w, device="cuda")
+    zb.zb_op_backward_weight_checkpoint(big_small, (codes, scales), dw, t, w, 64, scratch)
+    zb.zb_op_checkpoint_unpack((codes, scales), y, t, w)
+    assert torch.equal(dw, small[0].float()[:, None] * y[-1].float())
+    del scratch, codes, scales
+
+    # the norms
+    gamma = 1.0 + 0.1 * n(w)
+    op = zb.make_residual_norm(post="rms", pre="layer", post_gamma=gamma, pre_gamma=gamma)
+    h, normed, st, h1, n1, st1 = zeros(w), zeros(w), zeros(4, torch.float32), one(w), one(w), one(4, torch.float32)
+    zb.zb_op_residual_norm_forward(op, big, big, h, normed, st, t, w)
+    zb.zb_op_residual_norm_forward(op, row, row, h1, n1, st1, 1, w)
+    assert torch.equal(h[-1:], h1) and torch.equal(normed[-1:], n1) and torch.equal(st[-1:], st1)
+    dh, dy, dh1, dy1 = zeros(w), y, one(w), one(w)
+    zb.zb_op_residual_norm_backward_input(op, big, big, h, big, st, dh, dy, t, w)
+    zb.zb_op_residual_norm_backward_input(op, row, row, h1, row, st1, dh1, dy1, 1, w)
+    assert torch.equal(dh[-1:], dh1) and torch.equal(dy[-1:], dy1)
+    scratch = torch.empty(zb.zb_op_residual_norm_backward_weight_scratch_bytes(t, w), dtype=torch.uint8, device="cuda")
+    grads, grads1 = ([torch.zeros(w, device="cuda") for _ in range(2)] for _ in range(2))
+    for a, (d, x, e, v, s, rows) in ((grads, (big, h, dh, big, st, t)), (grads1, (row, h1, dh1, row, st1, 1))):
+        zb.zb_op_residual_norm_backward_weight(op, d, x, e, v, s, rows, w, scratch, dpost_gamma=a[0], dpre_gamma=a[1])
+    for a, b in zip(grads, grads1):
+        assert torch.equal(a, b) and torch.any(a != 0.0)
     assert zb.zb_device_status() == (0, 0)
