@@ -7,8 +7,8 @@
 // (cta_group::2, bf16 in, float32 in tensor memory), operands by TMA through a ring of six
 // 64-deep stages, two accumulators, one persistent pair per two SMs.  Warp 0 loads, warp 1
 // issues the MMAs (2 and 3 only fill their warpgroup), warps 4-11 are the epilogue: warp w
-// reads the 32 tensor-memory lanes 32 (w % 4) ... and one half of the columns.  Eight epilogue warps rather than the four of
-// the plain GEMM because an epilogue here costs up to 3500 cycles per 32 x 32 block (gelu, two 8-bit
+// reads the 32 tensor-memory lanes 32 (w % 4) ... and one half of the columns.  Eight epilogue warps
+// rather than the four of the plain GEMM because an epilogue here costs up to 3500 cycles per 32 x 32 block (gelu, two 8-bit
 // blocks), which has to stay below the tile's MMAs.
 //
 // Sums.  The tensor core drops what falls below its accumulator's last bit, always towards
@@ -19,9 +19,10 @@
 // the epilogue warps then add it to sums in their registers, while the MMAs fill the other accumulator.
 //
 // GB300, 4096 rows of an 8B-shaped layer (4096 x 14336; 252.5 us at the measured peak of 1905
-// TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 261
-// (and 9 for its operand's unpacking); 306, 306 and 310 once the power cap holds the clocks, where
-// a plain F takes 269 and a plain W 302.
+// TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 263
+// (and 9 for its operand's unpacking); 306, 308 and 302 once the power cap holds the clocks, where
+// a plain F takes 270 and a plain W 304.  While an epilogue computes, its MMAs take 630 to 740 cycles
+// for 64 terms, with the arithmetic alone, and 505 otherwise.
 #include <algorithm>
 #include <mutex>
 
@@ -71,18 +72,17 @@ __device__ __forceinline__ int lin_first_blocks(int k_blocks) {
     return EPI == kLinForward ? max(4, min(16, k_blocks / 3)) : max(kLinSumBlocks, min(14, k_blocks / 3));
 }
 
-// W pauses before each box of dw.  All SMs finish their tiles at about the same time, and the next tile's
-// loads waited 4000 cycles, instead of 1200, behind 20 MB of additions; spread over the time of two accumulators these
-// let them through.  14336 x 4096 columns, with the
-// operand's unpacking: 286 -> 272 us with 4096 rows (277 with 100 ns; 600 gain 1 %), 172 -> 161 with 2048,
-// 124 -> 116 with 1024.  Not where a tile has fewer than two accumulators (512 rows: 108 -> 110)
-// and not on a pair's last tile.
+// W pauses before each box of dw.  All SMs finish their tiles at about the same time, and the next
+// tile's loads waited 4000 cycles, instead of 1200, behind 20 MB of additions; spread over the time of
+// two accumulators these let them through.  14336 x 4096 weights, with the operand's unpacking: 286 -> 272 us
+// with 4096 rows (277 with 100 ns; 600 gain 1 %), 172 -> 161 with 2048, 124 -> 116 with 1024.  Not where a
+// tile has fewer than two accumulators (512 rows: 108 -> 110) and not on a pair's last tile.
 constexpr unsigned kLinPauseNs = 300;
 
 struct LinParams {
     int m, n, k_blocks;
     int tiles_m, tiles_n, group, group_m;
-    int tile_n;  // columns of a tile: 256, or fewer where that fills the last wave
+    int tile_n;  // columns of a tile: 256, or fewer where that fills a single wave
     // tiles from narrow_from on (a short last wave) are `parts` units of 256 / parts columns each;
     // with K split, the pairs of a unit
     int narrow_from, parts, num_units;
