@@ -14,9 +14,9 @@
 // Sums.  The tensor core drops what falls below its accumulator's last bit, always towards
 // zero: over 4096 terms a sum of products comes out 4e-6 short, over 16384 1.9e-5 (measured
 // against float64), where float32 sums that round to nearest stay below 1e-6.  bf16 results do not
-// show that, float32 gradients and the borders of 8-bit codes do.  So where results are float32
-// sums or codes (W, B with a bias gradient, F with an 8-bit output) an accumulator holds few terms:
-// the epilogue warps then add it to sums in their registers, while the MMAs fill the other accumulator.
+// show that, float32 gradients and the borders of 8-bit codes do.  So an accumulator holds few terms, fewest where
+// results are float32 sums or codes (W, B with a bias gradient, F with an 8-bit output): the epilogue warps add it to sums
+// in their registers, while the MMAs fill the other accumulator.
 //
 // GB300, 4096 rows of an 8B-shaped layer (4096 x 14336; 252.5 us at the measured peak of 1905
 // TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 263
@@ -56,20 +56,34 @@ constexpr int kLinFewRegs = 64, kLinManyRegs = 216;
 
 enum : int { kLinForward = 0, kLinActivationBackward = 1, kLinAccumulate = 2 };
 
-// k blocks (of 64 terms) that stay in tensor memory at a time.  Where the epilogue is long, a
-// tile's first two accumulators hold more: while its warps work on the tile before, the MMAs get
-// that far and no further.  8B-shaped (K = 4096), with 12, 14, 16 and 18 blocks first: B with gelu, z in 8
-// bits and a bias gradient takes 281, 275, 274 and 274 us, and that gradient is off by 5.9e-7, 6.7e-7,
-// 7.8e-7 and 8.9e-7 (the plain form in float32 arithmetic by 6.2e-7); F with gelu, z and y in 8 bits 286,
-// 279, 272 and 270 us, y's values off by 1.2e-4, 1.3e-4, 1.4e-4 and 1.5e-4 (1.2e-4).  Codes show sums that are
-// long for their K: 2112 terms with 16 blocks first put three times as many on the other side of a
-// border as float32 sums do, 640 with 8 likewise.  So F's are a third of K at most, which costs time where
-// the MMAs then wait for the epilogue (4096 rows, 1024 -> 4096: 48.5 us instead of 43.2 with 8 blocks).
-constexpr int kLinSumBlocks = 8;
-template <int EPI>
-__device__ __forceinline__ int lin_first_blocks(int k_blocks) {
-    if (EPI == kLinAccumulate) return kLinSumBlocks;
-    return EPI == kLinForward ? max(4, min(16, k_blocks / 3)) : max(kLinSumBlocks, min(14, k_blocks / 3));
+// k blocks (of 64 terms) that an accumulator in tensor memory holds: `first` in a tile's first two,
+// `later` in the others.  Where the epilogue is long the first two hold more: while its warps work on the tile
+// before, the MMAs get that far and no further.
+struct LinSums {
+    int first, later;
+};
+
+// W, and F and B where they make codes or a bias gradient (`fine`): no result is further from float64 than float32
+// arithmetic leaves it.  That one is nearer the smaller K is, so that sums are shorter there.
+// F with gelu, z and y in 8 bits, the error of z's values (float32 arithmetic's), first blocks in front:
+//   K = 4096: 16 1.33e-4, 12 1.05e-4, 11 0.99e-4 (1.02e-4); 2112: 11 1.23e-4, 6 0.83e-4 (1.00e-4);
+//   1024: 5 0.76e-4, 3 0.60e-4 (0.75e-4); 640: 4 0.66e-4, 2 0.51e-4 (0.53e-4)
+// and what it costs: 8B-shaped 274 us with 16 and 293 with 11, 4096 rows of K = 2048 to 4096 columns 58.5 and 64.8.
+// B with gelu from 8 bits, the error of the bias gradient (float32 arithmetic's):
+//   4096: 14 6.1e-7 (6.2e-7), 6.7e-7 with 8 blocks in later ones; 2112: 11 5.9e-7, 8 3.7e-7 (4.2e-7);
+//   1024: 8 4.8e-7, 4 2.5e-7 (2.7e-7); 640: 8 4.3e-7, 3 2.0e-7 (2.3e-7)
+// and what it costs: nothing 8B-shaped (277 us), 58.5 -> 62.6 at K = 2048.
+// W: 8 throughout, 1.1e-7 with 4096 rows (1.9e-7).
+// bf16 results alone: 16.  Their last bit is 2^13 times what those sums drop, and nothing is kept of them in float32; all
+// of K in one accumulator took 0.3 to 2 % less time, but with K = 14336 results differed from those of float32 arithmetic by
+// 2.2e-4, with 16 blocks by 0.7e-4.
+constexpr int kLinSumBlocks = 8, kLinPlainBlocks = 16;
+
+inline LinSums lin_sums(int epi, bool fine, int k_blocks) {
+    if (epi == kLinAccumulate) return {kLinSumBlocks, kLinSumBlocks};
+    if (!fine) return {kLinPlainBlocks, kLinPlainBlocks};
+    const int first = epi == kLinForward ? std::max(2, std::min(11, k_blocks / 5)) : std::max(3, std::min(14, k_blocks / 4));
+    return {first, std::min(first, 4)};
 }
 
 // W pauses before each box of dw.  All SMs finish their tiles at about the same time, and the next
@@ -81,6 +95,7 @@ constexpr unsigned kLinPauseNs = 300;
 
 struct LinParams {
     int m, n, k_blocks;
+    LinSums sums;
     int tiles_m, tiles_n, group, group_m;
     int tile_n;  // columns of a tile: 256, or fewer where that fills a single wave
     // tiles from narrow_from on (a short last wave) are `parts` units of 256 / parts columns each;
@@ -516,7 +531,8 @@ __device__ __forceinline__ void arrive_empty(uint32_t caddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
-// kSums: the accumulators are added up in registers every few k blocks (kLinSumBlocks).
+// kSums: a tile has several accumulators, which are added up in registers.  Where one holds all of K, its columns go
+// through the epilogue 32 at a time (K = 1024, 4096 rows, 4096 columns: 27.2 us against 30.2).
 template <bool A_MN, bool B_MN, int EPI, bool kSums>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -549,8 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     // k blocks of the accumulator that starts at block kc
     auto chunk_at = [&](int kc) {
         if (!kSums) return p.k_blocks;
-        const int first = lin_first_blocks<EPI>(p.k_blocks);
-        return kc < 2 * first ? first : min(first, kLinSumBlocks);
+        return kc < 2 * p.sums.first ? p.sums.first : p.sums.later;
     };
 
     if (threadIdx.x == 0) {
@@ -797,7 +812,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     // the box's last store has read it, its z is in registers
                     if (!reads_z && lane == 0) {
                         bulk_wait_group_read<kBoxes - 1>();
-                        if (EPI == kLinAccumulate && u + npairs < p.num_units && p.k_blocks >= 2 * kLinSumBlocks) __nanosleep(kLinPauseNs);
+                        if (EPI == kLinAccumulate && u + npairs < p.num_units && p.k_blocks >= 2 * p.sums.first) __nanosleep(kLinPauseNs);
                     }
                     __syncwarp();
                     if constexpr (EPI == kLinAccumulate) {
@@ -821,7 +836,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     }
                     ++n_stored;
                     // last: the box's store, which the next chunk waits for, runs meanwhile
-                    if constexpr (EPI == kLinActivationBackward && kSums) add_columns(p, v, n, row0, lane, ok);
+                    if constexpr (EPI == kLinActivationBackward) {
+                        if (p.col_sums) add_columns(p, v, n, row0, lane, ok);
+                    }
                 };
                 // the bias's 128 bytes of each chunk into L1, ahead of the loads that every lane makes
                 if constexpr (EPI == kLinForward) {
@@ -945,7 +962,7 @@ __device__ __forceinline__ uint32_t partial_at(uint32_t base, int r, uint32_t j)
     return base + static_cast<uint32_t>(r) * 512u + ((j ^ (static_cast<uint32_t>(r) & 31u)) << 4);
 }
 
-template <bool A_MN, bool B_MN, int EPI, bool kSums>
+template <bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinParams p) {
@@ -973,7 +990,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int kb0 = static_cast<int>(static_cast<int64_t>(split) * p.k_blocks / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * p.k_blocks / splits);
     // k blocks of the accumulator that starts at block kc
-    auto chunk_end = [&](int kc) { return kSums ? min(kc + kLinSumBlocks, kb1) : kb1; };
+    auto chunk_end = [&](int kc) { return min(kc + p.sums.later, kb1); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kLinStages; ++s) {
@@ -1180,7 +1197,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     tma_store_2d(&map_out, box, n, row0);
                 bulk_commit_group();
             }
-            if constexpr (EPI == kLinActivationBackward && kSums) add_columns(p, v, n, row0, lane, ok);
+            if constexpr (EPI == kLinActivationBackward) {
+                if (p.col_sums) add_columns(p, v, n, row0, lane, ok);
+            }
             if (lane == 0) bulk_wait_group_read<0>();
         }
     }
@@ -1338,9 +1357,10 @@ struct LinFit {
     int clusters[2];
 };
 
-cudaError_t lin_fit(const void* kern, const void* split_kern, LinFit* fit) {
+// (its forms with one accumulator and with several take the same registers and shared memory)
+cudaError_t lin_fit(const void* kern, const void* one_kern, const void* split_kern, LinFit* fit) {
     LinFit f{};
-    for (const void* k : {kern, split_kern}) {
+    for (const void* k : {kern, one_kern, split_kern}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLinSmem));
         if (e != cudaSuccess) return e;
     }
@@ -1395,7 +1415,7 @@ cudaError_t launch_clusters(void (*kernel)(P...), unsigned grid, unsigned cluste
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-template <bool A_MN, bool B_MN, int EPI, bool kSums>
+template <bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p, int k, cudaStream_t stream) try {
     constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -1422,8 +1442,12 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
                              reinterpret_cast<uintptr_t>(p.z_codes) | reinterpret_cast<uintptr_t>(p.y_codes);
     p.wide = starts % 32 == 0;
 
-    auto kern = linear_kernel<A_MN, B_MN, EPI, kSums>;
-    auto split_kern = linear_split_kernel<A_MN, B_MN, EPI, kSums>;
+    p.k_blocks = (k + kLinBK - 1) / kLinBK;
+    const bool fine = p.col_sums || (EPI == kLinForward && (p.z_codes || p.y_codes));
+    p.sums = lin_sums(EPI, fine, p.k_blocks);
+    auto sums_kern = linear_kernel<A_MN, B_MN, EPI, true>;
+    auto one_kern = linear_kernel<A_MN, B_MN, EPI, EPI == kLinAccumulate>;  // W's epilogue is short either way
+    auto split_kern = linear_split_kernel<A_MN, B_MN, EPI>;
     static std::mutex mu;
     static LinFit fits[64] = {};
     int dev = 0;
@@ -1432,13 +1456,13 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!fits[dev].pairs) {
-            const cudaError_t e = lin_fit(reinterpret_cast<const void*>(kern), reinterpret_cast<const void*>(split_kern), &fits[dev]);
+            const cudaError_t e = lin_fit(reinterpret_cast<const void*>(sums_kern), reinterpret_cast<const void*>(one_kern),
+                                          reinterpret_cast<const void*>(split_kern), &fits[dev]);
             if (e != cudaSuccess) return e;
         }
         fit = fits[dev];
     }
     const int pairs = fit.pairs;
-    p.k_blocks = (k + kLinBK - 1) / kLinBK;
     p.tiles_m = (p.m + kLinTile - 1) / kLinTile;
     // K split: the most pairs a unit for which all units run at once.
     const int units = p.tiles_m * ((p.n + kSplitUnit - 1) / kSplitUnit);
@@ -1446,6 +1470,8 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
         const int splits = 2 << i;
         if (units > fit.clusters[i] || p.k_blocks < kSplitMinBlocks) continue;
         p.parts = splits;
+        // 4 left the bias gradient 2.5e-7 off (185 rows, K = 11520), float32 arithmetic 2.3e-7, 3 leave it 2.1e-7
+        if (fine) p.sums.later = std::min(p.sums.later, 3);
         return launch_clusters(split_kern, static_cast<unsigned>(units * 2 * splits), 2u * splits, stream, ma, mb, mo, p);
     }
 
@@ -1462,7 +1488,7 @@ cudaError_t launch_linear(const void* a, const void* b, void* out, LinParams& p,
     p.parts = rem == 0 || 2 * rem > pairs ? 1 : 4 * rem > pairs ? 2 : 4;
     p.narrow_from = p.parts == 1 ? tiles : tiles - rem;
     p.num_units = p.narrow_from + p.parts * (tiles - p.narrow_from);
-    return launch_chained(kern, 2u * static_cast<unsigned>(std::min(p.num_units, pairs)), kLinThreads, kLinSmem, stream, ma, mb, mo,
+    return launch_chained(p.k_blocks <= p.sums.first ? one_kern : sums_kern, 2u * static_cast<unsigned>(std::min(p.num_units, pairs)), kLinThreads, kLinSmem, stream, ma, mb, mo,
                           mz, p);
 } catch (...) {  // the tile order is kept in a map, which may not get its memory
     return cudaErrorMemoryAllocation;
@@ -1507,10 +1533,7 @@ extern "C" zb_status zb_op_linear_activation_forward(const void* x, const void* 
         p.y_codes = static_cast<uint8_t*>(y_packed->codes);
         p.y_scales = static_cast<uint8_t*>(y_packed->scales);
     }
-    // 8-bit codes are whole numbers: a sum that is short by 4e-6 moves some across a border
-    if (z_packed || y_packed)
-        return cuda_status(launch_linear<false, false, kLinForward, true>(x, w, y, p, in_features, as_stream(stream)));
-    return cuda_status(launch_linear<false, false, kLinForward, false>(x, w, y, p, in_features, as_stream(stream)));
+    return cuda_status(launch_linear<false, false, kLinForward>(x, w, y, p, in_features, as_stream(stream)));
 }
 
 extern "C" size_t zb_op_backward_input_activation_scratch_bytes(int32_t tokens, int32_t in_features) {
@@ -1544,9 +1567,9 @@ extern "C" zb_status zb_op_backward_input_activation(const void* dy, const void*
         p.z_scales = static_cast<uint8_t*>(z_packed->scales);
     }
     cudaStream_t s = as_stream(stream);
-    if (!dbias) return cuda_status(launch_linear<false, true, kLinActivationBackward, false>(dy, w, dz, p, out_features, s));
-    p.col_sums = static_cast<float*>(scratch);
-    ZB_TRY(cuda_status(launch_linear<false, true, kLinActivationBackward, true>(dy, w, dz, p, out_features, s)));
+    if (dbias) p.col_sums = static_cast<float*>(scratch);
+    ZB_TRY(cuda_status(launch_linear<false, true, kLinActivationBackward>(dy, w, dz, p, out_features, s)));
+    if (!dbias) return ZB_OK;
     return cuda_status(launch_column_sum(p.col_sums, dbias, (tokens + 31) / 32, in_features, s));
 }
 
@@ -1612,5 +1635,5 @@ extern "C" zb_status zb_op_backward_weight_checkpoint(const void* dy, const zb_c
     LinParams p{};
     p.m = out_features;
     p.n = in_features;
-    return cuda_status(launch_linear<true, true, kLinAccumulate, true>(dy, scratch, dw, p, tokens, s));
+    return cuda_status(launch_linear<true, true, kLinAccumulate>(dy, scratch, dw, p, tokens, s));
 }

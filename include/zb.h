@@ -419,11 +419,16 @@ zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t
  *  - z is rounded to bf16 before it is packed, y is computed from z before that: the
  *    packed forms are the bits that zb_op_checkpoint_pack gives for the bf16 ones.
  *  - y may be residual, and dz may be z; other outputs overlap no input.
- *  - dbias adds the float32 dz, ahead of their rounding.  It and W hold their sums in
- *    float32 registers that take 512 to 896 terms at a time from tensor memory, whose own
- *    sums round towards zero (zb_op_backward_weight leaves all T terms there); F with a
- *    packed output likewise, a third of the terms at a time, from 256 to 1024.
- *  - Fixed orders throughout: the same bits every time.
+ *  - dbias adds the float32 dz, ahead of their rounding.
+ *  - Products are float32 sums.  Tensor memory's own round towards zero, so it holds few terms
+ *    at a time, which float32 registers add up (zb_op_backward_weight leaves all T terms there):
+ *    512 in W; in F with a packed output from 128 to 704, in B with dbias from 192 to 896, the
+ *    fewer the shorter the sum; 1024 in F and B without.  Codes, dbias and dw are no further from
+ *    the exact ones than float32 arithmetic leaves them.
+ *  - Fixed orders throughout: a call gives the same bits every time.  y of a call with a packed
+ *    output and of one without, or dz with dbias and without, may differ in their last bit, as
+ *    their sums are taken in other lengths.  Whoever computes y again, and needs the bits that
+ *    were, asks for the same outputs again.
  *  - scratch: device memory of at least the bytes the _scratch_bytes call names, contents
  *    ignored; only needed with dbias.  Calls that share it must not overlap on the GPU,
  *    captured and replayed ones included. */
