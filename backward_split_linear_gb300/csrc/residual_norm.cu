@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kRow * norm_rows<kRow>(), norm_blocks<kRow>(12
 // Two pairs of sums over the rows for every column: dn and dn hhat; gdh and gdh yhat, where
 // gdh is dh (times the gate per token) and yhat the normed y (y itself without a post norm).
 // A gate per channel is a factor of the sums, so dgate and the post norm's gradients come
-// from the same two.  Two passes in a fixed order: sums over parts of the rows
+// from the same two.  Where only a beta is asked for, its pair's h or y is not read (NULL) and
+// the second sum not used.  Two passes in a fixed order: sums over parts of the rows
 // ([parts][4][hidden]), then over the parts.
 
 constexpr int kWThreads = 256;
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6)
     const uint16_t* d_of = branch ? p.dh : p.dn;
     const uint16_t* v_of = branch ? p.y : p.h;
     const uint16_t* gate = kTokenGate && branch ? p.gate_token : nullptr;
-    const bool normed = !branch || p.post != ZB_NORM_NONE;
+    const bool normed = v_of && (!branch || p.post != ZB_NORM_NONE);
     F8 s0{}, s1{};
     if (col < p.hidden) {
         for (int tb = t0 + group; tb < t1; tb += kWGroups * kWUnroll) {
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kWThreads, kTokenGate ? 4 : 6)
                 if (t >= t1) continue;
                 const int64_t at = static_cast<int64_t>(t) * p.hidden + col;
                 dq[i] = load_q(d_of + at);
-                vq[i] = load_q(v_of + at);
+                if (v_of) vq[i] = load_q(v_of + at);
                 if constexpr (kTokenGate)
                     if (gate) gq[i] = load_q(gate + at);
                 if (normed) st[i] = reinterpret_cast<const float2*>(p.stats)[2 * static_cast<int64_t>(t) + (branch ? 0 : 1)];
@@ -680,8 +681,9 @@ extern "C" zb_status zb_op_residual_norm_backward_weight(const zb_residual_norm*
     for (const float* g : {dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, dgate})
         if (g && !aligned16(g)) return ZB_ERR_ARG;
     const bool pre = dpre_gamma || dpre_beta, branch = dpost_gamma || dpost_beta || dgate;
-    if (!rows_ok(stats, tokens) || (pre && (!rows_ok(dn, tokens) || !rows_ok(h, tokens))) ||
-        (branch && (!rows_ok(dh, tokens) || !rows_ok(y, tokens))))
+    const bool reads_h = dpre_gamma, reads_y = dpost_gamma || dgate;
+    if (!rows_ok(stats, tokens) || (pre && !rows_ok(dn, tokens)) || (reads_h && !rows_ok(h, tokens)) ||
+        (branch && !rows_ok(dh, tokens)) || (reads_y && !rows_ok(y, tokens)))
         return ZB_ERR_ARG;
     if (tokens > 0 && (pre || branch) &&
         (!fixed_ok(scratch) || scratch_bytes < zb_op_residual_norm_backward_weight_scratch_bytes(tokens, hidden)))
@@ -689,9 +691,9 @@ extern "C" zb_status zb_op_residual_norm_backward_weight(const zb_residual_norm*
     ZB_TRY(device_ok());
     if (tokens == 0 || (!pre && !branch)) return ZB_OK;
     p.dn = static_cast<const uint16_t*>(dn);
-    p.h = static_cast<uint16_t*>(const_cast<void*>(h));
+    p.h = reads_h ? static_cast<uint16_t*>(const_cast<void*>(h)) : nullptr;
     p.dh = static_cast<uint16_t*>(const_cast<void*>(dh));
-    p.y = static_cast<const uint16_t*>(y);
+    p.y = reads_y ? static_cast<const uint16_t*>(y) : nullptr;
     p.stats = reinterpret_cast<float4*>(const_cast<float*>(stats));
     const int parts = norm_parts(tokens, hidden);
     cudaStream_t s = as_stream(stream);

@@ -507,7 +507,9 @@ zb_status zb_op_backward_weight_checkpoint(const void* dy, const zb_checkpoint* 
  *    dres may be NULL where there is a pre norm (nothing else reads h).  y may be NULL in B
  *    without a post norm or dgate; dgate may be NULL.
  *  - h may be x; dh may be dres or dn.  Other outputs overlap no input.
- *  - In W a gradient that is NULL is not formed, and what only it would read may be NULL.
+ *  - In W a gradient that is NULL is not formed, and a tensor that only it would read may be
+ *    NULL: dn is for the pre norm's two, h for its gamma, dh for the others, y for the post
+ *    norm's gamma and the gate.  stats is always given.
  *  - hidden is at most 32768.  Rows of padding give rows of padding: no row reads another
  *    but in W, which adds all of them.  Fixed orders: the same bits every time. */
 typedef enum { ZB_NORM_NONE = 0, ZB_NORM_RMS = 1, ZB_NORM_LAYER = 2 } zb_norm_kind;

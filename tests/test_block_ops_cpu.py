@@ -127,6 +127,25 @@ def test_residual_norm_refusals(zblib):
     assert zb.zb_op_residual_norm_backward_weight_scratch_bytes(8, 40000 // 64 * 64) == 0
 
 
+def test_residual_norm_weight_takes_what_its_gradients_read(zblib):
+    """A beta's gradient reads neither h nor y: the call gets past the checks of its arguments (and ends at the device's, or
+    at the scratch)."""
+    def status(**kw):
+        a = {**dict(dn=FAKE, h=FAKE, dh=FAKE, y=FAKE), **{k: kw.pop(k) for k in ("dn", "h", "dh", "y") if k in kw}}
+        with pytest.raises(zb.ZBError) as e:
+            zb.zb_op_residual_norm_backward_weight(norm_op(post="layer", post_beta=FAKE), a["dn"], a["h"], a["dh"], a["y"], FAKE, 8, 64,
+                                                   None, 0, stream=0, **kw)
+        return e.value.status
+
+    for kw in (dict(dpre_beta=FAKE, h=None, dh=None, y=None), dict(dpost_beta=FAKE, dn=None, h=None, y=None),
+               dict(dgate=FAKE, dn=None, h=None), dict(dpre_gamma=FAKE, dh=None, y=None),
+               dict(dpre_beta=FAKE, dpost_gamma=FAKE, h=None), dict(dpre_gamma=FAKE, dpost_beta=FAKE, y=None)):
+        assert status(**kw) == -10, kw
+    for kw in (dict(dpre_beta=FAKE, dn=None), dict(dpre_gamma=FAKE, h=None), dict(dpost_beta=FAKE, dh=None),
+               dict(dpost_gamma=FAKE, y=None), dict(dgate=FAKE, y=None)):
+        assert status(**kw) == -1, kw
+
+
 # ---------------------------------------------------------------- the oracle
 
 
