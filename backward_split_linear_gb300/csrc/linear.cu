@@ -521,12 +521,13 @@ __device__ __forceinline__ void add_columns(const LinParams& p, float (&v)[32], 
 
 // ---------------------------------------------------------------- kernel
 
-// An epilogue warp is done with an accumulator: its loads from tensor memory have returned, and a
-// tcgen05 fence orders them.  No other memory is meant, so the arrival is relaxed.  A release waits
-// until the warp's stores of the tile before are out, a thousand cycles a warp and one warp after
-// another, with the MMAs waiting for all of them: 283 us against 272 for F with two 8-bit outputs, 281
-// against 269 for B with a bias gradient.  The waits are of the CTA's scope for the same reason: TMA, commits and
-// these arrivals are all that the barriers tell of.
+// An epilogue warp is done with an accumulator: its loads from tensor memory have returned
+// (tcgen05.wait::ld), and tcgen05 fences on both sides order them ahead of the next MMAs' writes, which
+// needs no release, only that the arrival comes before the wait's end: the PTX manual's pattern for tensor memory that passes
+// between threads, a relaxed arrival and a wait at cluster scope.  No other memory is meant.  A release would wait until the
+// warp's stores of the tile before are out, a thousand cycles a warp and one warp after another, with the MMAs waiting
+// for all of them: 283 us against 272 for F with two 8-bit outputs, 281 against 269 for B with a bias gradient.
+// All waits on barriers that the other CTA arrives on, or whose bytes its loads bring, are at cluster scope (1 us of 270).
 __device__ __forceinline__ void arrive_empty(uint32_t caddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
@@ -616,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const LinBoxes boxes = lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank));
                     const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, w.cols, static_cast<int>(rank ^ 1u)).bytes;
                     for (int kb = 0; kb < p.k_blocks; ++kb) {
-                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
+                        if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) {
                             ok = false;
                             break;
                         }
@@ -652,9 +653,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const uint32_t uses = ring_uses(n_fills, kLinStages, s);
                     if (uses > 0) {
                         if (leader)
-                            mbar_wait(full_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
+                            mbar_wait_cluster(full_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
                         else
-                            mbar_wait(empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
+                            mbar_wait_cluster(empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain, kWaitLimitNs);
                     }
                 }
             }
@@ -670,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const uint32_t idesc = mma_idesc_bf16(kLinTile, lin_unit(p, u).cols, A_MN, B_MN);
                     for (int kc = 0; ok && kc < p.k_blocks; kc += chunk_at(kc), ++it) {
                         const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
-                        if (!__all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
+                        if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) {
                             ok = false;
                             break;
                         }
@@ -678,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         const uint32_t d = tmem_base + acc * kLinTile;
                         const int kb1 = min(kc + chunk_at(kc), p.k_blocks);
                         for (int kb = kc; kb < kb1; ++kb) {
-                            if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
+                            if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
                                 ok = false;
                                 break;
                             }
@@ -717,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             uint32_t asked = 0, done = 0;  // boxes of z requested (lane 0) and used
             bool alive = true;
             auto acquire = [&]() {  // one verdict per warp: the tensor-memory loads are warp-wide
-                alive = __all_sync(0xffffffffu, mbar_wait(tfull_bar(it & 1u), (it >> 1) & 1u, status, kSiteEpiTmemFull));
+                alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(it & 1u), (it >> 1) & 1u, status, kSiteEpiTmemFull));
                 tc_fence_after();
                 return alive;
             };
@@ -1029,7 +1030,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const LinBoxes boxes = lin_boxes(p, tm, col0, kSplitUnit, static_cast<int>(rank));
             const uint32_t bytes = boxes.bytes + lin_boxes(p, tm, col0, kSplitUnit, static_cast<int>(rank ^ 1u)).bytes;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) break;
+                if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, status, kSiteProducerEmpty)) break;
                 if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
                 const uint32_t fb = map_to_cta(full_bar(stage), first);
                 const int k0 = kb * kLinBK;
@@ -1056,7 +1057,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             for (int s = 0; s < kLinStages; ++s) {
                 const uint32_t uses = ring_uses(n_fills, kLinStages, s);
-                if (uses > 0) mbar_wait(leader ? full_bar(s) : empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain);
+                if (uses > 0) mbar_wait_cluster(leader ? full_bar(s) : empty_bar(s), (uses - 1u) & 1u, status, kSiteDrain);
             }
         }
     } else if (usable && warp == 1) {
@@ -1069,11 +1070,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = true;
             for (int kc = kb0; ok && kc < kb1; kc = chunk_end(kc), ++it) {
                 const uint32_t acc = it & 1u, aph = (it >> 1) & 1u;
-                if (!__all_sync(0xffffffffu, mbar_wait_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(tempty_bar(acc), aph ^ 1u, status, kSiteMmaTmemEmpty))) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kLinTile;
                 for (int kb = kc; kb < chunk_end(kc); ++kb) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster_fast(full_bar(stage), phase, status, kSiteMmaFull))) {
                         ok = false;
                         break;
                     }
@@ -1106,7 +1107,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint32_t it = 0;
         for (int kc = kb0; kc < kb1; kc = chunk_end(kc), ++it) {
             const uint32_t acc = it & 1u;
-            alive = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), (it >> 1) & 1u, status, kSiteEpiTmemFull));
+            alive = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(acc), (it >> 1) & 1u, status, kSiteEpiTmemFull));
             if (!alive) break;
             tc_fence_after();
 #pragma unroll
