@@ -979,6 +979,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     auto tempty_bar = [&](int a) { return bars + 8u * (2 * kLinStages + 2 + a); };
     const uint32_t drain_bar = bars + 8u * (2 * kLinStages + 4);
     const uint32_t tmem_slot = bars + 8u * kLinBars;
+    const uint32_t gave_up = tmem_slot + 4u;  // not 0: a warp of this CTA has no partial sums to give
+    volatile uint32_t* gave_up_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (gave_up - raw));
     volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(smem_raw + (tmem_slot - raw));
 
     int* const status = p.status;
@@ -1003,6 +1005,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mbar_init(tempty_bar(a), 2 * kLinEpiWarps);
         }
         mbar_init(drain_bar, 1);
+        *gave_up_ptr = 0u;
         mbar_fence_init();
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
@@ -1136,10 +1139,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
     }
 
-    cluster_sync_all();  // every pair's partial sums are there
+    if (warp >= kLinFirstWarps && !alive && lane == 0) *gave_up_ptr = 1u;
+    cluster_sync_all();  // every pair's partial sums are there, or its word says that they are not
     const int per_cta = kSplitTasks / splits;
     const int warp_at = warp - kLinFirstWarps;
-    if (alive && warp_at >= 0 && warp_at < per_cta) {
+    bool finishes = warp_at >= 0 && warp_at < per_cta;
+    // a block that misses a pair's sums is left alone: in W it holds those of earlier calls
+    for (int s = 0; finishes && s < splits; ++s) finishes = ld_shared_cluster_u32(map_to_cta(gave_up, 2u * s + rank)) == 0u;
+    if (finishes) {
         const int task = split * per_cta + warp_at, q = task & 3, c = task >> 2;
         const int row0 = tm * kLinTile + static_cast<int>(rank) * kLinHalf + q * 32, m = row0 + lane;
         const int n = tn * kSplitUnit + 32 * c;
