@@ -1,8 +1,9 @@
-"""The feed-forward block's operators where their tests by size and kind do not come: gradients asked for alone."""
+"""The feed-forward block's operators where their tests by size and kind do not come: gradients asked for alone, K split in a cluster."""
 import pytest
 import torch
 
 from backward_split_linear_gb300 import binding as zb
+from oracle import block_ops as O
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,137 @@ def test_one_gradient_takes_only_what_it_reads(cuda_device, t, w, post, gate):
             err = (every[k].double() - before[k].double() - add.sum(0)).abs()
             bar = (t + 4) * 2.0 ** -24 * add.abs().sum(0) + 2.0 ** -22 * (before[k].double().abs() + 1)
             assert bool((err <= bar).all()), k
+
+
+# ---------------------------------------------------------------- K split among the CTA pairs of a cluster
+#
+# From K = 2048 on, where all units of 256 x 128 run at once: 25 units take two pairs each, 8 and 1 take four.
+
+HALF = 2.0 ** -8
+SPLIT = [(185, 2112, 3200), (300, 2304, 512), (33, 4160, 64)]
+
+
+def placed(x, off):
+    """x, or a copy of it that starts 16 bytes behind a 32-byte boundary."""
+    if x is None or not off:
+        return x
+    if isinstance(x, tuple):
+        return tuple(placed(v, off) for v in x)
+    at = 16 // x.element_size()
+    room = torch.zeros(x.numel() + at, dtype=x.dtype, device="cuda")
+    room[at:].copy_(x.reshape(-1))
+    assert room.data_ptr() % 32 == 0
+    return room[at:].view(x.shape)
+
+
+def codes_like(t, n, off=False):
+    return placed((torch.zeros(t, n, dtype=torch.uint8, device="cuda"), torch.zeros(t, n // 32, dtype=torch.uint8, device="cuda")), off)
+
+
+def slip(mass, k):
+    """A sum of k terms of this mass, 1024 at most at a time on the tensor cores: 16 terms an addition that drops what falls below the
+    last bit, some more inside, and float32 additions of the parts."""
+    return ((min(k, 1024) / 16 + 4) * 2.0 ** -22 + (k / 128) * 2.0 ** -24) * mass
+
+
+def within(got, ref, bar, what):
+    err = (got.double() - ref).abs()
+    assert bool((err <= bar).all()), f"{what}: {float((err / bar).max()):.3g} of the bar"
+
+
+def on_gpu(f, x, kind):
+    return torch.from_numpy(f(x.cpu().numpy(), kind)).cuda()
+
+
+@pytest.mark.parametrize("off", [False, True])
+@pytest.mark.parametrize("kind", ["none", "gelu", "relu2"])
+@pytest.mark.parametrize("t,k,n", SPLIT)
+def test_split_forward(cuda_device, t, k, n, kind, off):
+    normal = generator(t + k)
+    bf16 = lambda *s: normal(*s).to(torch.bfloat16)  # noqa: E731
+    x, w, res, bias = bf16(t, k), (normal(n, k) * k ** -0.5).to(torch.bfloat16), bf16(t, n), normal(n)
+    zz = x.double() @ w.double().t() + bias.double()
+    s = slip(x.double().abs() @ w.double().abs().t() + bias.double().abs(), k)
+    a = on_gpu(O.act, zz, kind)
+    steep = 1.2 if kind != "relu2" else 2.0 * zz.abs() + s
+    for r in (None, res):
+        ref = a if r is None else a + r.double()
+        bar = HALF * ref.abs() + 2.0 ** -12 * a.abs() + 2.0 ** -18 + steep * s + (0.0 if r is None else 2.0 ** -23 * r.double().abs())
+        args = [placed(v, off) for v in (x, w, bias, r)]
+        y, z, plain = (placed(torch.zeros_like(res), off) for _ in range(3))
+        y8, z8 = codes_like(t, n, off), codes_like(t, n, off)
+        zb.zb_op_linear_activation_forward(*args, y, t, k, n, kind, z=z, y_packed=y8)
+        within(y, ref, bar, "y")
+        within(z, zz, HALF * zz.abs() + s, "z")
+        for packed, v in ((y8, y), (z8, z)):
+            if packed is z8:
+                again = torch.zeros_like(res)
+                zb.zb_op_linear_activation_forward(*args, again, t, k, n, kind, z_packed=z8)
+                assert torch.equal(again, y)
+            c = codes_like(t, n)
+            zb.zb_op_checkpoint_pack(v, c, t, n)
+            assert torch.equal(c[0], packed[0]) and torch.equal(c[1], packed[1])
+        # bf16 alone, and over the residual
+        zb.zb_op_linear_activation_forward(*args, plain, t, k, n, kind)
+        within(plain, ref, bar, "y alone")
+        if r is not None:
+            zb.zb_op_linear_activation_forward(*args, args[3], t, k, n, kind)
+            assert torch.equal(args[3], plain)
+    assert zb.zb_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("off", [False, True])
+@pytest.mark.parametrize("kind", ["none", "gelu", "relu2"])
+@pytest.mark.parametrize("t,k,n", SPLIT)
+def test_split_backward(cuda_device, t, k, n, kind, off):
+    """dy [t, k], w [k, n], z [t, n]."""
+    normal = generator(t + n)
+    dy, w, z = normal(t, k).to(torch.bfloat16), (normal(k, n) * k ** -0.5).to(torch.bfloat16), (1.5 * normal(t, n)).to(torch.bfloat16)
+    z8 = codes_like(t, n, off)
+    zb.zb_op_checkpoint_pack(z, z8, t, n)
+    values = torch.zeros_like(z)
+    zb.zb_op_checkpoint_unpack(z8, values, t, n)
+    ds = dy.double() @ w.double()
+    s = slip(dy.double().abs() @ w.double().abs(), k)
+    dy, w = placed(dy, off), placed(w, off)
+    scratch = bytes_of(zb.zb_op_backward_input_activation_scratch_bytes(t, n))
+    before = normal(n)
+    for eight in (False, True):
+        slope = on_gpu(O.act_slope, (values if eight else z).double(), kind)
+        ref = ds * slope
+        bar = (HALF + 2.0 ** -12) * ref.abs() + 2.0 ** -18 * ds.abs() + (slope.abs() + 0.1) * s
+        zin, zin8 = (None, z8) if eight else (placed(z, off), None)
+        dz, plain = (placed(torch.zeros_like(z), off) for _ in range(2))
+        dbias = placed(before.clone(), off)
+        zb.zb_op_backward_input_activation(dy, w, zin, dz, t, n, k, kind, z_packed=zin8, dbias=dbias, scratch=scratch)
+        within(dz, ref, bar, "dz")
+        each = 2.0 ** -18 * ds.abs() + (slope.abs() + 0.1) * s + t * 2.0 ** -24 * ref.abs()
+        within(dbias, before.double() + ref.sum(0), each.sum(0) + 2.0 ** -22 * before.double().abs(), "dbias")
+        zb.zb_op_backward_input_activation(dy, w, zin, plain, t, n, k, kind, z_packed=zin8)
+        within(plain, ref, bar, "dz alone")
+        if not eight:
+            over = placed(z.clone(), off)
+            zb.zb_op_backward_input_activation(dy, w, over, over, t, n, k, kind)
+            assert torch.equal(over, plain)
+    assert zb.zb_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("off", [False, True])
+@pytest.mark.parametrize("t,k,n", [(2111, 3200, 192), (2048, 128, 448)])
+def test_split_weight(cuda_device, t, k, n, off):
+    """dy [t, n], x [t, k], dw [n, k]: 25 units and 2."""
+    normal = generator(t)
+    dy, x = normal(t, n).to(torch.bfloat16), normal(t, k).to(torch.bfloat16)
+    x8 = codes_like(t, k, off)
+    zb.zb_op_checkpoint_pack(x, x8, t, k)
+    zb.zb_op_checkpoint_unpack(x8, x, t, k)
+    before = normal(n, k)
+    scratch = bytes_of(zb.zb_op_backward_weight_checkpoint_scratch_bytes(t, k))
+    dw = [placed(before.clone(), off) for _ in range(2)]
+    for v in dw:
+        zb.zb_op_backward_weight_checkpoint(placed(dy, off), x8, v, t, k, n, scratch)
+    ref = before.double() + dy.double().t() @ x.double()
+    s = slip(dy.double().abs().t() @ x.double().abs(), t)
+    within(dw[0], ref, s + 2.0 ** -23 * (before.double().abs() + ref.abs()), "dw")
+    assert torch.equal(*dw)
+    assert zb.zb_device_status() == (0, 0)
