@@ -146,6 +146,15 @@ def test_residual_norm_weight_takes_what_its_gradients_read(zblib):
         assert status(**kw) == -1, kw
 
 
+def test_residual_norm_takes_every_finite_scale(zblib):
+    largest = float(np.finfo(np.float32).max)
+    for kw in (dict(residual_scale=largest), dict(branch_scale=-largest)):
+        op = norm_op(**kw)  # W without a scratch: the options are checked ahead of it
+        with pytest.raises(zb.ZBError) as e:
+            zb.zb_op_residual_norm_backward_weight(op, FAKE, FAKE, FAKE, FAKE, FAKE, 8, 64, None, 0, dpre_gamma=FAKE, stream=0)
+        assert e.value.status == -10, kw
+
+
 # ---------------------------------------------------------------- the oracle
 
 
