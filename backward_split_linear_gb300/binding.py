@@ -517,7 +517,8 @@ def zb_op_backward_input_activation_scratch_bytes(tokens, in_features):
 
 def zb_op_backward_input_activation(dy, w, z, dz, tokens, in_features, out_features, activation, z_packed=None, dbias=None,
                                     scratch=None, scratch_bytes=None, stream=None):
-    """scratch is read with dbias only; its size defaults to the tensor's."""
+    """scratch is read with dbias only; its size defaults to the tensor's.  With relu, z may be the layer's bf16 output
+    (without a residual); z_packed loses the gradient of positive values below half a unit."""
     _check(lib().zb_op_backward_input_activation(_ptr(dy), _ptr(w), _ptr(z), _packed(z_packed), _ptr(dz), _ptr(dbias), tokens,
                                                  in_features, out_features, ACTIVATIONS[activation], _ptr(scratch),
                                                  _size(scratch, scratch_bytes), _stream(stream)),

@@ -200,3 +200,64 @@ def test_split_weight(cuda_device, t, k, n, off):
     within(dw[0], ref, s + 2.0 ** -23 * (before.double().abs() + ref.abs()), "dw")
     assert torch.equal(*dw)
     assert zb.zb_device_status() == (0, 0)
+
+
+# ---------------------------------------------------------------- B from the checkpoints that F wrote
+#
+# The largest second derivatives: gelu 2 phi(0) = 0.798, its tanh form 0.798 too (0.81 taken), silu 1/2, max(z, 0)^2 2.
+
+CURVED = {"none": 0.0, "gelu": 0.81, "gelu_tanh": 0.81, "silu": 0.5, "relu2": 2.0}
+
+
+def forward_and_slopes(kind, outlier):
+    """F's bf16 z, y and 8-bit z of one layer, B through it from a z, dy w in float64 and its bound."""
+    t, k, n = 200, 256, 640
+    normal = generator(9)
+    x, w = normal(t, k).to(torch.bfloat16), (normal(n, k) * k ** -0.5).to(torch.bfloat16)
+    bias = 0.1 * normal(n)
+    if outlier:
+        w[5::32] *= 20.0
+    y, z = (torch.empty(t, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    z8 = codes_like(t, n)
+    zb.zb_op_linear_activation_forward(x, w, bias, None, y, t, k, n, kind, z=z)
+    zb.zb_op_checkpoint_pack(z, z8, t, n)
+    dy, w2 = normal(t, k).to(torch.bfloat16), (normal(k, n) * k ** -0.5).to(torch.bfloat16)
+
+    def back(z_given, packed):
+        dz = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+        zb.zb_op_backward_input_activation(dy, w2, z_given, dz, t, n, k, kind, z_packed=packed)
+        return dz
+
+    ds = dy.double() @ w2.double()
+    return y, z, z8, back, ds, ds.abs() + slip(dy.double().abs() @ w2.double().abs(), k)
+
+
+@pytest.mark.parametrize("outlier", [False, True])
+@pytest.mark.parametrize("kind", sorted(CURVED))
+def test_gradient_from_forwards_8_bits(cuda_device, kind, outlier):
+    """Against the gradient from the bf16 z that F computed: the slope is off by its own slope times the code's error."""
+    y, z, z8, back, _, most = forward_and_slopes(kind, outlier)
+    values = torch.empty_like(z)
+    zb.zb_op_checkpoint_unpack(z8, values, *z.shape)
+    exact, got = back(z, None).double(), back(None, z8).double()
+    # both are rounded to bf16, from float32 slopes and sums a little off
+    fine = (HALF + 2.0 ** -12) * (exact.abs() + got.abs()) + 2.0 ** -17 * most
+    within(got, exact, most * CURVED[kind] * (values.double() - z.double()).abs() + fine, kind)
+
+
+@pytest.mark.parametrize("outlier", [False, True])
+def test_relu_takes_its_output_for_z(cuda_device, outlier):
+    """The bf16 y gives the gradient that the bf16 z gives, bit for bit.  8 bits lose it where a positive z reads as 0, and only
+    there; the header says so."""
+    y, z, z8, back, ds, _ = forward_and_slopes("relu", outlier)
+    exact = back(z, None)
+    assert torch.equal(back(y, None), exact)
+    lost = (z > 0) & ((z8[0] & 127) == 0)
+    assert int(lost.sum()) > 0
+    got = back(None, z8)
+    assert torch.equal(got[~lost], exact[~lost]) and not bool(got[lost].any())
+    dy = ds.to(torch.bfloat16)  # the activation alone, likewise
+    alone = [torch.empty_like(dy) for _ in range(2)]
+    for v, zz in zip(alone, (z, y)):
+        zb.zb_op_activation_backward(dy, zz, v, *z.shape, "relu")
+    assert torch.equal(*alone)
