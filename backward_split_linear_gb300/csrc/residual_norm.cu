@@ -407,7 +407,10 @@ constexpr int kWGroups = 8;
 constexpr int kWUnroll = 2;
 // Blocks of each pair, at most: 3 of 256 threads on each of 152 SMs, six for both pairs, all at
 // once.  With a few more a second round starts: 8597 rows of 3776 columns in 60 us with 615 of 608 that
-// fit, 45 with 450.
+// fit, 45 with 450.  A gate per token takes the registers of four blocks an SM, so that both pairs' last blocks wait for a
+// second round; that form is no further from its bytes all the same (4096 rows of 4096: 32.3 us of 24.7, 26.7 of 19.8 without; 8597
+// of 3776: 55.7 of 47.9, 45.1 of 38.3).  The parts are the same whatever is formed, so that a gradient asked for alone has the
+// same bits; one pair alone then fills half of the SMs' blocks (19 us for half the bytes).
 constexpr int kWTargetBlocks = 456;
 constexpr int kWMostParts = 152;     // few columns: 16384 rows of 256 in 19 us (608 parts: 29)
 
