@@ -19,8 +19,8 @@
 // in their registers, while the MMAs fill the other accumulator.
 //
 // GB300, 4096 rows of an 8B-shaped layer (4096 x 14336; 252.5 us at the measured peak of 1905
-// TFLOP/s): F with gelu, z and y in 8 bits 270 us, B with gelu from 8 bits and a bias gradient 273, W 263
-// (and 9 for its operand's unpacking); 306, 308 and 302 once the power cap holds the clocks, where
+// TFLOP/s): F with gelu, z and y in 8 bits 281 us, B with gelu from 8 bits and a bias gradient 267, W 260
+// (and 9 for its operand's unpacking); 318, 307 and 298 once the power cap holds the clocks, where
 // a plain F takes 270 and a plain W 304.  While an epilogue computes, its MMAs take 630 to 740 cycles
 // for 64 terms, with the arithmetic alone, and 505 otherwise.
 #include <algorithm>
@@ -526,7 +526,8 @@ __device__ __forceinline__ void add_columns(const LinParams& p, float (&v)[32], 
 // needs no release, only that the arrival comes before the wait's end: the PTX manual's pattern for tensor memory that passes
 // between threads, a relaxed arrival and a wait at cluster scope.  No other memory is meant.  A release would wait until the
 // warp's stores of the tile before are out, a thousand cycles a warp and one warp after another, with the MMAs waiting
-// for all of them: 283 us against 272 for F with two 8-bit outputs, 281 against 269 for B with a bias gradient.
+// for all of them: 283 us against 272 for F with two 8-bit outputs, 281 against 269 for B with a bias gradient (with
+// first accumulators of 16 and 14 blocks).
 // All waits on barriers that the other CTA arrives on, or whose bytes its loads bring, are at cluster scope (1 us of 270).
 __device__ __forceinline__ void arrive_empty(uint32_t caddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
@@ -850,7 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     float sum[kChunks][32];
                     // The first accumulator without a wait between its columns, and what can wait
                     // behind it: the MMAs may stand still for it, after a tile whose epilogue was longer
-                    // than two accumulators (F 272 -> 266 us, B 284 -> 279).
+                    // than two accumulators (F 272 -> 266 us, B 284 -> 279, with 16 and 14 blocks in the first two).
                     if (!acquire()) break;
                     {
                         const uint32_t t0 = tlane + (it & 1u) * kLinTile + static_cast<uint32_t>(col0);
@@ -944,7 +945,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 // 128 unit, each pair over its share of K.  The partial sums go to shared memory, where the
 // operands were, and every CTA finishes some of the unit's 32 x 32 blocks from all pairs' partial
 // sums, added in the order of the pairs.  11 rows, K = 6720, 64 columns: 24.1 us on one pair, 13.0 on two, 10.0
-// on four, 10.1 on eight; 185 rows, K = 11520, 1088 columns: 39.3, 21.5, 20.1.  At K = 1024 it loses (256 rows,
+// on four, 10.1 on eight; 185 rows, K = 11520, 1088 columns: 39.3, 21.5, 20.1 (20.9 with its sums of 1024 terms
+// at a time, 22.6 with 8-bit outputs).  At K = 1024 it loses (256 rows,
 // 1024 columns: 8.2 against 9.3), at 2048 it gains (64 rows, 2048 columns: 10.6 against 9.1).
 
 constexpr int kSplitUnit = 128;       // columns of a unit
@@ -1395,7 +1397,7 @@ cudaError_t lin_fit(const void* kern, const void* one_kern, const void* split_ke
 
 // Columns of a tile: 256, or the fewest of 224, 192 and 160 with which a single wave that holds over
 // half of the pairs still is one.  1000 rows, K = 14336, 4096 columns: 64 tiles of 256 columns in 71.7 us,
-// 76 of 224 in 69.1; 1024 rows, K = 4096: 26.8 and 25.4.  (Two waves lose: 1533 rows, K = 3264, 4800 columns
+// 76 of 224 in 69.1 (in a burst; 81 under the power cap); 1024 rows, K = 4096: 26.8 and 25.4.  (Two waves lose: 1533 rows, K = 3264, 4800 columns
 // take 32.6 us in 114 tiles of 256 columns and 35.2 in 150 of 192.)
 int lin_tile_columns(int tiles_m, int n, int pairs) {
     auto tiles = [&](int w) { return static_cast<int64_t>(tiles_m) * ((n + w - 1) / w); };
