@@ -430,8 +430,9 @@ zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t
  *  - Products are float32 sums.  Tensor memory's own round towards zero, so it holds few terms
  *    at a time, which float32 registers add up (zb_op_backward_weight leaves all T terms there):
  *    512 in W; in F with a packed output from 128 to 704, in B with dbias from 192 to 896, the
- *    fewer the shorter the sum; 1024 in F and B without.  Codes, dbias and dw are no further from
- *    the exact ones than float32 arithmetic leaves them.
+ *    fewer the shorter the sum; 1024 in F and B without.  Float32 additions one after another are
+ *    further from the exact sums than these from 512 terms on (1500 in W); shorter ones are 1.8e-7
+ *    off at most where those are 0.5e-7 to 1.5e-7 (relative norms, normal values).
  *  - Fixed orders throughout: a call gives the same bits every time.  y of a call with a packed
  *    output and of one without, or dz with dbias and without, may differ in their last bit, as
  *    their sums are taken in other lengths.  Whoever computes y again, and needs the bits that
