@@ -418,7 +418,7 @@ zb_status zb_op_rotary_backward(const void* dy, int64_t ld_dy, void* dx, int64_t
  *    loses by that: a positive z below half its block's unit reads as 0 and lets no gradient
  *    through, 1.1 % of the positive ones of normally distributed z (dz off by 0.11 in the relative
  *    norm), 7 % (0.27) where one channel of 32 is twenty times as large; the others' slopes are
- *    off by half a unit of z at most.  With max(z, 0) and no residual give B the bf16 y in z's place:
+ *    off by the code's error in z, times 0.8 at most (2 for max(z, 0)^2).  With max(z, 0) and no residual give B the bf16 y in z's place:
  *    y > 0 exactly where z is, and W reads that y anyway, which takes less memory than z and y
  *    in 8 bits.
  *  - bias and dbias: float32 [out].  residual, z, y, dz: bf16 [T, out].  Any of bias,
